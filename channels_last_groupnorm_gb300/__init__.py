@@ -33,3 +33,12 @@ from .gnsilu import (  # noqa: F401
     upconv_fold,
     upsample_conv_nhwc,
 )
+from .block import (  # noqa: F401
+    attention_packed,
+    attention_packed_backward,
+    gn_attn_packed_workspace_bytes,
+    gn_layer_norm_workspace_bytes,
+    layer_norm,
+    layer_norm_backward,
+    rope_nd,
+)

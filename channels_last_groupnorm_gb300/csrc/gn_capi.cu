@@ -688,19 +688,20 @@ const char *gn_status_string(int status)
     switch (status) {
     case GN_OK: return "GN_OK: success";
     case GN_ERR_NULL: return "GN_ERR_NULL: a required pointer is NULL";
-    case GN_ERR_SHAPE: return "GN_ERR_SHAPE: N, L, H or W below 1, or the element count overflows";
+    case GN_ERR_SHAPE: return "GN_ERR_SHAPE: a size or stride out of range, or the element count overflows";
     case GN_ERR_CHANNELS:
         return "GN_ERR_CHANNELS: C must be a power of two in [8, 2048] (a multiple of 8 up to 2048 for "
-               "gn_silu_rows_any / gn_silu_ndhwc) and G must divide C";
-    case GN_ERR_ALIGN: return "GN_ERR_ALIGN: x/y need 16-byte, gamma/beta/statistics 4-byte, workspace 256-byte alignment";
-    case GN_ERR_EPS: return "GN_ERR_EPS: eps must be finite and non-negative";
-    case GN_ERR_ALIAS: return "GN_ERR_ALIAS: y overlaps x (other than in place) or another argument";
-    case GN_ERR_WORKSPACE: return "GN_ERR_WORKSPACE: workspace smaller than gn_silu_workspace_bytes()";
+               "gn_silu_rows_any / gn_silu_ndhwc) and G must divide C; or channels, heads or axes the other "
+               "operations do not take";
+    case GN_ERR_ALIGN: return "GN_ERR_ALIGN: a pointer or stride misaligned (x/y 16 bytes, gamma/beta/statistics 4, workspace 256)";
+    case GN_ERR_EPS: return "GN_ERR_EPS: eps (scale, cap, theta) must be finite and non-negative";
+    case GN_ERR_ALIAS: return "GN_ERR_ALIAS: an output overlaps an input (other than in place) or another argument";
+    case GN_ERR_WORKSPACE: return "GN_ERR_WORKSPACE: workspace smaller than the operation's workspace_bytes()";
     case GN_ERR_CUDA: return "GN_ERR_CUDA: a CUDA call or kernel launch failed";
     case GN_ERR_DEVICE: return "GN_ERR_DEVICE: no CUDA device, or the device is not sm_103";
     case GN_ERR_VARIANT: return "GN_ERR_VARIANT: unknown variant, or it cannot be launched for this shape";
     case GN_ERR_KERNEL: return "GN_ERR_KERNEL: a kernel gave up a bounded wait";
-    case GN_ERR_FORMAT: return "GN_ERR_FORMAT: the half format is neither bf16 (0) nor fp16 (1)";
+    case GN_ERR_FORMAT: return "GN_ERR_FORMAT: an element format the entry point does not take";
     default: return "unknown gn status";
     }
 }

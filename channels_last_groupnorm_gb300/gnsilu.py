@@ -18,7 +18,8 @@ the page's existing general kernel (same section, item 1, third bullet).
 ``residual_gate_add``, ``upconv_fold`` / ``upsample_conv_nhwc`` and
 ``attn_fold`` / ``attention_folded`` bind the residual-gate update, the
 fused nearest-2x upsample + 3x3 conv and the folded single-head attention
-the same way.
+the same way.  The operators of a transformer block (layer norm, rotary
+positions, attention of packed documents) are bound in ``block.py``.
 """
 from __future__ import annotations
 
@@ -85,6 +86,18 @@ EXPORTS = {
                        + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "gn_attn_folded_ex": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int64] * 2
                           + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p]),
+    "gn_layer_norm": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int64] * 4
+                      + [ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "gn_layer_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 2),
+    "gn_layer_norm_backward": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_int64] * 5
+                               + [ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "gn_rope_nd": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int64] * 4
+                   + [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_double,
+                      ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "gn_attn_packed": (ctypes.c_int, [ctypes.c_void_p] * 2),
+    "gn_attn_packed_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 2),
+    "gn_attn_packed_backward": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.c_int64] * 2 + [ctypes.c_void_p] * 4
+                                + [ctypes.c_size_t, ctypes.c_void_p]),
     "gn_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
                                                 ctypes.c_int, ctypes.c_void_p]),
     "gn_silu_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 4),

@@ -94,13 +94,22 @@ enum gn_status_code {
                               cluster variant does not fit it */
     GN_ERR_KERNEL = 11,    /* a kernel gave up a bounded wait and the status has not
                               been cleared (gn_device_status(1)) since; nothing ran */
-    GN_ERR_FORMAT = 12     /* gn_residual_gate_add(): unknown half format */
+    GN_ERR_FORMAT = 12     /* an element format the entry point does not take */
 };
 
-/* Element formats of gn_residual_gate_add(). */
+/* Element formats: gn_residual_gate_add() and gn_attn_packed() take the half
+ * formats, gn_layer_norm() and gn_rope_nd() all three. */
 enum gn_half_format {
     GN_FORMAT_BF16 = 0,
-    GN_FORMAT_FP16 = 1
+    GN_FORMAT_FP16 = 1,
+    GN_FORMAT_FP32 = 2
+};
+
+/* Formats of the positions of gn_rope_nd(). */
+enum gn_position_format {
+    GN_POSITIONS_INT32 = 0,
+    GN_POSITIONS_INT64 = 1,
+    GN_POSITIONS_FP32 = 2
 };
 
 /* Kernel schedules selectable through gn_silu_rows_ex(). */
@@ -444,6 +453,149 @@ int gn_attn_folded_ex(const void *q_bf16, const void *k_bf16, const void *xn_bf1
                       const float *bf, const void *residual_bf16, void *out_bf16, int64_t S, int64_t D,
                       void *workspace, size_t workspace_bytes, int schedule, void *stream);
 
+/* ---- layer norm and its backward pass ---------------------------------------
+ * Over the C channels of each row,
+ *
+ *   mean = sum(x) / C,  rstd = 1 / sqrt(sum((x - mean)^2) / C + eps),
+ *   y = (x - mean) rstd weight + bias
+ *
+ * (without weight and bias: y = (x - mean) rstd, the form ahead of a
+ * modulation), and with h = (x - mean) rstd, g = dy weight,
+ *
+ *   dx = rstd (g - sum(g) / C - h sum(g h) / C),
+ *   dweight = sum over rows of dy h,  dbias = sum over rows of dy.
+ *
+ * Sums are fp32 and added up in a fixed order: the same inputs give the same
+ * bits.  y and dx are rounded once to the format of x, dweight and dbias once
+ * to the format of the weight.
+ */
+
+/* Layer norm.
+ *   x, y       : DEVICE rows of cols elements, `format` (enum gn_half_format,
+ *                all three), x_stride / y_stride elements from one row to the
+ *                next (>= cols).  y may equal x with the same stride.
+ *   weight, bias : DEVICE [cols] of weight_format, or both NULL; bias alone may
+ *                be NULL.
+ *   mean, rstd : DEVICE fp32 [rows], written for the backward pass, or NULL.
+ *   rows >= 0 (0: nothing to do), 1 <= cols <= 16384.  Rows of whole 16-byte
+ *   vectors (pointers and strides too) are read and written in such vectors.
+ * Asynchronous on `stream`.  Errors: GN_ERR_NULL, GN_ERR_FORMAT, GN_ERR_SHAPE
+ * (rows < 0, a stride below cols, sizes overflow), GN_ERR_CHANNELS (cols),
+ * GN_ERR_EPS, GN_ERR_ALIGN (a pointer not a multiple of its element's size),
+ * GN_ERR_ALIAS (an output overlapping an input or another output, but for
+ * y == x), GN_ERR_DEVICE, GN_ERR_KERNEL, GN_ERR_CUDA. */
+int gn_layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean, float *rstd,
+                  int64_t rows, int64_t cols, int64_t x_stride, int64_t y_stride, float eps, int format,
+                  int weight_format, void *stream);
+
+/* Workspace bytes gn_layer_norm_backward() needs with a weight on the CURRENT
+ * device (partial sums of the weight's gradient); 0 if the shape is out of
+ * range or there is no usable device. */
+size_t gn_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Backward pass of gn_layer_norm().
+ *   dy, x, dx  : DEVICE rows as above, each with its own stride; dx may equal
+ *                dy or x with the same stride.
+ *   mean, rstd : from gn_layer_norm().
+ *   weight     : DEVICE [cols], or NULL; with it dweight and dbias (DEVICE
+ *                [cols] of weight_format) are written, with none they are NULL.
+ *   workspace  : DEVICE, 256-byte aligned, at least
+ *                gn_layer_norm_workspace_bytes(rows, cols); not used without a
+ *                weight.
+ *   rows >= 0 (0: dweight and dbias are set to zero).
+ * Asynchronous on `stream`.  Errors: as above, and GN_ERR_WORKSPACE. */
+int gn_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean, const float *rstd,
+                           void *dx, void *dweight, void *dbias, int64_t rows, int64_t cols, int64_t dy_stride,
+                           int64_t x_stride, int64_t dx_stride, int format, int weight_format, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* ---- rotary positions over several axes ---------------------------------------
+ * The first sum(axes_dim) = 2 P channels of every head form P pairs (a, b):
+ * neighbours (2p, 2p + 1) if `interleaved`, else channels (p, P + p).  The
+ * pairs are dealt to the axes in order, axes_dim[n] / 2 each; pair i of axis n
+ * turns by positions[token][n] theta^(-2 i / axes_dim[n]):
+ *
+ *   a' = a cos - b sin,  b' = a sin + b cos   (inverse != 0: the turn back,
+ *                                              which is the gradient's)
+ *
+ * Channels from 2 P on pass unchanged.  Angles are formed in fp64 turns, so far
+ * positions keep their phase; products are fp32, rounded once.
+ *
+ *   q, k       : DEVICE [tokens][heads][dim] and [tokens][kv_heads][dim] with
+ *                the strides given, channels contiguous; k may be NULL with
+ *                kv_heads 0.  Both are turned in one launch.
+ *   q_out, k_out : DEVICE outputs; each may equal its input with the same
+ *                strides (in place), but overlap no input otherwise.
+ *   strides    : HOST [8], elements: token and head stride of q, k, q_out, k_out.
+ *   positions  : DEVICE [tokens][axes] contiguous, enum gn_position_format.
+ *   axes_dim   : HOST [axes], even numbers >= 2, 1 <= axes <= 8,
+ *                sum <= min(dim, 256); dim <= 65536.
+ *   theta > 0.  format: enum gn_half_format (all three).
+ * Asynchronous on `stream`.  Errors: GN_ERR_NULL, GN_ERR_FORMAT, GN_ERR_SHAPE,
+ * GN_ERR_CHANNELS (dim, axes), GN_ERR_EPS (theta), GN_ERR_ALIGN, GN_ERR_ALIAS,
+ * GN_ERR_DEVICE, GN_ERR_KERNEL, GN_ERR_CUDA. */
+int gn_rope_nd(const void *q, const void *k, void *q_out, void *k_out, const int64_t *strides, int64_t tokens,
+               int64_t heads, int64_t kv_heads, int64_t dim, const void *positions, int position_format, int64_t axes,
+               const int64_t *axes_dim, double theta, int interleaved, int inverse, int format, void *stream);
+
+/* ---- attention of packed documents ---------------------------------------------
+ * Documents (images with their texts, prompts, sequences in a cache) lie one
+ * after the other along the token axis: document d owns the queries
+ * [cu_q[d], cu_q[d + 1]) and the keys [cu_k[d], cu_k[d + 1]).  Its last query
+ * stands at its last key.  Query i sees all keys of its document; if causal,
+ * those up to its own position and the first prefix[d] ones.
+ *
+ *   t_ij  = scale q_i . k_j;  cap > 0: t_ij = cap tanh(t_ij / cap)
+ *   t_ij -= slopes[h] |position of i - position of j|   (with slopes)
+ *   lse_i = log sum_j exp(t_ij),  out_i = sum_j exp(t_ij - lse_i) v_j
+ *
+ * A query that sees no key (or belongs to no document) has out = 0 and
+ * lse = -inf and adds nothing to any gradient.  What lies at keys that a query
+ * does not see (infinities and NaN too) has no influence on it.  Query head h
+ * reads key / value head h / (heads / kv_heads).  Scores, softmax and sums are
+ * fp32; the weights and the scores' gradients are rounded to the half format
+ * for the tensor cores' products.  Nothing depends on the order of atomics:
+ * the same inputs give the same bits.
+ */
+typedef struct gn_attn_packed_args {
+    const void *q, *k, *v;        /* DEVICE [tokens_q][heads][dim], [tokens_k][kv_heads][dim] twice */
+    void *out;                    /* DEVICE [tokens_q][heads][dim], contiguous */
+    float *lse;                   /* DEVICE [heads][tokens_q] */
+    int64_t q_token, q_head;      /* strides in elements: multiples of 8, >= dim; channels contiguous */
+    int64_t k_token, k_head;
+    int64_t v_token, v_head;
+    int64_t tokens_q, tokens_k;   /* 0 .. 2^30 */
+    const int32_t *cu_q, *cu_k;   /* DEVICE [docs + 1], non-decreasing; NULL with docs = 1: all tokens */
+    const int32_t *prefix;        /* DEVICE [docs] or NULL; only if causal */
+    const float *slopes;          /* DEVICE [heads] or NULL */
+    float scale, cap;             /* scale finite; cap 0 (none) or > 0 */
+    int heads, kv_heads, dim;     /* kv_heads divides heads; dim a multiple of 8, 8 .. 128 */
+    int docs;                     /* >= 1 */
+    int causal;
+    int format;                   /* GN_FORMAT_BF16 or GN_FORMAT_FP16 */
+} gn_attn_packed_args;
+
+/* Forward.  Pointers 16-byte aligned (cu_q, cu_k, prefix, slopes, lse: 4).
+ * Values of cu_q, cu_k and prefix are clamped into range on the device: bad
+ * ones give wrong results, never a wrong address.  out and lse overlap nothing.
+ * Asynchronous on `stream`.  Errors: GN_ERR_NULL, GN_ERR_FORMAT, GN_ERR_SHAPE
+ * (tokens, docs, strides), GN_ERR_CHANNELS (heads, kv_heads, dim), GN_ERR_EPS
+ * (scale, cap), GN_ERR_VARIANT (prefix without causal), GN_ERR_ALIGN,
+ * GN_ERR_ALIAS, GN_ERR_DEVICE, GN_ERR_KERNEL, GN_ERR_CUDA. */
+int gn_attn_packed(const gn_attn_packed_args *args, void *stream);
+
+/* Workspace bytes of gn_attn_packed_backward(); 0 if out of range. */
+size_t gn_attn_packed_workspace_bytes(int64_t tokens_q, int64_t heads);
+
+/* Backward.  args: those of the forward call, out and lse holding its results.
+ *   dout       : DEVICE [tokens_q][heads][dim], strides as for q.
+ *   dq, dk, dv : DEVICE, contiguous, shaped like q, k, v, overlapping nothing.
+ *   workspace  : DEVICE, 256-byte aligned, gn_attn_packed_workspace_bytes().
+ * The slopes have no gradient.  Asynchronous on `stream`.  Errors: as above,
+ * and GN_ERR_WORKSPACE. */
+int gn_attn_packed_backward(const gn_attn_packed_args *args, const void *dout, int64_t dout_token, int64_t dout_head,
+                            void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *gn_status_string(int status);
 
@@ -451,7 +603,9 @@ const char *gn_status_string(int status);
  * gn_release_workspaces and gn_library_workspaces, and its entry points did
  * not return GN_ERR_KERNEL;
  * 4 also lacked the gn_attn_* calls; 3 also the gn_upconv_* calls; 2 also
- * gn_residual_gate_add; 1 also gn_silu_rows_any and gn_silu_ndhwc). */
+ * gn_residual_gate_add; 1 also gn_silu_rows_any and gn_silu_ndhwc).  The
+ * calls gn_layer_norm*, gn_rope_nd and gn_attn_packed* were added to version 7,
+ * which changed nothing that it had. */
 int gn_abi_version(void);
 
 #ifdef __cplusplus
