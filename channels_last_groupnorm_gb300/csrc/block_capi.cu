@@ -334,8 +334,8 @@ int gn_attn_packed(const gn_attn_packed_args *args, void *stream)
     p.a = *args;
     p.group = args->heads / args->kv_heads;
     int launches = 0;
-    const cudaError_t e = gn::launch_packed_attn(p, d.sm_count, wait_timeout_ns(), static_cast<cudaStream_t>(stream),
-                                                 &launches);
+    const cudaError_t e = gn::launch_packed_attn(p, d.sm_count, {wait_timeout_ns(), d.status_word, d.status_host},
+                                                 static_cast<cudaStream_t>(stream), &launches);
     return launched(e, launches);
 }
 
@@ -385,7 +385,8 @@ int gn_attn_packed_backward(const gn_attn_packed_args *args, const void *dout, i
     p.dv = dv;
     p.delta = static_cast<float *>(workspace);
     int launches = 0;
-    const cudaError_t e = gn::launch_packed_attn_backward(p, d.sm_count, wait_timeout_ns(),
+    const cudaError_t e = gn::launch_packed_attn_backward(p, d.sm_count,
+                                                          {wait_timeout_ns(), d.status_word, d.status_host},
                                                           static_cast<cudaStream_t>(stream), &launches);
     return launched(e, launches);
 }

@@ -61,7 +61,13 @@ struct RopeArgs {
 
 cudaError_t launch_rope(const RopeArgs &a, int sm_count, cudaStream_t s);
 
-// ---- attention of packed documents (pattn_kernels.cu) -----------------------
+// ---- attention of packed documents (pattn_*.cu) ------------------------------
+// The bound on a kernel's waits, and the words that tell when one ran out.
+struct WaitLimit {
+    uint64_t timeout_ns;
+    unsigned int *status, *host_status;   // device addresses
+};
+
 struct PackedAttn {
     gn_attn_packed_args a;
     int group;                    // query heads per key / value head
@@ -72,9 +78,11 @@ struct PackedAttn {
     float *delta;                 // [heads][tokens_q]
 };
 
-cudaError_t launch_packed_attn(const PackedAttn &p, int sm_count, uint64_t timeout_ns, cudaStream_t s, int *launches);
+// On the tensor cores (pattn_forward.cu); tokens_q and tokens_k at least 1.
+cudaError_t launch_packed_attn_tiles(const PackedAttn &p, const WaitLimit &limit, cudaStream_t s);
+cudaError_t launch_packed_attn(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s, int *launches);
 size_t packed_attn_workspace_bytes(int64_t tokens_q, int heads);
-cudaError_t launch_packed_attn_backward(const PackedAttn &p, int sm_count, uint64_t timeout_ns, cudaStream_t s,
+cudaError_t launch_packed_attn_backward(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s,
                                         int *launches);
 
 }  // namespace gn

@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "block_internal.h"
+#include "gn_ptx.cuh"
 
 namespace gn {
 namespace pattn {
@@ -92,6 +93,14 @@ __device__ __forceinline__ float tanh_full(float x)
 {
     const float e = ex2_approx(2.0f * kLog2e * fabsf(x));
     return copysignf(1.0f - 2.0f * __frcp_rn(1.0f + e), x);
+}
+
+// The same in four instructions (rcp.approx: 2^-23 of a quotient of at most
+// 1), for the kernels that do it for every score.
+__device__ __forceinline__ float tanh_fast(float x)
+{
+    const float e = ex2_approx(2.0f * kLog2e * fabsf(x));
+    return copysignf(fmaf(-2.0f, rcp_approx(1.0f + e), 1.0f), x);
 }
 
 // The score of a pair in units of log2 (dot: q . k unscaled), and in `slack`

@@ -1,0 +1,443 @@
+// pattn_forward.cu -- packed attention's forward pass on the tensor cores.
+//
+// A CTA takes two tiles of 128 queries of one head (packed along the token
+// axis, whatever documents they belong to: a query's keys are one run, so a
+// tile's keys are the run from its queries' first to their last) and streams
+// the keys and values in blocks of 128 through a ring of shared memory:
+//   S_t = Q_t K^T            tcgen05, fp32 in tensor memory (128 columns a tile)
+//   P_t = 2^(S_t c - m)      one query per thread of tile t's four warps; the
+//                            half-precision weights go back to tensor memory,
+//                            over the scores
+//   O_t += P_t V             P from tensor memory, V read MN-major
+// While the warps of one tile turn scores into weights, the tensor core works
+// for the other.  m is a running maximum that only moves when a score is more
+// than 2^8 above it (the weights stay below 2^8), which is when O and the row
+// sum are rescaled; the row sum adds the unrounded weights, so lse is exact to
+// fp32.  fp16 weights are kept 2^7 higher, away from its subnormals.
+// Only blocks that some query of the tile sees in part are masked; there the
+// values are also looked over for infinities and NaN (0 x NaN is not 0).
+#include <algorithm>
+
+#include "pattn_tiles.cuh"
+
+namespace gn {
+
+namespace {
+
+using namespace pattn;
+
+constexpr int kThreads = 384;    // warps: 0 loads, 1 MMA, 4-7 and 8-11 the two tiles' softmax
+constexpr int kStages = 4;       // ring of key and value tiles, in the order K0 V0 K1 V1 ...
+constexpr float kRescaleLog2 = 8.0f;
+
+enum Bar { kQFull = 0, kFull = 2, kEmpty = kFull + kStages, kSFull = kEmpty + kStages, kPFull = kSFull + 2,
+           kOFull = kPFull + 2, kDrain = kOFull + 2, kBars };
+
+struct Layout {
+    uint32_t q, ring, bars, words, total;
+};
+
+__host__ __device__ inline Layout layout(int halves)
+{
+    Layout l;
+    const uint32_t tile = kHalfBytes * static_cast<uint32_t>(halves);
+    l.q = 0;
+    l.ring = 2 * tile;
+    l.bars = l.ring + kStages * tile;
+    l.words = l.bars + 8 * kBars;      // tensor-memory slot, abort, bad[2], 2 x 4 x 4 range words
+    l.total = l.words + 4 * (4 + 32);
+    return l;
+}
+
+// One query computed by one warp (four channels per lane) without ever
+// touching a key that it does not see.
+template <typename T>
+__device__ __noinline__ void row_forward(const gn_attn_packed_args &a, int group, int i, int h)
+{
+    const int lane = threadIdx.x & 31, hk = h / group;
+    const Span s = query_span(a, i);
+    const float slope = a.slopes ? a.slopes[h] : 0.f;
+    const float4 q = load4<T>(a.q, i * a.q_token + h * a.q_head, lane, a.dim);
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = s.lo; j < s.hi; ++j) {
+        const float4 k = load4<T>(a.k, j * a.k_token + hk * a.k_head, lane, a.dim);
+        const float4 v = load4<T>(a.v, j * a.v_token + hk * a.v_head, lane, a.dim);
+        float slack;
+        const float t = score_log2(a, slope, warp_sum(dot4(q, k)), s.pos, j, slack);
+        if (t > m) {
+            const float f = m == -INFINITY ? 0.f : ex2_approx(m - t);
+            l *= f;
+            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+            m = t;
+        }
+        const float w = t == -INFINITY ? 0.f : ex2_approx(t - m);
+        l += w;
+        axpy4(o, w, v);
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    store4<T>(a.out, (static_cast<int64_t>(i) * a.heads + h) * a.dim, lane, a.dim,
+              l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    if (lane == 0)
+        a.lse[static_cast<int64_t>(h) * a.tokens_q + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Where a query's row stands towards the block at j0: its run of keys and its
+// own position, relative to the block.
+struct RowBlock {
+    int lo, len, pos;
+    float slope2, cap_log2, inv_cap, c;
+};
+
+// Score number n of the block, in units of log2 (GENERAL: capped, biased, or
+// a scale that is not positive; otherwise the raw score, scaled in the
+// exponent).
+template <bool GENERAL>
+__device__ __forceinline__ float score(float s, int n, const RowBlock &r)
+{
+    if (!GENERAL) return s;
+    float t = s * r.c;
+    if (r.cap_log2 > 0.f) t = r.cap_log2 * tanh_fast(s * r.inv_cap);
+    return fmaf(-r.slope2, fabsf(static_cast<float>(r.pos - n)), t);
+}
+
+template <typename T, bool GENERAL>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ TileArgs args)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *const gbase = smem_raw + (base - raw);
+    const gn_attn_packed_args &a = args.p.a;
+    const int halves = a.dim > 64 ? 2 : 1;
+    const Layout lay = layout(halves);
+    const uint32_t tile_bytes = kHalfBytes * static_cast<uint32_t>(halves);
+    const auto bar = [&](int i) { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
+    volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(gbase + lay.words);
+    volatile int *abort = reinterpret_cast<volatile int *>(words + 1);
+    int *bad = reinterpret_cast<int *>(gbase + lay.words + 8);
+    volatile int *range = reinterpret_cast<volatile int *>(words + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x % a.heads, hk = h / args.p.group;
+    // the last tiles first: with causal runs they have the most keys
+    const int row0 = (args.tiles - 1 - static_cast<int>(blockIdx.x / a.heads)) * 2 * kTile;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i >= kPFull && i < kPFull + 2 ? 4 : 1);
+        *abort = (*reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) ? 1 : 0;
+        bad[0] = 0x7fffffff;
+        bad[1] = -1;
+        mbar_init_fence();
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+    }
+    if (warp == 1) {
+        tmem_alloc(base + lay.words, 512);
+        tmem_relinquish();
+    }
+    tc::griddep_wait();
+    if (threadIdx.x == 0) tc::griddep_launch_dependents();
+
+    // every query's run of keys, and what the tiles make of them: the keys that
+    // any query sees, and those that all see
+    Span span = {0, 0, 0};
+    const int tile = warp >= 8 ? 1 : 0, row = row0 + tile * kTile + (warp & 3) * 32 + lane;
+    if (warp >= 4) {
+        span = query_span_warp(a, row, lane);
+        const bool live = row < a.tokens_q, some = live && span.lo < span.hi;
+        const int lo = __reduce_min_sync(0xffffffffu, some ? span.lo : 0x7fffffff);
+        const int hi = __reduce_max_sync(0xffffffffu, some ? span.hi : 0);
+        const int all_lo = __reduce_max_sync(0xffffffffu, !live ? 0 : (some ? span.lo : 0x7fffffff));
+        const int all_hi = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : (some ? span.hi : 0));
+        if (lane == 0) {
+            volatile int *w = range + ((warp - 4) * 4);
+            w[0] = lo;
+            w[1] = hi;
+            w[2] = all_lo;
+            w[3] = all_hi;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = words[0];
+    int key0 = 0x7fffffff, key1 = 0, lo[2], hi[2], all_lo = 0, all_hi = 0x7fffffff;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        lo[t] = 0x7fffffff;
+        hi[t] = 0;
+        for (int w = 0; w < 4; ++w) {
+            volatile int *r = range + (t * 4 + w) * 4;
+            lo[t] = min(lo[t], r[0]);
+            hi[t] = max(hi[t], r[1]);
+            if (t == tile) {
+                all_lo = max(all_lo, r[2]);
+                all_hi = min(all_hi, r[3]);
+            }
+        }
+        key0 = min(key0, lo[t]);
+        key1 = max(key1, hi[t]);
+    }
+    // blocks of 128 keys from key0; tile t works on blocks [first[t], last[t])
+    int first[2], last[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        first[t] = lo[t] < hi[t] ? (lo[t] - key0) / kTile : 0;
+        last[t] = lo[t] < hi[t] ? (hi[t] - key0 + kTile - 1) / kTile : 0;
+    }
+    const int blocks = key0 < key1 ? (key1 - key0 + kTile - 1) / kTile : 0;
+    const bool skip = *abort != 0;
+
+    if (warp == 0) {
+        if (lane == 0 && !skip) {
+            // ---- loads ----
+            for (int t = 0; t < 2; ++t)
+                if (first[t] < last[t]) {
+                    mbar_arrive_expect_tx(bar(kQFull + t), tile_bytes);
+                    load_tile(base + lay.q + t * tile_bytes, &map_q, halves, h, row0 + t * kTile, bar(kQFull + t));
+                }
+            int n = 0;
+            bool go = true;
+            for (; go && n < 2 * blocks; ++n) {
+                const int st = n % kStages;
+                if (n >= kStages && !wait(bar(kEmpty + st), (n / kStages - 1) & 1, abort, args.limit)) {
+                    go = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(bar(kFull + st), tile_bytes);
+                load_tile(base + lay.ring + st * tile_bytes, (n & 1) ? &map_v : &map_k, halves, hk,
+                          key0 + (n >> 1) * kTile, bar(kFull + st));
+            }
+            // nothing is left in flight when the CTA ends, whatever became of the others
+            for (int k = max(0, n - kStages); k < n; ++k)
+                tc::drain(bar(kFull + k % kStages), (k / kStages) & 1, args.limit.timeout_ns);
+            for (int t = 0; t < 2; ++t)
+                if (first[t] < last[t]) tc::drain(bar(kQFull + t), 0, args.limit.timeout_ns);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && !skip) {
+            // ---- MMA: per block and tile the weighted values of the block
+            // before, then the scores of this one ----
+            const int steps = (a.dim + 15) / 16;
+            const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
+            bool go = true;
+            for (int b = 0; go && b <= blocks; ++b) {
+                const int nv = 2 * b - 1, nk = 2 * b;
+                bool have_v = false, have_k = false;
+                for (int t = 0; go && t < 2; ++t) {
+                    if (b - 1 >= first[t] && b - 1 < last[t]) {
+                        if (!have_v) go = wait(bar(kFull + nv % kStages), (nv / kStages) & 1, abort, args.limit);
+                        have_v = true;
+                        go = go && wait(bar(kPFull + t), (b - 1 - first[t]) & 1, abort, args.limit);
+                        if (!go) break;
+                        tc_fence_after_sync();
+                        mma_channels(tmem + 256 + 128 * t, tmem + 128 * t, base + lay.ring + (nv % kStages) * tile_bytes,
+                                     io, b - 1 > first[t]);
+                        if (b == last[t]) umma_commit(bar(kOFull + t));
+                    }
+                    if (b >= first[t] && b < last[t]) {
+                        if (!have_k) go = wait(bar(kFull + nk % kStages), (nk / kStages) & 1, abort, args.limit);
+                        have_k = true;
+                        if (b == first[t]) go = go && wait(bar(kQFull + t), 0, abort, args.limit);
+                        if (!go) break;
+                        mma_tokens(tmem + 128 * t, base + lay.q + t * tile_bytes,
+                                   base + lay.ring + (nk % kStages) * tile_bytes, steps, is);
+                        umma_commit(bar(kSFull + t));
+                    }
+                }
+                if (!go) break;
+                if (b > 0) {
+                    if (!have_v) go = wait(bar(kFull + nv % kStages), (nv / kStages) & 1, abort, args.limit);
+                    umma_commit(bar(kEmpty + nv % kStages));
+                }
+                if (b < blocks) {
+                    if (!have_k) go = go && wait(bar(kFull + nk % kStages), (nk / kStages) & 1, abort, args.limit);
+                    umma_commit(bar(kEmpty + nk % kStages));
+                }
+            }
+            umma_commit(bar(kDrain));
+            tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+        }
+    } else if (warp >= 4) {
+        // ---- softmax: one query per thread ----
+        constexpr float kShift = IsBf16<T>::value ? 0.f : 7.f;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + 128 * tile, to = tmem + lanes + 256 + 128 * tile;
+        const int b0 = tile ? first[1] : first[0], b1 = tile ? last[1] : last[0];
+        RowBlock rb = {};
+        if (GENERAL) {
+            rb.c = args.scale_log2;
+            rb.cap_log2 = a.cap * kLog2e;
+            rb.inv_cap = a.cap > 0.f ? a.scale / a.cap : 0.f;
+            rb.slope2 = a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
+        }
+        const float c = GENERAL ? 1.0f : args.scale_log2;
+        float m = -INFINITY, l = 0.f;
+        bool go = !skip;
+        for (int b = b0; go && b < b1; ++b) {
+            const int j0 = key0 + b * kTile;
+            const bool masked = j0 < all_lo || j0 + kTile > all_hi;
+            rb.lo = span.lo - j0;
+            rb.len = max(0, span.hi - span.lo);
+            rb.pos = span.pos - j0;
+            go = wait_warp(bar(kSFull + tile), (b - b0) & 1, abort, args.limit);
+            if (!go) break;
+            tc_fence_after_sync();
+            // one sweep over the block's scores: their maximum, the weights
+            // against m and the weights' sum
+            uint32_t pk[64];
+            float mx, sum;
+            const auto sweep = [&](float m_use, auto weigh, auto mask) {
+                mx = -INFINITY;
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float s[32];
+                    tmem_ld32(ts + 32 * q, s);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        s[k] = score<GENERAL>(s[k], 32 * q + k, rb);
+                        if (mask) s[k] = static_cast<unsigned>(32 * q + k - rb.lo) < static_cast<unsigned>(rb.len) ? s[k] : -INFINITY;
+                        mx = fmaxf(mx, s[k]);
+                    }
+                    if (weigh) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            s[k] = ex2_approx(fmaf(s[k], c, -m_use));
+                            part[k & 3] += s[k];
+                        }
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) pk[16 * q + k] = Half2<T>::pack(s[2 * k], s[2 * k + 1]);
+                    }
+                }
+                mx *= c;
+                sum = (part[0] + part[1]) + (part[2] + part[3]);
+            };
+            const auto run = [&](float m_use, auto weigh) {
+                if (masked)
+                    sweep(m_use, weigh, std::true_type{});
+                else
+                    sweep(m_use, weigh, std::false_type{});
+            };
+            if (b == b0) {
+                run(0.f, std::false_type{});
+                m = mx - kShift;
+            }
+            run(m == -INFINITY ? 0.f : m, std::true_type{});
+            const bool grew = mx > m + (kShift + kRescaleLog2);
+            if (__any_sync(0xffffffffu, grew)) {
+                const float top = grew ? mx - kShift : m;
+                const float f = grew && m != -INFINITY ? ex2_approx(m - top) : 1.0f;
+                m = top;
+                l *= f;
+                if (b > b0) {
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        float o[32];
+                        uint32_t u[32];
+                        tmem_ld32(to + 32 * q, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * f);
+                        tmem_st32(to + 32 * q, u);
+                    }
+                }
+                run(m == -INFINITY ? 0.f : m, std::true_type{});
+            }
+            l += sum;
+            tmem_st32(ts, pk);
+            tmem_st32(ts + 32, pk + 32);
+            if (masked) {
+                const int nv = 2 * b + 1, r = (warp & 3) * 32 + lane;
+                go = wait_warp(bar(kFull + nv % kStages), (nv / kStages) & 1, abort, args.limit);
+                if (go)
+                    clear_not_finite<T>(base + lay.ring + (nv % kStages) * tile_bytes, r, j0 + r, key0, key1, halves, bad);
+            }
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kPFull + tile));
+        }
+        if (b0 < b1 && go) go = wait_warp(bar(kOFull + tile), 0, abort, args.limit);
+        named_sync(1, 256);   // both tiles are done with looking at the values
+        if (go) {
+            tc_fence_after_sync();
+            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            T *dst = static_cast<T *>(a.out) + (static_cast<int64_t>(row) * a.heads + h) * a.dim;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                if (32 * q >= a.dim) break;
+                float o[32];
+                if (b0 < b1) {
+                    tmem_ld32(to + 32 * q, o);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int ch = 32 * q + 8 * k;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = l == 0.f ? 0u : Half2<T>::pack(o[8 * k + 2 * e] * inv, o[8 * k + 2 * e + 1] * inv);
+                    if (row < a.tokens_q && ch < a.dim)
+                        *reinterpret_cast<uint4 *>(dst + ch) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            if (row < a.tokens_q)
+                a.lse[static_cast<int64_t>(h) * a.tokens_q + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            // queries that see a value row which was cleared
+            unsigned again = __ballot_sync(0xffffffffu, row < a.tokens_q && span.lo < span.hi && span.lo <= bad[1] &&
+                                                            span.hi > bad[0]);
+            for (; again; again &= again - 1) row_forward<T>(a, args.p.group, row - lane + __ffs(again) - 1, h);
+        }
+        tc_fence_before_sync();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, bool GENERAL>
+cudaError_t launch(const TileArgs &args, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                   cudaStream_t s)
+{
+    const int halves = args.p.a.dim > 64 ? 2 : 1;
+    const size_t smem = layout(halves).total + 1024;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(attn_forward_kernel<T, GENERAL>),
+                                       layout(2).total + 1024, done);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = static_cast<int64_t>(args.tiles) * args.p.a.heads;
+    return tc::launch_pdl(attn_forward_kernel<T, GENERAL>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, mq,
+                          mk, mv, args);
+}
+
+}  // namespace
+
+cudaError_t launch_packed_attn_tiles(const PackedAttn &p, const WaitLimit &limit, cudaStream_t s)
+{
+    const gn_attn_packed_args &a = p.a;
+    const bool bf16 = a.format == GN_FORMAT_BF16;
+    CUtensorMap mq, mk, mv;
+    if (!encode_heads(&mq, a.q, bf16, a.tokens_q, a.q_token, a.heads, a.q_head, a.dim) ||
+        !encode_heads(&mk, a.k, bf16, a.tokens_k, a.k_token, a.kv_heads, a.k_head, a.dim) ||
+        !encode_heads(&mv, a.v, bf16, a.tokens_k, a.v_token, a.kv_heads, a.v_head, a.dim))
+        return cudaErrorInvalidValue;
+    TileArgs args = {};
+    args.p = p;
+    args.scale_log2 = a.scale * kLog2e;
+    args.limit = limit;
+    args.tiles = static_cast<int>((a.tokens_q + 2 * kTile - 1) / (2 * kTile));
+    const bool general = a.cap > 0.f || a.slopes || !(a.scale > 0.f);
+    if (bf16)
+        return general ? launch<__nv_bfloat16, true>(args, mq, mk, mv, s) : launch<__nv_bfloat16, false>(args, mq, mk, mv, s);
+    return general ? launch<__half, true>(args, mq, mk, mv, s) : launch<__half, false>(args, mq, mk, mv, s);
+}
+
+}  // namespace gn

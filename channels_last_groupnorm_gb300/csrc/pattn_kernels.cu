@@ -422,15 +422,19 @@ size_t packed_attn_workspace_bytes(int64_t tokens_q, int heads)
     return (static_cast<size_t>(tokens_q) * static_cast<size_t>(heads) * sizeof(float) + 255) / 256 * 256;
 }
 
-cudaError_t launch_packed_attn(const PackedAttn &p, int sm_count, uint64_t, cudaStream_t s, int *launches)
+cudaError_t launch_packed_attn(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s, int *launches)
 {
-    const cudaError_t e = p.a.format == GN_FORMAT_BF16 ? rows_forward<__nv_bfloat16>(p, sm_count, s)
+    cudaError_t e;
+    if (p.a.tokens_k > 0 && p.a.tokens_q > static_cast<int64_t>(4) * p.a.docs)
+        e = launch_packed_attn_tiles(p, limit, s);
+    else
+        e = p.a.format == GN_FORMAT_BF16 ? rows_forward<__nv_bfloat16>(p, sm_count, s)
                                                        : rows_forward<__half>(p, sm_count, s);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
 
-cudaError_t launch_packed_attn_backward(const PackedAttn &p, int, uint64_t, cudaStream_t s, int *launches)
+cudaError_t launch_packed_attn_backward(const PackedAttn &p, int, const WaitLimit &, cudaStream_t s, int *launches)
 {
     return p.a.format == GN_FORMAT_BF16 ? rows_backward<__nv_bfloat16>(p, s, launches)
                                         : rows_backward<__half>(p, s, launches);

@@ -1,0 +1,237 @@
+// pattn_tiles.cuh -- what the tensor-core kernels of packed attention share:
+// the shared-memory tiles and their descriptors, the MMA loops, the bounded
+// waits, and the tensor maps.
+//
+// A tile is 128 tokens of one head: one or two halves of 64 channels, each
+// [128][64] half-precision elements in rows of 128 bytes (128-byte swizzle, as
+// the tensor-map loads write them; channels past the head's width and tokens
+// past the end come as zeros).  The same tile serves as a K-major operand
+// (channels are the contraction) and as an MN-major one (tokens are).
+#pragma once
+
+#include <cuda.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "gn_ptx.cuh"
+#include "pattn_common.cuh"
+#include "tc_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace gn {
+
+namespace pattn {
+
+constexpr int kTile = 128;
+constexpr uint32_t kHalfBytes = kTile * 64 * 2;   // one half of a tile
+
+struct TileArgs {
+    PackedAttn p;
+    float scale_log2;
+    WaitLimit limit;
+    int tiles;             // tile groups along the token axis that the CTAs own
+};
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort, const WaitLimit &l)
+{
+    return tc::wait(bar, parity, abort, l.timeout_ns, l.status, l.host_status);
+}
+
+// The same for a whole warp, with one answer.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort, const WaitLimit &l)
+{
+    return __all_sync(0xffffffffu, wait(bar, parity, abort, l));
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int c0, int c1, int c2, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+// One tile: `halves` loads on one barrier (the caller has armed it).
+__device__ __forceinline__ void load_tile(uint32_t dst, const void *map, int halves, int head, int token, uint32_t bar)
+{
+    for (int n = 0; n < halves; ++n) tma_load_3d(dst + n * kHalfBytes, map, n * 64, head, token, bar);
+}
+
+// Matrix descriptor of a tile read MN-major (the 64 channels of a row are
+// contiguous along M or N, tokens along the contraction), 128-byte swizzle:
+// 16 KB from one group of 64 channels to the next (leading offset), 1 KB from 8
+// tokens to the next 8 (stride offset); a contraction step of 16 tokens
+// advances the start by 2 KB.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem)
+{
+    uint64_t d = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(kHalfBytes >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// Instruction descriptor: fp32 accumulator, M = 128, both operands of type T;
+// b_mn: the shared-memory B operand is MN-major.
+template <typename T> struct IsBf16 { static constexpr bool value = false; };
+template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; };
+
+template <typename T>
+__device__ __forceinline__ uint32_t instruction(int n, bool b_mn)
+{
+    const uint32_t fmt = IsBf16<T>::value ? 1u : 0u;
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(kTile >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A is 128 rows, one per lane, two elements per column.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// D = A B^T over the channels of two tiles (128 x 128, `steps` of 16 channels).
+__device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc)
+{
+    for (int k = 0; k < steps; ++k) {
+        const uint32_t at = static_cast<uint32_t>(k >> 2) * kHalfBytes + static_cast<uint32_t>(k & 3) * 32u;
+        umma_f16(d, sw128_kmajor_desc(a + at), sw128_kmajor_desc(b + at), idesc, k > 0);
+    }
+}
+
+// D (+)= A B over the 128 tokens of a tile: A in tensor memory (64 columns).
+__device__ __forceinline__ void mma_channels(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool accumulate)
+{
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        umma_ts(d, a_tmem + 8u * k, sw128_mnmajor_desc(b + 2048u * k), idesc, accumulate || k > 0);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
+{
+    uint32_t u[32];
+    tmem_ld_32x32b_x32(taddr, u);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+          "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+          "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Row r of a tile holds an infinity or a NaN.
+template <typename T>
+__device__ __forceinline__ bool row_not_finite(uint32_t tile, int r, int halves)
+{
+    constexpr uint32_t kExp = IsBf16<T>::value ? 0x7f80u : 0x7c00u;
+    uint32_t most = 0;
+    for (int h = 0; h < halves; ++h) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const uint4 v = lds128(tile + h * kHalfBytes + static_cast<uint32_t>(r) * 128u + c * 16u);
+            most = __vmaxu2(most, v.x & 0x7fff7fffu);
+            most = __vmaxu2(most, v.y & 0x7fff7fffu);
+            most = __vmaxu2(most, v.z & 0x7fff7fffu);
+            most = __vmaxu2(most, v.w & 0x7fff7fffu);
+        }
+    }
+    return (most & 0xffffu) >= kExp || (most >> 16) >= kExp;
+}
+
+__device__ __forceinline__ void zero_row(uint32_t tile, int r, int halves)
+{
+    for (int h = 0; h < halves; ++h)
+        for (int c = 0; c < 8; ++c)
+            sts128(tile + h * kHalfBytes + static_cast<uint32_t>(r) * 128u + c * 16u, make_uint4(0u, 0u, 0u, 0u));
+}
+
+// A whole tile's look at its rows (one per thread) ahead of a product whose
+// weights are zero for some of them: 0 x NaN is not 0.  A row with an infinity
+// or a NaN is cleared; if its token lies in [lo, hi), where something in the
+// CTA may see it, it is also noted in bad[0..1] (first and last such token):
+// whatever sees one of those is computed again, one by one, at the end.
+template <typename T>
+__device__ __forceinline__ void clear_not_finite(uint32_t tile, int r, int token, int lo, int hi, int halves, int *bad)
+{
+    if (row_not_finite<T>(tile, r, halves)) {
+        zero_row(tile, r, halves);
+        if (token >= lo && token < hi) {
+            atomicMin(bad, token);
+            atomicMax(bad + 1, token);
+        }
+    }
+    fence_proxy_async_smem();
+}
+
+// Document of `token` for a whole warp: with up to 32 documents their ends
+// come in one load and are handed round, otherwise every lane searches.
+__device__ __forceinline__ int doc_of_warp(const int32_t *ends, int docs, int token, int lane)
+{
+    if (docs > 32) return doc_of(ends, docs, token);
+    const int first = __ldg(ends), end = __ldg(ends + 1 + min(lane, docs - 1));
+    int d = 0;
+    for (int n = 0; n < docs - 1; ++n) d += __shfl_sync(0xffffffffu, end, n) <= token;
+    const int last = __shfl_sync(0xffffffffu, end, d);
+    return token >= first && token < last ? d : -1;
+}
+
+__device__ __forceinline__ Span query_span_warp(const gn_attn_packed_args &a, int i, int lane)
+{
+    const int d = a.cu_q ? doc_of_warp(a.cu_q, a.docs, i, lane) : 0;
+    if (d < 0) return Span{0, 0, 0};
+    return query_span_in(a, doc_bounds(a, d), i);
+}
+
+// Lets `kernel` have `bytes` of dynamic shared memory, once per device.
+inline cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (e != cudaSuccess || (dev < 64 && (done.load() & bit))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
+}
+
+// Tensor map over [tokens][heads][dim] with boxes of 128 tokens x 64 channels.
+inline bool encode_heads(CUtensorMap *map, const void *base, bool bf16, int64_t tokens, int64_t token_stride, int heads,
+                         int64_t head_stride, int dim)
+{
+    const tc::EncodeTiledFn fn = tc::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    // an axis of one has no stride of its own
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? head_stride : dim) * 2,
+                                   static_cast<cuuint64_t>(tokens > 1 ? token_stride : static_cast<int64_t>(heads) * dim) * 2};
+    const cuuint32_t box[3] = {64, 1, kTile};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace pattn
+}  // namespace gn
