@@ -383,10 +383,9 @@ int gn_attn_packed_backward(const gn_attn_packed_args *args, const void *dout, i
     p.dq = dq;
     p.dk = dk;
     p.dv = dv;
-    p.delta = static_cast<float *>(workspace);
+    p.workspace = workspace;
     int launches = 0;
-    const cudaError_t e = gn::launch_packed_attn_backward(p, d.sm_count,
-                                                          {wait_timeout_ns(), d.status_word, d.status_host},
+    const cudaError_t e = gn::launch_packed_attn_backward(p, {wait_timeout_ns(), d.status_word, d.status_host},
                                                           static_cast<cudaStream_t>(stream), &launches);
     return launched(e, launches);
 }

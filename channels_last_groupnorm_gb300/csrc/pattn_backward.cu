@@ -1,0 +1,772 @@
+// pattn_backward.cu -- packed attention's backward pass on the tensor cores:
+// three launches, every product a tcgen05 one and every sum in a fixed order.
+//
+//   attn_rows_info_kernel   per query: its run of keys; per query and head:
+//                           lse in units of log2 and delta = dout . out
+//   attn_dkv_kernel         a CTA owns 128 keys of one key / value head and
+//                           goes over the queries that see them, in blocks of
+//                           128, for every query head of the group:
+//     S^T = K Q^T, dP^T = V dO^T           (keys are the lanes)
+//     P^T = 2^(c S^T - lse),  dS^T = P^T (dP^T - delta) (1 - tanh^2)
+//     dV += P^T dO,  dK += dS^T Q          (P^T, dS^T from tensor memory)
+//   attn_dq_kernel          a CTA owns 128 queries of one head and goes over
+//                           their keys:  S = Q K^T, dP = dO V^T, dS, dQ += dS K
+//
+// Computing the scores in both costs 7 products of 128 x 128 x D per block
+// instead of 5, but dK, dV and dQ stay in tensor memory to the end: no fp32
+// atomics, so the same inputs give the same bits, and the shared heads' sums
+// are part of the accumulation.
+//
+// In either kernel the tensor core always has the other half of the work in
+// hand while the eight softmax warps (two per lane quarter, 64 columns each)
+// do theirs: weights are made while dK and the next dP run, score gradients
+// while dV and the next S run.  P and dS overwrite S and dP in place, every
+// warp within the columns that it has read.
+#include <algorithm>
+
+#include "pattn_tiles.cuh"
+
+namespace gn {
+namespace {
+
+using namespace pattn;
+
+constexpr int kThreads = 384;    // warps: 0 loads, 1 MMA, 4-11 softmax
+constexpr int kStages = 2;       // pairs of tiles in flight
+
+// Per query: the run of keys it sees and where it stands; per query and head:
+// (lse log2, delta).  Padded to whole blocks so that 128 rows can be copied
+// from any multiple of 4; padding rows see nothing.
+struct Info {
+    float2 *row;      // [heads][padded]
+    int4 *span;       // [padded]
+    int64_t padded;
+};
+
+__host__ __device__ inline int64_t padded_rows(int64_t tokens_q) { return (tokens_q + 2 * kTile - 1) / kTile * kTile; }
+
+template <typename T>
+__global__ void __launch_bounds__(256) attn_rows_info_kernel(const __grid_constant__ PackedAttn p, const Info info)
+{
+    tc::griddep_wait();
+    if (threadIdx.x == 0) tc::griddep_launch_dependents();
+    const gn_attn_packed_args &a = p.a;
+    // sixteen lanes (eight channels each) per query and head
+    const int lane = threadIdx.x & 31, place = lane & 15;
+    const int64_t n = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;
+    const int64_t i = n / a.heads;
+    const int h = static_cast<int>(n % a.heads);
+    if (n >= info.padded * a.heads) return;
+    if (h == 0 && place == 0) {
+        Span s = {0, 0, 0};
+        if (i < a.tokens_q) s = query_span(a, static_cast<int>(i));
+        info.span[i] = make_int4(s.lo, s.hi, s.pos, 0);
+    }
+    float s = 0.f;
+    if (i < a.tokens_q && place * 8 < a.dim) {
+        float x[8], g[8];
+        unpack8<T>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.out) + n * a.dim + place * 8)), x);
+        unpack8<T>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.dout) + i * p.dout_token + h * p.dout_head + place * 8)), g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(x[e], g[e], s);
+    }
+    const unsigned group = 0xffffu << (lane & 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(group, s, o);
+    if (place == 0) {
+        // a row without keys (lse -inf) weighs nothing anywhere
+        float lse = i < a.tokens_q ? a.lse[static_cast<int64_t>(h) * a.tokens_q + i] * kLog2e : INFINITY;
+        if (lse == -INFINITY) lse = INFINITY;
+        info.row[static_cast<int64_t>(h) * info.padded + i] = make_float2(lse, s);
+    }
+}
+
+// ---- one row by one warp, for what sees a row that was cleared -----------------
+template <typename T>
+__device__ __noinline__ void row_dq(const PackedAttn &p, const Info &info, int i, int h)
+{
+    const gn_attn_packed_args &a = p.a;
+    const int lane = threadIdx.x & 31, hk = h / p.group;
+    const int4 s = info.span[i];
+    const float2 row = info.row[static_cast<int64_t>(h) * info.padded + i];
+    const float slope = a.slopes ? a.slopes[h] : 0.f;
+    const float4 q = load4<T>(a.q, i * a.q_token + h * a.q_head, lane, a.dim);
+    const float4 g = load4<T>(p.dout, i * p.dout_token + h * p.dout_head, lane, a.dim);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = s.x; j < s.y; ++j) {
+        const float4 k = load4<T>(a.k, j * a.k_token + hk * a.k_head, lane, a.dim);
+        const float4 v = load4<T>(a.v, j * a.v_token + hk * a.v_head, lane, a.dim);
+        float slack;
+        const float t = score_log2(a, slope, warp_sum(dot4(q, k)), s.z, j, slack);
+        axpy4(acc, ex2_approx(t - row.x) * (warp_sum(dot4(g, v)) - row.y) * slack * a.scale, k);
+    }
+    store4<T>(p.dq, (static_cast<int64_t>(i) * a.heads + h) * a.dim, lane, a.dim, acc);
+}
+
+template <typename T>
+__device__ __noinline__ void row_dkv(const PackedAttn &p, const Info &info, int j, int hk)
+{
+    const gn_attn_packed_args &a = p.a;
+    const int lane = threadIdx.x & 31;
+    const Span s = key_span(a, j);
+    const float4 k = load4<T>(a.k, j * a.k_token + hk * a.k_head, lane, a.dim);
+    const float4 v = load4<T>(a.v, j * a.v_token + hk * a.v_head, lane, a.dim);
+    float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
+    for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
+        const float slope = a.slopes ? a.slopes[h] : 0.f;
+        for (int i = s.lo; i < s.hi; ++i) {
+            const float4 q = load4<T>(a.q, i * a.q_token + h * a.q_head, lane, a.dim);
+            const float4 g = load4<T>(p.dout, i * p.dout_token + h * p.dout_head, lane, a.dim);
+            const float2 row = info.row[static_cast<int64_t>(h) * info.padded + i];
+            float slack;
+            const float t = score_log2(a, slope, warp_sum(dot4(q, k)), info.span[i].z, j, slack);
+            const float w = ex2_approx(t - row.x);
+            axpy4(dv, w, g);
+            axpy4(dk, w * (warp_sum(dot4(g, v)) - row.y) * slack * a.scale, q);
+        }
+    }
+    store4<T>(p.dk, (static_cast<int64_t>(j) * a.kv_heads + hk) * a.dim, lane, a.dim, dk);
+    store4<T>(p.dv, (static_cast<int64_t>(j) * a.kv_heads + hk) * a.dim, lane, a.dim, dv);
+}
+
+// A score's exponent without its lse, and the slope of the cap there.
+struct Bend {
+    float c, cap_log2, inv_cap, slope2;
+};
+
+__device__ __forceinline__ Bend bend_of(const TileArgs &args, int h)
+{
+    const gn_attn_packed_args &a = args.p.a;
+    return {args.scale_log2, a.cap * kLog2e, a.cap > 0.f ? a.scale / a.cap : 0.f,
+            a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f};
+}
+
+__device__ __forceinline__ float bent(const Bend &b, float s, int far, float &slack)
+{
+    float t = s * b.c;
+    slack = 1.0f;
+    if (b.cap_log2 > 0.f) {
+        const float th = tanh_fast(s * b.inv_cap);
+        t = b.cap_log2 * th;
+        slack = fmaf(-th, th, 1.0f);
+    }
+    return fmaf(-b.slope2, fabsf(static_cast<float>(far)), t);
+}
+
+// Barriers and words of either kernel.  Own: the tiles a CTA owns; Full /
+// Empty: the pairs that stream by; S / Dp: an MMA result is there; P / Ds: the
+// softmax warps have put theirs in its place; Out: the accumulators are done.
+enum Bar { kOwn = 0, kFull, kEmpty = kFull + kStages, kS = kEmpty + kStages, kDp, kP, kDs, kOut, kDrain, kBars };
+constexpr int kSoftWarps = 8;
+
+__device__ __forceinline__ void init_bars(uint32_t bars)
+{
+    for (int i = 0; i < kBars; ++i) mbar_init(bars + 8u * i, i == kP || i == kDs ? kSoftWarps : 1);
+    mbar_init_fence();
+}
+
+// Writes one accumulator's rows: 64 channels (half 0 or 1) of the warp's 32
+// tokens, scaled and rounded once.
+template <typename T>
+__device__ __forceinline__ void store_half(void *out, int64_t row_offset, bool live, bool any, uint32_t taddr, int half,
+                                           int dim, float scale)
+{
+#pragma unroll 1
+    for (int q = 2 * half; q < 2 * half + 2; ++q) {
+        if (32 * q >= dim) break;
+        float o[32];
+        if (any) {
+            tmem_ld32(taddr + 32 * q, o);
+            tmem_wait_ld();
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = any ? Half2<T>::pack(o[8 * k + 2 * e] * scale, o[8 * k + 2 * e + 1] * scale) : 0u;
+            if (live && 32 * q + 8 * k < dim)
+                *reinterpret_cast<uint4 *>(static_cast<T *>(out) + row_offset + 32 * q + 8 * k) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dK and dV
+// ---------------------------------------------------------------------------
+struct KvLayout {
+    uint32_t own, ring, stage, rows, spans, bars, words, total;
+};
+
+__host__ __device__ inline KvLayout kv_layout(int halves)
+{
+    KvLayout l;
+    const uint32_t tile = kHalfBytes * static_cast<uint32_t>(halves);
+    l.own = 0;                                  // K, V
+    l.ring = 2 * tile;                          // kStages x (Q, dO)
+    l.stage = 2 * tile;
+    l.rows = l.ring + kStages * l.stage;        // kStages x 128 (lse, delta)
+    l.spans = l.rows + kStages * kTile * 8;     // kStages x 128 runs of keys
+    l.bars = l.spans + kStages * kTile * 16;
+    l.words = l.bars + 8 * kBars;               // tensor-memory slot, abort, bad[2], 8 x 4 range words
+    l.total = l.words + 4 * (4 + 32);
+    return l;
+}
+
+template <typename T, bool GENERAL>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+                    const __grid_constant__ TileArgs args, const Info info)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *const gbase = smem_raw + (base - raw);
+    const gn_attn_packed_args &a = args.p.a;
+    const int halves = a.dim > 64 ? 2 : 1, group = args.p.group;
+    const KvLayout lay = kv_layout(halves);
+    const uint32_t tile_bytes = kHalfBytes * static_cast<uint32_t>(halves);
+    const auto bar = [&](int i) { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
+    volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(gbase + lay.words);
+    volatile int *abort = reinterpret_cast<volatile int *>(words + 1);
+    int *bad = reinterpret_cast<int *>(gbase + lay.words + 8);
+    volatile int *range = reinterpret_cast<volatile int *>(words + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int hk = blockIdx.x % a.kv_heads;
+    // the first tiles first: with causal runs the most queries see them
+    const int key0 = static_cast<int>(blockIdx.x / a.kv_heads) * kTile;
+
+    if (threadIdx.x == 0) {
+        init_bars(bar(0));
+        *abort = (*reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) ? 1 : 0;
+        bad[0] = 0x7fffffff;
+        bad[1] = -1;
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+        prefetch_tensormap(&map_do);
+    }
+    if (warp == 1) {
+        tmem_alloc(base + lay.words, 512);
+        tmem_relinquish();
+    }
+    tc::griddep_wait();
+    if (threadIdx.x == 0) tc::griddep_launch_dependents();
+
+    // the queries that see any of the tile's keys, and those that see all
+    const int row = (warp & 3) * 32 + lane, key = key0 + row;
+    Span span = {0, 0, 0};
+    if (warp >= 4) {
+        if (key < a.tokens_k) span = key_span(a, key);
+        const bool live = key < a.tokens_k, some = live && span.lo < span.hi;
+        const int lo = __reduce_min_sync(0xffffffffu, some ? span.lo : 0x7fffffff);
+        const int hi = __reduce_max_sync(0xffffffffu, some ? span.hi : 0);
+        const int all_lo = __reduce_max_sync(0xffffffffu, !live ? 0 : (some ? span.lo : 0x7fffffff));
+        const int all_hi = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : (some ? span.hi : 0));
+        if (lane == 0) {
+            volatile int *w = range + ((warp - 4) * 4);
+            w[0] = lo;
+            w[1] = hi;
+            w[2] = all_lo;
+            w[3] = all_hi;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = words[0];
+    int q_lo = 0x7fffffff, q_hi = 0, all_lo = 0, all_hi = 0x7fffffff;
+    for (int w = 0; w < 4; ++w) {
+        q_lo = min(q_lo, range[4 * w]);
+        q_hi = max(q_hi, range[4 * w + 1]);
+        all_lo = max(all_lo, range[4 * w + 2]);
+        all_hi = min(all_hi, range[4 * w + 3]);
+    }
+    const bool any = q_lo < q_hi;
+    const int q0 = q_lo & ~3;                   // the rows' records are copied from a multiple of 32 bytes
+    const int blocks = any ? (q_hi - q0 + kTile - 1) / kTile : 0;
+    const int steps_all = blocks * group;       // query heads outermost
+    const bool skip = *abort != 0;
+    const uint32_t k_tile = base + lay.own, v_tile = k_tile + tile_bytes;
+    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dk = tmem + 256, t_dv = tmem + 384;
+
+    if (warp == 0) {
+        if (lane == 0 && !skip && any) {
+            mbar_arrive_expect_tx(bar(kOwn), 2 * tile_bytes);
+            load_tile(k_tile, &map_k, halves, hk, key0, bar(kOwn));
+            load_tile(v_tile, &map_v, halves, hk, key0, bar(kOwn));
+            int n = 0;
+            for (; n < steps_all; ++n) {
+                const int st = n % kStages, h = hk * group + n / blocks, i0 = q0 + (n % blocks) * kTile;
+                if (n >= kStages && !wait(bar(kEmpty + st), (n / kStages - 1) & 1, abort, args.limit)) break;
+                const uint32_t dst = base + lay.ring + st * lay.stage;
+                mbar_arrive_expect_tx(bar(kFull + st), 2 * tile_bytes + kTile * 8 + kTile * 16);
+                load_tile(dst, &map_q, halves, h, i0, bar(kFull + st));
+                load_tile(dst + tile_bytes, &map_do, halves, h, i0, bar(kFull + st));
+                bulk_load(base + lay.rows + st * kTile * 8, info.row + static_cast<int64_t>(h) * info.padded + i0,
+                          kTile * 8, bar(kFull + st));
+                bulk_load(base + lay.spans + st * kTile * 16, info.span + i0, kTile * 16, bar(kFull + st));
+            }
+            for (int k = max(0, n - kStages); k < n; ++k)
+                tc::drain(bar(kFull + k % kStages), (k / kStages) & 1, args.limit.timeout_ns);
+            tc::drain(bar(kOwn), 0, args.limit.timeout_ns);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && !skip && any) {
+            const int steps = (a.dim + 15) / 16;
+            const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
+            bool go = wait(bar(kOwn), 0, abort, args.limit) && wait(bar(kFull), 0, abort, args.limit);
+            if (go) {
+                tc_fence_after_sync();
+                mma_tokens(t_s, k_tile, base + lay.ring, steps, is);
+                umma_commit(bar(kS));
+                mma_tokens(t_dp, v_tile, base + lay.ring + tile_bytes, steps, is);
+                umma_commit(bar(kDp));
+            }
+            for (int n = 0; go && n < steps_all; ++n) {
+                const int st = n % kStages, nx = (n + 1) % kStages;
+                const uint32_t q_tile = base + lay.ring + st * lay.stage, q_next = base + lay.ring + nx * lay.stage;
+                const bool more = n + 1 < steps_all;
+                if (!(go = wait(bar(kP), n & 1, abort, args.limit))) break;
+                tc_fence_after_sync();
+                mma_channels(t_dv, t_s, 64, q_tile + tile_bytes, io, n > 0);
+                if (more) {
+                    if (!(go = wait(bar(kFull + nx), ((n + 1) / kStages) & 1, abort, args.limit))) break;
+                    mma_tokens(t_s, k_tile, q_next, steps, is);
+                    umma_commit(bar(kS));
+                }
+                if (!(go = wait(bar(kDs), n & 1, abort, args.limit))) break;
+                tc_fence_after_sync();
+                mma_channels(t_dk, t_dp, 64, q_tile, io, n > 0);
+                umma_commit(bar(kEmpty + st));
+                if (more) {
+                    mma_tokens(t_dp, v_tile, q_next + tile_bytes, steps, is);
+                    umma_commit(bar(kDp));
+                }
+            }
+            if (go) umma_commit(bar(kOut));
+            umma_commit(bar(kDrain));
+            tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+        }
+    } else if (warp >= 4) {
+        // ---- softmax: one key per thread, 64 of a block's queries per warp ----
+        const int half = (warp - 4) >> 2;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        bool go = !skip;
+        Bend bend = {};
+        for (int n = 0; go && n < steps_all; ++n) {
+            const int st = n % kStages, i0 = q0 + (n % blocks) * kTile;
+            const bool masked = i0 < all_lo || i0 + kTile > all_hi;
+            if (GENERAL && n % blocks == 0) bend = bend_of(args, hk * group + n / blocks);
+            const uint32_t rows = base + lay.rows + (st * kTile + 64 * half) * 8;
+            const uint32_t spans = base + lay.spans + (st * kTile + 64 * half) * 16;
+            const uint32_t q_tile = base + lay.ring + st * lay.stage;
+            // (the rows' records came with the tiles that S was made from)
+            go = wait_warp(bar(kFull + st), (n / kStages) & 1, abort, args.limit) &&
+                 wait_warp(bar(kS), n & 1, abort, args.limit);
+            if (!go) break;
+            tc_fence_after_sync();
+            float w[64];                         // weights, then times the cap's slope
+            const auto weigh = [&](auto mask) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float s[32];
+                    uint32_t pk[16];
+                    tmem_ld32(t_s + lanes + 64 * half + 32 * q, s);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const uint4 r = lds128(rows + (32 * q + k) * 8);
+                        const float lse[2] = {__uint_as_float(r.x), __uint_as_float(r.z)};
+                        float p[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int col = 32 * q + k + e;
+                            float slack = 1.0f, t;
+                            int4 sp = make_int4(0, 0, 0, 0);
+                            if (mask || (GENERAL && a.slopes)) {
+                                const uint4 v = lds128(spans + col * 16);
+                                sp = make_int4(v.x, v.y, v.z, 0);
+                            }
+                            if (GENERAL)
+                                t = bent(bend, s[k + e], sp.z - key, slack) - lse[e];
+                            else
+                                t = fmaf(s[k + e], args.scale_log2, -lse[e]);
+                            p[e] = ex2_approx(t);
+                            w[col] = GENERAL ? p[e] * slack : p[e];
+                            if (mask && (key < sp.x || key >= sp.y)) p[e] = w[col] = 0.f;
+                        }
+                        pk[k / 2] = Half2<T>::pack(p[0], p[1]);
+                    }
+                    tmem_st16(t_s + lanes + 64 * half + 16 * q, pk);
+                }
+            };
+            if (masked)
+                weigh(std::true_type{});
+            else
+                weigh(std::false_type{});
+            if (masked) {
+                const int r = (warp & 3) * 32 + lane;
+                clear_not_finite<T>(q_tile + (half ? tile_bytes : 0), r, i0 + r, q_lo, q_hi, halves, bad);
+            }
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kP));
+
+            go = wait_warp(bar(kDp), n & 1, abort, args.limit);
+            if (!go) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float dp[32];
+                uint32_t pk[16];
+                tmem_ld32(t_dp + lanes + 64 * half + 32 * q, dp);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    const uint4 r = lds128(rows + (32 * q + k) * 8);
+                    float d0 = w[32 * q + k] * (dp[k] - __uint_as_float(r.y));
+                    float d1 = w[32 * q + k + 1] * (dp[k + 1] - __uint_as_float(r.w));
+                    if (masked) {
+                        // a weight of zero times what an unseen row holds
+                        d0 = w[32 * q + k] == 0.f ? 0.f : d0;
+                        d1 = w[32 * q + k + 1] == 0.f ? 0.f : d1;
+                    }
+                    pk[k / 2] = Half2<T>::pack(d0, d1);
+                }
+                tmem_st16(t_dp + lanes + 64 * half + 16 * q, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kDs));
+        }
+        if (any && go) go = wait_warp(bar(kOut), 0, abort, args.limit);
+        if (!bar_any(1, 256, !go)) {   // one answer for all: there is another barrier inside
+            tc_fence_after_sync();
+            const int64_t at = (static_cast<int64_t>(key) * a.kv_heads + hk) * a.dim;
+            const bool live = key < a.tokens_k;
+            store_half<T>(args.p.dk, at, live, any, t_dk + lanes, half, a.dim, a.scale);
+            store_half<T>(args.p.dv, at, live, any, t_dv + lanes, half, a.dim, 1.0f);
+            named_sync(1, 256);
+            unsigned again = __ballot_sync(0xffffffffu, live && span.lo < span.hi && span.lo <= bad[1] && span.hi > bad[0]);
+            for (int n = 0; again; again &= again - 1, ++n)
+                if ((n & 1) == half) row_dkv<T>(args.p, info, key - lane + __ffs(again) - 1, hk);
+        }
+        tc_fence_before_sync();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dQ
+// ---------------------------------------------------------------------------
+struct QLayout {
+    uint32_t own, ring, stage, bars, words, total;
+};
+
+__host__ __device__ inline QLayout q_layout(int halves)
+{
+    QLayout l;
+    const uint32_t tile = kHalfBytes * static_cast<uint32_t>(halves);
+    l.own = 0;                                  // Q, dO
+    l.ring = 2 * tile;                          // kStages x (K, V)
+    l.stage = 2 * tile;
+    l.bars = l.ring + kStages * l.stage;
+    l.words = l.bars + 8 * kBars;
+    l.total = l.words + 4 * (4 + 32);
+    return l;
+}
+
+template <typename T, bool GENERAL>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+                   const __grid_constant__ TileArgs args, const Info info)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *const gbase = smem_raw + (base - raw);
+    const gn_attn_packed_args &a = args.p.a;
+    const int halves = a.dim > 64 ? 2 : 1;
+    const QLayout lay = q_layout(halves);
+    const uint32_t tile_bytes = kHalfBytes * static_cast<uint32_t>(halves);
+    const auto bar = [&](int i) { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
+    volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(gbase + lay.words);
+    volatile int *abort = reinterpret_cast<volatile int *>(words + 1);
+    int *bad = reinterpret_cast<int *>(gbase + lay.words + 8);
+    volatile int *range = reinterpret_cast<volatile int *>(words + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x % a.heads, hk = h / args.p.group;
+    const int row0 = (args.tiles - 1 - static_cast<int>(blockIdx.x / a.heads)) * kTile;
+
+    if (threadIdx.x == 0) {
+        init_bars(bar(0));
+        *abort = (*reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) ? 1 : 0;
+        bad[0] = 0x7fffffff;
+        bad[1] = -1;
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+        prefetch_tensormap(&map_do);
+    }
+    if (warp == 1) {
+        tmem_alloc(base + lay.words, 512);
+        tmem_relinquish();
+    }
+    tc::griddep_wait();
+    if (threadIdx.x == 0) tc::griddep_launch_dependents();
+
+    const int r = (warp & 3) * 32 + lane, row = row0 + r;   // (row < info.padded)
+    int4 span = make_int4(0, 0, 0, 0);
+    float2 stat = make_float2(INFINITY, 0.f);
+    if (warp >= 4) {
+        span = info.span[row];
+        stat = info.row[static_cast<int64_t>(h) * info.padded + row];
+        const bool live = row < a.tokens_q, some = live && span.x < span.y;
+        const int lo = __reduce_min_sync(0xffffffffu, some ? span.x : 0x7fffffff);
+        const int hi = __reduce_max_sync(0xffffffffu, some ? span.y : 0);
+        const int all_lo = __reduce_max_sync(0xffffffffu, !live ? 0 : (some ? span.x : 0x7fffffff));
+        const int all_hi = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : (some ? span.y : 0));
+        if (lane == 0) {
+            volatile int *w = range + ((warp - 4) * 4);
+            w[0] = lo;
+            w[1] = hi;
+            w[2] = all_lo;
+            w[3] = all_hi;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = words[0];
+    int key0 = 0x7fffffff, key1 = 0, all_lo = 0, all_hi = 0x7fffffff;
+    for (int w = 0; w < 4; ++w) {
+        key0 = min(key0, range[4 * w]);
+        key1 = max(key1, range[4 * w + 1]);
+        all_lo = max(all_lo, range[4 * w + 2]);
+        all_hi = min(all_hi, range[4 * w + 3]);
+    }
+    const bool any = key0 < key1;
+    const int blocks = any ? (key1 - key0 + kTile - 1) / kTile : 0;
+    const bool skip = *abort != 0;
+    const uint32_t q_tile = base + lay.own, do_tile = q_tile + tile_bytes;
+    // two buffers of scores (their gradients go over them)
+    const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;
+
+    if (warp == 0) {
+        if (lane == 0 && !skip && any) {
+            mbar_arrive_expect_tx(bar(kOwn), 2 * tile_bytes);
+            load_tile(q_tile, &map_q, halves, h, row0, bar(kOwn));
+            load_tile(do_tile, &map_do, halves, h, row0, bar(kOwn));
+            int n = 0;
+            for (; n < blocks; ++n) {
+                const int st = n % kStages;
+                if (n >= kStages && !wait(bar(kEmpty + st), (n / kStages - 1) & 1, abort, args.limit)) break;
+                const uint32_t dst = base + lay.ring + st * lay.stage;
+                mbar_arrive_expect_tx(bar(kFull + st), 2 * tile_bytes);
+                load_tile(dst, &map_k, halves, hk, key0 + n * kTile, bar(kFull + st));
+                load_tile(dst + tile_bytes, &map_v, halves, hk, key0 + n * kTile, bar(kFull + st));
+            }
+            for (int k = max(0, n - kStages); k < n; ++k)
+                tc::drain(bar(kFull + k % kStages), (k / kStages) & 1, args.limit.timeout_ns);
+            tc::drain(bar(kOwn), 0, args.limit.timeout_ns);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && !skip && any) {
+            const int steps = (a.dim + 15) / 16;
+            const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
+            bool go = wait(bar(kOwn), 0, abort, args.limit) && wait(bar(kFull), 0, abort, args.limit);
+            if (go) {
+                tc_fence_after_sync();
+                mma_tokens(t_s, q_tile, base + lay.ring, steps, is);
+                umma_commit(bar(kS));
+                mma_tokens(t_dp, do_tile, base + lay.ring + tile_bytes, steps, is);
+                umma_commit(bar(kDp));
+            }
+            for (int n = 0; go && n < blocks; ++n) {
+                const int st = n % kStages, nx = (n + 1) % kStages;
+                const uint32_t k_tile = base + lay.ring + st * lay.stage, k_next = base + lay.ring + nx * lay.stage;
+                const bool more = n + 1 < blocks;
+                if (more) {
+                    if (!(go = wait(bar(kFull + nx), ((n + 1) / kStages) & 1, abort, args.limit))) break;
+                    mma_tokens(t_s + 128 * ((n + 1) & 1), q_tile, k_next, steps, is);
+                    umma_commit(bar(kS));
+                }
+                if (!(go = wait(bar(kDs), n & 1, abort, args.limit))) break;
+                tc_fence_after_sync();
+                if (more) {
+                    mma_tokens(t_dp, do_tile, k_next + tile_bytes, steps, is);
+                    umma_commit(bar(kDp));
+                }
+                mma_channels(t_dq, t_s + 128 * (n & 1), 64, k_tile, io, n > 0);
+                umma_commit(bar(kEmpty + st));
+            }
+            if (go) umma_commit(bar(kOut));
+            umma_commit(bar(kDrain));
+            tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+        }
+    } else if (warp >= 4) {
+        // ---- softmax: one query per thread, 64 of a block's keys per warp ----
+        const int half = (warp - 4) >> 2;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        Bend bend = {};
+        if (GENERAL) bend = bend_of(args, h);
+        bool go = !skip;
+        for (int n = 0; go && n < blocks; ++n) {
+            const int j0 = key0 + n * kTile, st = n % kStages;
+            const bool masked = j0 < all_lo || j0 + kTile > all_hi;
+            const int lo = span.x - j0, len = max(0, span.y - span.x);
+            const uint32_t ts = t_s + lanes + 128 * (n & 1) + 64 * half;
+            go = wait_warp(bar(kS), n & 1, abort, args.limit);
+            if (!go) break;
+            tc_fence_after_sync();
+            float w[64];
+            const auto weigh = [&](auto mask) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float s[32];
+                    tmem_ld32(ts + 32 * q, s);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int col = 64 * half + 32 * q + k;
+                        float slack = 1.0f, t;
+                        if (GENERAL)
+                            t = bent(bend, s[k], span.z - j0 - col, slack) - stat.x;
+                        else
+                            t = fmaf(s[k], args.scale_log2, -stat.x);
+                        w[32 * q + k] = ex2_approx(t) * slack;
+                        if (mask && static_cast<unsigned>(col - lo) >= static_cast<unsigned>(len)) w[32 * q + k] = 0.f;
+                    }
+                }
+            };
+            if (masked)
+                weigh(std::true_type{});
+            else
+                weigh(std::false_type{});
+            go = wait_warp(bar(kDp), n & 1, abort, args.limit);
+            if (!go) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float dp[32];
+                uint32_t pk[16];
+                tmem_ld32(t_dp + lanes + 64 * half + 32 * q, dp);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    float d0 = w[32 * q + k] * (dp[k] - stat.y);
+                    float d1 = w[32 * q + k + 1] * (dp[k + 1] - stat.y);
+                    if (masked) {
+                        d0 = w[32 * q + k] == 0.f ? 0.f : d0;
+                        d1 = w[32 * q + k + 1] == 0.f ? 0.f : d1;
+                    }
+                    pk[k / 2] = Half2<T>::pack(d0, d1);
+                }
+                tmem_st16(ts + 16 * q, pk);
+            }
+            if (masked && half == 0)
+                clear_not_finite<T>(base + lay.ring + st * lay.stage, r, j0 + r, key0, key1, halves, bad);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kDs));
+        }
+        if (any && go) go = wait_warp(bar(kOut), 0, abort, args.limit);
+        if (!bar_any(1, 256, !go)) {   // one answer for all: there is another barrier inside
+            tc_fence_after_sync();
+            const bool live = row < a.tokens_q;
+            store_half<T>(args.p.dq, (static_cast<int64_t>(row) * a.heads + h) * a.dim, live, any, t_dq + lanes, half, a.dim,
+                          a.scale);
+            named_sync(1, 256);
+            unsigned again = __ballot_sync(0xffffffffu, live && span.x < span.y && span.x <= bad[1] && span.y > bad[0]);
+            for (int n = 0; again; again &= again - 1, ++n)
+                if ((n & 1) == half) row_dq<T>(args.p, info, row - lane + __ffs(again) - 1, h);
+        }
+        tc_fence_before_sync();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, bool GENERAL>
+cudaError_t launch(const TileArgs &args, const CUtensorMap (&map)[4], const Info &info, cudaStream_t s, int *launches)
+{
+    const gn_attn_packed_args &a = args.p.a;
+    const int halves = a.dim > 64 ? 2 : 1;
+    static std::atomic<uint64_t> done_kv{0}, done_q{0};
+    cudaError_t e = allow_shared(reinterpret_cast<const void *>(attn_dkv_kernel<T, GENERAL>), kv_layout(2).total + 1024, done_kv);
+    if (e == cudaSuccess)
+        e = allow_shared(reinterpret_cast<const void *>(attn_dq_kernel<T, GENERAL>), q_layout(2).total + 1024, done_q);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = info.padded * a.heads;
+    e = tc::launch_pdl(attn_rows_info_kernel<T>, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0, s, args.p, info);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    TileArgs kv = args, q = args;
+    kv.tiles = static_cast<int>((a.tokens_k + kTile - 1) / kTile);
+    q.tiles = static_cast<int>((a.tokens_q + kTile - 1) / kTile);
+    e = tc::launch_pdl(attn_dkv_kernel<T, GENERAL>, dim3(static_cast<unsigned>(static_cast<int64_t>(kv.tiles) * a.kv_heads)),
+                       dim3(kThreads), kv_layout(halves).total + 1024, s, map[0], map[1], map[2], map[3], kv, info);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    e = tc::launch_pdl(attn_dq_kernel<T, GENERAL>, dim3(static_cast<unsigned>(static_cast<int64_t>(q.tiles) * a.heads)),
+                       dim3(kThreads), q_layout(halves).total + 1024, s, map[0], map[1], map[2], map[3], q, info);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+}  // namespace
+
+size_t packed_attn_workspace_bytes(int64_t tokens_q, int heads)
+{
+    return static_cast<size_t>(padded_rows(tokens_q)) * (16 + 8 * static_cast<size_t>(heads));
+}
+
+cudaError_t launch_packed_attn_backward(const PackedAttn &p, const WaitLimit &limit, cudaStream_t s, int *launches)
+{
+    const gn_attn_packed_args &a = p.a;
+    if (a.tokens_q == 0 || a.tokens_k == 0) {
+        const size_t q = 2u * static_cast<size_t>(a.tokens_q) * a.heads * a.dim;
+        const size_t k = 2u * static_cast<size_t>(a.tokens_k) * a.kv_heads * a.dim;
+        cudaError_t e = q ? cudaMemsetAsync(p.dq, 0, q, s) : cudaSuccess;
+        if (e == cudaSuccess && k) e = cudaMemsetAsync(p.dk, 0, k, s);
+        if (e == cudaSuccess && k) e = cudaMemsetAsync(p.dv, 0, k, s);
+        return e;
+    }
+    const bool bf16 = a.format == GN_FORMAT_BF16;
+    CUtensorMap map[4];
+    if (!encode_heads(&map[0], a.q, bf16, a.tokens_q, a.q_token, a.heads, a.q_head, a.dim) ||
+        !encode_heads(&map[1], a.k, bf16, a.tokens_k, a.k_token, a.kv_heads, a.k_head, a.dim) ||
+        !encode_heads(&map[2], a.v, bf16, a.tokens_k, a.v_token, a.kv_heads, a.v_head, a.dim) ||
+        !encode_heads(&map[3], p.dout, bf16, a.tokens_q, p.dout_token, a.heads, p.dout_head, a.dim))
+        return cudaErrorInvalidValue;
+    TileArgs args = {};
+    args.p = p;
+    args.scale_log2 = a.scale * kLog2e;
+    args.limit = limit;
+    Info info;
+    info.padded = padded_rows(a.tokens_q);
+    info.span = static_cast<int4 *>(p.workspace);
+    info.row = reinterpret_cast<float2 *>(info.span + info.padded);
+    const bool general = a.cap > 0.f || a.slopes;
+    if (bf16)
+        return general ? launch<__nv_bfloat16, true>(args, map, info, s, launches)
+                       : launch<__nv_bfloat16, false>(args, map, info, s, launches);
+    return general ? launch<__half, true>(args, map, info, s, launches)
+                   : launch<__half, false>(args, map, info, s, launches);
+}
+
+}  // namespace gn

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         go = go && wait(bar(kPFull + t), (b - 1 - first[t]) & 1, abort, args.limit);
                         if (!go) break;
                         tc_fence_after_sync();
-                        mma_channels(tmem + 256 + 128 * t, tmem + 128 * t, base + lay.ring + (nv % kStages) * tile_bytes,
+                        mma_channels(tmem + 256 + 128 * t, tmem + 128 * t, 32, base + lay.ring + (nv % kStages) * tile_bytes,
                                      io, b - 1 > first[t]);
                         if (b == last[t]) umma_commit(bar(kOFull + t));
                     }
@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (row < a.tokens_q)
                 a.lse[static_cast<int64_t>(h) * a.tokens_q + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             // queries that see a value row which was cleared
+            __syncwarp();
             unsigned again = __ballot_sync(0xffffffffu, row < a.tokens_q && span.lo < span.hi && span.lo <= bad[1] &&
                                                             span.hi > bad[0]);
             for (; again; again &= again - 1) row_forward<T>(a, args.p.group, row - lane + __ffs(again) - 1, h);

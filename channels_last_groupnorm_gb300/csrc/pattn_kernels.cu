@@ -263,97 +263,6 @@ __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const PackedAttn
 }
 
 // ---------------------------------------------------------------------------
-// Backward, one warp per row (four channels per lane).
-// ---------------------------------------------------------------------------
-template <typename T>
-__global__ void __launch_bounds__(256) attn_delta_kernel(const PackedAttn p)
-{
-    tc::griddep_wait();
-    if (threadIdx.x == 0) tc::griddep_launch_dependents();
-    const gn_attn_packed_args &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (n >= a.tokens_q * a.heads) return;
-    const int64_t i = n / a.heads;
-    const int h = static_cast<int>(n % a.heads);
-    const float4 x = load4<T>(a.out, n * a.dim, lane, a.dim);
-    const float4 g = load4<T>(p.dout, i * p.dout_token + h * p.dout_head, lane, a.dim);
-    const float s = warp_sum(dot4(x, g));
-    if (lane == 0) p.delta[static_cast<int64_t>(h) * a.tokens_q + i] = s;
-}
-
-template <typename T>
-__device__ __forceinline__ void row_dq(const PackedAttn &p, int i, int h, int lane)
-{
-    const gn_attn_packed_args &a = p.a;
-    const Span s = query_span(a, i);
-    const int hk = h / p.group;
-    const float slope = a.slopes ? a.slopes[h] : 0.f;
-    const float4 q = load4<T>(a.q, i * a.q_token + h * a.q_head, lane, a.dim);
-    const float4 g = load4<T>(p.dout, i * p.dout_token + h * p.dout_head, lane, a.dim);
-    const float lse = a.lse[static_cast<int64_t>(h) * a.tokens_q + i] * kLog2e;
-    const float delta = p.delta[static_cast<int64_t>(h) * a.tokens_q + i];
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = s.lo; j < s.hi; ++j) {
-        const float4 k = load4<T>(a.k, j * a.k_token + hk * a.k_head, lane, a.dim);
-        const float4 v = load4<T>(a.v, j * a.v_token + hk * a.v_head, lane, a.dim);
-        float slack;
-        const float t = score_log2(a, slope, warp_sum(dot4(q, k)), s.pos, j, slack);
-        const float ds = ex2_approx(t - lse) * (warp_sum(dot4(g, v)) - delta) * slack;
-        axpy4(acc, ds * a.scale, k);
-    }
-    store4<T>(p.dq, (static_cast<int64_t>(i) * a.heads + h) * a.dim, lane, a.dim, acc);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) attn_dq_rows_kernel(const PackedAttn p)
-{
-    tc::griddep_wait();
-    if (threadIdx.x == 0) tc::griddep_launch_dependents();
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (n >= p.a.tokens_q * p.a.heads) return;
-    row_dq<T>(p, static_cast<int>(n / p.a.heads), static_cast<int>(n % p.a.heads), threadIdx.x & 31);
-}
-
-template <typename T>
-__device__ __forceinline__ void row_dkv(const PackedAttn &p, int j, int hk, int lane)
-{
-    const gn_attn_packed_args &a = p.a;
-    const Span s = key_span(a, j);
-    const float4 k = load4<T>(a.k, j * a.k_token + hk * a.k_head, lane, a.dim);
-    const float4 v = load4<T>(a.v, j * a.v_token + hk * a.v_head, lane, a.dim);
-    float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
-    for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
-        const float slope = a.slopes ? a.slopes[h] : 0.f;
-        for (int i = s.lo; i < s.hi; ++i) {
-            const float4 q = load4<T>(a.q, i * a.q_token + h * a.q_head, lane, a.dim);
-            const float4 g = load4<T>(p.dout, i * p.dout_token + h * p.dout_head, lane, a.dim);
-            const float lse = a.lse[static_cast<int64_t>(h) * a.tokens_q + i] * kLog2e;
-            const float delta = p.delta[static_cast<int64_t>(h) * a.tokens_q + i];
-            float slack;
-            const int pos = a.slopes ? query_span(a, i).pos : 0;
-            const float t = score_log2(a, slope, warp_sum(dot4(q, k)), pos, j, slack);
-            const float w = ex2_approx(t - lse);
-            const float ds = w * (warp_sum(dot4(g, v)) - delta) * slack;
-            axpy4(dv, w, g);
-            axpy4(dk, ds * a.scale, q);
-        }
-    }
-    store4<T>(p.dk, (static_cast<int64_t>(j) * a.kv_heads + hk) * a.dim, lane, a.dim, dk);
-    store4<T>(p.dv, (static_cast<int64_t>(j) * a.kv_heads + hk) * a.dim, lane, a.dim, dv);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) attn_dkv_rows_kernel(const PackedAttn p)
-{
-    tc::griddep_wait();
-    if (threadIdx.x == 0) tc::griddep_launch_dependents();
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (n >= p.a.tokens_k * p.a.kv_heads) return;
-    row_dkv<T>(p, static_cast<int>(n / p.a.kv_heads), static_cast<int>(n % p.a.kv_heads), threadIdx.x & 31);
-}
-
-// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 template <typename T, int LPK, int HC, int UN>
@@ -397,30 +306,7 @@ cudaError_t rows_forward(const PackedAttn &p, int sm_count, cudaStream_t s)
     return p.a.dim <= 64 ? launch_rows_heads<T, 8>(p, splits, s) : launch_rows_heads<T, 16>(p, splits, s);
 }
 
-template <typename T>
-cudaError_t rows_backward(const PackedAttn &p, cudaStream_t s, int *launches)
-{
-    const auto blocks = [](int64_t rows) { return dim3(static_cast<unsigned>((rows + 7) / 8)); };
-    cudaError_t e = cudaSuccess;
-    if (p.a.tokens_q > 0) {
-        e = tc::launch_pdl(attn_delta_kernel<T>, blocks(p.a.tokens_q * p.a.heads), dim3(256), 0, s, p);
-        if (e == cudaSuccess) ++*launches;
-        if (e == cudaSuccess) e = tc::launch_pdl(attn_dq_rows_kernel<T>, blocks(p.a.tokens_q * p.a.heads), dim3(256), 0, s, p);
-        if (e == cudaSuccess) ++*launches;
-    }
-    if (p.a.tokens_k > 0 && e == cudaSuccess) {
-        e = tc::launch_pdl(attn_dkv_rows_kernel<T>, blocks(p.a.tokens_k * p.a.kv_heads), dim3(256), 0, s, p);
-        if (e == cudaSuccess) ++*launches;
-    }
-    return e;
-}
-
 }  // namespace
-
-size_t packed_attn_workspace_bytes(int64_t tokens_q, int heads)
-{
-    return (static_cast<size_t>(tokens_q) * static_cast<size_t>(heads) * sizeof(float) + 255) / 256 * 256;
-}
 
 cudaError_t launch_packed_attn(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s, int *launches)
 {
@@ -432,12 +318,6 @@ cudaError_t launch_packed_attn(const PackedAttn &p, int sm_count, const WaitLimi
                                                        : rows_forward<__half>(p, sm_count, s);
     if (e == cudaSuccess) ++*launches;
     return e;
-}
-
-cudaError_t launch_packed_attn_backward(const PackedAttn &p, int, const WaitLimit &, cudaStream_t s, int *launches)
-{
-    return p.a.format == GN_FORMAT_BF16 ? rows_backward<__nv_bfloat16>(p, s, launches)
-                                        : rows_backward<__half>(p, s, launches);
 }
 
 }  // namespace gn

@@ -108,12 +108,14 @@ __device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, i
     }
 }
 
-// D (+)= A B over the 128 tokens of a tile: A in tensor memory (64 columns).
-__device__ __forceinline__ void mma_channels(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool accumulate)
+// D (+)= A B over the 128 tokens of a tile: A in tensor memory, 32 columns for
+// the first 64 tokens and, `second` columns further on, 32 for the others.
+__device__ __forceinline__ void mma_channels(uint32_t d, uint32_t a_tmem, uint32_t second, uint32_t b, uint32_t idesc,
+                                             bool accumulate)
 {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        umma_ts(d, a_tmem + 8u * k, sw128_mnmajor_desc(b + 2048u * k), idesc, accumulate || k > 0);
+        umma_ts(d, a_tmem + (k < 4 ? 8u * k : second + 8u * (k - 4)), sw128_mnmajor_desc(b + 2048u * k), idesc, accumulate || k > 0);
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
@@ -134,6 +136,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v)
           "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
           "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
           "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 
@@ -200,6 +212,21 @@ __device__ __forceinline__ Span query_span_warp(const gn_attn_packed_args &a, in
     const int d = a.cu_q ? doc_of_warp(a.cu_q, a.docs, i, lane) : 0;
     if (d < 0) return Span{0, 0, 0};
     return query_span_in(a, doc_bounds(a, d), i);
+}
+
+// A barrier of `count` threads that also tells whether any of them passed true.
+__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t count, bool pred)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "barrier.cta.red.or.pred p, %2, %3, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(pred ? 1u : 0u), "r"(id), "r"(count)
+        : "memory");
+    return r != 0;
 }
 
 // Lets `kernel` have `bytes` of dynamic shared memory, once per device.
