@@ -31,15 +31,15 @@ namespace {
 
 using namespace pattn;
 
-constexpr int kThreads = 384;    // warps: 0 loads, 1 MMA, 4-11 softmax
+constexpr int kThreads = 320;    // warps: 0 loads, 1 MMA, 2-9 softmax
 constexpr int kStages = 2;       // pairs of tiles in flight
 
 // Per query: the run of keys it sees and where it stands; per query and head:
-// (lse log2, delta).  Padded to whole blocks so that 128 rows can be copied
+// -lse in units of log2, and -delta.  Padded to whole blocks so that 128 rows can be copied
 // from any multiple of 4; padding rows see nothing.
 struct Info {
-    float2 *row;      // [heads][padded]
-    int4 *span;       // [padded]
+    float *lse, *delta;   // [heads][padded]
+    int4 *span;           // [padded]
     int64_t padded;
 };
 
@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(256) attn_rows_info_kernel(const __grid_consta
         // a row without keys (lse -inf) weighs nothing anywhere
         float lse = i < a.tokens_q ? a.lse[static_cast<int64_t>(h) * a.tokens_q + i] * kLog2e : INFINITY;
         if (lse == -INFINITY) lse = INFINITY;
-        info.row[static_cast<int64_t>(h) * info.padded + i] = make_float2(lse, s);
+        info.lse[static_cast<int64_t>(h) * info.padded + i] = -lse;
+        info.delta[static_cast<int64_t>(h) * info.padded + i] = -s;
     }
 }
 
@@ -88,7 +89,8 @@ __device__ __noinline__ void row_dq(const PackedAttn &p, const Info &info, int i
     const gn_attn_packed_args &a = p.a;
     const int lane = threadIdx.x & 31, hk = h / p.group;
     const int4 s = info.span[i];
-    const float2 row = info.row[static_cast<int64_t>(h) * info.padded + i];
+    const int64_t at = static_cast<int64_t>(h) * info.padded + i;
+    const float nlse = info.lse[at], ndelta = info.delta[at];
     const float slope = a.slopes ? a.slopes[h] : 0.f;
     const float4 q = load4<T>(a.q, i * a.q_token + h * a.q_head, lane, a.dim);
     const float4 g = load4<T>(p.dout, i * p.dout_token + h * p.dout_head, lane, a.dim);
@@ -98,7 +100,7 @@ __device__ __noinline__ void row_dq(const PackedAttn &p, const Info &info, int i
         const float4 v = load4<T>(a.v, j * a.v_token + hk * a.v_head, lane, a.dim);
         float slack;
         const float t = score_log2(a, slope, warp_sum(dot4(q, k)), s.z, j, slack);
-        axpy4(acc, ex2_approx(t - row.x) * (warp_sum(dot4(g, v)) - row.y) * slack * a.scale, k);
+        axpy4(acc, ex2_approx(t + nlse) * (warp_sum(dot4(g, v)) + ndelta) * slack * a.scale, k);
     }
     store4<T>(p.dq, (static_cast<int64_t>(i) * a.heads + h) * a.dim, lane, a.dim, acc);
 }
@@ -117,40 +119,39 @@ __device__ __noinline__ void row_dkv(const PackedAttn &p, const Info &info, int 
         for (int i = s.lo; i < s.hi; ++i) {
             const float4 q = load4<T>(a.q, i * a.q_token + h * a.q_head, lane, a.dim);
             const float4 g = load4<T>(p.dout, i * p.dout_token + h * p.dout_head, lane, a.dim);
-            const float2 row = info.row[static_cast<int64_t>(h) * info.padded + i];
+            const int64_t at = static_cast<int64_t>(h) * info.padded + i;
             float slack;
             const float t = score_log2(a, slope, warp_sum(dot4(q, k)), info.span[i].z, j, slack);
-            const float w = ex2_approx(t - row.x);
+            const float w = ex2_approx(t + info.lse[at]);
             axpy4(dv, w, g);
-            axpy4(dk, w * (warp_sum(dot4(g, v)) - row.y) * slack * a.scale, q);
+            axpy4(dk, w * (warp_sum(dot4(g, v)) + info.delta[at]) * slack * a.scale, q);
         }
     }
     store4<T>(p.dk, (static_cast<int64_t>(j) * a.kv_heads + hk) * a.dim, lane, a.dim, dk);
     store4<T>(p.dv, (static_cast<int64_t>(j) * a.kv_heads + hk) * a.dim, lane, a.dim, dv);
 }
 
-// A score's exponent without its lse, and the slope of the cap there.
-struct Bend {
-    float c, cap_log2, inv_cap, slope2;
-};
-
-__device__ __forceinline__ Bend bend_of(const TileArgs &args, int h)
+// Scores s[n] (raw, in place) to exponents in units of log2 before their lse,
+// capped and biased; far(n): distance of the pair.  slack[n]: the cap's slope.
+template <int N, typename Far>
+__device__ __forceinline__ void bend(float (&s)[N], float (&slack)[N], const TileArgs &args, float slope2, Far far)
 {
     const gn_attn_packed_args &a = args.p.a;
-    return {args.scale_log2, a.cap * kLog2e, a.cap > 0.f ? a.scale / a.cap : 0.f,
-            a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f};
-}
-
-__device__ __forceinline__ float bent(const Bend &b, float s, int far, float &slack)
-{
-    float t = s * b.c;
-    slack = 1.0f;
-    if (b.cap_log2 > 0.f) {
-        const float th = tanh_fast(s * b.inv_cap);
-        t = b.cap_log2 * th;
-        slack = fmaf(-th, th, 1.0f);
+    if (a.cap > 0.f) {
+        tanh_all(s, a.scale / a.cap);
+#pragma unroll
+        for (int n = 0; n < N; ++n) slack[n] = fmaf(-s[n], s[n], 1.0f);
+    } else {
+#pragma unroll
+        for (int n = 0; n < N; ++n) slack[n] = 1.0f;
     }
-    return fmaf(-b.slope2, fabsf(static_cast<float>(far)), t);
+    const float by = a.cap > 0.f ? a.cap * kLog2e : args.scale_log2;
+#pragma unroll
+    for (int n = 0; n < N; ++n) s[n] *= by;
+    if (a.slopes) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) s[n] = fmaf(-slope2, fabsf(far(n)), s[n]);
+    }
 }
 
 // Barriers and words of either kernel.  Own: the tiles a CTA owns; Full /
@@ -206,7 +207,7 @@ __host__ __device__ inline KvLayout kv_layout(int halves)
     l.own = 0;                                  // K, V
     l.ring = 2 * tile;                          // kStages x (Q, dO)
     l.stage = 2 * tile;
-    l.rows = l.ring + kStages * l.stage;        // kStages x 128 (lse, delta)
+    l.rows = l.ring + kStages * l.stage;        // kStages x (128 -lse, 128 -delta)
     l.spans = l.rows + kStages * kTile * 8;     // kStages x 128 runs of keys
     l.bars = l.spans + kStages * kTile * 16;
     l.words = l.bars + 8 * kBars;               // tensor-memory slot, abort, bad[2], 8 x 4 range words
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the queries that see any of the tile's keys, and those that see all
     const int row = (warp & 3) * 32 + lane, key = key0 + row;
     Span span = {0, 0, 0};
-    if (warp >= 4) {
+    if (warp >= 2) {
         if (key < a.tokens_k) span = key_span(a, key);
         const bool live = key < a.tokens_k, some = live && span.lo < span.hi;
         const int lo = __reduce_min_sync(0xffffffffu, some ? span.lo : 0x7fffffff);
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int all_lo = __reduce_max_sync(0xffffffffu, !live ? 0 : (some ? span.lo : 0x7fffffff));
         const int all_hi = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : (some ? span.hi : 0));
         if (lane == 0) {
-            volatile int *w = range + ((warp - 4) * 4);
+            volatile int *w = range + ((warp - 2) * 4);
             w[0] = lo;
             w[1] = hi;
             w[2] = all_lo;
@@ -304,8 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(bar(kFull + st), 2 * tile_bytes + kTile * 8 + kTile * 16);
                 load_tile(dst, &map_q, halves, h, i0, bar(kFull + st));
                 load_tile(dst + tile_bytes, &map_do, halves, h, i0, bar(kFull + st));
-                bulk_load(base + lay.rows + st * kTile * 8, info.row + static_cast<int64_t>(h) * info.padded + i0,
-                          kTile * 8, bar(kFull + st));
+                const int64_t at = static_cast<int64_t>(h) * info.padded + i0;
+                bulk_load(base + lay.rows + st * kTile * 8, info.lse + at, kTile * 4, bar(kFull + st));
+                bulk_load(base + lay.rows + st * kTile * 8 + kTile * 4, info.delta + at, kTile * 4, bar(kFull + st));
                 bulk_load(base + lay.spans + st * kTile * 16, info.span + i0, kTile * 16, bar(kFull + st));
             }
             for (int k = max(0, n - kStages); k < n; ++k)
@@ -330,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool more = n + 1 < steps_all;
                 if (!(go = wait(bar(kP), n & 1, abort, args.limit))) break;
                 tc_fence_after_sync();
-                mma_channels(t_dv, t_s, 64, q_tile + tile_bytes, io, n > 0);
+                mma_channels(t_dv, t_s, q_tile + tile_bytes, 0, io, n > 0);
+                mma_channels(t_dv, t_s + 64, q_tile + tile_bytes, 1, io, true);
                 if (more) {
                     if (!(go = wait(bar(kFull + nx), ((n + 1) / kStages) & 1, abort, args.limit))) break;
                     mma_tokens(t_s, k_tile, q_next, steps, is);
@@ -338,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!(go = wait(bar(kDs), n & 1, abort, args.limit))) break;
                 tc_fence_after_sync();
-                mma_channels(t_dk, t_dp, 64, q_tile, io, n > 0);
+                mma_channels(t_dk, t_dp, q_tile, 0, io, n > 0);
+                mma_channels(t_dk, t_dp + 64, q_tile, 1, io, true);
                 umma_commit(bar(kEmpty + st));
                 if (more) {
                     mma_tokens(t_dp, v_tile, q_next + tile_bytes, steps, is);
@@ -349,63 +353,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(bar(kDrain));
             tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
         }
-    } else if (warp >= 4) {
+    } else {
         // ---- softmax: one key per thread, 64 of a block's queries per warp ----
-        const int half = (warp - 4) >> 2;
+        const int half = (warp - 2) >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         bool go = !skip;
-        Bend bend = {};
+        float slope2 = 0.f;
         for (int n = 0; go && n < steps_all; ++n) {
             const int st = n % kStages, i0 = q0 + (n % blocks) * kTile;
             const bool masked = i0 < all_lo || i0 + kTile > all_hi;
-            if (GENERAL && n % blocks == 0) bend = bend_of(args, hk * group + n / blocks);
-            const uint32_t rows = base + lay.rows + (st * kTile + 64 * half) * 8;
-            const uint32_t spans = base + lay.spans + (st * kTile + 64 * half) * 16;
+            if (GENERAL && a.slopes && n % blocks == 0) slope2 = __ldg(a.slopes + hk * group + n / blocks) * kLog2e;
+            const float4 *nlse = reinterpret_cast<const float4 *>(gbase + lay.rows + st * kTile * 8) + 16 * half;
+            const float4 *ndelta = nlse + kTile / 4;
+            const int4 *spans = reinterpret_cast<const int4 *>(gbase + lay.spans + st * kTile * 16) + 64 * half;
             const uint32_t q_tile = base + lay.ring + st * lay.stage;
             // (the rows' records came with the tiles that S was made from)
             go = wait_warp(bar(kFull + st), (n / kStages) & 1, abort, args.limit) &&
                  wait_warp(bar(kS), n & 1, abort, args.limit);
             if (!go) break;
             tc_fence_after_sync();
-            float w[64];                         // weights, then times the cap's slope
-            const auto weigh = [&](auto mask) {
+            float w[64], slack[64];              // scores, then weights; the cap's slopes
+            tmem_ld_all(t_s + lanes + 64 * half, w);
+            if (GENERAL) bend(w, slack, args, slope2, [&](int k) { return static_cast<float>(spans[k].z - key); });
+            const float c = GENERAL ? 1.0f : args.scale_log2;
+            const uint64_t c2 = pack2(c, c);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float s[32];
-                    uint32_t pk[16];
-                    tmem_ld32(t_s + lanes + 64 * half + 32 * q, s);
-                    tmem_wait_ld();
+            for (int k = 0; k < 64; k += 4) {
+                const float4 e = nlse[k / 4];
+                const float2 x = unpack2(fma2(pack2(w[k], w[k + 1]), c2, pack2(e.x, e.y)));
+                const float2 y = unpack2(fma2(pack2(w[k + 2], w[k + 3]), c2, pack2(e.z, e.w)));
+                w[k] = ex2_approx(x.x);
+                w[k + 1] = ex2_approx(x.y);
+                w[k + 2] = ex2_approx(y.x);
+                w[k + 3] = ex2_approx(y.y);
+            }
+            if (masked) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        const uint4 r = lds128(rows + (32 * q + k) * 8);
-                        const float lse[2] = {__uint_as_float(r.x), __uint_as_float(r.z)};
-                        float p[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int col = 32 * q + k + e;
-                            float slack = 1.0f, t;
-                            int4 sp = make_int4(0, 0, 0, 0);
-                            if (mask || (GENERAL && a.slopes)) {
-                                const uint4 v = lds128(spans + col * 16);
-                                sp = make_int4(v.x, v.y, v.z, 0);
-                            }
-                            if (GENERAL)
-                                t = bent(bend, s[k + e], sp.z - key, slack) - lse[e];
-                            else
-                                t = fmaf(s[k + e], args.scale_log2, -lse[e]);
-                            p[e] = ex2_approx(t);
-                            w[col] = GENERAL ? p[e] * slack : p[e];
-                            if (mask && (key < sp.x || key >= sp.y)) p[e] = w[col] = 0.f;
-                        }
-                        pk[k / 2] = Half2<T>::pack(p[0], p[1]);
-                    }
-                    tmem_st16(t_s + lanes + 64 * half + 16 * q, pk);
+                for (int k = 0; k < 64; ++k) {
+                    const int4 sp = spans[k];
+                    w[k] = key >= sp.x && key < sp.y ? w[k] : 0.f;
                 }
-            };
-            if (masked)
-                weigh(std::true_type{});
-            else
-                weigh(std::false_type{});
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) pk[k] = Half2<T>::pack(w[32 * q + 2 * k], w[32 * q + 2 * k + 1]);
+                tmem_st16(t_s + lanes + 64 * half + 16 * q, pk);
+            }
             if (masked) {
                 const int r = (warp & 3) * 32 + lane;
                 clear_not_finite<T>(q_tile + (half ? tile_bytes : 0), r, i0 + r, q_lo, q_hi, halves, bad);
@@ -418,23 +413,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             go = wait_warp(bar(kDp), n & 1, abort, args.limit);
             if (!go) break;
             tc_fence_after_sync();
+            float dp[64];
+            tmem_ld_all(t_dp + lanes + 64 * half, dp);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                float dp[32];
                 uint32_t pk[16];
-                tmem_ld32(t_dp + lanes + 64 * half + 32 * q, dp);
-                tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    const uint4 r = lds128(rows + (32 * q + k) * 8);
-                    float d0 = w[32 * q + k] * (dp[k] - __uint_as_float(r.y));
-                    float d1 = w[32 * q + k + 1] * (dp[k + 1] - __uint_as_float(r.w));
+                for (int k = 0; k < 16; k += 2) {
+                    const int n0 = 32 * q + 2 * k;
+                    const float4 e = ndelta[n0 / 4];
+                    const float2 x = unpack2(mul2(pack2(w[n0], w[n0 + 1]), add2(pack2(dp[n0], dp[n0 + 1]), pack2(e.x, e.y))));
+                    const float2 y = unpack2(mul2(pack2(w[n0 + 2], w[n0 + 3]), add2(pack2(dp[n0 + 2], dp[n0 + 3]), pack2(e.z, e.w))));
+                    float d[4] = {x.x, x.y, y.x, y.y};
+                    if (GENERAL && a.cap > 0.f) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) d[i] *= slack[n0 + i];
+                    }
                     if (masked) {
                         // a weight of zero times what an unseen row holds
-                        d0 = w[32 * q + k] == 0.f ? 0.f : d0;
-                        d1 = w[32 * q + k + 1] == 0.f ? 0.f : d1;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) d[i] = w[n0 + i] == 0.f ? 0.f : d[i];
                     }
-                    pk[k / 2] = Half2<T>::pack(d0, d1);
+                    pk[k] = Half2<T>::pack(d[0], d[1]);
+                    pk[k + 1] = Half2<T>::pack(d[2], d[3]);
                 }
                 tmem_st16(t_dp + lanes + 64 * half + 16 * q, pk);
             }
@@ -526,17 +527,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int r = (warp & 3) * 32 + lane, row = row0 + r;   // (row < info.padded)
     int4 span = make_int4(0, 0, 0, 0);
-    float2 stat = make_float2(INFINITY, 0.f);
-    if (warp >= 4) {
+    float nlse = -INFINITY, ndelta = 0.f;
+    if (warp >= 2) {
         span = info.span[row];
-        stat = info.row[static_cast<int64_t>(h) * info.padded + row];
+        nlse = info.lse[static_cast<int64_t>(h) * info.padded + row];
+        ndelta = info.delta[static_cast<int64_t>(h) * info.padded + row];
         const bool live = row < a.tokens_q, some = live && span.x < span.y;
         const int lo = __reduce_min_sync(0xffffffffu, some ? span.x : 0x7fffffff);
         const int hi = __reduce_max_sync(0xffffffffu, some ? span.y : 0);
         const int all_lo = __reduce_max_sync(0xffffffffu, !live ? 0 : (some ? span.x : 0x7fffffff));
         const int all_hi = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : (some ? span.y : 0));
         if (lane == 0) {
-            volatile int *w = range + ((warp - 4) * 4);
+            volatile int *w = range + ((warp - 2) * 4);
             w[0] = lo;
             w[1] = hi;
             w[2] = all_lo;
@@ -606,19 +608,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_tokens(t_dp, do_tile, k_next + tile_bytes, steps, is);
                     umma_commit(bar(kDp));
                 }
-                mma_channels(t_dq, t_s + 128 * (n & 1), 64, k_tile, io, n > 0);
+                mma_channels(t_dq, t_s + 128 * (n & 1), k_tile, 0, io, n > 0);
+                mma_channels(t_dq, t_s + 128 * (n & 1) + 64, k_tile, 1, io, true);
                 umma_commit(bar(kEmpty + st));
             }
             if (go) umma_commit(bar(kOut));
             umma_commit(bar(kDrain));
             tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
         }
-    } else if (warp >= 4) {
+    } else {
         // ---- softmax: one query per thread, 64 of a block's keys per warp ----
-        const int half = (warp - 4) >> 2;
+        const int half = (warp - 2) >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        Bend bend = {};
-        if (GENERAL) bend = bend_of(args, h);
+        const float slope2 = GENERAL && a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
         bool go = !skip;
         for (int n = 0; go && n < blocks; ++n) {
             const int j0 = key0 + n * kTile, st = n % kStages;
@@ -628,48 +630,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             go = wait_warp(bar(kS), n & 1, abort, args.limit);
             if (!go) break;
             tc_fence_after_sync();
-            float w[64];
-            const auto weigh = [&](auto mask) {
+            float w[64], slack[64];              // scores, then weights; the cap's slopes
+            tmem_ld_all(ts, w);
+            if (GENERAL) {
+                const float pos = static_cast<float>(span.z - j0 - 64 * half);
+                bend(w, slack, args, slope2, [&](int k) { return pos - static_cast<float>(k); });
+            }
+            const float c = GENERAL ? 1.0f : args.scale_log2;
+            const uint64_t c2 = pack2(c, c), e2 = pack2(nlse, nlse);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float s[32];
-                    tmem_ld32(ts + 32 * q, s);
-                    tmem_wait_ld();
+            for (int k = 0; k < 64; k += 2) {
+                const float2 x = unpack2(fma2(pack2(w[k], w[k + 1]), c2, e2));
+                w[k] = ex2_approx(x.x);
+                w[k + 1] = ex2_approx(x.y);
+            }
+            if (masked) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int col = 64 * half + 32 * q + k;
-                        float slack = 1.0f, t;
-                        if (GENERAL)
-                            t = bent(bend, s[k], span.z - j0 - col, slack) - stat.x;
-                        else
-                            t = fmaf(s[k], args.scale_log2, -stat.x);
-                        w[32 * q + k] = ex2_approx(t) * slack;
-                        if (mask && static_cast<unsigned>(col - lo) >= static_cast<unsigned>(len)) w[32 * q + k] = 0.f;
-                    }
-                }
-            };
-            if (masked)
-                weigh(std::true_type{});
-            else
-                weigh(std::false_type{});
+                for (int k = 0; k < 64; ++k)
+                    w[k] = static_cast<unsigned>(k + 64 * half - lo) < static_cast<unsigned>(len) ? w[k] : 0.f;
+            }
             go = wait_warp(bar(kDp), n & 1, abort, args.limit);
             if (!go) break;
             tc_fence_after_sync();
+            float dp[64];
+            tmem_ld_all(t_dp + lanes + 64 * half, dp);
+            const uint64_t d2 = pack2(ndelta, ndelta);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                float dp[32];
                 uint32_t pk[16];
-                tmem_ld32(t_dp + lanes + 64 * half + 32 * q, dp);
-                tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    float d0 = w[32 * q + k] * (dp[k] - stat.y);
-                    float d1 = w[32 * q + k + 1] * (dp[k + 1] - stat.y);
-                    if (masked) {
-                        d0 = w[32 * q + k] == 0.f ? 0.f : d0;
-                        d1 = w[32 * q + k + 1] == 0.f ? 0.f : d1;
+                for (int k = 0; k < 16; ++k) {
+                    const int n0 = 32 * q + 2 * k;
+                    float2 x = unpack2(mul2(pack2(w[n0], w[n0 + 1]), add2(pack2(dp[n0], dp[n0 + 1]), d2)));
+                    if (GENERAL && a.cap > 0.f) {
+                        x.x *= slack[n0];
+                        x.y *= slack[n0 + 1];
                     }
-                    pk[k / 2] = Half2<T>::pack(d0, d1);
+                    if (masked) {
+                        x.x = w[n0] == 0.f ? 0.f : x.x;
+                        x.y = w[n0 + 1] == 0.f ? 0.f : x.y;
+                    }
+                    pk[k] = Half2<T>::pack(x.x, x.y);
                 }
                 tmem_st16(ts + 16 * q, pk);
             }
@@ -760,7 +761,8 @@ cudaError_t launch_packed_attn_backward(const PackedAttn &p, const WaitLimit &li
     Info info;
     info.padded = padded_rows(a.tokens_q);
     info.span = static_cast<int4 *>(p.workspace);
-    info.row = reinterpret_cast<float2 *>(info.span + info.padded);
+    info.lse = reinterpret_cast<float *>(info.span + info.padded);
+    info.delta = info.lse + info.padded * a.heads;
     const bool general = a.cap > 0.f || a.slopes;
     if (bf16)
         return general ? launch<__nv_bfloat16, true>(args, map, info, s, launches)

@@ -26,12 +26,13 @@ namespace {
 
 using namespace pattn;
 
-constexpr int kThreads = 384;    // warps: 0 loads, 1 MMA, 4-7 and 8-11 the two tiles' softmax
+constexpr int kThreads = 320;    // warps: 0 loads, 1 MMA, 2-5 and 6-9 the two tiles' softmax
 constexpr int kStages = 4;       // ring of key and value tiles, in the order K0 V0 K1 V1 ...
 constexpr float kRescaleLog2 = 8.0f;
 
+// kPFull: per tile the weights of the block's first and last 64 keys
 enum Bar { kQFull = 0, kFull = 2, kEmpty = kFull + kStages, kSFull = kEmpty + kStages, kPFull = kSFull + 2,
-           kOFull = kPFull + 2, kDrain = kOFull + 2, kBars };
+           kOFull = kPFull + 4, kDrain = kOFull + 2, kBars };
 
 struct Layout {
     uint32_t q, ring, bars, words, total;
@@ -82,25 +83,6 @@ __device__ __noinline__ void row_forward(const gn_attn_packed_args &a, int group
         a.lse[static_cast<int64_t>(h) * a.tokens_q + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// Where a query's row stands towards the block at j0: its run of keys and its
-// own position, relative to the block.
-struct RowBlock {
-    int lo, len, pos;
-    float slope2, cap_log2, inv_cap, c;
-};
-
-// Score number n of the block, in units of log2 (GENERAL: capped, biased, or
-// a scale that is not positive; otherwise the raw score, scaled in the
-// exponent).
-template <bool GENERAL>
-__device__ __forceinline__ float score(float s, int n, const RowBlock &r)
-{
-    if (!GENERAL) return s;
-    float t = s * r.c;
-    if (r.cap_log2 > 0.f) t = r.cap_log2 * tanh_fast(s * r.inv_cap);
-    return fmaf(-r.slope2, fabsf(static_cast<float>(r.pos - n)), t);
-}
-
 template <typename T, bool GENERAL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -124,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row0 = (args.tiles - 1 - static_cast<int>(blockIdx.x / a.heads)) * 2 * kTile;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i >= kPFull && i < kPFull + 2 ? 4 : 1);
+        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i >= kPFull && i < kPFull + 4 ? 4 : 1);
         *abort = (*reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) ? 1 : 0;
         bad[0] = 0x7fffffff;
         bad[1] = -1;
@@ -143,8 +125,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every query's run of keys, and what the tiles make of them: the keys that
     // any query sees, and those that all see
     Span span = {0, 0, 0};
-    const int tile = warp >= 8 ? 1 : 0, row = row0 + tile * kTile + (warp & 3) * 32 + lane;
-    if (warp >= 4) {
+    const int tile = warp >= 6 ? 1 : 0, row = row0 + tile * kTile + (warp & 3) * 32 + lane;
+    if (warp >= 2) {
         span = query_span_warp(a, row, lane);
         const bool live = row < a.tokens_q, some = live && span.lo < span.hi;
         const int lo = __reduce_min_sync(0xffffffffu, some ? span.lo : 0x7fffffff);
@@ -152,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int all_lo = __reduce_max_sync(0xffffffffu, !live ? 0 : (some ? span.lo : 0x7fffffff));
         const int all_hi = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : (some ? span.hi : 0));
         if (lane == 0) {
-            volatile int *w = range + ((warp - 4) * 4);
+            volatile int *w = range + ((warp - 2) * 4);
             w[0] = lo;
             w[1] = hi;
             w[2] = all_lo;
@@ -230,11 +212,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (b - 1 >= first[t] && b - 1 < last[t]) {
                         if (!have_v) go = wait(bar(kFull + nv % kStages), (nv / kStages) & 1, abort, args.limit);
                         have_v = true;
-                        go = go && wait(bar(kPFull + t), (b - 1 - first[t]) & 1, abort, args.limit);
+                        for (int half = 0; go && half < 2; ++half) {
+                            go = wait(bar(kPFull + 2 * t + half), (b - 1 - first[t]) & 1, abort, args.limit);
+                            if (!go) break;
+                            tc_fence_after_sync();
+                            mma_channels(tmem + 256 + 128 * t, tmem + 128 * t + 32 * half,
+                                         base + lay.ring + (nv % kStages) * tile_bytes, half, io, b - 1 > first[t] || half);
+                        }
                         if (!go) break;
-                        tc_fence_after_sync();
-                        mma_channels(tmem + 256 + 128 * t, tmem + 128 * t, 32, base + lay.ring + (nv % kStages) * tile_bytes,
-                                     io, b - 1 > first[t]);
                         if (b == last[t]) umma_commit(bar(kOFull + t));
                     }
                     if (b >= first[t] && b < last[t]) {
@@ -260,96 +245,84 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(bar(kDrain));
             tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
         }
-    } else if (warp >= 4) {
+    } else {
         // ---- softmax: one query per thread ----
         constexpr float kShift = IsBf16<T>::value ? 0.f : 7.f;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128 * tile, to = tmem + lanes + 256 + 128 * tile;
         const int b0 = tile ? first[1] : first[0], b1 = tile ? last[1] : last[0];
-        RowBlock rb = {};
-        if (GENERAL) {
-            rb.c = args.scale_log2;
-            rb.cap_log2 = a.cap * kLog2e;
-            rb.inv_cap = a.cap > 0.f ? a.scale / a.cap : 0.f;
-            rb.slope2 = a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
-        }
-        const float c = GENERAL ? 1.0f : args.scale_log2;
+        const float slope2 = GENERAL && a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
         float m = -INFINITY, l = 0.f;
         bool go = !skip;
         for (int b = b0; go && b < b1; ++b) {
             const int j0 = key0 + b * kTile;
             const bool masked = j0 < all_lo || j0 + kTile > all_hi;
-            rb.lo = span.lo - j0;
-            rb.len = max(0, span.hi - span.lo);
-            rb.pos = span.pos - j0;
             go = wait_warp(bar(kSFull + tile), (b - b0) & 1, abort, args.limit);
             if (!go) break;
             tc_fence_after_sync();
-            // one sweep over the block's scores: their maximum, the weights
-            // against m and the weights' sum
-            uint32_t pk[64];
-            float mx, sum;
-            const auto sweep = [&](float m_use, auto weigh, auto mask) {
-                mx = -INFINITY;
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
+            float s[kTile];
+            tmem_ld_all(ts, s);
+            float c = args.scale_log2;
+            if (GENERAL) {
+                c = 1.0f;
+                if (a.cap > 0.f) tanh_all(s, a.scale / a.cap);
+                const float by = a.cap > 0.f ? a.cap * kLog2e : args.scale_log2;
+                const float pos = static_cast<float>(span.pos - j0);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float s[32];
-                    tmem_ld32(ts + 32 * q, s);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        s[k] = score<GENERAL>(s[k], 32 * q + k, rb);
-                        if (mask) s[k] = static_cast<unsigned>(32 * q + k - rb.lo) < static_cast<unsigned>(rb.len) ? s[k] : -INFINITY;
-                        mx = fmaxf(mx, s[k]);
-                    }
-                    if (weigh) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            s[k] = ex2_approx(fmaf(s[k], c, -m_use));
-                            part[k & 3] += s[k];
-                        }
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) pk[16 * q + k] = Half2<T>::pack(s[2 * k], s[2 * k + 1]);
-                    }
-                }
-                mx *= c;
-                sum = (part[0] + part[1]) + (part[2] + part[3]);
-            };
-            const auto run = [&](float m_use, auto weigh) {
-                if (masked)
-                    sweep(m_use, weigh, std::true_type{});
-                else
-                    sweep(m_use, weigh, std::false_type{});
-            };
-            if (b == b0) {
-                run(0.f, std::false_type{});
-                m = mx - kShift;
+                for (int k = 0; k < kTile; ++k) s[k] = fmaf(-slope2, fabsf(pos - k), s[k] * by);
             }
-            run(m == -INFINITY ? 0.f : m, std::true_type{});
-            const bool grew = mx > m + (kShift + kRescaleLog2);
+            if (masked) {
+                const int lo = span.lo - j0;
+                const unsigned len = static_cast<unsigned>(max(0, span.hi - span.lo));
+#pragma unroll
+                for (int k = 0; k < kTile; ++k) s[k] = static_cast<unsigned>(k - lo) < len ? s[k] : -INFINITY;
+            }
+            float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int k = 4; k < kTile; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+            const bool grew = mx > m + (kShift + kRescaleLog2) || (b == b0 && mx > m);
             if (__any_sync(0xffffffffu, grew)) {
-                const float top = grew ? mx - kShift : m;
-                const float f = grew && m != -INFINITY ? ex2_approx(m - top) : 1.0f;
-                m = top;
+                const float to_m = grew ? mx - kShift : m;
+                const float f = grew && m != -INFINITY ? ex2_approx(m - to_m) : 1.0f;
+                m = to_m;
                 l *= f;
                 if (b > b0) {
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        float o[32];
-                        uint32_t u[32];
-                        tmem_ld32(to + 32 * q, o);
+                    for (int q = 0; q < 8; ++q) {
+                        uint32_t u[16];
+                        tmem_ld16(to + 16 * q, u);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * f);
-                        tmem_st32(to + 32 * q, u);
+                        for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * f);
+                        tmem_st16(to + 16 * q, u);
                     }
                 }
-                run(m == -INFINITY ? 0.f : m, std::true_type{});
             }
-            l += sum;
-            tmem_st32(ts, pk);
-            tmem_st32(ts + 32, pk + 32);
+            // the weights, 32 keys at a time; the first 64 are handed over early
+            const float m_use = m == -INFINITY ? 0.f : m;
+            const uint64_t c2 = pack2(c, c), m2 = pack2(-m_use, -m_use);
+            uint64_t sum2[2] = {0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float2 x = unpack2(fma2(pack2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]), c2, m2));
+                    const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+                    sum2[k & 1] = add2(sum2[k & 1], pack2(p0, p1));
+                    pk[k] = Half2<T>::pack(p0, p1);
+                }
+                tmem_st16(ts + 16 * q, pk);
+                if (q == 1 && !masked) {
+                    tmem_wait_st();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kPFull + 2 * tile));
+                }
+            }
+            const float2 sums = unpack2(add2(sum2[0], sum2[1]));
+            l += sums.x + sums.y;
             if (masked) {
                 const int nv = 2 * b + 1, r = (warp & 3) * 32 + lane;
                 go = wait_warp(bar(kFull + nv % kStages), (nv / kStages) & 1, abort, args.limit);
@@ -359,7 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kPFull + tile));
+            if (lane == 0) {
+                if (masked) mbar_arrive(bar(kPFull + 2 * tile));   // (not before the values were looked over)
+                mbar_arrive(bar(kPFull + 2 * tile + 1));
+            }
         }
         if (b0 < b1 && go) go = wait_warp(bar(kOFull + tile), 0, abort, args.limit);
         named_sync(1, 256);   // both tiles are done with looking at the values

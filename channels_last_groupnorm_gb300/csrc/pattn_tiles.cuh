@@ -99,23 +99,95 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
         : "memory");
 }
 
+// The issuing thread's own instructions would take longer than the products
+// (64 cycles a step) if it built a descriptor for each: the steps only add to
+// the descriptors' address field, and are unrolled.
+
 // D = A B^T over the channels of two tiles (128 x 128, `steps` of 16 channels).
 __device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc)
 {
-    for (int k = 0; k < steps; ++k) {
-        const uint32_t at = static_cast<uint32_t>(k >> 2) * kHalfBytes + static_cast<uint32_t>(k & 3) * 32u;
-        umma_f16(d, sw128_kmajor_desc(a + at), sw128_kmajor_desc(b + at), idesc, k > 0);
+    const uint64_t da = sw128_kmajor_desc(a), db = sw128_kmajor_desc(b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (k >= steps) break;
+        const uint64_t at = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
+        umma_f16(d, da + at, db + at, idesc, k > 0);
     }
 }
 
-// D (+)= A B over the 128 tokens of a tile: A in tensor memory, 32 columns for
-// the first 64 tokens and, `second` columns further on, 32 for the others.
-__device__ __forceinline__ void mma_channels(uint32_t d, uint32_t a_tmem, uint32_t second, uint32_t b, uint32_t idesc,
+// D (+)= A B over 64 of a tile's tokens (half 0 or 1): A in tensor memory, 32 columns.
+__device__ __forceinline__ void mma_channels(uint32_t d, uint32_t a_tmem, uint32_t b, int half, uint32_t idesc,
                                              bool accumulate)
 {
+    const uint64_t db = sw128_mnmajor_desc(b) + half * 4 * (2048u >> 4);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        umma_ts(d, a_tmem + (k < 4 ? 8u * k : second + 8u * (k - 4)), sw128_mnmajor_desc(b + 2048u * k), idesc, accumulate || k > 0);
+    for (int k = 0; k < 4; ++k) umma_ts(d, a_tmem + 8u * k, db + k * (2048u >> 4), idesc, accumulate || k > 0);
+}
+
+// ---- two fp32 operations per instruction ------------------------------------------
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// ---- the cap's tanh, for N scores in place -------------------------------------------
+// v <- tanh(v k).  Scores are mostly small against their cap: up to 1/4 the
+// series of tanh to x^9 is exact to fp32 (the next term is under 2^-27 of x),
+// two scores per instruction and no special-function unit; beyond, for the
+// whole warp, 1 - 2 / (1 + e^2|x|) with two of its instructions each.
+template <int N>
+__device__ __forceinline__ void tanh_all(float (&v)[N], float k)
+{
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(v[i]));
+    // (written so that a NaN or an infinity takes the second path)
+    if (__all_sync(0xffffffffu, top * fabsf(k) <= 0.25f)) {
+        const uint64_t k2 = pack2(k, k);
+        const uint64_t c9 = pack2(62.f / 2835.f, 62.f / 2835.f), c7 = pack2(-17.f / 315.f, -17.f / 315.f);
+        const uint64_t c5 = pack2(2.f / 15.f, 2.f / 15.f), c3 = pack2(-1.f / 3.f, -1.f / 3.f);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const uint64_t x = mul2(pack2(v[i], v[i + 1]), k2), y = mul2(x, x);
+            const uint64_t s = fma2(fma2(fma2(c9, y, c7), y, c5), y, c3);
+            const float2 r = unpack2(fma2(mul2(x, y), s, x));
+            v[i] = r.x;
+            v[i + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = tanh_fast(v[i] * k);
+    }
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
@@ -124,6 +196,20 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
     tmem_ld_32x32b_x32(taddr, u);
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+}
+
+// N columns of the thread's lane, loads issued together.
+template <int N>
+__device__ __forceinline__ void tmem_ld_all(uint32_t taddr, float (&v)[N])
+{
+#pragma unroll
+    for (int q = 0; q < N / 32; ++q) {
+        uint32_t u[32];
+        tmem_ld_32x32b_x32(taddr + 32 * q, u);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[32 * q + i] = __uint_as_float(u[i]);
+    }
+    tmem_wait_ld();
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v)
@@ -136,6 +222,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v)
           "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
           "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
           "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
         : "memory");
 }
 
