@@ -31,7 +31,7 @@ namespace {
 
 using namespace pattn;
 
-constexpr int kThreads = 320;    // warps: 0 loads, 1 MMA, 2-9 softmax
+constexpr int kThreads = 352;    // warps: 0 loads, 1 MMA, 2-9 softmax, 10 the MMA's waits
 constexpr int kStages = 2;       // pairs of tiles in flight
 
 // Per query: the run of keys it sees and where it stands; per query and head:
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the queries that see any of the tile's keys, and those that see all
     const int row = (warp & 3) * 32 + lane, key = key0 + row;
     Span span = {0, 0, 0};
-    if (warp >= 2) {
+    if (warp >= 2 && warp < 10) {
         if (key < a.tokens_k) span = key_span(a, key);
         const bool live = key < a.tokens_k, some = live && span.lo < span.hi;
         const int lo = __reduce_min_sync(0xffffffffu, some ? span.lo : 0x7fffffff);
@@ -314,44 +314,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::drain(bar(kFull + k % kStages), (k / kStages) & 1, args.limit.timeout_ns);
             tc::drain(bar(kOwn), 0, args.limit.timeout_ns);
         }
-    } else if (warp == 1) {
-        if (lane == 0 && !skip && any) {
+    } else if (warp == 1 || warp == 10) {
+        if (!skip && any) {
+            const bool waits = warp == 10;
             const int steps = (a.dim + 15) / 16;
             const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
-            bool go = wait(bar(kOwn), 0, abort, args.limit) && wait(bar(kFull), 0, abort, args.limit);
-            if (go) {
-                tc_fence_after_sync();
-                mma_tokens(t_s, k_tile, base + lay.ring, steps, is);
-                umma_commit(bar(kS));
-                mma_tokens(t_dp, v_tile, base + lay.ring + tile_bytes, steps, is);
-                umma_commit(bar(kDp));
+            const auto loaded = [&](int n) { wait_warp(bar(kFull + n % kStages), (n / kStages) & 1, abort, args.limit); };
+            if (waits) {
+                wait_warp(bar(kOwn), 0, abort, args.limit);
+                loaded(0);
             }
-            for (int n = 0; go && n < steps_all; ++n) {
+            hand_over();
+            if (!waits) {
+                mma_tokens(t_s, k_tile, base + lay.ring, steps, is);
+                commit(bar(kS));
+                mma_tokens(t_dp, v_tile, base + lay.ring + tile_bytes, steps, is);
+                commit(bar(kDp));
+            }
+            for (int n = 0; n < steps_all; ++n) {
                 const int st = n % kStages, nx = (n + 1) % kStages;
                 const uint32_t q_tile = base + lay.ring + st * lay.stage, q_next = base + lay.ring + nx * lay.stage;
                 const bool more = n + 1 < steps_all;
-                if (!(go = wait(bar(kP), n & 1, abort, args.limit))) break;
-                tc_fence_after_sync();
-                mma_channels(t_dv, t_s, q_tile + tile_bytes, 0, io, n > 0);
-                mma_channels(t_dv, t_s + 64, q_tile + tile_bytes, 1, io, true);
-                if (more) {
-                    if (!(go = wait(bar(kFull + nx), ((n + 1) / kStages) & 1, abort, args.limit))) break;
-                    mma_tokens(t_s, k_tile, q_next, steps, is);
-                    umma_commit(bar(kS));
+                if (waits) wait_warp(bar(kP), n & 1, abort, args.limit);
+                hand_over();
+                if (!waits) {
+                    tc_fence_after_sync();
+                    mma_channels(t_dv, t_s, q_tile + tile_bytes, 0, io, n > 0);
+                    mma_channels(t_dv, t_s + 64, q_tile + tile_bytes, 1, io, true);
                 }
-                if (!(go = wait(bar(kDs), n & 1, abort, args.limit))) break;
-                tc_fence_after_sync();
-                mma_channels(t_dk, t_dp, q_tile, 0, io, n > 0);
-                mma_channels(t_dk, t_dp + 64, q_tile, 1, io, true);
-                umma_commit(bar(kEmpty + st));
                 if (more) {
-                    mma_tokens(t_dp, v_tile, q_next + tile_bytes, steps, is);
-                    umma_commit(bar(kDp));
+                    if (waits) loaded(n + 1);
+                    hand_over();
+                    if (!waits) {
+                        mma_tokens(t_s, k_tile, q_next, steps, is);
+                        commit(bar(kS));
+                    }
+                }
+                if (waits) wait_warp(bar(kDs), n & 1, abort, args.limit);
+                hand_over();
+                if (!waits) {
+                    tc_fence_after_sync();
+                    mma_channels(t_dk, t_dp, q_tile, 0, io, n > 0);
+                    mma_channels(t_dk, t_dp + 64, q_tile, 1, io, true);
+                    commit(bar(kEmpty + st));
+                    if (more) {
+                        mma_tokens(t_dp, v_tile, q_next + tile_bytes, steps, is);
+                        commit(bar(kDp));
+                    }
                 }
             }
-            if (go) umma_commit(bar(kOut));
-            umma_commit(bar(kDrain));
-            tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+            if (!waits) {
+                commit(bar(kOut));
+                commit(bar(kDrain));
+                tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+            }
         }
     } else {
         // ---- softmax: one key per thread, 64 of a block's queries per warp ----
@@ -528,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane, row = row0 + r;   // (row < info.padded)
     int4 span = make_int4(0, 0, 0, 0);
     float nlse = -INFINITY, ndelta = 0.f;
-    if (warp >= 2) {
+    if (warp >= 2 && warp < 10) {
         span = info.span[row];
         nlse = info.lse[static_cast<int64_t>(h) * info.padded + row];
         ndelta = info.delta[static_cast<int64_t>(h) * info.padded + row];
@@ -581,40 +597,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::drain(bar(kFull + k % kStages), (k / kStages) & 1, args.limit.timeout_ns);
             tc::drain(bar(kOwn), 0, args.limit.timeout_ns);
         }
-    } else if (warp == 1) {
-        if (lane == 0 && !skip && any) {
+    } else if (warp == 1 || warp == 10) {
+        if (!skip && any) {
+            const bool waits = warp == 10;
             const int steps = (a.dim + 15) / 16;
             const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
-            bool go = wait(bar(kOwn), 0, abort, args.limit) && wait(bar(kFull), 0, abort, args.limit);
-            if (go) {
-                tc_fence_after_sync();
-                mma_tokens(t_s, q_tile, base + lay.ring, steps, is);
-                umma_commit(bar(kS));
-                mma_tokens(t_dp, do_tile, base + lay.ring + tile_bytes, steps, is);
-                umma_commit(bar(kDp));
+            const auto loaded = [&](int n) { wait_warp(bar(kFull + n % kStages), (n / kStages) & 1, abort, args.limit); };
+            if (waits) {
+                wait_warp(bar(kOwn), 0, abort, args.limit);
+                loaded(0);
             }
-            for (int n = 0; go && n < blocks; ++n) {
+            hand_over();
+            if (!waits) {
+                mma_tokens(t_s, q_tile, base + lay.ring, steps, is);
+                commit(bar(kS));
+                mma_tokens(t_dp, do_tile, base + lay.ring + tile_bytes, steps, is);
+                commit(bar(kDp));
+            }
+            for (int n = 0; n < blocks; ++n) {
                 const int st = n % kStages, nx = (n + 1) % kStages;
                 const uint32_t k_tile = base + lay.ring + st * lay.stage, k_next = base + lay.ring + nx * lay.stage;
                 const bool more = n + 1 < blocks;
                 if (more) {
-                    if (!(go = wait(bar(kFull + nx), ((n + 1) / kStages) & 1, abort, args.limit))) break;
-                    mma_tokens(t_s + 128 * ((n + 1) & 1), q_tile, k_next, steps, is);
-                    umma_commit(bar(kS));
+                    if (waits) loaded(n + 1);
+                    hand_over();
+                    if (!waits) {
+                        mma_tokens(t_s + 128 * ((n + 1) & 1), q_tile, k_next, steps, is);
+                        commit(bar(kS));
+                    }
                 }
-                if (!(go = wait(bar(kDs), n & 1, abort, args.limit))) break;
-                tc_fence_after_sync();
-                if (more) {
-                    mma_tokens(t_dp, do_tile, k_next + tile_bytes, steps, is);
-                    umma_commit(bar(kDp));
+                if (waits) wait_warp(bar(kDs), n & 1, abort, args.limit);
+                hand_over();
+                if (!waits) {
+                    tc_fence_after_sync();
+                    if (more) {
+                        mma_tokens(t_dp, do_tile, k_next + tile_bytes, steps, is);
+                        commit(bar(kDp));
+                    }
+                    mma_channels(t_dq, t_s + 128 * (n & 1), k_tile, 0, io, n > 0);
+                    mma_channels(t_dq, t_s + 128 * (n & 1) + 64, k_tile, 1, io, true);
+                    commit(bar(kEmpty + st));
                 }
-                mma_channels(t_dq, t_s + 128 * (n & 1), k_tile, 0, io, n > 0);
-                mma_channels(t_dq, t_s + 128 * (n & 1) + 64, k_tile, 1, io, true);
-                umma_commit(bar(kEmpty + st));
             }
-            if (go) umma_commit(bar(kOut));
-            umma_commit(bar(kDrain));
-            tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+            if (!waits) {
+                commit(bar(kOut));
+                commit(bar(kDrain));
+                tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+            }
         }
     } else {
         // ---- softmax: one query per thread, 64 of a block's keys per warp ----

@@ -26,7 +26,7 @@ namespace {
 
 using namespace pattn;
 
-constexpr int kThreads = 320;    // warps: 0 loads, 1 MMA, 2-5 and 6-9 the two tiles' softmax
+constexpr int kThreads = 352;    // warps: 0 loads, 1 MMA, 2-5 and 6-9 the two tiles' softmax, 10 the MMA's waits
 constexpr int kStages = 4;       // ring of key and value tiles, in the order K0 V0 K1 V1 ...
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // any query sees, and those that all see
     Span span = {0, 0, 0};
     const int tile = warp >= 6 ? 1 : 0, row = row0 + tile * kTile + (warp & 3) * 32 + lane;
-    if (warp >= 2) {
+    if (warp >= 2 && warp < 10) {
         span = query_span_warp(a, row, lane);
         const bool live = row < a.tokens_q, some = live && span.lo < span.hi;
         const int lo = __reduce_min_sync(0xffffffffu, some ? span.lo : 0x7fffffff);
@@ -198,52 +198,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < 2; ++t)
                 if (first[t] < last[t]) tc::drain(bar(kQFull + t), 0, args.limit.timeout_ns);
         }
-    } else if (warp == 1) {
-        if (lane == 0 && !skip) {
+    } else if (warp == 1 || warp == 10) {
+        if (!skip) {
             // ---- MMA: per block and tile the weighted values of the block
             // before, then the scores of this one ----
+            const bool waits = warp == 10;
             const int steps = (a.dim + 15) / 16;
             const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
-            bool go = true;
-            for (int b = 0; go && b <= blocks; ++b) {
+            const auto loaded = [&](int n) { wait_warp(bar(kFull + n % kStages), (n / kStages) & 1, abort, args.limit); };
+            for (int b = 0; b <= blocks; ++b) {
                 const int nv = 2 * b - 1, nk = 2 * b;
-                bool have_v = false, have_k = false;
-                for (int t = 0; go && t < 2; ++t) {
-                    if (b - 1 >= first[t] && b - 1 < last[t]) {
-                        if (!have_v) go = wait(bar(kFull + nv % kStages), (nv / kStages) & 1, abort, args.limit);
-                        have_v = true;
-                        for (int half = 0; go && half < 2; ++half) {
-                            go = wait(bar(kPFull + 2 * t + half), (b - 1 - first[t]) & 1, abort, args.limit);
-                            if (!go) break;
+                const uint32_t v_tile = base + lay.ring + (nv % kStages) * tile_bytes;
+                const uint32_t k_tile = base + lay.ring + (nk % kStages) * tile_bytes;
+                // (a tile may have no part in a block: its loads are waited for all the same)
+                if (waits) {
+                    if (b > 0) loaded(nv);
+                    if (b < blocks) loaded(nk);
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const bool weigh = b - 1 >= first[t] && b - 1 < last[t], score = b >= first[t] && b < last[t];
+                    if (weigh) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (waits) wait_warp(bar(kPFull + 2 * t + half), (b - 1 - first[t]) & 1, abort, args.limit);
+                            hand_over();
+                            if (waits) continue;
                             tc_fence_after_sync();
-                            mma_channels(tmem + 256 + 128 * t, tmem + 128 * t + 32 * half,
-                                         base + lay.ring + (nv % kStages) * tile_bytes, half, io, b - 1 > first[t] || half);
+                            mma_channels(tmem + 256 + 128 * t, tmem + 128 * t + 32 * half, v_tile, half, io,
+                                         b - 1 > first[t] || half);
                         }
-                        if (!go) break;
-                        if (b == last[t]) umma_commit(bar(kOFull + t));
+                        if (!waits && b == last[t]) commit(bar(kOFull + t));
                     }
-                    if (b >= first[t] && b < last[t]) {
-                        if (!have_k) go = wait(bar(kFull + nk % kStages), (nk / kStages) & 1, abort, args.limit);
-                        have_k = true;
-                        if (b == first[t]) go = go && wait(bar(kQFull + t), 0, abort, args.limit);
-                        if (!go) break;
-                        mma_tokens(tmem + 128 * t, base + lay.q + t * tile_bytes,
-                                   base + lay.ring + (nk % kStages) * tile_bytes, steps, is);
-                        umma_commit(bar(kSFull + t));
+                    if (score) {
+                        if (waits && b == first[t]) wait_warp(bar(kQFull + t), 0, abort, args.limit);
+                        if (!weigh) hand_over();
+                        if (waits) continue;
+                        mma_tokens(tmem + 128 * t, base + lay.q + t * tile_bytes, k_tile, steps, is);
+                        commit(bar(kSFull + t));
                     }
                 }
-                if (!go) break;
-                if (b > 0) {
-                    if (!have_v) go = wait(bar(kFull + nv % kStages), (nv / kStages) & 1, abort, args.limit);
-                    umma_commit(bar(kEmpty + nv % kStages));
-                }
-                if (b < blocks) {
-                    if (!have_k) go = go && wait(bar(kFull + nk % kStages), (nk / kStages) & 1, abort, args.limit);
-                    umma_commit(bar(kEmpty + nk % kStages));
+                hand_over();
+                if (!waits) {
+                    if (b > 0) commit(bar(kEmpty + nv % kStages));
+                    if (b < blocks) commit(bar(kEmpty + nk % kStages));
                 }
             }
-            umma_commit(bar(kDrain));
-            tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+            if (!waits) {
+                commit(bar(kDrain));
+                tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+            }
         }
     } else {
         // ---- softmax: one query per thread ----

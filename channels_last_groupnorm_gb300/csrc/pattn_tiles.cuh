@@ -99,6 +99,39 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
         : "memory");
 }
 
+// The products are issued by one warp, the waits ahead of them are done by
+// another: an mbarrier wait by a thread with products in flight only returns
+// when they are done (with both in one warp the forward pass took 252 us where
+// it takes 200).  Both warps run the same loop; the waiter waits, then both meet
+// at a named barrier, then the issuer goes on.  A wait that runs out sets the
+// abort flag, after which the waiter's waits return at once and the issuer runs
+// on over whatever is there: wrong values of a call that is reported as failed,
+// never a wrong address, and never a longer wait.
+constexpr uint32_t kHandBarrier = 2;
+
+__device__ __forceinline__ void hand_over() { named_sync(kHandBarrier, 64); }
+
+// One lane of the warp, the same one every time.  The whole warp runs the loop
+// and elects the issuer around each group of products: inside a branch on the
+// lane number the compiler has to take the operands for divergent.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// Arrival on `bar` (an mbarrier) once every product issued so far is done.
+__device__ __forceinline__ void commit(uint32_t bar)
+{
+    if (elect_one()) umma_commit(bar);
+    __syncwarp();
+}
+
 // The issuing thread's own instructions would take longer than the products
 // (64 cycles a step) if it built a descriptor for each: the steps only add to
 // the descriptors' address field, and are unrolled.
@@ -107,12 +140,15 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
 __device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc)
 {
     const uint64_t da = sw128_kmajor_desc(a), db = sw128_kmajor_desc(b);
+    if (elect_one()) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        if (k >= steps) break;
-        const uint64_t at = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
-        umma_f16(d, da + at, db + at, idesc, k > 0);
+        for (int k = 0; k < 8; ++k) {
+            if (k >= steps) break;
+            const uint64_t at = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
+            umma_f16(d, da + at, db + at, idesc, k > 0);
+        }
     }
+    __syncwarp();
 }
 
 // D (+)= A B over 64 of a tile's tokens (half 0 or 1): A in tensor memory, 32 columns.
@@ -120,8 +156,11 @@ __device__ __forceinline__ void mma_channels(uint32_t d, uint32_t a_tmem, uint32
                                              bool accumulate)
 {
     const uint64_t db = sw128_mnmajor_desc(b) + half * 4 * (2048u >> 4);
+    if (elect_one()) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) umma_ts(d, a_tmem + 8u * k, db + k * (2048u >> 4), idesc, accumulate || k > 0);
+        for (int k = 0; k < 4; ++k) umma_ts(d, a_tmem + 8u * k, db + k * (2048u >> 4), idesc, accumulate || k > 0);
+    }
+    __syncwarp();
 }
 
 // ---- two fp32 operations per instruction ------------------------------------------
