@@ -32,7 +32,12 @@ namespace {
 using namespace pattn;
 
 constexpr int kThreads = 352;    // warps: 0 loads, 1 MMA, 2-9 softmax, 10 the MMA's waits
-constexpr int kStages = 2;       // pairs of tiles in flight
+// Tiles in flight: of the ones that two products far apart in a step read (Q for
+// dK and dV, K for dQ), and of the ones that are done with sooner (dO, V).
+// With two of each, released together, the loads were waited for (dQ: 2300 of
+// 3900 cycles a step).
+constexpr int kLongStages = 3;
+constexpr int kShortStages = 2;
 
 // Per query: the run of keys it sees and where it stands; per query and head:
 // -lse in units of log2, and -delta.  Padded to whole blocks so that 128 rows can be copied
@@ -154,16 +159,58 @@ __device__ __forceinline__ void bend(float (&s)[N], float (&slack)[N], const Til
     }
 }
 
-// Barriers and words of either kernel.  Own: the tiles a CTA owns; Full /
-// Empty: the pairs that stream by; S / Dp: an MMA result is there; P / Ds: the
-// softmax warps have put theirs in its place; Out: the accumulators are done.
-enum Bar { kOwn = 0, kFull, kEmpty = kFull + kStages, kS = kEmpty + kStages, kDp, kP, kDs, kOut, kDrain, kBars };
+// Barriers and words of either kernel.  Own: the tiles a CTA owns; Long /
+// Short: a streamed tile is there, is done with; Info: a block's row records;
+// S / Dp: an MMA result is there; P / Ds: the softmax warps have put theirs in
+// its place; Out: the accumulators are done.
+enum Bar { kOwn = 0, kLong, kLongFree = kLong + kLongStages, kShort = kLongFree + kLongStages,
+           kShortFree = kShort + kShortStages, kInfo = kShortFree + kShortStages, kS = kInfo + 2, kDp, kP, kDs, kOut,
+           kDrain, kBars };
 constexpr int kSoftWarps = 8;
 
 __device__ __forceinline__ void init_bars(uint32_t bars)
 {
     for (int i = 0; i < kBars; ++i) mbar_init(bars + 8u * i, i == kP || i == kDs ? kSoftWarps : 1);
     mbar_init_fence();
+}
+
+// Shared memory of either kernel: the two tiles it owns, the two rings, for dK
+// and dV the row records of two blocks.  (It begins on a 1 KB boundary, as the
+// swizzled tiles need: there is no static shared memory ahead of it.)
+struct Layout {
+    uint32_t own, longs, shorts, rows, bars, words, total;
+};
+
+__host__ __device__ inline Layout layout(int halves)
+{
+    Layout l;
+    const uint32_t tile = kHalfBytes * static_cast<uint32_t>(halves);
+    l.own = 0;
+    l.longs = 2 * tile;
+    l.shorts = l.longs + kLongStages * tile;
+    l.rows = l.shorts + kShortStages * tile;    // 2 x (128 -lse, 128 -delta)
+    l.bars = l.rows + 2 * kTile * 8;
+    l.words = l.bars + 8 * kBars;               // tensor-memory slot, abort, bad[2], 8 x 4 range words
+    l.total = l.words + 4 * (4 + 32);
+    return l;
+}
+
+// How many of each load a CTA has issued; when it ends nothing is left in
+// flight, whatever became of the others.
+struct Loads {
+    int longs, shorts, infos;
+};
+
+__device__ __forceinline__ void drain_loads(uint32_t bars, const Loads &got, uint64_t timeout_ns)
+{
+    const auto ring = [&](int first, int stages, int n) {
+        for (int k = max(0, n - stages); k < n; ++k)
+            tc::drain(bars + 8u * (first + k % stages), (k / stages) & 1, timeout_ns);
+    };
+    tc::drain(bars + 8u * kOwn, 0, timeout_ns);
+    ring(kLong, kLongStages, got.longs);
+    ring(kShort, kShortStages, got.shorts);
+    ring(kInfo, 2, got.infos);
 }
 
 // Writes one accumulator's rows: 64 channels (half 0 or 1) of the warp's 32
@@ -196,43 +243,34 @@ __device__ __forceinline__ void store_half(void *out, int64_t row_offset, bool l
 // ---------------------------------------------------------------------------
 // dK and dV
 // ---------------------------------------------------------------------------
-struct KvLayout {
-    uint32_t own, ring, stage, rows, spans, bars, words, total;
-};
-
-__host__ __device__ inline KvLayout kv_layout(int halves)
-{
-    KvLayout l;
-    const uint32_t tile = kHalfBytes * static_cast<uint32_t>(halves);
-    l.own = 0;                                  // K, V
-    l.ring = 2 * tile;                          // kStages x (Q, dO)
-    l.stage = 2 * tile;
-    l.rows = l.ring + kStages * l.stage;        // kStages x (128 -lse, 128 -delta)
-    l.spans = l.rows + kStages * kTile * 8;     // kStages x 128 runs of keys
-    l.bars = l.spans + kStages * kTile * 16;
-    l.words = l.bars + 8 * kBars;               // tensor-memory slot, abort, bad[2], 8 x 4 range words
-    l.total = l.words + 4 * (4 + 32);
-    return l;
-}
-
 template <typename T, bool GENERAL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
                     const __grid_constant__ TileArgs args, const Info info)
 {
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
-    uint8_t *const gbase = smem_raw + (base - raw);
+    extern __shared__ __align__(1024) uint8_t gbase[];
+    const uint32_t base = smem_addr(gbase);
     const gn_attn_packed_args &a = args.p.a;
     const int halves = a.dim > 64 ? 2 : 1, group = args.p.group;
-    const KvLayout lay = kv_layout(halves);
+    const Layout lay = layout(halves);
     const uint32_t tile_bytes = kHalfBytes * static_cast<uint32_t>(halves);
     const auto bar = [&](int i) { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
     volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(gbase + lay.words);
     volatile int *abort = reinterpret_cast<volatile int *>(words + 1);
     int *bad = reinterpret_cast<int *>(gbase + lay.words + 8);
     volatile int *range = reinterpret_cast<volatile int *>(words + 4);
+    const auto long_tile = [&](int n) { return base + lay.longs + static_cast<uint32_t>(n % kLongStages) * tile_bytes; };
+    const auto short_tile = [&](int n) { return base + lay.shorts + static_cast<uint32_t>(n % kShortStages) * tile_bytes; };
+    // streamed tile n is there (a whole warp asks) / is done with (n < 0: there was none)
+    const auto has_long = [&](int n) { return wait_warp(bar(kLong + n % kLongStages), (n / kLongStages) & 1, abort, args.limit); };
+    const auto has_short = [&](int n) { return wait_warp(bar(kShort + n % kShortStages), (n / kShortStages) & 1, abort, args.limit); };
+    const auto long_free = [&](int n) {
+        return n < 0 || wait(bar(kLongFree + n % kLongStages), (n / kLongStages) & 1, abort, args.limit);
+    };
+    const auto short_free = [&](int n) {
+        return n < 0 || wait(bar(kShortFree + n % kShortStages), (n / kShortStages) & 1, abort, args.limit);
+    };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hk = blockIdx.x % a.kv_heads;
     // the first tiles first: with causal runs the most queries see them
@@ -297,56 +335,60 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(bar(kOwn), 2 * tile_bytes);
             load_tile(k_tile, &map_k, halves, hk, key0, bar(kOwn));
             load_tile(v_tile, &map_v, halves, hk, key0, bar(kOwn));
-            int n = 0;
-            for (; n < steps_all; ++n) {
-                const int st = n % kStages, h = hk * group + n / blocks, i0 = q0 + (n % blocks) * kTile;
-                if (n >= kStages && !wait(bar(kEmpty + st), (n / kStages - 1) & 1, abort, args.limit)) break;
-                const uint32_t dst = base + lay.ring + st * lay.stage;
-                mbar_arrive_expect_tx(bar(kFull + st), 2 * tile_bytes + kTile * 8 + kTile * 16);
-                load_tile(dst, &map_q, halves, h, i0, bar(kFull + st));
-                load_tile(dst + tile_bytes, &map_do, halves, h, i0, bar(kFull + st));
+            Loads got = {};
+            for (int n = 0; n < steps_all; ++n) {
+                const int h = hk * group + n / blocks, i0 = q0 + (n % blocks) * kTile;
+                if (!long_free(n - kLongStages)) break;
+                mbar_arrive_expect_tx(bar(kLong + n % kLongStages), tile_bytes);
+                load_tile(long_tile(n), &map_q, halves, h, i0, bar(kLong + n % kLongStages));
+                ++got.longs;
+                if (!short_free(n - kShortStages)) break;
+                mbar_arrive_expect_tx(bar(kShort + n % kShortStages), tile_bytes);
+                load_tile(short_tile(n), &map_do, halves, h, i0, bar(kShort + n % kShortStages));
+                ++got.shorts;
+                // the records are done with when the scores' gradients of their block are, as Q is
+                if (!long_free(n - 2)) break;
                 const int64_t at = static_cast<int64_t>(h) * info.padded + i0;
-                bulk_load(base + lay.rows + st * kTile * 8, info.lse + at, kTile * 4, bar(kFull + st));
-                bulk_load(base + lay.rows + st * kTile * 8 + kTile * 4, info.delta + at, kTile * 4, bar(kFull + st));
-                bulk_load(base + lay.spans + st * kTile * 16, info.span + i0, kTile * 16, bar(kFull + st));
+                const uint32_t rows = base + lay.rows + (n & 1) * kTile * 8;
+                mbar_arrive_expect_tx(bar(kInfo + (n & 1)), kTile * 8);
+                bulk_load(rows, info.lse + at, kTile * 4, bar(kInfo + (n & 1)));
+                bulk_load(rows + kTile * 4, info.delta + at, kTile * 4, bar(kInfo + (n & 1)));
+                ++got.infos;
             }
-            for (int k = max(0, n - kStages); k < n; ++k)
-                tc::drain(bar(kFull + k % kStages), (k / kStages) & 1, args.limit.timeout_ns);
-            tc::drain(bar(kOwn), 0, args.limit.timeout_ns);
+            drain_loads(bar(0), got, args.limit.timeout_ns);
         }
     } else if (warp == 1 || warp == 10) {
         if (!skip && any) {
             const bool waits = warp == 10;
             const int steps = (a.dim + 15) / 16;
             const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
-            const auto loaded = [&](int n) { wait_warp(bar(kFull + n % kStages), (n / kStages) & 1, abort, args.limit); };
             if (waits) {
                 wait_warp(bar(kOwn), 0, abort, args.limit);
-                loaded(0);
+                has_long(0);
+                has_short(0);
             }
             hand_over();
             if (!waits) {
-                mma_tokens(t_s, k_tile, base + lay.ring, steps, is);
+                mma_tokens(t_s, k_tile, long_tile(0), steps, is);
                 commit(bar(kS));
-                mma_tokens(t_dp, v_tile, base + lay.ring + tile_bytes, steps, is);
+                mma_tokens(t_dp, v_tile, short_tile(0), steps, is);
                 commit(bar(kDp));
             }
             for (int n = 0; n < steps_all; ++n) {
-                const int st = n % kStages, nx = (n + 1) % kStages;
-                const uint32_t q_tile = base + lay.ring + st * lay.stage, q_next = base + lay.ring + nx * lay.stage;
                 const bool more = n + 1 < steps_all;
                 if (waits) wait_warp(bar(kP), n & 1, abort, args.limit);
                 hand_over();
                 if (!waits) {
                     tc_fence_after_sync();
-                    mma_channels(t_dv, t_s, q_tile + tile_bytes, 0, io, n > 0);
-                    mma_channels(t_dv, t_s + 64, q_tile + tile_bytes, 1, io, true);
+                    mma_channels(t_dv, t_s, short_tile(n), 0, io, n > 0);
+                    mma_channels(t_dv, t_s + 64, short_tile(n), 1, io, true);
+                    commit(bar(kShortFree + n % kShortStages));
                 }
                 if (more) {
-                    if (waits) loaded(n + 1);
+                    if (waits) has_long(n + 1);
                     hand_over();
                     if (!waits) {
-                        mma_tokens(t_s, k_tile, q_next, steps, is);
+                        mma_tokens(t_s, k_tile, long_tile(n + 1), steps, is);
                         commit(bar(kS));
                     }
                 }
@@ -354,11 +396,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 hand_over();
                 if (!waits) {
                     tc_fence_after_sync();
-                    mma_channels(t_dk, t_dp, q_tile, 0, io, n > 0);
-                    mma_channels(t_dk, t_dp + 64, q_tile, 1, io, true);
-                    commit(bar(kEmpty + st));
-                    if (more) {
-                        mma_tokens(t_dp, v_tile, q_next + tile_bytes, steps, is);
+                    mma_channels(t_dk, t_dp, long_tile(n), 0, io, n > 0);
+                    mma_channels(t_dk, t_dp + 64, long_tile(n), 1, io, true);
+                    commit(bar(kLongFree + n % kLongStages));
+                }
+                if (more) {
+                    if (waits) has_short(n + 1);
+                    hand_over();
+                    if (!waits) {
+                        mma_tokens(t_dp, v_tile, short_tile(n + 1), steps, is);
                         commit(bar(kDp));
                     }
                 }
@@ -376,21 +422,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool go = !skip;
         float slope2 = 0.f;
         for (int n = 0; go && n < steps_all; ++n) {
-            const int st = n % kStages, i0 = q0 + (n % blocks) * kTile;
+            const int i0 = q0 + (n % blocks) * kTile;
             const bool masked = i0 < all_lo || i0 + kTile > all_hi;
             if (GENERAL && a.slopes && n % blocks == 0) slope2 = __ldg(a.slopes + hk * group + n / blocks) * kLog2e;
-            const float4 *nlse = reinterpret_cast<const float4 *>(gbase + lay.rows + st * kTile * 8) + 16 * half;
+            const float4 *nlse = reinterpret_cast<const float4 *>(gbase + lay.rows + (n & 1) * kTile * 8) + 16 * half;
             const float4 *ndelta = nlse + kTile / 4;
-            const int4 *spans = reinterpret_cast<const int4 *>(gbase + lay.spans + st * kTile * 16) + 64 * half;
-            const uint32_t q_tile = base + lay.ring + st * lay.stage;
-            // (the rows' records came with the tiles that S was made from)
-            go = wait_warp(bar(kFull + st), (n / kStages) & 1, abort, args.limit) &&
+            const int4 *spans = info.span + i0 + 64 * half;
+            go = wait_warp(bar(kInfo + (n & 1)), (n >> 1) & 1, abort, args.limit) &&
                  wait_warp(bar(kS), n & 1, abort, args.limit);
             if (!go) break;
             tc_fence_after_sync();
             float w[64], slack[64];              // scores, then weights; the cap's slopes
             tmem_ld_all(t_s + lanes + 64 * half, w);
-            if (GENERAL) bend(w, slack, args, slope2, [&](int k) { return static_cast<float>(spans[k].z - key); });
+            if (GENERAL) {
+                // (queries that all see the same keys stand one after the other)
+                const int at = a.slopes ? __ldg(&spans->z) - key : 0;
+                if (masked)
+                    bend(w, slack, args, slope2, [&](int k) { return static_cast<float>(__ldg(&spans[k].z) - key); });
+                else
+                    bend(w, slack, args, slope2, [&](int k) { return static_cast<float>(at + k); });
+            }
             const float c = GENERAL ? 1.0f : args.scale_log2;
             const uint64_t c2 = pack2(c, c);
 #pragma unroll
@@ -406,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (masked) {
 #pragma unroll
                 for (int k = 0; k < 64; ++k) {
-                    const int4 sp = spans[k];
+                    const int2 sp = __ldg(reinterpret_cast<const int2 *>(spans + k));
                     w[k] = key >= sp.x && key < sp.y ? w[k] : 0.f;
                 }
             }
@@ -419,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (masked) {
                 const int r = (warp & 3) * 32 + lane;
-                clear_not_finite<T>(q_tile + (half ? tile_bytes : 0), r, i0 + r, q_lo, q_hi, halves, bad);
+                if (half == 0 || has_short(n))
+                    clear_not_finite<T>(half ? short_tile(n) : long_tile(n), r, i0 + r, q_lo, q_hi, halves, bad);
             }
             tmem_wait_st();
             tc_fence_before_sync();
@@ -485,41 +537,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // dQ
 // ---------------------------------------------------------------------------
-struct QLayout {
-    uint32_t own, ring, stage, bars, words, total;
-};
-
-__host__ __device__ inline QLayout q_layout(int halves)
-{
-    QLayout l;
-    const uint32_t tile = kHalfBytes * static_cast<uint32_t>(halves);
-    l.own = 0;                                  // Q, dO
-    l.ring = 2 * tile;                          // kStages x (K, V)
-    l.stage = 2 * tile;
-    l.bars = l.ring + kStages * l.stage;
-    l.words = l.bars + 8 * kBars;
-    l.total = l.words + 4 * (4 + 32);
-    return l;
-}
-
 template <typename T, bool GENERAL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
                    const __grid_constant__ TileArgs args, const Info info)
 {
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
-    uint8_t *const gbase = smem_raw + (base - raw);
+    extern __shared__ __align__(1024) uint8_t gbase[];
+    const uint32_t base = smem_addr(gbase);
     const gn_attn_packed_args &a = args.p.a;
     const int halves = a.dim > 64 ? 2 : 1;
-    const QLayout lay = q_layout(halves);
+    const Layout lay = layout(halves);
     const uint32_t tile_bytes = kHalfBytes * static_cast<uint32_t>(halves);
     const auto bar = [&](int i) { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
     volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(gbase + lay.words);
     volatile int *abort = reinterpret_cast<volatile int *>(words + 1);
     int *bad = reinterpret_cast<int *>(gbase + lay.words + 8);
     volatile int *range = reinterpret_cast<volatile int *>(words + 4);
+    const auto long_tile = [&](int n) { return base + lay.longs + static_cast<uint32_t>(n % kLongStages) * tile_bytes; };
+    const auto short_tile = [&](int n) { return base + lay.shorts + static_cast<uint32_t>(n % kShortStages) * tile_bytes; };
+    // streamed tile n is there (a whole warp asks) / is done with (n < 0: there was none)
+    const auto has_long = [&](int n) { return wait_warp(bar(kLong + n % kLongStages), (n / kLongStages) & 1, abort, args.limit); };
+    const auto has_short = [&](int n) { return wait_warp(bar(kShort + n % kShortStages), (n / kShortStages) & 1, abort, args.limit); };
+    const auto long_free = [&](int n) {
+        return n < 0 || wait(bar(kLongFree + n % kLongStages), (n / kLongStages) & 1, abort, args.limit);
+    };
+    const auto short_free = [&](int n) {
+        return n < 0 || wait(bar(kShortFree + n % kShortStages), (n / kShortStages) & 1, abort, args.limit);
+    };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x % a.heads, hk = h / args.p.group;
     const int row0 = (args.tiles - 1 - static_cast<int>(blockIdx.x / a.heads)) * kTile;
@@ -584,59 +629,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(bar(kOwn), 2 * tile_bytes);
             load_tile(q_tile, &map_q, halves, h, row0, bar(kOwn));
             load_tile(do_tile, &map_do, halves, h, row0, bar(kOwn));
-            int n = 0;
-            for (; n < blocks; ++n) {
-                const int st = n % kStages;
-                if (n >= kStages && !wait(bar(kEmpty + st), (n / kStages - 1) & 1, abort, args.limit)) break;
-                const uint32_t dst = base + lay.ring + st * lay.stage;
-                mbar_arrive_expect_tx(bar(kFull + st), 2 * tile_bytes);
-                load_tile(dst, &map_k, halves, hk, key0 + n * kTile, bar(kFull + st));
-                load_tile(dst + tile_bytes, &map_v, halves, hk, key0 + n * kTile, bar(kFull + st));
+            Loads got = {};
+            for (int n = 0; n < blocks; ++n) {
+                if (!long_free(n - kLongStages)) break;
+                mbar_arrive_expect_tx(bar(kLong + n % kLongStages), tile_bytes);
+                load_tile(long_tile(n), &map_k, halves, hk, key0 + n * kTile, bar(kLong + n % kLongStages));
+                ++got.longs;
+                if (!short_free(n - kShortStages)) break;
+                mbar_arrive_expect_tx(bar(kShort + n % kShortStages), tile_bytes);
+                load_tile(short_tile(n), &map_v, halves, hk, key0 + n * kTile, bar(kShort + n % kShortStages));
+                ++got.shorts;
             }
-            for (int k = max(0, n - kStages); k < n; ++k)
-                tc::drain(bar(kFull + k % kStages), (k / kStages) & 1, args.limit.timeout_ns);
-            tc::drain(bar(kOwn), 0, args.limit.timeout_ns);
+            drain_loads(bar(0), got, args.limit.timeout_ns);
         }
     } else if (warp == 1 || warp == 10) {
         if (!skip && any) {
             const bool waits = warp == 10;
             const int steps = (a.dim + 15) / 16;
             const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
-            const auto loaded = [&](int n) { wait_warp(bar(kFull + n % kStages), (n / kStages) & 1, abort, args.limit); };
             if (waits) {
                 wait_warp(bar(kOwn), 0, abort, args.limit);
-                loaded(0);
+                has_long(0);
+                has_short(0);
             }
             hand_over();
             if (!waits) {
-                mma_tokens(t_s, q_tile, base + lay.ring, steps, is);
+                mma_tokens(t_s, q_tile, long_tile(0), steps, is);
                 commit(bar(kS));
-                mma_tokens(t_dp, do_tile, base + lay.ring + tile_bytes, steps, is);
+                mma_tokens(t_dp, do_tile, short_tile(0), steps, is);
                 commit(bar(kDp));
+                commit(bar(kShortFree));
             }
             for (int n = 0; n < blocks; ++n) {
-                const int st = n % kStages, nx = (n + 1) % kStages;
-                const uint32_t k_tile = base + lay.ring + st * lay.stage, k_next = base + lay.ring + nx * lay.stage;
                 const bool more = n + 1 < blocks;
                 if (more) {
-                    if (waits) loaded(n + 1);
+                    if (waits) has_long(n + 1);
                     hand_over();
                     if (!waits) {
-                        mma_tokens(t_s + 128 * ((n + 1) & 1), q_tile, k_next, steps, is);
+                        mma_tokens(t_s + 128 * ((n + 1) & 1), q_tile, long_tile(n + 1), steps, is);
                         commit(bar(kS));
                     }
                 }
-                if (waits) wait_warp(bar(kDs), n & 1, abort, args.limit);
+                if (waits) {
+                    if (more) has_short(n + 1);
+                    wait_warp(bar(kDs), n & 1, abort, args.limit);
+                }
                 hand_over();
                 if (!waits) {
                     tc_fence_after_sync();
                     if (more) {
-                        mma_tokens(t_dp, do_tile, k_next + tile_bytes, steps, is);
+                        mma_tokens(t_dp, do_tile, short_tile(n + 1), steps, is);
                         commit(bar(kDp));
+                        commit(bar(kShortFree + (n + 1) % kShortStages));
                     }
-                    mma_channels(t_dq, t_s + 128 * (n & 1), k_tile, 0, io, n > 0);
-                    mma_channels(t_dq, t_s + 128 * (n & 1) + 64, k_tile, 1, io, true);
-                    commit(bar(kEmpty + st));
+                    mma_channels(t_dq, t_s + 128 * (n & 1), long_tile(n), 0, io, n > 0);
+                    mma_channels(t_dq, t_s + 128 * (n & 1) + 64, long_tile(n), 1, io, true);
+                    commit(bar(kLongFree + n % kLongStages));
                 }
             }
             if (!waits) {
@@ -652,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float slope2 = GENERAL && a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
         bool go = !skip;
         for (int n = 0; go && n < blocks; ++n) {
-            const int j0 = key0 + n * kTile, st = n % kStages;
+            const int j0 = key0 + n * kTile;
             const bool masked = j0 < all_lo || j0 + kTile > all_hi;
             const int lo = span.x - j0, len = max(0, span.y - span.x);
             const uint32_t ts = t_s + lanes + 128 * (n & 1) + 64 * half;
@@ -704,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st16(ts + 16 * q, pk);
             }
             if (masked && half == 0)
-                clear_not_finite<T>(base + lay.ring + st * lay.stage, r, j0 + r, key0, key1, halves, bad);
+                clear_not_finite<T>(long_tile(n), r, j0 + r, key0, key1, halves, bad);
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
@@ -737,9 +785,9 @@ cudaError_t launch(const TileArgs &args, const CUtensorMap (&map)[4], const Info
     const gn_attn_packed_args &a = args.p.a;
     const int halves = a.dim > 64 ? 2 : 1;
     static std::atomic<uint64_t> done_kv{0}, done_q{0};
-    cudaError_t e = allow_shared(reinterpret_cast<const void *>(attn_dkv_kernel<T, GENERAL>), kv_layout(2).total + 1024, done_kv);
+    cudaError_t e = allow_shared(reinterpret_cast<const void *>(attn_dkv_kernel<T, GENERAL>), layout(2).total, done_kv);
     if (e == cudaSuccess)
-        e = allow_shared(reinterpret_cast<const void *>(attn_dq_kernel<T, GENERAL>), q_layout(2).total + 1024, done_q);
+        e = allow_shared(reinterpret_cast<const void *>(attn_dq_kernel<T, GENERAL>), layout(2).total, done_q);
     if (e != cudaSuccess) return e;
     const int64_t rows = info.padded * a.heads;
     e = tc::launch_pdl(attn_rows_info_kernel<T>, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0, s, args.p, info);
@@ -749,11 +797,11 @@ cudaError_t launch(const TileArgs &args, const CUtensorMap (&map)[4], const Info
     kv.tiles = static_cast<int>((a.tokens_k + kTile - 1) / kTile);
     q.tiles = static_cast<int>((a.tokens_q + kTile - 1) / kTile);
     e = tc::launch_pdl(attn_dkv_kernel<T, GENERAL>, dim3(static_cast<unsigned>(static_cast<int64_t>(kv.tiles) * a.kv_heads)),
-                       dim3(kThreads), kv_layout(halves).total + 1024, s, map[0], map[1], map[2], map[3], kv, info);
+                       dim3(kThreads), layout(halves).total, s, map[0], map[1], map[2], map[3], kv, info);
     if (e != cudaSuccess) return e;
     ++*launches;
     e = tc::launch_pdl(attn_dq_kernel<T, GENERAL>, dim3(static_cast<unsigned>(static_cast<int64_t>(q.tiles) * a.heads)),
-                       dim3(kThreads), q_layout(halves).total + 1024, s, map[0], map[1], map[2], map[3], q, info);
+                       dim3(kThreads), layout(halves).total, s, map[0], map[1], map[2], map[3], q, info);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
