@@ -119,7 +119,8 @@ int gn_layer_norm(const void *x, const void *weight, const void *bias, void *y, 
     if (rows == 0) return GN_OK;
     gn::NormArgs a = {x, weight, bias, y, mean, rstd, rows, static_cast<int>(cols), x_stride, y_stride, eps, format,
                       weight_format};
-    const cudaError_t e = gn::launch_layer_norm(a, d.sm_count, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = gn::launch_layer_norm(a, d.sm_count, {wait_timeout_ns(), d.status_word, d.status_host},
+                                               static_cast<cudaStream_t>(stream));
     return launched(e, e == cudaSuccess);
 }
 
@@ -178,7 +179,8 @@ int gn_layer_norm_backward(const void *dy, const void *x, const void *weight, co
     gn::NormGradArgs a = {dy, x, weight, mean, rstd, dx, dweight, dbias, rows, static_cast<int>(cols), dy_stride,
                           x_stride, dx_stride, format, weight_format, static_cast<float *>(workspace)};
     int launches = 0;
-    const cudaError_t e = gn::launch_layer_norm_backward(a, d.sm_count, s, &launches);
+    const cudaError_t e = gn::launch_layer_norm_backward(a, d.sm_count, {wait_timeout_ns(), d.status_word, d.status_host}, s,
+                                                         &launches);
     return launched(e, launches);
 }
 

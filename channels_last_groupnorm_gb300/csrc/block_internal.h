@@ -12,6 +12,12 @@
 
 namespace gn {
 
+// The bound on a kernel's waits, and the words that tell when one ran out.
+struct WaitLimit {
+    uint64_t timeout_ns;
+    unsigned int *status, *host_status;   // device addresses
+};
+
 // ---- layer norm (norm_kernels.cu) -------------------------------------------
 constexpr int kNormMaxCols = 16384;
 
@@ -37,10 +43,11 @@ struct NormGradArgs {
     float *partial;               // [blocks][2][cols] when the weight's gradient is wanted
 };
 
-cudaError_t launch_layer_norm(const NormArgs &a, int sm_count, cudaStream_t s);
-// The CTAs that launch_layer_norm_backward uses, each with a row of partial sums.
+cudaError_t launch_layer_norm(const NormArgs &a, int sm_count, const WaitLimit &limit, cudaStream_t s);
+// The most CTAs that launch_layer_norm_backward uses, each with a row of partial sums.
 int layer_norm_blocks(int64_t rows, int cols, int sm_count);
-cudaError_t launch_layer_norm_backward(const NormGradArgs &a, int sm_count, cudaStream_t s, int *launches);
+cudaError_t launch_layer_norm_backward(const NormGradArgs &a, int sm_count, const WaitLimit &limit, cudaStream_t s,
+                                       int *launches);
 
 // ---- rotary positions over several axes (rope_kernels.cu) -------------------
 constexpr int kRopeMaxPairs = 128;
@@ -62,12 +69,6 @@ struct RopeArgs {
 cudaError_t launch_rope(const RopeArgs &a, int sm_count, cudaStream_t s);
 
 // ---- attention of packed documents (pattn_*.cu) ------------------------------
-// The bound on a kernel's waits, and the words that tell when one ran out.
-struct WaitLimit {
-    uint64_t timeout_ns;
-    unsigned int *status, *host_status;   // device addresses
-};
-
 struct PackedAttn {
     gn_attn_packed_args a;
     int group;                    // query heads per key / value head

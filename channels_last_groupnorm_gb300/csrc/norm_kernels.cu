@@ -7,18 +7,31 @@
 //             dx = rstd (g - sum(g) / C - h sum(g h) / C),
 //             dw = sum over rows of dy h,  db = sum over rows of dy
 //
+// Both are bound by memory (forward x in, y out; backward x, dy in, dx out).
 // A row is held in the registers of `tpr` threads (NV slots each of EPV
 // consecutive elements), so that x (and dy) are read once, the variance is
 // the second pass over registers about the exact mean, and nothing is
-// recomputed.  All sums are fp32; y and dx are rounded once to the type of x,
-// dw and db once to the type of the weight.
+// recomputed.  A thread keeps its columns for every row that it meets: in the
+// backward pass it adds up its part of dw and db in registers.  All sums are
+// fp32; y and dx are rounded once to the type of x, dw and db once to the type
+// of the weight.
+//
+// Two ways to the rows:
+//  * streamed: one CTA per SM, rows brought by bulk copies into a ring of
+//    shared memory that a warp of its own keeps full, so that up to 200 KB per
+//    SM are in flight whatever the arithmetic does.  For rows of whole 16-byte
+//    vectors, when every CTA meets several batches of rows.
+//  * direct: plain loads, many CTAs.  For few rows, where the ring would not
+//    fill, and for rows that are not made of 16-byte vectors.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "block_internal.h"
+#include "gn_ptx.cuh"
 #include "tc_common.cuh"
 
 namespace gn {
@@ -38,12 +51,37 @@ struct alignas(sizeof(T) * N) Pack {
     T v[N];
 };
 
-// One element of the weight or the bias, in its own format.
-__device__ __forceinline__ float load_param(const void *p, int format, int c)
+template <typename T, int N>
+__device__ __forceinline__ void load_as(const T *p, float (&f)[N])
 {
-    if (format == GN_FORMAT_FP32) return __ldg(static_cast<const float *>(p) + c);
-    if (format == GN_FORMAT_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[c]);
-    return __half2float(static_cast<const __half *>(p)[c]);
+    // (a parameter vector has only its element's alignment)
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = to_float(p[e]);
+}
+
+// N consecutive elements of the weight or the bias, in its own format.
+template <int N>
+__device__ __forceinline__ void load_params(const void *p, int format, int c, float (&f)[N])
+{
+    if (format == GN_FORMAT_FP32) {
+        const float *q = static_cast<const float *>(p) + c;
+        if (N % 4 == 0 && reinterpret_cast<uintptr_t>(q) % 16 == 0) {
+#pragma unroll
+            for (int e = 0; e < N / 4; ++e) {
+                const float4 v = reinterpret_cast<const float4 *>(q)[e];
+                f[4 * e] = v.x;
+                f[(4 * e + 1) % N] = v.y;
+                f[(4 * e + 2) % N] = v.z;
+                f[(4 * e + 3) % N] = v.w;
+            }
+        } else {
+            load_as(q, f);
+        }
+    } else if (format == GN_FORMAT_BF16) {
+        load_as(static_cast<const __nv_bfloat16 *>(p) + c, f);
+    } else {
+        load_as(static_cast<const __half *>(p) + c, f);
+    }
 }
 
 __device__ __forceinline__ void store_param(void *p, int format, int c, float v)
@@ -56,181 +94,461 @@ __device__ __forceinline__ void store_param(void *p, int format, int c, float v)
         static_cast<__half *>(p)[c] = __float2half_rn(v);
 }
 
-// Sum of one or two values over the tpr threads that share a row: within a
-// warp (tpr <= 32, a power of two), or over the whole CTA (tpr == blockDim.x).
-// The CTA's sums go through `scratch`, two buffers taken in turn so that one
-// barrier per reduction is enough.
+// The threads of one row: tpr of them (a power of two up to 32, or whole
+// warps), group g of the CTA's.
+struct Group {
+    int tpr, g, lane;                // lane: this thread's place in its group
+    float (*scratch)[32][2];         // two buffers of the group, taken in turn
+    int turn;
+};
+
+// Sums of N values over a group.  Within a warp by shuffles; over several
+// warps through the group's scratch, whose two buffers make one barrier per
+// reduction enough.
 template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float (*scratch)[32][2], int &turn)
+__device__ __forceinline__ void row_sum(float (&v)[N], Group &gr)
 {
-    const int width = tpr < 32 ? tpr : 32;
-    for (int o = width >> 1; o > 0; o >>= 1)
+    if (gr.tpr < 32) {
+        for (int o = gr.tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+        return;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
         for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-    if (tpr <= 32) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = tpr >> 5;
-    float(*s)[2] = scratch[turn];
-    turn ^= 1;
+    if (gr.tpr == 32) return;
+    const int warp = gr.lane >> 5, lane = threadIdx.x & 31, warps = gr.tpr >> 5;
+    float(*s)[2] = gr.scratch[gr.turn];
+    gr.turn ^= 1;
     if (lane == 0)
 #pragma unroll
         for (int n = 0; n < N; ++n) s[warp][n] = v[n];
-    __syncthreads();
+    named_sync(1 + gr.g, gr.tpr);
 #pragma unroll
     for (int n = 0; n < N; ++n) v[n] = lane < warps ? s[lane][n] : 0.f;
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
         for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
 }
 
+// A thread's slots of a row: slot k at element (lane + k tpr) EPV; zeros past
+// the end.  They stay in the row's own type: half the registers for half the
+// cost of converting them twice.
 template <typename T, int EPV, int NV>
-__device__ __forceinline__ void load_row(const T *row, int lane, int tpr, int cols, float (&f)[NV][EPV])
+struct Row {
+    Pack<T, EPV> p[NV];
+
+    __device__ __forceinline__ Row(const T *row, const Group &gr, int cols)
+    {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (gr.lane + k * gr.tpr) * EPV;
+            if (c < cols) {
+                p[k] = *reinterpret_cast<const Pack<T, EPV> *>(row + c);
+            } else {
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) p[k].v[e] = from_float<T>(0.f);
+            }
+        }
+    }
+    __device__ __forceinline__ float at(int k, int e) const { return to_float(p[k].v[e]); }
+};
+
+// The thread's part of the weight (ones without) or the bias (zeros): held in
+// registers, or (kHeld false: where those are full) asked for at every row.
+template <int EPV, int NV, bool kHeld = (NV * EPV <= 16)>
+struct Own {
+    const void *p;
+    int format, cols;
+    float fill, v[kHeld ? NV : 1][EPV];
+
+    __device__ __forceinline__ void fetch(const Group &gr, int k, float (&f)[EPV]) const
+    {
+        const int c = (gr.lane + k * gr.tpr) * EPV;
+        if (p && c < cols) {
+            load_params<EPV>(p, format, c, f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) f[e] = fill;
+        }
+    }
+    __device__ __forceinline__ Own(const void *ptr, int fmt, const Group &gr, int n, float other)
+        : p(ptr), format(fmt), cols(n), fill(other)
+    {
+        if (kHeld)
+#pragma unroll
+            for (int k = 0; k < (kHeld ? NV : 1); ++k) fetch(gr, k, v[k]);
+    }
+    __device__ __forceinline__ void get(const Group &gr, int k, float (&f)[EPV]) const
+    {
+        if (kHeld) {
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) f[e] = v[kHeld ? k : 0][e];
+        } else {
+            fetch(gr, k, f);
+        }
+    }
+};
+
+// One row from registers: statistics out, y out.
+template <typename T, int EPV, int NV, typename Params>
+__device__ __forceinline__ void norm_row(const NormArgs &a, const Row<T, EPV, NV> &x, const Params &w, const Params &b,
+                                         Group &gr, int64_t row, bool live)
 {
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    float s[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) s[0] += x.at(k, e);
+    row_sum(s, gr);
+    const float mean = s[0] * inv;
+    float q[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int c = (lane + k * tpr) * EPV;
-        Pack<T, EPV> p;
-        if (c < cols) p = *reinterpret_cast<const Pack<T, EPV> *>(row + c);
+        if ((gr.lane + k * gr.tpr) * EPV >= a.cols) break;
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) f[k][e] = c < cols ? to_float(p.v[e]) : 0.f;
+        for (int e = 0; e < EPV; ++e) {
+            const float d = x.at(k, e) - mean;
+            q[0] = fmaf(d, d, q[0]);
+        }
+    }
+    row_sum(q, gr);
+    const float rstd = rsqrtf(fmaf(q[0], inv, a.eps));   // (two steps of fp32 at most)
+    if (!live) return;
+    if (gr.lane == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+    T *y = static_cast<T *>(a.y) + row * a.y_stride;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = (gr.lane + k * gr.tpr) * EPV;
+        if (c >= a.cols) break;
+        Pack<T, EPV> p;
+        float wk[EPV], bk[EPV];
+        w.get(gr, k, wk);
+        b.get(gr, k, bk);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) p.v[e] = from_float<T>(fmaf((x.at(k, e) - mean) * rstd, wk[e], bk[e]));
+        *reinterpret_cast<Pack<T, EPV> *>(y + c) = p;
     }
 }
 
+// One row of the backward pass from registers: dx out, column sums on.
+template <typename T, int EPV, int NV, typename Params>
+__device__ __forceinline__ void norm_grad_row(const NormGradArgs &a, const Row<T, EPV, NV> &x, const Row<T, EPV, NV> &dy,
+                                              const Params &w, float (&sw)[NV][EPV], float (&sb)[NV][EPV], float mean,
+                                              float rstd, Group &gr, int64_t row, bool live)
+{
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    const bool sums = live && a.weight;
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        if ((gr.lane + k * gr.tpr) * EPV >= a.cols) break;
+        float wk[EPV];
+        w.get(gr, k, wk);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) {
+            const float h = (x.at(k, e) - mean) * rstd, d = dy.at(k, e), g = d * wk[e];
+            if (sums) {
+                sw[k][e] = fmaf(d, h, sw[k][e]);
+                sb[k][e] += d;
+            }
+            s[0] += g;
+            s[1] = fmaf(g, h, s[1]);
+        }
+    }
+    row_sum(s, gr);
+    if (!live) return;
+    T *dx = static_cast<T *>(a.dx) + row * a.dx_stride;
+    const float m0 = s[0] * inv, m1 = s[1] * inv;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = (gr.lane + k * gr.tpr) * EPV;
+        if (c >= a.cols) break;
+        Pack<T, EPV> p;
+        float wk[EPV];
+        w.get(gr, k, wk);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) {
+            const float h = (x.at(k, e) - mean) * rstd;
+            p.v[e] = from_float<T>(rstd * (fmaf(dy.at(k, e), wk[e], -m0) - h * m1));
+        }
+        *reinterpret_cast<Pack<T, EPV> *>(dx + c) = p;
+    }
+}
+
+// A CTA's column sums into its row of partial sums.  Groups that share a warp
+// are added up by shuffles; then every group (or warp) puts its sums down in
+// `columns` ([groups or warps][2 cols]) and all threads add them up, column by
+// column, in a fixed order.  One group of several warps needs neither.
+template <int EPV, int NV>
+__device__ __forceinline__ void write_partial(const NormGradArgs &a, float (&sw)[NV][EPV], float (&sb)[NV][EPV],
+                                              const Group &gr, int workers, float *columns)
+{
+    float *out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    const int parts = gr.tpr < 32 ? workers / 32 : workers / gr.tpr;
+    const bool worker = static_cast<int>(threadIdx.x) < workers;
+    if (worker) {
+        for (int o = gr.tpr; o < 32; o <<= 1)
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) {
+                    sw[k][e] += __shfl_xor_sync(0xffffffffu, sw[k][e], o);
+                    sb[k][e] += __shfl_xor_sync(0xffffffffu, sb[k][e], o);
+                }
+        const int part = gr.tpr < 32 ? threadIdx.x >> 5 : gr.g;
+        float *to = parts > 1 ? columns + static_cast<int64_t>(part) * 2 * a.cols : out;
+        if (gr.tpr >= 32 || (static_cast<int>(threadIdx.x) & 31) < gr.tpr) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (gr.lane + k * gr.tpr) * EPV;
+                if (c >= a.cols) break;
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) {
+                    to[c + e] = sw[k][e];
+                    to[a.cols + c + e] = sb[k][e];
+                }
+            }
+        }
+    }
+    if (parts == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.cols; c += blockDim.x) {
+        float v = columns[c];
+        for (int p = 1; p < parts; ++p) v += columns[p * 2 * a.cols + c];
+        out[c] = v;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// direct
+// ---------------------------------------------------------------------------
+// (rows up to kNormMaxCols: 2048 slots of 8 or 4096 of 4 take 4 a thread)
+template <int EPV, int NV>
+constexpr int direct_threads() { return EPV == 8 && NV == 4 ? 512 : 1024; }
+
 template <typename T, int EPV, int NV>
-__global__ void __launch_bounds__(1024) norm_forward_kernel(const NormArgs a, int tpr)
+__global__ void __launch_bounds__(direct_threads<EPV, NV>()) norm_direct_kernel(const NormArgs a, int tpr)
 {
     __shared__ float scratch[2][32][2];
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
-    const int per = blockDim.x / tpr, lane = threadIdx.x % tpr;
-    const float inv = 1.0f / static_cast<float>(a.cols);
-    int turn = 0;
+    const int per = blockDim.x / tpr;
+    Group gr = {tpr, 0, static_cast<int>(threadIdx.x) % tpr, scratch, 0};
+    const Own<EPV, NV> w(a.weight, a.weight_format, gr, a.cols, 1.f), b(a.bias, a.weight_format, gr, a.cols, 0.f);
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * per; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * per) {
         const int64_t row = r0 + threadIdx.x / tpr;
         const bool live = row < a.rows;   // whole warps stay for the shuffles
-        float f[NV][EPV];
-        const T *x = static_cast<const T *>(a.x) + (live ? row : r0) * a.x_stride;
-        load_row<T, EPV, NV>(x, lane, tpr, a.cols, f);
-        float s[1] = {0.f};
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int e = 0; e < EPV; ++e) s[0] += f[k][e];
-        row_sum(s, tpr, scratch, turn);
-        const float mean = s[0] * inv;
-        float q[1] = {0.f};
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int e = 0; e < EPV; ++e) {
-                f[k][e] -= mean;
-                if ((lane + k * tpr) * EPV < a.cols) q[0] = fmaf(f[k][e], f[k][e], q[0]);
-            }
-        row_sum(q, tpr, scratch, turn);
-        const float rstd = 1.0f / sqrtf(fmaf(q[0], inv, a.eps));
-        if (!live) continue;
-        if (lane == 0) {
-            if (a.mean) a.mean[row] = mean;
-            if (a.rstd) a.rstd[row] = rstd;
-        }
-        T *y = static_cast<T *>(a.y) + row * a.y_stride;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (lane + k * tpr) * EPV;
-            if (c >= a.cols) break;
-            Pack<T, EPV> p;
-#pragma unroll
-            for (int e = 0; e < EPV; ++e) {
-                float v = f[k][e] * rstd;
-                if (a.weight) v *= load_param(a.weight, a.weight_format, c + e);
-                if (a.bias) v += load_param(a.bias, a.weight_format, c + e);
-                p.v[e] = from_float<T>(v);
-            }
-            *reinterpret_cast<Pack<T, EPV> *>(y + c) = p;
-        }
+        const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + (live ? row : r0) * a.x_stride, gr, a.cols);
+        norm_row(a, x, w, b, gr, row, live);
     }
 }
 
 template <typename T, int EPV, int NV>
-__global__ void __launch_bounds__(1024) norm_backward_kernel(const NormGradArgs a, int tpr)
+__global__ void __launch_bounds__(direct_threads<EPV, NV>()) norm_grad_direct_kernel(const NormGradArgs a, int tpr)
 {
-    extern __shared__ float columns[];    // [2][cols], tpr < blockDim.x with a weight
+    extern __shared__ __align__(128) uint8_t smem[];    // with a weight and several groups: their column sums
     __shared__ float scratch[2][32][2];
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
-    const int per = blockDim.x / tpr, lane = threadIdx.x % tpr;
-    const float inv = 1.0f / static_cast<float>(a.cols);
+    const int per = blockDim.x / tpr;
+    Group gr = {tpr, 0, static_cast<int>(threadIdx.x) % tpr, scratch, 0};
     float sw[NV][EPV] = {}, sb[NV][EPV] = {};
-    int turn = 0;
+    const Own<EPV, NV> w(a.weight, a.weight_format, gr, a.cols, 1.f);
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * per; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * per) {
         const int64_t row = r0 + threadIdx.x / tpr;
         const bool live = row < a.rows;
         const int64_t at = live ? row : r0;
-        float x[NV][EPV], g[NV][EPV];
-        load_row<T, EPV, NV>(static_cast<const T *>(a.x) + at * a.x_stride, lane, tpr, a.cols, x);
-        load_row<T, EPV, NV>(static_cast<const T *>(a.dy) + at * a.dy_stride, lane, tpr, a.cols, g);
-        const float mean = a.mean[at], rstd = a.rstd[at];
-        float s[2] = {0.f, 0.f};
+        const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + at * a.x_stride, gr, a.cols);
+        const Row<T, EPV, NV> dy(static_cast<const T *>(a.dy) + at * a.dy_stride, gr, a.cols);
+        norm_grad_row(a, x, dy, w, sw, sb, a.mean[at], a.rstd[at], gr, row, live);
+    }
+    if (!a.weight) return;
+    gr.g = threadIdx.x / tpr;
+    write_partial<EPV, NV>(a, sw, sb, gr, blockDim.x, reinterpret_cast<float *>(smem));
+}
+
+// ---------------------------------------------------------------------------
+// streamed
+// ---------------------------------------------------------------------------
+constexpr uint32_t kRingBytes = 208 * 1024;   // (with a copy of the weight in the backward pass)
+constexpr int kMaxStages = 24;
+constexpr int kStreamThreads = 384;           // of the row groups; 128 registers each
+
+// The ring: `tensors` x `per` rows of row_bytes a stage; a batch is the next
+// `per` rows, one for each group of threads.
+struct Stream {
+    int tpr, per, stages;
+    uint32_t row_bytes, stage_bytes;
+    WaitLimit limit;
+};
+
+// Brings a CTA's batches: `rows` of N tensors whose rows are `stride` bytes
+// apart.  One warp; a copy per tensor where its rows lie end to end.
+template <int N>
+__device__ __forceinline__ void stream_rows(const Stream &s, const char *const (&src)[N], const int64_t (&stride)[N],
+                                            int64_t rows, uint32_t ring, uint32_t full, uint32_t empty, volatile int *abort)
+{
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * s.per; r0 < rows;
+         r0 += static_cast<int64_t>(gridDim.x) * s.per, ++n) {
+        const int st = n % s.stages;
+        const int have = static_cast<int>(min(static_cast<int64_t>(s.per), rows - r0));
+        bool go = true;
+        if (n >= s.stages)
+            go = tc::wait(empty + 8 * st, (n / s.stages - 1) & 1, abort, s.limit.timeout_ns, s.limit.status, s.limit.host_status);
+        if (!__all_sync(0xffffffffu, go)) break;
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, N * have * s.row_bytes);
+        __syncwarp();
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (lane + k * tpr) * EPV;
-            if (c >= a.cols) break;
-#pragma unroll
-            for (int e = 0; e < EPV; ++e) {
-                x[k][e] = (x[k][e] - mean) * rstd;
-                if (a.weight) {
-                    if (live) {
-                        sw[k][e] = fmaf(g[k][e], x[k][e], sw[k][e]);
-                        sb[k][e] += g[k][e];
-                    }
-                    g[k][e] *= load_param(a.weight, a.weight_format, c + e);
-                }
-                s[0] += g[k][e];
-                s[1] = fmaf(g[k][e], x[k][e], s[1]);
+        for (int t = 0; t < N; ++t) {
+            const uint32_t dst = ring + st * s.stage_bytes + t * s.per * s.row_bytes;
+            if (stride[t] == s.row_bytes) {
+                if (lane == 0) bulk_load(dst, src[t] + r0 * stride[t], have * s.row_bytes, full + 8 * st);
+            } else {
+                for (int r = lane; r < have; r += 32)
+                    bulk_load(dst + r * s.row_bytes, src[t] + (r0 + r) * stride[t], s.row_bytes, full + 8 * st);
             }
         }
-        row_sum(s, tpr, scratch, turn);
-        if (!live) continue;
-        T *dx = static_cast<T *>(a.dx) + row * a.dx_stride;
-        const float m0 = s[0] * inv, m1 = s[1] * inv;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (lane + k * tpr) * EPV;
-            if (c >= a.cols) break;
-            Pack<T, EPV> p;
-#pragma unroll
-            for (int e = 0; e < EPV; ++e) p.v[e] = from_float<T>(rstd * (g[k][e] - m0 - x[k][e] * m1));
-            *reinterpret_cast<Pack<T, EPV> *>(dx + c) = p;
+    }
+    // what is still in flight lands before the CTA ends
+    for (int k = max(0, n - s.stages); k < n; ++k) tc::drain(full + 8 * (k % s.stages), (k / s.stages) & 1, s.limit.timeout_ns);
+}
+
+struct StreamShared {
+    float scratch[6][2][32][2];           // per group of several warps
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    int abort;
+};
+
+// The setup both kernels share; the ring begins after the fixed part.
+__device__ __forceinline__ void stream_setup(StreamShared &sh, const Stream &s, int workers)
+{
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < s.stages; ++i) {
+            mbar_init(smem_addr(&sh.full[i]), 1);
+            mbar_init(smem_addr(&sh.empty[i]), workers / 32);
+        }
+        sh.abort = (*reinterpret_cast<volatile unsigned int *>(s.limit.status) != 0u) ? 1 : 0;
+        mbar_init_fence();
+    }
+    tc::griddep_wait();
+    if (threadIdx.x == 0) tc::griddep_launch_dependents();
+}
+
+// (a wait that runs out is reported and answered with whatever the stage
+// holds: every thread goes on, so that none is left at a barrier)
+__device__ __forceinline__ void stream_wait(StreamShared &sh, const Stream &s, int st, int parity)
+{
+    tc::wait(smem_addr(&sh.full[st]), parity, &sh.abort, s.limit.timeout_ns, s.limit.status, s.limit.host_status);
+}
+
+__device__ __forceinline__ void stream_release(StreamShared &sh, int st)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&sh.empty[st]));
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kStreamThreads + 32, 1)
+    norm_stream_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ Stream s)
+{
+    constexpr int EPV = 16 / sizeof(T);
+    extern __shared__ __align__(128) uint8_t smem[];
+    StreamShared &sh = *reinterpret_cast<StreamShared *>(smem);
+    uint8_t *ring = smem + (sizeof(StreamShared) + 127) / 128 * 128;
+    const int workers = s.per * s.tpr;
+    stream_setup(sh, s, workers);
+    __syncthreads();
+    const bool skip = sh.abort != 0;
+    if (static_cast<int>(threadIdx.x) >= workers) {
+        const char *const src[1] = {static_cast<const char *>(a.x)};
+        const int64_t stride[1] = {a.x_stride * static_cast<int64_t>(sizeof(T))};
+        if (!skip)
+            stream_rows<1>(s, src, stride, a.rows, smem_addr(ring), smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
+        return;
+    }
+    if (skip) return;
+    Group gr = {s.tpr, static_cast<int>(threadIdx.x) / s.tpr, static_cast<int>(threadIdx.x) % s.tpr, nullptr, 0};
+    if (s.tpr > 32) gr.scratch = sh.scratch[gr.g];
+    const Own<EPV, NV, true> w(a.weight, a.weight_format, gr, a.cols, 1.f), b(a.bias, a.weight_format, gr, a.cols, 0.f);
+    int st = 0, parity = 0;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * s.per; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * s.per) {
+        const int64_t row = r0 + gr.g;
+        stream_wait(sh, s, st, parity);
+        const Row<T, EPV, NV> x(reinterpret_cast<const T *>(ring + st * s.stage_bytes + gr.g * s.row_bytes), gr, a.cols);
+        stream_release(sh, st);
+        if (++st == s.stages) {
+            st = 0;
+            parity ^= 1;
+        }
+        norm_row(a, x, w, b, gr, row, row < a.rows);
+    }
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kStreamThreads + 32, 1)
+    norm_grad_stream_kernel(const __grid_constant__ NormGradArgs a, const __grid_constant__ Stream s)
+{
+    constexpr int EPV = 16 / sizeof(T);
+    extern __shared__ __align__(128) uint8_t smem[];
+    StreamShared &sh = *reinterpret_cast<StreamShared *>(smem);
+    float *weight = reinterpret_cast<float *>(smem + (sizeof(StreamShared) + 127) / 128 * 128);
+    uint8_t *ring = reinterpret_cast<uint8_t *>(weight) + (a.weight ? (4 * a.cols + 127) / 128 * 128 : 0);
+    const int workers = s.per * s.tpr;
+    stream_setup(sh, s, workers);
+    if (a.weight)
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            float one[1];
+            load_params<1>(a.weight, a.weight_format, c, one);
+            weight[c] = one[0];
+        }
+    __syncthreads();
+    const bool skip = sh.abort != 0;
+    Group gr = {s.tpr, static_cast<int>(threadIdx.x) / s.tpr, static_cast<int>(threadIdx.x) % s.tpr, nullptr, 0};
+    float sw[NV][EPV] = {}, sb[NV][EPV] = {};
+    if (static_cast<int>(threadIdx.x) >= workers) {
+        const char *const src[2] = {static_cast<const char *>(a.x), static_cast<const char *>(a.dy)};
+        const int64_t stride[2] = {a.x_stride * static_cast<int64_t>(sizeof(T)), a.dy_stride * static_cast<int64_t>(sizeof(T))};
+        if (!skip)
+            stream_rows<2>(s, src, stride, a.rows, smem_addr(ring), smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
+    } else if (!skip) {
+        if (s.tpr > 32) gr.scratch = sh.scratch[gr.g];
+        const Own<EPV, NV, false> w(a.weight ? weight : nullptr, GN_FORMAT_FP32, gr, a.cols, 1.f);
+        const int64_t step = static_cast<int64_t>(gridDim.x) * s.per;
+        int64_t row = static_cast<int64_t>(blockIdx.x) * s.per + gr.g;
+        // (the statistics are asked for a batch ahead)
+        float mean = row < a.rows ? __ldg(a.mean + row) : 0.f, rstd = row < a.rows ? __ldg(a.rstd + row) : 0.f;
+        int st = 0, parity = 0;
+        for (int64_t r0 = row - gr.g; r0 < a.rows; r0 += step, row += step) {
+            const float mean_now = mean, rstd_now = rstd;
+            if (row + step < a.rows) {
+                mean = __ldg(a.mean + row + step);
+                rstd = __ldg(a.rstd + row + step);
+            }
+            stream_wait(sh, s, st, parity);
+            const uint8_t *at = ring + st * s.stage_bytes + gr.g * s.row_bytes;
+            const Row<T, EPV, NV> x(reinterpret_cast<const T *>(at), gr, a.cols);
+            const Row<T, EPV, NV> dy(reinterpret_cast<const T *>(at + s.per * s.row_bytes), gr, a.cols);
+            stream_release(sh, st);
+            if (++st == s.stages) {
+                st = 0;
+                parity ^= 1;
+            }
+            norm_grad_row(a, x, dy, w, sw, sb, mean_now, rstd_now, gr, row, row < a.rows);
         }
     }
     if (!a.weight) return;
-    // the CTA's sums: the row groups one after the other (a fixed order), then out
-    float *out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-    if (per > 1) {
-        for (int g = 0; g < per; ++g) {
-            if (static_cast<int>(threadIdx.x) / tpr == g)
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-#pragma unroll
-                    for (int e = 0; e < EPV; ++e) {
-                        const int c = (lane + k * tpr) * EPV + e;
-                        if (c >= a.cols) continue;
-                        columns[c] = (g ? columns[c] : 0.f) + sw[k][e];
-                        columns[a.cols + c] = (g ? columns[a.cols + c] : 0.f) + sb[k][e];
-                    }
-            __syncthreads();
-        }
-        for (int c = threadIdx.x; c < 2 * a.cols; c += blockDim.x) out[c] = columns[c];
-    } else {
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int e = 0; e < EPV; ++e) {
-                const int c = (lane + k * tpr) * EPV + e;
-                if (c >= a.cols) continue;
-                out[c] = sw[k][e];
-                out[a.cols + c] = sb[k][e];
-            }
-    }
+    __syncthreads();                      // every copy has landed, every row is done: the ring is free
+    write_partial<EPV, NV>(a, sw, sb, gr, workers, reinterpret_cast<float *>(ring));
 }
 
 // dw and db from the CTAs' partial sums: a warp's lanes take 32 neighbouring
@@ -244,6 +562,7 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormGradArgs a,
     const int c = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (c < 2 * a.cols)
+#pragma unroll 8
         for (int b = warp; b < blocks; b += 8) v += a.partial[static_cast<int64_t>(b) * 2 * a.cols + c];
     part[warp][lane] = v;
     __syncthreads();
@@ -256,26 +575,17 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormGradArgs a,
         store_param(a.dbias, a.weight_format, c - a.cols, v);
 }
 
-struct Shape {
-    int tpr, threads, nv;
-};
-
-// `slots` pieces of a row over tpr threads of nv slots: four slots a thread
-// where that leaves at least a warp's worth of rows, one thread group per row.
-Shape norm_shape(int slots)
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// Threads per row for `slots` of a row, nv each.
+int threads_per_row(int slots, int nv)
 {
-    Shape s;
-    s.nv = 4;
-    int tpr = 1;
-    while (tpr * s.nv < slots) tpr *= 2;
-    if (tpr > 1024) {
-        tpr = 1024;
-        s.nv = 16;
-    }
-    s.tpr = tpr;
-    s.threads = std::max(tpr, 256);
-    if (tpr > 32) s.threads = tpr;
-    return s;
+    const int need = (slots + nv - 1) / nv;
+    if (need > 32) return (need + 31) / 32 * 32;
+    int t = 1;
+    while (t < need) t *= 2;
+    return t;
 }
 
 bool vectors_ok(int cols, int epv, const void *const *ptrs, int n, const int64_t *strides)
@@ -286,64 +596,167 @@ bool vectors_ok(int cols, int epv, const void *const *ptrs, int n, const int64_t
     return true;
 }
 
+// The streamed form's shape, or stages = 0 where it does not pay: it wants at
+// least three stages of ring, and at least four batches of rows for every SM.
+// A thread has two slots of a short row and four of a longer one: with one slot
+// each (24 warps on a row of 6144) the reductions' instructions took longer
+// than the row's memory does (62 us against 38 us for 4608 x 6144 forward).
+Stream stream_shape(int64_t rows, int cols, int size, int tensors, size_t fixed, int sm_count, int *nv)
+{
+    Stream s = {};
+    const int slots = cols * size / 16;
+    *nv = slots <= 64 ? 2 : 4;
+    s.tpr = threads_per_row(slots, *nv);
+    s.per = std::max(1, kStreamThreads / s.tpr);
+    s.row_bytes = static_cast<uint32_t>(cols * size);
+    s.stage_bytes = static_cast<uint32_t>(tensors * s.per) * s.row_bytes;
+    s.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kRingBytes - fixed) / s.stage_bytes));
+    if (s.tpr > kStreamThreads || s.stages < 3 || rows < static_cast<int64_t>(4) * sm_count * s.per) s.stages = 0;
+    return s;
+}
+
+// Lets `kernel` have `bytes` of dynamic shared memory, once per device.
+cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (e != cudaSuccess || (dev < 64 && (done.load() & bit))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
+}
+
+constexpr size_t kStreamFixed = (sizeof(StreamShared) + 127) / 128 * 128;
+constexpr size_t kStreamBytes = kStreamFixed + kRingBytes;
+
+size_t weight_copy(const NormGradArgs &a) { return a.weight ? (4u * static_cast<size_t>(a.cols) + 127) / 128 * 128 : 0; }
+
+// Floats that `threads` of a CTA put down in write_partial.
+size_t columns_bytes(const NormGradArgs &a, int tpr, int threads)
+{
+    const size_t parts = static_cast<size_t>(tpr < 32 ? threads / 32 : threads / tpr);
+    return a.weight && parts > 1 ? parts * 8u * static_cast<size_t>(a.cols) : 0;
+}
+
+template <typename T, int NV>
+cudaError_t forward_stream(const NormArgs &a, const Stream &s, int sm_count, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_stream_kernel<T, NV>), kStreamBytes, done);
+    if (e != cudaSuccess) return e;
+    return tc::launch_pdl(norm_stream_kernel<T, NV>, dim3(static_cast<unsigned>(sm_count)), dim3(s.per * s.tpr + 32),
+                          kStreamFixed + s.stages * s.stage_bytes, st, a, s);
+}
+
+template <typename T, int NV>
+cudaError_t backward_stream(const NormGradArgs &a, const Stream &s, int sm_count, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_grad_stream_kernel<T, NV>), kStreamBytes, done);
+    if (e != cudaSuccess) return e;
+    // (per groups of four or two slots a thread: the column sums are at most 98 KB)
+    const size_t ring = std::max<size_t>(s.stages * s.stage_bytes, columns_bytes(a, s.tpr, s.per * s.tpr));
+    return tc::launch_pdl(norm_grad_stream_kernel<T, NV>, dim3(static_cast<unsigned>(sm_count)), dim3(s.per * s.tpr + 32),
+                          kStreamFixed + weight_copy(a) + ring, st, a, s);
+}
+
+// The direct form: up to nv slots a thread, a row's threads one CTA or, for
+// short rows, a part of one of 256 threads.
+struct Direct {
+    int nv, tpr, threads;
+};
+
+Direct direct_shape(int slots, bool vec)
+{
+    Direct d;
+    d.nv = vec || slots <= 4096 ? 4 : 16;
+    // few slots: one each, so that a short row is spread over a warp
+    if (vec && slots <= 1024) d.nv = 1;
+    d.tpr = threads_per_row(slots, d.nv);
+    d.threads = d.tpr > 32 ? d.tpr : 256;
+    return d;
+}
+
 template <typename T>
-cudaError_t forward(const NormArgs &a, int sm_count, cudaStream_t s)
+cudaError_t forward(const NormArgs &a, int sm_count, const WaitLimit &limit, cudaStream_t s)
 {
     constexpr int EPV = 16 / sizeof(T);
     const void *ptrs[] = {a.x, a.y};
     const int64_t strides[] = {a.x_stride, a.y_stride};
     const bool vec = vectors_ok(a.cols, EPV, ptrs, 2, strides);
-    const Shape sh = norm_shape(vec ? a.cols / EPV : a.cols);
-    const int64_t per = sh.threads / sh.tpr;
+    if (vec) {
+        int nv;
+        Stream st = stream_shape(a.rows, a.cols, sizeof(T), 1, 0, sm_count, &nv);
+        st.limit = limit;
+        if (st.stages) return nv == 2 ? forward_stream<T, 2>(a, st, sm_count, s) : forward_stream<T, 4>(a, st, sm_count, s);
+    }
+    const Direct d = direct_shape(vec ? a.cols / EPV : a.cols, vec);
+    const int64_t per = d.threads / d.tpr;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>((a.rows + per - 1) / per, 8 * sm_count)));
-    if (vec) return tc::launch_pdl(norm_forward_kernel<T, EPV, 4>, grid, dim3(sh.threads), 0, s, a, sh.tpr);
-    if (sh.nv == 4) return tc::launch_pdl(norm_forward_kernel<T, 1, 4>, grid, dim3(sh.threads), 0, s, a, sh.tpr);
-    return tc::launch_pdl(norm_forward_kernel<T, 1, 16>, grid, dim3(sh.threads), 0, s, a, sh.tpr);
+    if (vec && d.nv == 1) return tc::launch_pdl(norm_direct_kernel<T, EPV, 1>, grid, dim3(d.threads), 0, s, a, d.tpr);
+    if (vec) return tc::launch_pdl(norm_direct_kernel<T, EPV, 4>, grid, dim3(d.threads), 0, s, a, d.tpr);
+    if (d.nv == 4) return tc::launch_pdl(norm_direct_kernel<T, 1, 4>, grid, dim3(d.threads), 0, s, a, d.tpr);
+    return tc::launch_pdl(norm_direct_kernel<T, 1, 16>, grid, dim3(d.threads), 0, s, a, d.tpr);
 }
 
 template <typename T>
-cudaError_t backward(const NormGradArgs &a, int sm_count, cudaStream_t s)
+cudaError_t backward(const NormGradArgs &a, int sm_count, const WaitLimit &limit, cudaStream_t s, int *blocks)
 {
     constexpr int EPV = 16 / sizeof(T);
     const void *ptrs[] = {a.x, a.dy, a.dx};
     const int64_t strides[] = {a.x_stride, a.dy_stride, a.dx_stride};
     const bool vec = vectors_ok(a.cols, EPV, ptrs, 3, strides);
-    const Shape sh = norm_shape(vec ? a.cols / EPV : a.cols);
-    const dim3 grid(static_cast<unsigned>(layer_norm_blocks(a.rows, a.cols, sm_count)));
-    const size_t smem = a.weight && sh.threads > sh.tpr ? 8u * static_cast<size_t>(a.cols) : 0;
-    if (vec) return tc::launch_pdl(norm_backward_kernel<T, EPV, 4>, grid, dim3(sh.threads), smem, s, a, sh.tpr);
-    if (sh.nv == 4) return tc::launch_pdl(norm_backward_kernel<T, 1, 4>, grid, dim3(sh.threads), smem, s, a, sh.tpr);
-    return tc::launch_pdl(norm_backward_kernel<T, 1, 16>, grid, dim3(sh.threads), smem, s, a, sh.tpr);
+    if (vec) {
+        int nv;
+        Stream st = stream_shape(a.rows, a.cols, sizeof(T), 2, weight_copy(a), sm_count, &nv);
+        st.limit = limit;
+        if (st.stages) {
+            *blocks = sm_count;
+            return nv == 2 ? backward_stream<T, 2>(a, st, sm_count, s) : backward_stream<T, 4>(a, st, sm_count, s);
+        }
+    }
+    const Direct d = direct_shape(vec ? a.cols / EPV : a.cols, vec);
+    const int64_t per = d.threads / d.tpr;
+    *blocks = static_cast<int>(std::min<int64_t>((a.rows + per - 1) / per, layer_norm_blocks(a.rows, a.cols, sm_count)));
+    const dim3 grid(static_cast<unsigned>(*blocks));
+    // (several groups only for rows of up to 32 threads: 16 KB at most)
+    const size_t smem = columns_bytes(a, d.tpr, d.threads);
+    if (vec && d.nv == 1) return tc::launch_pdl(norm_grad_direct_kernel<T, EPV, 1>, grid, dim3(d.threads), smem, s, a, d.tpr);
+    if (vec) return tc::launch_pdl(norm_grad_direct_kernel<T, EPV, 4>, grid, dim3(d.threads), smem, s, a, d.tpr);
+    if (d.nv == 4) return tc::launch_pdl(norm_grad_direct_kernel<T, 1, 4>, grid, dim3(d.threads), smem, s, a, d.tpr);
+    return tc::launch_pdl(norm_grad_direct_kernel<T, 1, 16>, grid, dim3(d.threads), smem, s, a, d.tpr);
 }
 
 }  // namespace
 
 int layer_norm_blocks(int64_t rows, int, int sm_count)
 {
-    return static_cast<int>(std::min<int64_t>(rows, 2 * sm_count));
+    return static_cast<int>(std::min<int64_t>(rows, 4 * sm_count));
 }
 
-cudaError_t launch_layer_norm(const NormArgs &a, int sm_count, cudaStream_t s)
+cudaError_t launch_layer_norm(const NormArgs &a, int sm_count, const WaitLimit &limit, cudaStream_t s)
 {
-    if (a.format == GN_FORMAT_BF16) return forward<__nv_bfloat16>(a, sm_count, s);
-    if (a.format == GN_FORMAT_FP16) return forward<__half>(a, sm_count, s);
-    return forward<float>(a, sm_count, s);
+    if (a.format == GN_FORMAT_BF16) return forward<__nv_bfloat16>(a, sm_count, limit, s);
+    if (a.format == GN_FORMAT_FP16) return forward<__half>(a, sm_count, limit, s);
+    return forward<float>(a, sm_count, limit, s);
 }
 
-cudaError_t launch_layer_norm_backward(const NormGradArgs &a, int sm_count, cudaStream_t s, int *launches)
+cudaError_t launch_layer_norm_backward(const NormGradArgs &a, int sm_count, const WaitLimit &limit, cudaStream_t s,
+                                       int *launches)
 {
     cudaError_t e;
+    int blocks = 0;
     if (a.format == GN_FORMAT_BF16)
-        e = backward<__nv_bfloat16>(a, sm_count, s);
+        e = backward<__nv_bfloat16>(a, sm_count, limit, s, &blocks);
     else if (a.format == GN_FORMAT_FP16)
-        e = backward<__half>(a, sm_count, s);
+        e = backward<__half>(a, sm_count, limit, s, &blocks);
     else
-        e = backward<float>(a, sm_count, s);
+        e = backward<float>(a, sm_count, limit, s, &blocks);
     if (e != cudaSuccess) return e;
     *launches = 1;
     if (!a.weight) return e;
-    e = tc::launch_pdl(norm_columns_kernel, dim3((2 * a.cols + 31) / 32), dim3(256), 0, s, a,
-                       layer_norm_blocks(a.rows, a.cols, sm_count));
+    e = tc::launch_pdl(norm_columns_kernel, dim3((2 * a.cols + 31) / 32), dim3(256), 0, s, a, blocks);
     if (e == cudaSuccess) *launches = 2;
     return e;
 }

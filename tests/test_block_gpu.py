@@ -72,6 +72,23 @@ def test_layer_norm(rows, cols, dtype, weight):
         assert dw is None and db is None
 
 
+@pytest.mark.parametrize("rows,cols,wide,dtype", [
+    (40001, 128, 128, FP), (130000, 32, 32, F32), (2000, 6144, 6144, BF), (1301, 8192, 8192, BF), (700, 12288, 12288, BF),
+    (1999, 1000, 1024, BF), (5003, 520, 520, FP), (9000, 264, 272, F32), (64000, 64, 72, BF)])
+def test_layer_norm_many_rows(rows, cols, wide, dtype):
+    """Enough rows for the streamed kernels, rows end to end and out of a wider tensor."""
+    x = rand((rows, wide), dtype, 1, 2.0, 1.0)[:, :cols]
+    dy = rand((rows, wide), dtype, 2)[:, :cols]
+    for w, b in ((rand((cols,), F32, 3, 0.3, 1.0), rand((cols,), F32, 4)), (None, None)):
+        y, mean, rstd = gn.layer_norm(x, w, b)
+        dx, dw, db = gn.layer_norm_backward(dy, x, mean, rstd, w)
+        got = dict(y=y, mean=mean, rstd=rstd, dx=dx, dw=dw, db=db)
+        for name, (value, bound) in br.layer_norm(x, w, b, 1e-6, dy).items():
+            br.check(got[name], value, bound, name)
+        again = gn.layer_norm_backward(dy, x, mean, rstd, w)
+        assert all(p is q or torch.equal(p, q) for p, q in zip(again, (dx, dw, db)))
+
+
 @pytest.mark.parametrize("cols,start,wide", [(64, 0, 64 + 8), (64, 3, 80), (129, 1, 200), (512, 8, 1024)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_layer_norm_of_column_slices(cols, start, wide, dtype):
