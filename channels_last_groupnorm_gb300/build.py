@@ -18,7 +18,7 @@ SOURCES = ["gn_kernels.cu", "gn_cluster.cu", "gn_capi.cu", "gn_static.cu", "rga_
            "norm_kernels.cu", "rope_kernels.cu", "pattn_kernels.cu", "pattn_forward.cu", "pattn_backward.cu",
            "block_capi.cu"]
 HEADERS = ["gn_internal.h", "gn_math.cuh", "gn_ptx.cuh", "tc_ptx.cuh", "tc_common.cuh", "tc_internal.h", "capi_util.h",
-           "block_internal.h", "pattn_common.cuh", "pattn_tiles.cuh"]
+           "block_internal.h", "block_math.cuh", "pattn_common.cuh", "pattn_tiles.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -31,6 +31,7 @@
 #include <cstdint>
 
 #include "block_internal.h"
+#include "block_math.cuh"
 #include "gn_ptx.cuh"
 #include "tc_common.cuh"
 
@@ -46,10 +47,11 @@ template <> __device__ __forceinline__ float from_float<float>(float v) { return
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 
-template <typename T, int N>
-struct alignas(sizeof(T) * N) Pack {
-    T v[N];
-};
+// A word of two half-precision values (fp32 rows have no use for it).
+template <typename T> __device__ __forceinline__ float2 unpack_word(uint32_t v) { return Half2<T>::unpack(v); }
+template <> __device__ __forceinline__ float2 unpack_word<float>(uint32_t) { return make_float2(0.f, 0.f); }
+template <typename T> __device__ __forceinline__ uint32_t pack_word(float a, float b) { return Half2<T>::pack(a, b); }
+template <> __device__ __forceinline__ uint32_t pack_word<float>(float, float) { return 0u; }
 
 template <typename T, int N>
 __device__ __forceinline__ void load_as(const T *p, float (&f)[N])
@@ -134,36 +136,50 @@ __device__ __forceinline__ void row_sum(float (&v)[N], Group &gr)
         for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
 }
 
-// A thread's slots of a row: slot k at element (lane + k tpr) EPV; zeros past
-// the end.  They stay in the row's own type: half the registers for half the
-// cost of converting them twice.
+// A thread's elements of a row, NV slots of EPV: slot k begins at element (lane +
+// k tpr) EPV; zeros past the end.  They stay in the row's own type (half the
+// registers, converted twice) and are handed out two at a time.
 template <typename T, int EPV, int NV>
 struct Row {
-    Pack<T, EPV> p[NV];
+    static constexpr int kPairs = NV * EPV / 2;
+    static constexpr int kWords = EPV == 1 ? 1 : 4;
+    uint32_t raw[NV][kWords];
 
     __device__ __forceinline__ Row(const T *row, const Group &gr, int cols)
     {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = (gr.lane + k * gr.tpr) * EPV;
-            if (c < cols) {
-                p[k] = *reinterpret_cast<const Pack<T, EPV> *>(row + c);
+            if (EPV == 1) {
+                raw[k][0] = __float_as_uint(c < cols ? to_float(row[c]) : 0.f);
             } else {
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) p[k].v[e] = from_float<T>(0.f);
+                const uint4 v = c < cols ? *reinterpret_cast<const uint4 *>(row + c) : make_uint4(0u, 0u, 0u, 0u);
+                raw[k][0] = v.x;
+                raw[k][1 % kWords] = v.y;
+                raw[k][2 % kWords] = v.z;
+                raw[k][3 % kWords] = v.w;
             }
         }
     }
-    __device__ __forceinline__ float at(int k, int e) const { return to_float(p[k].v[e]); }
+    // elements 2 j and 2 j + 1
+    __device__ __forceinline__ uint64_t pair(int j) const
+    {
+        if (EPV == 1) return pack2(__uint_as_float(raw[2 * j][0]), __uint_as_float(raw[2 * j + 1][0]));
+        if (sizeof(T) == 4)
+            return pack2(__uint_as_float(raw[j / 2][(j % 2) * 2 % kWords]), __uint_as_float(raw[j / 2][((j % 2) * 2 + 1) % kWords]));
+        const float2 v = unpack_word<T>(raw[j / 4 % NV][j % 4 % kWords]);
+        return pack2(v.x, v.y);
+    }
 };
 
-// The thread's part of the weight (ones without) or the bias (zeros): held in
-// registers, or (kHeld false: where those are full) asked for at every row.
+// The thread's part of the weight (ones without) or the bias (zeros), in pairs:
+// held in registers, or asked for at every row (where the registers are full).
 template <int EPV, int NV, bool kHeld = (NV * EPV <= 16)>
 struct Own {
     const void *p;
     int format, cols;
-    float fill, v[kHeld ? NV : 1][EPV];
+    float fill;
+    uint64_t v[kHeld ? NV * EPV / 2 : 1];
 
     __device__ __forceinline__ void fetch(const Group &gr, int k, float (&f)[EPV]) const
     {
@@ -175,47 +191,100 @@ struct Own {
             for (int e = 0; e < EPV; ++e) f[e] = fill;
         }
     }
+    // the pairs of slot k (EPV > 1) or of slots k and k + 1
+    __device__ __forceinline__ void fetch_pairs(const Group &gr, int k, uint64_t (&f)[EPV == 1 ? 1 : EPV / 2]) const
+    {
+        float one[EPV], two[EPV];
+        fetch(gr, k, one);
+        if (EPV == 1) {
+            fetch(gr, k + 1, two);
+            f[0] = pack2(one[0], two[0]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < EPV / 2; ++e) f[e % (EPV == 1 ? 1 : EPV / 2)] = pack2(one[2 * e % EPV], one[(2 * e + 1) % EPV]);
+        }
+    }
     __device__ __forceinline__ Own(const void *ptr, int fmt, const Group &gr, int n, float other)
         : p(ptr), format(fmt), cols(n), fill(other)
     {
-        if (kHeld)
+        if (!kHeld) return;
+        constexpr int kStep = EPV == 1 ? 2 : 1, kEach = EPV == 1 ? 1 : EPV / 2;
 #pragma unroll
-            for (int k = 0; k < (kHeld ? NV : 1); ++k) fetch(gr, k, v[k]);
+        for (int k = 0; k < NV; k += kStep) {
+            uint64_t f[kEach];
+            fetch_pairs(gr, k, f);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) v[kHeld ? k / kStep * kEach + e : 0] = f[e];
+        }
     }
-    __device__ __forceinline__ void get(const Group &gr, int k, float (&f)[EPV]) const
+    // the pairs of group k of slots (one slot, or two of one element)
+    __device__ __forceinline__ void get(const Group &gr, int k, uint64_t (&f)[EPV == 1 ? 1 : EPV / 2]) const
     {
+        constexpr int kEach = EPV == 1 ? 1 : EPV / 2;
         if (kHeld) {
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) f[e] = v[kHeld ? k : 0][e];
+            for (int e = 0; e < kEach; ++e) f[e] = v[kHeld ? k * kEach + e : 0];
         } else {
-            fetch(gr, k, f);
+            fetch_pairs(gr, EPV == 1 ? 2 * k : k, f);
         }
     }
 };
+
+// Writes the pairs of group k of slots, rounded once.
+template <typename T, int EPV>
+__device__ __forceinline__ void store_pairs(T *row, const Group &gr, int k, int cols, const uint64_t (&f)[EPV == 1 ? 1 : EPV / 2])
+{
+    if (EPV == 1) {
+        const float2 v = unpack2(f[0]);
+        const int c = gr.lane + 2 * k * gr.tpr;
+        if (c < cols) row[c] = from_float<T>(v.x);
+        if (c + gr.tpr < cols) row[c + gr.tpr] = from_float<T>(v.y);
+        return;
+    }
+    const int c = (gr.lane + k * gr.tpr) * EPV;
+    if (c >= cols) return;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (sizeof(T) == 4) {
+            const float2 v = unpack2(f[e / 2 % (EPV == 1 ? 1 : EPV / 2)]);
+            w[e] = __float_as_uint(e % 2 ? v.y : v.x);
+        } else {
+            const float2 v = unpack2(f[e % (EPV == 1 ? 1 : EPV / 2)]);
+            w[e] = pack_word<T>(v.x, v.y);
+        }
+    }
+    *reinterpret_cast<uint4 *>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 // One row from registers: statistics out, y out.
 template <typename T, int EPV, int NV, typename Params>
 __device__ __forceinline__ void norm_row(const NormArgs &a, const Row<T, EPV, NV> &x, const Params &w, const Params &b,
                                          Group &gr, int64_t row, bool live)
 {
+    constexpr int kEach = EPV == 1 ? 1 : EPV / 2, kGroups = Row<T, EPV, NV>::kPairs / kEach;
     const float inv = 1.0f / static_cast<float>(a.cols);
-    float s[1] = {0.f};
+    uint64_t s2 = 0;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) s[0] += x.at(k, e);
+    for (int j = 0; j < Row<T, EPV, NV>::kPairs; ++j) s2 = add2(s2, x.pair(j));
+    float s[1] = {unpack2(s2).x + unpack2(s2).y};
     row_sum(s, gr);
     const float mean = s[0] * inv;
-    float q[1] = {0.f};
+    const uint64_t minus = pack2(-mean, -mean);
+    uint64_t q2 = 0;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        if ((gr.lane + k * gr.tpr) * EPV >= a.cols) break;
+    for (int k = 0; k < kGroups; ++k) {
+        // what lies past the row's end adds nothing
+        const int c = EPV == 1 ? gr.lane + 2 * k * gr.tpr : (gr.lane + k * gr.tpr) * EPV;
+        if (c >= a.cols) break;
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-            const float d = x.at(k, e) - mean;
-            q[0] = fmaf(d, d, q[0]);
+        for (int e = 0; e < kEach; ++e) {
+            uint64_t d = add2(x.pair(k * kEach + e), minus);
+            if (EPV == 1 && c + gr.tpr >= a.cols) d = pack2(unpack2(d).x, 0.f);
+            q2 = fma2(d, d, q2);
         }
     }
+    float q[1] = {unpack2(q2).x + unpack2(q2).y};
     row_sum(q, gr);
     const float rstd = rsqrtf(fmaf(q[0], inv, a.eps));   // (two steps of fp32 at most)
     if (!live) return;
@@ -224,62 +293,61 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Row<T, EPV, NV
         if (a.rstd) a.rstd[row] = rstd;
     }
     T *y = static_cast<T *>(a.y) + row * a.y_stride;
+    const uint64_t r2 = pack2(rstd, rstd);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (gr.lane + k * gr.tpr) * EPV;
-        if (c >= a.cols) break;
-        Pack<T, EPV> p;
-        float wk[EPV], bk[EPV];
-        w.get(gr, k, wk);
+    for (int k = 0; k < kGroups; ++k) {
+        uint64_t f[kEach], bk[kEach];
+        w.get(gr, k, f);
         b.get(gr, k, bk);
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) p.v[e] = from_float<T>(fmaf((x.at(k, e) - mean) * rstd, wk[e], bk[e]));
-        *reinterpret_cast<Pack<T, EPV> *>(y + c) = p;
+        for (int e = 0; e < kEach; ++e) f[e] = fma2(mul2(add2(x.pair(k * kEach + e), minus), r2), f[e], bk[e]);
+        store_pairs<T, EPV>(y, gr, k, a.cols, f);
     }
 }
 
-// One row of the backward pass from registers: dx out, column sums on.
+// One row of the backward pass from registers: dx out, column sums on.  (Past
+// the row's end dy is zero and adds nothing; so is all of it for a row that is
+// not there.)
 template <typename T, int EPV, int NV, typename Params>
 __device__ __forceinline__ void norm_grad_row(const NormGradArgs &a, const Row<T, EPV, NV> &x, const Row<T, EPV, NV> &dy,
-                                              const Params &w, float (&sw)[NV][EPV], float (&sb)[NV][EPV], float mean,
-                                              float rstd, Group &gr, int64_t row, bool live)
+                                              const Params &w, uint64_t (&sw)[NV * EPV / 2], uint64_t (&sb)[NV * EPV / 2],
+                                              float mean, float rstd, Group &gr, int64_t row, bool live)
 {
+    constexpr int kEach = EPV == 1 ? 1 : EPV / 2, kGroups = Row<T, EPV, NV>::kPairs / kEach;
     const float inv = 1.0f / static_cast<float>(a.cols);
-    const bool sums = live && a.weight;
-    float s[2] = {0.f, 0.f};
+    const uint64_t minus = pack2(-mean, -mean), r2 = pack2(rstd, rstd);
+    uint64_t s0 = 0, s1 = 0;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        if ((gr.lane + k * gr.tpr) * EPV >= a.cols) break;
-        float wk[EPV];
+    for (int k = 0; k < kGroups; ++k) {
+        uint64_t wk[kEach];
         w.get(gr, k, wk);
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-            const float h = (x.at(k, e) - mean) * rstd, d = dy.at(k, e), g = d * wk[e];
-            if (sums) {
-                sw[k][e] = fmaf(d, h, sw[k][e]);
-                sb[k][e] += d;
-            }
-            s[0] += g;
-            s[1] = fmaf(g, h, s[1]);
+        for (int e = 0; e < kEach; ++e) {
+            const int j = k * kEach + e;
+            const uint64_t h = mul2(add2(x.pair(j), minus), r2), d = dy.pair(j), g = mul2(d, wk[e]);
+            sw[j] = fma2(d, h, sw[j]);
+            sb[j] = add2(sb[j], d);
+            s0 = add2(s0, g);
+            s1 = fma2(g, h, s1);
         }
     }
+    float s[2] = {unpack2(s0).x + unpack2(s0).y, unpack2(s1).x + unpack2(s1).y};
     row_sum(s, gr);
     if (!live) return;
     T *dx = static_cast<T *>(a.dx) + row * a.dx_stride;
-    const float m0 = s[0] * inv, m1 = s[1] * inv;
+    const float m0 = -s[0] * inv, m1 = -s[1] * inv;
+    const uint64_t m02 = pack2(m0, m0), m12 = pack2(m1, m1);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (gr.lane + k * gr.tpr) * EPV;
-        if (c >= a.cols) break;
-        Pack<T, EPV> p;
-        float wk[EPV];
-        w.get(gr, k, wk);
+    for (int k = 0; k < kGroups; ++k) {
+        uint64_t f[kEach];
+        w.get(gr, k, f);
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-            const float h = (x.at(k, e) - mean) * rstd;
-            p.v[e] = from_float<T>(rstd * (fmaf(dy.at(k, e), wk[e], -m0) - h * m1));
+        for (int e = 0; e < kEach; ++e) {
+            const int j = k * kEach + e;
+            const uint64_t h = mul2(add2(x.pair(j), minus), r2);
+            f[e] = mul2(r2, fma2(h, m12, fma2(dy.pair(j), f[e], m02)));
         }
-        *reinterpret_cast<Pack<T, EPV> *>(dx + c) = p;
+        store_pairs<T, EPV>(dx, gr, k, a.cols, f);
     }
 }
 
@@ -288,32 +356,34 @@ __device__ __forceinline__ void norm_grad_row(const NormGradArgs &a, const Row<T
 // `columns` ([groups or warps][2 cols]) and all threads add them up, column by
 // column, in a fixed order.  One group of several warps needs neither.
 template <int EPV, int NV>
-__device__ __forceinline__ void write_partial(const NormGradArgs &a, float (&sw)[NV][EPV], float (&sb)[NV][EPV],
-                                              const Group &gr, int workers, float *columns)
+__device__ __forceinline__ void write_partial(const NormGradArgs &a, uint64_t (&sw)[NV * EPV / 2],
+                                              uint64_t (&sb)[NV * EPV / 2], const Group &gr, int workers, float *columns)
 {
     float *out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
     const int parts = gr.tpr < 32 ? workers / 32 : workers / gr.tpr;
-    const bool worker = static_cast<int>(threadIdx.x) < workers;
-    if (worker) {
+    if (static_cast<int>(threadIdx.x) < workers) {
         for (int o = gr.tpr; o < 32; o <<= 1)
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) {
-                    sw[k][e] += __shfl_xor_sync(0xffffffffu, sw[k][e], o);
-                    sb[k][e] += __shfl_xor_sync(0xffffffffu, sb[k][e], o);
-                }
+            for (int j = 0; j < NV * EPV / 2; ++j) {
+                sw[j] = add2(sw[j], __shfl_xor_sync(0xffffffffu, sw[j], o));
+                sb[j] = add2(sb[j], __shfl_xor_sync(0xffffffffu, sb[j], o));
+            }
         const int part = gr.tpr < 32 ? threadIdx.x >> 5 : gr.g;
         float *to = parts > 1 ? columns + static_cast<int64_t>(part) * 2 * a.cols : out;
         if (gr.tpr >= 32 || (static_cast<int>(threadIdx.x) & 31) < gr.tpr) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = (gr.lane + k * gr.tpr) * EPV;
-                if (c >= a.cols) break;
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) {
-                    to[c + e] = sw[k][e];
-                    to[a.cols + c + e] = sb[k][e];
+            for (int j = 0; j < NV * EPV / 2; ++j) {
+                const float2 v = unpack2(sw[j]), u = unpack2(sb[j]);
+                // (columns of the pair's two elements)
+                const int c0 = EPV == 1 ? gr.lane + 2 * j * gr.tpr : (gr.lane + 2 * j / EPV * gr.tpr) * EPV + 2 * j % EPV;
+                const int c1 = EPV == 1 ? c0 + gr.tpr : c0 + 1;
+                if (c0 < a.cols) {
+                    to[c0] = v.x;
+                    to[a.cols + c0] = u.x;
+                }
+                if (c1 < a.cols) {
+                    to[c1] = v.y;
+                    to[a.cols + c1] = u.y;
                 }
             }
         }
@@ -360,14 +430,14 @@ __global__ void __launch_bounds__(direct_threads<EPV, NV>()) norm_grad_direct_ke
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     const int per = blockDim.x / tpr;
     Group gr = {tpr, 0, static_cast<int>(threadIdx.x) % tpr, scratch, 0};
-    float sw[NV][EPV] = {}, sb[NV][EPV] = {};
+    uint64_t sw[NV * EPV / 2] = {}, sb[NV * EPV / 2] = {};
     const Own<EPV, NV> w(a.weight, a.weight_format, gr, a.cols, 1.f);
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * per; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * per) {
         const int64_t row = r0 + threadIdx.x / tpr;
         const bool live = row < a.rows;
         const int64_t at = live ? row : r0;
         const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + at * a.x_stride, gr, a.cols);
-        const Row<T, EPV, NV> dy(static_cast<const T *>(a.dy) + at * a.dy_stride, gr, a.cols);
+        const Row<T, EPV, NV> dy(static_cast<const T *>(a.dy) + at * a.dy_stride, gr, live ? a.cols : 0);
         norm_grad_row(a, x, dy, w, sw, sb, a.mean[at], a.rstd[at], gr, row, live);
     }
     if (!a.weight) return;
@@ -380,7 +450,7 @@ __global__ void __launch_bounds__(direct_threads<EPV, NV>()) norm_grad_direct_ke
 // ---------------------------------------------------------------------------
 constexpr uint32_t kRingBytes = 208 * 1024;   // (with a copy of the weight in the backward pass)
 constexpr int kMaxStages = 24;
-constexpr int kStreamThreads = 384;           // of the row groups; 128 registers each
+constexpr int kStreamThreads = 512;           // of the row groups; 96 registers each
 
 // The ring: `tensors` x `per` rows of row_bytes a stage; a batch is the next
 // `per` rows, one for each group of threads.
@@ -424,7 +494,7 @@ __device__ __forceinline__ void stream_rows(const Stream &s, const char *const (
 }
 
 struct StreamShared {
-    float scratch[6][2][32][2];           // per group of several warps
+    float scratch[8][2][32][2];           // per group of several warps
     uint64_t full[kMaxStages], empty[kMaxStages];
     int abort;
 };
@@ -514,7 +584,7 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
     __syncthreads();
     const bool skip = sh.abort != 0;
     Group gr = {s.tpr, static_cast<int>(threadIdx.x) / s.tpr, static_cast<int>(threadIdx.x) % s.tpr, nullptr, 0};
-    float sw[NV][EPV] = {}, sb[NV][EPV] = {};
+    uint64_t sw[NV * EPV / 2] = {}, sb[NV * EPV / 2] = {};
     if (static_cast<int>(threadIdx.x) >= workers) {
         const char *const src[2] = {static_cast<const char *>(a.x), static_cast<const char *>(a.dy)};
         const int64_t stride[2] = {a.x_stride * static_cast<int64_t>(sizeof(T)), a.dy_stride * static_cast<int64_t>(sizeof(T))};
@@ -536,8 +606,8 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
             }
             stream_wait(sh, s, st, parity);
             const uint8_t *at = ring + st * s.stage_bytes + gr.g * s.row_bytes;
-            const Row<T, EPV, NV> x(reinterpret_cast<const T *>(at), gr, a.cols);
-            const Row<T, EPV, NV> dy(reinterpret_cast<const T *>(at + s.per * s.row_bytes), gr, a.cols);
+            const Row<T, EPV, NV> x(reinterpret_cast<const T *>(at), gr, row < a.rows ? a.cols : 0);
+            const Row<T, EPV, NV> dy(reinterpret_cast<const T *>(at + s.per * s.row_bytes), gr, row < a.rows ? a.cols : 0);
             stream_release(sh, st);
             if (++st == s.stages) {
                 st = 0;
@@ -598,14 +668,16 @@ bool vectors_ok(int cols, int epv, const void *const *ptrs, int n, const int64_t
 
 // The streamed form's shape, or stages = 0 where it does not pay: it wants at
 // least three stages of ring, and at least four batches of rows for every SM.
-// A thread has two slots of a short row and four of a longer one: with one slot
-// each (24 warps on a row of 6144) the reductions' instructions took longer
-// than the row's memory does (62 us against 38 us for 4608 x 6144 forward).
+// A thread has two or three slots, whichever leaves fewer empty (two keep a row
+// of up to 64 slots within a warp, three one of up to 96): with one (24 warps
+// on a row of 6144) the reductions' instructions took longer than the row's
+// memory does (62 us against 34 us for 4608 x 6144 forward), with four the
+// backward pass spilled (143 us against 62 us).
 Stream stream_shape(int64_t rows, int cols, int size, int tensors, size_t fixed, int sm_count, int *nv)
 {
     Stream s = {};
     const int slots = cols * size / 16;
-    *nv = slots <= 64 ? 2 : 4;
+    *nv = threads_per_row(slots, 3) * 3 <= threads_per_row(slots, 2) * 2 ? 3 : 2;
     s.tpr = threads_per_row(slots, *nv);
     s.per = std::max(1, kStreamThreads / s.tpr);
     s.row_bytes = static_cast<uint32_t>(cols * size);
@@ -655,7 +727,7 @@ cudaError_t backward_stream(const NormGradArgs &a, const Stream &s, int sm_count
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_grad_stream_kernel<T, NV>), kStreamBytes, done);
     if (e != cudaSuccess) return e;
-    // (per groups of four or two slots a thread: the column sums are at most 98 KB)
+    // (with at most three slots a thread the column sums take at most 98 KB)
     const size_t ring = std::max<size_t>(s.stages * s.stage_bytes, columns_bytes(a, s.tpr, s.per * s.tpr));
     return tc::launch_pdl(norm_grad_stream_kernel<T, NV>, dim3(static_cast<unsigned>(sm_count)), dim3(s.per * s.tpr + 32),
                           kStreamFixed + weight_copy(a) + ring, st, a, s);
@@ -689,7 +761,7 @@ cudaError_t forward(const NormArgs &a, int sm_count, const WaitLimit &limit, cud
         int nv;
         Stream st = stream_shape(a.rows, a.cols, sizeof(T), 1, 0, sm_count, &nv);
         st.limit = limit;
-        if (st.stages) return nv == 2 ? forward_stream<T, 2>(a, st, sm_count, s) : forward_stream<T, 4>(a, st, sm_count, s);
+        if (st.stages) return nv == 2 ? forward_stream<T, 2>(a, st, sm_count, s) : forward_stream<T, 3>(a, st, sm_count, s);
     }
     const Direct d = direct_shape(vec ? a.cols / EPV : a.cols, vec);
     const int64_t per = d.threads / d.tpr;
@@ -713,7 +785,7 @@ cudaError_t backward(const NormGradArgs &a, int sm_count, const WaitLimit &limit
         st.limit = limit;
         if (st.stages) {
             *blocks = sm_count;
-            return nv == 2 ? backward_stream<T, 2>(a, st, sm_count, s) : backward_stream<T, 4>(a, st, sm_count, s);
+            return nv == 2 ? backward_stream<T, 2>(a, st, sm_count, s) : backward_stream<T, 3>(a, st, sm_count, s);
         }
     }
     const Direct d = direct_shape(vec ? a.cols / EPV : a.cols, vec);

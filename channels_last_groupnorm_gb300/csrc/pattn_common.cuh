@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "block_internal.h"
+#include "block_math.cuh"
 #include "gn_ptx.cuh"
 
 namespace gn {
@@ -117,30 +118,6 @@ __device__ __forceinline__ float score_log2(const gn_attn_packed_args &a, float 
     }
     return (t - slope * fabsf(static_cast<float>(pos - j))) * kLog2e;
 }
-
-template <typename T> struct Half2;
-template <> struct Half2<__nv_bfloat16> {
-    static __device__ __forceinline__ float2 unpack(uint32_t v)
-    {
-        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-    }
-    static __device__ __forceinline__ uint32_t pack(float a, float b)
-    {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-};
-template <> struct Half2<__half> {
-    static __device__ __forceinline__ float2 unpack(uint32_t v)
-    {
-        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
-    }
-    static __device__ __forceinline__ uint32_t pack(float a, float b)
-    {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-};
 
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8])
