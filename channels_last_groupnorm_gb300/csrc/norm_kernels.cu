@@ -448,9 +448,11 @@ __global__ void __launch_bounds__(direct_threads<EPV, NV>()) norm_grad_direct_ke
 // ---------------------------------------------------------------------------
 // streamed
 // ---------------------------------------------------------------------------
-constexpr uint32_t kRingBytes = 208 * 1024;   // (with a copy of the weight in the backward pass)
+// The ring holds about kRingWant, at least three stages, and at most kRingMost
+// (with a copy of the weight in the backward pass); what it leaves is L1.
+constexpr uint32_t kRingWant = 112 * 1024, kRingMost = 208 * 1024;
 constexpr int kMaxStages = 24;
-constexpr int kStreamThreads = 512;           // of the row groups; 96 registers each
+constexpr int kStreamThreads = 384;           // of the row groups; 128 registers each
 
 // The ring: `tensors` x `per` rows of row_bytes a stage; a batch is the next
 // `per` rows, one for each group of threads.
@@ -494,7 +496,7 @@ __device__ __forceinline__ void stream_rows(const Stream &s, const char *const (
 }
 
 struct StreamShared {
-    float scratch[8][2][32][2];           // per group of several warps
+    float scratch[6][2][32][2];           // per group of several warps
     uint64_t full[kMaxStages], empty[kMaxStages];
     int abort;
 };
@@ -668,22 +670,24 @@ bool vectors_ok(int cols, int epv, const void *const *ptrs, int n, const int64_t
 
 // The streamed form's shape, or stages = 0 where it does not pay: it wants at
 // least three stages of ring, and at least four batches of rows for every SM.
-// A thread has two or three slots, whichever leaves fewer empty (two keep a row
-// of up to 64 slots within a warp, three one of up to 96): with one (24 warps
-// on a row of 6144) the reductions' instructions took longer than the row's
-// memory does (62 us against 34 us for 4608 x 6144 forward), with four the
-// backward pass spilled (143 us against 62 us).
+// A thread has two slots of a row as long as that takes at most all threads;
+// the forward pass, which has no column sums to keep, four of a row longer than
+// a warp's two.  With one slot (24 warps on a row of 6144) the reductions'
+// instructions took longer than the row's memory does (62 us forward for 4608 x
+// 6144), and with four in the backward pass the sums spilled (143 us).
 Stream stream_shape(int64_t rows, int cols, int size, int tensors, size_t fixed, int sm_count, int *nv)
 {
     Stream s = {};
     const int slots = cols * size / 16;
-    *nv = threads_per_row(slots, 3) * 3 <= threads_per_row(slots, 2) * 2 ? 3 : 2;
+    *nv = slots <= (tensors == 1 ? 64 : 2 * kStreamThreads) ? 2 : 4;
     s.tpr = threads_per_row(slots, *nv);
     s.per = std::max(1, kStreamThreads / s.tpr);
     s.row_bytes = static_cast<uint32_t>(cols * size);
     s.stage_bytes = static_cast<uint32_t>(tensors * s.per) * s.row_bytes;
-    s.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kRingBytes - fixed) / s.stage_bytes));
-    if (s.tpr > kStreamThreads || s.stages < 3 || rows < static_cast<int64_t>(4) * sm_count * s.per) s.stages = 0;
+    s.stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(3, kRingWant / s.stage_bytes)));
+    if (s.tpr > kStreamThreads || s.stages * static_cast<size_t>(s.stage_bytes) + fixed > kRingMost ||
+        rows < static_cast<int64_t>(4) * sm_count * s.per)
+        s.stages = 0;
     return s;
 }
 
@@ -700,7 +704,7 @@ cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<uint64_t>
 }
 
 constexpr size_t kStreamFixed = (sizeof(StreamShared) + 127) / 128 * 128;
-constexpr size_t kStreamBytes = kStreamFixed + kRingBytes;
+constexpr size_t kStreamBytes = kStreamFixed + kRingMost;
 
 size_t weight_copy(const NormGradArgs &a) { return a.weight ? (4u * static_cast<size_t>(a.cols) + 127) / 128 * 128 : 0; }
 
@@ -727,7 +731,7 @@ cudaError_t backward_stream(const NormGradArgs &a, const Stream &s, int sm_count
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_grad_stream_kernel<T, NV>), kStreamBytes, done);
     if (e != cudaSuccess) return e;
-    // (with at most three slots a thread the column sums take at most 98 KB)
+    // (with at most four slots a thread the column sums take at most 98 KB)
     const size_t ring = std::max<size_t>(s.stages * s.stage_bytes, columns_bytes(a, s.tpr, s.per * s.tpr));
     return tc::launch_pdl(norm_grad_stream_kernel<T, NV>, dim3(static_cast<unsigned>(sm_count)), dim3(s.per * s.tpr + 32),
                           kStreamFixed + weight_copy(a) + ring, st, a, s);
@@ -761,7 +765,7 @@ cudaError_t forward(const NormArgs &a, int sm_count, const WaitLimit &limit, cud
         int nv;
         Stream st = stream_shape(a.rows, a.cols, sizeof(T), 1, 0, sm_count, &nv);
         st.limit = limit;
-        if (st.stages) return nv == 2 ? forward_stream<T, 2>(a, st, sm_count, s) : forward_stream<T, 3>(a, st, sm_count, s);
+        if (st.stages) return nv == 2 ? forward_stream<T, 2>(a, st, sm_count, s) : forward_stream<T, 4>(a, st, sm_count, s);
     }
     const Direct d = direct_shape(vec ? a.cols / EPV : a.cols, vec);
     const int64_t per = d.threads / d.tpr;
@@ -785,7 +789,7 @@ cudaError_t backward(const NormGradArgs &a, int sm_count, const WaitLimit &limit
         st.limit = limit;
         if (st.stages) {
             *blocks = sm_count;
-            return nv == 2 ? backward_stream<T, 2>(a, st, sm_count, s) : backward_stream<T, 3>(a, st, sm_count, s);
+            return nv == 2 ? backward_stream<T, 2>(a, st, sm_count, s) : backward_stream<T, 4>(a, st, sm_count, s);
         }
     }
     const Direct d = direct_shape(vec ? a.cols / EPV : a.cols, vec);
