@@ -17,42 +17,70 @@ as everywhere in torch.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 
-from .gnsilu import _finish, _grad_blocked, _stream_handle, _torch, lib
+from . import gnsilu
+from .gnsilu import _finish, _grad_blocked, _torch, lib
 
-FORMATS = {"bfloat16": 0, "float16": 1, "float32": 2}
-POSITIONS = {"int32": 0, "int64": 1, "float32": 2}
 MAX_AXES = 8
 
 
-def _kind(t, table=FORMATS):
+# A call of a small size costs more on the host than on the GPU, so what every
+# call asks is looked up once.
+@functools.cache
+def _formats():
+    torch = _torch()
+    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+@functools.cache
+def _position_formats():
+    torch = _torch()
+    return {torch.int32: 0, torch.int64: 1, torch.float32: 2}
+
+
+@functools.cache
+def _raw_stream():
+    """Device index -> the current stream's handle."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _kind(t):
     """The C format of a tensor's dtype, or None."""
-    return table.get(str(t.dtype).replace("torch.", ""))
+    return _formats().get(t.dtype)
 
 
 def _is_cuda(*ts) -> bool:
-    torch = _torch()
-    return all(isinstance(t, torch.Tensor) and t.is_cuda for t in ts)
+    Tensor = _torch().Tensor
+    for t in ts:
+        if not (isinstance(t, Tensor) and t.is_cuda):
+            return False
+    return True
 
 
-@contextlib.contextmanager
-def _on(device, stream, *inputs):
-    """Allocate and launch on `device`, and on `stream` if one is given: what
-    is allocated inside belongs to it, and the inputs are kept from being
-    reused before it is done with them."""
+def _run(device, stream, inputs, go):
+    """``go(handle)`` on `device` and, if one is given, `stream`: what it
+    allocates belongs to that stream, and the inputs are kept from being
+    reused before the stream is done with them."""
     torch = _torch()
-    with torch.cuda.device(device):
-        if stream is None or stream == torch.cuda.current_stream(device):
-            yield
-            return
-        with torch.cuda.stream(stream):
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(stream)
-            yield
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return go(_raw_stream()(device.index))
+        with torch.cuda.device(device):
+            return go(_raw_stream()(device.index))
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+        return go(stream.cuda_stream)
+
+
+def _lib():
+    return gnsilu._lib or lib()
 
 
 def _ptr(t):
@@ -70,7 +98,7 @@ def _head_strides(t):
 # layer norm
 # ---------------------------------------------------------------------------
 def gn_layer_norm_workspace_bytes(rows: int, cols: int) -> int:
-    return int(lib().gn_layer_norm_workspace_bytes(rows, cols))
+    return int(_lib().gn_layer_norm_workspace_bytes(rows, cols))
 
 
 def _rows_of(t):
@@ -107,7 +135,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stream=No
     ``weight`` and ``bias`` (bias only with a weight): contiguous [C] tensors
     of one dtype, any of the three.  x's rows need a contiguous last axis and
     one stride between rows (a column slice of a wider tensor is fine)."""
-    lib()
+    L = _lib()
     torch = _torch()
     if not _is_cuda(x) or _kind(x) is None or x.dim() < 1 or x.shape[-1] < 1 or _grad_blocked(x, weight, bias):
         return None
@@ -119,18 +147,21 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stream=No
         return None
     if out is not None and not _norm_operand(out, x):
         return None
-    with _on(x.device, stream, x, weight, bias, out):
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        rx, ry = _rows_of(x), _rows_of(out)
-        if rx is None or ry is None:
-            return None
+    rx = _rows_of(x)
+    ry = rx if out is None and x.is_contiguous() else _rows_of(out) if out is not None else None
+    if rx is None or (out is not None and ry is None):
+        return None
+
+    def go(handle):
+        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
-        rc = lib().gn_layer_norm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(mean), _ptr(rstd), rx[0],
-                                 x.shape[-1], rx[1], ry[1], float(eps), _kind(x),
-                                 0 if weight is None else _kind(weight), _stream_handle(x.device, stream))
-    return (out, mean, rstd) if _finish(rc, "gn_layer_norm") else None
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        cols = x.shape[-1]
+        rc = L.gn_layer_norm(x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                             rx[0], cols, rx[1], cols if ry is None else ry[1], eps, _kind(x),
+                             0 if weight is None else _kind(weight), handle)
+        return (y, mean, rstd) if rc == 0 or _finish(rc, "gn_layer_norm") else None
+    return _run(x.device, stream, (x, weight, bias, out), go)
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
@@ -139,7 +170,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
     and its weight; dweight and dbias have the weight's dtype and are None
     without one.  dx is ``out`` if given (it may be dy or x).  None when not
     supported."""
-    lib()
+    L = _lib()
     torch = _torch()
     if not _is_cuda(x, dy, mean, rstd) or _kind(x) is None or x.dim() < 1 or x.shape[-1] < 1:
         return None
@@ -152,28 +183,37 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
         return None
     if out is not None and not _norm_operand(out, x):
         return None
-    with _on(x.device, stream, dy, x, mean, rstd, weight, out):
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        rg, rx, ro = _rows_of(dy), _rows_of(x), _rows_of(out)
-        if rg is None or rx is None or ro is None:
-            return None
+    cols = x.shape[-1]
+    rg, rx, ro = _rows_of(dy), _rows_of(x), (None, cols) if out is None else _rows_of(out)
+    if rg is None or rx is None or ro is None:
+        return None
+
+    def go(handle):
+        dx = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dw = db = workspace = None
+        need = 0
         if weight is not None:
             dw, db = torch.empty_like(weight), torch.empty_like(weight)
-            workspace = torch.empty(max(1, gn_layer_norm_workspace_bytes(rx[0], x.shape[-1])), dtype=torch.uint8,
-                                    device=x.device)
-        rc = lib().gn_layer_norm_backward(_ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(out), _ptr(dw),
-                                          _ptr(db), rx[0], x.shape[-1], rg[1], rx[1], ro[1], _kind(x),
-                                          0 if weight is None else _kind(weight), _ptr(workspace),
-                                          0 if workspace is None else workspace.numel(),
-                                          _stream_handle(x.device, stream))
-    return (out, dw, db) if _finish(rc, "gn_layer_norm_backward") else None
+            need = max(1, L.gn_layer_norm_workspace_bytes(rx[0], cols))
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        rc = L.gn_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
+                                      dx.data_ptr(), _ptr(dw), _ptr(db), rx[0], cols, rg[1], rx[1], ro[1], _kind(x),
+                                      0 if weight is None else _kind(weight), _ptr(workspace), need, handle)
+        return (dx, dw, db) if rc == 0 or _finish(rc, "gn_layer_norm_backward") else None
+    return _run(x.device, stream, (dy, x, mean, rstd, weight, out), go)
 
 
 # ---------------------------------------------------------------------------
 # rotary positions over several axes
 # ---------------------------------------------------------------------------
+_Strides = ctypes.c_int64 * 8
+
+
+@functools.lru_cache(maxsize=64)
+def _axes_array(*axes_dim):
+    return (ctypes.c_int64 * len(axes_dim))(*axes_dim)
+
+
 def rope_nd(q, k, positions, axes_dim, theta: float = 10000.0, interleaved: bool = True, inverse: bool = False,
             out=None, stream=None):
     """Rotary positions over several axes (time, height, width, ...) of the
@@ -189,7 +229,7 @@ def rope_nd(q, k, positions, axes_dim, theta: float = 10000.0, interleaved: bool
     turned channels.  ``inverse`` turns back: applied to the outputs'
     gradients it gives the inputs'.  ``out``: a pair of tensors for the
     results, which may be q and k themselves."""
-    lib()
+    L = _lib()
     torch = _torch()
     ts = [q] if k is None else [q, k]
     if not _is_cuda(*ts, positions) or _grad_blocked(*ts) or _kind(q) is None:
@@ -198,33 +238,32 @@ def rope_nd(q, k, positions, axes_dim, theta: float = 10000.0, interleaved: bool
     if not 1 <= len(axes_dim) <= MAX_AXES:
         return None
     if positions.dim() != 2 or positions.shape[1] != len(axes_dim) or not positions.is_contiguous() \
-            or _kind(positions, POSITIONS) is None or positions.device != q.device:
+            or _position_formats().get(positions.dtype) is None or positions.device != q.device:
         return None
     for t in ts:
         if t.dim() != 3 or t.dtype != q.dtype or t.device != q.device or t.shape[0] != positions.shape[0] \
                 or t.shape[2] != q.shape[2] or (t.shape[2] > 1 and t.stride(2) != 1) or t.shape[1] < 1:
             return None
-    outs = list(out) if out is not None else []
     if out is not None:
-        if len(outs) != 2 or (k is None) != (outs[1] is None):
+        if len(out) != 2 or (k is None) != (out[1] is None):
             return None
-        for t, o in zip(ts, outs):
+        for t, o in zip(ts, out):
             if not (_is_cuda(o) and o.shape == t.shape and o.dtype == t.dtype and o.device == t.device
                     and (o.shape[2] <= 1 or o.stride(2) == 1)):
                 return None
-    with _on(q.device, stream, *ts, positions, *outs):
-        if out is None:
-            outs = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in ts] + [None]
-        strides = (ctypes.c_int64 * 8)()
+
+    def go(handle):
+        outs = out if out is not None else [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in ts]
+        strides = [0] * 8
         for n, t in enumerate(ts):
-            strides[2 * n], strides[2 * n + 1] = _head_strides(t)
-            strides[4 + 2 * n], strides[5 + 2 * n] = _head_strides(outs[n])
-        dims = (ctypes.c_int64 * len(axes_dim))(*axes_dim)
-        rc = lib().gn_rope_nd(_ptr(q), _ptr(k), _ptr(outs[0]), _ptr(outs[1]), strides, q.shape[0], q.shape[1],
-                              0 if k is None else k.shape[1], q.shape[2], _ptr(positions),
-                              _kind(positions, POSITIONS), len(axes_dim), dims, float(theta), int(bool(interleaved)),
-                              int(bool(inverse)), _kind(q), _stream_handle(q.device, stream))
-    return (outs[0], outs[1]) if _finish(rc, "gn_rope_nd") else None
+            strides[2 * n:2 * n + 2] = _head_strides(t)
+            strides[4 + 2 * n:6 + 2 * n] = _head_strides(outs[n])
+        rc = L.gn_rope_nd(q.data_ptr(), _ptr(k), outs[0].data_ptr(), None if k is None else outs[1].data_ptr(),
+                          _Strides(*strides), q.shape[0], q.shape[1], 0 if k is None else k.shape[1], q.shape[2],
+                          positions.data_ptr(), _position_formats()[positions.dtype], len(axes_dim), _axes_array(*axes_dim),
+                          theta, bool(interleaved), bool(inverse), _kind(q), handle)
+        return (outs[0], None if k is None else outs[1]) if rc == 0 or _finish(rc, "gn_rope_nd") else None
+    return _run(q.device, stream, (*ts, positions, *(out or ())), go)
 
 
 # ---------------------------------------------------------------------------
@@ -241,7 +280,7 @@ class PackedAttnArgs(ctypes.Structure):
 
 
 def gn_attn_packed_workspace_bytes(tokens_q: int, heads: int) -> int:
-    return int(lib().gn_attn_packed_workspace_bytes(tokens_q, heads))
+    return int(_lib().gn_attn_packed_workspace_bytes(tokens_q, heads))
 
 
 def _heads_ok(t, like=None) -> bool:
@@ -306,7 +345,7 @@ def attention_packed(q, k, v, cu_q=None, cu_k=None, causal: bool = False, prefix
     cap).  ``slopes`` (fp32 [H]): slopes[h] times the distance of the two
     positions is taken off.  ``scale``: 1 / sqrt(D) if None.  A query that sees
     no key has out 0 and lse -inf."""
-    lib()
+    L = _lib()
     torch = _torch()
     a = _packed_args(q, k, v, cu_q, cu_k, causal, prefix, slopes, cap, scale)
     if a is None:
@@ -314,13 +353,14 @@ def attention_packed(q, k, v, cu_q=None, cu_k=None, causal: bool = False, prefix
     if out is not None and not (_is_cuda(out) and out.shape == q.shape and out.dtype == q.dtype
                                 and out.device == q.device and out.is_contiguous()):
         return None
-    with _on(q.device, stream, q, k, v, cu_q, cu_k, prefix, slopes, out):
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+
+    def go(handle):
+        o = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
         lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-        a.out, a.lse = _ptr(out), _ptr(lse)
-        rc = lib().gn_attn_packed(ctypes.byref(a), _stream_handle(q.device, stream))
-    return (out, lse) if _finish(rc, "gn_attn_packed") else None
+        a.out, a.lse = o.data_ptr(), lse.data_ptr()
+        rc = L.gn_attn_packed(ctypes.byref(a), handle)
+        return (o, lse) if rc == 0 or _finish(rc, "gn_attn_packed") else None
+    return _run(q.device, stream, (q, k, v, cu_q, cu_k, prefix, slopes, out), go)
 
 
 def attention_packed_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, causal: bool = False, prefix=None,
@@ -331,7 +371,7 @@ def attention_packed_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, cau
     remaining arguments as for the forward call.  dk and dv are summed over
     the query heads that share a key / value head.  The slopes have no
     gradient.  None when not supported."""
-    lib()
+    L = _lib()
     torch = _torch()
     a = _packed_args(q, k, v, cu_q, cu_k, causal, prefix, slopes, cap, scale)
     if a is None or not _heads_ok(dout, q) or dout.shape != q.shape or _grad_blocked(dout, out, lse):
@@ -341,11 +381,12 @@ def attention_packed_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, cau
             and lse.is_contiguous() and lse.device == q.device):
         return None
     a.out, a.lse = _ptr(out), _ptr(lse)
-    with _on(q.device, stream, dout, q, k, v, out, lse, cu_q, cu_k, prefix, slopes):
+
+    def go(handle):
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-        workspace = torch.empty(max(1, gn_attn_packed_workspace_bytes(q.shape[0], q.shape[1])), dtype=torch.uint8,
-                                device=q.device)
-        rc = lib().gn_attn_packed_backward(ctypes.byref(a), _ptr(dout), *_head_strides(dout), _ptr(dq),
-                                           _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
-                                           _stream_handle(q.device, stream))
-    return (dq, dk, dv) if _finish(rc, "gn_attn_packed_backward") else None
+        need = max(1, L.gn_attn_packed_workspace_bytes(q.shape[0], q.shape[1]))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        rc = L.gn_attn_packed_backward(ctypes.byref(a), dout.data_ptr(), *_head_strides(dout), dq.data_ptr(),
+                                       dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), need, handle)
+        return (dq, dk, dv) if rc == 0 or _finish(rc, "gn_attn_packed_backward") else None
+    return _run(q.device, stream, (dout, q, k, v, out, lse, cu_q, cu_k, prefix, slopes), go)
