@@ -22,108 +22,109 @@ import functools
 import math
 
 from . import gnsilu
-from .gnsilu import _finish, _grad_blocked, _torch, lib
+from .gnsilu import _finish, lib
 
 MAX_AXES = 8
 
 
 # A call of a small size costs more on the host than on the GPU, so what every
-# call asks is looked up once.
-@functools.cache
-def _formats():
-    torch = _torch()
-    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+# call asks is looked up once, and a tensor's shape and strides are asked for
+# once each.
+class _Torch:
+    """torch, its tensor type and what the entry points need of it, from the
+    first call on."""
+    ready = False
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.torch, cls.Tensor, cls.empty = torch, torch.Tensor, torch.empty
+        cls.formats = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        cls.positions = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
+        cls.float32, cls.int32, cls.uint8 = torch.float32, torch.int32, torch.uint8
+        cls.recording = staticmethod(torch.is_grad_enabled)
+        cls.current = staticmethod(torch.cuda.current_device)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        cls.handle = staticmethod(raw or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+        cls.ready = True
 
 
-@functools.cache
-def _position_formats():
-    torch = _torch()
-    return {torch.int32: 0, torch.int64: 1, torch.float32: 2}
+def _start():
+    """(The library, torch's parts)."""
+    if not _Torch.ready:
+        _Torch.load()
+    return gnsilu._lib or lib(), _Torch
 
 
-@functools.cache
-def _raw_stream():
-    """Device index -> the current stream's handle."""
-    torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _kind(t):
-    """The C format of a tensor's dtype, or None."""
-    return _formats().get(t.dtype)
-
-
-def _is_cuda(*ts) -> bool:
-    Tensor = _torch().Tensor
-    for t in ts:
-        if not (isinstance(t, Tensor) and t.is_cuda):
-            return False
-    return True
+def _wants_grad(*ts) -> bool:
+    if _Torch.recording():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 def _run(device, stream, inputs, go):
     """``go(handle)`` on `device` and, if one is given, `stream`: what it
     allocates belongs to that stream, and the inputs are kept from being
     reused before the stream is done with them."""
-    torch = _torch()
+    T = _Torch
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return go(_raw_stream()(device.index))
-        with torch.cuda.device(device):
-            return go(_raw_stream()(device.index))
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+        index = device.index
+        if index == T.current():
+            return go(T.handle(index))
+        with T.torch.cuda.device(device):
+            return go(T.handle(index))
+    with T.torch.cuda.device(device), T.torch.cuda.stream(stream):
         for t in inputs:
             if t is not None:
                 t.record_stream(stream)
         return go(stream.cuda_stream)
 
 
-def _lib():
-    return gnsilu._lib or lib()
-
-
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _head_strides(t):
+def _head_strides(shape, strides):
     """Token and head stride; of an axis of length one the packed ones (torch
     leaves it any stride there)."""
-    return (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2],
-            t.stride(1) if t.shape[1] > 1 else t.shape[2])
+    return (strides[0] if shape[0] > 1 else shape[1] * shape[2], strides[1] if shape[1] > 1 else shape[2])
 
 
 # ---------------------------------------------------------------------------
 # layer norm
 # ---------------------------------------------------------------------------
 def gn_layer_norm_workspace_bytes(rows: int, cols: int) -> int:
-    return int(_lib().gn_layer_norm_workspace_bytes(rows, cols))
+    return int(_start()[0].gn_layer_norm_workspace_bytes(rows, cols))
 
 
-def _rows_of(t):
-    """(rows, row stride) of a tensor seen as rows of its contiguous last
-    axis with one stride between them, or None if it is not that."""
-    cols = t.shape[-1]
-    if t.stride(-1) != 1 and cols > 1:
+def _row_stride(shape, strides):
+    """The stride between the rows of a tensor's contiguous last axis, or None
+    if the rows do not have one between them."""
+    cols = shape[-1]
+    if strides[-1] != 1 and cols > 1:
         return None
-    rows = t.numel() // cols
-    if rows <= 1:
-        return rows, cols
-    dims = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
+    if len(shape) == 2:
+        return cols if shape[0] <= 1 else strides[0] if strides[0] >= cols else None
+    dims = [(n, s) for n, s in zip(shape[:-1], strides) if n != 1]
+    if not dims or 0 in shape:
+        return cols
     for (_, outer), (n, inner) in zip(dims, dims[1:]):
         if outer != n * inner:
             return None
-    return (rows, dims[-1][1]) if dims[-1][1] >= cols else None
+    return dims[-1][1] if dims[-1][1] >= cols else None
 
 
-def _norm_operand(t, like) -> bool:
-    return _is_cuda(t) and t.shape == like.shape and t.dtype == like.dtype and t.device == like.device
+def _like(t, x, T) -> bool:
+    return isinstance(t, T.Tensor) and t.shape == x.shape and t.dtype == x.dtype and t.device == x.device
 
 
-def _param_ok(t, x, dtype=None) -> bool:
-    return (_is_cuda(t) and t.device == x.device and t.dim() == 1 and t.numel() == x.shape[-1] and t.is_contiguous()
-            and _kind(t) is not None and (dtype is None or t.dtype == dtype))
+def _param_format(t, cols, device, T):
+    """The format of a weight or bias vector, or None."""
+    if not (isinstance(t, T.Tensor) and t.device == device and t.dim() == 1 and t.numel() == cols and t.is_contiguous()):
+        return None
+    return T.formats.get(t.dtype)
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stream=None):
@@ -135,33 +136,33 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stream=No
     ``weight`` and ``bias`` (bias only with a weight): contiguous [C] tensors
     of one dtype, any of the three.  x's rows need a contiguous last axis and
     one stride between rows (a column slice of a wider tensor is fine)."""
-    L = _lib()
-    torch = _torch()
-    if not _is_cuda(x) or _kind(x) is None or x.dim() < 1 or x.shape[-1] < 1 or _grad_blocked(x, weight, bias):
+    L, T = _start()
+    if not (isinstance(x, T.Tensor) and x.is_cuda):
         return None
-    if bias is not None and weight is None:
+    shape, device, kind = x.shape, x.device, T.formats.get(x.dtype)
+    if kind is None or not shape or shape[-1] < 1 or _wants_grad(x, weight, bias):
         return None
-    if weight is not None and not _param_ok(weight, x):
+    cols, wkind = shape[-1], 0
+    if weight is not None:
+        wkind = _param_format(weight, cols, device, T)
+        if wkind is None or (bias is not None and _param_format(bias, cols, device, T) != wkind):
+            return None
+    elif bias is not None:
         return None
-    if bias is not None and not _param_ok(bias, x, weight.dtype):
-        return None
-    if out is not None and not _norm_operand(out, x):
-        return None
-    rx = _rows_of(x)
-    ry = rx if out is None and x.is_contiguous() else _rows_of(out) if out is not None else None
-    if rx is None or (out is not None and ry is None):
+    sx, sy = _row_stride(shape, x.stride()), cols
+    if out is not None:
+        sy = _row_stride(shape, out.stride()) if _like(out, x, T) else None
+    if sx is None or sy is None:
         return None
 
     def go(handle):
-        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        cols = x.shape[-1]
+        y = T.empty(shape, dtype=x.dtype, device=device) if out is None else out
+        mean = T.empty(shape[:-1], dtype=T.float32, device=device)
+        rstd = T.empty(shape[:-1], dtype=T.float32, device=device)
         rc = L.gn_layer_norm(x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                             rx[0], cols, rx[1], cols if ry is None else ry[1], eps, _kind(x),
-                             0 if weight is None else _kind(weight), handle)
+                             mean.numel(), cols, sx, sy, eps, kind, wkind, handle)
         return (y, mean, rstd) if rc == 0 or _finish(rc, "gn_layer_norm") else None
-    return _run(x.device, stream, (x, weight, bias, out), go)
+    return _run(device, stream, (x, weight, bias, out), go)
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
@@ -170,37 +171,41 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
     and its weight; dweight and dbias have the weight's dtype and are None
     without one.  dx is ``out`` if given (it may be dy or x).  None when not
     supported."""
-    L = _lib()
-    torch = _torch()
-    if not _is_cuda(x, dy, mean, rstd) or _kind(x) is None or x.dim() < 1 or x.shape[-1] < 1:
+    L, T = _start()
+    if not (isinstance(x, T.Tensor) and x.is_cuda):
         return None
-    if not _norm_operand(dy, x) or _grad_blocked(dy, x, weight):
+    shape, device, kind = x.shape, x.device, T.formats.get(x.dtype)
+    if kind is None or not shape or shape[-1] < 1 or not _like(dy, x, T) or _wants_grad(dy, x, weight):
         return None
     for s in (mean, rstd):
-        if s.dtype != torch.float32 or s.shape != x.shape[:-1] or not s.is_contiguous() or s.device != x.device:
+        if not (isinstance(s, T.Tensor) and s.dtype == T.float32 and s.shape == shape[:-1] and s.is_contiguous()
+                and s.device == device):
             return None
-    if weight is not None and not _param_ok(weight, x):
-        return None
-    if out is not None and not _norm_operand(out, x):
-        return None
-    cols = x.shape[-1]
-    rg, rx, ro = _rows_of(dy), _rows_of(x), (None, cols) if out is None else _rows_of(out)
-    if rg is None or rx is None or ro is None:
+    cols, wkind = shape[-1], 0
+    if weight is not None:
+        wkind = _param_format(weight, cols, device, T)
+        if wkind is None:
+            return None
+    sg, sx, so = _row_stride(shape, dy.stride()), _row_stride(shape, x.stride()), cols
+    if out is not None:
+        so = _row_stride(shape, out.stride()) if _like(out, x, T) else None
+    if sg is None or sx is None or so is None:
         return None
 
     def go(handle):
-        dx = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = T.empty(shape, dtype=x.dtype, device=device) if out is None else out
+        rows = mean.numel()
         dw = db = workspace = None
         need = 0
         if weight is not None:
-            dw, db = torch.empty_like(weight), torch.empty_like(weight)
-            need = max(1, L.gn_layer_norm_workspace_bytes(rx[0], cols))
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            dw, db = T.torch.empty_like(weight), T.torch.empty_like(weight)
+            need = max(1, L.gn_layer_norm_workspace_bytes(rows, cols))
+            workspace = T.empty(need, dtype=T.uint8, device=device)
         rc = L.gn_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
-                                      dx.data_ptr(), _ptr(dw), _ptr(db), rx[0], cols, rg[1], rx[1], ro[1], _kind(x),
-                                      0 if weight is None else _kind(weight), _ptr(workspace), need, handle)
+                                      dx.data_ptr(), _ptr(dw), _ptr(db), rows, cols, sg, sx, so, kind, wkind,
+                                      _ptr(workspace), need, handle)
         return (dx, dw, db) if rc == 0 or _finish(rc, "gn_layer_norm_backward") else None
-    return _run(x.device, stream, (dy, x, mean, rstd, weight, out), go)
+    return _run(device, stream, (dy, x, mean, rstd, weight, out), go)
 
 
 # ---------------------------------------------------------------------------
@@ -210,8 +215,14 @@ _Strides = ctypes.c_int64 * 8
 
 
 @functools.lru_cache(maxsize=64)
-def _axes_array(*axes_dim):
+def _axes_array(axes_dim):
     return (ctypes.c_int64 * len(axes_dim))(*axes_dim)
+
+
+def _heads_like(t, dtype, device, T) -> bool:
+    """[tokens, heads, channels] with contiguous channels."""
+    return (isinstance(t, T.Tensor) and t.dtype == dtype and t.device == device and t.dim() == 3 and t.shape[1] >= 1
+            and (t.stride(2) == 1 or t.shape[2] <= 1))
 
 
 def rope_nd(q, k, positions, axes_dim, theta: float = 10000.0, interleaved: bool = True, inverse: bool = False,
@@ -229,41 +240,46 @@ def rope_nd(q, k, positions, axes_dim, theta: float = 10000.0, interleaved: bool
     turned channels.  ``inverse`` turns back: applied to the outputs'
     gradients it gives the inputs'.  ``out``: a pair of tensors for the
     results, which may be q and k themselves."""
-    L = _lib()
-    torch = _torch()
-    ts = [q] if k is None else [q, k]
-    if not _is_cuda(*ts, positions) or _grad_blocked(*ts) or _kind(q) is None:
+    L, T = _start()
+    if not (isinstance(q, T.Tensor) and q.is_cuda and isinstance(positions, T.Tensor)):
         return None
-    axes_dim = [int(n) for n in axes_dim]
-    if not 1 <= len(axes_dim) <= MAX_AXES:
+    dtype, device = q.dtype, q.device
+    kind, place, axes_dim = T.formats.get(dtype), T.positions.get(positions.dtype), tuple(axes_dim)
+    ts = (q,) if k is None else (q, k)
+    if kind is None or place is None or _wants_grad(*ts) or not 1 <= len(axes_dim) <= MAX_AXES:
         return None
-    if positions.dim() != 2 or positions.shape[1] != len(axes_dim) or not positions.is_contiguous() \
-            or _position_formats().get(positions.dtype) is None or positions.device != q.device:
+    if positions.shape != (q.shape[0], len(axes_dim)) or positions.device != device or not positions.is_contiguous():
         return None
+    shapes, strides = [], []
     for t in ts:
-        if t.dim() != 3 or t.dtype != q.dtype or t.device != q.device or t.shape[0] != positions.shape[0] \
-                or t.shape[2] != q.shape[2] or (t.shape[2] > 1 and t.stride(2) != 1) or t.shape[1] < 1:
+        if not _heads_like(t, dtype, device, T):
             return None
+        shapes.append(t.shape)
+        strides.append(_head_strides(shapes[-1], t.stride()))
+    if k is not None and (shapes[1][0] != shapes[0][0] or shapes[1][2] != shapes[0][2]):
+        return None
     if out is not None:
         if len(out) != 2 or (k is None) != (out[1] is None):
             return None
-        for t, o in zip(ts, out):
-            if not (_is_cuda(o) and o.shape == t.shape and o.dtype == t.dtype and o.device == t.device
-                    and (o.shape[2] <= 1 or o.stride(2) == 1)):
+        for shape, o in zip(shapes, out):
+            if not _heads_like(o, dtype, device, T) or o.shape != shape:
                 return None
 
     def go(handle):
-        outs = out if out is not None else [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in ts]
-        strides = [0] * 8
-        for n, t in enumerate(ts):
-            strides[2 * n:2 * n + 2] = _head_strides(t)
-            strides[4 + 2 * n:6 + 2 * n] = _head_strides(outs[n])
-        rc = L.gn_rope_nd(q.data_ptr(), _ptr(k), outs[0].data_ptr(), None if k is None else outs[1].data_ptr(),
-                          _Strides(*strides), q.shape[0], q.shape[1], 0 if k is None else k.shape[1], q.shape[2],
-                          positions.data_ptr(), _position_formats()[positions.dtype], len(axes_dim), _axes_array(*axes_dim),
-                          theta, bool(interleaved), bool(inverse), _kind(q), handle)
+        outs = [T.empty(s, dtype=dtype, device=device) for s in shapes] if out is None else out
+        to = [(s[1] * s[2], s[2]) if out is None else _head_strides(s, o.stride()) for s, o in zip(shapes, outs)]
+        tokens, heads, dim = shapes[0]
+        if k is None:
+            rc = L.gn_rope_nd(q.data_ptr(), None, outs[0].data_ptr(), None, _Strides(*strides[0], 0, 0, *to[0], 0, 0),
+                              tokens, heads, 0, dim, positions.data_ptr(), place, len(axes_dim), _axes_array(axes_dim),
+                              theta, bool(interleaved), bool(inverse), kind, handle)
+        else:
+            rc = L.gn_rope_nd(q.data_ptr(), k.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(),
+                              _Strides(*strides[0], *strides[1], *to[0], *to[1]), tokens, heads, shapes[1][1], dim,
+                              positions.data_ptr(), place, len(axes_dim), _axes_array(axes_dim), theta,
+                              bool(interleaved), bool(inverse), kind, handle)
         return (outs[0], None if k is None else outs[1]) if rc == 0 or _finish(rc, "gn_rope_nd") else None
-    return _run(q.device, stream, (*ts, positions, *(out or ())), go)
+    return _run(device, stream, (*ts, positions, *(out or ())), go)
 
 
 # ---------------------------------------------------------------------------
@@ -280,51 +296,50 @@ class PackedAttnArgs(ctypes.Structure):
 
 
 def gn_attn_packed_workspace_bytes(tokens_q: int, heads: int) -> int:
-    return int(_lib().gn_attn_packed_workspace_bytes(tokens_q, heads))
+    return int(_start()[0].gn_attn_packed_workspace_bytes(tokens_q, heads))
 
 
-def _heads_ok(t, like=None) -> bool:
-    return (_is_cuda(t) and t.dim() == 3 and _kind(t) in (0, 1) and (t.shape[2] <= 1 or t.stride(2) == 1)
-            and (like is None or (t.dtype == like.dtype and t.device == like.device and t.shape[2] == like.shape[2])))
+def _ends_like(t, docs, device, T) -> bool:
+    return (isinstance(t, T.Tensor) and t.dtype == T.int32 and t.device == device and t.dim() == 1
+            and t.numel() == docs and t.is_contiguous())
 
 
-def _packed_args(q, k, v, cu_q, cu_k, causal, prefix, slopes, cap, scale):
+def _packed_args(q, k, v, cu_q, cu_k, causal, prefix, slopes, cap, scale, T):
     """The C arguments without the outputs, or None if not supported."""
-    torch = _torch()
-    if not (_heads_ok(q) and _heads_ok(k, q) and _heads_ok(v, q)) or k.shape != v.shape or _grad_blocked(q, k, v):
+    if not (isinstance(q, T.Tensor) and q.is_cuda):
         return None
-    if q.shape[1] < 1 or k.shape[1] < 1 or q.shape[1] % k.shape[1]:
+    dtype, device = q.dtype, q.device
+    kind = T.formats.get(dtype)
+    if kind not in (0, 1) or _wants_grad(q, k, v, slopes):
+        return None
+    for t in (q, k, v):
+        if not _heads_like(t, dtype, device, T):
+            return None
+    shape, kv_shape = q.shape, k.shape
+    tokens, heads, dim = shape
+    if v.shape != kv_shape or kv_shape[2] != dim or heads % kv_shape[1]:
         return None
     docs = 1
-    if (cu_q is None) != (cu_k is None):
-        return None
-    if cu_q is not None:
-        for t in (cu_q, cu_k):
-            if not (_is_cuda(t) and t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous()
-                    and t.device == q.device and t.numel() == cu_q.numel() and t.numel() >= 2):
-                return None
+    if cu_q is None:
+        if cu_k is not None:
+            return None
+    else:
+        if not isinstance(cu_q, T.Tensor):
+            return None
         docs = cu_q.numel() - 1
-    if prefix is not None and not (causal and _is_cuda(prefix) and prefix.dtype == torch.int32
-                                   and prefix.shape == (docs,) and prefix.is_contiguous()
-                                   and prefix.device == q.device):
+        if docs < 1 or not _ends_like(cu_q, docs + 1, device, T) or not _ends_like(cu_k, docs + 1, device, T):
+            return None
+    if prefix is not None and not (causal and _ends_like(prefix, docs, device, T)):
         return None
-    if slopes is not None and not (_is_cuda(slopes) and slopes.dtype == torch.float32
-                                   and slopes.shape == (q.shape[1],) and slopes.is_contiguous()
-                                   and slopes.device == q.device) or _grad_blocked(slopes):
+    if slopes is not None and not (isinstance(slopes, T.Tensor) and slopes.dtype == T.float32 and slopes.device == device
+                                   and slopes.shape == (heads,) and slopes.is_contiguous()):
         return None
-    a = PackedAttnArgs()
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        setattr(a, name, _ptr(t))
-        token, head = _head_strides(t)
-        setattr(a, name + "_token", token)
-        setattr(a, name + "_head", head)
-    a.tokens_q, a.tokens_k = q.shape[0], k.shape[0]
-    a.cu_q, a.cu_k, a.prefix, a.slopes = _ptr(cu_q), _ptr(cu_k), _ptr(prefix), _ptr(slopes)
-    a.scale = 1.0 / math.sqrt(max(1, q.shape[2])) if scale is None else float(scale)
-    a.cap = float(cap or 0.0)
-    a.heads, a.kv_heads, a.dim, a.docs = q.shape[1], k.shape[1], q.shape[2], docs
-    a.causal, a.format = int(bool(causal)), _kind(q)
-    return a
+    # (in the order of the structure; the outputs come later)
+    return PackedAttnArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), None, None, *_head_strides(shape, q.stride()),
+                          *_head_strides(kv_shape, k.stride()), *_head_strides(kv_shape, v.stride()), tokens, kv_shape[0],
+                          _ptr(cu_q), _ptr(cu_k), _ptr(prefix), _ptr(slopes),
+                          1.0 / math.sqrt(max(1, dim)) if scale is None else scale, cap or 0.0, heads, kv_shape[1], dim,
+                          docs, bool(causal), kind)
 
 
 def attention_packed(q, k, v, cu_q=None, cu_k=None, causal: bool = False, prefix=None, slopes=None, cap: float = 0.0,
@@ -345,22 +360,19 @@ def attention_packed(q, k, v, cu_q=None, cu_k=None, causal: bool = False, prefix
     cap).  ``slopes`` (fp32 [H]): slopes[h] times the distance of the two
     positions is taken off.  ``scale``: 1 / sqrt(D) if None.  A query that sees
     no key has out 0 and lse -inf."""
-    L = _lib()
-    torch = _torch()
-    a = _packed_args(q, k, v, cu_q, cu_k, causal, prefix, slopes, cap, scale)
-    if a is None:
+    L, T = _start()
+    a = _packed_args(q, k, v, cu_q, cu_k, causal, prefix, slopes, cap, scale, T)
+    if a is None or (out is not None and not (_like(out, q, T) and out.is_contiguous())):
         return None
-    if out is not None and not (_is_cuda(out) and out.shape == q.shape and out.dtype == q.dtype
-                                and out.device == q.device and out.is_contiguous()):
-        return None
+    shape, device = q.shape, q.device
 
     def go(handle):
-        o = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        o = T.empty(shape, dtype=q.dtype, device=device) if out is None else out
+        lse = T.empty((shape[1], shape[0]), dtype=T.float32, device=device)
         a.out, a.lse = o.data_ptr(), lse.data_ptr()
         rc = L.gn_attn_packed(ctypes.byref(a), handle)
         return (o, lse) if rc == 0 or _finish(rc, "gn_attn_packed") else None
-    return _run(q.device, stream, (q, k, v, cu_q, cu_k, prefix, slopes, out), go)
+    return _run(device, stream, (q, k, v, cu_q, cu_k, prefix, slopes, out), go)
 
 
 def attention_packed_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, causal: bool = False, prefix=None,
@@ -371,22 +383,21 @@ def attention_packed_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, cau
     remaining arguments as for the forward call.  dk and dv are summed over
     the query heads that share a key / value head.  The slopes have no
     gradient.  None when not supported."""
-    L = _lib()
-    torch = _torch()
-    a = _packed_args(q, k, v, cu_q, cu_k, causal, prefix, slopes, cap, scale)
-    if a is None or not _heads_ok(dout, q) or dout.shape != q.shape or _grad_blocked(dout, out, lse):
+    L, T = _start()
+    a = _packed_args(q, k, v, cu_q, cu_k, causal, prefix, slopes, cap, scale, T)
+    if a is None or not _like(dout, q, T) or not _heads_like(dout, q.dtype, q.device, T) or _wants_grad(dout, out, lse):
         return None
-    if not (_is_cuda(out, lse) and out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
-            and out.device == q.device and lse.shape == (q.shape[1], q.shape[0]) and lse.dtype == torch.float32
-            and lse.is_contiguous() and lse.device == q.device):
+    shape, device = q.shape, q.device
+    if not (_like(out, q, T) and out.is_contiguous() and isinstance(lse, T.Tensor) and lse.device == device
+            and lse.shape == (shape[1], shape[0]) and lse.dtype == T.float32 and lse.is_contiguous()):
         return None
-    a.out, a.lse = _ptr(out), _ptr(lse)
+    a.out, a.lse = out.data_ptr(), lse.data_ptr()
 
     def go(handle):
-        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-        need = max(1, L.gn_attn_packed_workspace_bytes(q.shape[0], q.shape[1]))
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        rc = L.gn_attn_packed_backward(ctypes.byref(a), dout.data_ptr(), *_head_strides(dout), dq.data_ptr(),
-                                       dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), need, handle)
+        dq, dk, dv = (T.empty(t.shape, dtype=t.dtype, device=device) for t in (q, k, v))
+        need = max(1, L.gn_attn_packed_workspace_bytes(shape[0], shape[1]))
+        workspace = T.empty(need, dtype=T.uint8, device=device)
+        rc = L.gn_attn_packed_backward(ctypes.byref(a), dout.data_ptr(), *_head_strides(shape, dout.stride()),
+                                       dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), need, handle)
         return (dq, dk, dv) if rc == 0 or _finish(rc, "gn_attn_packed_backward") else None
-    return _run(q.device, stream, (dout, q, k, v, out, lse, cu_q, cu_k, prefix, slopes), go)
+    return _run(device, stream, (dout, q, k, v, out, lse, cu_q, cu_k, prefix, slopes), go)

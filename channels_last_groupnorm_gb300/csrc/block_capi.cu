@@ -257,11 +257,12 @@ int gn_rope_nd(const void *q, const void *k, void *q_out, void *k_out, const int
     a.interleaved = interleaved != 0;
     a.inverse = inverse != 0;
     a.format = format;
+    const double log_theta = std::log(theta);
     int p = 0;
     for (int n = 0; n < a.axes; ++n)
         for (int i = 0; i < axes_dim[n] / 2; ++i, ++p) {
             a.axis[p] = static_cast<unsigned char>(n);
-            a.turns[p] = std::pow(theta, -2.0 * i / static_cast<double>(axes_dim[n])) / 6.283185307179586476925;
+            a.turns[p] = std::exp(-log_theta * (2.0 * i / static_cast<double>(axes_dim[n]))) / 6.283185307179586476925;
         }
     const cudaError_t e = gn::launch_rope(a, d.sm_count, static_cast<cudaStream_t>(stream));
     return launched(e, e == cudaSuccess);
