@@ -31,7 +31,7 @@ namespace {
 
 using namespace pattn;
 
-constexpr int kThreads = 352;    // warps: 0 loads, 1 MMA, 2-9 softmax, 10 the MMA's waits
+constexpr int kThreads = 384;    // warps: 0 loads, 1 MMA, 2 the MMA's waits, 4-11 softmax
 // Tiles in flight: of the ones that two products far apart in a step read (Q for
 // dK and dV, K for dQ), and of the ones that are done with sooner (dO, V).
 // With two of each, released together, the loads were waited for (dQ: 2300 of
@@ -136,27 +136,30 @@ __device__ __noinline__ void row_dkv(const PackedAttn &p, const Info &info, int 
     store4<T>(p.dv, (static_cast<int64_t>(j) * a.kv_heads + hk) * a.dim, lane, a.dim, dv);
 }
 
-// Scores s[n] (raw, in place) to exponents in units of log2 before their lse,
-// capped and biased; far(n): distance of the pair.  slack[n]: the cap's slope.
-template <int N, typename Far>
-__device__ __forceinline__ void bend(float (&s)[N], float (&slack)[N], const TileArgs &args, float slope2, Far far)
+// Scores of N pairs (raw, in place) to what times the returned factor is in
+// units of log2 before lse, capped and biased; far(n): the pair's distance.
+// slack[n], with a cap: its slope there.
+template <bool GENERAL, int N, typename Far>
+__device__ __forceinline__ float bend(float (&s)[N], float (&slack)[N], const TileArgs &args, float slope2, Far far)
 {
+    if (!GENERAL) return args.scale_log2;
     const gn_attn_packed_args &a = args.p.a;
+    float by = args.scale_log2;
     if (a.cap > 0.f) {
         tanh_all(s, a.scale / a.cap);
+        by = a.cap * kLog2e;
 #pragma unroll
-        for (int n = 0; n < N; ++n) slack[n] = fmaf(-s[n], s[n], 1.0f);
-    } else {
-#pragma unroll
-        for (int n = 0; n < N; ++n) slack[n] = 1.0f;
+        for (int n = 0; n < N; n += 2) {
+            const uint64_t v = pack2(s[n], s[n + 1]);
+            const float2 r = unpack2(fma2(mul2(v, pack2(-1.0f, -1.0f)), v, pack2(1.0f, 1.0f)));
+            slack[n] = r.x;
+            slack[n + 1] = r.y;
+        }
     }
-    const float by = a.cap > 0.f ? a.cap * kLog2e : args.scale_log2;
+    if (!a.slopes) return by;
 #pragma unroll
-    for (int n = 0; n < N; ++n) s[n] *= by;
-    if (a.slopes) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) s[n] = fmaf(-slope2, fabsf(far(n)), s[n]);
-    }
+    for (int n = 0; n < N; ++n) s[n] = fmaf(-slope2, fabsf(far(n)), s[n] * by);
+    return 1.0f;
 }
 
 // Barriers and words of either kernel.  Own: the tiles a CTA owns; Long /
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the queries that see any of the tile's keys, and those that see all
     const int row = (warp & 3) * 32 + lane, key = key0 + row;
     Span span = {0, 0, 0};
-    if (warp >= 2 && warp < 10) {
+    if (warp >= 4) {
         if (key < a.tokens_k) span = key_span(a, key);
         const bool live = key < a.tokens_k, some = live && span.lo < span.hi;
         const int lo = __reduce_min_sync(0xffffffffu, some ? span.lo : 0x7fffffff);
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int all_lo = __reduce_max_sync(0xffffffffu, !live ? 0 : (some ? span.lo : 0x7fffffff));
         const int all_hi = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : (some ? span.hi : 0));
         if (lane == 0) {
-            volatile int *w = range + ((warp - 2) * 4);
+            volatile int *w = range + ((warp - 4) * 4);
             w[0] = lo;
             w[1] = hi;
             w[2] = all_lo;
@@ -330,94 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t k_tile = base + lay.own, v_tile = k_tile + tile_bytes;
     const uint32_t t_s = tmem, t_dp = tmem + 128, t_dk = tmem + 256, t_dv = tmem + 384;
 
-    if (warp == 0) {
-        if (lane == 0 && !skip && any) {
-            mbar_arrive_expect_tx(bar(kOwn), 2 * tile_bytes);
-            load_tile(k_tile, &map_k, halves, hk, key0, bar(kOwn));
-            load_tile(v_tile, &map_v, halves, hk, key0, bar(kOwn));
-            Loads got = {};
-            for (int n = 0; n < steps_all; ++n) {
-                const int h = hk * group + n / blocks, i0 = q0 + (n % blocks) * kTile;
-                if (!long_free(n - kLongStages)) break;
-                mbar_arrive_expect_tx(bar(kLong + n % kLongStages), tile_bytes);
-                load_tile(long_tile(n), &map_q, halves, h, i0, bar(kLong + n % kLongStages));
-                ++got.longs;
-                if (!short_free(n - kShortStages)) break;
-                mbar_arrive_expect_tx(bar(kShort + n % kShortStages), tile_bytes);
-                load_tile(short_tile(n), &map_do, halves, h, i0, bar(kShort + n % kShortStages));
-                ++got.shorts;
-                // the records are done with when the scores' gradients of their block are, as Q is
-                if (!long_free(n - 2)) break;
-                const int64_t at = static_cast<int64_t>(h) * info.padded + i0;
-                const uint32_t rows = base + lay.rows + (n & 1) * kTile * 8;
-                mbar_arrive_expect_tx(bar(kInfo + (n & 1)), kTile * 8);
-                bulk_load(rows, info.lse + at, kTile * 4, bar(kInfo + (n & 1)));
-                bulk_load(rows + kTile * 4, info.delta + at, kTile * 4, bar(kInfo + (n & 1)));
-                ++got.infos;
-            }
-            drain_loads(bar(0), got, args.limit.timeout_ns);
-        }
-    } else if (warp == 1 || warp == 10) {
-        if (!skip && any) {
-            const bool waits = warp == 10;
-            const int steps = (a.dim + 15) / 16;
-            const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
-            if (waits) {
-                wait_warp(bar(kOwn), 0, abort, args.limit);
-                has_long(0);
-                has_short(0);
-            }
-            hand_over();
-            if (!waits) {
-                mma_tokens(t_s, k_tile, long_tile(0), steps, is);
-                commit(bar(kS));
-                mma_tokens(t_dp, v_tile, short_tile(0), steps, is);
-                commit(bar(kDp));
-            }
-            for (int n = 0; n < steps_all; ++n) {
-                const bool more = n + 1 < steps_all;
-                if (waits) wait_warp(bar(kP), n & 1, abort, args.limit);
-                hand_over();
-                if (!waits) {
-                    tc_fence_after_sync();
-                    mma_channels(t_dv, t_s, short_tile(n), 0, io, n > 0);
-                    mma_channels(t_dv, t_s + 64, short_tile(n), 1, io, true);
-                    commit(bar(kShortFree + n % kShortStages));
-                }
-                if (more) {
-                    if (waits) has_long(n + 1);
-                    hand_over();
-                    if (!waits) {
-                        mma_tokens(t_s, k_tile, long_tile(n + 1), steps, is);
-                        commit(bar(kS));
-                    }
-                }
-                if (waits) wait_warp(bar(kDs), n & 1, abort, args.limit);
-                hand_over();
-                if (!waits) {
-                    tc_fence_after_sync();
-                    mma_channels(t_dk, t_dp, long_tile(n), 0, io, n > 0);
-                    mma_channels(t_dk, t_dp + 64, long_tile(n), 1, io, true);
-                    commit(bar(kLongFree + n % kLongStages));
-                }
-                if (more) {
-                    if (waits) has_short(n + 1);
-                    hand_over();
-                    if (!waits) {
-                        mma_tokens(t_dp, v_tile, short_tile(n + 1), steps, is);
-                        commit(bar(kDp));
-                    }
-                }
-            }
-            if (!waits) {
-                commit(bar(kOut));
-                commit(bar(kDrain));
-                tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
-            }
-        }
-    } else {
+    if (warp >= 4) {
+        many_registers();
         // ---- softmax: one key per thread, 64 of a block's queries per warp ----
-        const int half = (warp - 2) >> 2;
+        const int half = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         bool go = !skip;
         float slope2 = 0.f;
@@ -434,15 +353,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             float w[64], slack[64];              // scores, then weights; the cap's slopes
             tmem_ld_all(t_s + lanes + 64 * half, w);
-            if (GENERAL) {
-                // (queries that all see the same keys stand one after the other)
-                const int at = a.slopes ? __ldg(&spans->z) - key : 0;
-                if (masked)
-                    bend(w, slack, args, slope2, [&](int k) { return static_cast<float>(__ldg(&spans[k].z) - key); });
-                else
-                    bend(w, slack, args, slope2, [&](int k) { return static_cast<float>(at + k); });
-            }
-            const float c = GENERAL ? 1.0f : args.scale_log2;
+            // (queries that all see the same keys stand one after the other)
+            const int at = GENERAL && a.slopes ? __ldg(&spans->z) - key : 0;
+            const float c = masked ? bend<GENERAL>(w, slack, args, slope2, [&](int k) { return static_cast<float>(__ldg(&spans[k].z) - key); })
+                                   : bend<GENERAL>(w, slack, args, slope2, [&](int k) { return static_cast<float>(at + k); });
             const uint64_t c2 = pack2(c, c);
 #pragma unroll
             for (int k = 0; k < 64; k += 4) {
@@ -525,6 +439,94 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((n & 1) == half) row_dkv<T>(args.p, info, key - lane + __ffs(again) - 1, hk);
         }
         tc_fence_before_sync();
+    } else {
+        few_registers();
+        if (warp == 0) {
+            if (lane == 0 && !skip && any) {
+                mbar_arrive_expect_tx(bar(kOwn), 2 * tile_bytes);
+                load_tile(k_tile, &map_k, halves, hk, key0, bar(kOwn));
+                load_tile(v_tile, &map_v, halves, hk, key0, bar(kOwn));
+                Loads got = {};
+                for (int n = 0; n < steps_all; ++n) {
+                    const int h = hk * group + n / blocks, i0 = q0 + (n % blocks) * kTile;
+                    if (!long_free(n - kLongStages)) break;
+                    mbar_arrive_expect_tx(bar(kLong + n % kLongStages), tile_bytes);
+                    load_tile(long_tile(n), &map_q, halves, h, i0, bar(kLong + n % kLongStages));
+                    ++got.longs;
+                    if (!short_free(n - kShortStages)) break;
+                    mbar_arrive_expect_tx(bar(kShort + n % kShortStages), tile_bytes);
+                    load_tile(short_tile(n), &map_do, halves, h, i0, bar(kShort + n % kShortStages));
+                    ++got.shorts;
+                    // the records are done with when the scores' gradients of their block are, as Q is
+                    if (!long_free(n - 2)) break;
+                    const int64_t at = static_cast<int64_t>(h) * info.padded + i0;
+                    const uint32_t rows = base + lay.rows + (n & 1) * kTile * 8;
+                    mbar_arrive_expect_tx(bar(kInfo + (n & 1)), kTile * 8);
+                    bulk_load(rows, info.lse + at, kTile * 4, bar(kInfo + (n & 1)));
+                    bulk_load(rows + kTile * 4, info.delta + at, kTile * 4, bar(kInfo + (n & 1)));
+                    ++got.infos;
+                }
+                drain_loads(bar(0), got, args.limit.timeout_ns);
+            }
+        } else if (warp == 1 || warp == 2) {
+            if (!skip && any) {
+                const bool waits = warp == 2;
+                const int steps = (a.dim + 15) / 16;
+                const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
+                if (waits) {
+                    wait_warp(bar(kOwn), 0, abort, args.limit);
+                    has_long(0);
+                    has_short(0);
+                }
+                hand_over();
+                if (!waits) {
+                    mma_tokens(t_s, k_tile, long_tile(0), steps, is);
+                    commit(bar(kS));
+                    mma_tokens(t_dp, v_tile, short_tile(0), steps, is);
+                    commit(bar(kDp));
+                }
+                for (int n = 0; n < steps_all; ++n) {
+                    const bool more = n + 1 < steps_all;
+                    if (waits) wait_warp(bar(kP), n & 1, abort, args.limit);
+                    hand_over();
+                    if (!waits) {
+                        tc_fence_after_sync();
+                        mma_channels(t_dv, t_s, short_tile(n), 0, io, n > 0);
+                        mma_channels(t_dv, t_s + 64, short_tile(n), 1, io, true);
+                        commit(bar(kShortFree + n % kShortStages));
+                    }
+                    if (more) {
+                        if (waits) has_long(n + 1);
+                        hand_over();
+                        if (!waits) {
+                            mma_tokens(t_s, k_tile, long_tile(n + 1), steps, is);
+                            commit(bar(kS));
+                        }
+                    }
+                    if (waits) wait_warp(bar(kDs), n & 1, abort, args.limit);
+                    hand_over();
+                    if (!waits) {
+                        tc_fence_after_sync();
+                        mma_channels(t_dk, t_dp, long_tile(n), 0, io, n > 0);
+                        mma_channels(t_dk, t_dp + 64, long_tile(n), 1, io, true);
+                        commit(bar(kLongFree + n % kLongStages));
+                    }
+                    if (more) {
+                        if (waits) has_short(n + 1);
+                        hand_over();
+                        if (!waits) {
+                            mma_tokens(t_dp, v_tile, short_tile(n + 1), steps, is);
+                            commit(bar(kDp));
+                        }
+                    }
+                }
+                if (!waits) {
+                    commit(bar(kOut));
+                    commit(bar(kDrain));
+                    tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+                }
+            }
+        }
     }
     __syncwarp();
     __syncthreads();
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane, row = row0 + r;   // (row < info.padded)
     int4 span = make_int4(0, 0, 0, 0);
     float nlse = -INFINITY, ndelta = 0.f;
-    if (warp >= 2 && warp < 10) {
+    if (warp >= 4) {
         span = info.span[row];
         nlse = info.lse[static_cast<int64_t>(h) * info.padded + row];
         ndelta = info.delta[static_cast<int64_t>(h) * info.padded + row];
@@ -599,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int all_lo = __reduce_max_sync(0xffffffffu, !live ? 0 : (some ? span.x : 0x7fffffff));
         const int all_hi = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : (some ? span.y : 0));
         if (lane == 0) {
-            volatile int *w = range + ((warp - 2) * 4);
+            volatile int *w = range + ((warp - 4) * 4);
             w[0] = lo;
             w[1] = hi;
             w[2] = all_lo;
@@ -624,78 +626,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // two buffers of scores (their gradients go over them)
     const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;
 
-    if (warp == 0) {
-        if (lane == 0 && !skip && any) {
-            mbar_arrive_expect_tx(bar(kOwn), 2 * tile_bytes);
-            load_tile(q_tile, &map_q, halves, h, row0, bar(kOwn));
-            load_tile(do_tile, &map_do, halves, h, row0, bar(kOwn));
-            Loads got = {};
-            for (int n = 0; n < blocks; ++n) {
-                if (!long_free(n - kLongStages)) break;
-                mbar_arrive_expect_tx(bar(kLong + n % kLongStages), tile_bytes);
-                load_tile(long_tile(n), &map_k, halves, hk, key0 + n * kTile, bar(kLong + n % kLongStages));
-                ++got.longs;
-                if (!short_free(n - kShortStages)) break;
-                mbar_arrive_expect_tx(bar(kShort + n % kShortStages), tile_bytes);
-                load_tile(short_tile(n), &map_v, halves, hk, key0 + n * kTile, bar(kShort + n % kShortStages));
-                ++got.shorts;
-            }
-            drain_loads(bar(0), got, args.limit.timeout_ns);
-        }
-    } else if (warp == 1 || warp == 10) {
-        if (!skip && any) {
-            const bool waits = warp == 10;
-            const int steps = (a.dim + 15) / 16;
-            const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
-            if (waits) {
-                wait_warp(bar(kOwn), 0, abort, args.limit);
-                has_long(0);
-                has_short(0);
-            }
-            hand_over();
-            if (!waits) {
-                mma_tokens(t_s, q_tile, long_tile(0), steps, is);
-                commit(bar(kS));
-                mma_tokens(t_dp, do_tile, short_tile(0), steps, is);
-                commit(bar(kDp));
-                commit(bar(kShortFree));
-            }
-            for (int n = 0; n < blocks; ++n) {
-                const bool more = n + 1 < blocks;
-                if (more) {
-                    if (waits) has_long(n + 1);
-                    hand_over();
-                    if (!waits) {
-                        mma_tokens(t_s + 128 * ((n + 1) & 1), q_tile, long_tile(n + 1), steps, is);
-                        commit(bar(kS));
-                    }
-                }
-                if (waits) {
-                    if (more) has_short(n + 1);
-                    wait_warp(bar(kDs), n & 1, abort, args.limit);
-                }
-                hand_over();
-                if (!waits) {
-                    tc_fence_after_sync();
-                    if (more) {
-                        mma_tokens(t_dp, do_tile, short_tile(n + 1), steps, is);
-                        commit(bar(kDp));
-                        commit(bar(kShortFree + (n + 1) % kShortStages));
-                    }
-                    mma_channels(t_dq, t_s + 128 * (n & 1), long_tile(n), 0, io, n > 0);
-                    mma_channels(t_dq, t_s + 128 * (n & 1) + 64, long_tile(n), 1, io, true);
-                    commit(bar(kLongFree + n % kLongStages));
-                }
-            }
-            if (!waits) {
-                commit(bar(kOut));
-                commit(bar(kDrain));
-                tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
-            }
-        }
-    } else {
+    if (warp >= 4) {
+        many_registers();
         // ---- softmax: one query per thread, 64 of a block's keys per warp ----
-        const int half = (warp - 2) >> 2;
+        const int half = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float slope2 = GENERAL && a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
         bool go = !skip;
@@ -709,11 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             float w[64], slack[64];              // scores, then weights; the cap's slopes
             tmem_ld_all(ts, w);
-            if (GENERAL) {
-                const float pos = static_cast<float>(span.z - j0 - 64 * half);
-                bend(w, slack, args, slope2, [&](int k) { return pos - static_cast<float>(k); });
-            }
-            const float c = GENERAL ? 1.0f : args.scale_log2;
+            const float pos = static_cast<float>(span.z - j0 - 64 * half);
+            const float c = bend<GENERAL>(w, slack, args, slope2, [&](int k) { return pos - static_cast<float>(k); });
             const uint64_t c2 = pack2(c, c), e2 = pack2(nlse, nlse);
 #pragma unroll
             for (int k = 0; k < 64; k += 2) {
@@ -770,6 +701,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((n & 1) == half) row_dq<T>(args.p, info, row - lane + __ffs(again) - 1, h);
         }
         tc_fence_before_sync();
+    } else {
+        few_registers();
+        if (warp == 0) {
+            if (lane == 0 && !skip && any) {
+                mbar_arrive_expect_tx(bar(kOwn), 2 * tile_bytes);
+                load_tile(q_tile, &map_q, halves, h, row0, bar(kOwn));
+                load_tile(do_tile, &map_do, halves, h, row0, bar(kOwn));
+                Loads got = {};
+                for (int n = 0; n < blocks; ++n) {
+                    if (!long_free(n - kLongStages)) break;
+                    mbar_arrive_expect_tx(bar(kLong + n % kLongStages), tile_bytes);
+                    load_tile(long_tile(n), &map_k, halves, hk, key0 + n * kTile, bar(kLong + n % kLongStages));
+                    ++got.longs;
+                    if (!short_free(n - kShortStages)) break;
+                    mbar_arrive_expect_tx(bar(kShort + n % kShortStages), tile_bytes);
+                    load_tile(short_tile(n), &map_v, halves, hk, key0 + n * kTile, bar(kShort + n % kShortStages));
+                    ++got.shorts;
+                }
+                drain_loads(bar(0), got, args.limit.timeout_ns);
+            }
+        } else if (warp == 1 || warp == 2) {
+            if (!skip && any) {
+                const bool waits = warp == 2;
+                const int steps = (a.dim + 15) / 16;
+                const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
+                if (waits) {
+                    wait_warp(bar(kOwn), 0, abort, args.limit);
+                    has_long(0);
+                    has_short(0);
+                }
+                hand_over();
+                if (!waits) {
+                    mma_tokens(t_s, q_tile, long_tile(0), steps, is);
+                    commit(bar(kS));
+                    mma_tokens(t_dp, do_tile, short_tile(0), steps, is);
+                    commit(bar(kDp));
+                    commit(bar(kShortFree));
+                }
+                for (int n = 0; n < blocks; ++n) {
+                    const bool more = n + 1 < blocks;
+                    if (more) {
+                        if (waits) has_long(n + 1);
+                        hand_over();
+                        if (!waits) {
+                            mma_tokens(t_s + 128 * ((n + 1) & 1), q_tile, long_tile(n + 1), steps, is);
+                            commit(bar(kS));
+                        }
+                    }
+                    if (waits) {
+                        if (more) has_short(n + 1);
+                        wait_warp(bar(kDs), n & 1, abort, args.limit);
+                    }
+                    hand_over();
+                    if (!waits) {
+                        tc_fence_after_sync();
+                        if (more) {
+                            mma_tokens(t_dp, do_tile, short_tile(n + 1), steps, is);
+                            commit(bar(kDp));
+                            commit(bar(kShortFree + (n + 1) % kShortStages));
+                        }
+                        mma_channels(t_dq, t_s + 128 * (n & 1), long_tile(n), 0, io, n > 0);
+                        mma_channels(t_dq, t_s + 128 * (n & 1) + 64, long_tile(n), 1, io, true);
+                        commit(bar(kLongFree + n % kLongStages));
+                    }
+                }
+                if (!waits) {
+                    commit(bar(kOut));
+                    commit(bar(kDrain));
+                    tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+                }
+            }
+        }
     }
     __syncwarp();
     __syncthreads();

@@ -26,9 +26,8 @@ namespace {
 
 using namespace pattn;
 
-constexpr int kThreads = 352;    // warps: 0 loads, 1 MMA, 2-5 and 6-9 the two tiles' softmax, 10 the MMA's waits
+constexpr int kThreads = 384;    // warps: 0 loads, 1 MMA, 2 the MMA's waits, 4-7 and 8-11 the two tiles' softmax
 constexpr int kStages = 4;       // ring of key and value tiles, in the order K0 V0 K1 V1 ...
-constexpr float kRescaleLog2 = 8.0f;
 
 // kPFull: per tile the weights of the block's first and last 64 keys
 enum Bar { kQFull = 0, kFull = 2, kEmpty = kFull + kStages, kSFull = kEmpty + kStages, kPFull = kSFull + 2,
@@ -125,8 +124,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every query's run of keys, and what the tiles make of them: the keys that
     // any query sees, and those that all see
     Span span = {0, 0, 0};
-    const int tile = warp >= 6 ? 1 : 0, row = row0 + tile * kTile + (warp & 3) * 32 + lane;
-    if (warp >= 2 && warp < 10) {
+    const int tile = warp >= 8 ? 1 : 0, row = row0 + tile * kTile + (warp & 3) * 32 + lane;
+    if (warp >= 4) {
         span = query_span_warp(a, row, lane);
         const bool live = row < a.tokens_q, some = live && span.lo < span.hi;
         const int lo = __reduce_min_sync(0xffffffffu, some ? span.lo : 0x7fffffff);
@@ -134,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int all_lo = __reduce_max_sync(0xffffffffu, !live ? 0 : (some ? span.lo : 0x7fffffff));
         const int all_hi = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : (some ? span.hi : 0));
         if (lane == 0) {
-            volatile int *w = range + ((warp - 2) * 4);
+            volatile int *w = range + ((warp - 4) * 4);
             w[0] = lo;
             w[1] = hi;
             w[2] = all_lo;
@@ -172,86 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int blocks = key0 < key1 ? (key1 - key0 + kTile - 1) / kTile : 0;
     const bool skip = *abort != 0;
 
-    if (warp == 0) {
-        if (lane == 0 && !skip) {
-            // ---- loads ----
-            for (int t = 0; t < 2; ++t)
-                if (first[t] < last[t]) {
-                    mbar_arrive_expect_tx(bar(kQFull + t), tile_bytes);
-                    load_tile(base + lay.q + t * tile_bytes, &map_q, halves, h, row0 + t * kTile, bar(kQFull + t));
-                }
-            int n = 0;
-            bool go = true;
-            for (; go && n < 2 * blocks; ++n) {
-                const int st = n % kStages;
-                if (n >= kStages && !wait(bar(kEmpty + st), (n / kStages - 1) & 1, abort, args.limit)) {
-                    go = false;
-                    break;
-                }
-                mbar_arrive_expect_tx(bar(kFull + st), tile_bytes);
-                load_tile(base + lay.ring + st * tile_bytes, (n & 1) ? &map_v : &map_k, halves, hk,
-                          key0 + (n >> 1) * kTile, bar(kFull + st));
-            }
-            // nothing is left in flight when the CTA ends, whatever became of the others
-            for (int k = max(0, n - kStages); k < n; ++k)
-                tc::drain(bar(kFull + k % kStages), (k / kStages) & 1, args.limit.timeout_ns);
-            for (int t = 0; t < 2; ++t)
-                if (first[t] < last[t]) tc::drain(bar(kQFull + t), 0, args.limit.timeout_ns);
-        }
-    } else if (warp == 1 || warp == 10) {
-        if (!skip) {
-            // ---- MMA: per block and tile the weighted values of the block
-            // before, then the scores of this one ----
-            const bool waits = warp == 10;
-            const int steps = (a.dim + 15) / 16;
-            const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
-            const auto loaded = [&](int n) { wait_warp(bar(kFull + n % kStages), (n / kStages) & 1, abort, args.limit); };
-            for (int b = 0; b <= blocks; ++b) {
-                const int nv = 2 * b - 1, nk = 2 * b;
-                const uint32_t v_tile = base + lay.ring + (nv % kStages) * tile_bytes;
-                const uint32_t k_tile = base + lay.ring + (nk % kStages) * tile_bytes;
-                // (a tile may have no part in a block: its loads are waited for all the same)
-                if (waits) {
-                    if (b > 0) loaded(nv);
-                    if (b < blocks) loaded(nk);
-                }
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const bool weigh = b - 1 >= first[t] && b - 1 < last[t], score = b >= first[t] && b < last[t];
-                    if (weigh) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            if (waits) wait_warp(bar(kPFull + 2 * t + half), (b - 1 - first[t]) & 1, abort, args.limit);
-                            hand_over();
-                            if (waits) continue;
-                            tc_fence_after_sync();
-                            mma_channels(tmem + 256 + 128 * t, tmem + 128 * t + 32 * half, v_tile, half, io,
-                                         b - 1 > first[t] || half);
-                        }
-                        if (!waits && b == last[t]) commit(bar(kOFull + t));
-                    }
-                    if (score) {
-                        if (waits && b == first[t]) wait_warp(bar(kQFull + t), 0, abort, args.limit);
-                        if (!weigh) hand_over();
-                        if (waits) continue;
-                        mma_tokens(tmem + 128 * t, base + lay.q + t * tile_bytes, k_tile, steps, is);
-                        commit(bar(kSFull + t));
-                    }
-                }
-                hand_over();
-                if (!waits) {
-                    if (b > 0) commit(bar(kEmpty + nv % kStages));
-                    if (b < blocks) commit(bar(kEmpty + nk % kStages));
-                }
-            }
-            if (!waits) {
-                commit(bar(kDrain));
-                tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
-            }
-        }
-    } else {
+    if (warp >= 4) {
+        many_registers();
         // ---- softmax: one query per thread ----
-        constexpr float kShift = IsBf16<T>::value ? 0.f : 7.f;
+        constexpr float kShift = weight_shift<T>();
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128 * tile, to = tmem + lanes + 256 + 128 * tile;
         const int b0 = tile ? first[1] : first[0], b1 = tile ? last[1] : last[0];
@@ -266,42 +189,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             float s[kTile];
             tmem_ld_all(ts, s);
-            float c = args.scale_log2;
-            if (GENERAL) {
-                c = 1.0f;
-                if (a.cap > 0.f) tanh_all(s, a.scale / a.cap);
-                const float by = a.cap > 0.f ? a.cap * kLog2e : args.scale_log2;
-                const float pos = static_cast<float>(span.pos - j0);
-#pragma unroll
-                for (int k = 0; k < kTile; ++k) s[k] = fmaf(-slope2, fabsf(pos - k), s[k] * by);
-            }
-            if (masked) {
-                const int lo = span.lo - j0;
-                const unsigned len = static_cast<unsigned>(max(0, span.hi - span.lo));
-#pragma unroll
-                for (int k = 0; k < kTile; ++k) s[k] = static_cast<unsigned>(k - lo) < len ? s[k] : -INFINITY;
-            }
-            float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int k = 4; k < kTile; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
-            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+            const float c = bend_scores<GENERAL>(s, a, args.scale_log2, slope2, span.pos - j0);
+            if (masked) mask_scores(s, span.lo - j0, static_cast<unsigned>(max(0, span.hi - span.lo)));
+            const float mx = top_score(s) * c;
             const bool grew = mx > m + (kShift + kRescaleLog2) || (b == b0 && mx > m);
             if (__any_sync(0xffffffffu, grew)) {
                 const float to_m = grew ? mx - kShift : m;
                 const float f = grew && m != -INFINITY ? ex2_approx(m - to_m) : 1.0f;
                 m = to_m;
                 l *= f;
-                if (b > b0) {
-#pragma unroll 1
-                    for (int q = 0; q < 8; ++q) {
-                        uint32_t u[16];
-                        tmem_ld16(to + 16 * q, u);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * f);
-                        tmem_st16(to + 16 * q, u);
-                    }
-                }
+                if (b > b0) rescale_columns(to, f);
             }
             // the weights, 32 keys at a time; the first 64 are handed over early
             const float m_use = m == -INFINITY ? 0.f : m;
@@ -310,13 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t pk[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float2 x = unpack2(fma2(pack2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]), c2, m2));
-                    const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-                    sum2[k & 1] = add2(sum2[k & 1], pack2(p0, p1));
-                    pk[k] = Half2<T>::pack(p0, p1);
-                }
+                weigh_32<T>(s + 32 * q, c2, m2, sum2, pk);
                 tmem_st16(ts + 16 * q, pk);
                 if (q == 1 && !masked) {
                     tmem_wait_st();
@@ -375,6 +266,86 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; again; again &= again - 1) row_forward<T>(a, args.p.group, row - lane + __ffs(again) - 1, h);
         }
         tc_fence_before_sync();
+    } else {
+        few_registers();
+        if (warp == 0) {
+            if (lane == 0 && !skip) {
+                // ---- loads ----
+                for (int t = 0; t < 2; ++t)
+                    if (first[t] < last[t]) {
+                        mbar_arrive_expect_tx(bar(kQFull + t), tile_bytes);
+                        load_tile(base + lay.q + t * tile_bytes, &map_q, halves, h, row0 + t * kTile, bar(kQFull + t));
+                    }
+                int n = 0;
+                bool go = true;
+                for (; go && n < 2 * blocks; ++n) {
+                    const int st = n % kStages;
+                    if (n >= kStages && !wait(bar(kEmpty + st), (n / kStages - 1) & 1, abort, args.limit)) {
+                        go = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(bar(kFull + st), tile_bytes);
+                    load_tile(base + lay.ring + st * tile_bytes, (n & 1) ? &map_v : &map_k, halves, hk,
+                              key0 + (n >> 1) * kTile, bar(kFull + st));
+                }
+                // nothing is left in flight when the CTA ends, whatever became of the others
+                for (int k = max(0, n - kStages); k < n; ++k)
+                    tc::drain(bar(kFull + k % kStages), (k / kStages) & 1, args.limit.timeout_ns);
+                for (int t = 0; t < 2; ++t)
+                    if (first[t] < last[t]) tc::drain(bar(kQFull + t), 0, args.limit.timeout_ns);
+            }
+        } else if (warp == 1 || warp == 2) {
+            if (!skip) {
+                // ---- MMA: per block and tile the weighted values of the block
+                // before, then the scores of this one ----
+                const bool waits = warp == 2;
+                const int steps = (a.dim + 15) / 16;
+                const uint32_t is = instruction<T>(kTile, false), io = instruction<T>(steps * 16, true);
+                const auto loaded = [&](int n) { wait_warp(bar(kFull + n % kStages), (n / kStages) & 1, abort, args.limit); };
+                for (int b = 0; b <= blocks; ++b) {
+                    const int nv = 2 * b - 1, nk = 2 * b;
+                    const uint32_t v_tile = base + lay.ring + (nv % kStages) * tile_bytes;
+                    const uint32_t k_tile = base + lay.ring + (nk % kStages) * tile_bytes;
+                    // (a tile may have no part in a block: its loads are waited for all the same)
+                    if (waits) {
+                        if (b > 0) loaded(nv);
+                        if (b < blocks) loaded(nk);
+                    }
+    #pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const bool weigh = b - 1 >= first[t] && b - 1 < last[t], score = b >= first[t] && b < last[t];
+                        if (weigh) {
+    #pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                if (waits) wait_warp(bar(kPFull + 2 * t + half), (b - 1 - first[t]) & 1, abort, args.limit);
+                                hand_over();
+                                if (waits) continue;
+                                tc_fence_after_sync();
+                                mma_channels(tmem + 256 + 128 * t, tmem + 128 * t + 32 * half, v_tile, half, io,
+                                             b - 1 > first[t] || half);
+                            }
+                            if (!waits && b == last[t]) commit(bar(kOFull + t));
+                        }
+                        if (score) {
+                            if (waits && b == first[t]) wait_warp(bar(kQFull + t), 0, abort, args.limit);
+                            if (!weigh) hand_over();
+                            if (waits) continue;
+                            mma_tokens(tmem + 128 * t, base + lay.q + t * tile_bytes, k_tile, steps, is);
+                            commit(bar(kSFull + t));
+                        }
+                    }
+                    hand_over();
+                    if (!waits) {
+                        if (b > 0) commit(bar(kEmpty + nv % kStages));
+                        if (b < blocks) commit(bar(kEmpty + nk % kStages));
+                    }
+                }
+                if (!waits) {
+                    commit(bar(kDrain));
+                    tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+                }
+            }
+        }
     }
     __syncwarp();
     __syncthreads();

@@ -59,6 +59,12 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const void *map, int hal
     for (int n = 0; n < halves; ++n) tma_load_3d(dst + n * kHalfBytes, map, n * 64, head, token, bar);
 }
 
+// Registers between a kernel's warp groups of four: the first has the loads and
+// the MMA issue, the others the softmax (384 threads are launched with 168 each:
+// 128 x 72 + 256 x 216 = 384 x 168).
+__device__ __forceinline__ void few_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+__device__ __forceinline__ void many_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
+
 // Matrix descriptor of a tile read MN-major (the 64 channels of a row are
 // contiguous along M or N, tokens along the contraction), 128-byte swizzle:
 // 16 KB from one group of 64 channels to the next (leading offset), 1 KB from 8
@@ -136,16 +142,18 @@ __device__ __forceinline__ void commit(uint32_t bar)
 // (64 cycles a step) if it built a descriptor for each: the steps only add to
 // the descriptors' address field, and are unrolled.
 
-// D = A B^T over the channels of two tiles (128 x 128, `steps` of 16 channels).
-__device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc)
+// D = A B^T over the channels of two tiles (128 x 128, `steps` of 16 channels);
+// a_half: bytes from A's first 64 channels to its others.
+__device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc,
+                                           uint32_t a_half = kHalfBytes)
 {
     const uint64_t da = sw128_kmajor_desc(a), db = sw128_kmajor_desc(b);
     if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             if (k >= steps) break;
-            const uint64_t at = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
-            umma_f16(d, da + at, db + at, idesc, k > 0);
+            umma_f16(d, da + (k >> 2) * (a_half >> 4) + (k & 3) * 2, db + (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2, idesc,
+                     k > 0);
         }
     }
     __syncwarp();
@@ -250,6 +258,98 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---- scores of one query against N neighbouring keys -----------------------------------
+// In place, to what times the returned factor is in units of log2 (capped,
+// biased, masked).  at: the query's position relative to the first key; keys lo
+// .. lo + len - 1, relative to it too, are seen.  Without GENERAL (no cap, no
+// bias, a positive scale) the raw scores only want their factor.
+//
+// The bias of a block that lies wholly on one side of the warp's queries is
+// linear in the key: two operations for two scores instead of three for one.
+template <bool GENERAL, int N>
+__device__ __forceinline__ float bend_scores(float (&s)[N], const gn_attn_packed_args &a, float scale_log2, float slope2,
+                                             int at)
+{
+    if (!GENERAL) return scale_log2;
+    float by = scale_log2;
+    if (a.cap > 0.f) {
+        tanh_all(s, a.scale / a.cap);
+        by = a.cap * kLog2e;
+    }
+    if (a.slopes) {
+        const bool left = __all_sync(0xffffffffu, at >= N - 1), right = __all_sync(0xffffffffu, at <= 0);
+        const float p = static_cast<float>(at);
+        if (left || right) {
+            const float toward = left ? slope2 : -slope2;
+            const uint64_t by2 = pack2(by, by), t2 = pack2(toward, toward), b2 = pack2(-toward * p, -toward * p);
+#pragma unroll
+            for (int k = 0; k < N; k += 2) {
+                const float2 v = unpack2(fma2(pack2(s[k], s[k + 1]), by2,
+                                              fma2(t2, pack2(static_cast<float>(k), static_cast<float>(k + 1)), b2)));
+                s[k] = v.x;
+                s[k + 1] = v.y;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) s[k] = fmaf(-slope2, fabsf(p - k), s[k] * by);
+        }
+        return 1.0f;
+    }
+    if (by > 0.f) return by;
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] *= by;
+    return 1.0f;
+}
+
+template <int N>
+__device__ __forceinline__ void mask_scores(float (&s)[N], int lo, unsigned len)
+{
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = static_cast<unsigned>(k - lo) < len ? s[k] : -INFINITY;
+}
+
+template <int N>
+__device__ __forceinline__ float top_score(const float (&s)[N])
+{
+    float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int k = 4; k < N; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
+    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+
+// Multiplies 128 accumulator columns of the thread's lane by f.
+__device__ __forceinline__ void rescale_columns(uint32_t taddr, float f)
+{
+#pragma unroll 1
+    for (int q = 0; q < 8; ++q) {
+        uint32_t u[16];
+        tmem_ld16(taddr + 16 * q, u);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * f);
+        tmem_st16(taddr + 16 * q, u);
+    }
+}
+
+// The running maximum only moves when a score is more than 2^8 above it; fp16
+// weights are kept 2^7 higher than bf16 ones, away from fp16's subnormals (the
+// largest is then 2^15, under its 65504).
+constexpr float kRescaleLog2 = 8.0f;
+template <typename T> constexpr float weight_shift() { return IsBf16<T>::value ? 0.f : 7.f; }
+
+// Weights 2^(c s - m) of 32 scores: packed for the tensor core, their sums added up.
+template <typename T>
+__device__ __forceinline__ void weigh_32(const float *s, uint64_t c2, uint64_t m2, uint64_t (&sum2)[2], uint32_t (&pk)[16])
+{
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const float2 x = unpack2(fma2(pack2(s[2 * k], s[2 * k + 1]), c2, m2));
+        const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+        sum2[k & 1] = add2(sum2[k & 1], pack2(p0, p1));
+        pk[k] = Half2<T>::pack(p0, p1);
+    }
+}
 
 // Row r of a tile holds an infinity or a NaN.
 template <typename T>
