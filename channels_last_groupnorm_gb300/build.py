@@ -15,7 +15,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libgnsilu.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["gn_kernels.cu", "gn_cluster.cu", "gn_capi.cu", "gn_static.cu", "rga_kernels.cu", "upconv_kernels.cu", "attn_kernels.cu", "tc_capi.cu",
-           "norm_kernels.cu", "rope_kernels.cu", "pattn_kernels.cu", "pattn_forward.cu", "pattn_backward.cu",
+           "norm_kernels.cu", "rope_kernels.cu", "pattn_kernels.cu", "pattn_forward.cu", "pattn_split.cu", "pattn_backward.cu",
            "block_capi.cu"]
 HEADERS = ["gn_internal.h", "gn_math.cuh", "gn_ptx.cuh", "tc_ptx.cuh", "tc_common.cuh", "tc_internal.h", "capi_util.h",
            "block_internal.h", "block_math.cuh", "pattn_common.cuh", "pattn_tiles.cuh"]

@@ -49,39 +49,6 @@ __host__ __device__ inline Layout layout(int halves)
     return l;
 }
 
-// One query computed by one warp (four channels per lane) without ever
-// touching a key that it does not see.
-template <typename T>
-__device__ __noinline__ void row_forward(const gn_attn_packed_args &a, int group, int i, int h)
-{
-    const int lane = threadIdx.x & 31, hk = h / group;
-    const Span s = query_span(a, i);
-    const float slope = a.slopes ? a.slopes[h] : 0.f;
-    const float4 q = load4<T>(a.q, i * a.q_token + h * a.q_head, lane, a.dim);
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = s.lo; j < s.hi; ++j) {
-        const float4 k = load4<T>(a.k, j * a.k_token + hk * a.k_head, lane, a.dim);
-        const float4 v = load4<T>(a.v, j * a.v_token + hk * a.v_head, lane, a.dim);
-        float slack;
-        const float t = score_log2(a, slope, warp_sum(dot4(q, k)), s.pos, j, slack);
-        if (t > m) {
-            const float f = m == -INFINITY ? 0.f : ex2_approx(m - t);
-            l *= f;
-            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-            m = t;
-        }
-        const float w = t == -INFINITY ? 0.f : ex2_approx(t - m);
-        l += w;
-        axpy4(o, w, v);
-    }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    store4<T>(a.out, (static_cast<int64_t>(i) * a.heads + h) * a.dim, lane, a.dim,
-              l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (lane == 0)
-        a.lse[static_cast<int64_t>(h) * a.tokens_q + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
 template <typename T, bool GENERAL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,

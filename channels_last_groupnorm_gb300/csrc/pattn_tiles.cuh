@@ -395,6 +395,39 @@ __device__ __forceinline__ void clear_not_finite(uint32_t tile, int r, int token
     fence_proxy_async_smem();
 }
 
+// One query computed by one warp (four channels per lane) without ever
+// touching a key that it does not see.
+template <typename T>
+static __device__ __noinline__ void row_forward(const gn_attn_packed_args &a, int group, int i, int h)
+{
+    const int lane = threadIdx.x & 31, hk = h / group;
+    const Span s = query_span(a, i);
+    const float slope = a.slopes ? a.slopes[h] : 0.f;
+    const float4 q = load4<T>(a.q, i * a.q_token + h * a.q_head, lane, a.dim);
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = s.lo; j < s.hi; ++j) {
+        const float4 k = load4<T>(a.k, j * a.k_token + hk * a.k_head, lane, a.dim);
+        const float4 v = load4<T>(a.v, j * a.v_token + hk * a.v_head, lane, a.dim);
+        float slack;
+        const float t = score_log2(a, slope, warp_sum(dot4(q, k)), s.pos, j, slack);
+        if (t > m) {
+            const float f = m == -INFINITY ? 0.f : ex2_approx(m - t);
+            l *= f;
+            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+            m = t;
+        }
+        const float w = t == -INFINITY ? 0.f : ex2_approx(t - m);
+        l += w;
+        axpy4(o, w, v);
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    store4<T>(a.out, (static_cast<int64_t>(i) * a.heads + h) * a.dim, lane, a.dim,
+              l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    if (lane == 0)
+        a.lse[static_cast<int64_t>(h) * a.tokens_q + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
 // Document of `token` for a whole warp: with up to 32 documents their ends
 // come in one load and are handed round, otherwise every lane searches.
 __device__ __forceinline__ int doc_of_warp(const int32_t *ends, int docs, int token, int lane)
@@ -441,9 +474,22 @@ inline cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<ui
     return e;
 }
 
-// Tensor map over [tokens][heads][dim] with boxes of 128 tokens x 64 channels.
+// Lets `kernel` run in clusters of more than eight CTAs, once per device.
+inline cudaError_t allow_clusters(const void *kernel, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (e != cudaSuccess || (dev < 64 && (done.load() & bit))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
+}
+
+// Tensor map over [tokens][heads][dim] with boxes of 64 channels x box_heads x
+// box_tokens.
 inline bool encode_heads(CUtensorMap *map, const void *base, bool bf16, int64_t tokens, int64_t token_stride, int heads,
-                         int64_t head_stride, int dim)
+                         int64_t head_stride, int dim, int box_heads = 1, int box_tokens = kTile)
 {
     const tc::EncodeTiledFn fn = tc::encode_fn();
     if (!fn) return false;
@@ -452,7 +498,7 @@ inline bool encode_heads(CUtensorMap *map, const void *base, bool bf16, int64_t 
     // an axis of one has no stride of its own
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? head_stride : dim) * 2,
                                    static_cast<cuuint64_t>(tokens > 1 ? token_stride : static_cast<int64_t>(heads) * dim) * 2};
-    const cuuint32_t box[3] = {64, 1, kTile};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
     const cuuint32_t step[3] = {1, 1, 1};
     return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
               const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
