@@ -9,12 +9,19 @@
 //  * the keys are split between the CTAs of a cluster (up to 16), each with
 //    its own blocks of 128, and the parts are joined over distributed shared
 //    memory at the end: one launch, no workspace;
-//  * two CTAs share an SM (112 KB of shared memory and half of tensor memory
-//    each), so that one's start, softmax or end is covered by the other's
-//    loads.
-// Per block: S = Q K^T, the weights of one row per thread (only warps that have
-// rows), O += P V, as in the kernel for long runs of queries.  Rows past the
-// tile's count read whatever lies there; nobody reads what becomes of them.
+//  * two CTAs share an SM, so that one's start, softmax or end is covered by the
+//    other's loads.
+// Two kernels, by the number of rows:
+//  * up to 32 (attn_few_kernel): the keys are the accumulator's lanes and the
+//    rows its columns, S^T = K Q^T and O^T += V^T P^T, so that every thread of
+//    the softmax warps has a key, and a block costs a thread as many
+//    exponentials as there are rows.
+//  * more (attn_split_kernel): as in the kernel for long runs of queries, one
+//    row per thread and 128 keys each.  With 4 rows, 4 lanes of one warp would do
+//    128 exponentials each: 1.5 us for a block that takes 0.35 us to load (85 us
+//    against XX us for 24 single tokens over caches of up to 8000 keys).
+// Rows past the tile's count read whatever lies there; nobody reads what becomes
+// of them.
 #include <algorithm>
 
 #include "pattn_tiles.cuh"
@@ -63,6 +70,74 @@ __device__ __forceinline__ float peer_float(uint32_t addr, int rank)
     return v;
 }
 
+// The end of either kernel: the cluster's parts (per row a maximum and a sum at
+// `stats`, unnormalised outputs [rows][dim] at `parts`, first and last cleared
+// key at `cleared`) joined, every CTA writing some of the channels; then the
+// rows that see a value row which any CTA cleared, one by one.  `live`, `span`:
+// of row r, held by the threads of warps 4 on.
+template <typename T>
+__device__ __forceinline__ void join_parts(const SplitArgs &args, uint32_t stats, uint32_t parts, uint32_t cleared,
+                                           bool failed, int split, int token0, int hk, int first_head, bool live, Span span,
+                                           int r)
+{
+    const gn_attn_packed_args &a = args.p.a;
+    const int rows = args.tokens * args.heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (args.splits > 1) cluster_sync_all();
+    if (!failed) {
+        for (int n = split * kThreads + static_cast<int>(threadIdx.x); n < rows * a.dim; n += args.splits * kThreads) {
+            const int row = n / a.dim, c = n - row * a.dim;
+            const int token = token0 + row / args.heads, g = first_head + row % args.heads;
+            if (token >= a.tokens_q || g >= args.p.group) continue;
+            // (all the peers' values are asked for before the first is used)
+            float ms[kMaxSplits], ls[kMaxSplits], vs[kMaxSplits];
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s) {
+                ms[s] = -INFINITY;
+                ls[s] = vs[s] = 0.f;
+                if (s < args.splits) {
+                    ms[s] = peer_float(stats + 4u * row, s);
+                    ls[s] = peer_float(stats + 4u * (kTile + row), s);
+                    vs[s] = peer_float(parts + 4u * static_cast<uint32_t>(n), s);
+                }
+            }
+            float top = -INFINITY, sum = 0.f, v = 0.f;
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s) top = fmaxf(top, ms[s]);
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s) {
+                // (a part that saw nothing has a sum of zero, and may have written no outputs)
+                const float f = ls[s] == 0.f ? 0.f : ex2_approx(ms[s] - top);
+                sum = fmaf(f, ls[s], sum);
+                v += ls[s] == 0.f ? 0.f : f * vs[s];
+            }
+            const int head = hk * args.p.group + g;
+            static_cast<T *>(a.out)[(static_cast<int64_t>(token) * a.heads + head) * a.dim + c] =
+                static_cast<T>(sum == 0.f ? 0.f : v / sum);
+            if (c == 0)
+                a.lse[static_cast<int64_t>(head) * a.tokens_q + token] =
+                    sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        }
+    }
+    int bad_lo = 0x7fffffff, bad_hi = -1;
+    if (split == 0 && warp >= 4 && lane < args.splits) {
+        bad_lo = __float_as_int(peer_float(cleared, lane));
+        bad_hi = __float_as_int(peer_float(cleared + 4, lane));
+    }
+    bad_lo = __reduce_min_sync(0xffffffffu, bad_lo);
+    bad_hi = __reduce_max_sync(0xffffffffu, bad_hi);
+    if (args.splits > 1)
+        cluster_sync_all();      // a CTA's parts stay until every peer has read them
+    else
+        __syncthreads();
+    if (split == 0 && warp >= 4 && !failed) {
+        unsigned again = __ballot_sync(0xffffffffu, live && span.lo < span.hi && span.lo <= bad_hi && span.hi > bad_lo);
+        for (; again; again &= again - 1) {
+            const int row = r - lane + __ffs(again) - 1;
+            row_forward<T>(a, args.p.group, token0 + row / args.heads, hk * args.p.group + first_head + row % args.heads);
+        }
+    }
+}
+
 template <typename T, bool GENERAL>
 __global__ void __launch_bounds__(kThreads, 2)
     attn_split_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -81,9 +156,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     int *bad = reinterpret_cast<int *>(gbase + lay.words + 8);
     volatile int *range = reinterpret_cast<volatile int *>(words + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = static_cast<int>(blockIdx.x) % args.splits;
-    const int token0 = static_cast<int>(blockIdx.x) / args.splits * args.tokens;
-    const int hk = blockIdx.y / args.chunks, first_head = blockIdx.y % args.chunks * args.heads;   // within the group
+    // splits innermost (a cluster), then the heads: CTAs that run at the same time
+    // read the same tokens, whose heads lie next to each other
+    const int split = static_cast<int>(blockIdx.x) % args.splits, part = static_cast<int>(blockIdx.x) / args.splits;
+    const int parts = a.kv_heads * args.chunks, token0 = part / parts * args.tokens;
+    const int hk = part % parts / args.chunks, first_head = part % args.chunks * args.heads;   // within the group
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i == kP ? 4 : 1);
@@ -284,63 +361,324 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_dealloc(tmem, 256);
     }
     __syncwarp();
-    if (args.splits > 1) cluster_sync_all();
-
-    // ---- the parts joined: every CTA some of the tile's channels ----
-    const bool failed = *abort != 0;
-    const uint32_t stats = base + lay.stats, out = base + lay.ring;
-    if (!failed) {
-        for (int n = split * kThreads + static_cast<int>(threadIdx.x); n < rows * a.dim; n += args.splits * kThreads) {
-            const int row = n / a.dim, c = n - row * a.dim;
-            const int token = token0 + row / args.heads, gg = first_head + row % args.heads;
-            if (token >= a.tokens_q || gg >= args.p.group) continue;
-            float top = -INFINITY, sum = 0.f, v = 0.f;
-            for (int s = 0; s < args.splits; ++s) top = fmaxf(top, peer_float(stats + 4u * row, s));
-            for (int s = 0; s < args.splits; ++s) {
-                const float ms = peer_float(stats + 4u * row, s), ls = peer_float(stats + 4u * (kTile + row), s);
-                if (ls == 0.f) continue;                      // saw nothing, and may have written nothing
-                const float f = ex2_approx(ms - top);
-                sum = fmaf(f, ls, sum);
-                v = fmaf(f, peer_float(out + 4u * static_cast<uint32_t>(n), s), v);
-            }
-            const int head = hk * args.p.group + gg;
-            static_cast<T *>(a.out)[(static_cast<int64_t>(token) * a.heads + head) * a.dim + c] =
-                static_cast<T>(sum == 0.f ? 0.f : v / sum);
-            if (c == 0)
-                a.lse[static_cast<int64_t>(head) * a.tokens_q + token] =
-                    sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-        }
-    }
-    // queries that see a value row which was cleared, whichever CTA cleared it
-    int bad_lo = 0x7fffffff, bad_hi = -1;
-    for (int s = 0; s < args.splits; ++s) {
-        bad_lo = min(bad_lo, __float_as_int(peer_float(base + lay.words + 8, s)));
-        bad_hi = max(bad_hi, __float_as_int(peer_float(base + lay.words + 12, s)));
-    }
-    if (args.splits > 1)
-        cluster_sync_all();      // a CTA's parts stay until every peer has read them
-    else
-        __syncthreads();
-    if (split == 0 && warp >= 4 && !failed) {
-        unsigned again = __ballot_sync(0xffffffffu, live && span.lo < span.hi && span.lo <= bad_hi && span.hi > bad_lo);
-        for (; again; again &= again - 1) {
-            const int row = r - lane + __ffs(again) - 1;
-            row_forward<T>(a, args.p.group, token0 + row / args.heads, hk * args.p.group + first_head + row % args.heads);
-        }
-    }
+    join_parts<T>(args, base + lay.stats, base + lay.ring, base + lay.words + 8, *abort != 0, split, token0, hk, first_head,
+                  live, span, r);
 }
+
+// ---------------------------------------------------------------------------
+// up to N = 16 or 32 rows: keys on the lanes
+// ---------------------------------------------------------------------------
+struct FewLayout {
+    uint32_t q, weights, ring, info, stats, tops, bars, words, total;
+};
+
+__host__ __device__ inline FewLayout few_layout(int halves, int n, int stages)
+{
+    FewLayout l;
+    const uint32_t tile = kHalfBytes * static_cast<uint32_t>(halves), rows = static_cast<uint32_t>(n) * 128u;
+    l.q = 0;                                    // [halves][n][64 channels]
+    l.weights = l.q + 2 * rows;                 // [2][n][64 keys], swizzled like a tile
+    l.ring = l.weights + 2 * rows;
+    // (with one half of channels the product with V reads another half past the last tile)
+    l.info = l.ring + static_cast<uint32_t>(stages) * tile + (halves == 1 ? kHalfBytes : 0u);
+    l.stats = l.info + static_cast<uint32_t>(n) * 16u;          // n runs of keys and slopes
+    l.tops = l.stats + 2 * kTile * 4;                           // 4 x n row maxima (or sums) of a warp
+    l.bars = l.tops + 4u * static_cast<uint32_t>(n) * 4u;
+    l.words = l.bars + 8 * kBars;
+    l.total = l.words + 4 * (4 + 16);
+    return l;
+}
+
+// An order-preserving whole number of a float, for the warp-wide maximum.
+__device__ __forceinline__ int ordered(float v)
+{
+    const int i = __float_as_int(v);
+    return i >= 0 ? i : i ^ 0x7fffffff;
+}
+__device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&v)[N])
+{
+#pragma unroll
+    for (int q = 0; q < N / 16; ++q) {
+        uint32_t u[16];
+        tmem_ld16(taddr + 16 * q, u);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[16 * q + k] = __uint_as_float(u[k]);
+    }
+    tmem_wait_ld();
+}
+
+template <typename T, bool GENERAL, int N>
+__global__ void __launch_bounds__(kThreads, 2)
+    attn_few_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SplitArgs args)
+{
+    extern __shared__ __align__(1024) uint8_t gbase[];
+    const uint32_t base = smem_addr(gbase);
+    const gn_attn_packed_args &a = args.p.a;
+    const int halves = a.dim > 64 ? 2 : 1, rows = args.tokens * args.heads;
+    const FewLayout lay = few_layout(halves, N, args.stages);
+    const uint32_t tile_bytes = kHalfBytes * static_cast<uint32_t>(halves), n_bytes = N * 128u;
+    const auto bar = [&](int i) { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
+    const auto stage = [&](int n) { return base + lay.ring + static_cast<uint32_t>(n % args.stages) * tile_bytes; };
+    volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(gbase + lay.words);
+    volatile int *abort = reinterpret_cast<volatile int *>(words + 1);
+    int *bad = reinterpret_cast<int *>(gbase + lay.words + 8);
+    volatile int *range = reinterpret_cast<volatile int *>(words + 4);
+    int4 *info = reinterpret_cast<int4 *>(gbase + lay.info);
+    float *tops = reinterpret_cast<float *>(gbase + lay.tops);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // splits innermost (a cluster), then the heads: CTAs that run at the same time
+    // read the same tokens, whose heads lie next to each other
+    const int split = static_cast<int>(blockIdx.x) % args.splits, part = static_cast<int>(blockIdx.x) / args.splits;
+    const int parts = a.kv_heads * args.chunks, token0 = part / parts * args.tokens;
+    const int hk = part % parts / args.chunks, first_head = part % args.chunks * args.heads;   // within the group
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i == kP ? 4 : 1);
+        *abort = (*reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) ? 1 : 0;
+        bad[0] = 0x7fffffff;
+        bad[1] = -1;
+        mbar_init_fence();
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+    }
+    if (warp == 1) {
+        tmem_alloc(base + lay.words, 64);
+        tmem_relinquish();
+    }
+    tc::griddep_wait();
+
+    // the rows (of which the first warp of four has all)
+    const int r = (warp & 3) * 32 + lane, i = token0 + r / args.heads, g = first_head + r % args.heads;
+    const int h = hk * args.p.group + g;
+    const bool live = warp >= 4 && r < rows && i < a.tokens_q && g < args.p.group;
+    Span span = {0, 0, 0};
+    if (warp == 4) {
+        span = query_span_warp(a, i, lane);
+        const bool some = live && span.lo < span.hi;
+        if (!some) span.lo = span.hi = 0;
+        if (r < N)
+            info[r] = make_int4(span.lo, span.hi, span.pos,
+                                __float_as_int(GENERAL && a.slopes && live ? __ldg(a.slopes + h) * kLog2e : 0.f));
+        const int lo = __reduce_min_sync(0xffffffffu, some ? span.lo : 0x7fffffff);
+        const int hi = __reduce_max_sync(0xffffffffu, some ? span.hi : 0);
+        const int all_lo = __reduce_max_sync(0xffffffffu, !live ? 0 : (some ? span.lo : 0x7fffffff));
+        const int all_hi = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : (some ? span.hi : 0));
+        if (lane == 0) {
+            range[0] = lo;
+            range[1] = hi;
+            range[2] = all_lo;
+            range[3] = all_hi;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    // (only now: a kernel that starts early must not find tensor memory that a
+    // CTA of this one has yet to take)
+    if (threadIdx.x == 0) tc::griddep_launch_dependents();
+    const uint32_t tmem = words[0], t_s = tmem, t_o = tmem + 32;
+    const int key0 = range[0], key1 = range[1], all_lo = range[2], all_hi = range[3];
+    // this CTA's blocks [b0, b1) of the tile's
+    const int total = key0 < key1 ? (key1 - key0 + kTile - 1) / kTile : 0;
+    const int share = (total + args.splits - 1) / args.splits;
+    const int b0 = min(total, split * share), b1 = min(total, b0 + share), blocks = b1 - b0;
+    const bool skip = *abort != 0;
+    const int k_first = key0 + b0 * kTile;     // (of no use without blocks)
+
+    if (warp == 0) {
+        if (lane == 0 && !skip && blocks > 0) {
+            mbar_arrive_expect_tx(bar(kQ), static_cast<uint32_t>(rows * halves) * 128u);
+            for (int n = 0; n < halves; ++n)
+                tma_load_3d(base + lay.q + n * n_bytes, &map_q, n * 64, hk * args.p.group + first_head, token0, bar(kQ));
+            int n = 0;
+            for (; n < 2 * blocks; ++n) {
+                const int st = n % args.stages;
+                if (n >= args.stages && !wait(bar(kEmpty + st), (n / args.stages - 1) & 1, abort, args.limit)) break;
+                mbar_arrive_expect_tx(bar(kFull + st), tile_bytes);
+                load_tile(stage(n), (n & 1) ? &map_v : &map_k, halves, hk, k_first + (n >> 1) * kTile, bar(kFull + st));
+            }
+            // nothing is left in flight when the CTA goes on, whatever became of the others
+            for (int k = max(0, n - args.stages); k < n; ++k)
+                tc::drain(bar(kFull + k % args.stages), (k / args.stages) & 1, args.limit.timeout_ns);
+            tc::drain(bar(kQ), 0, args.limit.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp == 1 || warp == 2) {
+        if (!skip && blocks > 0) {
+            const bool waits = warp == 2;
+            const int steps = (a.dim + 15) / 16;
+            // the rows are N; V is the A operand, read MN-major (bit 15)
+            const uint32_t is = instruction<T>(N, false), io = instruction<T>(N, false) | 1u << 15;
+            const auto loaded = [&](int n) {
+                wait_warp(bar(kFull + n % args.stages), (n / args.stages) & 1, abort, args.limit);
+            };
+            if (waits) wait_warp(bar(kQ), 0, abort, args.limit);
+            for (int b = 0; b < blocks; ++b) {
+                if (waits) loaded(2 * b);
+                hand_over();
+                if (!waits) {
+                    mma_tokens(t_s, stage(2 * b), base + lay.q, steps, is, kHalfBytes, n_bytes);
+                    commit(bar(kS));
+                    commit(bar(kEmpty + 2 * b % args.stages));
+                }
+                if (waits) {
+                    loaded(2 * b + 1);
+                    wait_warp(bar(kP), b & 1, abort, args.limit);
+                }
+                hand_over();
+                if (!waits) {
+                    tc_fence_after_sync();
+                    mma_values(t_o, stage(2 * b + 1), base + lay.weights, n_bytes, io, b > 0);
+                    commit(bar(kEmpty + (2 * b + 1) % args.stages));
+                }
+            }
+            if (!waits) {
+                commit(bar(kO));
+                commit(bar(kDrain));
+                tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+            }
+        }
+    } else if (warp >= 4 && !skip) {
+        constexpr float kShift = weight_shift<T>();
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        // this thread's key within the block: its place in the weights' rows
+        const uint32_t place = base + lay.weights + static_cast<uint32_t>(r >> 6) * n_bytes + static_cast<uint32_t>(r & 7) * 2u;
+        const uint32_t chunk = static_cast<uint32_t>(r >> 3) & 7u;
+        float m[N], l[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            m[n] = -INFINITY;
+            l[n] = 0.f;
+        }
+        float by = args.scale_log2, inv_cap = 0.f;
+        if (GENERAL && a.cap > 0.f) {
+            by = a.cap * kLog2e;
+            inv_cap = a.scale / a.cap;
+        }
+        for (int b = 0; b < blocks; ++b) {
+            const int first = k_first + b * kTile, j = first + r;
+            const bool masked = first < all_lo || first + kTile > all_hi;
+            wait_warp(bar(kS), b & 1, abort, args.limit);
+            tc_fence_after_sync();
+            float s[N];
+            tmem_ld_rows<N>(t_s + lanes, s);
+            bool grew = b == 0;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                if (GENERAL && a.cap > 0.f) s[n] = tanh_fast(s[n] * inv_cap);
+                s[n] *= by;
+                if (GENERAL || masked) {
+                    const int4 w = info[n];
+                    if (GENERAL && a.slopes) s[n] = fmaf(-__int_as_float(w.w), fabsf(static_cast<float>(w.z - j)), s[n]);
+                    if (masked) s[n] = j >= w.x && j < w.y ? s[n] : -INFINITY;
+                }
+                grew = grew || (n < rows && s[n] > m[n] + (kShift + kRescaleLog2));
+            }
+            // the maxima are the same in all threads, and only looked for when a
+            // score is far above one of them
+            if (bar_any(1, 128, grew)) {
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const int top = __reduce_max_sync(0xffffffffu, ordered(s[n] == s[n] ? s[n] : -INFINITY));
+                    if (lane == 0) tops[(warp & 3) * N + n] = from_ordered(top);
+                }
+                named_sync(1, 128);
+                float f[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const float top = fmaxf(fmaxf(tops[n], tops[N + n]), fmaxf(tops[2 * N + n], tops[3 * N + n])) - kShift;
+                    const bool up = top > m[n];
+                    f[n] = up && m[n] != -INFINITY ? ex2_approx(m[n] - top) : 1.0f;
+                    if (up) m[n] = top;
+                    l[n] *= f[n];
+                }
+                if (b > 0) {
+                    float o[N];
+                    tmem_ld_rows<N>(t_o + lanes, o);
+#pragma unroll
+                    for (int q = 0; q < N / 16; ++q) {
+                        uint32_t u[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[16 * q + k] * f[16 * q + k]);
+                        tmem_st16(t_o + lanes + 16 * q, u);
+                    }
+                    tmem_wait_st();
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const float p = ex2_approx(s[n] - (m[n] == -INFINITY ? 0.f : m[n]));
+                l[n] += p;
+                sts_u16(place + n * 128u + ((chunk ^ (n & 7u)) << 4), Half2<T>::pack(p, 0.f));
+            }
+            if (masked) {
+                const int nv = 2 * b + 1;
+                wait_warp(bar(kFull + nv % args.stages), (nv / args.stages) & 1, abort, args.limit);
+                clear_not_finite<T>(stage(nv), r, j, key0, key1, halves, bad);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kP));
+        }
+        if (blocks > 0) wait_warp(bar(kO), 0, abort, args.limit);
+        tc_fence_after_sync();
+        // (the ring is free: every product is done; a failed call reads nothing of it)
+        float *out = reinterpret_cast<float *>(gbase + lay.ring), *stats = reinterpret_cast<float *>(gbase + lay.stats);
+        if (blocks > 0) {
+            float o[N];
+            tmem_ld_rows<N>(t_o + lanes, o);
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                if (n < rows && r < a.dim) out[n * a.dim + r] = o[n];
+        }
+        named_sync(1, 128);           // the maxima in `tops` have been read
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const float sum = warp_sum(l[n]);
+            if (lane == 0) tops[(warp & 3) * N + n] = sum;
+        }
+        named_sync(1, 128);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (r == n) {
+                stats[n] = m[n];
+                stats[kTile + n] = (tops[n] + tops[N + n]) + (tops[2 * N + n] + tops[3 * N + n]);
+            }
+        tc_fence_before_sync();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 64);
+    }
+    __syncwarp();
+    join_parts<T>(args, base + lay.stats, base + lay.ring, base + lay.words + 8, *abort != 0, split, token0, hk, first_head,
+                  live, span, r);
+}
+
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const SplitArgs);
 
 template <typename T, bool GENERAL>
 cudaError_t launch(const SplitArgs &args, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s)
 {
-    const int halves = args.p.a.dim > 64 ? 2 : 1;
-    // (never so little that three CTAs would share an SM: they take 256 columns
-    // of its 512 of tensor memory each)
-    const size_t smem = std::max<size_t>(layout(halves, args.tokens * args.heads, args.stages).total, 80 * 1024);
-    static std::atomic<uint64_t> done{0}, wide{0};
-    const void *kernel = reinterpret_cast<const void *>(attn_split_kernel<T, GENERAL>);
-    cudaError_t e = allow_shared(kernel, layout(2, kTile, 3).total, done);
-    if (e == cudaSuccess) e = allow_clusters(kernel, wide);
+    const int halves = args.p.a.dim > 64 ? 2 : 1, rows = args.tokens * args.heads;
+    static std::atomic<uint64_t> done[3], wide[3];
+    const int which = rows <= 16 ? 0 : (rows <= 32 ? 1 : 2);
+    const Kernel kernels[3] = {attn_few_kernel<T, GENERAL, 16>, attn_few_kernel<T, GENERAL, 32>, attn_split_kernel<T, GENERAL>};
+    const Kernel kernel = kernels[which];
+    // (never so little that three CTAs would share an SM: attn_split_kernel's
+    // take 256 columns of its 512 of tensor memory each)
+    const size_t smem = std::max<size_t>(which < 2 ? few_layout(halves, which ? 32 : 16, args.stages).total
+                                                   : layout(halves, rows, args.stages).total, 80 * 1024);
+    cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), 160 * 1024, done[which]);
+    if (e == cudaSuccess) e = allow_clusters(reinterpret_cast<const void *>(kernel), wide[which]);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -351,13 +689,13 @@ cudaError_t launch(const SplitArgs &args, const CUtensorMap &mq, const CUtensorM
     at[1].val.clusterDim.z = 1;
     const int64_t tiles = (args.p.a.tokens_q + args.tokens - 1) / args.tokens;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * args.splits), static_cast<unsigned>(args.p.a.kv_heads * args.chunks));
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * args.splits * args.p.a.kv_heads * args.chunks));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = args.splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, attn_split_kernel<T, GENERAL>, mq, mk, mv, args);
+    return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, args);
 }
 
 }  // namespace

@@ -143,16 +143,16 @@ __device__ __forceinline__ void commit(uint32_t bar)
 // the descriptors' address field, and are unrolled.
 
 // D = A B^T over the channels of two tiles (128 x 128, `steps` of 16 channels);
-// a_half: bytes from A's first 64 channels to its others.
+// a_half, b_half: bytes from an operand's first 64 channels to its others.
 __device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc,
-                                           uint32_t a_half = kHalfBytes)
+                                           uint32_t a_half = kHalfBytes, uint32_t b_half = kHalfBytes)
 {
     const uint64_t da = sw128_kmajor_desc(a), db = sw128_kmajor_desc(b);
     if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             if (k >= steps) break;
-            umma_f16(d, da + (k >> 2) * (a_half >> 4) + (k & 3) * 2, db + (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2, idesc,
+            umma_f16(d, da + (k >> 2) * (a_half >> 4) + (k & 3) * 2, db + (k >> 2) * (b_half >> 4) + (k & 3) * 2, idesc,
                      k > 0);
         }
     }
@@ -199,6 +199,24 @@ __device__ __forceinline__ void tanh_all(float (&v)[N], float k)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = tanh_fast(v[i] * k);
     }
+}
+
+// D (+)= A^T B over the 128 tokens of a tile A (channels are the lanes), B the
+// weights of some rows, [2][rows][64 tokens], `half` bytes apart.
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b, uint32_t half, uint32_t idesc, bool accumulate)
+{
+    const uint64_t da = sw128_mnmajor_desc(a), db = sw128_kmajor_desc(b);
+    if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            umma_f16(d, da + k * (2048u >> 4), db + (k >> 2) * (half >> 4) + (k & 3) * 2, idesc, accumulate || k > 0);
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(static_cast<unsigned short>(v)) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
