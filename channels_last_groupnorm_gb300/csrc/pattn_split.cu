@@ -570,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             bool grew = b == 0;
 #pragma unroll
             for (int n = 0; n < N; ++n) {
+                if (n >= rows) break;             // (the same for all: rows that are not there cost nothing)
                 if (GENERAL && a.cap > 0.f) s[n] = tanh_fast(s[n] * inv_cap);
                 s[n] *= by;
                 if (GENERAL || masked) {
@@ -577,13 +578,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (GENERAL && a.slopes) s[n] = fmaf(-__int_as_float(w.w), fabsf(static_cast<float>(w.z - j)), s[n]);
                     if (masked) s[n] = j >= w.x && j < w.y ? s[n] : -INFINITY;
                 }
-                grew = grew || (n < rows && s[n] > m[n] + (kShift + kRescaleLog2));
+                grew = grew || s[n] > m[n] + (kShift + kRescaleLog2);
             }
             // the maxima are the same in all threads, and only looked for when a
             // score is far above one of them
             if (bar_any(1, 128, grew)) {
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
+                    if (n >= rows) break;
                     const int top = __reduce_max_sync(0xffffffffu, ordered(s[n] == s[n] ? s[n] : -INFINITY));
                     if (lane == 0) tops[(warp & 3) * N + n] = from_ordered(top);
                 }
@@ -591,6 +593,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 float f[N];
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
+                    f[n] = 1.0f;
+                    if (n >= rows) continue;
                     const float top = fmaxf(fmaxf(tops[n], tops[N + n]), fmaxf(tops[2 * N + n], tops[3 * N + n])) - kShift;
                     const bool up = top > m[n];
                     f[n] = up && m[n] != -INFINITY ? ex2_approx(m[n] - top) : 1.0f;
@@ -612,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
 #pragma unroll
             for (int n = 0; n < N; ++n) {
+                if (n >= rows) break;
                 const float p = ex2_approx(s[n] - (m[n] == -INFINITY ? 0.f : m[n]));
                 l[n] += p;
                 sts_u16(place + n * 128u + ((chunk ^ (n & 7u)) << 4), Half2<T>::pack(p, 0.f));
@@ -640,6 +645,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         named_sync(1, 128);           // the maxima in `tops` have been read
 #pragma unroll
         for (int n = 0; n < N; ++n) {
+            if (n >= rows) break;
             const float sum = warp_sum(l[n]);
             if (lane == 0) tops[(warp & 3) * N + n] = sum;
         }
