@@ -19,7 +19,7 @@
 //  * more (attn_split_kernel): as in the kernel for long runs of queries, one
 //    row per thread and 128 keys each.  With 4 rows, 4 lanes of one warp would do
 //    128 exponentials each: 1.5 us for a block that takes 0.35 us to load (85 us
-//    against XX us for 24 single tokens over caches of up to 8000 keys).
+//    against 75 us for 24 single tokens over caches of up to 8000 keys).
 // Rows past the tile's count read whatever lies there; nobody reads what becomes
 // of them.
 #include <algorithm>
@@ -32,7 +32,7 @@ namespace {
 using namespace pattn;
 
 constexpr int kThreads = 256;   // warps: 0 loads, 1 MMA, 2 the MMA's waits, 4-7 softmax
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 5;
 constexpr int kMaxSplits = 16;
 
 struct SplitArgs {
@@ -717,13 +717,22 @@ cudaError_t launch_packed_attn_split(const PackedAttn &p, int sm_count, const Wa
     args.chunks = (p.group + args.heads - 1) / args.heads;
     const int64_t per_doc = (a.tokens_q + a.docs - 1) / a.docs;
     args.tokens = static_cast<int>(std::min<int64_t>(kTile / args.heads, per_doc));
-    // Splits: until every SM has four tiles, as long as a part of an average
-    // document keeps two blocks.
+    // Splits: the number that should end first.  CTAs run in rounds of two per
+    // SM, and one takes as long as its blocks and about seven more (start, first
+    // loads and join: 9 us where a block of its stream takes 1.3 us); documents
+    // are taken for half as long again as their average, since the longest ends
+    // last.  (24 caches of 2880 keys, 8 heads: 192 tiles, 3 splits: two rounds.)
     const int64_t tiles = (a.tokens_q + args.tokens - 1) / args.tokens * a.kv_heads * args.chunks;
-    const int64_t blocks = (a.tokens_k / a.docs + kTile - 1) / kTile;
-    args.splits = 1;
-    while (args.splits < kMaxSplits && tiles * args.splits < 4 * sm_count && blocks >= 4 * args.splits) args.splits *= 2;
-    args.stages = a.dim > 64 ? 3 : kMaxStages;
+    const double blocks = 1.5 * static_cast<double>(a.tokens_k) / a.docs / kTile;
+    double best = 0.0;
+    for (int s = 1; s <= kMaxSplits && (s == 1 || s <= blocks); ++s) {
+        const double cost = static_cast<double>((tiles * s + 2 * sm_count - 1) / (2 * sm_count)) * (7.0 + blocks / s);
+        if (s == 1 || cost < best) {
+            best = cost;
+            args.splits = s;
+        }
+    }
+    args.stages = a.dim > 64 ? 3 : 5;      // (two CTAs' shared memory fits an SM)
     const bool bf16 = a.format == GN_FORMAT_BF16;
     CUtensorMap mq, mk, mv;
     if (!encode_heads(&mq, a.q, bf16, a.tokens_q, a.q_token, a.heads, a.q_head, a.dim, args.heads, args.tokens) ||

@@ -500,6 +500,8 @@ inline cudaError_t allow_clusters(const void *kernel, std::atomic<uint64_t> &don
     const uint64_t bit = 1ull << (dev & 63);
     if (e != cudaSuccess || (dev < 64 && (done.load() & bit))) return e;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess) done.fetch_or(bit);
     return e;
 }
