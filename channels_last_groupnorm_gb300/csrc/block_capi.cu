@@ -388,7 +388,7 @@ int gn_attn_packed_backward(const gn_attn_packed_args *args, const void *dout, i
     p.dv = dv;
     p.workspace = workspace;
     int launches = 0;
-    const cudaError_t e = gn::launch_packed_attn_backward(p, {wait_timeout_ns(), d.status_word, d.status_host},
+    const cudaError_t e = gn::launch_packed_attn_backward(p, d.sm_count, {wait_timeout_ns(), d.status_word, d.status_host},
                                                           static_cast<cudaStream_t>(stream), &launches);
     return launched(e, launches);
 }

@@ -85,6 +85,7 @@ cudaError_t launch_packed_attn_tiles(const PackedAttn &p, const WaitLimit &limit
 cudaError_t launch_packed_attn_split(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s);
 cudaError_t launch_packed_attn(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s, int *launches);
 size_t packed_attn_workspace_bytes(int64_t tokens_q, int heads);
-cudaError_t launch_packed_attn_backward(const PackedAttn &p, const WaitLimit &limit, cudaStream_t s, int *launches);
+cudaError_t launch_packed_attn_backward(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s,
+                                        int *launches);
 
 }  // namespace gn

@@ -5,7 +5,10 @@
 //                           lse in units of log2 and delta = dout . out
 //   attn_dkv_kernel         a CTA owns 128 keys of one key / value head and
 //                           goes over the queries that see them, in blocks of
-//                           128, for every query head of the group:
+//                           128, for every query head of the group (or, where
+//                           those CTAs would be few, a cluster of CTAs shares
+//                           the heads and adds up over distributed shared
+//                           memory at the end):
 //     S^T = K Q^T, dP^T = V dO^T           (keys are the lanes)
 //     P^T = 2^(c S^T - lse),  dS^T = P^T (dP^T - delta) (1 - tanh^2)
 //     dV += P^T dO,  dK += dS^T Q          (P^T, dS^T from tensor memory)
@@ -137,10 +140,12 @@ __device__ __noinline__ void row_dkv(const PackedAttn &p, const Info &info, int 
 }
 
 // Scores of N pairs (raw, in place) to what times the returned factor is in
-// units of log2 before lse, capped and biased; far(n): the pair's distance.
-// slack[n], with a cap: its slope there.
-template <bool GENERAL, int N, typename Far>
-__device__ __forceinline__ float bend(float (&s)[N], float (&slack)[N], const TileArgs &args, float slope2, Far far)
+// units of log2 before lse, capped, and biased by the distance |at + DIR n| (or,
+// for queries of several documents, by what far(n) says).  slack[n], with a cap:
+// its slope there.
+template <bool GENERAL, int DIR, int N, typename Far>
+__device__ __forceinline__ float bend(float (&s)[N], float (&slack)[N], const TileArgs &args, float slope2, int at,
+                                      bool several, Far far)
 {
     if (!GENERAL) return args.scale_log2;
     const gn_attn_packed_args &a = args.p.a;
@@ -157,9 +162,28 @@ __device__ __forceinline__ float bend(float (&s)[N], float (&slack)[N], const Ti
         }
     }
     if (!a.slopes) return by;
+    if (several) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) s[n] = fmaf(-slope2, fabsf(far(n)), s[n] * by);
+        for (int n = 0; n < N; ++n) s[n] = fmaf(-slope2, fabsf(far(n)), s[n] * by);
+    } else {
+        take_distance<DIR>(s, by, slope2, at);
+    }
     return 1.0f;
+}
+
+// The weights times the cap's slopes, which is all that the scores' gradients
+// want of either (and keeps 64 registers free for dP).
+template <bool GENERAL, int N>
+__device__ __forceinline__ void fold_slack(float (&w)[N], const float (&slack)[N], float cap)
+{
+    if (GENERAL && cap != 0.f) {
+#pragma unroll
+        for (int n = 0; n < N; n += 2) {
+            const float2 v = unpack2(mul2(pack2(w[n], w[n + 1]), pack2(slack[n], slack[n + 1])));
+            w[n] = v.x;
+            w[n + 1] = v.y;
+        }
+    }
 }
 
 // Barriers and words of either kernel.  Own: the tiles a CTA owns; Long /
@@ -275,9 +299,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return n < 0 || wait(bar(kShortFree + n % kShortStages), (n / kShortStages) & 1, abort, args.limit);
     };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int hk = blockIdx.x % a.kv_heads;
+    // a cluster's CTAs take `heads` of the group's query heads each
+    const int parts = args.parts, part = static_cast<int>(blockIdx.x) % parts, heads = group / parts;
+    const int hk = static_cast<int>(blockIdx.x) / parts % a.kv_heads, first_head = hk * group + part * heads;
     // the first tiles first: with causal runs the most queries see them
-    const int key0 = static_cast<int>(blockIdx.x / a.kv_heads) * kTile;
+    const int key0 = static_cast<int>(blockIdx.x) / parts / a.kv_heads * kTile;
 
     if (threadIdx.x == 0) {
         init_bars(bar(0));
@@ -328,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool any = q_lo < q_hi;
     const int q0 = q_lo & ~3;                   // the rows' records are copied from a multiple of 32 bytes
     const int blocks = any ? (q_hi - q0 + kTile - 1) / kTile : 0;
-    const int steps_all = blocks * group;       // query heads outermost
+    const int steps_all = blocks * heads;       // query heads outermost
     const bool skip = *abort != 0;
     const uint32_t k_tile = base + lay.own, v_tile = k_tile + tile_bytes;
     const uint32_t t_s = tmem, t_dp = tmem + 128, t_dk = tmem + 256, t_dv = tmem + 384;
@@ -343,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; go && n < steps_all; ++n) {
             const int i0 = q0 + (n % blocks) * kTile;
             const bool masked = i0 < all_lo || i0 + kTile > all_hi;
-            if (GENERAL && a.slopes && n % blocks == 0) slope2 = __ldg(a.slopes + hk * group + n / blocks) * kLog2e;
+            if (GENERAL && a.slopes && n % blocks == 0) slope2 = __ldg(a.slopes + first_head + n / blocks) * kLog2e;
             const float4 *nlse = reinterpret_cast<const float4 *>(gbase + lay.rows + (n & 1) * kTile * 8) + 16 * half;
             const float4 *ndelta = nlse + kTile / 4;
             const int4 *spans = info.span + i0 + 64 * half;
@@ -355,8 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_all(t_s + lanes + 64 * half, w);
             // (queries that all see the same keys stand one after the other)
             const int at = GENERAL && a.slopes ? __ldg(&spans->z) - key : 0;
-            const float c = masked ? bend<GENERAL>(w, slack, args, slope2, [&](int k) { return static_cast<float>(__ldg(&spans[k].z) - key); })
-                                   : bend<GENERAL>(w, slack, args, slope2, [&](int k) { return static_cast<float>(at + k); });
+            const float c = bend<GENERAL, 1>(w, slack, args, slope2, at, masked,
+                                             [&](int k) { return static_cast<float>(__ldg(&spans[k].z) - key); });
             const uint64_t c2 = pack2(c, c);
 #pragma unroll
             for (int k = 0; k < 64; k += 4) {
@@ -382,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 16; ++k) pk[k] = Half2<T>::pack(w[32 * q + 2 * k], w[32 * q + 2 * k + 1]);
                 tmem_st16(t_s + lanes + 64 * half + 16 * q, pk);
             }
+            fold_slack<GENERAL>(w, slack, a.cap);
             if (masked) {
                 const int r = (warp & 3) * 32 + lane;
                 if (half == 0 || has_short(n))
@@ -407,10 +434,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 x = unpack2(mul2(pack2(w[n0], w[n0 + 1]), add2(pack2(dp[n0], dp[n0 + 1]), pack2(e.x, e.y))));
                     const float2 y = unpack2(mul2(pack2(w[n0 + 2], w[n0 + 3]), add2(pack2(dp[n0 + 2], dp[n0 + 3]), pack2(e.z, e.w))));
                     float d[4] = {x.x, x.y, y.x, y.y};
-                    if (GENERAL && a.cap > 0.f) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) d[i] *= slack[n0 + i];
-                    }
                     if (masked) {
                         // a weight of zero times what an unseen row holds
 #pragma unroll
@@ -427,17 +450,63 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(kDs));
         }
         if (any && go) go = wait_warp(bar(kOut), 0, abort, args.limit);
-        if (!bar_any(1, 256, !go)) {   // one answer for all: there is another barrier inside
-            tc_fence_after_sync();
-            const int64_t at = (static_cast<int64_t>(key) * a.kv_heads + hk) * a.dim;
-            const bool live = key < a.tokens_k;
-            store_half<T>(args.p.dk, at, live, any, t_dk + lanes, half, a.dim, a.scale);
-            store_half<T>(args.p.dv, at, live, any, t_dv + lanes, half, a.dim, 1.0f);
+        const bool failed = bar_any(1, 256, !go), live = key < a.tokens_k;   // one answer for all: barriers follow
+        const int64_t at = (static_cast<int64_t>(key) * a.kv_heads + hk) * a.dim;
+        int bad_lo = 0x7fffffff, bad_hi = -1;
+        tc_fence_after_sync();
+        if (parts == 1) {
+            if (!failed) {
+                store_half<T>(args.p.dk, at, live, any, t_dk + lanes, half, a.dim, a.scale);
+                store_half<T>(args.p.dv, at, live, any, t_dv + lanes, half, a.dim, 1.0f);
+            }
             named_sync(1, 256);
-            unsigned again = __ballot_sync(0xffffffffu, live && span.lo < span.hi && span.lo <= bad[1] && span.hi > bad[0]);
-            for (int n = 0; again; again &= again - 1, ++n)
-                if ((n & 1) == half) row_dkv<T>(args.p, info, key - lane + __ffs(again) - 1, hk);
+            bad_lo = bad[0];
+            bad_hi = bad[1];
+        } else {
+            // this CTA's sums into its shared memory (all of which is free now:
+            // every product is done), [dk, dv][channels][keys]; then every CTA
+            // adds up all parts of some of the channels, in the parts' order
+            float *sums = reinterpret_cast<float *>(gbase);
+            if (any && !failed)
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    const int c = 64 * half + 32 * (q & 1);
+                    if (c >= a.dim) continue;
+                    float o[32];
+                    tmem_ld32((q < 2 ? t_dk : t_dv) + lanes + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (c + k < a.dim) sums[((q < 2 ? 0 : a.dim) + c + k) * kTile + row] = o[k];
+                }
+            cluster_sync_all();
+            const int eighths = 2 * a.dim / 8;
+            if (!failed)
+                for (int n = 2 * part + half; n < eighths; n += 2 * parts) {
+                    float v[8] = {};
+                    if (any)
+                        for (int p = 0; p < parts; ++p)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] += peer_float(base + ((n * 8 + e) * kTile + row) * 4u, p);
+                    const int c = n * 8 % a.dim;
+                    const float by = n * 8 < a.dim ? a.scale : 1.0f;
+                    if (live)
+                        *reinterpret_cast<uint4 *>(static_cast<T *>(n * 8 < a.dim ? args.p.dk : args.p.dv) + at + c) =
+                            make_uint4(Half2<T>::pack(v[0] * by, v[1] * by), Half2<T>::pack(v[2] * by, v[3] * by),
+                                       Half2<T>::pack(v[4] * by, v[5] * by), Half2<T>::pack(v[6] * by, v[7] * by));
+                }
+            if (lane < parts) {
+                bad_lo = __float_as_int(peer_float(base + lay.words + 8, lane));
+                bad_hi = __float_as_int(peer_float(base + lay.words + 12, lane));
+            }
+            bad_lo = __reduce_min_sync(0xffffffffu, bad_lo);
+            bad_hi = __reduce_max_sync(0xffffffffu, bad_hi);
+            cluster_sync_all();
         }
+        unsigned again = failed || part ? 0u : __ballot_sync(0xffffffffu, live && span.lo < span.hi && span.lo <= bad_hi &&
+                                                                              span.hi > bad_lo);
+        for (int n = 0; again; again &= again - 1, ++n)
+            if ((n & 1) == half) row_dkv<T>(args.p, info, key - lane + __ffs(again) - 1, hk);
         tc_fence_before_sync();
     } else {
         few_registers();
@@ -448,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_tile(v_tile, &map_v, halves, hk, key0, bar(kOwn));
                 Loads got = {};
                 for (int n = 0; n < steps_all; ++n) {
-                    const int h = hk * group + n / blocks, i0 = q0 + (n % blocks) * kTile;
+                    const int h = first_head + n / blocks, i0 = q0 + (n % blocks) * kTile;
                     if (!long_free(n - kLongStages)) break;
                     mbar_arrive_expect_tx(bar(kLong + n % kLongStages), tile_bytes);
                     load_tile(long_tile(n), &map_q, halves, h, i0, bar(kLong + n % kLongStages));
@@ -526,6 +595,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
                 }
             }
+        }
+        __syncwarp();
+        if (parts > 1) {        // (the softmax warps' two)
+            cluster_sync_all();
+            cluster_sync_all();
         }
     }
     __syncwarp();
@@ -643,8 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             float w[64], slack[64];              // scores, then weights; the cap's slopes
             tmem_ld_all(ts, w);
-            const float pos = static_cast<float>(span.z - j0 - 64 * half);
-            const float c = bend<GENERAL>(w, slack, args, slope2, [&](int k) { return pos - static_cast<float>(k); });
+            const float c = bend<GENERAL, -1>(w, slack, args, slope2, span.z - j0 - 64 * half, false, [](int) { return 0.f; });
             const uint64_t c2 = pack2(c, c), e2 = pack2(nlse, nlse);
 #pragma unroll
             for (int k = 0; k < 64; k += 2) {
@@ -652,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[k] = ex2_approx(x.x);
                 w[k + 1] = ex2_approx(x.y);
             }
+            fold_slack<GENERAL>(w, slack, a.cap);
             if (masked) {
 #pragma unroll
                 for (int k = 0; k < 64; ++k)
@@ -670,10 +744,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 16; ++k) {
                     const int n0 = 32 * q + 2 * k;
                     float2 x = unpack2(mul2(pack2(w[n0], w[n0 + 1]), add2(pack2(dp[n0], dp[n0 + 1]), d2)));
-                    if (GENERAL && a.cap > 0.f) {
-                        x.x *= slack[n0];
-                        x.y *= slack[n0 + 1];
-                    }
                     if (masked) {
                         x.x = w[n0] == 0.f ? 0.f : x.x;
                         x.y = w[n0 + 1] == 0.f ? 0.f : x.y;
@@ -783,7 +853,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename T, bool GENERAL>
-cudaError_t launch(const TileArgs &args, const CUtensorMap (&map)[4], const Info &info, cudaStream_t s, int *launches)
+cudaError_t launch(const TileArgs &args, const CUtensorMap (&map)[4], const Info &info, int sm_count, cudaStream_t s,
+                   int *launches)
 {
     const gn_attn_packed_args &a = args.p.a;
     const int halves = a.dim > 64 ? 2 : 1;
@@ -798,9 +869,32 @@ cudaError_t launch(const TileArgs &args, const CUtensorMap (&map)[4], const Info
     ++*launches;
     TileArgs kv = args, q = args;
     kv.tiles = static_cast<int>((a.tokens_k + kTile - 1) / kTile);
+    // Shared heads: one CTA for all query heads of a key / value head and tile,
+    // or (a divisor up to 8 of them) a cluster, when those CTAs are fewer than
+    // four for each SM and the longest would be waited for: 4360 tokens, 16 heads
+    // on 4, D = 64, 319 us in 140 CTAs, XX in 560.
+    kv.parts = 1;
+    while (kv.parts < 8 && args.p.group % (2 * kv.parts) == 0 &&
+           static_cast<int64_t>(kv.tiles) * a.kv_heads * kv.parts < 4 * sm_count)
+        kv.parts *= 2;
+    for (const int odd : {7, 5, 3})
+        if (kv.parts == 1 && args.p.group % odd == 0 && static_cast<int64_t>(kv.tiles) * a.kv_heads < 4 * sm_count) kv.parts = odd;
     q.tiles = static_cast<int>((a.tokens_q + kTile - 1) / kTile);
-    e = tc::launch_pdl(attn_dkv_kernel<T, GENERAL>, dim3(static_cast<unsigned>(static_cast<int64_t>(kv.tiles) * a.kv_heads)),
-                       dim3(kThreads), layout(halves).total, s, map[0], map[1], map[2], map[3], kv, info);
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(kv.parts);
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(kv.tiles) * a.kv_heads * kv.parts));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = layout(halves).total;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = kv.parts > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, attn_dkv_kernel<T, GENERAL>, map[0], map[1], map[2], map[3], kv, info);
     if (e != cudaSuccess) return e;
     ++*launches;
     e = tc::launch_pdl(attn_dq_kernel<T, GENERAL>, dim3(static_cast<unsigned>(static_cast<int64_t>(q.tiles) * a.heads)),
@@ -816,7 +910,8 @@ size_t packed_attn_workspace_bytes(int64_t tokens_q, int heads)
     return static_cast<size_t>(padded_rows(tokens_q)) * (16 + 8 * static_cast<size_t>(heads));
 }
 
-cudaError_t launch_packed_attn_backward(const PackedAttn &p, const WaitLimit &limit, cudaStream_t s, int *launches)
+cudaError_t launch_packed_attn_backward(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s,
+                                        int *launches)
 {
     const gn_attn_packed_args &a = p.a;
     if (a.tokens_q == 0 || a.tokens_k == 0) {
@@ -845,10 +940,10 @@ cudaError_t launch_packed_attn_backward(const PackedAttn &p, const WaitLimit &li
     info.delta = info.lse + info.padded * a.heads;
     const bool general = a.cap > 0.f || a.slopes;
     if (bf16)
-        return general ? launch<__nv_bfloat16, true>(args, map, info, s, launches)
-                       : launch<__nv_bfloat16, false>(args, map, info, s, launches);
-    return general ? launch<__half, true>(args, map, info, s, launches)
-                   : launch<__half, false>(args, map, info, s, launches);
+        return general ? launch<__nv_bfloat16, true>(args, map, info, sm_count, s, launches)
+                       : launch<__nv_bfloat16, false>(args, map, info, sm_count, s, launches);
+    return general ? launch<__half, true>(args, map, info, sm_count, s, launches)
+                   : launch<__half, false>(args, map, info, sm_count, s, launches);
 }
 
 }  // namespace gn

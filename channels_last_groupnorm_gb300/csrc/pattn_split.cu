@@ -63,13 +63,6 @@ __host__ __device__ inline Layout layout(int halves, int rows, int stages)
     return l;
 }
 
-__device__ __forceinline__ float peer_float(uint32_t addr, int rank)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(addr, rank)) : "memory");
-    return v;
-}
-
 // The end of either kernel: the cluster's parts (per row a maximum and a sum at
 // `stats`, unnormalised outputs [rows][dim] at `parts`, first and last cleared
 // key at `cleared`) joined, every CTA writing some of the channels; then the

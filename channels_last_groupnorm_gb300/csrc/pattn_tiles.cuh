@@ -31,6 +31,7 @@ struct TileArgs {
     float scale_log2;
     WaitLimit limit;
     int tiles;             // tile groups along the token axis that the CTAs own
+    int parts;             // dK and dV: CTAs that share a group's query heads
 };
 
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort, const WaitLimit &l)
@@ -277,14 +278,36 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// s[k] <- by s[k] - slope2 |at + DIR k| for N neighbouring tokens of the other
+// side.  Where all of them lie on one side for the whole warp, the distance is
+// linear in k: two operations for two scores instead of three for one.
+template <int DIR, int N>
+__device__ __forceinline__ void take_distance(float (&s)[N], float by, float slope2, int at)
+{
+    const int end = at + DIR * (N - 1);
+    const bool ahead = __all_sync(0xffffffffu, min(at, end) >= 0), behind = __all_sync(0xffffffffu, max(at, end) <= 0);
+    const float p = static_cast<float>(at);
+    if (ahead || behind) {
+        const float by_one = ahead ? -slope2 : slope2;    // per unit of at + DIR k
+        const uint64_t by2 = pack2(by, by), t2 = pack2(by_one, by_one), b2 = pack2(by_one * p, by_one * p);
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+            const float2 v = unpack2(fma2(pack2(s[k], s[k + 1]), by2,
+                                          fma2(t2, pack2(static_cast<float>(DIR * k), static_cast<float>(DIR * (k + 1))), b2)));
+            s[k] = v.x;
+            s[k + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[k] = fmaf(-slope2, fabsf(p + static_cast<float>(DIR * k)), s[k] * by);
+    }
+}
+
 // ---- scores of one query against N neighbouring keys -----------------------------------
 // In place, to what times the returned factor is in units of log2 (capped,
 // biased, masked).  at: the query's position relative to the first key; keys lo
 // .. lo + len - 1, relative to it too, are seen.  Without GENERAL (no cap, no
 // bias, a positive scale) the raw scores only want their factor.
-//
-// The bias of a block that lies wholly on one side of the warp's queries is
-// linear in the key: two operations for two scores instead of three for one.
 template <bool GENERAL, int N>
 __device__ __forceinline__ float bend_scores(float (&s)[N], const gn_attn_packed_args &a, float scale_log2, float slope2,
                                              int at)
@@ -296,22 +319,7 @@ __device__ __forceinline__ float bend_scores(float (&s)[N], const gn_attn_packed
         by = a.cap * kLog2e;
     }
     if (a.slopes) {
-        const bool left = __all_sync(0xffffffffu, at >= N - 1), right = __all_sync(0xffffffffu, at <= 0);
-        const float p = static_cast<float>(at);
-        if (left || right) {
-            const float toward = left ? slope2 : -slope2;
-            const uint64_t by2 = pack2(by, by), t2 = pack2(toward, toward), b2 = pack2(-toward * p, -toward * p);
-#pragma unroll
-            for (int k = 0; k < N; k += 2) {
-                const float2 v = unpack2(fma2(pack2(s[k], s[k + 1]), by2,
-                                              fma2(t2, pack2(static_cast<float>(k), static_cast<float>(k + 1)), b2)));
-                s[k] = v.x;
-                s[k + 1] = v.y;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k) s[k] = fmaf(-slope2, fabsf(p - k), s[k] * by);
-        }
+        take_distance<-1>(s, by, slope2, at);
         return 1.0f;
     }
     if (by > 0.f) return by;
@@ -367,6 +375,14 @@ __device__ __forceinline__ void weigh_32(const float *s, uint64_t c2, uint64_t m
         sum2[k & 1] = add2(sum2[k & 1], pack2(p0, p1));
         pk[k] = Half2<T>::pack(p0, p1);
     }
+}
+
+// A float at the same place of the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ float peer_float(uint32_t addr, int rank)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(addr, rank)) : "memory");
+    return v;
 }
 
 // Row r of a tile holds an infinity or a NaN.
