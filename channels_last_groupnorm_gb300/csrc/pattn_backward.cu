@@ -139,18 +139,20 @@ __device__ __noinline__ void row_dkv(const PackedAttn &p, const Info &info, int 
     store4<T>(p.dv, (static_cast<int64_t>(j) * a.kv_heads + hk) * a.dim, lane, a.dim, dv);
 }
 
+// What a kernel is built for: scores capped, biased by distance.
+constexpr int kCap = 1, kBias = 2;
+
 // Scores of N pairs (raw, in place) to what times the returned factor is in
 // units of log2 before lse, capped, and biased by the distance |at + DIR n| (or,
 // for queries of several documents, by what far(n) says).  slack[n], with a cap:
 // its slope there.
-template <bool GENERAL, int DIR, int N, typename Far>
+template <int MODE, int DIR, int N, typename Far>
 __device__ __forceinline__ float bend(float (&s)[N], float (&slack)[N], const TileArgs &args, float slope2, int at,
                                       bool several, Far far)
 {
-    if (!GENERAL) return args.scale_log2;
     const gn_attn_packed_args &a = args.p.a;
     float by = args.scale_log2;
-    if (a.cap > 0.f) {
+    if (MODE & kCap) {
         tanh_all(s, a.scale / a.cap);
         by = a.cap * kLog2e;
 #pragma unroll
@@ -161,7 +163,7 @@ __device__ __forceinline__ float bend(float (&s)[N], float (&slack)[N], const Ti
             slack[n + 1] = r.y;
         }
     }
-    if (!a.slopes) return by;
+    if (!(MODE & kBias)) return by;
     if (several) {
 #pragma unroll
         for (int n = 0; n < N; ++n) s[n] = fmaf(-slope2, fabsf(far(n)), s[n] * by);
@@ -173,10 +175,10 @@ __device__ __forceinline__ float bend(float (&s)[N], float (&slack)[N], const Ti
 
 // The weights times the cap's slopes, which is all that the scores' gradients
 // want of either (and keeps 64 registers free for dP).
-template <bool GENERAL, int N>
-__device__ __forceinline__ void fold_slack(float (&w)[N], const float (&slack)[N], float cap)
+template <int MODE, int N>
+__device__ __forceinline__ void fold_slack(float (&w)[N], const float (&slack)[N])
 {
-    if (GENERAL && cap != 0.f) {
+    if (MODE & kCap) {
 #pragma unroll
         for (int n = 0; n < N; n += 2) {
             const float2 v = unpack2(mul2(pack2(w[n], w[n + 1]), pack2(slack[n], slack[n + 1])));
@@ -270,7 +272,7 @@ __device__ __forceinline__ void store_half(void *out, int64_t row_offset, bool l
 // ---------------------------------------------------------------------------
 // dK and dV
 // ---------------------------------------------------------------------------
-template <typename T, bool GENERAL>
+template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; go && n < steps_all; ++n) {
             const int i0 = q0 + (n % blocks) * kTile;
             const bool masked = i0 < all_lo || i0 + kTile > all_hi;
-            if (GENERAL && a.slopes && n % blocks == 0) slope2 = __ldg(a.slopes + first_head + n / blocks) * kLog2e;
+            if ((MODE & kBias) && n % blocks == 0) slope2 = __ldg(a.slopes + first_head + n / blocks) * kLog2e;
             const float4 *nlse = reinterpret_cast<const float4 *>(gbase + lay.rows + (n & 1) * kTile * 8) + 16 * half;
             const float4 *ndelta = nlse + kTile / 4;
             const int4 *spans = info.span + i0 + 64 * half;
@@ -380,8 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float w[64], slack[64];              // scores, then weights; the cap's slopes
             tmem_ld_all(t_s + lanes + 64 * half, w);
             // (queries that all see the same keys stand one after the other)
-            const int at = GENERAL && a.slopes ? __ldg(&spans->z) - key : 0;
-            const float c = bend<GENERAL, 1>(w, slack, args, slope2, at, masked,
+            const int at = (MODE & kBias) ? __ldg(&spans->z) - key : 0;
+            const float c = bend<MODE, 1>(w, slack, args, slope2, at, masked,
                                              [&](int k) { return static_cast<float>(__ldg(&spans[k].z) - key); });
             const uint64_t c2 = pack2(c, c);
 #pragma unroll
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 16; ++k) pk[k] = Half2<T>::pack(w[32 * q + 2 * k], w[32 * q + 2 * k + 1]);
                 tmem_st16(t_s + lanes + 64 * half + 16 * q, pk);
             }
-            fold_slack<GENERAL>(w, slack, a.cap);
+            fold_slack<MODE>(w, slack);
             if (masked) {
                 const int r = (warp & 3) * 32 + lane;
                 if (half == 0 || has_short(n))
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // dQ
 // ---------------------------------------------------------------------------
-template <typename T, bool GENERAL>
+template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
@@ -705,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- softmax: one query per thread, 64 of a block's keys per warp ----
         const int half = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const float slope2 = GENERAL && a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
+        const float slope2 = (MODE & kBias) ? __ldg(a.slopes + h) * kLog2e : 0.f;
         bool go = !skip;
         for (int n = 0; go && n < blocks; ++n) {
             const int j0 = key0 + n * kTile;
@@ -717,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             float w[64], slack[64];              // scores, then weights; the cap's slopes
             tmem_ld_all(ts, w);
-            const float c = bend<GENERAL, -1>(w, slack, args, slope2, span.z - j0 - 64 * half, false, [](int) { return 0.f; });
+            const float c = bend<MODE, -1>(w, slack, args, slope2, span.z - j0 - 64 * half, false, [](int) { return 0.f; });
             const uint64_t c2 = pack2(c, c), e2 = pack2(nlse, nlse);
 #pragma unroll
             for (int k = 0; k < 64; k += 2) {
@@ -725,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[k] = ex2_approx(x.x);
                 w[k + 1] = ex2_approx(x.y);
             }
-            fold_slack<GENERAL>(w, slack, a.cap);
+            fold_slack<MODE>(w, slack);
             if (masked) {
 #pragma unroll
                 for (int k = 0; k < 64; ++k)
@@ -852,16 +854,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <typename T, bool GENERAL>
+template <typename T, int MODE>
 cudaError_t launch(const TileArgs &args, const CUtensorMap (&map)[4], const Info &info, int sm_count, cudaStream_t s,
                    int *launches)
 {
     const gn_attn_packed_args &a = args.p.a;
     const int halves = a.dim > 64 ? 2 : 1;
     static std::atomic<uint64_t> done_kv{0}, done_q{0};
-    cudaError_t e = allow_shared(reinterpret_cast<const void *>(attn_dkv_kernel<T, GENERAL>), layout(2).total, done_kv);
+    cudaError_t e = allow_shared(reinterpret_cast<const void *>(attn_dkv_kernel<T, MODE>), layout(2).total, done_kv);
     if (e == cudaSuccess)
-        e = allow_shared(reinterpret_cast<const void *>(attn_dq_kernel<T, GENERAL>), layout(2).total, done_q);
+        e = allow_shared(reinterpret_cast<const void *>(attn_dq_kernel<T, MODE>), layout(2).total, done_q);
     if (e != cudaSuccess) return e;
     const int64_t rows = info.padded * a.heads;
     e = tc::launch_pdl(attn_rows_info_kernel<T>, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0, s, args.p, info);
@@ -894,13 +896,23 @@ cudaError_t launch(const TileArgs &args, const CUtensorMap (&map)[4], const Info
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = kv.parts > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, attn_dkv_kernel<T, GENERAL>, map[0], map[1], map[2], map[3], kv, info);
+    e = cudaLaunchKernelEx(&cfg, attn_dkv_kernel<T, MODE>, map[0], map[1], map[2], map[3], kv, info);
     if (e != cudaSuccess) return e;
     ++*launches;
-    e = tc::launch_pdl(attn_dq_kernel<T, GENERAL>, dim3(static_cast<unsigned>(static_cast<int64_t>(q.tiles) * a.heads)),
+    e = tc::launch_pdl(attn_dq_kernel<T, MODE>, dim3(static_cast<unsigned>(static_cast<int64_t>(q.tiles) * a.heads)),
                        dim3(kThreads), layout(halves).total, s, map[0], map[1], map[2], map[3], q, info);
     if (e == cudaSuccess) ++*launches;
     return e;
+}
+
+template <typename T>
+cudaError_t launch_mode(int mode, const TileArgs &args, const CUtensorMap (&map)[4], const Info &info, int sm_count,
+                        cudaStream_t s, int *launches)
+{
+    if (mode == 0) return launch<T, 0>(args, map, info, sm_count, s, launches);
+    if (mode == kCap) return launch<T, kCap>(args, map, info, sm_count, s, launches);
+    if (mode == kBias) return launch<T, kBias>(args, map, info, sm_count, s, launches);
+    return launch<T, kCap | kBias>(args, map, info, sm_count, s, launches);
 }
 
 }  // namespace
@@ -938,12 +950,9 @@ cudaError_t launch_packed_attn_backward(const PackedAttn &p, int sm_count, const
     info.span = static_cast<int4 *>(p.workspace);
     info.lse = reinterpret_cast<float *>(info.span + info.padded);
     info.delta = info.lse + info.padded * a.heads;
-    const bool general = a.cap > 0.f || a.slopes;
-    if (bf16)
-        return general ? launch<__nv_bfloat16, true>(args, map, info, sm_count, s, launches)
-                       : launch<__nv_bfloat16, false>(args, map, info, sm_count, s, launches);
-    return general ? launch<__half, true>(args, map, info, sm_count, s, launches)
-                   : launch<__half, false>(args, map, info, sm_count, s, launches);
+    const int mode = (a.cap > 0.f ? kCap : 0) | (a.slopes ? kBias : 0);
+    return bf16 ? launch_mode<__nv_bfloat16>(mode, args, map, info, sm_count, s, launches)
+                : launch_mode<__half>(mode, args, map, info, sm_count, s, launches);
 }
 
 }  // namespace gn
