@@ -99,21 +99,50 @@ def gn_layer_norm_workspace_bytes(rows: int, cols: int) -> int:
     return int(_start()[0].gn_layer_norm_workspace_bytes(rows, cols))
 
 
-def _row_stride(shape, strides):
-    """The stride between the rows of a tensor's contiguous last axis, or None
-    if the rows do not have one between them."""
-    cols = shape[-1]
-    if strides[-1] != 1 and cols > 1:
-        return None
-    if len(shape) == 2:
-        return cols if shape[0] <= 1 else strides[0] if strides[0] >= cols else None
-    dims = [(n, s) for n, s in zip(shape[:-1], strides) if n != 1]
-    if not dims or 0 in shape:
-        return cols
+def _flat_stride(dims):
+    """The one stride of axes [(length, stride), ...], or None."""
+    dims = [(n, s) for n, s in dims if n != 1]
     for (_, outer), (n, inner) in zip(dims, dims[1:]):
         if outer != n * inner:
             return None
-    return dims[-1][1] if dims[-1][1] >= cols else None
+    return dims[-1][1] if dims else 0
+
+
+def _row_strides(shape, all_strides):
+    """(inner, (outer, stride) of each tensor, ...) of the rows of tensors of
+    one shape with contiguous last axes: inner 0 where every one has a single
+    stride between its rows, else the last but one axis' length.  None if the
+    rows have no such strides."""
+    cols = shape[-1]
+    lead, found = shape[:-1], []
+    for strides in all_strides:
+        if strides[-1] != 1 and cols > 1:
+            return None
+        stride = strides[0] if len(lead) == 1 and lead[0] != 1 else _flat_stride(list(zip(lead, strides)))
+        if stride is None:
+            break
+        found += [0, stride or cols]
+    else:
+        return 0, found
+    if len(lead) < 2:
+        return None
+    found = []
+    for strides in all_strides:
+        outer = _flat_stride(list(zip(lead[:-1], strides)))
+        if outer is None:
+            return None
+        found += [outer, strides[-2] if lead[-1] > 1 else cols]
+    return lead[-1], found
+
+
+_Strides4, _Strides6 = ctypes.c_int64 * 4, ctypes.c_int64 * 6
+
+
+def _packed_strides(shape):
+    strides = [1]
+    for n in shape[:0:-1]:
+        strides.insert(0, strides[0] * n)
+    return strides
 
 
 def _like(t, x, T) -> bool:
@@ -134,8 +163,9 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stream=No
     ``layer_norm_backward``; None when not supported.
 
     ``weight`` and ``bias`` (bias only with a weight): contiguous [C] tensors
-    of one dtype, any of the three.  x's rows need a contiguous last axis and
-    one stride between rows (a column slice of a wider tensor is fine)."""
+    of one dtype, any of the three.  x needs a contiguous last axis and one or
+    two strides between its rows: a column slice of a wider tensor is fine, and
+    so are some heads [T, H, C] of a fused projection."""
     L, T = _start()
     if not (isinstance(x, T.Tensor) and x.is_cuda):
         return None
@@ -149,18 +179,23 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stream=No
             return None
     elif bias is not None:
         return None
-    sx, sy = _row_stride(shape, x.stride()), cols
-    if out is not None:
-        sy = _row_stride(shape, out.stride()) if _like(out, x, T) else None
-    if sx is None or sy is None:
+    if out is not None and not _like(out, x, T):
         return None
+    if out is None and x.is_contiguous():
+        inner, strides = 0, (0, cols, 0, cols)
+    else:
+        y_strides = _packed_strides(shape) if out is None else out.stride()
+        rows_at = _row_strides(shape, (x.stride(), y_strides))
+        if rows_at is None:
+            return None
+        inner, strides = rows_at
 
     def go(handle):
         y = T.empty(shape, dtype=x.dtype, device=device) if out is None else out
         mean = T.empty(shape[:-1], dtype=T.float32, device=device)
         rstd = T.empty(shape[:-1], dtype=T.float32, device=device)
         rc = L.gn_layer_norm(x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                             mean.numel(), cols, sx, sy, eps, kind, wkind, handle)
+                             mean.numel(), cols, inner or max(1, mean.numel()), _Strides4(*strides), eps, kind, wkind, handle)
         return (y, mean, rstd) if rc == 0 or _finish(rc, "gn_layer_norm") else None
     return _run(device, stream, (x, weight, bias, out), go)
 
@@ -186,11 +221,12 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
         wkind = _param_format(weight, cols, device, T)
         if wkind is None:
             return None
-    sg, sx, so = _row_stride(shape, dy.stride()), _row_stride(shape, x.stride()), cols
-    if out is not None:
-        so = _row_stride(shape, out.stride()) if _like(out, x, T) else None
-    if sg is None or sx is None or so is None:
+    if out is not None and not _like(out, x, T):
         return None
+    rows_at = _row_strides(shape, (dy.stride(), x.stride(), _packed_strides(shape) if out is None else out.stride()))
+    if rows_at is None:
+        return None
+    inner, strides = rows_at
 
     def go(handle):
         dx = T.empty(shape, dtype=x.dtype, device=device) if out is None else out
@@ -202,7 +238,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
             need = max(1, L.gn_layer_norm_workspace_bytes(rows, cols))
             workspace = T.empty(need, dtype=T.uint8, device=device)
         rc = L.gn_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
-                                      dx.data_ptr(), _ptr(dw), _ptr(db), rows, cols, sg, sx, so, kind, wkind,
+                                      dx.data_ptr(), _ptr(dw), _ptr(db), rows, cols, inner or max(1, rows), _Strides6(*strides),
+                                      kind, wkind,
                                       _ptr(workspace), need, handle)
         return (dx, dw, db) if rc == 0 or _finish(rc, "gn_layer_norm_backward") else None
     return _run(device, stream, (dy, x, mean, rstd, weight, out), go)

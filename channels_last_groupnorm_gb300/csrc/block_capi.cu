@@ -81,6 +81,23 @@ int launched(cudaError_t e, int launches)
     return GN_ERR_CUDA;
 }
 
+// Rows in two levels: false if they run into one another or overflow.  A flat
+// tensor's outer stride is made to fit.
+bool norm_rows(Range *r, gn::RowsAt *at, const void *p, int64_t rows, int64_t cols, int64_t inner, const int64_t *strides,
+               size_t size)
+{
+    *at = {strides[0], strides[1]};
+    if (at->stride < cols) return false;
+    const int64_t in = rows < inner ? rows : inner;
+    if (in > 1 && at->stride > kMaxElements / in) return false;
+    if (rows <= inner) {
+        at->outer = 0;
+        return strided(r, p, rows, at->stride, 1, 0, cols, size);
+    }
+    if (at->outer < (in - 1) * at->stride + cols) return false;
+    return strided(r, p, (rows + inner - 1) / inner, at->outer, inner, at->stride, cols, size);
+}
+
 bool norm_cols_ok(int64_t cols) { return cols >= 1 && cols <= gn::kNormMaxCols; }
 
 }  // namespace
@@ -89,27 +106,28 @@ extern "C" {
 
 // ---- layer norm --------------------------------------------------------------
 int gn_layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean, float *rstd,
-                  int64_t rows, int64_t cols, int64_t x_stride, int64_t y_stride, float eps, int format,
+                  int64_t rows, int64_t cols, int64_t inner, const int64_t *strides, float eps, int format,
                   int weight_format, void *stream)
 {
-    if (rows != 0 && (!x || !y)) return GN_ERR_NULL;
+    if (!strides || (rows != 0 && (!x || !y))) return GN_ERR_NULL;
     if (bias && !weight) return GN_ERR_NULL;
     if (!format_ok(format) || (weight && !format_ok(weight_format))) return GN_ERR_FORMAT;
-    if (rows < 0) return GN_ERR_SHAPE;
+    if (rows < 0 || inner < 1 || (rows > inner && rows > UINT32_MAX)) return GN_ERR_SHAPE;
     if (!norm_cols_ok(cols)) return GN_ERR_CHANNELS;
-    if (x_stride < cols || y_stride < cols) return GN_ERR_SHAPE;
     if (!std::isfinite(eps) || eps < 0.f) return GN_ERR_EPS;
     const size_t size = format_size(format), wsize = weight ? format_size(weight_format) : 1;
     if (addr(x) % size || addr(y) % size || addr(weight) % wsize || addr(bias) % wsize || addr(mean) % 4 ||
         addr(rstd) % 4)
         return GN_ERR_ALIGN;
     Range in, out;
-    if (!strided(&in, x, rows, x_stride, 1, 0, cols, size) || !strided(&out, y, rows, y_stride, 1, 0, cols, size) ||
-        rows > kMaxElements)
+    gn::RowsAt x_at, y_at;
+    if (rows > kMaxElements || !norm_rows(&in, &x_at, x, rows, cols, inner, strides, size) ||
+        !norm_rows(&out, &y_at, y, rows, cols, inner, strides + 2, size))
         return GN_ERR_SHAPE;
     const size_t wb = wsize * static_cast<size_t>(cols), sb = 4u * static_cast<size_t>(rows);
     const Range w = {weight, wb}, b = {bias, wb}, m = {mean, sb}, r = {rstd, sb};
-    if (!(x == y && x_stride == y_stride) && overlap(out, in)) return GN_ERR_ALIAS;
+    const bool place = x == y && x_at.stride == y_at.stride && x_at.outer == y_at.outer;
+    if (!place && overlap(out, in)) return GN_ERR_ALIAS;
     for (const Range &o : {out, m, r})
         if (overlap(o, w) || overlap(o, b)) return GN_ERR_ALIAS;
     if (overlap(m, r) || overlap(m, in) || overlap(r, in) || overlap(m, out) || overlap(r, out)) return GN_ERR_ALIAS;
@@ -117,7 +135,7 @@ int gn_layer_norm(const void *x, const void *weight, const void *bias, void *y, 
     const int rc = ready(&d);
     if (rc != GN_OK) return rc;
     if (rows == 0) return GN_OK;
-    gn::NormArgs a = {x, weight, bias, y, mean, rstd, rows, static_cast<int>(cols), x_stride, y_stride, eps, format,
+    gn::NormArgs a = {x, weight, bias, y, mean, rstd, rows, static_cast<int>(cols), x_at, y_at, inner, eps, format,
                       weight_format};
     const cudaError_t e = gn::launch_layer_norm(a, d.sm_count, {wait_timeout_ns(), d.status_word, d.status_host},
                                                static_cast<cudaStream_t>(stream));
@@ -136,29 +154,32 @@ size_t gn_layer_norm_workspace_bytes(int64_t rows, int64_t cols)
 }
 
 int gn_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean, const float *rstd,
-                           void *dx, void *dweight, void *dbias, int64_t rows, int64_t cols, int64_t dy_stride,
-                           int64_t x_stride, int64_t dx_stride, int format, int weight_format, void *workspace,
+                           void *dx, void *dweight, void *dbias, int64_t rows, int64_t cols, int64_t inner,
+                           const int64_t *strides, int format, int weight_format, void *workspace,
                            size_t workspace_bytes, void *stream)
 {
+    if (!strides) return GN_ERR_NULL;
     if (rows != 0 && (!dy || !x || !mean || !rstd || !dx)) return GN_ERR_NULL;
     if (weight ? (!dweight || !dbias || !workspace) : (dweight || dbias)) return GN_ERR_NULL;
     if (!format_ok(format) || (weight && !format_ok(weight_format))) return GN_ERR_FORMAT;
-    if (rows < 0) return GN_ERR_SHAPE;
+    if (rows < 0 || inner < 1 || (rows > inner && rows > UINT32_MAX)) return GN_ERR_SHAPE;
     if (!norm_cols_ok(cols)) return GN_ERR_CHANNELS;
-    if (dy_stride < cols || x_stride < cols || dx_stride < cols) return GN_ERR_SHAPE;
     const size_t size = format_size(format), wsize = weight ? format_size(weight_format) : 1;
     if (addr(dy) % size || addr(x) % size || addr(dx) % size || addr(mean) % 4 || addr(rstd) % 4 ||
         addr(weight) % wsize || addr(dweight) % wsize || addr(dbias) % wsize || (weight && addr(workspace) % 256))
         return GN_ERR_ALIGN;
     Range g, in, out;
-    if (!strided(&g, dy, rows, dy_stride, 1, 0, cols, size) || !strided(&in, x, rows, x_stride, 1, 0, cols, size) ||
-        !strided(&out, dx, rows, dx_stride, 1, 0, cols, size) || rows > kMaxElements)
+    gn::RowsAt dy_at, x_at, dx_at;
+    if (rows > kMaxElements || !norm_rows(&g, &dy_at, dy, rows, cols, inner, strides, size) ||
+        !norm_rows(&in, &x_at, x, rows, cols, inner, strides + 2, size) ||
+        !norm_rows(&out, &dx_at, dx, rows, cols, inner, strides + 4, size))
         return GN_ERR_SHAPE;
+    const auto same = [&](const gn::RowsAt &o) { return o.stride == dx_at.stride && o.outer == dx_at.outer; };
     const size_t wb = wsize * static_cast<size_t>(cols), sb = 4u * static_cast<size_t>(rows);
     const Range w = {weight, wb}, dw = {dweight, wb}, db = {dbias, wb}, m = {mean, sb}, r = {rstd, sb};
     const Range ws = {weight ? workspace : nullptr, workspace_bytes};
-    if (!(dx == dy && dx_stride == dy_stride) && overlap(out, g)) return GN_ERR_ALIAS;
-    if (!(dx == x && dx_stride == x_stride) && overlap(out, in)) return GN_ERR_ALIAS;
+    if (!(dx == dy && same(dy_at)) && overlap(out, g)) return GN_ERR_ALIAS;
+    if (!(dx == x && same(x_at)) && overlap(out, in)) return GN_ERR_ALIAS;
     if (overlap(out, w) || overlap(out, m) || overlap(out, r) || overlap(dw, db) || overlap(ws, out) ||
         overlap(ws, dw) || overlap(ws, db) || overlap(dw, out) || overlap(db, out))
         return GN_ERR_ALIAS;
@@ -176,8 +197,8 @@ int gn_layer_norm_backward(const void *dy, const void *x, const void *weight, co
         if (e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, wb, s);
         return launched(e, 0);
     }
-    gn::NormGradArgs a = {dy, x, weight, mean, rstd, dx, dweight, dbias, rows, static_cast<int>(cols), dy_stride,
-                          x_stride, dx_stride, format, weight_format, static_cast<float *>(workspace)};
+    gn::NormGradArgs a = {dy, x, weight, mean, rstd, dx, dweight, dbias, rows, static_cast<int>(cols), dy_at,
+                          x_at, dx_at, inner, format, weight_format, static_cast<float *>(workspace)};
     int launches = 0;
     const cudaError_t e = gn::launch_layer_norm_backward(a, d.sm_count, {wait_timeout_ns(), d.status_word, d.status_host}, s,
                                                          &launches);

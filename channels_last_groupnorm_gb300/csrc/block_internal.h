@@ -21,13 +21,19 @@ struct WaitLimit {
 // ---- layer norm (norm_kernels.cu) -------------------------------------------
 constexpr int kNormMaxCols = 16384;
 
+// Where rows lie: row n = a inner + b at a outer + b stride elements (flat: n stride).
+struct RowsAt {
+    int64_t outer, stride;
+};
+
 struct NormArgs {
     const void *x, *weight, *bias;
     void *y;
     float *mean, *rstd;
     int64_t rows;
     int cols;
-    int64_t x_stride, y_stride;   // elements between rows
+    RowsAt x_at, y_at;
+    int64_t inner;                // >= rows: flat
     float eps;
     int format, weight_format;
 };
@@ -38,7 +44,8 @@ struct NormGradArgs {
     void *dx, *dweight, *dbias;
     int64_t rows;
     int cols;
-    int64_t dy_stride, x_stride, dx_stride;
+    RowsAt dy_at, x_at, dx_at;
+    int64_t inner;
     int format, weight_format;
     float *partial;               // [blocks][2][cols] when the weight's gradient is wanted
 };

@@ -96,6 +96,14 @@ __device__ __forceinline__ void store_param(void *p, int format, int c, float v)
         static_cast<__half *>(p)[c] = __float2half_rn(v);
 }
 
+// Element offset of row n (rows are counted in 32 bits where they are in two levels).
+__device__ __forceinline__ int64_t row_offset(const RowsAt &at, int64_t inner, int64_t rows, int64_t n)
+{
+    if (inner >= rows) return n * at.stride;
+    const uint32_t a = static_cast<uint32_t>(n) / static_cast<uint32_t>(inner);
+    return a * at.outer + (n - a * inner) * at.stride;
+}
+
 // The threads of one row: tpr of them (a power of two up to 32, or whole
 // warps), group g of the CTA's.
 struct Group {
@@ -292,7 +300,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Row<T, EPV, NV
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
     }
-    T *y = static_cast<T *>(a.y) + row * a.y_stride;
+    T *y = static_cast<T *>(a.y) + row_offset(a.y_at, a.inner, a.rows, row);
     const uint64_t r2 = pack2(rstd, rstd);
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
@@ -334,7 +342,7 @@ __device__ __forceinline__ void norm_grad_row(const NormGradArgs &a, const Row<T
     float s[2] = {unpack2(s0).x + unpack2(s0).y, unpack2(s1).x + unpack2(s1).y};
     row_sum(s, gr);
     if (!live) return;
-    T *dx = static_cast<T *>(a.dx) + row * a.dx_stride;
+    T *dx = static_cast<T *>(a.dx) + row_offset(a.dx_at, a.inner, a.rows, row);
     const float m0 = -s[0] * inv, m1 = -s[1] * inv;
     const uint64_t m02 = pack2(m0, m0), m12 = pack2(m1, m1);
 #pragma unroll
@@ -416,7 +424,7 @@ __global__ void __launch_bounds__(direct_threads<EPV, NV>()) norm_direct_kernel(
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * per; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * per) {
         const int64_t row = r0 + threadIdx.x / tpr;
         const bool live = row < a.rows;   // whole warps stay for the shuffles
-        const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + (live ? row : r0) * a.x_stride, gr, a.cols);
+        const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, live ? row : r0), gr, a.cols);
         norm_row(a, x, w, b, gr, row, live);
     }
 }
@@ -436,8 +444,8 @@ __global__ void __launch_bounds__(direct_threads<EPV, NV>()) norm_grad_direct_ke
         const int64_t row = r0 + threadIdx.x / tpr;
         const bool live = row < a.rows;
         const int64_t at = live ? row : r0;
-        const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + at * a.x_stride, gr, a.cols);
-        const Row<T, EPV, NV> dy(static_cast<const T *>(a.dy) + at * a.dy_stride, gr, live ? a.cols : 0);
+        const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, at), gr, a.cols);
+        const Row<T, EPV, NV> dy(static_cast<const T *>(a.dy) + row_offset(a.dy_at, a.inner, a.rows, at), gr, live ? a.cols : 0);
         norm_grad_row(a, x, dy, w, sw, sb, a.mean[at], a.rstd[at], gr, row, live);
     }
     if (!a.weight) return;
@@ -462,11 +470,11 @@ struct Stream {
     WaitLimit limit;
 };
 
-// Brings a CTA's batches: `rows` of N tensors whose rows are `stride` bytes
-// apart.  One warp; a copy per tensor where its rows lie end to end.
+// Brings a CTA's batches of N tensors' rows.  One warp; a copy per tensor where
+// its rows lie end to end.
 template <int N>
-__device__ __forceinline__ void stream_rows(const Stream &s, const char *const (&src)[N], const int64_t (&stride)[N],
-                                            int64_t rows, uint32_t ring, uint32_t full, uint32_t empty, volatile int *abort)
+__device__ __forceinline__ void stream_rows(const Stream &s, const char *const (&src)[N], const RowsAt (&at)[N],
+                                            int64_t inner, int size, int64_t rows, uint32_t ring, uint32_t full, uint32_t empty, volatile int *abort)
 {
     const int lane = threadIdx.x & 31;
     int n = 0;
@@ -483,11 +491,12 @@ __device__ __forceinline__ void stream_rows(const Stream &s, const char *const (
 #pragma unroll
         for (int t = 0; t < N; ++t) {
             const uint32_t dst = ring + st * s.stage_bytes + t * s.per * s.row_bytes;
-            if (stride[t] == s.row_bytes) {
-                if (lane == 0) bulk_load(dst, src[t] + r0 * stride[t], have * s.row_bytes, full + 8 * st);
+            if (inner >= rows && at[t].stride * size == s.row_bytes) {
+                if (lane == 0) bulk_load(dst, src[t] + r0 * s.row_bytes, have * s.row_bytes, full + 8 * st);
             } else {
                 for (int r = lane; r < have; r += 32)
-                    bulk_load(dst + r * s.row_bytes, src[t] + (r0 + r) * stride[t], s.row_bytes, full + 8 * st);
+                    bulk_load(dst + r * s.row_bytes, src[t] + row_offset(at[t], inner, rows, r0 + r) * size, s.row_bytes,
+                              full + 8 * st);
             }
         }
     }
@@ -543,9 +552,9 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
     const bool skip = sh.abort != 0;
     if (static_cast<int>(threadIdx.x) >= workers) {
         const char *const src[1] = {static_cast<const char *>(a.x)};
-        const int64_t stride[1] = {a.x_stride * static_cast<int64_t>(sizeof(T))};
+        const RowsAt at[1] = {a.x_at};
         if (!skip)
-            stream_rows<1>(s, src, stride, a.rows, smem_addr(ring), smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
+            stream_rows<1>(s, src, at, a.inner, sizeof(T), a.rows, smem_addr(ring), smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
         return;
     }
     if (skip) return;
@@ -589,9 +598,9 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
     uint64_t sw[NV * EPV / 2] = {}, sb[NV * EPV / 2] = {};
     if (static_cast<int>(threadIdx.x) >= workers) {
         const char *const src[2] = {static_cast<const char *>(a.x), static_cast<const char *>(a.dy)};
-        const int64_t stride[2] = {a.x_stride * static_cast<int64_t>(sizeof(T)), a.dy_stride * static_cast<int64_t>(sizeof(T))};
+        const RowsAt at[2] = {a.x_at, a.dy_at};
         if (!skip)
-            stream_rows<2>(s, src, stride, a.rows, smem_addr(ring), smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
+            stream_rows<2>(s, src, at, a.inner, sizeof(T), a.rows, smem_addr(ring), smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
     } else if (!skip) {
         if (s.tpr > 32) gr.scratch = sh.scratch[gr.g];
         const Own<EPV, NV, false> w(a.weight ? weight : nullptr, GN_FORMAT_FP32, gr, a.cols, 1.f);
@@ -664,7 +673,7 @@ bool vectors_ok(int cols, int epv, const void *const *ptrs, int n, const int64_t
 {
     if (cols % epv) return false;
     for (int i = 0; i < n; ++i)
-        if (reinterpret_cast<uintptr_t>(ptrs[i]) % 16 || strides[i] % epv) return false;
+        if (reinterpret_cast<uintptr_t>(ptrs[i]) % 16 || strides[2 * i] % epv || strides[2 * i + 1] % epv) return false;
     return true;
 }
 
@@ -759,7 +768,7 @@ cudaError_t forward(const NormArgs &a, int sm_count, const WaitLimit &limit, cud
 {
     constexpr int EPV = 16 / sizeof(T);
     const void *ptrs[] = {a.x, a.y};
-    const int64_t strides[] = {a.x_stride, a.y_stride};
+    const int64_t strides[] = {a.x_at.outer, a.x_at.stride, a.y_at.outer, a.y_at.stride};
     const bool vec = vectors_ok(a.cols, EPV, ptrs, 2, strides);
     if (vec) {
         int nv;
@@ -781,7 +790,7 @@ cudaError_t backward(const NormGradArgs &a, int sm_count, const WaitLimit &limit
 {
     constexpr int EPV = 16 / sizeof(T);
     const void *ptrs[] = {a.x, a.dy, a.dx};
-    const int64_t strides[] = {a.x_stride, a.dy_stride, a.dx_stride};
+    const int64_t strides[] = {a.x_at.outer, a.x_at.stride, a.dy_at.outer, a.dy_at.stride, a.dx_at.outer, a.dx_at.stride};
     const bool vec = vectors_ok(a.cols, EPV, ptrs, 3, strides);
     if (vec) {
         int nv;

@@ -86,11 +86,11 @@ EXPORTS = {
                        + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "gn_attn_folded_ex": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int64] * 2
                           + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p]),
-    "gn_layer_norm": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int64] * 4
-                      + [ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "gn_layer_norm": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int64] * 3
+                      + [ctypes.c_void_p, ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
     "gn_layer_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 2),
-    "gn_layer_norm_backward": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_int64] * 5
-                               + [ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "gn_layer_norm_backward": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_int64] * 3
+                               + [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "gn_rope_nd": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int64] * 4
                    + [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_double,
                       ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),

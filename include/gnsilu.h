@@ -472,20 +472,25 @@ int gn_attn_folded_ex(const void *q_bf16, const void *k_bf16, const void *xn_bf1
 
 /* Layer norm.
  *   x, y       : DEVICE rows of cols elements, `format` (enum gn_half_format,
- *                all three), x_stride / y_stride elements from one row to the
- *                next (>= cols).  y may equal x with the same stride.
+ *                all three).  Row n = a inner + b lies a outer + b stride
+ *                elements on (the heads of a slice of a fused projection); with
+ *                inner >= rows there is only the one stride.  y may equal x with
+ *                the same strides.
+ *   strides    : HOST [4], elements: outer and stride of x, outer and stride of y
+ *                (stride >= cols; outer >= (inner - 1) stride + cols where rows >
+ *                inner).
  *   weight, bias : DEVICE [cols] of weight_format, or both NULL; bias alone may
  *                be NULL.
  *   mean, rstd : DEVICE fp32 [rows], written for the backward pass, or NULL.
- *   rows >= 0 (0: nothing to do), 1 <= cols <= 16384.  Rows of whole 16-byte
+ *   rows >= 0 (0: nothing to do), inner >= 1, 1 <= cols <= 16384.  Rows of whole 16-byte
  *   vectors (pointers and strides too) are read and written in such vectors.
  * Asynchronous on `stream`.  Errors: GN_ERR_NULL, GN_ERR_FORMAT, GN_ERR_SHAPE
- * (rows < 0, a stride below cols, sizes overflow), GN_ERR_CHANNELS (cols),
+ * (rows < 0, inner < 1, strides that run rows into one another, sizes overflow), GN_ERR_CHANNELS (cols),
  * GN_ERR_EPS, GN_ERR_ALIGN (a pointer not a multiple of its element's size),
  * GN_ERR_ALIAS (an output overlapping an input or another output, but for
  * y == x), GN_ERR_DEVICE, GN_ERR_KERNEL, GN_ERR_CUDA. */
 int gn_layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean, float *rstd,
-                  int64_t rows, int64_t cols, int64_t x_stride, int64_t y_stride, float eps, int format,
+                  int64_t rows, int64_t cols, int64_t inner, const int64_t *strides, float eps, int format,
                   int weight_format, void *stream);
 
 /* Workspace bytes gn_layer_norm_backward() needs with a weight on the CURRENT
@@ -494,8 +499,9 @@ int gn_layer_norm(const void *x, const void *weight, const void *bias, void *y, 
 size_t gn_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
 
 /* Backward pass of gn_layer_norm().
- *   dy, x, dx  : DEVICE rows as above, each with its own stride; dx may equal
- *                dy or x with the same stride.
+ *   dy, x, dx  : DEVICE rows as above; dx may equal dy or x with the same
+ *                strides.
+ *   strides    : HOST [6]: outer and stride of dy, of x and of dx.
  *   mean, rstd : from gn_layer_norm().
  *   weight     : DEVICE [cols], or NULL; with it dweight and dbias (DEVICE
  *                [cols] of weight_format) are written, with none they are NULL.
@@ -505,8 +511,8 @@ size_t gn_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
  *   rows >= 0 (0: dweight and dbias are set to zero).
  * Asynchronous on `stream`.  Errors: as above, and GN_ERR_WORKSPACE. */
 int gn_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean, const float *rstd,
-                           void *dx, void *dweight, void *dbias, int64_t rows, int64_t cols, int64_t dy_stride,
-                           int64_t x_stride, int64_t dx_stride, int format, int weight_format, void *workspace,
+                           void *dx, void *dweight, void *dbias, int64_t rows, int64_t cols, int64_t inner,
+                           const int64_t *strides, int format, int weight_format, void *workspace,
                            size_t workspace_bytes, void *stream);
 
 /* ---- rotary positions over several axes ---------------------------------------

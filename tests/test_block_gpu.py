@@ -102,6 +102,29 @@ def test_layer_norm_of_column_slices(cols, start, wide, dtype):
         br.check(got, *want[name], name)
 
 
+@pytest.mark.parametrize("tokens,heads,cols,dtype", [(3, 5, 64, BF), (700, 24, 128, FP), (9, 1, 40, F32), (4000, 8, 72, BF),
+                                                     (1, 7, 33, F32)])
+def test_layer_norm_of_some_heads_of_a_projection(tokens, heads, cols, dtype):
+    """Rows with two strides: [tokens, heads, cols] slices of a wider tensor."""
+    qkv, grads = rand((tokens, heads + 3, cols), dtype, 1, 2.0, 1.0), rand((tokens, heads + 1, cols), dtype, 2)
+    x, dy = qkv[:, 2:2 + heads], grads[:, :heads]
+    w, b = rand((cols,), F32, 3, 0.2, 1.0), rand((cols,), F32, 4)
+    y, mean, rstd = gn.layer_norm(x, w, b)
+    dx, dw, db = gn.layer_norm_backward(dy, x, mean, rstd, w)
+    assert y.is_contiguous() and mean.shape == (tokens, heads)
+    want = br.layer_norm(x.reshape(-1, cols), w, b, 1e-6, dy.reshape(-1, cols))
+    got = dict(y=y.view(-1, cols), mean=mean.view(-1), rstd=rstd.view(-1), dx=dx.view(-1, cols), dw=dw, db=db)
+    for name, (value, bound) in want.items():
+        br.check(got[name], value, bound, name)
+    # in place, and onto slices of another tensor
+    keep = qkv.clone()
+    assert gn.layer_norm(x, w, b, out=x)[0] is x
+    assert torch.equal(x, y) and torch.equal(qkv[:, :2], keep[:, :2]) and torch.equal(qkv[:, 2 + heads:], keep[:, 2 + heads:])
+    onto = torch.zeros((tokens, heads + 1, cols), dtype=dtype, device="cuda")
+    gn.layer_norm_backward(dy, keep[:, 2:2 + heads], mean, rstd, w, out=onto[:, 1:])
+    assert torch.equal(onto[:, 1:], dx) and not onto[:, 0].any()
+
+
 def test_layer_norm_shapes_in_place_and_repeated():
     x = rand((3, 5, 7, 256), BF, 9, 2.0, 3.0)
     w, b = rand((256,), BF, 10), rand((256,), BF, 11)

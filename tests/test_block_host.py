@@ -26,8 +26,9 @@ def built():
 def norm(**kw):
     a = dict(x=A, w=B, b=C, y=D, mean=E, rstd=F, rows=16, cols=64, xs=64, ys=64, eps=1e-6, fmt=0, wfmt=2)
     a.update(kw)
-    return gs.lib().gn_layer_norm(a["x"], a["w"], a["b"], a["y"], a["mean"], a["rstd"], a["rows"], a["cols"], a["xs"],
-                                  a["ys"], a["eps"], a["fmt"], a["wfmt"], None)
+    strides = (ctypes.c_int64 * 4)(a.get("xo", 0), a["xs"], a.get("yo", 0), a["ys"])
+    return gs.lib().gn_layer_norm(a["x"], a["w"], a["b"], a["y"], a["mean"], a["rstd"], a["rows"], a["cols"],
+                                  a.get("inner", 1 << 40), strides, a["eps"], a["fmt"], a["wfmt"], None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -36,6 +37,9 @@ def norm(**kw):
     (dict(rows=-1), gs.GN_ERR_SHAPE), (dict(cols=0), gs.GN_ERR_CHANNELS), (dict(cols=16385, xs=S, ys=S), gs.GN_ERR_CHANNELS),
     (dict(xs=63), gs.GN_ERR_SHAPE), (dict(ys=0), gs.GN_ERR_SHAPE), (dict(rows=1 << 60), gs.GN_ERR_SHAPE),
     (dict(xs=1 << 62), gs.GN_ERR_SHAPE),
+    (dict(inner=0), gs.GN_ERR_SHAPE), (dict(inner=4, xo=100, yo=256), gs.GN_ERR_SHAPE),
+    (dict(inner=4, xo=256, yo=255), gs.GN_ERR_SHAPE), (dict(inner=4, rows=1 << 33, xo=256, yo=256), gs.GN_ERR_SHAPE),
+    (dict(inner=4, xo=512, yo=512, y=A + 256), gs.GN_ERR_ALIAS),
     (dict(eps=math.nan), gs.GN_ERR_EPS), (dict(eps=-1.0), gs.GN_ERR_EPS), (dict(eps=math.inf), gs.GN_ERR_EPS),
     (dict(x=A + 1), gs.GN_ERR_ALIGN), (dict(y=D + 1), gs.GN_ERR_ALIGN), (dict(w=B + 2), gs.GN_ERR_ALIGN),
     (dict(mean=E + 2), gs.GN_ERR_ALIGN), (dict(fmt=2, x=A + 2), gs.GN_ERR_ALIGN),
@@ -51,7 +55,8 @@ def norm_grad(**kw):
              ws=H, wsb=1 << 30)
     a.update(kw)
     return gs.lib().gn_layer_norm_backward(a["dy"], a["x"], a["w"], a["mean"], a["rstd"], a["dx"], a["dw"], a["db"],
-                                           a["rows"], a["cols"], a["gs"], a["xs"], a["ds"], a["fmt"], a["wfmt"],
+                                           a["rows"], a["cols"], a.get("inner", 1 << 40),
+                                           (ctypes.c_int64 * 6)(0, a["gs"], 0, a["xs"], 0, a["ds"]), a["fmt"], a["wfmt"],
                                            a["ws"], a["wsb"], None)
 
 
