@@ -89,6 +89,8 @@ struct PackedAttn {
 // On the tensor cores (pattn_forward.cu); tokens_q and tokens_k at least 1.
 cudaError_t launch_packed_attn_tiles(const PackedAttn &p, const WaitLimit &limit, cudaStream_t s);
 // On the tensor cores for few queries per document (pattn_split.cu); tokens_q and tokens_k at least 1.
+// (about how long that takes, for the choice between the two)
+double packed_attn_split_us(const PackedAttn &p, int sm_count);
 cudaError_t launch_packed_attn_split(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s);
 cudaError_t launch_packed_attn(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s, int *launches);
 size_t packed_attn_workspace_bytes(int64_t tokens_q, int heads);

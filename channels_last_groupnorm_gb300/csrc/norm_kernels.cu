@@ -38,15 +38,6 @@
 namespace gn {
 namespace {
 
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-
-template <typename T> __device__ __forceinline__ T from_float(float v);
-template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
-
 // A word of two half-precision values (fp32 rows have no use for it).
 template <typename T> __device__ __forceinline__ float2 unpack_word(uint32_t v) { return Half2<T>::unpack(v); }
 template <> __device__ __forceinline__ float2 unpack_word<float>(uint32_t) { return make_float2(0.f, 0.f); }
@@ -698,18 +689,6 @@ Stream stream_shape(int64_t rows, int cols, int size, int tensors, size_t fixed,
         rows < static_cast<int64_t>(4) * sm_count * s.per)
         s.stages = 0;
     return s;
-}
-
-// Lets `kernel` have `bytes` of dynamic shared memory, once per device.
-cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<uint64_t> &done)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    const uint64_t bit = 1ull << (dev & 63);
-    if (e != cudaSuccess || (dev < 64 && (done.load() & bit))) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e == cudaSuccess) done.fetch_or(bit);
-    return e;
 }
 
 constexpr size_t kStreamFixed = (sizeof(StreamShared) + 127) / 128 * 128;

@@ -9,7 +9,7 @@
 //   dq_i = scale sum_j ds_ij k_j, dk_j = scale sum_i ds_ij q_i, dv_j = sum_i p_ij dout_i
 // with dk and dv summed over the query heads that share a key / value head.
 // A query that sees no key has out = 0, lse = -inf and adds nothing to any
-// gradient.  Keys outside a query's run are never read for it.
+// gradient; what keys outside its run hold has no influence on it.
 #include <algorithm>
 
 #include "pattn_common.cuh"
@@ -29,20 +29,31 @@ __global__ void __launch_bounds__(256) attn_nothing_kernel(const gn_attn_packed_
     for (int64_t i = first; i < n * a.dim / 8; i += step) static_cast<uint4 *>(a.out)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// About how long the kernel with tiles of 256 queries of one head takes, in us:
+// a tile meets the keys of every document that it touches, 1.6 us for a block of
+// 128, and about 4 us besides, one tile per SM at a time.  Few queries per
+// document make that long, and the splitting kernel, which reads the keys once
+// for all heads that share them, the better one (24 caches of up to 8000 keys, 32
+// heads on 8: 1 new token each 75 against 1031 us, 16 each 157 against 1031 us);
+// for many short documents of many queries it is the other way round.
+double tiles_us(const PackedAttn &p, int sm_count)
+{
+    const gn_attn_packed_args &a = p.a;
+    const double per_doc = static_cast<double>(a.tokens_q) / a.docs, keys = static_cast<double>(a.tokens_k) / a.docs;
+    const int64_t tiles = (a.tokens_q + 255) / 256 * a.heads;
+    const double blocks = std::max(1.0, 256.0 / std::max(per_doc, 1.0 / 256)) * keys / 128 + 1;
+    return static_cast<double>((tiles + sm_count - 1) / sm_count) * (4.0 + 1.6 * blocks);
+}
+
 }  // namespace
 
 cudaError_t launch_packed_attn(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s, int *launches)
 {
     const gn_attn_packed_args &a = p.a;
     cudaError_t e;
-    // Few queries per document (with all heads that share its keys no more than
-    // one tile's 128 rows): the keys are split and read once for all of them.
-    // Else tiles of 128 queries of one head.  24 caches of up to 8000 keys, 32
-    // heads on 8: 1 token each 85 against 1031 us (the tiles pack neighbouring
-    // documents and meet every one's keys), 16 tokens each 165 against 1031 us.
     if (a.tokens_k == 0)
         e = tc::launch_pdl(attn_nothing_kernel, dim3(static_cast<unsigned>(sm_count)), dim3(256), 0, s, a);
-    else if ((a.tokens_q + a.docs - 1) / a.docs * std::min(p.group, 128) <= 128)
+    else if (packed_attn_split_us(p, sm_count) < tiles_us(p, sm_count))
         e = launch_packed_attn_split(p, sm_count, limit, s);
     else
         e = launch_packed_attn_tiles(p, limit, s);

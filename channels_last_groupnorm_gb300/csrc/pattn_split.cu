@@ -697,24 +697,25 @@ cudaError_t launch(const SplitArgs &args, const CUtensorMap &mq, const CUtensorM
     return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, args);
 }
 
-}  // namespace
-
-cudaError_t launch_packed_attn_split(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s)
+// A call's tiles and splits, and about how long it takes (us).
+//
+// Splits: the number that should end first.  CTAs run in rounds of two per SM,
+// and one takes as long as its blocks and about seven more (start, first loads
+// and join: 9 us where a block of its stream takes 1.3 us, or 2.2 us with more
+// than 32 rows); documents are taken for half as long again as their average,
+// since the longest ends last.  (24 caches of 2880 keys, 8 heads: 192 tiles, 3
+// splits: two rounds.)
+SplitArgs plan(const PackedAttn &p, int sm_count, double *us)
 {
     const gn_attn_packed_args &a = p.a;
     SplitArgs args = {};
     args.p = p;
     args.scale_log2 = a.scale * kLog2e;
-    args.limit = limit;
     args.heads = std::min(p.group, kTile);
     args.chunks = (p.group + args.heads - 1) / args.heads;
     const int64_t per_doc = (a.tokens_q + a.docs - 1) / a.docs;
     args.tokens = static_cast<int>(std::min<int64_t>(kTile / args.heads, per_doc));
-    // Splits: the number that should end first.  CTAs run in rounds of two per
-    // SM, and one takes as long as its blocks and about seven more (start, first
-    // loads and join: 9 us where a block of its stream takes 1.3 us); documents
-    // are taken for half as long again as their average, since the longest ends
-    // last.  (24 caches of 2880 keys, 8 heads: 192 tiles, 3 splits: two rounds.)
+    args.stages = a.dim > 64 ? 3 : 5;      // (two CTAs' shared memory fits an SM)
     const int64_t tiles = (a.tokens_q + args.tokens - 1) / args.tokens * a.kv_heads * args.chunks;
     const double blocks = 1.5 * static_cast<double>(a.tokens_k) / a.docs / kTile;
     double best = 0.0;
@@ -725,7 +726,25 @@ cudaError_t launch_packed_attn_split(const PackedAttn &p, int sm_count, const Wa
             args.splits = s;
         }
     }
-    args.stages = a.dim > 64 ? 3 : 5;      // (two CTAs' shared memory fits an SM)
+    *us = best * (args.tokens * args.heads > 32 ? 2.2 : 1.3);
+    return args;
+}
+
+}  // namespace
+
+double packed_attn_split_us(const PackedAttn &p, int sm_count)
+{
+    double us;
+    plan(p, sm_count, &us);
+    return us;
+}
+
+cudaError_t launch_packed_attn_split(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s)
+{
+    const gn_attn_packed_args &a = p.a;
+    double us;
+    SplitArgs args = plan(p, sm_count, &us);
+    args.limit = limit;
     const bool bf16 = a.format == GN_FORMAT_BF16;
     CUtensorMap mq, mk, mv;
     if (!encode_heads(&mq, a.q, bf16, a.tokens_q, a.q_token, a.heads, a.q_head, a.dim, args.heads, args.tokens) ||

@@ -496,18 +496,6 @@ __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t count, bool pred)
     return r != 0;
 }
 
-// Lets `kernel` have `bytes` of dynamic shared memory, once per device.
-inline cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<uint64_t> &done)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    const uint64_t bit = 1ull << (dev & 63);
-    if (e != cudaSuccess || (dev < 64 && (done.load() & bit))) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e == cudaSuccess) done.fetch_or(bit);
-    return e;
-}
-
 // Lets `kernel` run in clusters of more than eight CTAs, once per device.
 inline cudaError_t allow_clusters(const void *kernel, std::atomic<uint64_t> &done)
 {

@@ -20,21 +20,13 @@
 #include <cstdint>
 
 #include "block_internal.h"
+#include "block_math.cuh"
 #include "tc_common.cuh"
 
 namespace gn {
 namespace {
 
 constexpr int kRopeThreads = 256;
-
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-
-template <typename T> __device__ __forceinline__ T from_float(float v);
-template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Pack {

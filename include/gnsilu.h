@@ -33,7 +33,10 @@
  * (gn_residual_gate_add), the fused nearest-2x upsample + 3x3 convolution
  * (gn_upconv_fold, gn_upconv_nhwc) and the single-head attention with its
  * output projection folded into V (gn_attn_fold, gn_attn_folded); the last
- * two run on the tensor cores.
+ * two run on the tensor cores.  Three operators of a transformer block over
+ * packed images and texts, forward and backward, stand beside them: layer norm
+ * (gn_layer_norm), rotary positions over several axes (gn_rope_nd) and attention
+ * of packed documents (gn_attn_packed).
  *
  * Memory and streams: every pointer argument is a DEVICE pointer owned by
  * the caller; the library never frees caller memory.  x and y are bf16
