@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(256) attn_nothing_kernel(const gn_attn_packed_
 // 128, and about 4 us besides, one tile per SM at a time.  Few queries per
 // document make that long, and the splitting kernel, which reads the keys once
 // for all heads that share them, the better one (24 caches of up to 8000 keys, 32
-// heads on 8: 1 new token each 75 against 1031 us, 16 each 157 against 1031 us);
+// heads on 8: 1 new token each 77 against 1568 us, 16 each 158 against 1046 us);
 // for many short documents of many queries it is the other way round.
 double tiles_us(const PackedAttn &p, int sm_count)
 {

@@ -108,8 +108,8 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
 
 // The products are issued by one warp, the waits ahead of them are done by
 // another: an mbarrier wait by a thread with products in flight only returns
-// when they are done (with both in one warp the forward pass took 252 us where
-// it takes 200).  Both warps run the same loop; the waiter waits, then both meet
+// when they are done (2 x 4096 tokens, 19 heads, D = 128: 252 us forward with
+// both in one warp, 216 us so).  Both warps run the same loop; the waiter waits, then both meet
 // at a named barrier, then the issuer goes on.  A wait that runs out sets the
 // abort flag, after which the waiter's waits return at once and the issuer runs
 // on over whatever is there: wrong values of a call that is reported as failed,
