@@ -307,10 +307,10 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Row<T, EPV, NV
 // One row of the backward pass from registers: dx out, column sums on.  (Past
 // the row's end dy is zero and adds nothing; so is all of it for a row that is
 // not there.)
-template <typename T, int EPV, int NV, typename Params>
+template <typename T, int EPV, int NV, typename Params, typename After>
 __device__ __forceinline__ void norm_grad_row(const NormGradArgs &a, const Row<T, EPV, NV> &x, const Row<T, EPV, NV> &dy,
                                               const Params &w, uint64_t (&sw)[NV * EPV / 2], uint64_t (&sb)[NV * EPV / 2],
-                                              float mean, float rstd, Group &gr, int64_t row, bool live)
+                                              float mean, float rstd, Group &gr, int64_t row, bool live, const After &after)
 {
     constexpr int kEach = EPV == 1 ? 1 : EPV / 2, kGroups = Row<T, EPV, NV>::kPairs / kEach;
     const float inv = 1.0f / static_cast<float>(a.cols);
@@ -332,6 +332,7 @@ __device__ __forceinline__ void norm_grad_row(const NormGradArgs &a, const Row<T
     }
     float s[2] = {unpack2(s0).x + unpack2(s0).y, unpack2(s1).x + unpack2(s1).y};
     row_sum(s, gr);
+    after();                              // (every thread of the row holds its elements in registers)
     if (!live) return;
     T *dx = static_cast<T *>(a.dx) + row_offset(a.dx_at, a.inner, a.rows, row);
     const float m0 = -s[0] * inv, m1 = -s[1] * inv;
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(direct_threads<EPV, NV>()) norm_grad_direct_ke
         const int64_t at = live ? row : r0;
         const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, at), gr, a.cols);
         const Row<T, EPV, NV> dy(static_cast<const T *>(a.dy) + row_offset(a.dy_at, a.inner, a.rows, at), gr, live ? a.cols : 0);
-        norm_grad_row(a, x, dy, w, sw, sb, a.mean[at], a.rstd[at], gr, row, live);
+        norm_grad_row(a, x, dy, w, sw, sb, a.mean[at], a.rstd[at], gr, row, live, [] {});
     }
     if (!a.weight) return;
     gr.g = threadIdx.x / tpr;
@@ -566,11 +567,11 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
     }
 }
 
-template <typename T, int NV>
+template <typename T>
 __global__ void __launch_bounds__(kStreamThreads + 32, 1)
     norm_grad_stream_kernel(const __grid_constant__ NormGradArgs a, const __grid_constant__ Stream s)
 {
-    constexpr int EPV = 16 / sizeof(T);
+    constexpr int EPV = 16 / sizeof(T), NV = 2;
     extern __shared__ __align__(128) uint8_t smem[];
     StreamShared &sh = *reinterpret_cast<StreamShared *>(smem);
     float *weight = reinterpret_cast<float *>(smem + (sizeof(StreamShared) + 127) / 128 * 128);
@@ -615,12 +616,91 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
                 st = 0;
                 parity ^= 1;
             }
-            norm_grad_row(a, x, dy, w, sw, sb, mean_now, rstd_now, gr, row, row < a.rows);
+            norm_grad_row(a, x, dy, w, sw, sb, mean_now, rstd_now, gr, row, row < a.rows, [] {});
         }
     }
     if (!a.weight) return;
     __syncthreads();                      // every copy has landed, every row is done: the ring is free
     write_partial<EPV, NV>(a, sw, sb, gr, workers, reinterpret_cast<float *>(ring));
+}
+
+// The same for a row that 384 threads with two slots do not hold: four slots a
+// thread, one row per batch, and no loader warp.  The barrier of a row's sums
+// says that its stage has been read, and thread 0 then fills the stage again.
+// With a loader warp the CTA's 13 warps are given registers as 16, 128 a thread,
+// and the column sums spill beside a ring that leaves little L1; 12 warps may
+// have 168 (bf16, weight in fp32, with the kernel that adds the columns up: 4608 x
+// 12288 173 us with a loader warp, 120 us so, 4608 x 8192 118 and 99 us; fp32,
+// which does not spill either way, 4608 x 4096 57 and 58 us).  768 threads with
+// two slots spill as well (181 us).
+template <typename T>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    norm_grad_wide_kernel(const __grid_constant__ NormGradArgs a, const __grid_constant__ Stream s)
+{
+    constexpr int EPV = 16 / sizeof(T), NV = 4;
+    extern __shared__ __align__(128) uint8_t smem[];
+    StreamShared &sh = *reinterpret_cast<StreamShared *>(smem);
+    float *weight = reinterpret_cast<float *>(smem + (sizeof(StreamShared) + 127) / 128 * 128);
+    uint8_t *ring = reinterpret_cast<uint8_t *>(weight) + (a.weight ? (4 * a.cols + 127) / 128 * 128 : 0);
+    stream_setup(sh, s, s.tpr);
+    if (a.weight)
+        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            float one[1];
+            load_params<1>(a.weight, a.weight_format, c, one);
+            weight[c] = one[0];
+        }
+    __syncthreads();
+    const bool skip = sh.abort != 0;
+    Group gr = {s.tpr, 0, static_cast<int>(threadIdx.x), sh.scratch[0], 0};
+    uint64_t sw[NV * EPV / 2] = {}, sb[NV * EPV / 2] = {};
+    if (!skip) {
+        int issued = 0, fill = 0;             // copies begun, and the stage of the next (thread 0)
+        int64_t next = blockIdx.x;
+        const auto load = [&] {
+            if (next >= a.rows) return;
+            const uint32_t full = smem_addr(&sh.full[fill]), to = smem_addr(ring) + fill * s.stage_bytes;
+            mbar_arrive_expect_tx(full, 2 * s.row_bytes);
+            bulk_load(to, static_cast<const char *>(a.x) + row_offset(a.x_at, a.inner, a.rows, next) * sizeof(T), s.row_bytes, full);
+            bulk_load(to + s.row_bytes, static_cast<const char *>(a.dy) + row_offset(a.dy_at, a.inner, a.rows, next) * sizeof(T),
+                      s.row_bytes, full);
+            next += gridDim.x;
+            ++issued;
+            if (++fill == s.stages) fill = 0;
+        };
+        if (threadIdx.x == 0)
+            for (int i = 0; i < s.stages; ++i) load();
+        const Own<EPV, NV, false> w(a.weight ? weight : nullptr, GN_FORMAT_FP32, gr, a.cols, 1.f);
+        int64_t row = blockIdx.x;
+        // (the statistics are asked for a row ahead)
+        float mean = row < a.rows ? __ldg(a.mean + row) : 0.f, rstd = row < a.rows ? __ldg(a.rstd + row) : 0.f;
+        int st = 0, parity = 0;
+        bool good = true;
+        for (; row < a.rows; row += gridDim.x) {
+            const float mean_now = mean, rstd_now = rstd;
+            if (row + gridDim.x < a.rows) {
+                mean = __ldg(a.mean + row + gridDim.x);
+                rstd = __ldg(a.rstd + row + gridDim.x);
+            }
+            // (after a wait that ran out nothing more is asked for)
+            good = tc::wait(smem_addr(&sh.full[st]), parity, &sh.abort, s.limit.timeout_ns, s.limit.status, s.limit.host_status) && good;
+            const uint8_t *at = ring + st * s.stage_bytes;
+            const Row<T, EPV, NV> x(reinterpret_cast<const T *>(at), gr, a.cols);
+            const Row<T, EPV, NV> dy(reinterpret_cast<const T *>(at + s.row_bytes), gr, a.cols);
+            if (++st == s.stages) {
+                st = 0;
+                parity ^= 1;
+            }
+            norm_grad_row(a, x, dy, w, sw, sb, mean_now, rstd_now, gr, row, true, [&] {
+                if (threadIdx.x == 0 && good) load();
+            });
+        }
+        // what is still in flight lands before the CTA ends
+        if (threadIdx.x == 0 && !good)
+            for (int k = max(0, issued - s.stages); k < issued; ++k)
+                tc::drain(smem_addr(&sh.full[k % s.stages]), (k / s.stages) & 1, s.limit.timeout_ns);
+    }
+    if (!a.weight) return;
+    write_partial<EPV, NV>(a, sw, sb, gr, s.tpr, nullptr);    // (one row at a time: nothing to add up)
 }
 
 // dw and db from the CTAs' partial sums: a warp's lanes take 32 neighbouring
@@ -674,7 +754,7 @@ bool vectors_ok(int cols, int epv, const void *const *ptrs, int n, const int64_t
 // the forward pass, which has no column sums to keep, four of a row longer than
 // a warp's two.  With one slot (24 warps on a row of 6144) the reductions'
 // instructions took longer than the row's memory does (62 us forward for 4608 x
-// 6144), and with four in the backward pass the sums spilled (143 us).
+// 6144); with four the backward pass has a kernel of its own.
 Stream stream_shape(int64_t rows, int cols, int size, int tensors, size_t fixed, int sm_count, int *nv)
 {
     Stream s = {};
@@ -713,16 +793,26 @@ cudaError_t forward_stream(const NormArgs &a, const Stream &s, int sm_count, cud
                           kStreamFixed + s.stages * s.stage_bytes, st, a, s);
 }
 
-template <typename T, int NV>
+template <typename T>
 cudaError_t backward_stream(const NormGradArgs &a, const Stream &s, int sm_count, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_grad_stream_kernel<T, NV>), kStreamBytes, done);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_grad_stream_kernel<T>), kStreamBytes, done);
     if (e != cudaSuccess) return e;
-    // (with at most four slots a thread the column sums take at most 98 KB)
+    // (384 threads with two slots of 16 bytes: the column sums take at most 48 KB)
     const size_t ring = std::max<size_t>(s.stages * s.stage_bytes, columns_bytes(a, s.tpr, s.per * s.tpr));
-    return tc::launch_pdl(norm_grad_stream_kernel<T, NV>, dim3(static_cast<unsigned>(sm_count)), dim3(s.per * s.tpr + 32),
+    return tc::launch_pdl(norm_grad_stream_kernel<T>, dim3(static_cast<unsigned>(sm_count)), dim3(s.per * s.tpr + 32),
                           kStreamFixed + weight_copy(a) + ring, st, a, s);
+}
+
+template <typename T>
+cudaError_t backward_wide(const NormGradArgs &a, const Stream &s, int sm_count, cudaStream_t st)
+{
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_grad_wide_kernel<T>), kStreamBytes, done);
+    if (e != cudaSuccess) return e;
+    return tc::launch_pdl(norm_grad_wide_kernel<T>, dim3(static_cast<unsigned>(sm_count)), dim3(s.tpr),
+                          kStreamFixed + weight_copy(a) + s.stages * s.stage_bytes, st, a, s);
 }
 
 // The direct form: up to nv slots a thread, a row's threads one CTA or, for
@@ -777,7 +867,7 @@ cudaError_t backward(const NormGradArgs &a, int sm_count, const WaitLimit &limit
         st.limit = limit;
         if (st.stages) {
             *blocks = sm_count;
-            return nv == 2 ? backward_stream<T, 2>(a, st, sm_count, s) : backward_stream<T, 4>(a, st, sm_count, s);
+            return nv == 2 ? backward_stream<T>(a, st, sm_count, s) : backward_wide<T>(a, st, sm_count, s);
         }
     }
     const Direct d = direct_shape(vec ? a.cols / EPV : a.cols, vec);

@@ -89,6 +89,25 @@ def test_layer_norm_many_rows(rows, cols, wide, dtype):
         assert all(p is q or torch.equal(p, q) for p, q in zip(again, (dx, dw, db)))
 
 
+@pytest.mark.parametrize("rows,cols,wide,dtype", [
+    (613, 6152, 6152, BF), (1217, 6400, 6416, FP), (1500, 12288, 12296, BF), (608, 9000, 9000, FP), (700, 6144, 6144, F32),
+    (1999, 3080, 3092, F32)])
+def test_layer_norm_wide_rows_backward(rows, cols, wide, dtype):
+    """Rows of which the backward pass holds four slots a thread: one batch short of and past the ring's turns."""
+    x = rand((rows, wide), dtype, 5, 2.0, 1.0)[:, :cols]
+    dy = rand((rows, wide), dtype, 6)[:, :cols]
+    for w, b in ((rand((cols,), F32, 7, 0.3, 1.0), rand((cols,), F32, 8)), (None, None)):
+        y, mean, rstd = gn.layer_norm(x, w, b)
+        dx, dw, db = gn.layer_norm_backward(dy, x, mean, rstd, w)
+        got = dict(y=y, mean=mean, rstd=rstd, dx=dx, dw=dw, db=db)
+        for name, (value, bound) in br.layer_norm(x, w, b, 1e-6, dy).items():
+            br.check(got[name], value, bound, name)
+        # in place over dy, and the same bits again
+        onto = dy.clone()
+        again = gn.layer_norm_backward(onto, x, mean, rstd, w, out=onto)
+        assert all(p is q or torch.equal(p, q) for p, q in zip(again, (dx, dw, db)))
+
+
 @pytest.mark.parametrize("cols,start,wide", [(64, 0, 64 + 8), (64, 3, 80), (129, 1, 200), (512, 8, 1024)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_layer_norm_of_column_slices(cols, start, wide, dtype):
