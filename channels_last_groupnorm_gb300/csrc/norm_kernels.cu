@@ -19,10 +19,11 @@
 // Two ways to the rows:
 //  * streamed: one CTA per SM, rows brought by bulk copies into a ring of
 //    shared memory that a warp of its own keeps full, so that up to 200 KB per
-//    SM are in flight whatever the arithmetic does.  For rows of whole 16-byte
-//    vectors, when every CTA meets several batches of rows.
+//    SM are in flight whatever the arithmetic does.  When every CTA meets several
+//    batches of rows.  Rows that begin at any element come as the 16-byte blocks
+//    that hold them and are shifted into place on their way to the registers.
 //  * direct: plain loads, many CTAs.  For few rows, where the ring would not
-//    fill, and for rows that are not made of 16-byte vectors.
+//    fill, and for rows too long for the ring.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -135,6 +136,8 @@ __device__ __forceinline__ void row_sum(float (&v)[N], Group &gr)
         for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
 }
 
+struct Shifted {};
+
 // A thread's elements of a row, NV slots of EPV: slot k begins at element (lane +
 // k tpr) EPV; zeros past the end.  They stay in the row's own type (half the
 // registers, converted twice) and are handed out two at a time.
@@ -160,6 +163,34 @@ struct Row {
             }
         }
     }
+    // From shared memory where the row begins at any element: a slot's 16 bytes
+    // come out of the two aligned blocks that hold them.  (16 bytes past the row's
+    // last block are read and dropped; what lies past its end is zero.)
+    __device__ __forceinline__ Row(const uint8_t *row, const Group &gr, int cols, Shifted)
+    {
+        const uint32_t at = smem_addr(row) & 15u;
+        const uint8_t *base = row - at;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (gr.lane + k * gr.tpr) * EPV;
+            uint32_t w[8] = {};
+            if (c < cols) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(base + c * sizeof(T));
+                const uint4 b = *reinterpret_cast<const uint4 *>(base + c * sizeof(T) + 16);
+                w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = at & 8u ? w[i + 2] : w[i];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = at & 4u ? w[i + 1] : w[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (sizeof(T) == 2 && (at & 2u)) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+                const int left = (cols - c) * static_cast<int>(sizeof(T)) - 4 * i;    // bytes of the row from this word on
+                raw[k][i % kWords] = left >= 4 ? w[i] : left == 2 ? w[i] & 0xffffu : 0u;
+            }
+        }
+    }
     // elements 2 j and 2 j + 1
     __device__ __forceinline__ uint64_t pair(int j) const
     {
@@ -173,7 +204,7 @@ struct Row {
 
 // The thread's part of the weight (ones without) or the bias (zeros), in pairs:
 // held in registers, or asked for at every row (where the registers are full).
-template <int EPV, int NV, bool kHeld = (NV * EPV <= 16)>
+template <int EPV, int NV, bool kHeld = (NV * EPV <= 16), bool kTail = false>
 struct Own {
     const void *p;
     int format, cols;
@@ -183,8 +214,15 @@ struct Own {
     __device__ __forceinline__ void fetch(const Group &gr, int k, float (&f)[EPV]) const
     {
         const int c = (gr.lane + k * gr.tpr) * EPV;
-        if (p && c < cols) {
+        if (p && (kTail ? c + EPV : c + 1) <= cols) {
             load_params<EPV>(p, format, c, f);
+        } else if (kTail && p && c < cols) {
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) {
+                float one[1] = {fill};
+                if (c + e < cols) load_params<1>(p, format, c + e, one);
+                f[e] = one[0];
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < EPV; ++e) f[e] = fill;
@@ -256,10 +294,82 @@ __device__ __forceinline__ void store_pairs(T *row, const Group &gr, int k, int 
     *reinterpret_cast<uint4 *>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Where a row's results go: straight to memory,
+template <typename T, int EPV>
+struct Straight {
+    static constexpr bool kTail = false;
+    __device__ __forceinline__ void put(T *row, const Group &gr, int k, int cols, const uint64_t (&f)[EPV == 1 ? 1 : EPV / 2])
+    {
+        store_pairs<T, EPV>(row, gr, k, cols, f);
+    }
+    __device__ __forceinline__ void done(T *, const Group &, int, bool) {}
+};
+
+// or, for a row that begins at any element, through a copy in shared memory that
+// lies to 16 bytes as the row does: whole blocks of it leave as vectors, and the
+// blocks that it shares with its neighbours element by element.
+template <typename T, int EPV>
+struct Staged {
+    static constexpr bool kTail = true;   // (a slot may reach over the row's end)
+    uint8_t *buffer;                      // the group's
+    __device__ __forceinline__ void put(T *row, const Group &gr, int k, int cols, const uint64_t (&f)[EPV == 1 ? 1 : EPV / 2])
+    {
+        const int c = (gr.lane + k * gr.tpr) * EPV;
+        if (c >= cols) return;
+        uint8_t *to = buffer + (reinterpret_cast<uintptr_t>(row) & 15u) + c * sizeof(T);
+        if (c + EPV > cols) {
+            T *one = reinterpret_cast<T *>(to);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e)
+                if (c + e < cols) {
+                    const float2 v = unpack2(f[e / 2]);
+                    one[e] = from_float<T>(e % 2 ? v.y : v.x);
+                }
+            return;
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 v = unpack2(f[sizeof(T) == 4 ? e / 2 : e % (EPV / 2)]);
+            w[e] = sizeof(T) == 4 ? __float_as_uint(e % 2 ? v.y : v.x) : pack_word<T>(v.x, v.y);
+        }
+        if (sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(row) & 2u)) {
+            *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(w[0]);
+#pragma unroll
+            for (int e = 0; e < 3; ++e) *reinterpret_cast<uint32_t *>(to + 2 + 4 * e) = __funnelshift_r(w[e], w[e + 1], 16);
+            *reinterpret_cast<uint16_t *>(to + 14) = static_cast<uint16_t>(w[3] >> 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t *>(to + 4 * e) = w[e];
+        }
+    }
+    // (all threads of the group; the next row's sums come before its next put)
+    __device__ __forceinline__ void done(T *row, const Group &gr, int cols, bool live)
+    {
+        if (gr.tpr > 32)
+            named_sync(1 + gr.g, gr.tpr);
+        else
+            __syncwarp();
+        if (live) {
+            const int at = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u), end = at + cols * static_cast<int>(sizeof(T));
+            uint8_t *base = reinterpret_cast<uint8_t *>(row) - at;
+            const int first = at ? 1 : 0, last = end / 16;
+            for (int i = first + gr.lane; i < last; i += gr.tpr)
+                reinterpret_cast<uint4 *>(base)[i] = reinterpret_cast<const uint4 *>(buffer)[i];
+            const int head = min(16 * first, end), tail = max(16 * last, head);
+            for (int i = at + gr.lane * static_cast<int>(sizeof(T)); i < head; i += gr.tpr * static_cast<int>(sizeof(T)))
+                *reinterpret_cast<T *>(base + i) = *reinterpret_cast<const T *>(buffer + i);
+            for (int i = tail + gr.lane * static_cast<int>(sizeof(T)); i < end; i += gr.tpr * static_cast<int>(sizeof(T)))
+                *reinterpret_cast<T *>(base + i) = *reinterpret_cast<const T *>(buffer + i);
+        }
+        if (gr.tpr <= 32) __syncwarp();
+    }
+};
+
 // One row from registers: statistics out, y out.
-template <typename T, int EPV, int NV, typename Params>
+template <typename T, int EPV, int NV, typename Params, typename Out>
 __device__ __forceinline__ void norm_row(const NormArgs &a, const Row<T, EPV, NV> &x, const Params &w, const Params &b,
-                                         Group &gr, int64_t row, bool live)
+                                         Group &gr, int64_t row, bool live, Out out)
 {
     constexpr int kEach = EPV == 1 ? 1 : EPV / 2, kGroups = Row<T, EPV, NV>::kPairs / kEach;
     const float inv = 1.0f / static_cast<float>(a.cols);
@@ -280,37 +390,41 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Row<T, EPV, NV
         for (int e = 0; e < kEach; ++e) {
             uint64_t d = add2(x.pair(k * kEach + e), minus);
             if (EPV == 1 && c + gr.tpr >= a.cols) d = pack2(unpack2(d).x, 0.f);
+            if (Out::kTail && c + EPV > a.cols)
+                d = pack2(c + 2 * e < a.cols ? unpack2(d).x : 0.f, c + 2 * e + 1 < a.cols ? unpack2(d).y : 0.f);
             q2 = fma2(d, d, q2);
         }
     }
     float q[1] = {unpack2(q2).x + unpack2(q2).y};
     row_sum(q, gr);
     const float rstd = rsqrtf(fmaf(q[0], inv, a.eps));   // (two steps of fp32 at most)
-    if (!live) return;
-    if (gr.lane == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
-    }
-    T *y = static_cast<T *>(a.y) + row_offset(a.y_at, a.inner, a.rows, row);
-    const uint64_t r2 = pack2(rstd, rstd);
+    T *y = static_cast<T *>(a.y) + (live ? row_offset(a.y_at, a.inner, a.rows, row) : 0);
+    if (live) {
+        if (gr.lane == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        const uint64_t r2 = pack2(rstd, rstd);
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-        uint64_t f[kEach], bk[kEach];
-        w.get(gr, k, f);
-        b.get(gr, k, bk);
+        for (int k = 0; k < kGroups; ++k) {
+            uint64_t f[kEach], bk[kEach];
+            w.get(gr, k, f);
+            b.get(gr, k, bk);
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) f[e] = fma2(mul2(add2(x.pair(k * kEach + e), minus), r2), f[e], bk[e]);
-        store_pairs<T, EPV>(y, gr, k, a.cols, f);
+            for (int e = 0; e < kEach; ++e) f[e] = fma2(mul2(add2(x.pair(k * kEach + e), minus), r2), f[e], bk[e]);
+            out.put(y, gr, k, a.cols, f);
+        }
     }
+    out.done(y, gr, a.cols, live);
 }
 
 // One row of the backward pass from registers: dx out, column sums on.  (Past
 // the row's end dy is zero and adds nothing; so is all of it for a row that is
 // not there.)
-template <typename T, int EPV, int NV, typename Params, typename After>
+template <typename T, int EPV, int NV, typename Params, typename After, typename Out>
 __device__ __forceinline__ void norm_grad_row(const NormGradArgs &a, const Row<T, EPV, NV> &x, const Row<T, EPV, NV> &dy,
                                               const Params &w, uint64_t (&sw)[NV * EPV / 2], uint64_t (&sb)[NV * EPV / 2],
-                                              float mean, float rstd, Group &gr, int64_t row, bool live, const After &after)
+                                              float mean, float rstd, Group &gr, int64_t row, bool live, const After &after, Out out)
 {
     constexpr int kEach = EPV == 1 ? 1 : EPV / 2, kGroups = Row<T, EPV, NV>::kPairs / kEach;
     const float inv = 1.0f / static_cast<float>(a.cols);
@@ -333,22 +447,24 @@ __device__ __forceinline__ void norm_grad_row(const NormGradArgs &a, const Row<T
     float s[2] = {unpack2(s0).x + unpack2(s0).y, unpack2(s1).x + unpack2(s1).y};
     row_sum(s, gr);
     after();                              // (every thread of the row holds its elements in registers)
-    if (!live) return;
-    T *dx = static_cast<T *>(a.dx) + row_offset(a.dx_at, a.inner, a.rows, row);
-    const float m0 = -s[0] * inv, m1 = -s[1] * inv;
-    const uint64_t m02 = pack2(m0, m0), m12 = pack2(m1, m1);
+    T *dx = static_cast<T *>(a.dx) + (live ? row_offset(a.dx_at, a.inner, a.rows, row) : 0);
+    if (live) {
+        const float m0 = -s[0] * inv, m1 = -s[1] * inv;
+        const uint64_t m02 = pack2(m0, m0), m12 = pack2(m1, m1);
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-        uint64_t f[kEach];
-        w.get(gr, k, f);
+        for (int k = 0; k < kGroups; ++k) {
+            uint64_t f[kEach];
+            w.get(gr, k, f);
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const int j = k * kEach + e;
-            const uint64_t h = mul2(add2(x.pair(j), minus), r2);
-            f[e] = mul2(r2, fma2(h, m12, fma2(dy.pair(j), f[e], m02)));
+            for (int e = 0; e < kEach; ++e) {
+                const int j = k * kEach + e;
+                const uint64_t h = mul2(add2(x.pair(j), minus), r2);
+                f[e] = mul2(r2, fma2(h, m12, fma2(dy.pair(j), f[e], m02)));
+            }
+            out.put(dx, gr, k, a.cols, f);
         }
-        store_pairs<T, EPV>(dx, gr, k, a.cols, f);
     }
+    out.done(dx, gr, a.cols, live);
 }
 
 // A CTA's column sums into its row of partial sums.  Groups that share a warp
@@ -400,36 +516,38 @@ __device__ __forceinline__ void write_partial(const NormGradArgs &a, uint64_t (&
 // ---------------------------------------------------------------------------
 // direct
 // ---------------------------------------------------------------------------
-// (rows up to kNormMaxCols: 2048 slots of 8 or 4096 of 4 take 4 a thread)
-template <int EPV, int NV>
-constexpr int direct_threads() { return EPV == 8 && NV == 4 ? 512 : 1024; }
+// (rows up to kNormMaxCols: 2048 slots of 8 or 4096 of 4 take 4 a thread, single
+// elements 16; THREADS bounds the CTA, and so the registers a thread may have)
+constexpr int kDirectGroups = 8;               // groups of several warps in a CTA
 
-template <typename T, int EPV, int NV>
-__global__ void __launch_bounds__(direct_threads<EPV, NV>()) norm_direct_kernel(const NormArgs a, int tpr)
+template <typename T, int EPV, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_direct_kernel(const NormArgs a, int tpr)
 {
-    __shared__ float scratch[2][32][2];
+    __shared__ float scratch[kDirectGroups][2][32][2];
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     const int per = blockDim.x / tpr;
-    Group gr = {tpr, 0, static_cast<int>(threadIdx.x) % tpr, scratch, 0};
+    Group gr = {tpr, static_cast<int>(threadIdx.x) / tpr, static_cast<int>(threadIdx.x) % tpr, nullptr, 0};
+    if (tpr > 32) gr.scratch = scratch[gr.g];
     const Own<EPV, NV> w(a.weight, a.weight_format, gr, a.cols, 1.f), b(a.bias, a.weight_format, gr, a.cols, 0.f);
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * per; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * per) {
         const int64_t row = r0 + threadIdx.x / tpr;
         const bool live = row < a.rows;   // whole warps stay for the shuffles
         const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, live ? row : r0), gr, a.cols);
-        norm_row(a, x, w, b, gr, row, live);
+        norm_row(a, x, w, b, gr, row, live, Straight<T, EPV>());
     }
 }
 
-template <typename T, int EPV, int NV>
-__global__ void __launch_bounds__(direct_threads<EPV, NV>()) norm_grad_direct_kernel(const NormGradArgs a, int tpr)
+template <typename T, int EPV, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_grad_direct_kernel(const NormGradArgs a, int tpr)
 {
     extern __shared__ __align__(128) uint8_t smem[];    // with a weight and several groups: their column sums
-    __shared__ float scratch[2][32][2];
+    __shared__ float scratch[kDirectGroups][2][32][2];
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     const int per = blockDim.x / tpr;
-    Group gr = {tpr, 0, static_cast<int>(threadIdx.x) % tpr, scratch, 0};
+    Group gr = {tpr, static_cast<int>(threadIdx.x) / tpr, static_cast<int>(threadIdx.x) % tpr, nullptr, 0};
+    if (tpr > 32) gr.scratch = scratch[gr.g];
     uint64_t sw[NV * EPV / 2] = {}, sb[NV * EPV / 2] = {};
     const Own<EPV, NV> w(a.weight, a.weight_format, gr, a.cols, 1.f);
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * per; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * per) {
@@ -438,10 +556,9 @@ __global__ void __launch_bounds__(direct_threads<EPV, NV>()) norm_grad_direct_ke
         const int64_t at = live ? row : r0;
         const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, at), gr, a.cols);
         const Row<T, EPV, NV> dy(static_cast<const T *>(a.dy) + row_offset(a.dy_at, a.inner, a.rows, at), gr, live ? a.cols : 0);
-        norm_grad_row(a, x, dy, w, sw, sb, a.mean[at], a.rstd[at], gr, row, live, [] {});
+        norm_grad_row(a, x, dy, w, sw, sb, a.mean[at], a.rstd[at], gr, row, live, [] {}, Straight<T, EPV>());
     }
     if (!a.weight) return;
-    gr.g = threadIdx.x / tpr;
     write_partial<EPV, NV>(a, sw, sb, gr, blockDim.x, reinterpret_cast<float *>(smem));
 }
 
@@ -458,9 +575,66 @@ constexpr int kStreamThreads = 384;           // of the row groups; 128 register
 // `per` rows, one for each group of threads.
 struct Stream {
     int tpr, per, stages;
-    uint32_t row_bytes, stage_bytes;
+    uint32_t row_bytes, slot_bytes, stage_bytes;    // slot_bytes: of one row in the ring
     WaitLimit limit;
 };
+
+// Rows that are not whole 16-byte vectors, or do not begin at one, are brought
+// with the 16-byte blocks that they begin and end in (what belongs to their
+// neighbours is dropped), and lie in the ring to 16 bytes as they do in memory.
+// A block that reaches out of the tensor, at its first and last row, is not
+// touched: its elements are copied one by one.
+struct Piece {
+    uintptr_t a0, b0, b1, head, tail, end;          // bulk copy [b0, b1); elements [begin, head) and [tail, end)
+};
+
+__device__ __forceinline__ Piece piece_of(const char *src, int64_t bytes, const char *low, const char *high)
+{
+    Piece p;
+    const uintptr_t s = reinterpret_cast<uintptr_t>(src);
+    p.end = s + bytes;
+    p.a0 = s & ~static_cast<uintptr_t>(15);
+    const uintptr_t a1 = (p.end + 15) & ~static_cast<uintptr_t>(15);
+    p.b0 = p.a0 < reinterpret_cast<uintptr_t>(low) && p.a0 < s ? p.a0 + 16 : p.a0;
+    p.b1 = a1 > reinterpret_cast<uintptr_t>(high) && a1 > p.end ? a1 - 16 : a1;
+    if (p.b1 < p.b0) p.b1 = p.b0;
+    p.head = p.b0 > p.a0 ? min(p.b0, p.end) : s;
+    p.tail = max(max(p.b1, p.head), s);
+    return p;
+}
+
+template <typename T>
+__device__ __forceinline__ void piece_ends(const Piece &p, const char *src, uint8_t *to)
+{
+    const uintptr_t s = reinterpret_cast<uintptr_t>(src);
+    if (p.head <= s && p.tail >= p.end) return;
+    for (uintptr_t i = s; i < p.head; i += sizeof(T)) *reinterpret_cast<T *>(to + (i - p.a0)) = *reinterpret_cast<const T *>(i);
+    for (uintptr_t i = p.tail; i < p.end; i += sizeof(T)) *reinterpret_cast<T *>(to + (i - p.a0)) = *reinterpret_cast<const T *>(i);
+    fence_proxy_async_smem();                       // (a later copy comes to the same place)
+}
+
+__device__ __forceinline__ void piece_load(const Piece &p, uint8_t *to, uint32_t full)
+{
+    if (p.b1 > p.b0)
+        bulk_load(smem_addr(to) + static_cast<uint32_t>(p.b0 - p.a0), reinterpret_cast<const void *>(p.b0),
+                  static_cast<uint32_t>(p.b1 - p.b0), full);
+}
+
+// One past the last byte of a tensor's last row.
+__device__ __forceinline__ const char *rows_end(const char *src, const RowsAt &at, int64_t inner, int64_t rows, int size, uint32_t row_bytes)
+{
+    return src + row_offset(at, inner, rows, rows - 1) * size + row_bytes;
+}
+
+// Where row r0 + g of a batch lies in the ring.
+__device__ __forceinline__ const uint8_t *row_in_ring(const Stream &s, const uint8_t *slots, const void *src, const RowsAt &at,
+                                                      int64_t inner, int64_t rows, int size, int64_t r0, int g)
+{
+    const uintptr_t base = reinterpret_cast<uintptr_t>(src);
+    if (inner >= rows && at.stride * size == s.row_bytes)
+        return slots + ((base + r0 * s.row_bytes) & 15u) + g * s.row_bytes;
+    return slots + g * s.slot_bytes + ((base + row_offset(at, inner, rows, min(r0 + g, rows - 1)) * size) & 15u);
+}
 
 // Brings a CTA's batches of N tensors' rows.  One warp; a copy per tensor where
 // its rows lie end to end.
@@ -493,6 +667,51 @@ __device__ __forceinline__ void stream_rows(const Stream &s, const char *const (
         }
     }
     // what is still in flight lands before the CTA ends
+    for (int k = max(0, n - s.stages); k < n; ++k) tc::drain(full + 8 * (k % s.stages), (k / s.stages) & 1, s.limit.timeout_ns);
+}
+
+// The same for rows that begin at any element.
+template <typename T, int N>
+__device__ __forceinline__ void stream_odd_rows(const Stream &s, const char *const (&src)[N], const RowsAt (&at)[N], int64_t inner,
+                                                int64_t rows, uint8_t *ring, uint32_t full, uint32_t empty, volatile int *abort)
+{
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * s.per; r0 < rows;
+         r0 += static_cast<int64_t>(gridDim.x) * s.per, ++n) {
+        const int st = n % s.stages;
+        const int have = static_cast<int>(min(static_cast<int64_t>(s.per), rows - r0));
+        bool go = true;
+        if (n >= s.stages)
+            go = tc::wait(empty + 8 * st, (n / s.stages - 1) & 1, abort, s.limit.timeout_ns, s.limit.status, s.limit.host_status);
+        if (!__all_sync(0xffffffffu, go)) break;
+        // the bytes of the copies and the tensor's ends first, then the copies
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                uint8_t *to = ring + st * s.stage_bytes + t * s.per * s.slot_bytes;
+                const bool whole = inner >= rows && at[t].stride * static_cast<int64_t>(sizeof(T)) == s.row_bytes;
+                const char *high = rows_end(src[t], at[t], inner, rows, sizeof(T), s.row_bytes);
+                for (int r = lane; r < (whole ? 1 : have); r += 32) {
+                    const char *from = src[t] + (whole ? r0 * s.row_bytes : row_offset(at[t], inner, rows, r0 + r) * static_cast<int64_t>(sizeof(T)));
+                    const Piece p = piece_of(from, whole ? static_cast<int64_t>(have) * s.row_bytes : s.row_bytes, src[t], high);
+                    if (pass == 0) {
+                        piece_ends<T>(p, from, to + r * s.slot_bytes);
+                        bytes += static_cast<uint32_t>(p.b1 - p.b0);
+                    } else {
+                        piece_load(p, to + r * s.slot_bytes, full + 8 * st);
+                    }
+                }
+            }
+            if (pass == 0) {
+                bytes = __reduce_add_sync(0xffffffffu, bytes);
+                if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, bytes);
+                __syncwarp();
+            }
+        }
+    }
     for (int k = max(0, n - s.stages); k < n; ++k) tc::drain(full + 8 * (k % s.stages), (k / s.stages) & 1, s.limit.timeout_ns);
 }
 
@@ -530,7 +749,15 @@ __device__ __forceinline__ void stream_release(StreamShared &sh, int st)
     if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&sh.empty[st]));
 }
 
-template <typename T, int NV>
+template <typename T, int EPV, int NV, bool ODD>
+__device__ __forceinline__ Row<T, EPV, NV> ring_row(const Stream &s, const uint8_t *slots, const void *src, const RowsAt &at, int64_t inner,
+                                                    int64_t rows, int64_t r0, const Group &gr, int cols)
+{
+    if (ODD) return Row<T, EPV, NV>(row_in_ring(s, slots, src, at, inner, rows, sizeof(T), r0, gr.g), gr, cols, Shifted());
+    return Row<T, EPV, NV>(reinterpret_cast<const T *>(slots + gr.g * s.slot_bytes), gr, cols);
+}
+
+template <typename T, int NV, bool ODD>
 __global__ void __launch_bounds__(kStreamThreads + 32, 1)
     norm_stream_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ Stream s)
 {
@@ -545,29 +772,37 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
     if (static_cast<int>(threadIdx.x) >= workers) {
         const char *const src[1] = {static_cast<const char *>(a.x)};
         const RowsAt at[1] = {a.x_at};
-        if (!skip)
-            stream_rows<1>(s, src, at, a.inner, sizeof(T), a.rows, smem_addr(ring), smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
+        if (!skip) {
+            if (ODD)
+                stream_odd_rows<T, 1>(s, src, at, a.inner, a.rows, ring, smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
+            else
+                stream_rows<1>(s, src, at, a.inner, sizeof(T), a.rows, smem_addr(ring), smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
+        }
         return;
     }
     if (skip) return;
     Group gr = {s.tpr, static_cast<int>(threadIdx.x) / s.tpr, static_cast<int>(threadIdx.x) % s.tpr, nullptr, 0};
     if (s.tpr > 32) gr.scratch = sh.scratch[gr.g];
-    const Own<EPV, NV, true> w(a.weight, a.weight_format, gr, a.cols, 1.f), b(a.bias, a.weight_format, gr, a.cols, 0.f);
+    const Own<EPV, NV, true, ODD> w(a.weight, a.weight_format, gr, a.cols, 1.f), b(a.bias, a.weight_format, gr, a.cols, 0.f);
     int st = 0, parity = 0;
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * s.per; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * s.per) {
         const int64_t row = r0 + gr.g;
         stream_wait(sh, s, st, parity);
-        const Row<T, EPV, NV> x(reinterpret_cast<const T *>(ring + st * s.stage_bytes + gr.g * s.row_bytes), gr, a.cols);
+        const Row<T, EPV, NV> x = ring_row<T, EPV, NV, ODD>(s, ring + st * s.stage_bytes, a.x, a.x_at, a.inner, a.rows, r0, gr,
+                                                            row < a.rows ? a.cols : 0);
         stream_release(sh, st);
         if (++st == s.stages) {
             st = 0;
             parity ^= 1;
         }
-        norm_row(a, x, w, b, gr, row, row < a.rows);
+        if (ODD)
+            norm_row(a, x, w, b, gr, row, row < a.rows, Staged<T, EPV>{ring + s.stages * s.stage_bytes + gr.g * s.slot_bytes});
+        else
+            norm_row(a, x, w, b, gr, row, row < a.rows, Straight<T, EPV>());
     }
 }
 
-template <typename T>
+template <typename T, bool ODD>
 __global__ void __launch_bounds__(kStreamThreads + 32, 1)
     norm_grad_stream_kernel(const __grid_constant__ NormGradArgs a, const __grid_constant__ Stream s)
 {
@@ -576,12 +811,14 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
     StreamShared &sh = *reinterpret_cast<StreamShared *>(smem);
     float *weight = reinterpret_cast<float *>(smem + (sizeof(StreamShared) + 127) / 128 * 128);
     uint8_t *ring = reinterpret_cast<uint8_t *>(weight) + (a.weight ? (4 * a.cols + 127) / 128 * 128 : 0);
+    const int padded = (a.cols + EPV - 1) / EPV * EPV;
+    uint8_t *const staging = ring + s.stages * s.stage_bytes;
     const int workers = s.per * s.tpr;
     stream_setup(sh, s, workers);
     if (a.weight)
-        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-            float one[1];
-            load_params<1>(a.weight, a.weight_format, c, one);
+        for (int c = threadIdx.x; c < padded; c += blockDim.x) {
+            float one[1] = {0.f};
+            if (c < a.cols) load_params<1>(a.weight, a.weight_format, c, one);
             weight[c] = one[0];
         }
     __syncthreads();
@@ -591,11 +828,15 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
     if (static_cast<int>(threadIdx.x) >= workers) {
         const char *const src[2] = {static_cast<const char *>(a.x), static_cast<const char *>(a.dy)};
         const RowsAt at[2] = {a.x_at, a.dy_at};
-        if (!skip)
-            stream_rows<2>(s, src, at, a.inner, sizeof(T), a.rows, smem_addr(ring), smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
+        if (!skip) {
+            if (ODD)
+                stream_odd_rows<T, 2>(s, src, at, a.inner, a.rows, ring, smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
+            else
+                stream_rows<2>(s, src, at, a.inner, sizeof(T), a.rows, smem_addr(ring), smem_addr(sh.full), smem_addr(sh.empty), &sh.abort);
+        }
     } else if (!skip) {
         if (s.tpr > 32) gr.scratch = sh.scratch[gr.g];
-        const Own<EPV, NV, false> w(a.weight ? weight : nullptr, GN_FORMAT_FP32, gr, a.cols, 1.f);
+        const Own<EPV, NV, false> w(a.weight ? weight : nullptr, GN_FORMAT_FP32, gr, padded, 1.f);
         const int64_t step = static_cast<int64_t>(gridDim.x) * s.per;
         int64_t row = static_cast<int64_t>(blockIdx.x) * s.per + gr.g;
         // (the statistics are asked for a batch ahead)
@@ -608,15 +849,20 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
                 rstd = __ldg(a.rstd + row + step);
             }
             stream_wait(sh, s, st, parity);
-            const uint8_t *at = ring + st * s.stage_bytes + gr.g * s.row_bytes;
-            const Row<T, EPV, NV> x(reinterpret_cast<const T *>(at), gr, row < a.rows ? a.cols : 0);
-            const Row<T, EPV, NV> dy(reinterpret_cast<const T *>(at + s.per * s.row_bytes), gr, row < a.rows ? a.cols : 0);
+            const uint8_t *at = ring + st * s.stage_bytes;
+            const int cols = row < a.rows ? a.cols : 0;
+            const Row<T, EPV, NV> x = ring_row<T, EPV, NV, ODD>(s, at, a.x, a.x_at, a.inner, a.rows, r0, gr, cols);
+            const Row<T, EPV, NV> dy = ring_row<T, EPV, NV, ODD>(s, at + s.per * s.slot_bytes, a.dy, a.dy_at, a.inner, a.rows, r0, gr, cols);
             stream_release(sh, st);
             if (++st == s.stages) {
                 st = 0;
                 parity ^= 1;
             }
-            norm_grad_row(a, x, dy, w, sw, sb, mean_now, rstd_now, gr, row, row < a.rows, [] {});
+            if (ODD)
+                norm_grad_row(a, x, dy, w, sw, sb, mean_now, rstd_now, gr, row, row < a.rows, [] {},
+                              Staged<T, EPV>{staging + gr.g * s.slot_bytes});
+            else
+                norm_grad_row(a, x, dy, w, sw, sb, mean_now, rstd_now, gr, row, row < a.rows, [] {}, Straight<T, EPV>());
         }
     }
     if (!a.weight) return;
@@ -633,7 +879,7 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
 // 12288 173 us with a loader warp, 120 us so, 4608 x 8192 118 and 99 us; fp32,
 // which does not spill either way, 4608 x 4096 57 and 58 us).  768 threads with
 // two slots spill as well (181 us).
-template <typename T>
+template <typename T, bool ODD>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     norm_grad_wide_kernel(const __grid_constant__ NormGradArgs a, const __grid_constant__ Stream s)
 {
@@ -642,11 +888,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     StreamShared &sh = *reinterpret_cast<StreamShared *>(smem);
     float *weight = reinterpret_cast<float *>(smem + (sizeof(StreamShared) + 127) / 128 * 128);
     uint8_t *ring = reinterpret_cast<uint8_t *>(weight) + (a.weight ? (4 * a.cols + 127) / 128 * 128 : 0);
+    const int padded = (a.cols + EPV - 1) / EPV * EPV;
     stream_setup(sh, s, s.tpr);
     if (a.weight)
-        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-            float one[1];
-            load_params<1>(a.weight, a.weight_format, c, one);
+        for (int c = threadIdx.x; c < padded; c += blockDim.x) {
+            float one[1] = {0.f};
+            if (c < a.cols) load_params<1>(a.weight, a.weight_format, c, one);
             weight[c] = one[0];
         }
     __syncthreads();
@@ -658,18 +905,31 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         int64_t next = blockIdx.x;
         const auto load = [&] {
             if (next >= a.rows) return;
-            const uint32_t full = smem_addr(&sh.full[fill]), to = smem_addr(ring) + fill * s.stage_bytes;
-            mbar_arrive_expect_tx(full, 2 * s.row_bytes);
-            bulk_load(to, static_cast<const char *>(a.x) + row_offset(a.x_at, a.inner, a.rows, next) * sizeof(T), s.row_bytes, full);
-            bulk_load(to + s.row_bytes, static_cast<const char *>(a.dy) + row_offset(a.dy_at, a.inner, a.rows, next) * sizeof(T),
-                      s.row_bytes, full);
+            const uint32_t full = smem_addr(&sh.full[fill]);
+            uint8_t *const to = ring + fill * s.stage_bytes;
+            const char *const x0 = static_cast<const char *>(a.x), *const dy0 = static_cast<const char *>(a.dy);
+            const char *const xr = x0 + row_offset(a.x_at, a.inner, a.rows, next) * static_cast<int64_t>(sizeof(T));
+            const char *const dyr = dy0 + row_offset(a.dy_at, a.inner, a.rows, next) * static_cast<int64_t>(sizeof(T));
+            if (ODD) {
+                const Piece px = piece_of(xr, s.row_bytes, x0, rows_end(x0, a.x_at, a.inner, a.rows, sizeof(T), s.row_bytes));
+                const Piece pd = piece_of(dyr, s.row_bytes, dy0, rows_end(dy0, a.dy_at, a.inner, a.rows, sizeof(T), s.row_bytes));
+                piece_ends<T>(px, xr, to);
+                piece_ends<T>(pd, dyr, to + s.slot_bytes);
+                mbar_arrive_expect_tx(full, static_cast<uint32_t>(px.b1 - px.b0 + pd.b1 - pd.b0));
+                piece_load(px, to, full);
+                piece_load(pd, to + s.slot_bytes, full);
+            } else {
+                mbar_arrive_expect_tx(full, 2 * s.row_bytes);
+                bulk_load(smem_addr(to), xr, s.row_bytes, full);
+                bulk_load(smem_addr(to) + s.slot_bytes, dyr, s.row_bytes, full);
+            }
             next += gridDim.x;
             ++issued;
             if (++fill == s.stages) fill = 0;
         };
         if (threadIdx.x == 0)
             for (int i = 0; i < s.stages; ++i) load();
-        const Own<EPV, NV, false> w(a.weight ? weight : nullptr, GN_FORMAT_FP32, gr, a.cols, 1.f);
+        const Own<EPV, NV, false> w(a.weight ? weight : nullptr, GN_FORMAT_FP32, gr, padded, 1.f);
         int64_t row = blockIdx.x;
         // (the statistics are asked for a row ahead)
         float mean = row < a.rows ? __ldg(a.mean + row) : 0.f, rstd = row < a.rows ? __ldg(a.rstd + row) : 0.f;
@@ -684,15 +944,20 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             // (after a wait that ran out nothing more is asked for)
             good = tc::wait(smem_addr(&sh.full[st]), parity, &sh.abort, s.limit.timeout_ns, s.limit.status, s.limit.host_status) && good;
             const uint8_t *at = ring + st * s.stage_bytes;
-            const Row<T, EPV, NV> x(reinterpret_cast<const T *>(at), gr, a.cols);
-            const Row<T, EPV, NV> dy(reinterpret_cast<const T *>(at + s.row_bytes), gr, a.cols);
+            const Row<T, EPV, NV> x = ring_row<T, EPV, NV, ODD>(s, at, a.x, a.x_at, a.inner, a.rows, row, gr, a.cols);
+            const Row<T, EPV, NV> dy = ring_row<T, EPV, NV, ODD>(s, at + s.slot_bytes, a.dy, a.dy_at, a.inner, a.rows, row, gr, a.cols);
             if (++st == s.stages) {
                 st = 0;
                 parity ^= 1;
             }
-            norm_grad_row(a, x, dy, w, sw, sb, mean_now, rstd_now, gr, row, true, [&] {
+            const auto refill = [&] {
                 if (threadIdx.x == 0 && good) load();
-            });
+            };
+            if (ODD)
+                norm_grad_row(a, x, dy, w, sw, sb, mean_now, rstd_now, gr, row, true, refill,
+                              Staged<T, EPV>{ring + s.stages * s.stage_bytes});
+            else
+                norm_grad_row(a, x, dy, w, sw, sb, mean_now, rstd_now, gr, row, true, refill, Straight<T, EPV>());
         }
         // what is still in flight lands before the CTA ends
         if (threadIdx.x == 0 && !good)
@@ -755,16 +1020,20 @@ bool vectors_ok(int cols, int epv, const void *const *ptrs, int n, const int64_t
 // a warp's two.  With one slot (24 warps on a row of 6144) the reductions'
 // instructions took longer than the row's memory does (62 us forward for 4608 x
 // 6144); with four the backward pass has a kernel of its own.
-Stream stream_shape(int64_t rows, int cols, int size, int tensors, size_t fixed, int sm_count, int *nv)
+Stream stream_shape(int64_t rows, int cols, int size, bool vec, int tensors, size_t fixed, int sm_count, int *nv)
 {
     Stream s = {};
-    const int slots = cols * size / 16;
+    const int slots = (cols * size + 15) / 16;
     *nv = slots <= (tensors == 1 ? 64 : 2 * kStreamThreads) ? 2 : 4;
     s.tpr = threads_per_row(slots, *nv);
     s.per = std::max(1, kStreamThreads / s.tpr);
     s.row_bytes = static_cast<uint32_t>(cols * size);
-    s.stage_bytes = static_cast<uint32_t>(tensors * s.per) * s.row_bytes;
+    // (a row that begins at any element: its blocks, and one more that is read)
+    s.slot_bytes = vec ? s.row_bytes : (s.row_bytes + 15) / 16 * 16 + 32;
+    s.stage_bytes = static_cast<uint32_t>(tensors * s.per) * s.slot_bytes;
+    if (!vec) fixed += s.per * s.slot_bytes;
     s.stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(3, kRingWant / s.stage_bytes)));
+    if (!vec && s.stages == 3 && 3 * static_cast<size_t>(s.stage_bytes) + fixed > kRingMost) s.stages = 2;
     if (s.tpr > kStreamThreads || s.stages * static_cast<size_t>(s.stage_bytes) + fixed > kRingMost ||
         rows < static_cast<int64_t>(4) * sm_count * s.per)
         s.stages = 0;
@@ -783,36 +1052,39 @@ size_t columns_bytes(const NormGradArgs &a, int tpr, int threads)
     return a.weight && parts > 1 ? parts * 8u * static_cast<size_t>(a.cols) : 0;
 }
 
-template <typename T, int NV>
+// Bytes of the results' rows in shared memory.
+size_t staging_bytes(const Stream &s) { return s.slot_bytes == s.row_bytes ? 0 : static_cast<size_t>(s.per) * s.slot_bytes; }
+
+template <typename T, int NV, bool ODD>
 cudaError_t forward_stream(const NormArgs &a, const Stream &s, int sm_count, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_stream_kernel<T, NV>), kStreamBytes, done);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_stream_kernel<T, NV, ODD>), kStreamBytes, done);
     if (e != cudaSuccess) return e;
-    return tc::launch_pdl(norm_stream_kernel<T, NV>, dim3(static_cast<unsigned>(sm_count)), dim3(s.per * s.tpr + 32),
-                          kStreamFixed + s.stages * s.stage_bytes, st, a, s);
+    return tc::launch_pdl(norm_stream_kernel<T, NV, ODD>, dim3(static_cast<unsigned>(sm_count)), dim3(s.per * s.tpr + 32),
+                          kStreamFixed + s.stages * s.stage_bytes + staging_bytes(s), st, a, s);
 }
 
-template <typename T>
+template <typename T, bool ODD>
 cudaError_t backward_stream(const NormGradArgs &a, const Stream &s, int sm_count, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_grad_stream_kernel<T>), kStreamBytes, done);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_grad_stream_kernel<T, ODD>), kStreamBytes, done);
     if (e != cudaSuccess) return e;
     // (384 threads with two slots of 16 bytes: the column sums take at most 48 KB)
-    const size_t ring = std::max<size_t>(s.stages * s.stage_bytes, columns_bytes(a, s.tpr, s.per * s.tpr));
-    return tc::launch_pdl(norm_grad_stream_kernel<T>, dim3(static_cast<unsigned>(sm_count)), dim3(s.per * s.tpr + 32),
+    const size_t ring = std::max<size_t>(s.stages * s.stage_bytes + staging_bytes(s), columns_bytes(a, s.tpr, s.per * s.tpr));
+    return tc::launch_pdl(norm_grad_stream_kernel<T, ODD>, dim3(static_cast<unsigned>(sm_count)), dim3(s.per * s.tpr + 32),
                           kStreamFixed + weight_copy(a) + ring, st, a, s);
 }
 
-template <typename T>
+template <typename T, bool ODD>
 cudaError_t backward_wide(const NormGradArgs &a, const Stream &s, int sm_count, cudaStream_t st)
 {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_grad_wide_kernel<T>), kStreamBytes, done);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(norm_grad_wide_kernel<T, ODD>), kStreamBytes, done);
     if (e != cudaSuccess) return e;
-    return tc::launch_pdl(norm_grad_wide_kernel<T>, dim3(static_cast<unsigned>(sm_count)), dim3(s.tpr),
-                          kStreamFixed + weight_copy(a) + s.stages * s.stage_bytes, st, a, s);
+    return tc::launch_pdl(norm_grad_wide_kernel<T, ODD>, dim3(static_cast<unsigned>(sm_count)), dim3(s.tpr),
+                          kStreamFixed + weight_copy(a) + s.stages * s.stage_bytes + staging_bytes(s), st, a, s);
 }
 
 // The direct form: up to nv slots a thread, a row's threads one CTA or, for
@@ -821,14 +1093,24 @@ struct Direct {
     int nv, tpr, threads;
 };
 
-Direct direct_shape(int slots, bool vec)
+Direct direct_shape(int slots, bool vec, int64_t rows, int sm_count)
 {
     Direct d;
-    d.nv = vec || slots <= 4096 ? 4 : 16;
-    // few slots: one each, so that a short row is spread over a warp
-    if (vec && slots <= 1024) d.nv = 1;
+    if (vec) {
+        // few slots: one each, so that a short row is spread over a warp
+        d.nv = slots <= 1024 ? 1 : 4;
+    } else {
+        // Single elements: four a thread while the rows do not fill the SMs, then 8
+        // or 16, which leave a row to a warp or a few and several rows to a CTA
+        // (forward and backward, fp32 and weight: 12000 x 131 21 + 43 us with four,
+        // 13 + 24 with 8; 6600 x 4001 106 + 136 with four, 54 + 83 with 16).  Rows of
+        // up to 1024 fill them later (4800 x 515 fp16 backward 27 with 16, 3001 x 1003
+        // 39 with 16 and 26 with four).
+        const int few = (slots > 256 && slots <= 1024 ? 32 : 4) * sm_count;
+        d.nv = slots <= 128 || (slots <= 4096 && rows <= few) ? 4 : slots <= 256 ? 8 : 16;
+    }
     d.tpr = threads_per_row(slots, d.nv);
-    d.threads = d.tpr > 32 ? d.tpr : 256;
+    d.threads = d.tpr <= 32 ? 256 : vec ? d.tpr : d.tpr * std::max(1, 256 / d.tpr);
     return d;
 }
 
@@ -839,19 +1121,24 @@ cudaError_t forward(const NormArgs &a, int sm_count, const WaitLimit &limit, cud
     const void *ptrs[] = {a.x, a.y};
     const int64_t strides[] = {a.x_at.outer, a.x_at.stride, a.y_at.outer, a.y_at.stride};
     const bool vec = vectors_ok(a.cols, EPV, ptrs, 2, strides);
-    if (vec) {
-        int nv;
-        Stream st = stream_shape(a.rows, a.cols, sizeof(T), 1, 0, sm_count, &nv);
-        st.limit = limit;
-        if (st.stages) return nv == 2 ? forward_stream<T, 2>(a, st, sm_count, s) : forward_stream<T, 4>(a, st, sm_count, s);
+    int nv;
+    Stream st = stream_shape(a.rows, a.cols, sizeof(T), vec, 1, 0, sm_count, &nv);
+    st.limit = limit;
+    if (st.stages && vec) return nv == 2 ? forward_stream<T, 2, false>(a, st, sm_count, s) : forward_stream<T, 4, false>(a, st, sm_count, s);
+    // (Rows that begin at any element: half types are streamed, 4608 x 6143 bf16 73
+    // us straight and 54 so; fp32 elements are wide enough for plain loads, 4608 x
+    // 6143 77 us streamed and 67 straight.)
+    if constexpr (sizeof(T) == 2) {
+        if (st.stages) return nv == 2 ? forward_stream<T, 2, true>(a, st, sm_count, s) : forward_stream<T, 4, true>(a, st, sm_count, s);
     }
-    const Direct d = direct_shape(vec ? a.cols / EPV : a.cols, vec);
+    const Direct d = direct_shape(vec ? a.cols / EPV : a.cols, vec, a.rows, sm_count);
     const int64_t per = d.threads / d.tpr;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>((a.rows + per - 1) / per, 8 * sm_count)));
-    if (vec && d.nv == 1) return tc::launch_pdl(norm_direct_kernel<T, EPV, 1>, grid, dim3(d.threads), 0, s, a, d.tpr);
-    if (vec) return tc::launch_pdl(norm_direct_kernel<T, EPV, 4>, grid, dim3(d.threads), 0, s, a, d.tpr);
-    if (d.nv == 4) return tc::launch_pdl(norm_direct_kernel<T, 1, 4>, grid, dim3(d.threads), 0, s, a, d.tpr);
-    return tc::launch_pdl(norm_direct_kernel<T, 1, 16>, grid, dim3(d.threads), 0, s, a, d.tpr);
+    if (vec && d.nv == 1) return tc::launch_pdl(norm_direct_kernel<T, EPV, 1, 1024>, grid, dim3(d.threads), 0, s, a, d.tpr);
+    if (vec) return tc::launch_pdl(norm_direct_kernel<T, EPV, 4, EPV == 8 ? 512 : 1024>, grid, dim3(d.threads), 0, s, a, d.tpr);
+    if (d.nv == 4) return tc::launch_pdl(norm_direct_kernel<T, 1, 4, 1024>, grid, dim3(d.threads), 0, s, a, d.tpr);
+    if (d.nv == 8) return tc::launch_pdl(norm_direct_kernel<T, 1, 8, 256>, grid, dim3(d.threads), 0, s, a, d.tpr);
+    return tc::launch_pdl(norm_direct_kernel<T, 1, 16, 1024>, grid, dim3(d.threads), 0, s, a, d.tpr);
 }
 
 template <typename T>
@@ -861,25 +1148,32 @@ cudaError_t backward(const NormGradArgs &a, int sm_count, const WaitLimit &limit
     const void *ptrs[] = {a.x, a.dy, a.dx};
     const int64_t strides[] = {a.x_at.outer, a.x_at.stride, a.dy_at.outer, a.dy_at.stride, a.dx_at.outer, a.dx_at.stride};
     const bool vec = vectors_ok(a.cols, EPV, ptrs, 3, strides);
-    if (vec) {
-        int nv;
-        Stream st = stream_shape(a.rows, a.cols, sizeof(T), 2, weight_copy(a), sm_count, &nv);
-        st.limit = limit;
-        if (st.stages) {
-            *blocks = sm_count;
-            return nv == 2 ? backward_stream<T>(a, st, sm_count, s) : backward_wide<T>(a, st, sm_count, s);
+    int nv;
+    Stream st = stream_shape(a.rows, a.cols, sizeof(T), vec, 2, weight_copy(a), sm_count, &nv);
+    st.limit = limit;
+    // (Rows that begin at any element: half types are streamed, 4608 x 6143 bf16 323
+    // us straight and 90 so; fp32 where a row takes more than 256 threads straight,
+    // 4608 x 6143 112 us straight and 104 so, 6600 x 4001 83 and 118.)
+    if (st.stages && (vec || sizeof(T) == 2 || a.cols > 4096)) {
+        *blocks = sm_count;
+        if (vec) return nv == 2 ? backward_stream<T, false>(a, st, sm_count, s) : backward_wide<T, false>(a, st, sm_count, s);
+        if constexpr (sizeof(T) == 2) {
+            if (nv == 2) return backward_stream<T, true>(a, st, sm_count, s);
         }
+        return backward_wide<T, true>(a, st, sm_count, s);
     }
-    const Direct d = direct_shape(vec ? a.cols / EPV : a.cols, vec);
+    const Direct d = direct_shape(vec ? a.cols / EPV : a.cols, vec, a.rows, sm_count);
     const int64_t per = d.threads / d.tpr;
     *blocks = static_cast<int>(std::min<int64_t>((a.rows + per - 1) / per, layer_norm_blocks(a.rows, a.cols, sm_count)));
     const dim3 grid(static_cast<unsigned>(*blocks));
     // (several groups only for rows of up to 32 threads: 16 KB at most)
     const size_t smem = columns_bytes(a, d.tpr, d.threads);
-    if (vec && d.nv == 1) return tc::launch_pdl(norm_grad_direct_kernel<T, EPV, 1>, grid, dim3(d.threads), smem, s, a, d.tpr);
-    if (vec) return tc::launch_pdl(norm_grad_direct_kernel<T, EPV, 4>, grid, dim3(d.threads), smem, s, a, d.tpr);
-    if (d.nv == 4) return tc::launch_pdl(norm_grad_direct_kernel<T, 1, 4>, grid, dim3(d.threads), smem, s, a, d.tpr);
-    return tc::launch_pdl(norm_grad_direct_kernel<T, 1, 16>, grid, dim3(d.threads), smem, s, a, d.tpr);
+    if (vec && d.nv == 1) return tc::launch_pdl(norm_grad_direct_kernel<T, EPV, 1, 1024>, grid, dim3(d.threads), smem, s, a, d.tpr);
+    if (vec) return tc::launch_pdl(norm_grad_direct_kernel<T, EPV, 4, EPV == 8 ? 512 : 1024>, grid, dim3(d.threads), smem, s, a, d.tpr);
+    if (d.nv == 4) return tc::launch_pdl(norm_grad_direct_kernel<T, 1, 4, 1024>, grid, dim3(d.threads), smem, s, a, d.tpr);
+    if (d.nv == 8) return tc::launch_pdl(norm_grad_direct_kernel<T, 1, 8, 256>, grid, dim3(d.threads), smem, s, a, d.tpr);
+    if (d.threads <= 512) return tc::launch_pdl(norm_grad_direct_kernel<T, 1, 16, 512>, grid, dim3(d.threads), smem, s, a, d.tpr);
+    return tc::launch_pdl(norm_grad_direct_kernel<T, 1, 16, 1024>, grid, dim3(d.threads), smem, s, a, d.tpr);
 }
 
 }  // namespace

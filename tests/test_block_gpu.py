@@ -108,6 +108,39 @@ def test_layer_norm_wide_rows_backward(rows, cols, wide, dtype):
         assert all(p is q or torch.equal(p, q) for p, q in zip(again, (dx, dw, db)))
 
 
+@pytest.mark.parametrize("rows,cols,wide,start,dtype", [
+    (300000, 1, 1, 0, BF), (300000, 5, 5, 3, FP), (240000, 7, 9, 1, F32), (60001, 67, 67, 0, BF), (40000, 131, 131, 1, FP),
+    (30011, 131, 140, 5, BF), (9001, 257, 257, 0, F32), (9000, 514, 515, 1, FP), (5003, 1001, 1001, 7, BF), (5000, 1003, 1003, 0, F32),
+    (2500, 2050, 2050, 0, BF), (1301, 6143, 6143, 1, FP), (1300, 6150, 6157, 2, BF), (700, 10007, 10007, 0, FP),
+    (700, 12001, 12001, 3, BF), (640, 5001, 5003, 1, F32), (640, 15001, 15001, 0, FP), (40000, 128, 128, 1, BF),
+    (2003, 200, 203, 1, F32), (3001, 131, 131, 0, FP), (40001, 133, 133, 0, F32), (9999, 515, 515, 2, F32), (2000, 2051, 2051, 0, F32),
+    (5001, 1003, 1010, 3, BF), (700, 12002, 12002, 0, F32)])
+def test_layer_norm_many_rows_that_begin_anywhere(rows, cols, wide, start, dtype):
+    """Many rows that are not whole vectors, or lie at any element, end to end and out of a wider tensor."""
+    def lie(seed, scale, shift=0.0):
+        return rand((rows * wide + start,), dtype, seed, scale, shift)[start:].view(rows, wide)[:, :cols]
+    x, dy = lie(5, 2.0, 1.0), lie(6, 1.0)
+    for w, b in ((rand((cols,), F32, 7, 0.3, 1.0), rand((cols,), F32, 8)), (rand((cols,), dtype, 7, 0.3, 1.0), None), (None, None)):
+        out, clean = guarded((rows, cols), dtype)
+        y, mean, rstd = gn.layer_norm(x, w, b, out=out)
+        grad, clean_grad = guarded((rows, cols), dtype)
+        dx, dw, db = gn.layer_norm_backward(dy, x, mean, rstd, w, out=grad)
+        clean()
+        clean_grad()
+        got = dict(y=y, mean=mean, rstd=rstd, dx=dx, dw=dw, db=db)
+        for name, (value, bound) in br.layer_norm(x, w, b, 1e-6, dy).items():
+            br.check(got[name], value, bound, name)
+    # in place on rows of a wider tensor, whose other elements stay; the same bits
+    whole = torch.full((rows * (wide + 2) + start,), -7.0, dtype=dtype, device="cuda")
+    onto = whole[start:].view(rows, wide + 2)[:, 1:1 + cols]
+    onto.copy_(dy)
+    keep = whole.clone()
+    again = gn.layer_norm_backward(onto, x, mean, rstd, w, out=onto)
+    assert torch.equal(again[0], dx)
+    onto.copy_(keep[start:].view(rows, wide + 2)[:, 1:1 + cols])
+    assert torch.equal(whole, keep)
+
+
 @pytest.mark.parametrize("cols,start,wide", [(64, 0, 64 + 8), (64, 3, 80), (129, 1, 200), (512, 8, 1024)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_layer_norm_of_column_slices(cols, start, wide, dtype):
