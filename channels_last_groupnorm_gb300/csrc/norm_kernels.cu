@@ -517,7 +517,10 @@ __device__ __forceinline__ void write_partial(const NormGradArgs &a, uint64_t (&
 // direct
 // ---------------------------------------------------------------------------
 // (rows up to kNormMaxCols: 2048 slots of 8 or 4096 of 4 take 4 a thread, single
-// elements 16; THREADS bounds the CTA, and so the registers a thread may have)
+// elements 16; THREADS bounds the CTA, and so the registers a thread may have.
+// The longest rows' backward pass asks for one CTA per SM: left to itself the
+// compiler gives its 1024 threads 32 registers and spills: 2300 x 12002 fp32 347
+// us, and 201 with the 64 that there are.)
 constexpr int kDirectGroups = 8;               // groups of several warps in a CTA
 
 template <typename T, int EPV, int NV, int THREADS>
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(THREADS) norm_direct_kernel(const NormArgs a, 
 }
 
 template <typename T, int EPV, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_grad_direct_kernel(const NormGradArgs a, int tpr)
+__global__ void __launch_bounds__(THREADS, NV == 16 && THREADS == 1024 ? 1 : 0) norm_grad_direct_kernel(const NormGradArgs a, int tpr)
 {
     extern __shared__ __align__(128) uint8_t smem[];    // with a weight and several groups: their column sums
     __shared__ float scratch[kDirectGroups][2][32][2];
