@@ -710,8 +710,9 @@ __device__ __forceinline__ void stream_odd_rows(const Stream &s, const char *con
             }
             if (pass == 0) {
                 bytes = __reduce_add_sync(0xffffffffu, bytes);
+                __syncwarp();                       // every lane's elements are in the ring ahead of the arrival
                 if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, bytes);
-                __syncwarp();
+                __syncwarp();                       // and the arrival is ahead of the copies
             }
         }
     }
