@@ -99,13 +99,14 @@ def gn_layer_norm_workspace_bytes(rows: int, cols: int) -> int:
     return int(_start()[0].gn_layer_norm_workspace_bytes(rows, cols))
 
 
-def _flat_stride(dims):
-    """The one stride of axes [(length, stride), ...], or None."""
+def _flat_stride(dims, alone):
+    """The one stride of axes [(length, stride), ...] (0 of a broadcast one;
+    `alone` where every axis has length one), or None."""
     dims = [(n, s) for n, s in dims if n != 1]
     for (_, outer), (n, inner) in zip(dims, dims[1:]):
         if outer != n * inner:
             return None
-    return dims[-1][1] if dims else 0
+    return dims[-1][1] if dims else alone
 
 
 def _row_strides(shape, all_strides):
@@ -118,17 +119,17 @@ def _row_strides(shape, all_strides):
     for strides in all_strides:
         if strides[-1] != 1 and cols > 1:
             return None
-        stride = strides[0] if len(lead) == 1 and lead[0] != 1 else _flat_stride(list(zip(lead, strides)))
+        stride = strides[0] if len(lead) == 1 and lead[0] != 1 else _flat_stride(list(zip(lead, strides)), cols)
         if stride is None:
             break
-        found += [0, stride or cols]
+        found += [0, stride]
     else:
         return 0, found
     if len(lead) < 2:
         return None
     found = []
     for strides in all_strides:
-        outer = _flat_stride(list(zip(lead[:-1], strides)))
+        outer = _flat_stride(list(zip(lead[:-1], strides)), 0)
         if outer is None:
             return None
         found += [outer, strides[-2] if lead[-1] > 1 else cols]
@@ -165,7 +166,8 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stream=No
     ``weight`` and ``bias`` (bias only with a weight): contiguous [C] tensors
     of one dtype, any of the three.  x needs a contiguous last axis and one or
     two strides between its rows: a column slice of a wider tensor is fine, and
-    so are some heads [T, H, C] of a fused projection."""
+    so are some heads [T, H, C] of a fused projection, and rows broadcast by
+    ``expand`` (``out`` must have rows of its own)."""
     L, T = _start()
     if not (isinstance(x, T.Tensor) and x.is_cuda):
         return None
@@ -204,7 +206,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
     """Backward pass of ``layer_norm``: ``(dx, dweight, dbias)`` from the
     gradient dy of its output, its input x, the statistics that it returned
     and its weight; dweight and dbias have the weight's dtype and are None
-    without one.  dx is ``out`` if given (it may be dy or x).  None when not
+    without one.  dy may be broadcast over rows, as the gradient of a sum over
+    tokens is.  dx is ``out`` if given (it may be dy or x).  None when not
     supported."""
     L, T = _start()
     if not (isinstance(x, T.Tensor) and x.is_cuda):

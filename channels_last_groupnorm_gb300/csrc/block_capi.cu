@@ -81,20 +81,21 @@ int launched(cudaError_t e, int launches)
     return GN_ERR_CUDA;
 }
 
-// Rows in two levels: false if they run into one another or overflow.  A flat
-// tensor's outer stride is made to fit.
+// Rows in two levels: false if they run into one another or overflow.  Rows that
+// are only read may be broadcast (a stride of 0).  A flat tensor's outer stride
+// is made to fit.
 bool norm_rows(Range *r, gn::RowsAt *at, const void *p, int64_t rows, int64_t cols, int64_t inner, const int64_t *strides,
-               size_t size)
+               size_t size, bool read_only)
 {
     *at = {strides[0], strides[1]};
-    if (at->stride < cols) return false;
+    if (at->stride < cols && !(read_only && at->stride == 0)) return false;
     const int64_t in = rows < inner ? rows : inner;
     if (in > 1 && at->stride > kMaxElements / in) return false;
     if (rows <= inner) {
         at->outer = 0;
         return strided(r, p, rows, at->stride, 1, 0, cols, size);
     }
-    if (at->outer < (in - 1) * at->stride + cols) return false;
+    if (at->outer < (in - 1) * at->stride + cols && !(read_only && at->outer == 0)) return false;
     return strided(r, p, (rows + inner - 1) / inner, at->outer, inner, at->stride, cols, size);
 }
 
@@ -121,8 +122,8 @@ int gn_layer_norm(const void *x, const void *weight, const void *bias, void *y, 
         return GN_ERR_ALIGN;
     Range in, out;
     gn::RowsAt x_at, y_at;
-    if (rows > kMaxElements || !norm_rows(&in, &x_at, x, rows, cols, inner, strides, size) ||
-        !norm_rows(&out, &y_at, y, rows, cols, inner, strides + 2, size))
+    if (rows > kMaxElements || !norm_rows(&in, &x_at, x, rows, cols, inner, strides, size, true) ||
+        !norm_rows(&out, &y_at, y, rows, cols, inner, strides + 2, size, false))
         return GN_ERR_SHAPE;
     const size_t wb = wsize * static_cast<size_t>(cols), sb = 4u * static_cast<size_t>(rows);
     const Range w = {weight, wb}, b = {bias, wb}, m = {mean, sb}, r = {rstd, sb};
@@ -170,9 +171,9 @@ int gn_layer_norm_backward(const void *dy, const void *x, const void *weight, co
         return GN_ERR_ALIGN;
     Range g, in, out;
     gn::RowsAt dy_at, x_at, dx_at;
-    if (rows > kMaxElements || !norm_rows(&g, &dy_at, dy, rows, cols, inner, strides, size) ||
-        !norm_rows(&in, &x_at, x, rows, cols, inner, strides + 2, size) ||
-        !norm_rows(&out, &dx_at, dx, rows, cols, inner, strides + 4, size))
+    if (rows > kMaxElements || !norm_rows(&g, &dy_at, dy, rows, cols, inner, strides, size, true) ||
+        !norm_rows(&in, &x_at, x, rows, cols, inner, strides + 2, size, true) ||
+        !norm_rows(&out, &dx_at, dx, rows, cols, inner, strides + 4, size, false))
         return GN_ERR_SHAPE;
     const auto same = [&](const gn::RowsAt &o) { return o.stride == dx_at.stride && o.outer == dx_at.outer; };
     const size_t wb = wsize * static_cast<size_t>(cols), sb = 4u * static_cast<size_t>(rows);

@@ -481,7 +481,7 @@ int gn_attn_folded_ex(const void *q_bf16, const void *k_bf16, const void *xn_bf1
  *                the same strides.
  *   strides    : HOST [4], elements: outer and stride of x, outer and stride of y
  *                (stride >= cols; outer >= (inner - 1) stride + cols where rows >
- *                inner).
+ *                inner; of rows that are only read either may be 0: broadcast).
  *   weight, bias : DEVICE [cols] of weight_format, or both NULL; bias alone may
  *                be NULL.
  *   mean, rstd : DEVICE fp32 [rows], written for the backward pass, or NULL.
