@@ -191,9 +191,13 @@ __device__ __forceinline__ void fold_slack(float (&w)[N], const float (&slack)[N
 // Barriers and words of either kernel.  Own: the tiles a CTA owns; Long /
 // Short: a streamed tile is there, is done with; Info: a block's row records;
 // S / Dp: an MMA result is there; P / Ds: the softmax warps have put theirs in
-// its place; Out: the accumulators are done.
+// its place; Out: the accumulators are done.  A phase of a barrier must have been
+// seen by all that wait for it before the next one can complete.  dK and dV issue
+// S of a block only after P of the block before, one S is enough; dQ issues it a
+// block earlier, into the other buffer of scores, and has an S for each: S of block
+// n + 2 follows Ds of block n, whose warps have seen S of block n.
 enum Bar { kOwn = 0, kLong, kLongFree = kLong + kLongStages, kShort = kLongFree + kLongStages,
-           kShortFree = kShort + kShortStages, kInfo = kShortFree + kShortStages, kS = kInfo + 2, kDp, kP, kDs, kOut,
+           kShortFree = kShort + kShortStages, kInfo = kShortFree + kShortStages, kS = kInfo + 2, kDp = kS + 2, kP, kDs, kOut,
            kDrain, kBars };
 constexpr int kSoftWarps = 8;
 
@@ -714,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool masked = j0 < all_lo || j0 + kTile > all_hi;
             const int lo = span.x - j0, len = max(0, span.y - span.x);
             const uint32_t ts = t_s + lanes + 128 * (n & 1) + 64 * half;
-            go = wait_warp(bar(kS), n & 1, abort, args.limit);
+            go = wait_warp(bar(kS + (n & 1)), (n >> 1) & 1, abort, args.limit);
             if (!go) break;
             tc_fence_after_sync();
             float w[64], slack[64];              // scores, then weights; the cap's slopes
@@ -818,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         hand_over();
                         if (!waits) {
                             mma_tokens(t_s + 128 * ((n + 1) & 1), q_tile, long_tile(n + 1), steps, is);
-                            commit(bar(kS));
+                            commit(bar(kS + ((n + 1) & 1)));
                         }
                     }
                     if (waits) {
