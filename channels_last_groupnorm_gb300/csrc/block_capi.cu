@@ -219,6 +219,7 @@ int gn_rope_nd(const void *q, const void *k, void *q_out, void *k_out, const int
     if (tokens < 0 || heads < 1 || kv_heads < 0 || heads > (1 << 16) || kv_heads > (1 << 16) || (k && kv_heads < 1))
         return GN_ERR_SHAPE;
     if (dim < 2 || dim > 65536 || axes < 1 || axes > 8) return GN_ERR_CHANNELS;
+    if ((heads + kv_heads) * dim > gn::kRopeMaxElements) return GN_ERR_SHAPE;
     int64_t width = 0;
     for (int64_t n = 0; n < axes; ++n) {
         if (axes_dim[n] < 2 || axes_dim[n] % 2 || axes_dim[n] > 2 * gn::kRopeMaxPairs) return GN_ERR_CHANNELS;

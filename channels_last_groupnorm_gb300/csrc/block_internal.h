@@ -58,6 +58,7 @@ cudaError_t launch_layer_norm_backward(const NormGradArgs &a, int sm_count, cons
 
 // ---- rotary positions over several axes (rope_kernels.cu) -------------------
 constexpr int kRopeMaxPairs = 128;
+constexpr int64_t kRopeMaxElements = 1 << 30;   // of one token: its pieces are counted in an int, plus a grid's step
 
 struct RopeArgs {
     const void *in[2];            // query and key heads (the second may be null)

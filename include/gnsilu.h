@@ -539,6 +539,7 @@ int gn_layer_norm_backward(const void *dy, const void *x, const void *weight, co
  *   positions  : DEVICE [tokens][axes] contiguous, enum gn_position_format.
  *   axes_dim   : HOST [axes], even numbers >= 2, 1 <= axes <= 8,
  *                sum <= min(dim, 256); dim <= 65536.
+ *   heads, kv_heads <= 65536; (heads + kv_heads) dim <= 2^30.
  *   theta > 0.  format: enum gn_half_format (all three).
  * Asynchronous on `stream`.  Errors: GN_ERR_NULL, GN_ERR_FORMAT, GN_ERR_SHAPE,
  * GN_ERR_CHANNELS (dim, axes), GN_ERR_EPS (theta), GN_ERR_ALIGN, GN_ERR_ALIAS,
