@@ -404,7 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 64; ++k) {
                     const int2 sp = __ldg(reinterpret_cast<const int2 *>(spans + k));
-                    w[k] = key >= sp.x && key < sp.y ? w[k] : 0.f;
+                    const bool sees = key >= sp.x && key < sp.y;
+                    w[k] = sees ? w[k] : 0.f;
+                    if (MODE & kCap) slack[k] = sees ? slack[k] : 0.f;    // (of an unseen NaN: 0 x NaN is not 0)
                 }
             }
 #pragma unroll

@@ -1,0 +1,92 @@
+"""What lies at tokens that a query (or key) does not see has no influence on
+its results, to the last bit, whatever the scores are made of: infinities and
+NaN, huge scores, several documents that hold such values around one that
+does not, capped and biased scores, prefix masks, few and many queries."""
+import math
+
+import pytest
+import torch
+
+import channels_last_groupnorm_gb300 as gn
+from channels_last_groupnorm_gb300 import build as gnbuild
+from channels_last_groupnorm_gb300 import gnsilu as gs
+from tests import gpu_util as gu
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    gnbuild.build()
+    gs.lib()
+    yield
+    gu.assert_clean_device()
+
+
+def rand(shape, dtype, seed, scale=1.0):
+    return (torch.randn(shape, generator=torch.Generator().manual_seed(seed)) * scale).to(dtype).cuda()
+
+
+def i32(x):
+    return None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def attend(t, cu_q, cu_k, prefix=None, backward=True, **how):
+    how = dict(how, prefix=i32(prefix))
+    out, lse = gn.attention_packed(t["q"], t["k"], t["v"], i32(cu_q), i32(cu_k), **how)
+    got = dict(out=out, lse=lse)
+    if backward:
+        grads = gn.attention_packed_backward(t["dout"], t["q"], t["k"], t["v"], out, lse, i32(cu_q), i32(cu_k), **how)
+        got |= dict(zip(("dq", "dk", "dv"), grads))
+    torch.cuda.synchronize()
+    return got
+
+
+def tensors(tq, tk, h, hk, dim, dtype, scale=1.0):
+    return dict(q=rand((tq, h, dim), dtype, 1, scale), k=rand((tk, hk, dim), dtype, 2, scale), v=rand((tk, hk, dim), dtype, 3),
+                dout=rand((tq, h, dim), dtype, 4))
+
+
+HOW = [dict(), dict(cap=20.0), dict(bias=True), dict(cap=20.0, bias=True), dict(cap=2.0, causal=True, prefix=[40, 3, 17]),
+       dict(causal=True), dict(cap=30.0, bias=True, causal=True, prefix=[0, 90, 2])]
+
+
+def spread(how, h):
+    how = dict(how)
+    if how.pop("bias", False):
+        how["slopes"] = 2.0 ** -torch.arange(1, h + 1, device="cuda").float()
+    return how
+
+
+def with_bad(t, what, value, docs):
+    """A copy whose tensors named in `what` hold value and -value at tokens `docs[name]`."""
+    bad = {n: x.clone() for n, x in t.items()}
+    for n in what:
+        for lo, hi in docs[n]:
+            bad[n][lo:hi:2] = value
+            bad[n][lo + 1:hi:2] = -value
+    return bad
+
+
+CU_Q, CU_K = [3, 60, 261, 300], [5, 90, 291, 330]
+MIDDLE = dict(q=((0, 3), (60, 261), (300, 310)), dout=((0, 3), (60, 261), (300, 310)),
+              k=((0, 5), (90, 291), (330, 340)), v=((0, 5), (90, 291), (330, 340)))
+
+
+@pytest.mark.parametrize("how", range(len(HOW)))
+@pytest.mark.parametrize("h,hk,dim,dtype", [(2, 1, 64, BF), (4, 4, 128, FP), (8, 1, 40, BF)])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_nothing_infinite_reaches_other_documents(how, h, hk, dim, dtype, value):
+    """One document (and what belongs to none) full of them: the other two stay finite."""
+    how = spread(HOW[how], h)
+    t = tensors(310, 340, h, hk, dim, dtype)
+    for what in (("q",), ("k",), ("v",), ("dout",), ("q", "k", "v", "dout")):
+        got = attend(with_bad(t, what, value, MIDDLE), CU_Q, CU_K, **how)
+        for name, x in got.items():
+            for lo, hi in ((5, 90), (291, 330)) if name in ("dk", "dv") else ((3, 60), (261, 300)):
+                part = x[:, lo:hi] if name == "lse" else x[lo:hi]
+                assert torch.isfinite(part.float()).all(), (name, what, lo)
