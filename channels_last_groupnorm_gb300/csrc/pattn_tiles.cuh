@@ -174,31 +174,40 @@ __device__ __forceinline__ void mma_channels(uint32_t d, uint32_t a_tmem, uint32
 
 // ---- the cap's tanh, for N scores in place -------------------------------------------
 // v <- tanh(v k).  Scores are mostly small against their cap: up to 1/4 the
-// series of tanh to x^9 is exact to fp32 (the next term is under 2^-27 of x),
-// two scores per instruction and no special-function unit; beyond, for the
-// whole warp, 1 - 2 / (1 + e^2|x|) with two of its instructions each.
+// series of tanh to x^9 is good to fp32 (the next term is 9e-9 of x there), two
+// scores per instruction and no special-function unit; beyond, 1 - 2 / (1 +
+// e^2|x|) with two of its instructions each.  A score's value depends on itself
+// alone, never on its neighbours, which may be ones that nobody sees: the warp
+// leaves the second formula out where no score wants it, and otherwise takes
+// either for each.  (NaN passes through both.)
 template <int N>
 __device__ __forceinline__ void tanh_all(float (&v)[N], float k)
 {
+    constexpr float kSmall = 0.25f;
+    const uint64_t k2 = pack2(k, k);
+    const uint64_t c9 = pack2(62.f / 2835.f, 62.f / 2835.f), c7 = pack2(-17.f / 315.f, -17.f / 315.f);
+    const uint64_t c5 = pack2(2.f / 15.f, 2.f / 15.f), c3 = pack2(-1.f / 3.f, -1.f / 3.f);
+    const auto series = [&](uint64_t x) {
+        const uint64_t y = mul2(x, x), s = fma2(fma2(fma2(c9, y, c7), y, c5), y, c3);
+        return unpack2(fma2(mul2(x, y), s, x));
+    };
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(v[i]));
-    // (written so that a NaN or an infinity takes the second path)
-    if (__all_sync(0xffffffffu, top * fabsf(k) <= 0.25f)) {
-        const uint64_t k2 = pack2(k, k);
-        const uint64_t c9 = pack2(62.f / 2835.f, 62.f / 2835.f), c7 = pack2(-17.f / 315.f, -17.f / 315.f);
-        const uint64_t c5 = pack2(2.f / 15.f, 2.f / 15.f), c3 = pack2(-1.f / 3.f, -1.f / 3.f);
+    if (__all_sync(0xffffffffu, top * fabsf(k) <= kSmall)) {
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            const uint64_t x = mul2(pack2(v[i], v[i + 1]), k2), y = mul2(x, x);
-            const uint64_t s = fma2(fma2(fma2(c9, y, c7), y, c5), y, c3);
-            const float2 r = unpack2(fma2(mul2(x, y), s, x));
+            const float2 r = series(mul2(pack2(v[i], v[i + 1]), k2));
             v[i] = r.x;
             v[i + 1] = r.y;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = tanh_fast(v[i] * k);
+        for (int i = 0; i < N; i += 2) {
+            const float2 x = unpack2(mul2(pack2(v[i], v[i + 1]), k2)), r = series(pack2(x.x, x.y));
+            v[i] = fabsf(v[i]) * fabsf(k) <= kSmall ? r.x : tanh_fast(x.x);
+            v[i + 1] = fabsf(v[i + 1]) * fabsf(k) <= kSmall ? r.y : tanh_fast(x.y);
+        }
     }
 }
 

@@ -10,6 +10,7 @@ import torch
 import channels_last_groupnorm_gb300 as gn
 from channels_last_groupnorm_gb300 import build as gnbuild
 from channels_last_groupnorm_gb300 import gnsilu as gs
+from tests import block_ref as br
 from tests import gpu_util as gu
 
 pytestmark = pytest.mark.gpu
@@ -51,6 +52,15 @@ def tensors(tq, tk, h, hk, dim, dtype, scale=1.0):
                 dout=rand((tq, h, dim), dtype, 4))
 
 
+def same_at(got, clean, queries, keys):
+    """The results of these queries and keys have the same bits."""
+    for name, t in got.items():
+        for lo, hi in keys if name in ("dk", "dv") else queries:
+            part = (lambda x: x[:, lo:hi]) if name == "lse" else (lambda x: x[lo:hi])
+            a, b = part(t), part(clean[name])
+            assert torch.equal(a, b), (name, lo, hi, int((a != b).sum()), int(torch.isnan(a.float()).sum()))
+
+
 HOW = [dict(), dict(cap=20.0), dict(bias=True), dict(cap=20.0, bias=True), dict(cap=2.0, causal=True, prefix=[40, 3, 17]),
        dict(causal=True), dict(cap=30.0, bias=True, causal=True, prefix=[0, 90, 2])]
 
@@ -90,3 +100,29 @@ def test_nothing_infinite_reaches_other_documents(how, h, hk, dim, dtype, value)
             for lo, hi in ((5, 90), (291, 330)) if name in ("dk", "dv") else ((3, 60), (261, 300)):
                 part = x[:, lo:hi] if name == "lse" else x[lo:hi]
                 assert torch.isfinite(part.float()).all(), (name, what, lo)
+
+
+@pytest.mark.parametrize("how", range(len(HOW)))
+@pytest.mark.parametrize("h,hk,dim,dtype", [(2, 1, 64, BF), (4, 4, 128, FP), (8, 1, 40, BF)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, 3e4, 0.0])
+def test_other_documents_keep_their_bits(how, h, hk, dim, dtype, value):
+    how = spread(HOW[how], h)
+    t = tensors(310, 340, h, hk, dim, dtype)
+    clean = attend(t, CU_Q, CU_K, **how)
+    for what in (("q",), ("k",), ("v",), ("dout",), ("q", "k", "v", "dout")):
+        got = attend(with_bad(t, what, value, MIDDLE), CU_Q, CU_K, **how)
+        same_at(got, clean, ((3, 60), (261, 300)), ((5, 90), (291, 330)))
+
+
+@pytest.mark.parametrize("scale", [1.0, 4.0, 30.0])
+@pytest.mark.parametrize("cap", [1.5, 25.0])
+def test_capped_scores_on_both_sides_of_the_formulas(scale, cap):
+    """Small and large scores in one tile against the formulas."""
+    cu = [0, 150, 400]
+    t = tensors(400, 400, 4, 2, 64, BF)
+    t["q"][::3] *= scale
+    t["k"][::2] *= scale
+    how = dict(cap=cap, causal=True, prefix=[50, 0])
+    got = attend(t, cu, cu, **how)
+    for name, (value, bound) in br.attention(t["q"], t["k"], t["v"], cu, cu, dout=t["dout"], **how).items():
+        br.check(got[name], value, bound, name)
