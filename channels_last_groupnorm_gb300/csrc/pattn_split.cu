@@ -588,10 +588,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int n = 0; n < N; ++n) {
                     f[n] = 1.0f;
                     if (n >= rows) continue;
-                    const float top = fmaxf(fmaxf(tops[n], tops[N + n]), fmaxf(tops[2 * N + n], tops[3 * N + n])) - kShift;
-                    const bool up = top > m[n];
-                    f[n] = up && m[n] != -INFINITY ? ex2_approx(m[n] - top) : 1.0f;
-                    if (up) m[n] = top;
+                    const float top = fmaxf(fmaxf(tops[n], tops[N + n]), fmaxf(tops[2 * N + n], tops[3 * N + n]));
+                    // (a row's maximum moves for its own scores only: not by what another row's keys hold)
+                    const bool up = top > m[n] + (kShift + kRescaleLog2);
+                    f[n] = up && m[n] != -INFINITY ? ex2_approx(m[n] - (top - kShift)) : 1.0f;
+                    if (up) m[n] = top - kShift;
                     l[n] *= f[n];
                 }
                 if (b > 0) {

@@ -126,3 +126,37 @@ def test_capped_scores_on_both_sides_of_the_formulas(scale, cap):
     got = attend(t, cu, cu, **how)
     for name, (value, bound) in br.attention(t["q"], t["k"], t["v"], cu, cu, dout=t["dout"], **how).items():
         br.check(got[name], value, bound, name)
+
+
+@pytest.mark.parametrize("how", [dict(), dict(cap=20.0), dict(cap=9.0, bias=True), dict(causal=True)])
+@pytest.mark.parametrize("h,hk,dim,dtype,lens", [(4, 1, 64, BF, [1, 3, 2, 2, 1]), (8, 2, 128, FP, [3, 1, 1, 3, 1]), (16, 1, 40, BF, [1, 3, 2, 2, 2]),
+                                                 (24, 1, 128, BF, [1, 3, 2, 2, 2])])
+@pytest.mark.parametrize("value", [math.nan, math.inf, 50.0])
+def test_few_queries_of_several_documents(h, hk, dim, dtype, lens, how, value):
+    """Documents that share a tile of few rows: every other one's keys hold such values."""
+    how = spread(how, h)
+    k_lens = [333, 200, 61, 700, 150]
+    cu_q, cu_k = ([sum(n[:i]) for i in range(6)] for n in (lens, k_lens))
+    t = tensors(cu_q[-1], cu_k[-1], h, hk, dim, dtype)
+    clean = attend(t, cu_q, cu_k, backward=False, **how)
+    for first in (0, 1):
+        docs = tuple((cu_k[d], cu_k[d + 1]) for d in range(first, 5, 2))
+        keep = tuple((cu_q[d], cu_q[d + 1]) for d in range(1 - first, 5, 2))
+        for what in (("k",), ("v",), ("k", "v")):
+            got = attend(with_bad(t, what, value, dict(k=docs, v=docs)), cu_q, cu_k, backward=False, **how)
+            same_at(got, clean, keep, ())
+
+
+@pytest.mark.parametrize("how", [dict(), dict(cap=20.0), dict(cap=9.0, bias=True)])
+@pytest.mark.parametrize("h,hk,dim,dtype,new", [(4, 1, 64, BF, 4), (16, 2, 128, FP, 4), (16, 4, 128, BF, 2), (32, 2, 64, BF, 4)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, 40.0])
+def test_new_tokens_do_not_see_each_others_keys_ahead(h, hk, dim, dtype, new, how, value):
+    """The last token's key and value change: the tokens before it in the same tile keep their bits."""
+    how = dict(spread(how, h), causal=True)
+    cu_q, cu_k = [0, new, 2 * new], [0, 300, 1000]
+    t = tensors(cu_q[-1], cu_k[-1], h, hk, dim, dtype, scale=1.5)
+    clean = attend(t, cu_q, cu_k, backward=False, **how)
+    for what in (("k",), ("v",), ("k", "v")):
+        last = ((299, 300), (999, 1000))
+        got = attend(with_bad(t, what, value, dict(k=last, v=last)), cu_q, cu_k, backward=False, **how)
+        same_at(got, clean, ((0, new - 1), (new, 2 * new - 1)), ())
