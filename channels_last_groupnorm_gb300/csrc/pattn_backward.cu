@@ -513,8 +513,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         unsigned again = failed || part ? 0u : __ballot_sync(0xffffffffu, live && span.lo < span.hi && span.lo <= bad_hi &&
                                                                               span.hi > bad_lo);
-        for (int n = 0; again; again &= again - 1, ++n)
-            if ((n & 1) == half) row_dkv<T>(args.p, info, key - lane + __ffs(again) - 1, hk);
+        for (int n = 0; again; again &= again - 1, ++n) {
+            if ((n & 1) != half) continue;
+            const int from = __ffs(again) - 1;
+            const int i0 = max(__shfl_sync(0xffffffffu, span.lo, from), bad_lo);
+            const int i1 = min(__shfl_sync(0xffffffffu, span.hi, from), bad_hi + 1);
+            bool bad_seen = false;
+            for (int h = hk * group; !bad_seen && h < (hk + 1) * group; ++h)
+                bad_seen = any_not_finite<T>(a.q, a.q_token, h * a.q_head, i0, i1, a.dim) ||
+                           any_not_finite<T>(args.p.dout, args.p.dout_token, h * args.p.dout_head, i0, i1, a.dim);
+            if (bad_seen) row_dkv<T>(args.p, info, key - lane + from, hk);
+        }
         tc_fence_before_sync();
     } else {
         few_registers();
@@ -775,8 +784,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                           a.scale);
             named_sync(1, 256);
             unsigned again = __ballot_sync(0xffffffffu, live && span.x < span.y && span.x <= bad[1] && span.y > bad[0]);
-            for (int n = 0; again; again &= again - 1, ++n)
-                if ((n & 1) == half) row_dq<T>(args.p, info, row - lane + __ffs(again) - 1, h);
+            for (int n = 0; again; again &= again - 1, ++n) {
+                if ((n & 1) != half) continue;
+                const int from = __ffs(again) - 1;
+                const int j0 = max(__shfl_sync(0xffffffffu, span.x, from), bad[0]);
+                const int j1 = min(__shfl_sync(0xffffffffu, span.y, from), bad[1] + 1);
+                if (any_not_finite<T>(a.k, a.k_token, hk * a.k_head, j0, j1, a.dim)) row_dq<T>(args.p, info, row - lane + from, h);
+            }
         }
         tc_fence_before_sync();
     } else {

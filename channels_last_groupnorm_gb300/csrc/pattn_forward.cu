@@ -230,7 +230,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             unsigned again = __ballot_sync(0xffffffffu, row < a.tokens_q && span.lo < span.hi && span.lo <= bad[1] &&
                                                             span.hi > bad[0]);
-            for (; again; again &= again - 1) row_forward<T>(a, args.p.group, row - lane + __ffs(again) - 1, h);
+            for (; again; again &= again - 1) {
+                const int n = __ffs(again) - 1;
+                const int j0 = max(__shfl_sync(0xffffffffu, span.lo, n), bad[0]);
+                const int j1 = min(__shfl_sync(0xffffffffu, span.hi, n), bad[1] + 1);
+                if (any_not_finite<T>(a.v, a.v_token, hk * a.v_head, j0, j1, a.dim))
+                    row_forward<T>(a, args.p.group, row - lane + n, h);
+            }
         }
         tc_fence_before_sync();
     } else {

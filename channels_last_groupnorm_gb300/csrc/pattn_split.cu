@@ -125,7 +125,10 @@ __device__ __forceinline__ void join_parts(const SplitArgs &args, uint32_t stats
     if (split == 0 && warp >= 4 && !failed) {
         unsigned again = __ballot_sync(0xffffffffu, live && span.lo < span.hi && span.lo <= bad_hi && span.hi > bad_lo);
         for (; again; again &= again - 1) {
-            const int row = r - lane + __ffs(again) - 1;
+            const int n = __ffs(again) - 1, row = r - lane + n;
+            const int j0 = max(__shfl_sync(0xffffffffu, span.lo, n), bad_lo);
+            const int j1 = min(__shfl_sync(0xffffffffu, span.hi, n), bad_hi + 1);
+            if (!any_not_finite<T>(a.v, a.v_token, hk * a.v_head, j0, j1, a.dim)) continue;
             row_forward<T>(a, args.p.group, token0 + row / args.heads, hk * args.p.group + first_head + row % args.heads);
         }
     }

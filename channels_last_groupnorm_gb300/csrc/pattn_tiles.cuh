@@ -420,11 +420,34 @@ __device__ __forceinline__ void zero_row(uint32_t tile, int r, int halves)
             sts128(tile + h * kHalfBytes + static_cast<uint32_t>(r) * 128u + c * 16u, make_uint4(0u, 0u, 0u, 0u));
 }
 
+// Whether a warp finds an infinity or a NaN in one head's rows of tokens [lo, hi).
+template <typename T>
+static __device__ __noinline__ bool any_not_finite(const void *base, int64_t token, int64_t head, int lo, int hi, int dim)
+{
+    constexpr uint32_t kExp = IsBf16<T>::value ? 0x7f80u : 0x7c00u;
+    const int lane = threadIdx.x & 31;
+    for (int j0 = lo; j0 < hi; j0 += 32) {
+        uint32_t most = 0;
+        if (j0 + lane < hi) {
+            const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const T *>(base) + (j0 + lane) * token + head);
+            for (int c = 0; c < dim / 8; ++c) {
+                const uint4 v = __ldg(row + c);
+                most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                               __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+            }
+        }
+        if (__any_sync(0xffffffffu, (most & 0xffffu) >= kExp || (most >> 16) >= kExp)) return true;
+    }
+    return false;
+}
+
 // A whole tile's look at its rows (one per thread) ahead of a product whose
 // weights are zero for some of them: 0 x NaN is not 0.  A row with an infinity
 // or a NaN is cleared; if its token lies in [lo, hi), where something in the
-// CTA may see it, it is also noted in bad[0..1] (first and last such token):
-// whatever sees one of those is computed again, one by one, at the end.
+// CTA may see it, it is also noted in bad[0..1] (first and last such token).
+// What sees one of those is computed again, one by one, at the end: of all that
+// see a token between the first and the last, each looks for one that it sees
+// itself (any_not_finite), since the ones around it may be others' alone.
 template <typename T>
 __device__ __forceinline__ void clear_not_finite(uint32_t tile, int r, int token, int lo, int hi, int halves, int *bad)
 {

@@ -130,7 +130,7 @@ def test_capped_scores_on_both_sides_of_the_formulas(scale, cap):
 
 @pytest.mark.parametrize("how", [dict(), dict(cap=20.0), dict(cap=9.0, bias=True), dict(causal=True)])
 @pytest.mark.parametrize("h,hk,dim,dtype,lens", [(4, 1, 64, BF, [1, 3, 2, 2, 1]), (8, 2, 128, FP, [3, 1, 1, 3, 1]), (16, 1, 40, BF, [1, 3, 2, 2, 2]),
-                                                 (24, 1, 128, BF, [1, 3, 2, 2, 2])])
+                                                 (24, 1, 128, BF, [1, 3, 2, 2, 2]), (8, 8, 64, BF, [2, 4, 8, 1, 5])])
 @pytest.mark.parametrize("value", [math.nan, math.inf, 50.0])
 def test_few_queries_of_several_documents(h, hk, dim, dtype, lens, how, value):
     """Documents that share a tile of few rows: every other one's keys hold such values."""
@@ -160,3 +160,38 @@ def test_new_tokens_do_not_see_each_others_keys_ahead(h, hk, dim, dtype, new, ho
         last = ((299, 300), (999, 1000))
         got = attend(with_bad(t, what, value, dict(k=last, v=last)), cu_q, cu_k, backward=False, **how)
         same_at(got, clean, ((0, new - 1), (new, 2 * new - 1)), ())
+
+
+@pytest.mark.parametrize("how", range(len(HOW)))
+@pytest.mark.parametrize("h,hk,dim,dtype", [(2, 1, 64, BF), (3, 3, 128, FP), (8, 1, 24, BF)])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_documents_between_two_that_hold_such_values(how, h, hk, dim, dtype, value):
+    """The first and the last of three hold them, and the middle one none."""
+    how = spread(HOW[how], h)
+    cu_q, cu_k = [0, 37, 90, 222], [0, 41, 111, 280]
+    t = tensors(222, 280, h, hk, dim, dtype)
+    clean = attend(t, cu_q, cu_k, **how)
+    docs = dict(q=((0, 37), (90, 222)), dout=((0, 37), (90, 222)), k=((0, 41), (111, 280)), v=((0, 41), (111, 280)))
+    for what in (("q",), ("k",), ("v",), ("dout",), ("q", "k", "v", "dout")):
+        same_at(attend(with_bad(t, what, value, docs), cu_q, cu_k, **how), clean, ((37, 90),), ((41, 111),))
+
+
+@pytest.mark.parametrize("h,hk,dim,dtype", [(2, 1, 64, BF), (4, 4, 128, FP)])
+@pytest.mark.parametrize("how", [dict(), dict(cap=6.0, bias=True)])
+def test_what_sees_such_a_value_shows_it(h, hk, dim, dtype, how):
+    """One value row, key row, query row or gradient row at a time, of a causal document between two clean ones."""
+    how = dict(spread(how, h), causal=True)
+    cu, at = [0, 50, 300, 340], 200
+    t = tensors(340, 340, h, hk, dim, dtype)
+    clean = attend(t, cu, cu, **how)
+    for name, shows in (("v", {"out": (at, 300), "dq": (at, 300)}), ("k", {"out": (at, 300), "dq": (at, 300)}),
+                        ("q", {"out": (at, at + 1), "dk": (50, at + 1), "dv": (50, at + 1), "dq": (at, at + 1)}),
+                        ("dout", {"dq": (at, at + 1), "dk": (50, at + 1), "dv": (50, at + 1)})):
+        bad = {n: x.clone() for n, x in t.items()}
+        bad[name][at] = math.nan
+        got = attend(bad, cu, cu, **how)
+        for what, (lo, hi) in shows.items():
+            assert torch.isnan(got[what][lo:hi].float()).all(), (name, what)
+            assert torch.equal(got[what][:50], clean[what][:50]) and torch.equal(got[what][300:], clean[what][300:]), (name, what)
+            if what in ("out", "dq"):
+                assert torch.equal(got[what][50:lo], clean[what][50:lo]), (name, what)
