@@ -535,8 +535,8 @@ __global__ void __launch_bounds__(THREADS) norm_direct_kernel(const NormArgs a, 
     const Own<EPV, NV> w(a.weight, a.weight_format, gr, a.cols, 1.f), b(a.bias, a.weight_format, gr, a.cols, 0.f);
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * per; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * per) {
         const int64_t row = r0 + threadIdx.x / tpr;
-        const bool live = row < a.rows;   // whole warps stay for the shuffles
-        const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, live ? row : r0), gr, a.cols);
+        const bool live = row < a.rows;   // whole warps stay for the shuffles (with zeros)
+        const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, live ? row : r0), gr, live ? a.cols : 0);
         norm_row(a, x, w, b, gr, row, live, Straight<T, EPV>());
     }
 }
@@ -557,9 +557,10 @@ __global__ void __launch_bounds__(THREADS, NV == 16 && THREADS == 1024 ? 1 : 0) 
         const int64_t row = r0 + threadIdx.x / tpr;
         const bool live = row < a.rows;
         const int64_t at = live ? row : r0;
-        const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, at), gr, a.cols);
-        const Row<T, EPV, NV> dy(static_cast<const T *>(a.dy) + row_offset(a.dy_at, a.inner, a.rows, at), gr, live ? a.cols : 0);
-        norm_grad_row(a, x, dy, w, sw, sb, a.mean[at], a.rstd[at], gr, row, live, [] {}, Straight<T, EPV>());
+        const int cols = live ? a.cols : 0;   // (a row that is not there is zeros, not row r0, which may be overwritten meanwhile)
+        const Row<T, EPV, NV> x(static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, at), gr, cols);
+        const Row<T, EPV, NV> dy(static_cast<const T *>(a.dy) + row_offset(a.dy_at, a.inner, a.rows, at), gr, cols);
+        norm_grad_row(a, x, dy, w, sw, sb, live ? a.mean[at] : 0.f, live ? a.rstd[at] : 0.f, gr, row, live, [] {}, Straight<T, EPV>());
     }
     if (!a.weight) return;
     write_partial<EPV, NV>(a, sw, sb, gr, blockDim.x, reinterpret_cast<float *>(smem));

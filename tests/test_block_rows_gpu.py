@@ -113,3 +113,19 @@ def test_broadcast_outputs_are_refused():
         assert gn.layer_norm(cube, out=rand((4, 64), BF, 19).expand(3, 4, 64)) is None
     torch.cuda.synchronize()
     assert torch.equal(row, keep)
+
+
+@pytest.mark.parametrize("rows,cols", [(9, 256), (1, 128), (3, 64), (17, 255), (5, 1003), (1025, 32)])
+def test_gradient_in_place_whose_last_row_overflows(rows, cols):
+    """dx written over x, past fp16's range in the last row: the threads that have
+    no row beside it bring none of its infinities into the weight's gradient."""
+    for n in range(10):
+        x, dy = rand((rows, cols), FP, 20 + n, 2.0 ** -12), rand((rows, cols), FP, 40 + n)
+        dy[-1, ::2] = 6e4
+        w, b = rand((cols,), F32, 3, 0.3, 1.0), rand((cols,), F32, 4)
+        y, mean, rstd = gn.layer_norm(x, w, b, eps=1e-12)
+        dx, dw, db = gn.layer_norm_backward(dy, x, mean, rstd, w)
+        assert torch.isinf(dx[-1]).any() and torch.isfinite(dw).all() and torch.isfinite(db).all()
+        onto = x.clone()
+        again = gn.layer_norm_backward(dy, onto, mean, rstd, w, out=onto)
+        assert all(torch.equal(p, q) for p, q in zip(again, (dx, dw, db)))
