@@ -139,9 +139,6 @@ __device__ __noinline__ void row_dkv(const PackedAttn &p, const Info &info, int 
     store4<T>(p.dv, (static_cast<int64_t>(j) * a.kv_heads + hk) * a.dim, lane, a.dim, dv);
 }
 
-// What a kernel is built for: scores capped, biased by distance.
-constexpr int kCap = 1, kBias = 2;
-
 // Scores of N pairs (raw, in place) to what times the returned factor is in
 // units of log2 before lse, capped, and biased by the distance |at + DIR n| (or,
 // for queries of several documents, by what far(n) says).  slack[n], with a cap:

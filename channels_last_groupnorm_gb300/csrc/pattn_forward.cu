@@ -49,7 +49,7 @@ __host__ __device__ inline Layout layout(int halves)
     return l;
 }
 
-template <typename T, bool GENERAL>
+template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ TileArgs args)
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128 * tile, to = tmem + lanes + 256 + 128 * tile;
         const int b0 = tile ? first[1] : first[0], b1 = tile ? last[1] : last[0];
-        const float slope2 = GENERAL && a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
+        const float slope2 = (MODE & kBias) && a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
         float m = -INFINITY, l = 0.f;
         bool go = !skip;
         for (int b = b0; go && b < b1; ++b) {
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             float s[kTile];
             tmem_ld_all(ts, s);
-            const float c = bend_scores<GENERAL>(s, a, args.scale_log2, slope2, span.pos - j0);
+            const float c = bend_scores<MODE>(s, a, args.scale_log2, slope2, span.pos - j0);
             if (masked) mask_scores(s, span.lo - j0, static_cast<unsigned>(max(0, span.hi - span.lo)));
             const float mx = top_score(s) * c;
             const bool grew = mx > m + (kShift + kRescaleLog2) || (b == b0 && mx > m);
@@ -328,19 +328,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <typename T, bool GENERAL>
+template <typename T, int MODE>
 cudaError_t launch(const TileArgs &args, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                    cudaStream_t s)
 {
     const int halves = args.p.a.dim > 64 ? 2 : 1;
     const size_t smem = layout(halves).total + 1024;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(attn_forward_kernel<T, GENERAL>),
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(attn_forward_kernel<T, MODE>),
                                        layout(2).total + 1024, done);
     if (e != cudaSuccess) return e;
     const int64_t grid = static_cast<int64_t>(args.tiles) * args.p.a.heads;
-    return tc::launch_pdl(attn_forward_kernel<T, GENERAL>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, mq,
+    return tc::launch_pdl(attn_forward_kernel<T, MODE>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, mq,
                           mk, mv, args);
+}
+
+template <typename T>
+cudaError_t launch_mode(int mode, const TileArgs &args, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                        cudaStream_t s)
+{
+    if (mode == 0) return launch<T, 0>(args, mq, mk, mv, s);
+    if (mode == kCap) return launch<T, kCap>(args, mq, mk, mv, s);
+    if (mode == kBias) return launch<T, kBias>(args, mq, mk, mv, s);
+    return launch<T, kCap | kBias>(args, mq, mk, mv, s);
 }
 
 }  // namespace
@@ -359,10 +369,8 @@ cudaError_t launch_packed_attn_tiles(const PackedAttn &p, const WaitLimit &limit
     args.scale_log2 = a.scale * kLog2e;
     args.limit = limit;
     args.tiles = static_cast<int>((a.tokens_q + 2 * kTile - 1) / (2 * kTile));
-    const bool general = a.cap > 0.f || a.slopes || !(a.scale > 0.f);
-    if (bf16)
-        return general ? launch<__nv_bfloat16, true>(args, mq, mk, mv, s) : launch<__nv_bfloat16, false>(args, mq, mk, mv, s);
-    return general ? launch<__half, true>(args, mq, mk, mv, s) : launch<__half, false>(args, mq, mk, mv, s);
+    const int mode = score_mode(a);
+    return bf16 ? launch_mode<__nv_bfloat16>(mode, args, mq, mk, mv, s) : launch_mode<__half>(mode, args, mq, mk, mv, s);
 }
 
 }  // namespace gn

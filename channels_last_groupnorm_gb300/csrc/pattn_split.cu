@@ -134,7 +134,7 @@ __device__ __forceinline__ void join_parts(const SplitArgs &args, uint32_t stats
     }
 }
 
-template <typename T, bool GENERAL>
+template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 2)
     attn_split_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SplitArgs args)
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = t_s + lanes, to = t_o + lanes;
         const bool busy = (warp & 3) * 32 < rows;    // has any row
-        const float slope2 = GENERAL && a.slopes && live ? __ldg(a.slopes + h) * kLog2e : 0.f;
+        const float slope2 = (MODE & kBias) && a.slopes && live ? __ldg(a.slopes + h) * kLog2e : 0.f;
         for (int b = 0; b < blocks; ++b) {
             const int j0 = k_first + b * kTile;
             const bool masked = j0 < all_lo || j0 + kTile > all_hi;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 float s[64], c = 1.0f;
                 const auto scores = [&](int q) {
                     tmem_ld_all(ts + 64 * q, s);
-                    c = bend_scores<GENERAL>(s, a, args.scale_log2, slope2, span.pos - j0 - 64 * q);
+                    c = bend_scores<MODE>(s, a, args.scale_log2, slope2, span.pos - j0 - 64 * q);
                     if (masked) mask_scores(s, span.lo - j0 - 64 * q, static_cast<unsigned>(max(0, span.hi - span.lo)));
                 };
                 scores(0);
@@ -406,7 +406,7 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&v)[N])
     tmem_wait_ld();
 }
 
-template <typename T, bool GENERAL, int N>
+template <typename T, int MODE, int N>
 __global__ void __launch_bounds__(kThreads, 2)
     attn_few_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ SplitArgs args)
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!some) span.lo = span.hi = 0;
         if (r < N)
             info[r] = make_int4(span.lo, span.hi, span.pos,
-                                __float_as_int(GENERAL && a.slopes && live ? __ldg(a.slopes + h) * kLog2e : 0.f));
+                                __float_as_int((MODE & kBias) && a.slopes && live ? __ldg(a.slopes + h) * kLog2e : 0.f));
         const int lo = __reduce_min_sync(0xffffffffu, some ? span.lo : 0x7fffffff);
         const int hi = __reduce_max_sync(0xffffffffu, some ? span.hi : 0);
         const int all_lo = __reduce_max_sync(0xffffffffu, !live ? 0 : (some ? span.lo : 0x7fffffff));
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             l[n] = 0.f;
         }
         float by = args.scale_log2, inv_cap = 0.f;
-        if (GENERAL && a.cap > 0.f) {
+        if (MODE & kCap) {
             by = a.cap * kLog2e;
             inv_cap = a.scale / a.cap;
         }
@@ -567,11 +567,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 if (n >= rows) break;             // (the same for all: rows that are not there cost nothing)
-                if (GENERAL && a.cap > 0.f) s[n] = tanh_fast(s[n] * inv_cap);
+                if (MODE & kCap) s[n] = tanh_fast(s[n] * inv_cap);
                 s[n] *= by;
-                if (GENERAL || masked) {
+                if ((MODE & kBias) || masked) {
                     const int4 w = info[n];
-                    if (GENERAL && a.slopes) s[n] = fmaf(-__int_as_float(w.w), fabsf(static_cast<float>(w.z - j)), s[n]);
+                    if (MODE & kBias) s[n] = fmaf(-__int_as_float(w.w), fabsf(static_cast<float>(w.z - j)), s[n]);
                     if (masked) s[n] = j >= w.x && j < w.y ? s[n] : -INFINITY;
                 }
                 grew = grew || s[n] > m[n] + (kShift + kRescaleLog2);
@@ -668,13 +668,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const SplitArgs);
 
-template <typename T, bool GENERAL>
+template <typename T, int MODE>
 cudaError_t launch(const SplitArgs &args, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s)
 {
     const int halves = args.p.a.dim > 64 ? 2 : 1, rows = args.tokens * args.heads;
     static std::atomic<uint64_t> done[3], wide[3];
     const int which = rows <= 16 ? 0 : (rows <= 32 ? 1 : 2);
-    const Kernel kernels[3] = {attn_few_kernel<T, GENERAL, 16>, attn_few_kernel<T, GENERAL, 32>, attn_split_kernel<T, GENERAL>};
+    const Kernel kernels[3] = {attn_few_kernel<T, MODE, 16>, attn_few_kernel<T, MODE, 32>, attn_split_kernel<T, MODE>};
     const Kernel kernel = kernels[which];
     // (never so little that three CTAs would share an SM: attn_split_kernel's
     // take 256 columns of its 512 of tensor memory each)
@@ -699,6 +699,16 @@ cudaError_t launch(const SplitArgs &args, const CUtensorMap &mq, const CUtensorM
     cfg.attrs = at;
     cfg.numAttrs = args.splits > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, args);
+}
+
+template <typename T>
+cudaError_t launch_mode(int mode, const SplitArgs &args, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                        cudaStream_t s)
+{
+    if (mode == 0) return launch<T, 0>(args, mq, mk, mv, s);
+    if (mode == kCap) return launch<T, kCap>(args, mq, mk, mv, s);
+    if (mode == kBias) return launch<T, kBias>(args, mq, mk, mv, s);
+    return launch<T, kCap | kBias>(args, mq, mk, mv, s);
 }
 
 // A call's tiles and splits, and about how long it takes (us).
@@ -755,10 +765,8 @@ cudaError_t launch_packed_attn_split(const PackedAttn &p, int sm_count, const Wa
         !encode_heads(&mk, a.k, bf16, a.tokens_k, a.k_token, a.kv_heads, a.k_head, a.dim) ||
         !encode_heads(&mv, a.v, bf16, a.tokens_k, a.v_token, a.kv_heads, a.v_head, a.dim))
         return cudaErrorInvalidValue;
-    const bool general = a.cap > 0.f || a.slopes || !(a.scale > 0.f);
-    if (bf16)
-        return general ? launch<__nv_bfloat16, true>(args, mq, mk, mv, s) : launch<__nv_bfloat16, false>(args, mq, mk, mv, s);
-    return general ? launch<__half, true>(args, mq, mk, mv, s) : launch<__half, false>(args, mq, mk, mv, s);
+    const int mode = score_mode(a);
+    return bf16 ? launch_mode<__nv_bfloat16>(mode, args, mq, mk, mv, s) : launch_mode<__half>(mode, args, mq, mk, mv, s);
 }
 
 }  // namespace gn

@@ -172,24 +172,32 @@ __device__ __forceinline__ void mma_channels(uint32_t d, uint32_t a_tmem, uint32
     __syncwarp();
 }
 
+// What a kernel is built for: scores capped, biased by distance.
+constexpr int kCap = 1, kBias = 2;
+
 // ---- the cap's tanh, for N scores in place -------------------------------------------
-// v <- tanh(v k).  Scores are mostly small against their cap: up to 1/4 the
-// series of tanh to x^9 is good to fp32 (the next term is 9e-9 of x there), two
-// scores per instruction and no special-function unit; beyond, 1 - 2 / (1 +
-// e^2|x|) with two of its instructions each.  A score's value depends on itself
-// alone, never on its neighbours, which may be ones that nobody sees: the warp
-// leaves the second formula out where no score wants it, and otherwise takes
-// either for each.  (NaN passes through both.)
+// v <- tanh(v k).  Scores are mostly small against their cap: up to 1/2 by x + x^3
+// p(x^2), two scores per instruction and no special-function unit; beyond, by 1 - 2 /
+// (1 + e^2|x|) with two of its instructions each.  p is the polynomial of degree
+// three whose largest relative error is least there, 2^-26 (Remez' exchange on
+// tanh(x) / x in 40 digits; the coefficients' sum in fp32 is within 1.3 2^-24).
+// A score's value depends on itself alone, never on its neighbours, which may be
+// ones that nobody sees: the warp leaves the second formula out where no score
+// wants it, and otherwise takes either for each (NaN passes through both).  Choosing
+// one for the whole warp or for a thread's scores would let unseen ones have a say,
+// or want them cleared first.  (4360 tokens, 16 heads on 4, D = 64, prefix mask,
+// scores of deviation 2: cap 50 and 30 80 us forward, cap 2 120 us; the series of
+// tanh up to 1/4 79, 158 and 120; a choice per thread 95, 136 and 113.)
 template <int N>
 __device__ __forceinline__ void tanh_all(float (&v)[N], float k)
 {
-    constexpr float kSmall = 0.25f;
+    constexpr float kSmall = 0.5f;
     const uint64_t k2 = pack2(k, k);
-    const uint64_t c9 = pack2(62.f / 2835.f, 62.f / 2835.f), c7 = pack2(-17.f / 315.f, -17.f / 315.f);
-    const uint64_t c5 = pack2(2.f / 15.f, 2.f / 15.f), c3 = pack2(-1.f / 3.f, -1.f / 3.f);
-    const auto series = [&](uint64_t x) {
-        const uint64_t y = mul2(x, x), s = fma2(fma2(fma2(c9, y, c7), y, c5), y, c3);
-        return unpack2(fma2(mul2(x, y), s, x));
+    const uint64_t c0 = pack2(-0.33333144f, -0.33333144f), c1 = pack2(0.13325879f, 0.13325879f);
+    const uint64_t c2 = pack2(-0.053045496f, -0.053045496f), c3 = pack2(0.017241493f, 0.017241493f);
+    const auto small = [&](uint64_t x) {
+        const uint64_t y = mul2(x, x), p = fma2(fma2(fma2(c3, y, c2), y, c1), y, c0);
+        return unpack2(fma2(mul2(x, y), p, x));
     };
     float top = 0.f;
 #pragma unroll
@@ -197,14 +205,14 @@ __device__ __forceinline__ void tanh_all(float (&v)[N], float k)
     if (__all_sync(0xffffffffu, top * fabsf(k) <= kSmall)) {
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            const float2 r = series(mul2(pack2(v[i], v[i + 1]), k2));
+            const float2 r = small(mul2(pack2(v[i], v[i + 1]), k2));
             v[i] = r.x;
             v[i + 1] = r.y;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            const float2 x = unpack2(mul2(pack2(v[i], v[i + 1]), k2)), r = series(pack2(x.x, x.y));
+            const float2 x = unpack2(mul2(pack2(v[i], v[i + 1]), k2)), r = small(pack2(x.x, x.y));
             v[i] = fabsf(v[i]) * fabsf(k) <= kSmall ? r.x : tanh_fast(x.x);
             v[i + 1] = fabsf(v[i + 1]) * fabsf(k) <= kSmall ? r.y : tanh_fast(x.y);
         }
@@ -249,19 +257,6 @@ __device__ __forceinline__ void tmem_ld_all(uint32_t taddr, float (&v)[N])
         for (int i = 0; i < 32; ++i) v[32 * q + i] = __uint_as_float(u[i]);
     }
     tmem_wait_ld();
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
-          "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
-          "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16])
@@ -313,27 +308,21 @@ __device__ __forceinline__ void take_distance(float (&s)[N], float by, float slo
 }
 
 // ---- scores of one query against N neighbouring keys -----------------------------------
-// In place, to what times the returned factor is in units of log2 (capped,
-// biased, masked).  at: the query's position relative to the first key; keys lo
-// .. lo + len - 1, relative to it too, are seen.  Without GENERAL (no cap, no
-// bias, a positive scale) the raw scores only want their factor.
-template <bool GENERAL, int N>
+// In place, to what times the returned factor is in units of log2 (capped and
+// biased).  at: the query's position relative to the first key.  Without a cap or
+// a bias (and with a positive scale: see score_mode) the raw scores only want
+// their factor.
+template <int MODE, int N>
 __device__ __forceinline__ float bend_scores(float (&s)[N], const gn_attn_packed_args &a, float scale_log2, float slope2,
                                              int at)
 {
-    if (!GENERAL) return scale_log2;
     float by = scale_log2;
-    if (a.cap > 0.f) {
+    if (MODE & kCap) {
         tanh_all(s, a.scale / a.cap);
         by = a.cap * kLog2e;
     }
-    if (a.slopes) {
-        take_distance<-1>(s, by, slope2, at);
-        return 1.0f;
-    }
-    if (by > 0.f) return by;
-#pragma unroll
-    for (int k = 0; k < N; ++k) s[k] *= by;
+    if (!(MODE & kBias)) return by;
+    take_distance<-1>(s, by, slope2, at);
     return 1.0f;
 }
 
@@ -384,6 +373,16 @@ __device__ __forceinline__ void weigh_32(const float *s, uint64_t c2, uint64_t m
         sum2[k & 1] = add2(sum2[k & 1], pack2(p0, p1));
         pk[k] = Half2<T>::pack(p0, p1);
     }
+}
+
+// The forward kernels' MODE of a call (a scale that is not positive needs more
+// than a factor at the end: a bias with slopes of 0).  The modes have kernels of
+// their own: the cap's tanh, never taken, cost a biased call of 16384 tokens, 8 heads,
+// D = 96 29 us of 522.
+inline int score_mode(const gn_attn_packed_args &a)
+{
+    const int mode = (a.cap > 0.f ? kCap : 0) | (a.slopes ? kBias : 0);
+    return mode == 0 && !(a.scale > 0.f) ? kBias : mode;
 }
 
 // A float at the same place of the shared memory of CTA `rank` of the cluster.
