@@ -391,13 +391,15 @@ def attention_packed(q, k, v, cu_q=None, cu_k=None, causal: bool = False, prefix
     (images of several sizes with their texts, prompts, new tokens beside a
     cache): q [Tq, H, D], k and v [Tk, Hk, D] in bf16 or fp16, Hk dividing H,
     D a multiple of 8 up to 128, any token and head strides that are multiples
-    of 8 elements.  Returns ``(out, lse)`` -- out [Tq, H, D] contiguous, lse
+    of 8 elements and at least D.  Returns ``(out, lse)`` -- out [Tq, H, D] contiguous, lse
     [H, Tq] fp32, natural -- or None when not supported.
 
     ``cu_q`` and ``cu_k`` (int32 [docs + 1], on the GPU) hold where each
     document's queries and keys begin; both None: one document of everything.
     A document's last query stands at its last key, so one query for each
-    document is a decode step.  A query sees its document's keys: all of them,
+    document is a decode step; room behind a cache's documents is told by
+    documents without queries (cu_q 0 1 1 2 2 ..., cu_k 0 end begin end ...).
+    A query sees its document's keys: all of them,
     or with ``causal`` those up to its own position and the first
     ``prefix[d]`` (int32 [docs]).  ``cap``: scores are bent to cap tanh(t /
     cap).  ``slopes`` (fp32 [H]): slopes[h] times the distance of the two
@@ -421,9 +423,9 @@ def attention_packed(q, k, v, cu_q=None, cu_k=None, causal: bool = False, prefix
 def attention_packed_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, causal: bool = False, prefix=None,
                               slopes=None, cap: float = 0.0, scale=None, stream=None):
     """Backward pass of ``attention_packed``: ``(dq, dk, dv)``, contiguous and
-    shaped like q, k and v, from the gradient dout of its output (any strides
-    that are multiples of 8 elements), its inputs and what it returned; the
-    remaining arguments as for the forward call.  dk and dv are summed over
+    shaped like q, k and v, from the gradient dout of its output (strides as
+    for q), its inputs and what it returned; the remaining arguments as for the
+    forward call.  In fp16, scale the loss so that dout is not far below 1.  dk and dv are summed over
     the query heads that share a key / value head.  The slopes have no
     gradient.  None when not supported."""
     L, T = _start()

@@ -1109,8 +1109,8 @@ Direct direct_shape(int slots, bool vec, int64_t rows, int sm_count)
         // or 16, which leave a row to a warp or a few and several rows to a CTA
         // (forward and backward, fp32 and weight: 12000 x 131 21 + 43 us with four,
         // 13 + 24 with 8; 6600 x 4001 106 + 136 with four, 54 + 83 with 16).  Rows of
-        // up to 1024 fill them later (4800 x 515 fp16 backward 27 with 16, 3001 x 1003
-        // 39 with 16 and 26 with four).
+        // up to 1024 fill them later (3001 x 1003 18 + 24 with four, 18 + 31 with 16;
+        // 4800 x 515 20 + 26 and 18 + 28; 9000 x 515 29 + 36 and 22 + 36).
         const int few = (slots > 256 && slots <= 1024 ? 32 : 4) * sm_count;
         d.nv = slots <= 128 || (slots <= 4096 && rows <= few) ? 4 : slots <= 256 ? 8 : 16;
     }
@@ -1171,7 +1171,7 @@ cudaError_t backward(const NormGradArgs &a, int sm_count, const WaitLimit &limit
     const int64_t per = d.threads / d.tpr;
     *blocks = static_cast<int>(std::min<int64_t>((a.rows + per - 1) / per, layer_norm_blocks(a.rows, a.cols, sm_count)));
     const dim3 grid(static_cast<unsigned>(*blocks));
-    // (several groups only for rows of up to 32 threads: 16 KB at most)
+    // (several groups for rows of up to 128 threads: 32 KB at most)
     const size_t smem = columns_bytes(a, d.tpr, d.threads);
     if (vec && d.nv == 1) return tc::launch_pdl(norm_grad_direct_kernel<T, EPV, 1, 1024>, grid, dim3(d.threads), smem, s, a, d.tpr);
     if (vec) return tc::launch_pdl(norm_grad_direct_kernel<T, EPV, 4, EPV == 8 ? 512 : 1024>, grid, dim3(d.threads), smem, s, a, d.tpr);

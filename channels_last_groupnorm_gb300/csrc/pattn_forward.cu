@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *range = reinterpret_cast<volatile int *>(words + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x % a.heads, hk = h / args.p.group;
-    // the last tiles first: with causal runs they have the most keys
+    // the last tiles first: with causal runs they have the most keys (without, a
+    // document's length decides, which no order of the tiles knows)
     const int row0 = (args.tiles - 1 - static_cast<int>(blockIdx.x / a.heads)) * 2 * kTile;
 
     if (threadIdx.x == 0) {

@@ -9,8 +9,8 @@
 //  * the keys are split between the CTAs of a cluster (up to 16), each with
 //    its own blocks of 128, and the parts are joined over distributed shared
 //    memory at the end: one launch, no workspace;
-//  * two CTAs share an SM, so that one's start, softmax or end is covered by the
-//    other's loads.
+//  * two CTAs share an SM where their shared memory lets them (plan), so that
+//    one's start, softmax or end is covered by the other's loads.
 // Two kernels, by the number of rows:
 //  * up to 32 (attn_few_kernel): the keys are the accumulator's lanes and the
 //    rows its columns, S^T = K Q^T and O^T += V^T P^T, so that every thread of
@@ -713,10 +713,10 @@ cudaError_t launch_mode(int mode, const SplitArgs &args, const CUtensorMap &mq, 
 
 // A call's tiles and splits, and about how long it takes (us).
 //
-// Splits: the number that should end first.  CTAs run in rounds of two per SM,
-// and one takes as long as its blocks and about seven more (start, first loads
-// and join: 9 us where a block of its stream takes 1.3 us, or 2.2 us with more
-// than 32 rows); documents are taken for half as long again as their average,
+// Splits: the number that should end first.  CTAs are taken to run in rounds of
+// two per SM (also where an SM holds one), and one takes as long as its blocks and
+// about seven more (start, first loads and join: 9 us where a block of its stream
+// takes 1.3 us, or 2.2 us with more than 32 rows); documents are taken for half as long again as their average,
 // since the longest ends last.  (24 caches of 2880 keys, 8 heads: 192 tiles, 3
 // splits: two rounds.)
 SplitArgs plan(const PackedAttn &p, int sm_count, double *us)
@@ -729,7 +729,9 @@ SplitArgs plan(const PackedAttn &p, int sm_count, double *us)
     args.chunks = (p.group + args.heads - 1) / args.heads;
     const int64_t per_doc = (a.tokens_q + a.docs - 1) / a.docs;
     args.tokens = static_cast<int>(std::min<int64_t>(kTile / args.heads, per_doc));
-    args.stages = a.dim > 64 ? 3 : 5;      // (two CTAs' shared memory fits an SM)
+    // (with up to 16 rows two CTAs' shared memory fits an SM, and so it does with 33
+    // to 56, or with more of up to 64 channels; otherwise an SM holds one)
+    args.stages = a.dim > 64 ? 3 : 5;
     const int64_t tiles = (a.tokens_q + args.tokens - 1) / args.tokens * a.kv_heads * args.chunks;
     const double blocks = 1.5 * static_cast<double>(a.tokens_k) / a.docs / kTile;
     double best = 0.0;

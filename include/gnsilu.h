@@ -564,8 +564,12 @@ int gn_rope_nd(const void *q, const void *k, void *q_out, void *k_out, const int
  * does not see (infinities and NaN too) has no influence on it.  Query head h
  * reads key / value head h / (heads / kv_heads).  Scores, softmax and sums are
  * fp32; the weights and the scores' gradients are rounded to the half format
- * for the tensor cores' products.  Nothing depends on the order of atomics:
- * the same inputs give the same bits.
+ * for the tensor cores' products.  In fp16 the scores' gradients (a weight times
+ * dout . v) keep their bits down to 2^-14: scale the loss so that dout is not far
+ * below 1.  Nothing depends on the order of atomics: the same inputs give the same
+ * bits.
+ * A cache with room behind each document is told by documents without queries:
+ * cu_q = 0 1 1 2 2 3 3 ..., cu_k = 0 end0 begin1 end1 begin2 ...
  */
 typedef struct gn_attn_packed_args {
     const void *q, *k, *v;        /* DEVICE [tokens_q][heads][dim], [tokens_k][kv_heads][dim] twice */

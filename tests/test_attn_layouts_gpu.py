@@ -66,6 +66,34 @@ def test_every_count_of_few_rows(h, hk, new, dim):
         check([new] * 3, [700, new, 129], h, hk, dim, BF, False, **how)
 
 
+def test_cache_with_room_behind_each_document():
+    """Room is told by documents without queries; whatever it holds changes nothing."""
+    lens, room = [700, 1, 129, 333, 50], [68, 127, 383, 179, 14]
+    q = rand((5, 16, 128), BF, 1)
+    k, v = (rand((sum(lens), 4, 128), BF, s) for s in (2, 3))
+    ends = lambda e: torch.tensor(e, dtype=torch.int32, device="cuda")  # noqa: E731
+    cu = [sum(lens[:n]) for n in range(6)]
+    want = br.attention(q, k, v, list(range(6)), cu, causal=True)
+    for fill in (0.0, float("nan")):
+        wide_k, wide_v = (torch.full((sum(lens) + sum(room), 4, 128), fill, dtype=BF, device="cuda") for _ in range(2))
+        cu_q, cu_k, at = [0], [0], 0
+        for n, (length, free) in enumerate(zip(lens, room)):
+            wide_k[at:at + length], wide_v[at:at + length] = k[cu[n]:cu[n + 1]], v[cu[n]:cu[n + 1]]
+            at += length + free
+            cu_q += [n + 1, n + 1]
+            cu_k += [at - free, at]
+        out, lse = gn.attention_packed(q, wide_k, wide_v, ends(cu_q), ends(cu_k), causal=True)
+        br.check(out, *want["out"], "out")
+        br.check(lse, *want["lse"], "lse")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+@pytest.mark.parametrize("q_lens,k_lens,h,hk,dim", [([200, 7], [200, 300], 2, 2, 64), ([1, 1], [300, 5], 8, 2, 128), ([3, 2], [300, 70], 40, 2, 64)])
+def test_scales_that_are_not_positive(q_lens, k_lens, h, hk, dim, scale):
+    for how in (dict(), dict(cap=3.0), dict(slopes=torch.full((h,), 0.05, device="cuda")), dict(causal=True)):
+        check(q_lens, k_lens, h, hk, dim, BF, True, scale=scale, **how)
+
+
 def test_norm_and_rotation_on_another_stream():
     """The work lands on the stream that was named, and its inputs may be let go at once."""
     x, w, b = rand((3001, 1536), BF, 1, 2.0), rand((1536,), F32, 2), rand((1536,), F32, 3)
