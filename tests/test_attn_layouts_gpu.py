@@ -116,3 +116,26 @@ def test_norm_and_rotation_on_another_stream():
     side.synchronize()
     assert torch.equal(y2, y) and torch.equal(m2, mean) and torch.equal(r2, rstd)
     assert all(torch.equal(p, s) for p, s in zip(g2 + t2, grads + turned))
+
+
+def test_norm_and_rotation_in_a_graph():
+    """Forward and backward captured together, replayed on new inputs."""
+    x, w, b = rand((2003, 1000), BF, 1, 2.0), rand((1000,), F32, 2), rand((1000,), F32, 3)
+    dy = rand(x.shape, BF, 4)
+    q, k = rand((500, 6, 128), BF, 5), rand((500, 2, 128), BF, 6)
+    pos = torch.arange(1000, device="cuda", dtype=torch.int32).view(500, 2)
+
+    def run():
+        y, mean, rstd = gn.layer_norm(x, w, b)
+        return (y, mean, rstd, *gn.layer_norm_backward(dy, x, mean, rstd, w), *gn.rope_nd(q, k, pos, [64, 64]))
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    for seed in (7, 8):
+        x.copy_(rand(x.shape, BF, seed))
+        q.copy_(rand(q.shape, BF, seed))
+        pos.add_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(captured, run()))
