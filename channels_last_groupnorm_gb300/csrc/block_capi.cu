@@ -64,6 +64,21 @@ bool side_by_side(const TokenSlice &a, const TokenSlice &b, size_t size)
            off + static_cast<uintptr_t>(hi.extent) * size <= static_cast<uintptr_t>(lo.token) * size;
 }
 
+// Whether some of tokens x heads runs of `dim` elements lie on one another.
+bool collide(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t dim)
+{
+    if ((tokens > 1 && token < dim) || (heads > 1 && head < dim)) return true;
+    if (tokens <= 1 || heads <= 1) return false;
+    // heads within tokens, or tokens within heads
+    if (token - dim >= (heads - 1) * head || head - dim >= (tokens - 1) * token) return false;
+    // some heads further on, and some tokens further back
+    for (int64_t h = 1; h < heads; ++h) {
+        const int64_t t = h * head / token, left = h * head - t * token;
+        if ((t < tokens && left < dim) || (t + 1 < tokens && token - left < dim)) return true;
+    }
+    return false;
+}
+
 // The device's properties, or the status to return.
 int ready(DeviceInfo *d)
 {
@@ -249,11 +264,10 @@ int gn_rope_nd(const void *q, const void *k, void *q_out, void *k_out, const int
         a.out_token[i] = strides[4 + 2 * i];
         a.out_head[i] = strides[4 + 2 * i + 1];
         if (!in[i]) continue;
-        // an output's heads (and tokens) must not lie on one another
-        if ((count[i] > 1 && a.out_head[i] < dim) || (tokens > 1 && a.out_token[i] < dim)) return GN_ERR_SHAPE;
         if (!strided(&ri[i], in[i], tokens, a.in_token[i], count[i], a.in_head[i], dim, size) ||
             !strided(&ro[i], out[i], tokens, a.out_token[i], count[i], a.out_head[i], dim, size))
             return GN_ERR_SHAPE;
+        if (collide(tokens, a.out_token[i], count[i], a.out_head[i], dim)) return GN_ERR_SHAPE;
     }
     for (int i = 0; i < 2; ++i) {
         if (!in[i]) continue;

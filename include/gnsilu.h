@@ -533,8 +533,9 @@ int gn_layer_norm_backward(const void *dy, const void *x, const void *weight, co
  *   q, k       : DEVICE [tokens][heads][dim] and [tokens][kv_heads][dim] with
  *                the strides given, channels contiguous; k may be NULL with
  *                kv_heads 0.  Both are turned in one launch.
- *   q_out, k_out : DEVICE outputs; each may equal its input with the same
- *                strides (in place), but overlap no input otherwise.
+ *   q_out, k_out : DEVICE outputs, no two of whose heads lie on one another; each
+ *                may equal its input with the same strides (in place), but overlap
+ *                no input otherwise.
  *   strides    : HOST [8], elements: token and head stride of q, k, q_out, k_out.
  *   positions  : DEVICE [tokens][axes] contiguous, enum gn_position_format.
  *   axes_dim   : HOST [axes], even numbers >= 2, 1 <= axes <= 8,

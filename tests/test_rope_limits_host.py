@@ -1,5 +1,6 @@
-"""How many channels of a token gn_rope_nd takes, without a GPU: the kernel
-counts a token's pieces in 32 bits."""
+"""What gn_rope_nd refuses of sizes and output strides, without a GPU: the kernel
+counts a token's pieces in 32 bits, and no two heads of its outputs may lie on
+one another."""
 import ctypes
 
 import pytest
@@ -32,3 +33,21 @@ def test_more_pieces_than_are_counted(heads, kv_heads, dim, interleaved):
 @pytest.mark.parametrize("heads,kv_heads,dim", [(16384, 16384, 32768), (65536, 65536, 8192), (8191, 8193, 65536), (48, 8, 128)])
 def test_as_many_as_are_counted(heads, kv_heads, dim):
     assert rope(heads, kv_heads, dim) == gs.GN_ERR_ALIAS
+
+
+def lies(token, head, tokens=3, heads=3, dim=64):
+    """The status for outputs with these strides (refused in any case: the positions lie on an output)."""
+    far = 1 << 20
+    strides = (ctypes.c_int64 * 8)(far, dim, far, dim, token, head, token, head)
+    return gs.lib().gn_rope_nd(A, B, C, D, strides, tokens, heads, heads, dim, C, 0, 1, (ctypes.c_int64 * 1)(64), 1e4, 1, 0, 0, None)
+
+
+@pytest.mark.parametrize("token,head", [(64, 64), (128, 64), (64, 128), (100, 200), (128, 250), (65, 130), (191, 65), (0, 64), (64, 0)])
+def test_output_heads_on_one_another(token, head):
+    assert lies(token, head) == gs.GN_ERR_SHAPE
+
+
+@pytest.mark.parametrize("token,head", [(192, 64), (64, 192), (256, 128), (80, 224), (192, 128), (224, 80), (128, 193)])
+def test_output_heads_beside_one_another(token, head):
+    spots = sorted(t * token + h * head for t in range(3) for h in range(3))
+    assert all(b - a >= 64 for a, b in zip(spots, spots[1:])) == (lies(token, head) == gs.GN_ERR_ALIAS)
