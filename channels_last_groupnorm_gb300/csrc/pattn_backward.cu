@@ -118,6 +118,7 @@ __device__ __noinline__ void row_dq(const PackedAttn &p, const Info &info, int i
         float slack;
         const float t = score_log2(a, slope, warp_sum(dot4(q, k)), s.z, j, slack);
         axpy4(acc, ex2_approx(t + nlse) * (warp_sum(dot4(g, v)) + ndelta) * slack * a.scale, k);
+        if (all_nan(acc, lane, a.dim)) break;
     }
     store4<T>(p.dq, (static_cast<int64_t>(i) * a.heads + h) * a.dim, lane, a.dim, acc);
 }
@@ -131,9 +132,10 @@ __device__ __noinline__ void row_dkv(const PackedAttn &p, const Info &info, int 
     const float4 k = load4<T>(a.k, j * a.k_token + hk * a.k_head, lane, a.dim);
     const float4 v = load4<T>(a.v, j * a.v_token + hk * a.v_head, lane, a.dim);
     float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
-    for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
+    bool settled = false;
+    for (int h = hk * p.group; !settled && h < (hk + 1) * p.group; ++h) {
         const float slope = a.slopes ? a.slopes[h] : 0.f;
-        for (int i = s.lo; i < s.hi; ++i) {
+        for (int i = s.lo; !settled && i < s.hi; ++i) {
             const float4 q = load4<T>(a.q, i * a.q_token + h * a.q_head, lane, a.dim);
             const float4 g = load4<T>(p.dout, i * p.dout_token + h * p.dout_head, lane, a.dim);
             const int64_t at = static_cast<int64_t>(h) * info.padded + i;
@@ -142,6 +144,7 @@ __device__ __noinline__ void row_dkv(const PackedAttn &p, const Info &info, int 
             const float w = ex2_approx(t + info.lse[at]);
             axpy4(dv, w, g);
             axpy4(dk, w * (warp_sum(dot4(g, v)) + info.delta[at]) * slack * a.scale, q);
+            settled = all_nan(dk, lane, a.dim) && all_nan(dv, lane, a.dim);
         }
     }
     store4<T>(p.dk, (static_cast<int64_t>(j) * a.kv_heads + hk) * a.dim, lane, a.dim, dk);

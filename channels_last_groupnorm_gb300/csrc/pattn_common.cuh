@@ -160,6 +160,13 @@ __device__ __forceinline__ void axpy4(float4 &acc, float s, float4 x)
     acc.w = fmaf(s, x.w, acc.w);
 }
 
+// Whether a warp's sums (four channels a lane, dim in all) are NaN throughout:
+// nothing that is added changes them any more.
+__device__ __forceinline__ bool all_nan(float4 f, int lane, int dim)
+{
+    return __all_sync(0xffffffffu, 4 * lane >= dim || (isnan(f.x) && isnan(f.y) && isnan(f.z) && isnan(f.w)));
+}
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll

@@ -460,8 +460,9 @@ __device__ __forceinline__ void clear_not_finite(uint32_t tile, int r, int token
     fence_proxy_async_smem();
 }
 
-// One query computed by one warp (four channels per lane) without ever
-// touching a key that it does not see.
+// One query's output computed by one warp (four channels per lane) without ever
+// touching a key that it does not see.  (Its lse has no part in the values: the
+// tile's stands.)
 template <typename T>
 static __device__ __noinline__ void row_forward(const gn_attn_packed_args &a, int group, int i, int h)
 {
@@ -485,12 +486,11 @@ static __device__ __noinline__ void row_forward(const gn_attn_packed_args &a, in
         const float w = t == -INFINITY ? 0.f : ex2_approx(t - m);
         l += w;
         axpy4(o, w, v);
+        if (l != 0.f && all_nan(o, lane, a.dim)) break;
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     store4<T>(a.out, (static_cast<int64_t>(i) * a.heads + h) * a.dim, lane, a.dim,
               l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (lane == 0)
-        a.lse[static_cast<int64_t>(h) * a.tokens_q + i] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Document of `token` for a whole warp: with up to 32 documents their ends

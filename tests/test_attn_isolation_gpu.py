@@ -178,6 +178,31 @@ def test_documents_between_two_that_hold_such_values(how, h, hk, dim, dtype, val
 
 @pytest.mark.parametrize("h,hk,dim,dtype", [(2, 1, 64, BF), (4, 4, 128, FP)])
 @pytest.mark.parametrize("how", [dict(), dict(cap=6.0, bias=True)])
+def test_a_document_of_nan_throughout(h, hk, dim, dtype, how):
+    """Values or gradients that are NaN everywhere in a document give NaN everywhere
+    there, its lse stays, and so do the two documents beside it."""
+    cu = [0, 50, 700, 740]
+    t = tensors(740, 740, h, hk, dim, dtype)
+    for causal in (False, True):
+        own = dict(spread(how, h), causal=causal)
+        clean = attend(t, cu, cu, **own)
+        for name, shows in (("v", ("out", "dq", "dk")), ("dout", ("dq", "dk", "dv"))):
+            bad = {n: x.clone() for n, x in t.items()}
+            bad[name][50:700] = math.nan
+            got = attend(bad, cu, cu, **own)
+            assert torch.equal(got["lse"], clean["lse"])
+            same_at(got, clean, ((0, 50), (700, 740)), ((0, 50), (700, 740)))
+            for what in shows:
+                assert torch.isnan(got[what][50:700].float()).all(), (name, what)
+        few = attend(dict(bad, q=t["q"][:9], v=torch.where(torch.arange(740, device="cuda")[:, None, None] < 700, math.nan, t["v"])),
+                     [0, 3, 6, 9], cu, backward=False, **own)
+        kept = attend(dict(t, q=t["q"][:9]), [0, 3, 6, 9], cu, backward=False, **own)
+        assert torch.isnan(few["out"][:6].float()).all() and torch.equal(few["out"][6:], kept["out"][6:])
+        assert torch.equal(few["lse"], kept["lse"])
+
+
+@pytest.mark.parametrize("h,hk,dim,dtype", [(2, 1, 64, BF), (4, 4, 128, FP)])
+@pytest.mark.parametrize("how", [dict(), dict(cap=6.0, bias=True)])
 def test_what_sees_such_a_value_shows_it(h, hk, dim, dtype, how):
     """One value row, key row, query row or gradient row at a time, of a causal document between two clean ones."""
     how = dict(spread(how, h), causal=True)
