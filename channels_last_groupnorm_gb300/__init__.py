@@ -42,3 +42,11 @@ from .block import (  # noqa: F401
     layer_norm_backward,
     rope_nd,
 )
+from .serve import (  # noqa: F401
+    attention_cached,
+    cache_append,
+    gn_attn_cached_workspace_bytes,
+    gn_rms_norm_workspace_bytes,
+    rms_norm,
+    rms_norm_backward,
+)

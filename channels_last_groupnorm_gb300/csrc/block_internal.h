@@ -1,6 +1,6 @@
 // block_internal.h -- host-side declarations of the transformer-block kernels
-// (norm_kernels.cu, rope_kernels.cu, pattn_kernels.cu) for the C ABI in
-// block_capi.cu.
+// (norm_kernels.cu, rms_kernels.cu, rope_kernels.cu, pattn_*.cu, append_kernels.cu,
+// cattn_*.cu) for the C ABI in block_capi.cu and serve_capi.cu.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -56,6 +56,36 @@ int layer_norm_blocks(int64_t rows, int cols, int sm_count);
 cudaError_t launch_layer_norm_backward(const NormGradArgs &a, int sm_count, const WaitLimit &limit, cudaStream_t s,
                                        int *launches);
 
+// ---- RMS norm (rms_kernels.cu) ------------------------------------------------
+struct RmsArgs {
+    const void *x, *residual, *weight;
+    void *y, *total;              // total null without a residual
+    float *scales, *rstd;         // scales: y is e4m3
+    int64_t rows;
+    int cols;
+    RowsAt x_at, residual_at, y_at, total_at;
+    int64_t inner;
+    float eps;
+    int format, weight_format;
+};
+
+struct RmsGradArgs {
+    const void *dy, *total, *weight, *dtotal;
+    const float *rstd;
+    void *dx, *dweight;
+    int64_t rows;
+    int cols;
+    RowsAt dy_at, total_at, dtotal_at, dx_at;
+    int64_t inner;
+    int format, weight_format;
+    float *partial;               // [blocks][cols] when the weight's gradient is wanted
+};
+
+cudaError_t launch_rms_norm(const RmsArgs &a, int sm_count, cudaStream_t s);
+// The most CTAs that launch_rms_norm_backward uses, each with a row of partial sums.
+int rms_norm_blocks(int64_t rows, int sm_count);
+cudaError_t launch_rms_norm_backward(const RmsGradArgs &a, int sm_count, cudaStream_t s, int *launches);
+
 // ---- rotary positions over several axes (rope_kernels.cu) -------------------
 constexpr int kRopeMaxPairs = 128;
 constexpr int64_t kRopeMaxElements = 1 << 30;   // of one token: its pieces are counted in an int, plus a grid's step
@@ -97,5 +127,26 @@ cudaError_t launch_packed_attn(const PackedAttn &p, int sm_count, const WaitLimi
 size_t packed_attn_workspace_bytes(int64_t tokens_q, int heads);
 cudaError_t launch_packed_attn_backward(const PackedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s,
                                         int *launches);
+
+// ---- the paged cache in 8 bits (append_kernels.cu, cattn_*.cu) -----------------
+struct Append {
+    gn_cache c;
+    gn_append_args a;
+    int pairs;                                // that a head's channels turn as (0: none)
+    uint64_t turns[kRopeMaxPairs];            // turns of a pair per unit of its axis' position, times 2^64
+    unsigned char axis[kRopeMaxPairs];
+};
+
+cudaError_t launch_cache_append(const Append &p, int sm_count, cudaStream_t s);
+
+struct CachedAttn {
+    gn_cache c;
+    gn_attn_cached_args a;
+    int group;                                // query heads per key / value head
+    void *workspace;
+};
+
+size_t cached_attn_workspace_bytes(int64_t tokens, int sequences, int heads, int kv_heads, int dim, int sm_count);
+cudaError_t launch_cached_attn(const CachedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s, int *launches);
 
 }  // namespace gn

@@ -45,6 +45,38 @@ template <> struct Half2<__half> {
     }
 };
 
+// ---- e4m3 -----------------------------------------------------------------------
+// Two values rounded to nearest, in the low and the high byte (past 448: 448; NaN: 0x7f).
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi)
+{
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3_four(float a, float b, float c, float d)
+{
+    return e4m3_pair(a, b) | e4m3_pair(c, d) << 16;
+}
+
+// The values of the two low bytes (exact).
+__device__ __forceinline__ uint32_t e4m3_half2(uint32_t pair)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(pair)));
+    return r;
+}
+
+__device__ __forceinline__ float2 e4m3_values(uint32_t pair) { return Half2<__half>::unpack(e4m3_half2(pair)); }
+
+// The larger, or NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // ---- two fp32 operations per instruction ------------------------------------------
 __device__ __forceinline__ uint64_t pack2(float a, float b)
 {

@@ -19,7 +19,9 @@ the page's existing general kernel (same section, item 1, third bullet).
 ``attn_fold`` / ``attention_folded`` bind the residual-gate update, the
 fused nearest-2x upsample + 3x3 conv and the folded single-head attention
 the same way.  The operators of a transformer block (layer norm, rotary
-positions, attention of packed documents) are bound in ``block.py``.
+positions, attention of packed documents) are bound in ``block.py``, and those
+of serving from a paged cache in 8 bits (RMS norm, appending, attention over the
+cache) in ``serve.py``.
 """
 from __future__ import annotations
 
@@ -98,6 +100,14 @@ EXPORTS = {
     "gn_attn_packed_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 2),
     "gn_attn_packed_backward": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.c_int64] * 2 + [ctypes.c_void_p] * 4
                                 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "gn_rms_norm": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int64] * 3
+                    + [ctypes.c_void_p, ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "gn_rms_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 2),
+    "gn_rms_norm_backward": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int64] * 3
+                             + [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "gn_cache_append": (ctypes.c_int, [ctypes.c_void_p] * 3),
+    "gn_attn_cached_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 5),
+    "gn_attn_cached": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_size_t, ctypes.c_void_p]),
     "gn_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
                                                 ctypes.c_int, ctypes.c_void_p]),
     "gn_silu_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 4),

@@ -611,6 +611,162 @@ size_t gn_attn_packed_workspace_bytes(int64_t tokens_q, int64_t heads);
 int gn_attn_packed_backward(const gn_attn_packed_args *args, const void *dout, int64_t dout_token, int64_t dout_head,
                             void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- RMS norm, with the residual's addition and an output in 8 bits ------------
+ * Over the C channels of each row,
+ *
+ *   t = x + residual (rounded to the format of x: what a residual stream stores),
+ *   rstd = 1 / sqrt(sum(t^2) / C + eps),  y = t rstd weight
+ *
+ * (t = x without a residual, no factor without a weight), and with g = dy weight,
+ *
+ *   dx = rstd (g - h sum(g h) / C) + dtotal,  h = t rstd,  dweight = sum over rows of dy h
+ *
+ * (dx is the gradient of x and of the residual; dtotal is what the stream behind
+ * the norm sends back).  In 8 bits a row is stored as e4m3 of y / scale with
+ * scale = max |y| / 448, so that its largest magnitude becomes 448; a row whose
+ * largest magnitude is below 1e-30 has scale 0 and bytes 0.  y is taken in fp32 and
+ * rounded once.  Sums are fp32 and added up in a fixed order: the same inputs give
+ * the same bits.
+ */
+
+/* RMS norm.
+ *   x, residual, y, total : DEVICE rows as for gn_layer_norm(), `format` (all three).
+ *                residual and total both or neither; total receives t and may equal
+ *                x or residual, y may equal x (without a residual), each with the same
+ *                strides.
+ *   strides    : HOST [8], elements: outer and stride of x, residual, y, total.
+ *   weight     : DEVICE [cols] of weight_format, or NULL.
+ *   scales     : DEVICE fp32 [rows], or NULL; with it y is e4m3 (one byte an
+ *                element, strides in bytes).
+ *   rstd       : DEVICE fp32 [rows], written for the backward pass, or NULL.
+ *   rows, inner, cols, eps: as for gn_layer_norm().
+ * Asynchronous on `stream`.  Errors: as for gn_layer_norm(). */
+int gn_rms_norm(const void *x, const void *residual, const void *weight, void *y, void *total, float *scales,
+                float *rstd, int64_t rows, int64_t cols, int64_t inner, const int64_t *strides, float eps, int format,
+                int weight_format, void *stream);
+
+/* Workspace bytes gn_rms_norm_backward() needs with a weight on the CURRENT device;
+ * 0 if the shape is out of range or there is no usable device. */
+size_t gn_rms_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Backward pass of gn_rms_norm() with its output in the format of x.
+ *   dy, total, dtotal, dx : DEVICE rows; total is what the norm was taken of (x
+ *                without a residual); dtotal may be NULL; dx may equal any of the
+ *                others with the same strides.
+ *   strides    : HOST [8]: outer and stride of dy, total, dtotal, dx.
+ *   weight, dweight : DEVICE [cols] of weight_format, both or neither.
+ *   workspace  : DEVICE, 256-byte aligned, gn_rms_norm_workspace_bytes(); not used
+ *                without a weight.
+ *   rows >= 0 (0: dweight is set to zero).
+ * Asynchronous on `stream`.  Errors: as for gn_layer_norm_backward(). */
+int gn_rms_norm_backward(const void *dy, const void *total, const void *weight, const float *rstd, const void *dtotal,
+                         void *dx, void *dweight, int64_t rows, int64_t cols, int64_t inner, const int64_t *strides,
+                         int format, int weight_format, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- a paged cache of keys and values in 8 bits ----------------------------------
+ * Pages of page_size tokens hold the keys and values of a sequence as e4m3, with a
+ * scale for each page and head: an element is its byte's value times the scale.
+ * table[s][p] is the page with tokens [p page_size, (p + 1) page_size) of sequence s,
+ * and lengths[s] its tokens, the call's new ones among them: of the n new ones,
+ * number i stands at lengths[s] - n + i.  Sequence s owns the packed tokens
+ * [cu[s], cu[s + 1]); cu NULL: tokens / sequences each.
+ *
+ * Values of table, lengths and cu are clamped into range on the device: bad ones
+ * give wrong results, never a wrong address.  A new token whose place is negative or
+ * past the table, or whose page is not one of `pages`, is not stored; keys of such a
+ * page read as zeros.
+ */
+typedef struct gn_cache {
+    void *k_pages, *v_pages;          /* DEVICE e4m3 [pages][page_size][kv_heads][dim], 16-byte aligned, any order
+                                         of the first three axes; channels contiguous */
+    float *k_scales, *v_scales;       /* DEVICE [pages][kv_heads] */
+    int64_t k_page, k_token, k_head;  /* strides in bytes, multiples of 16; no two elements on one another */
+    int64_t v_page, v_token, v_head;
+    const int32_t *table;             /* DEVICE [sequences][table_width] */
+    const int32_t *lengths;           /* DEVICE [sequences] */
+    const int32_t *cu;                /* DEVICE [sequences + 1], non-decreasing, or NULL */
+    int64_t pages;                    /* 1 .. 2^31 - 1 */
+    int64_t table_width;              /* table_width page_size <= 2^30 */
+    int sequences;                    /* 1 .. 2^20 */
+    int page_size;                    /* a multiple of 8, 8 .. 256 */
+    int kv_heads, dim;                /* 1 .. 1024; a multiple of 16, 16 .. 128 */
+} gn_cache;
+
+/* Appending: the new tokens' keys, turned by rotary positions as by gn_rope_nd(), and
+ * their values go into the cache, and the query heads are turned in the same launch.
+ *
+ * A page's scale is the least power of two of which 448 times is not less than its
+ * largest magnitude, 2^-100 at least; NaN if a magnitude is not finite, which makes the page
+ * read as NaN (its new bytes are zero).  A page whose first slot the call fills
+ * starts anew; one that is filled further keeps its scale or takes a larger one, and what it
+ * holds is then rounded to that (with scales that are powers of two exactly, but for
+ * what falls under e4m3's smallest step).  Slots behind the new tokens are left as
+ * they are.  Keys are turned in fp32 and rounded once.  A page that
+ * the call appends to belongs to one sequence: if the table names it twice, which
+ * tokens it holds is undefined.
+ */
+typedef struct gn_append_args {
+    const void *q, *k, *v;        /* DEVICE [tokens][heads][dim], [tokens][kv_heads][dim] twice; q NULL with heads 0 */
+    void *q_out;                  /* DEVICE like q; may equal q with the same strides, overlaps nothing otherwise */
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head, q_out_token, q_out_head;   /* elements; channels contiguous */
+    int64_t tokens;               /* 0 .. 2^30 */
+    const void *positions;        /* DEVICE [tokens][axes] of position_format; NULL with axes 0: nothing turns */
+    const int64_t *axes_dim;      /* HOST [axes], as for gn_rope_nd(): sum <= dim */
+    double theta;
+    int heads;                    /* 0 .. 65536 */
+    int axes, position_format, interleaved;
+    int format;                   /* of q, k and v: enum gn_half_format (all three) */
+} gn_append_args;
+
+/* Asynchronous on `stream`.  Errors: GN_ERR_NULL, GN_ERR_FORMAT, GN_ERR_SHAPE (tokens,
+ * sequences, pages, strides; tokens not a multiple of sequences without cu),
+ * GN_ERR_CHANNELS (heads, dim, page_size, axes), GN_ERR_EPS (theta), GN_ERR_ALIGN,
+ * GN_ERR_ALIAS, GN_ERR_DEVICE, GN_ERR_KERNEL, GN_ERR_CUDA. */
+int gn_cache_append(const gn_cache *cache, const gn_append_args *args, void *stream);
+
+/* Attention of new tokens over the cache, which holds theirs already:
+ *
+ *   t_ij  = scale q_i . k_j;  cap > 0: t_ij = cap tanh(t_ij / cap)
+ *   t_ij -= slopes[h] |position of i - j|   (with slopes)
+ *   lse_i = log sum_j exp(t_ij),  out_i = sum_j exp(t_ij - lse_i) v_j
+ *
+ * over the keys j < lengths[s] of the query's sequence, those up to its own position
+ * if causal.  A query that sees no key (or belongs to no sequence) has out = 0 and
+ * lse = -inf.  What slots hold that a query does not see has no influence on it, with two
+ * exceptions: a page has one scale, and a byte that is no number (0x7f, 0xff, which
+ * gn_cache_append() never writes) among a sequence's values makes every query of its
+ * new tokens NaN there.  v_scales are 0 or 2^-100 .. 2^100 in magnitude and not
+ * negative.  Query head h reads key / value head h / (heads / kv_heads).
+ *
+ * Scores, softmax and sums are fp32.  For the tensor cores' products a query is split into
+ * two (bf16) or three (fp16) e4m3 numbers that add up to it, less what lies under 2^-17 of its
+ * largest channel.  The weights are split likewise, to 2^-9 of each (bf16) or 2^-13 (fp16) and
+ * 2^-19 of the row's largest; with many new tokens they are rounded to fp16.  The same inputs
+ * give the same bits.
+ */
+typedef struct gn_attn_cached_args {
+    const void *q;                /* DEVICE [tokens][heads][dim], 16-byte aligned */
+    void *out;                    /* DEVICE [tokens][heads][dim], contiguous, 16-byte aligned */
+    float *lse;                   /* DEVICE [heads][tokens] */
+    const float *slopes;          /* DEVICE [heads] or NULL */
+    int64_t q_token, q_head;      /* strides in elements: multiples of 8, >= dim; channels contiguous */
+    int64_t tokens;               /* 0 .. 2^30 */
+    float scale, cap;             /* scale finite; cap 0 (none) or > 0 */
+    int heads;                    /* a multiple of kv_heads, up to 1024 */
+    int causal;
+    int format;                   /* GN_FORMAT_BF16 or GN_FORMAT_FP16 */
+} gn_attn_cached_args;
+
+/* Workspace bytes of gn_attn_cached() on the CURRENT device; 0 if out of range or
+ * without a usable device.  A workspace belongs to one call at a time. */
+size_t gn_attn_cached_workspace_bytes(int64_t tokens, int64_t sequences, int64_t heads, int64_t kv_heads, int64_t dim);
+
+/* workspace: DEVICE, 256-byte aligned.  out, lse and workspace overlap nothing.
+ * Asynchronous on `stream`.  Errors: as for gn_cache_append(), and GN_ERR_EPS (scale,
+ * cap), GN_ERR_WORKSPACE. */
+int gn_attn_cached(const gn_cache *cache, const gn_attn_cached_args *args, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *gn_status_string(int status);
 
@@ -620,7 +776,8 @@ const char *gn_status_string(int status);
  * 4 also lacked the gn_attn_* calls; 3 also the gn_upconv_* calls; 2 also
  * gn_residual_gate_add; 1 also gn_silu_rows_any and gn_silu_ndhwc).  The
  * calls gn_layer_norm*, gn_rope_nd and gn_attn_packed* were added to version 7,
- * which changed nothing that it had. */
+ * and gn_rms_norm*, gn_cache_append and gn_attn_cached* after them, which changed
+ * nothing that it had. */
 int gn_abi_version(void);
 
 #ifdef __cplusplus
