@@ -1,0 +1,257 @@
+// cattn_common.cuh -- what the kernels of attention over the paged cache share: how
+// the work is dealt out, and where pieces of a tile go that several CTAs share.
+//
+// A tile is a run of a sequence's new tokens times some of the query heads that share
+// a key / value head; its keys are cut into blocks of 128.  All (tile, block) pairs of
+// a call, in the order of sequences, heads, runs and blocks, are dealt to the CTAs in
+// equal consecutive parts, whatever the sequences' lengths are (only the device
+// knows them).  A CTA's part is a list of segments, one for each tile that it meets; a
+// tile that several CTAs share leaves unnormalised pieces in the workspace, which
+// a second kernel joins in the order of the keys.
+#pragma once
+
+#include <cstdint>
+
+#include "cache_common.cuh"
+#include "pattn_tiles.cuh"
+
+namespace gn {
+namespace cattn {
+
+using namespace pattn;
+using cache::Sequence;
+
+struct CattnArgs {
+    CachedAttn p;
+    WaitLimit limit;
+    float scale_log2;
+    int tokens, heads, chunks;    // of a tile: its tokens, its query heads; chunks of heads per key / value head
+    int rows;                     // room for rows in a tile's piece
+    int chunk;                    // keys that one load brings: they lie in one page
+    int stages;
+    float *pieces;                // [CTAs][2][rows][2 + dim]: maxima, sums, outputs
+};
+
+// A CTA's piece: slot 0 of a tile that it did not begin, slot 1 of one that it did.
+__device__ __forceinline__ float *piece_of(const CattnArgs &a, int64_t cta, int slot)
+{
+    return a.pieces + (cta * 2 + slot) * static_cast<int64_t>(a.rows) * (2 + a.p.c.dim);
+}
+
+// What is to be done for one tile: blocks [b0, b1) of its `total`.
+struct Segment {
+    int seq, hk, first_head, run;     // first_head within the group
+    int b0, b1, total;
+    Sequence s;
+};
+
+// The keys that the last token of a run sees, and the run's blocks (one at least:
+// rows that see nothing are written too).
+__device__ __forceinline__ int keys_of(const CattnArgs &a, const Sequence &s, int run)
+{
+    if (!a.p.a.causal) return s.length;
+    return min(max(s.first_place() + min(s.end - s.begin, (run + 1) * a.tokens), 0), s.length);
+}
+
+__device__ __forceinline__ int blocks_of(const CattnArgs &a, const Sequence &s, int run)
+{
+    return max(1, (keys_of(a, s, run) + kTile - 1) / kTile);
+}
+
+__device__ __forceinline__ int first_sequence(const CattnArgs &a) { return a.p.c.cu ? -1 : 0; }
+__device__ __forceinline__ int sequence_count(const CattnArgs &a) { return a.p.c.sequences + (a.p.c.cu ? 2 : 0); }
+
+struct Walk {
+    const CattnArgs &a;
+    int64_t left, per_head;
+    int seq, head, run, block, runs;
+    Sequence s;
+
+    __device__ __forceinline__ explicit Walk(const CattnArgs &args) : a(args) {}
+
+    __device__ __forceinline__ void load(int n)
+    {
+        seq = n;
+        s = cache::sequence_of(a.p.c, a.p.a.tokens, n);
+        runs = (s.end - s.begin + a.tokens - 1) / a.tokens;
+        per_head = 0;
+        for (int r = 0; r < runs; ++r) per_head += blocks_of(a, s, r);
+    }
+    __device__ __forceinline__ int heads() const { return a.p.c.kv_heads * a.chunks; }
+    __device__ __forceinline__ int64_t units() const { return per_head * heads(); }
+
+    // begins `offset` units into sequence n
+    __device__ __forceinline__ void start(int n, int64_t offset, int64_t count)
+    {
+        left = count;
+        if (count <= 0) return;
+        load(n);
+        head = static_cast<int>(offset / per_head);
+        offset -= head * per_head;
+        for (run = 0; run < runs - 1; ++run) {
+            const int b = blocks_of(a, s, run);
+            if (offset < b) break;
+            offset -= b;
+        }
+        block = static_cast<int>(offset);
+    }
+    __device__ __forceinline__ bool next(Segment &g)
+    {
+        if (left <= 0) return false;
+        g.seq = seq;
+        g.s = s;
+        g.hk = head / a.chunks;
+        g.first_head = (head - g.hk * a.chunks) * a.heads;
+        g.run = run;
+        g.total = blocks_of(a, s, run);
+        g.b0 = block;
+        g.b1 = block + static_cast<int>(left < g.total - block ? left : g.total - block);
+        left -= g.b1 - g.b0;
+        block = 0;
+        if (left > 0 && ++run == runs) {
+            run = 0;
+            if (++head == heads()) {
+                head = 0;
+                const int last = first_sequence(a) + sequence_count(a);
+                int n = seq + 1;
+                for (load(n); runs == 0 && n + 1 < last; load(n)) ++n;
+                if (runs == 0) left = 0;
+            }
+        }
+        return true;
+    }
+};
+
+// This CTA's part of the work: `count` units that begin `offset` into sequence `seq`;
+// also its number among those with work (G of them), the first unit and how many
+// there are.  For the whole CTA (threads a multiple of 32, at most 1024).
+struct Part {
+    int64_t offset, count, first, all;
+    int seq, ctas;
+};
+
+__device__ __forceinline__ int64_t part_begin(int64_t all, int ctas, int64_t n) { return all / ctas * n + all % ctas * n / ctas; }
+
+struct DealRoom {
+    int64_t sums[32];
+    Part part;
+};
+
+__device__ __forceinline__ Part deal(const CattnArgs &a, DealRoom &room, int ctas)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int count = sequence_count(a), each = (count + blockDim.x - 1) / blockDim.x;
+    const int n0 = first_sequence(a) + threadIdx.x * each, n1 = min(n0 + each, first_sequence(a) + count);
+    Walk w(a);
+    int64_t own = 0;
+    for (int n = n0; n < n1; ++n) {
+        w.load(n);
+        own += w.units();
+    }
+    int64_t before = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+    }
+    if (lane == 31) room.sums[warp] = before;
+    if (threadIdx.x == 0) room.part.count = 0;
+    __syncthreads();
+    int64_t all = 0;
+    before -= own;
+    for (int i = 0; i < warps; ++i) {
+        if (i < warp) before += room.sums[i];
+        all += room.sums[i];
+    }
+    const int busy = static_cast<int>(all < ctas ? (all > 0 ? all : 1) : ctas);
+    if (static_cast<int>(blockIdx.x) < busy && all > 0) {
+        const int64_t u0 = part_begin(all, busy, blockIdx.x), u1 = part_begin(all, busy, blockIdx.x + 1);
+        if (u0 >= before && u0 < before + own) {
+            int n = n0;
+            for (w.load(n); before + w.units() <= u0 && n + 1 < n1; w.load(n)) {
+                before += w.units();
+                ++n;
+            }
+            room.part = {u0 - before, u1 - u0, u0, all, n, busy};
+        }
+    }
+    __syncthreads();
+    return room.part;
+}
+
+cudaError_t launch_join(const CattnArgs &a, int ctas, cudaStream_t s);
+cudaError_t launch_cached_few(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s);
+
+// ---- operands in 8 bits ------------------------------------------------------------
+// Instruction descriptor: fp32 accumulator, M = 128, e4m3 operands, both K-major but
+// for a_mn: the A operand is MN-major.
+__device__ __forceinline__ uint32_t instruction_e4m3(int n, bool a_mn)
+{
+    return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// A tile of 128 tokens in 8 bits: rows of 128 bytes (channels past the head's width
+// come as zeros), 128-byte swizzle.
+constexpr uint32_t kTileBytes = kTile * 128;
+
+// One tile's loads by a warp: lane n brings keys [n chunk, (n + 1) chunk) of the block,
+// from `page` (its own), on one barrier.
+__device__ __forceinline__ void load_pages(uint32_t dst, const void *map, const CattnArgs &a, int key, int page, int hk, uint32_t bar, bool go)
+{
+    const int lane = threadIdx.x & 31;
+    const unsigned loads = __ballot_sync(0xffffffffu, go);
+    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(loads)) * static_cast<uint32_t>(a.chunk) * 128u);
+    __syncwarp();
+    if (go)
+        tma_load_4d(dst + static_cast<uint32_t>(lane * a.chunk) * 128u, map, 0, key % a.p.c.page_size, hk, page, bar);
+    __syncwarp();
+}
+
+// The page for lane n's chunk of a block (pages past the pool: zeros), if the chunk has a key.
+__device__ __forceinline__ int page_for(const CattnArgs &a, int seq, int key)
+{
+    const int page = cache::page_of(a.p.c, seq, key / a.p.c.page_size);
+    return page < 0 ? static_cast<int>(a.p.c.pages) : page;
+}
+
+__device__ __forceinline__ void zero_tile_row(uint32_t tile, int r)
+{
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sts128(tile + static_cast<uint32_t>(r) * 128u + c * 16u, make_uint4(0u, 0u, 0u, 0u));
+}
+
+// Four channels of a query, scaled to 2^7 .. 2^8 for its largest, in PARTS e4m3 numbers
+// that add up to them.
+template <int PARTS>
+__device__ __forceinline__ void split_e4m3(float (&x)[4], uint32_t (&w)[PARTS])
+{
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+        const uint32_t lo = e4m3_pair(x[0], x[1]), hi = e4m3_pair(x[2], x[3]);
+        w[p] = lo | hi << 16;
+        const float2 a = e4m3_values(lo), b = e4m3_values(hi);
+        x[0] -= a.x, x[1] -= a.y, x[2] -= b.x, x[3] -= b.y;
+    }
+}
+
+// The power of two that takes `most` to [2^7, 2^8) (within 2^120).
+__device__ __forceinline__ int query_shift(float most)
+{
+    const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;
+    return min(7 - e, 120);
+}
+
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+}  // namespace cattn
+}  // namespace gn
