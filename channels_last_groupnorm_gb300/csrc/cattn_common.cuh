@@ -5,7 +5,8 @@
 // a key / value head; its keys are cut into blocks of 128.  All (tile, block) pairs of
 // a call, in the order of sequences, heads, runs and blocks, are dealt to the CTAs in
 // equal consecutive parts, whatever the sequences' lengths are (only the device
-// knows them).  A CTA's part is a list of segments, one for each tile that it meets; a
+// knows them); a tile counts as some blocks more than it has (`extra`), for its start
+// and end.  A CTA's part is a list of segments, one for each tile that it meets; a
 // tile that several CTAs share leaves unnormalised pieces in the workspace, which
 // a second kernel joins in the order of the keys.
 #pragma once
@@ -28,6 +29,7 @@ struct CattnArgs {
     int tokens, heads, chunks;    // of a tile: its tokens, its query heads; chunks of heads per key / value head
     int rows;                     // room for rows in a tile's piece
     int chunk;                    // keys that one load brings: they lie in one page
+    int extra;                    // blocks that a tile's start and end count as
     int stages;
     float *pieces;                // [CTAs][2][rows][2 + dim]: maxima, sums, outputs
 };
@@ -61,10 +63,11 @@ __device__ __forceinline__ int blocks_of(const CattnArgs &a, const Sequence &s, 
 __device__ __forceinline__ int first_sequence(const CattnArgs &a) { return a.p.c.cu ? -1 : 0; }
 __device__ __forceinline__ int sequence_count(const CattnArgs &a) { return a.p.c.sequences + (a.p.c.cu ? 2 : 0); }
 
+// (units of work: a tile's first `extra` are its start and end, the others its blocks)
 struct Walk {
     const CattnArgs &a;
     int64_t left, per_head;
-    int seq, head, run, block, runs;
+    int seq, head, run, unit, runs;
     Sequence s;
 
     __device__ __forceinline__ explicit Walk(const CattnArgs &args) : a(args) {}
@@ -75,7 +78,7 @@ struct Walk {
         s = cache::sequence_of(a.p.c, a.p.a.tokens, n);
         runs = (s.end - s.begin + a.tokens - 1) / a.tokens;
         per_head = 0;
-        for (int r = 0; r < runs; ++r) per_head += blocks_of(a, s, r);
+        for (int r = 0; r < runs; ++r) per_head += a.extra + blocks_of(a, s, r);
     }
     __device__ __forceinline__ int heads() const { return a.p.c.kv_heads * a.chunks; }
     __device__ __forceinline__ int64_t units() const { return per_head * heads(); }
@@ -89,36 +92,40 @@ struct Walk {
         head = static_cast<int>(offset / per_head);
         offset -= head * per_head;
         for (run = 0; run < runs - 1; ++run) {
-            const int b = blocks_of(a, s, run);
+            const int b = a.extra + blocks_of(a, s, run);
             if (offset < b) break;
             offset -= b;
         }
-        block = static_cast<int>(offset);
+        unit = static_cast<int>(offset);
     }
+    // the next tile of which the part has blocks
     __device__ __forceinline__ bool next(Segment &g)
     {
-        if (left <= 0) return false;
-        g.seq = seq;
-        g.s = s;
-        g.hk = head / a.chunks;
-        g.first_head = (head - g.hk * a.chunks) * a.heads;
-        g.run = run;
-        g.total = blocks_of(a, s, run);
-        g.b0 = block;
-        g.b1 = block + static_cast<int>(left < g.total - block ? left : g.total - block);
-        left -= g.b1 - g.b0;
-        block = 0;
-        if (left > 0 && ++run == runs) {
-            run = 0;
-            if (++head == heads()) {
-                head = 0;
-                const int last = first_sequence(a) + sequence_count(a);
-                int n = seq + 1;
-                for (load(n); runs == 0 && n + 1 < last; load(n)) ++n;
-                if (runs == 0) left = 0;
+        while (left > 0) {
+            g.seq = seq;
+            g.s = s;
+            g.hk = head / a.chunks;
+            g.first_head = (head - g.hk * a.chunks) * a.heads;
+            g.run = run;
+            g.total = blocks_of(a, s, run);
+            const int all = a.extra + g.total, take = static_cast<int>(left < all - unit ? left : all - unit);
+            g.b0 = max(unit - a.extra, 0);
+            g.b1 = max(unit + take - a.extra, 0);
+            left -= take;
+            unit = 0;
+            if (left > 0 && ++run == runs) {
+                run = 0;
+                if (++head == heads()) {
+                    head = 0;
+                    const int last = first_sequence(a) + sequence_count(a);
+                    int n = seq + 1;
+                    for (load(n); runs == 0 && n + 1 < last; load(n)) ++n;
+                    if (runs == 0) left = 0;
+                }
             }
+            if (g.b0 < g.b1) return true;
         }
-        return true;
+        return false;
     }
 };
 
@@ -131,6 +138,15 @@ struct Part {
 };
 
 __device__ __forceinline__ int64_t part_begin(int64_t all, int ctas, int64_t n) { return all / ctas * n + all % ctas * n / ctas; }
+
+// The part that holds a unit.
+__device__ __forceinline__ int part_of(int64_t all, int ctas, int64_t unit)
+{
+    int64_t n = unit * ctas / all;
+    while (n + 1 < ctas && part_begin(all, ctas, n + 1) <= unit) ++n;
+    while (n > 0 && part_begin(all, ctas, n) > unit) --n;
+    return static_cast<int>(n);
+}
 
 struct DealRoom {
     int64_t sums[32];

@@ -27,39 +27,49 @@ namespace gn {
 namespace cattn {
 namespace {
 
-constexpr int kThreads = 256;   // warps: 0 loads, 1 MMA, 2 the MMA's waits, 4-7 softmax
+constexpr int kThreads = 256;   // warps: 0 loads, 1 MMA, 2 the MMA's waits, 3 the next tile's rows, 4-7 softmax
+constexpr int kScales = 4;      // blocks whose scales are in shared memory
 constexpr int kMaxStages = 6;
 // Weights: the row's largest at 2^6 when the maximum moves, which it does once a score
 // is 2^2 above it: below 448 = 2^8.8, and as far as can be from e4m3's smallest step.
 constexpr float kShift = 6.0f, kRescale = 2.0f;
 constexpr float kLeastScale = 0x1p-100f;
 
-enum Bar { kQ = 0, kFull, kEmpty = kFull + kMaxStages, kS = kEmpty + kMaxStages, kP = kS + 2, kO = kP + 2, kDrain = kO + 2, kBars };
+enum Bar { kQ = 0, kQFree = 2, kFull = kQFree + 2, kEmpty = kFull + kMaxStages, kS = kEmpty + kMaxStages, kP = kS + 2, kO = kP + 2,
+           kScale = kO + 2, kDrain = kScale + kScales, kBars };
+
+// One row of a tile: its scores' factor, its running maximum, the bias and the query's
+// place; what the maximum's last move makes of sums, and the keys that it sees; where its
+// results go (-1: it has none).
+struct __align__(16) Row {
+    float factor, top, slope, place;
+    float grow;
+    int end;
+    int64_t out, lse;
+    int64_t pad;
+};
 
 struct Layout {
-    uint32_t q, weights, weights_bytes, ring, rows, tops, bars, words, deal, total;
+    uint32_t q, weights, operand, ring, rows, tops, scales, bars, words, deal, total;
 };
 
 __host__ __device__ inline Layout layout(int n, int parts, int stages)
 {
     Layout l;
     const uint32_t operand = static_cast<uint32_t>(parts) * static_cast<uint32_t>(n) * 128u;
-    l.q = 0;
-    l.weights = operand;
-    l.weights_bytes = operand;
-    l.ring = 3 * operand;
-    l.rows = l.ring + static_cast<uint32_t>(stages) * kTileBytes;   // n x (factor, maximum, rescaling, slope), n x (end, position)
-    l.tops = l.rows + static_cast<uint32_t>(n) * 24u;               // 4 x n maxima or sums of a warp
-    l.bars = l.tops + 16u * static_cast<uint32_t>(n);
+    l.operand = operand;
+    l.q = 0;                                                        // two of each: this tile's and the next one's,
+    l.weights = 2 * operand;                                        // this block's and the next one's
+    l.ring = 4 * operand;
+    l.rows = l.ring + static_cast<uint32_t>(stages) * kTileBytes;   // 2 x n Row
+    l.tops = l.rows + 2 * static_cast<uint32_t>(n) * sizeof(Row);   // 4 x n maxima or sums of a warp
+    l.scales = l.tops + 16u * static_cast<uint32_t>(n);             // kScales x 16 chunks
+    l.bars = l.scales + kScales * 16 * sizeof(float4);
     l.words = l.bars + 8 * kBars;                                   // tensor-memory slot, abort
     l.deal = l.words + 16;
     l.total = l.deal + sizeof(DealRoom);
     return l;
 }
-
-struct Row {
-    float factor, top, grow, slope;
-};
 
 __device__ __forceinline__ int ordered(float v)
 {
@@ -71,6 +81,21 @@ __device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i >
 __device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v)
 {
     asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Two fp16 values as e4m3, and 16 times what that leaves of them (exact).
+__device__ __forceinline__ uint32_t e4m3_pair_half(uint32_t v)
+{
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t sixteen_times_rest(uint32_t v, uint32_t near)
+{
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&near));
+    const __half2 r = __hmul2(d, __float2half2_rn(16.0f));
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 template <int N>
@@ -85,11 +110,6 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[N])
     }
     tmem_wait_ld();
 }
-
-// A key's scales and where they are.
-struct KeyScale {
-    float k, v;
-};
 
 template <typename T, int MODE, int N>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -106,13 +126,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     const auto stage = [&](int n) { return base + lay.ring + static_cast<uint32_t>(n % args.stages) * kTileBytes; };
     volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(gbase + lay.words);
     volatile int *abort = reinterpret_cast<volatile int *>(words + 1);
-    Row *rows = reinterpret_cast<Row *>(gbase + lay.rows);
-    int2 *ends = reinterpret_cast<int2 *>(gbase + lay.rows + N * sizeof(Row));
+    Row *all_rows = reinterpret_cast<Row *>(gbase + lay.rows);
+    float4 *scales = reinterpret_cast<float4 *>(gbase + lay.scales);
     float *tops = reinterpret_cast<float *>(gbase + lay.tops);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i == kQ || i == kP || i == kP + 1 ? 4 : 1);
+        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i == kQFree || i == kQFree + 1 || i == kP || i == kP + 1 ? 4 : 1);
         *abort = (*reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) ? 1 : 0;
         mbar_init_fence();
         prefetch_tensormap(&map_k);
@@ -138,16 +158,25 @@ __global__ void __launch_bounds__(kThreads, 2)
     walk.start(part.seq, part.offset, skip ? 0 : part.count);
     Segment g;
     if (warp == 0) {
-        int n = 0;                    // tiles so far: keys and values by turns
+        // The pages, and each chunk's scales by the lane that brings it: a block's are
+        // asked for ahead of its loads and stored behind them.  (Their slot was last read
+        // by the softmax kScales blocks ago, whose products the values' stage has waited for.)
+        const float by = (MODE & kCap) ? a.scale / a.cap : args.scale_log2;
+        int n = 0, block = 0;         // tiles so far (keys and values by turns), blocks so far
         bool go = true;
         while (go && walk.next(g)) {
             const int keys = keys_of(args, g.s, g.run);
             int key = g.b0 * kTile + lane * args.chunk;
             bool mine = lane * args.chunk < kTile && key < keys;
             int page = mine ? page_for(args, g.seq, key) : 0;
-            for (int b = g.b0; go && b < g.b1; ++b) {
+            for (int b = g.b0; go && b < g.b1; ++b, ++block) {
                 const int key_now = key, page_now = page;
                 const bool now = mine;
+                float ks = 0.f, vs = 0.f;
+                if (now && page_now < c.pages) {
+                    ks = __ldg(c.k_scales + static_cast<int64_t>(page_now) * c.kv_heads + g.hk);
+                    vs = __ldg(c.v_scales + static_cast<int64_t>(page_now) * c.kv_heads + g.hk);
+                }
                 key += kTile;
                 mine = lane * args.chunk < kTile && key < keys && b + 1 < g.b1;
                 if (mine) page = page_for(args, g.seq, key);
@@ -159,6 +188,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     load_pages(stage(n), e ? &map_v : &map_k, args, key_now, page_now, g.hk, bar(kFull + st), now);
                 }
+                vs = vs < kLeastScale ? kLeastScale : vs;
+                if (lane < 16) scales[(block % kScales) * 16 + lane] = make_float4(ks * by, log2f(vs), 1.0f / vs, 0.f);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kScale + block % kScales));
             }
         }
         // nothing is left in flight when the CTA goes on, whatever became of the others
@@ -170,11 +203,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int steps = (c.dim + 31) / 32;
         const uint32_t is = instruction_e4m3(N, false), io = instruction_e4m3(PARTS * N, true);
         const auto loaded = [&](int n) { wait_warp(bar(kFull + n % args.stages), (n / args.stages) & 1, abort, args.limit); };
-        const auto scores = [&](int n) {              // block n's, into buffer n & 1
+        const auto scores = [&](int n, int q) {       // block n's with query buffer q, into buffer n & 1
             if (elect_one()) {
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p) {
-                    const uint64_t dk = sw128_kmajor_desc(stage(2 * n)), dq = sw128_kmajor_desc(base + lay.q + p * N * 128u);
+                    const uint64_t dk = sw128_kmajor_desc(stage(2 * n)), dq = sw128_kmajor_desc(base + lay.q + q * lay.operand + p * N * 128u);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (k >= steps) break;
@@ -189,20 +222,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         int n = 0, segment = 0;                       // blocks, tiles so far
         for (; walk.next(g); ++segment) {
             if (waits) {
-                wait_warp(bar(kQ), segment & 1, abort, args.limit);
+                wait_warp(bar(kQ + (segment & 1)), (segment >> 1) & 1, abort, args.limit);
                 loaded(2 * n);
             }
             hand_over();
             if (!waits) {
                 tc_fence_after_sync();
-                scores(n);
+                scores(n, segment & 1);
             }
             for (int b = g.b0; b < g.b1; ++b, ++n) {
                 if (b + 1 < g.b1) {
                     // (the buffer's last scores have been read: their weights were waited for)
                     if (waits) loaded(2 * n + 2);
                     hand_over();
-                    if (!waits) scores(n + 1);
+                    if (!waits) scores(n + 1, segment & 1);
                 }
                 if (waits) {
                     loaded(2 * n + 1);
@@ -212,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (!waits) {
                     tc_fence_after_sync();
                     const uint64_t dv = sw128_mnmajor_desc(stage(2 * n + 1));
-                    const uint64_t dw = sw128_kmajor_desc(base + lay.weights + (n & 1) * lay.weights_bytes);
+                    const uint64_t dw = sw128_kmajor_desc(base + lay.weights + (n & 1) * lay.operand);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) umma_e4m3(t_o, dv + k * (4096u >> 4), dw + 2 * k, io, b > g.b0 || k > 0);
@@ -227,30 +260,30 @@ __global__ void __launch_bounds__(kThreads, 2)
             commit(bar(kDrain));
             tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
         }
-    } else if (warp >= 4) {
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const int r = (warp & 3) * 32 + lane;
-        // this thread's key within the block: its place in the weights' rows
-        const uint32_t place = base + lay.weights + static_cast<uint32_t>(r & 15);
-        const uint32_t piece = static_cast<uint32_t>(r >> 4);
-        float by = args.scale_log2, inv_cap = 0.f;
-        if (MODE & kCap) {
-            by = a.cap * kLog2e;
-            inv_cap = a.scale / a.cap;
-        }
-        int n = 0;
-        while (walk.next(g)) {
-            const int first_token = g.run * args.tokens, count = min(args.tokens, g.s.end - g.s.begin - first_token);
-            const int live = count * args.heads, keys = keys_of(args, g.s, g.run);
-            // the tile's rows: what they see, and their queries in parts
-            if (r < live) {
-                const int pos = g.s.first_place() + first_token + r / args.heads, h = g.first_head + r % args.heads;
-                ends[r] = make_int2(a.causal ? min(max(pos + 1, 0), g.s.length) : g.s.length, pos);
-                rows[r].top = -INFINITY;
-                rows[r].slope = (MODE & kBias) && a.slopes && h < args.p.group ? __ldg(a.slopes + g.hk * args.p.group + h) * kLog2e : 0.f;
+    } else if (warp == 3) {
+        // the rows of a tile while the one before it is worked on
+        for (int segment = 0; walk.next(g); ++segment) {
+            const int buffer = segment & 1;
+            Row *rows = all_rows + buffer * N;
+            const int first_token = g.run * args.tokens, live = min(args.tokens, g.s.end - g.s.begin - first_token) * args.heads;
+            if (segment >= 2) wait_warp(bar(kQFree + buffer), ((segment >> 1) - 1) & 1, abort, args.limit);
+            if (lane < N) {
+                const int h = g.first_head + lane % args.heads, i = first_token + lane / args.heads, place = g.s.first_place() + i;
+                const int64_t token = g.s.begin + i, head = g.hk * args.p.group + h;
+                const bool there = lane < live && h < args.p.group;
+                Row row;
+                row.factor = row.grow = 1.0f;
+                row.top = -INFINITY;
+                row.slope = (MODE & kBias) && a.slopes && there ? __ldg(a.slopes + head) * kLog2e : 0.f;
+                row.place = static_cast<float>(place);
+                row.end = a.causal ? min(max(place + 1, 0), g.s.length) : g.s.length;
+                row.out = there ? token * a.heads + head : -1;
+                row.lse = head * a.tokens + token;
+                rows[lane] = row;
             }
-            const int all = a.causal ? min(max(g.s.first_place() + first_token + 1, 0), g.s.length) : g.s.length;
-            for (int q = warp & 3; q < live; q += 4) {
+            __syncwarp();
+#pragma unroll 4
+            for (int q = 0; q < live; ++q) {
                 const int h = g.first_head + q % args.heads;
                 const int64_t token = g.s.begin + first_token + q / args.heads;
                 const bool there = h < args.p.group && 4 * lane < c.dim;
@@ -267,68 +300,82 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] *= up;
                 split_e4m3<PARTS>(x, w);
-                const uint32_t at = base + lay.q + q * 128u + (((lane >> 2) ^ (q & 7u)) << 4) + (lane & 3u) * 4u;
+                const uint32_t at = base + lay.q + buffer * lay.operand + q * 128u + (((lane >> 2) ^ (q & 7u)) << 4) + (lane & 3u) * 4u;
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p)
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + p * N * 128u), "r"(w[p]) : "memory");
                 if (lane == 0) rows[q].factor = power_of_two(-shift);
             }
             fence_proxy_async_smem();
-            named_sync(1, 128);
-            if (lane == 0) mbar_arrive(bar(kQ));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kQ + buffer));
+        }
+    } else if (warp >= 4) {
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int r = (warp & 3) * 32 + lane;
+        // this thread's key within the block: its place in the weights' rows
+        const uint32_t place = base + lay.weights + static_cast<uint32_t>(r & 15);
+        const uint32_t piece = static_cast<uint32_t>(r >> 4);
+        const int my_chunk = r / args.chunk;
+        int n = 0;
+        for (int segment = 0; walk.next(g); ++segment) {
+            Row *rows = all_rows + (segment & 1) * N;
+            const int first_token = g.run * args.tokens, live = min(args.tokens, g.s.end - g.s.begin - first_token) * args.heads;
+            const int keys = keys_of(args, g.s, g.run);
+            const int all = a.causal ? min(max(g.s.first_place() + first_token + 1, 0), g.s.length) : g.s.length;
+            wait_warp(bar(kQ + (segment & 1)), (segment >> 1) & 1, abort, args.limit);
             float l[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) l[i] = 0.f;
-            // the scales of this thread's key, a block ahead
-            const auto scales_of = [&](int j) {
-                KeyScale s = {0.f, 0.f};
-                const int page = j < keys ? cache::page_of(c, g.seq, j / c.page_size) : -1;
-                if (page >= 0) {
-                    s.k = __ldg(c.k_scales + static_cast<int64_t>(page) * c.kv_heads + g.hk);
-                    s.v = __ldg(c.v_scales + static_cast<int64_t>(page) * c.kv_heads + g.hk);
-                }
-                return s;
-            };
-            KeyScale ahead = scales_of(g.b0 * kTile + r);
             for (int b = g.b0; b < g.b1; ++b, ++n) {
                 const int first = b * kTile, j = first + r;
                 const bool masked = first + kTile > all;
-                const KeyScale key = ahead;
-                if (b + 1 < g.b1) ahead = scales_of(j + kTile);
-                const float vs = key.v < kLeastScale ? kLeastScale : key.v, inv_vs = 1.0f / vs, log_vs = log2f(vs);
-                const float ks = (MODE & kCap) ? key.k * inv_cap : key.k * by;
+                wait_warp(bar(kScale + n % kScales), (n / kScales) & 1, abort, args.limit);
+                const float4 key = scales[(n % kScales) * 16 + my_chunk];
+                const float ks = key.x, log_vs = key.y, inv_vs = key.z;
                 wait_warp(bar(kS + (n & 1)), (n >> 1) & 1, abort, args.limit);
                 tc_fence_after_sync();
                 float s[N];
                 tmem_ld_cols<N>(t_s + (n & 1) * N + lanes, s);
                 bool grew = b == g.b0;
+                // (four rows at a time: the tile may have fewer, what the others hold goes
+                // nowhere, and the four run side by side)
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    if (i >= live) break;             // (the same for all: rows that are not there cost nothing)
-                    const Row row = rows[i];
-                    float t = s[i] * (ks * row.factor);
-                    if (MODE & kCap) t = tanh_fast(t) * by;
-                    if ((MODE & kBias) || masked) {
-                        const int2 e = ends[i];
-                        if (MODE & kBias) t = fmaf(-row.slope, fabsf(static_cast<float>(e.y - j)), t);
-                        t = t + log_vs;
-                        if (masked) t = j < e.x ? t : -INFINITY;
-                    } else {
-                        t = t + log_vs;
+                for (int i = 0; i < N; i += 4) {
+                    if (i >= live) break;
+                    float4 row[4];
+                    int end[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        row[e] = *reinterpret_cast<const float4 *>(&rows[i + e]);
+                        if (masked) end[e] = rows[i + e].end;
                     }
-                    s[i] = t;
-                    grew = grew || t > row.top + (kShift + kRescale);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float t = s[i + e] * (ks * row[e].x);
+                        if (MODE & kCap) t = tanh_fast(t) * (a.cap * kLog2e);
+                        if (MODE & kBias) t = fmaf(-row[e].z, fabsf(row[e].w - static_cast<float>(j)), t);
+                        t += log_vs;
+                        if (masked) t = j < end[e] ? t : -INFINITY;
+                        s[i + e] = t;
+                        grew = grew || t > row[e].y + (kShift + kRescale);
+                    }
                 }
                 // the maxima are only looked for when a score is far above one of them
                 if (bar_any(1, 128, grew)) {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
+                    for (int i = 0; i < N; i += 4) {
                         if (i >= live) break;
-                        const int top = __reduce_max_sync(0xffffffffu, ordered(s[i] == s[i] ? s[i] : -INFINITY));
-                        if (lane == 0) tops[(warp & 3) * N + i] = from_ordered(top);
+                        int top[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            top[e] = __reduce_max_sync(0xffffffffu, ordered(s[i + e] == s[i + e] ? s[i + e] : -INFINITY));
+                        if (lane == 0)
+                            *reinterpret_cast<float4 *>(tops + (warp & 3) * N + i) =
+                                make_float4(from_ordered(top[0]), from_ordered(top[1]), from_ordered(top[2]), from_ordered(top[3]));
                     }
                     named_sync(1, 128);
-                    if (r < live) {
+                    if (r < N && r < live) {
                         const float old = rows[r].top;
                         const float top = fmaxf(fmaxf(tops[r], tops[N + r]), fmaxf(tops[2 * N + r], tops[3 * N + r]));
                         // (a row's maximum moves for its own scores only: not by what another row's keys hold)
@@ -338,10 +385,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     named_sync(1, 128);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        if (i >= live) break;
-                        l[i] *= rows[i].grow;
-                    }
+                    for (int i = 0; i < N; ++i) l[i] *= rows[i].grow;
                     if (b > g.b0) {
                         wait_warp(bar(kO + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort, args.limit);
                         tc_fence_after_sync();
@@ -359,28 +403,30 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 // the weights' buffer is free once the products of two blocks ago are done
                 if (n >= 2) wait_warp(bar(kO + (n & 1)), ((n - 2) >> 1) & 1, abort, args.limit);
-                const uint32_t to = place + (n & 1) * lay.weights_bytes;
+                const uint32_t to = place + (n & 1) * lay.operand;
 #pragma unroll
-                for (int i = 0; i < N; i += 2) {
+                for (int i = 0; i < N; i += 4) {
                     if (i >= live) break;
-                    float p[2];
+                    float p[4];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         const float top = rows[i + e].top;
                         // (0 x inv_vs would not be 0 if an unseen key's scale is no number)
                         const bool seen = s[i + e] != -INFINITY;
                         p[e] = seen ? ex2_approx(s[i + e] - (top == -INFINITY ? 0.f : top)) : 0.f;
                         l[i + e] = seen ? fmaf(p[e], inv_vs, l[i + e]) : l[i + e];
                     }
+                    // in fp16, whose 11 bits the parts hold
+                    uint32_t h[2] = {Half2<__half>::pack(p[0], p[1]), Half2<__half>::pack(p[2], p[3])};
 #pragma unroll
                     for (int q = 0; q < PARTS; ++q) {
-                        const uint32_t w = e4m3_pair(p[0], p[1]);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            sts_u8(to + static_cast<uint32_t>(q * N + i + e) * 128u + ((piece ^ ((i + e) & 7u)) << 4), w >> (8 * e));
-                        const float2 v = e4m3_values(w);
-                        p[0] = (p[0] - v.x) * 16.0f;
-                        p[1] = (p[1] - v.y) * 16.0f;
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t w = e4m3_pair_half(h[e]), row = q * N + i + 2 * e, bits = (i + 2 * e) & 7u;
+                            sts_u8(to + row * 128u + ((piece ^ bits) << 4), w);
+                            sts_u8(to + (row + 1) * 128u + ((piece ^ (bits + 1)) << 4), w >> 8);
+                            if (q + 1 < PARTS) h[e] = sixteen_times_rest(h[e], e4m3_half2(w));
+                        }
                     }
                 }
                 if (first + kTile > keys) {
@@ -398,10 +444,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             tc_fence_after_sync();
             named_sync(1, 128);           // the maxima in `tops` have been read
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
+            for (int i = 0; i < N; i += 4) {
                 if (i >= live) break;
-                const float sum = warp_sum(l[i]);
-                if (lane == 0) tops[(warp & 3) * N + i] = sum;
+                float4 sum;
+                sum.x = warp_sum(l[i]);
+                sum.y = warp_sum(l[i + 1]);
+                sum.z = warp_sum(l[i + 2]);
+                sum.w = warp_sum(l[i + 3]);
+                if (lane == 0) *reinterpret_cast<float4 *>(tops + (warp & 3) * N + i) = sum;
             }
             named_sync(1, 128);
             const bool whole = g.b0 == 0 && g.b1 == g.total, good = *abort == 0;
@@ -416,27 +466,38 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < N; ++i) o[i] = fmaf(more[i], step, o[i]);
             }
+            tc_fence_before_sync();
+            const auto sum_of = [&](int i) { return (tops[i] + tops[N + i]) + (tops[2 * N + i] + tops[3 * N + i]); };
+            // thread r has channel r of every row, and the sums of row r
+            if (good && whole) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (i >= live) break;
-                const int h = g.first_head + i % args.heads;
-                const int64_t token = g.s.begin + first_token + i / args.heads;
-                if (h >= args.p.group || !good) continue;
-                const float sum = (tops[i] + tops[N + i]) + (tops[2 * N + i] + tops[3 * N + i]), top = rows[i].top;
-                if (whole) {
-                    const int64_t head = g.hk * args.p.group + h;
-                    if (r < c.dim) static_cast<T *>(a.out)[(token * a.heads + head) * c.dim + r] = from_float<T>(sum == 0.f ? 0.f : o[i] / sum);
-                    if (r == 0) a.lse[head * a.tokens + token] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-                } else {
-                    if (r < c.dim) to[2 * N + i * c.dim + r] = o[i];
-                    if (r == 0) {
-                        to[i] = top;
-                        to[N + i] = sum;
+                for (int i = 0; i < N; i += 4) {
+                    if (i >= live) break;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float sum = sum_of(i + e);
+                        const int64_t at = rows[i + e].out;
+                        if (at >= 0 && r < c.dim)
+                            static_cast<T *>(a.out)[at * c.dim + r] = from_float<T>(sum == 0.f ? 0.f : __fdividef(o[i + e], sum));
                     }
                 }
+                if (r < N && rows[r].out >= 0) {
+                    const float sum = sum_of(r);
+                    a.lse[rows[r].lse] = sum == 0.f ? -INFINITY : (rows[r].top + log2f(sum)) * kLn2;
+                }
+            } else if (good) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    if (i >= live) break;
+                    if (r < c.dim) to[2 * N + i * c.dim + r] = o[i];
+                }
+                if (r < N && r < live) {
+                    to[r] = rows[r].top;
+                    to[N + r] = sum_of(r);
+                }
             }
-            tc_fence_before_sync();
-            named_sync(1, 128);           // rows and tops are free
+            named_sync(1, 128);           // `tops` is free
+            if (lane == 0) mbar_arrive(bar(kQFree + (segment & 1)));
         }
     }
     __syncwarp();

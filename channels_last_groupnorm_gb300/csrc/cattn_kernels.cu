@@ -8,11 +8,14 @@ namespace gn {
 namespace cattn {
 namespace {
 
-// Joins the pieces of the tiles that several CTAs shared.  CTA c looks after the tile
-// in which the c-th part of the work begins, if it is the second to work on it: part
-// c - 1 holds the tile's beginning, and parts c, c + 1, ... go on with it.
+// Joins the pieces of the tiles that several CTAs shared.  Block (c, y) looks after the
+// tile in which the c-th part of the work begins, if part c - 1 holds the tile's first
+// unit, and there after some of its rows, a warp each: the pieces' maxima and sums on the lanes first,
+// then their outputs, four channels a lane, whose loads wait for nothing.
+constexpr int kJoinThreads = 256;
+
 template <typename T>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ CattnArgs args)
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ CattnArgs args)
 {
     __shared__ DealRoom room;
     tc::griddep_wait();
@@ -21,46 +24,49 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Cattn
     const gn_attn_cached_args &a = args.p.a;
     const Part part = deal(args, room, gridDim.x);
     if (part.count == 0 || *reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) return;
+    // the tile in which this part begins, and its units [begin, end)
     Walk walk(args);
     walk.start(part.seq, part.offset, part.count);
-    Segment g;
-    walk.next(g);
-    const int64_t begin = part.first - g.b0, end = begin + g.total;     // of the tile, among all units
-    const int cta = blockIdx.x;
-    if (g.b0 == 0 || part_begin(part.all, part.ctas, cta - 1) > begin) return;
-    int others = 0;                       // parts after the first
-    while (cta + others < part.ctas && part_begin(part.all, part.ctas, cta + others) < end) ++others;
-    const int first_token = g.run * args.tokens, count = min(args.tokens, g.s.end - g.s.begin - first_token);
-    const float *first = piece_of(args, cta - 1, 1);
-    const int64_t step = 2 * static_cast<int64_t>(args.rows) * (2 + c.dim);
-    const float *next = piece_of(args, cta, 0);
-    const int quads = c.dim / 4;
-    for (int n = threadIdx.x; n < count * args.heads * quads; n += blockDim.x) {
-        const int row = n / quads, q = n - row * quads;
-        const int h = g.first_head + row % args.heads;
+    const int64_t begin = part.first - walk.unit;
+    if (walk.unit == 0 || part_begin(part.all, part.ctas, static_cast<int64_t>(blockIdx.x) - 1) > begin) return;
+    const Sequence s = walk.s;
+    const int hk = walk.head / args.chunks, first_head = (walk.head - hk * args.chunks) * args.heads;
+    const int64_t blocks = begin + args.extra, end = blocks + blocks_of(args, s, walk.run);
+    // the parts that have blocks of it: the first left its piece in slot 1, the others in slot 0
+    const int from = part_of(part.all, part.ctas, blocks), pieces = part_of(part.all, part.ctas, end - 1) + 1 - from;
+    if (pieces == 1) return;              // it wrote the outputs itself
+    const int first_token = walk.run * args.tokens, live = min(args.tokens, s.end - s.begin - first_token) * args.heads;
+    const int lane = threadIdx.x & 31;
+    const auto piece = [&](int p) { return piece_of(args, from + p, p == 0 ? 1 : 0); };
+    for (int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); row < live; row += gridDim.y * (kJoinThreads / 32)) {
+        const int h = first_head + row % args.heads;
         if (h >= args.p.group) continue;
-        float top = first[row], sum = first[args.rows + row];
-        float4 o = *reinterpret_cast<const float4 *>(first + 2 * args.rows + row * c.dim + 4 * q);
-#pragma unroll 4
-        for (int p = 0; p < others; ++p) {
-            const float *piece = next + p * step;
-            const float m = piece[row], l = piece[args.rows + row];
-            const float4 v = *reinterpret_cast<const float4 *>(piece + 2 * args.rows + row * c.dim + 4 * q);
-            // (a part that saw nothing has a sum of zero; NaN stays)
-            const float now = fmaxf(top, m);
-            const float f = sum == 0.f ? 0.f : ex2_approx(top - now), e = l == 0.f ? 0.f : ex2_approx(m - now);
-            o.x = fmaf(o.x, f, v.x * e);
-            o.y = fmaf(o.y, f, v.y * e);
-            o.z = fmaf(o.z, f, v.z * e);
-            o.w = fmaf(o.w, f, v.w * e);
-            sum = fmaf(sum, f, l * e);
-            top = now;
+        float top = -INFINITY, sum = 0.f;
+        for (int p = lane; p < pieces; p += 32) top = fmaxf(top, piece(p)[row]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p0 = 0; p0 < pieces; p0 += 32) {
+            float f = 0.f;
+            if (p0 + lane < pieces) {
+                const float l = piece(p0 + lane)[args.rows + row];
+                // (a part that saw nothing has a sum of zero)
+                f = l == 0.f ? 0.f : ex2_approx(piece(p0 + lane)[row] - top);
+                sum = fmaf(f, l, sum);
+            }
+            const int count = min(32, pieces - p0);
+#pragma unroll 8
+            for (int p = 0; p < count; ++p) {
+                const float g = __shfl_sync(0xffffffffu, f, p);
+                if (4 * lane < c.dim)
+                    axpy4(out, g, *reinterpret_cast<const float4 *>(piece(p0 + p) + 2 * args.rows + row * c.dim + 4 * lane));
+            }
         }
+        sum = warp_sum(sum);
         const float by = sum == 0.f ? 0.f : 1.0f / sum;
-        const int64_t token = g.s.begin + first_token + row / args.heads, head = g.hk * args.p.group + h;
-        *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + (token * a.heads + head) * c.dim + 4 * q) =
-            make_uint2(Half2<T>::pack(o.x * by, o.y * by), Half2<T>::pack(o.z * by, o.w * by));
-        if (q == 0) a.lse[head * a.tokens + token] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        const int64_t token = s.begin + first_token + row / args.heads, head = hk * args.p.group + h;
+        store4<T>(a.out, (token * a.heads + head) * c.dim, lane, c.dim, make_float4(out.x * by, out.y * by, out.z * by, out.w * by));
+        if (lane == 0) a.lse[head * a.tokens + token] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
 }
 
@@ -98,6 +104,7 @@ CattnArgs plan(const CachedAttn &p)
     a.tokens = std::max(1, most / a.heads);
     if (!p.c.cu) a.tokens = static_cast<int>(std::min<int64_t>(a.tokens, each));
     a.rows = a.tokens * a.heads <= 16 ? 16 : 32;
+    a.extra = 3;
     a.chunk = 128;
     while (p.c.page_size % a.chunk) a.chunk /= 2;
     return a;
@@ -110,7 +117,7 @@ int few_ctas(int sm_count) { return 2 * sm_count; }
 cudaError_t launch_join(const CattnArgs &a, int ctas, cudaStream_t s)
 {
     return tc::launch_pdl(a.p.a.format == GN_FORMAT_BF16 ? join_kernel<__nv_bfloat16> : join_kernel<__half>,
-                          dim3(static_cast<unsigned>(ctas)), dim3(128), 0, s, a);
+                          dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(a.rows / 8)), dim3(kJoinThreads), 0, s, a);
 }
 
 }  // namespace cattn
