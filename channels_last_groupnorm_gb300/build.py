@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(HERE, "libgnsilu.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["gn_kernels.cu", "gn_cluster.cu", "gn_capi.cu", "gn_static.cu", "rga_kernels.cu", "upconv_kernels.cu", "attn_kernels.cu", "tc_capi.cu",
            "norm_kernels.cu", "rope_kernels.cu", "pattn_kernels.cu", "pattn_forward.cu", "pattn_split.cu", "pattn_backward.cu",
-           "block_capi.cu", "rms_kernels.cu", "append_kernels.cu", "cattn_kernels.cu", "cattn_few.cu", "serve_capi.cu"]
+           "block_capi.cu", "rms_kernels.cu", "append_kernels.cu", "cattn_kernels.cu", "cattn_few.cu", "cattn_tiles.cu", "serve_capi.cu"]
 HEADERS = ["gn_internal.h", "gn_math.cuh", "gn_ptx.cuh", "tc_ptx.cuh", "tc_common.cuh", "tc_internal.h", "capi_util.h",
            "block_internal.h", "block_math.cuh", "pattn_common.cuh", "pattn_tiles.cuh",
            "norm_common.cuh", "cache_common.cuh", "cattn_common.cuh", "block_checks.h"]

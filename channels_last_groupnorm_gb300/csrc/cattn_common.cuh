@@ -197,6 +197,7 @@ __device__ __forceinline__ Part deal(const CattnArgs &a, DealRoom &room, int cta
 
 cudaError_t launch_join(const CattnArgs &a, int ctas, cudaStream_t s);
 cudaError_t launch_cached_few(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s);
+cudaError_t launch_cached_tiles(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s);
 
 // ---- operands in 8 bits ------------------------------------------------------------
 // Instruction descriptor: fp32 accumulator, M = 128, e4m3 operands, both K-major but
@@ -220,16 +221,14 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
 // come as zeros), 128-byte swizzle.
 constexpr uint32_t kTileBytes = kTile * 128;
 
-// One tile's loads by a warp: lane n brings keys [n chunk, (n + 1) chunk) of the block,
-// from `page` (its own), on one barrier.
+// One tile's loads by a warp: a lane with `go` brings `chunk` keys from `key` on, which lie
+// in `page` (its own), on one barrier.
 __device__ __forceinline__ void load_pages(uint32_t dst, const void *map, const CattnArgs &a, int key, int page, int hk, uint32_t bar, bool go)
 {
-    const int lane = threadIdx.x & 31;
     const unsigned loads = __ballot_sync(0xffffffffu, go);
-    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(loads)) * static_cast<uint32_t>(a.chunk) * 128u);
+    if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(loads)) * static_cast<uint32_t>(a.chunk) * 128u);
     __syncwarp();
-    if (go)
-        tma_load_4d(dst + static_cast<uint32_t>(lane * a.chunk) * 128u, map, 0, key % a.p.c.page_size, hk, page, bar);
+    if (go) tma_load_4d(dst + static_cast<uint32_t>(key % kTile) * 128u, map, 0, key % a.p.c.page_size, hk, page, bar);
     __syncwarp();
 }
 

@@ -88,48 +88,49 @@ bool encode_pool(CUtensorMap *map, const void *base, const gn_cache &c, int64_t 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kFewRows = 32;
+constexpr int kFewRows = 32, kManyRows = 2 * kTile;
 
-// The tiles of a call: up to 32 rows, 16 where that is all there is (half the
-// registers, a deeper ring).
-CattnArgs plan(const CachedAttn &p)
+// The tiles of a call and the kernel for them: up to 32 rows on the tensor core's narrow
+// side (16 where that is all there is), or 256 on its wide side.
+CattnArgs plan(const CachedAttn &p, bool *few)
 {
     CattnArgs a = {};
     a.p = p;
     a.scale_log2 = p.a.scale * kLog2e;
-    a.heads = std::min(p.group, kFewRows);
-    a.chunks = (p.group + a.heads - 1) / a.heads;
     const int64_t each = p.c.cu ? std::max<int64_t>(1, p.a.tokens / p.c.sequences) : p.a.tokens / p.c.sequences;
-    const int most = each * a.heads <= 16 ? std::max(16, a.heads) : kFewRows;
-    a.tokens = std::max(1, most / a.heads);
+    *few = each * p.group <= kFewRows;
+    a.heads = std::min(p.group, *few ? kFewRows : kManyRows);
+    const int most = !*few ? kManyRows : each * a.heads <= 16 ? 16 : kFewRows;
+    a.chunks = (p.group + a.heads - 1) / a.heads;
+    a.tokens = most / a.heads;
     if (!p.c.cu) a.tokens = static_cast<int>(std::min<int64_t>(a.tokens, each));
-    a.rows = a.tokens * a.heads <= 16 ? 16 : 32;
+    a.rows = !*few ? kManyRows : a.tokens * a.heads <= 16 ? 16 : kFewRows;
     a.extra = 3;
-    a.chunk = 128;
+    a.chunk = kTile;
     while (p.c.page_size % a.chunk) a.chunk /= 2;
     return a;
 }
-
-int few_ctas(int sm_count) { return 2 * sm_count; }
 
 }  // namespace
 
 cudaError_t launch_join(const CattnArgs &a, int ctas, cudaStream_t s)
 {
     return tc::launch_pdl(a.p.a.format == GN_FORMAT_BF16 ? join_kernel<__nv_bfloat16> : join_kernel<__half>,
-                          dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(a.rows / 8)), dim3(kJoinThreads), 0, s, a);
+                          dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(std::min(a.rows / 8, 8))), dim3(kJoinThreads), 0, s, a);
 }
 
 }  // namespace cattn
 
+// (the few rows of two CTAs an SM, or the many of one)
 size_t cached_attn_workspace_bytes(int64_t, int, int, int, int dim, int sm_count)
 {
-    return 4u * 2u * static_cast<size_t>(cattn::few_ctas(sm_count)) * cattn::kFewRows * static_cast<size_t>(2 + dim);
+    return 4u * 2u * static_cast<size_t>(sm_count) * cattn::kManyRows * static_cast<size_t>(2 + dim);
 }
 
 cudaError_t launch_cached_attn(const CachedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s, int *launches)
 {
-    cattn::CattnArgs a = cattn::plan(p);
+    bool few;
+    cattn::CattnArgs a = cattn::plan(p, &few);
     a.limit = limit;
     a.pieces = static_cast<float *>(p.workspace);
     const gn_cache &c = p.c;
@@ -137,8 +138,8 @@ cudaError_t launch_cached_attn(const CachedAttn &p, int sm_count, const WaitLimi
     if (!cattn::encode_pool(&mk, c.k_pages, c, c.k_page, c.k_token, c.k_head, a.chunk) ||
         !cattn::encode_pool(&mv, c.v_pages, c, c.v_page, c.v_token, c.v_head, a.chunk))
         return cudaErrorInvalidValue;
-    const int ctas = cattn::few_ctas(sm_count);
-    cudaError_t e = cattn::launch_cached_few(a, mk, mv, ctas, s);
+    const int ctas = few ? 2 * sm_count : sm_count;
+    cudaError_t e = few ? cattn::launch_cached_few(a, mk, mv, ctas, s) : cattn::launch_cached_tiles(a, mk, mv, ctas, s);
     if (e == cudaSuccess) ++*launches, e = cattn::launch_join(a, ctas, s);
     if (e == cudaSuccess) ++*launches;
     return e;

@@ -1,0 +1,484 @@
+// cattn_tiles.cu -- attention over the paged cache for many rows: chunks of prompts.
+//
+// As the forward kernel of packed attention (pattn_forward.cu): a CTA has two halves of
+// 128 rows, whose warps turn scores into weights by turns while the tensor core works
+// for the other half.  Rows are a run of a sequence's new tokens times the query heads
+// that share a key / value head, so that the pages are read once for all of them.  The
+// cache's 8 bits make the difference:
+//   S_t = Q_t K^T      the keys go into the tensor core as they are; a query is split into
+//                      2 (bf16) or 3 (fp16) e4m3 numbers that add up to it, whose products go
+//                      into the same accumulator.  e4m3 products take half the time of
+//                      half-precision ones, so bf16 queries cost no more than before;
+//   P_t = 2^(S_t c + log2 v - m)   c the key's scale, v the value's, both one number for every 8
+//                      keys: v leaves the weights' sum again;
+//   O_t += P_t V       in fp16: a warp of its own widens the values, e4m3 is exact there.
+//                      (Splitting the weights would cost the softmax warps, which
+//                      bound this kernel, six operations more for every two.)
+// One CTA per SM, with an equal part of all blocks (cattn_common.cuh).
+#include <algorithm>
+
+#include "cattn_common.cuh"
+
+namespace gn {
+namespace cattn {
+namespace {
+
+constexpr int kThreads = 384;    // warps: 0 loads, 1 MMA, 2 the MMA's waits, 3 widens values, 4-7 and 8-11 the halves' softmax
+constexpr int kKeyStages = 3;    // at most
+constexpr int kScales = 4;       // blocks whose scales are in shared memory
+constexpr float kLeastScale = 0x1p-100f;
+constexpr float kShift = 7.0f;   // fp16 weights, away from its subnormals (weight_shift of packed attention)
+constexpr uint32_t kWide = 2 * kHalfBytes;    // a tile of values in fp16
+
+// kP: per half the weights of a block's first and last 64 keys; kWideFull: the values widened
+enum Bar { kQ = 0, kKFull = 2, kKEmpty = kKFull + kKeyStages, kVFull = kKEmpty + kKeyStages, kVEmpty = kVFull + 2,
+           kWideFull = kVEmpty + 2, kWideEmpty = kWideFull + 2, kS = kWideEmpty + 2, kP = kS + 2, kO = kP + 4, kScale = kO + 2,
+           kDrain = kScale + kScales, kBars };
+
+struct Layout {
+    uint32_t q, keys, values, wide, scales, bars, words, deal, total;
+};
+
+__host__ __device__ constexpr Layout layout(int parts)
+{
+    Layout l = {};
+    l.q = 0;                                                       // [2][parts] tiles
+    l.keys = 2 * static_cast<uint32_t>(parts) * kTileBytes;
+    l.values = l.keys + (parts == 2 ? kKeyStages : 2) * kTileBytes;
+    l.wide = l.values + 2 * kTileBytes;
+    l.scales = l.wide + 2 * kWide;                                 // kScales x 16 groups of 8 keys
+    l.bars = l.scales + kScales * 16 * sizeof(float4);
+    l.words = l.bars + 8 * kBars;                                  // tensor-memory slot, abort
+    l.deal = (l.words + 16 + 15) / 16 * 16;
+    l.total = l.deal + sizeof(DealRoom);
+    return l;
+}
+
+// One tile's values in fp16 ([2][128 tokens][64 channels], 128-byte swizzle) from their
+// bytes; rows from `rows` on become zeros (0 x NaN is not 0).  Eight lanes at a time take
+// four pieces of 16 channels of rows r and r ^ 5, which lie in all 32 banks, both where
+// they are read and where they are written.
+__device__ __forceinline__ void widen(uint32_t from, uint32_t to, int dim, int rows)
+{
+    const int lane = threadIdx.x & 31, q0 = lane & 3, flip = lane & 4 ? 5 : 0, base = lane >> 3;
+    for (int part = 0; part * 64 < dim; ++part) {
+        const int q = part * 4 + q0;
+#pragma unroll 4
+        for (int i = 0; i < kTile / 8; ++i) {
+            // rows 8 i + {0, 1, 2, 3} and, flipped, 8 i + {5, 4, 7, 6}
+            const int r = 8 * i + (base ^ flip);
+            const uint32_t key = r & 7u;
+            uint4 v = lds128(from + r * 128u + ((q ^ key) << 4));
+            if (r >= rows) v = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t at = to + part * kHalfBytes + r * 128u;
+            sts128(at + (((2u * q0) ^ key) << 4),
+                   make_uint4(e4m3_half2(v.x), e4m3_half2(v.x >> 16), e4m3_half2(v.y), e4m3_half2(v.y >> 16)));
+            sts128(at + (((2u * q0 + 1u) ^ key) << 4),
+                   make_uint4(e4m3_half2(v.z), e4m3_half2(v.z >> 16), e4m3_half2(v.w), e4m3_half2(v.w >> 16)));
+        }
+    }
+}
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    cached_tiles_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                        const __grid_constant__ CattnArgs args)
+{
+    constexpr int PARTS = IsBf16<T>::value ? 2 : 3, KEYS = PARTS == 2 ? kKeyStages : 2;
+    constexpr Layout lay = layout(PARTS);
+    extern __shared__ __align__(1024) uint8_t gbase[];
+    const uint32_t base = smem_addr(gbase);
+    const gn_cache &c = args.p.c;
+    const gn_attn_cached_args &a = args.p.a;
+    const auto bar = [&](int i) { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
+    volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(gbase + lay.words);
+    volatile int *abort = reinterpret_cast<volatile int *>(words + 1);
+    float4 *scales = reinterpret_cast<float4 *>(gbase + lay.scales);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i < kQ + 2 || (i >= kP && i < kP + 4) ? 4 : 1);
+        *abort = (*reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) ? 1 : 0;
+        mbar_init_fence();
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+    }
+    if (warp == 1) {
+        tmem_alloc(base + lay.words, 512);
+        tmem_relinquish();
+    }
+    tc::griddep_wait();
+    const Part part = deal(args, *reinterpret_cast<DealRoom *>(gbase + lay.deal), gridDim.x);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    // (only now: a kernel that starts early must not find tensor memory that a
+    // CTA of this one has yet to take)
+    if (threadIdx.x == 0) tc::griddep_launch_dependents();
+    const uint32_t tmem = words[0];
+    const bool skip = *abort != 0;
+
+    Walk walk(args);
+    walk.start(part.seq, part.offset, skip ? 0 : part.count);
+    Segment g;
+    const auto rows_of = [&](const Segment &s) {
+        return min(args.tokens, s.s.end - s.s.begin - s.run * args.tokens) * args.heads;
+    };
+    if (warp >= 4) {
+        many_registers();
+        // ---- softmax: one row per thread ----
+        const int half = warp >= 8 ? 1 : 0, r = (warp & 3) * 32 + lane, row = half * kTile + r;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + 128 * half, to = tmem + lanes + 256 + 128 * half;
+        gn_attn_packed_args bend = {};
+        bend.scale = a.scale;
+        bend.cap = a.cap;
+        int n = 0, block = 0, mine = 0;        // blocks of this half, of the CTA, tiles of this half
+        while (walk.next(g)) {
+            const int live = rows_of(g);
+            if (half * kTile >= live) {        // (the whole half has no rows)
+                block += g.b1 - g.b0;
+                continue;
+            }
+            const int first_token = g.run * args.tokens, keys = keys_of(args, g.s, g.run);
+            const auto place_of = [&](int i) { return g.s.first_place() + first_token + i / args.heads; };
+            const auto end_of = [&](int place) { return a.causal ? min(max(place + 1, 0), g.s.length) : g.s.length; };
+            const int place = place_of(min(row, live - 1)), end = end_of(place), all = end_of(place_of(half * kTile));
+            // the queries in parts
+            float factor = 0.f;
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i) {
+                const int at = (warp & 3) * 32 + i, h = g.first_head + (half * kTile + at) % args.heads;
+                const int64_t token = g.s.begin + first_token + (half * kTile + at) / args.heads;
+                const bool there = half * kTile + at < live && h < args.p.group && 4 * lane < c.dim;
+                const float4 f = there ? load4<T>(a.q, token * a.q_token + (g.hk * args.p.group + h) * a.q_head, lane, c.dim)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                float x[4] = {f.x, f.y, f.z, f.w}, most = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) most = max_nan(most, fabsf(x[e]));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+                const int shift = most < INFINITY ? query_shift(most) : 0;
+                const float up = most < INFINITY ? power_of_two(shift) : NAN;
+                uint32_t w[PARTS];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] *= up;
+                split_e4m3<PARTS>(x, w);
+                const uint32_t dst = base + lay.q + half * PARTS * kTileBytes + at * 128u + (((lane >> 2) ^ (at & 7u)) << 4) + (lane & 3u) * 4u;
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + p * kTileBytes), "r"(w[p]) : "memory");
+                if (lane == i) factor = power_of_two(-shift);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kQ + half));
+            const int head = g.hk * args.p.group + g.first_head + row % args.heads;
+            const bool there = row < live && g.first_head + row % args.heads < args.p.group;
+            const float slope2 = (MODE & kBias) && a.slopes && there ? __ldg(a.slopes + head) * kLog2e : 0.f;
+            const float by = MODE ? factor : factor * args.scale_log2;
+            float m = -INFINITY, l = 0.f;
+            for (int b = g.b0; b < g.b1; ++b, ++n, ++block) {
+                const int j0 = b * kTile;
+                const bool masked = j0 + kTile > all;
+                wait_warp(bar(kScale + block % kScales), (block / kScales) & 1, abort, args.limit);
+                const float4 *scale = scales + (block % kScales) * 16;
+                wait_warp(bar(kS + half), n & 1, abort, args.limit);
+                tc_fence_after_sync();
+                float s[kTile];
+                tmem_ld_all(ts, s);
+                float bent = 1.0f;
+                if (MODE) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        const float f = by * scale[q].x;
+                        const uint64_t f2 = pack2(f, f);
+#pragma unroll
+                        for (int k = 8 * q; k < 8 * q + 8; k += 2) {
+                            const float2 v = unpack2(mul2(pack2(s[k], s[k + 1]), f2));
+                            s[k] = v.x;
+                            s[k + 1] = v.y;
+                        }
+                    }
+                    bent = bend_scores<MODE>(s, bend, args.scale_log2, slope2, place - j0);
+                }
+                if (masked) mask_scores(s, 0, static_cast<unsigned>(max(0, end - j0)));
+                float mx = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const float2 kv = *reinterpret_cast<const float2 *>(scale + q);
+                    float top = fmaxf(s[8 * q], s[8 * q + 1]);
+#pragma unroll
+                    for (int k = 2; k < 8; ++k) top = fmaxf(top, s[8 * q + k]);
+                    mx = fmaxf(mx, fmaf(top, MODE ? bent : by * kv.x, kv.y));
+                }
+                const bool grew = mx > m + (kShift + kRescaleLog2) || (b == g.b0 && mx > m);
+                if (__any_sync(0xffffffffu, grew)) {
+                    const float to_m = grew ? mx - kShift : m;
+                    const float f = grew && m != -INFINITY ? ex2_approx(m - to_m) : 1.0f;
+                    m = to_m;
+                    l *= f;
+                    if (b > g.b0) rescale_columns(to, f);
+                }
+                // the weights, 32 keys at a time; the first 64 are handed over early
+                const float m_use = m == -INFINITY ? 0.f : m;
+                uint64_t sum2[2] = {0, 0};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 kv = scale[4 * q + e];
+                        const float f = MODE ? bent : by * kv.x, add = kv.y - m_use;
+                        const uint64_t c2 = pack2(f, f), m2 = pack2(add, add);
+                        uint64_t eight = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int at = 32 * q + 8 * e + 2 * k;
+                            const float2 x = unpack2(fma2(pack2(s[at], s[at + 1]), c2, m2));
+                            float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+                            if (masked) {
+                                // (an unseen key's scale may be no number)
+                                p0 = s[at] == -INFINITY ? 0.f : p0;
+                                p1 = s[at + 1] == -INFINITY ? 0.f : p1;
+                            }
+                            eight = add2(eight, pack2(p0, p1));
+                            pk[4 * e + k] = Half2<__half>::pack(p0, p1);
+                        }
+                        const float2 sum = unpack2(eight);
+                        const float got = sum.x + sum.y;
+                        if (!masked || got != 0.f) sum2[0] = fma2(eight, pack2(kv.z, kv.z), sum2[0]);
+                    }
+                    tmem_st16(ts + 16 * q, pk);
+                    if (q == 1) {
+                        tmem_wait_st();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kP + 2 * half));
+                    }
+                }
+                const float2 sums = unpack2(add2(sum2[0], sum2[1]));
+                l += sums.x + sums.y;
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kP + 2 * half + 1));
+            }
+            wait_warp(bar(kO + half), mine & 1, abort, args.limit);
+            ++mine;
+            tc_fence_after_sync();
+            const bool whole = g.b0 == 0 && g.b1 == g.total, good = *abort == 0;
+            const int64_t token = g.s.begin + first_token + row / args.heads;
+            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            T *dst = static_cast<T *>(a.out) + (token * a.heads + head) * c.dim;
+            float *piece = piece_of(args, blockIdx.x, g.b0 == 0 ? 1 : 0);
+            float *dst_piece = piece + 2 * args.rows + static_cast<int64_t>(row) * c.dim;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                if (32 * q >= c.dim) break;
+                float o[32];
+                tmem_ld32(to + 32 * q, o);
+                tmem_wait_ld();
+                if (!there || !good) continue;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int ch = 32 * q + 8 * k;
+                    if (ch >= c.dim) continue;
+                    if (whole) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = l == 0.f ? 0u : Half2<T>::pack(o[8 * k + 2 * e] * inv, o[8 * k + 2 * e + 1] * inv);
+                        *reinterpret_cast<uint4 *>(dst + ch) = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; e += 4)
+                            *reinterpret_cast<float4 *>(dst_piece + ch + e) =
+                                make_float4(o[8 * k + e], o[8 * k + e + 1], o[8 * k + e + 2], o[8 * k + e + 3]);
+                    }
+                }
+            }
+            if (there && good) {
+                if (whole) {
+                    a.lse[static_cast<int64_t>(head) * a.tokens + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                } else {
+                    piece[row] = m;
+                    piece[args.rows + row] = l;
+                }
+            }
+            tc_fence_before_sync();
+        }
+    } else {
+        few_registers();
+        if (warp == 0) {
+            // ---- loads, and every 8 keys' scales by a lane of its own: asked for ahead of a
+            // block's loads and stored behind them.  (Their slot was last read kScales blocks
+            // ago, by a softmax whose products the values' stages have waited for.)
+            const int step = args.chunk / 8;
+            int block = 0, key_tiles = 0, value_tiles = 0;
+            bool go = true;
+            while (go && walk.next(g)) {
+                const int keys = keys_of(args, g.s, g.run);
+                int key = g.b0 * kTile + lane * 8;
+                bool mine = lane < 16 && key < keys;
+                int page = mine ? page_for(args, g.seq, key) : 0;
+                for (int b = g.b0; go && b < g.b1; ++b, ++block) {
+                    const int key_now = key, page_now = page;
+                    const bool now = mine, load = lane < 16 && lane % step == 0 && now;
+                    float ks = 0.f, vs = 0.f;
+                    if (now && page_now < c.pages) {
+                        ks = __ldg(c.k_scales + static_cast<int64_t>(page_now) * c.kv_heads + g.hk);
+                        vs = __ldg(c.v_scales + static_cast<int64_t>(page_now) * c.kv_heads + g.hk);
+                    }
+                    key += kTile;
+                    mine = lane < 16 && key < keys && b + 1 < g.b1;
+                    if (mine) page = page_for(args, g.seq, key);
+                    go = block < KEYS || wait_warp(bar(kKEmpty + block % KEYS), (block / KEYS - 1) & 1, abort, args.limit);
+                    if (!go) break;
+                    load_pages(base + lay.keys + block % KEYS * kTileBytes, &map_k, args, key_now, page_now, g.hk, bar(kKFull + block % KEYS), load);
+                    ++key_tiles;
+                    go = block < 2 || wait_warp(bar(kVEmpty + block % 2), (block / 2 - 1) & 1, abort, args.limit);
+                    if (!go) break;
+                    load_pages(base + lay.values + block % 2 * kTileBytes, &map_v, args, key_now, page_now, g.hk, bar(kVFull + block % 2), load);
+                    ++value_tiles;
+                    vs = vs < kLeastScale ? kLeastScale : vs;
+                    if (lane < 16) scales[(block % kScales) * 16 + lane] = make_float4(ks, log2f(vs), 1.0f / vs, 0.f);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kScale + block % kScales));
+                }
+            }
+            // nothing is left in flight when the CTA ends, whatever became of the others
+            for (int k = max(0, key_tiles - KEYS); k < key_tiles; ++k)
+                tc::drain(bar(kKFull + k % KEYS), (k / KEYS) & 1, args.limit.timeout_ns);
+            for (int k = max(0, value_tiles - 2); k < value_tiles; ++k)
+                tc::drain(bar(kVFull + k % 2), (k / 2) & 1, args.limit.timeout_ns);
+            __syncwarp();
+        } else if (warp == 3) {
+            // ---- values to fp16 ----
+            int block = 0;
+            while (walk.next(g)) {
+                const int keys = keys_of(args, g.s, g.run);
+                for (int b = g.b0; b < g.b1; ++b, ++block) {
+                    wait_warp(bar(kVFull + block % 2), (block / 2) & 1, abort, args.limit);
+                    if (block >= 2) wait_warp(bar(kWideEmpty + block % 2), (block / 2 - 1) & 1, abort, args.limit);
+                    widen(base + lay.values + block % 2 * kTileBytes, base + lay.wide + block % 2 * kWide, c.dim, keys - b * kTile);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(kWideFull + block % 2));
+                        mbar_arrive(bar(kVEmpty + block % 2));
+                    }
+                }
+            }
+        } else {
+            // ---- MMA: per block and half the weighted values of the block before, then
+            // the scores of this one ----
+            const bool waits = warp == 2;
+            const int steps = (c.dim + 31) / 32;
+            const uint32_t is = instruction_e4m3(kTile, false), io = instruction<__half>((c.dim + 15) / 16 * 16, true);
+            int block = 0, tiles = 0, n[2] = {0, 0}, q_full[2] = {0, 0};
+            for (; walk.next(g); ++tiles) {
+                const int halves = rows_of(g) > kTile ? 2 : 1, blocks = g.b1 - g.b0;
+                for (int b = 0; b <= blocks; ++b) {
+                    const int nv = block + b - 1, nk = block + b;
+                    const uint32_t v_tile = base + lay.wide + (nv & 1) * kWide;
+                    if (waits) {
+                        if (b > 0) wait_warp(bar(kWideFull + (nv & 1)), (nv >> 1) & 1, abort, args.limit);
+                        if (b < blocks) wait_warp(bar(kKFull + nk % KEYS), (nk / KEYS) & 1, abort, args.limit);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t >= halves) break;
+                        if (b > 0) {
+#pragma unroll
+                            for (int part_of_keys = 0; part_of_keys < 2; ++part_of_keys) {
+                                if (waits) wait_warp(bar(kP + 2 * t + part_of_keys), (n[t] + b - 1) & 1, abort, args.limit);
+                                hand_over();
+                                if (waits) continue;
+                                tc_fence_after_sync();
+                                mma_channels(tmem + 256 + 128 * t, tmem + 128 * t + 32 * part_of_keys, v_tile, part_of_keys, io,
+                                             b > 1 || part_of_keys);
+                            }
+                            if (!waits && b == blocks) commit(bar(kO + t));
+                        }
+                        if (b < blocks) {
+                            if (waits && b == 0) wait_warp(bar(kQ + t), q_full[t] & 1, abort, args.limit);
+                            if (b == 0) hand_over();
+                            if (waits) continue;
+                            if (b == 0) tc_fence_after_sync();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int p = 0; p < PARTS; ++p) {
+                                    const uint64_t dq = sw128_kmajor_desc(base + lay.q + (t * PARTS + p) * kTileBytes);
+                                    const uint64_t dk = sw128_kmajor_desc(base + lay.keys + nk % KEYS * kTileBytes);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        if (k >= steps) break;
+                                        umma_e4m3(tmem + 128 * t, dq + 2 * k, dk + 2 * k, is, p > 0 || k > 0);
+                                    }
+                                }
+                            }
+                            __syncwarp();
+                            commit(bar(kS + t));
+                        }
+                    }
+                    hand_over();
+                    if (!waits) {
+                        if (b > 0) commit(bar(kWideEmpty + (nv & 1)));
+                        if (b < blocks) commit(bar(kKEmpty + nk % KEYS));
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (t < halves) {
+                        n[t] += blocks;
+                        ++q_full[t];
+                    }
+                block += blocks;
+            }
+            if (!waits && block > 0) {
+                commit(bar(kDrain));
+                tc::drain(bar(kDrain), 0, args.limit.timeout_ns);
+            }
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int MODE>
+cudaError_t launch(const CattnArgs &args, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s)
+{
+    constexpr uint32_t bytes = layout(IsBf16<T>::value ? 2 : 3).total;
+    static_assert(bytes <= 227 * 1024, "a CTA's shared memory");
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(cached_tiles_kernel<T, MODE>), bytes, done);
+    if (e != cudaSuccess) return e;
+    return tc::launch_pdl(cached_tiles_kernel<T, MODE>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), bytes, s, mk, mv, args);
+}
+
+template <typename T>
+cudaError_t launch_mode(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s)
+{
+    // (a scale that is not positive needs more than a factor at the end: a bias with slopes of 0)
+    int mode = (a.p.a.cap > 0.f ? kCap : 0) | (a.p.a.slopes ? kBias : 0);
+    if (mode == 0 && !(a.p.a.scale > 0.f)) mode = kBias;
+    if (mode == 0) return launch<T, 0>(a, mk, mv, ctas, s);
+    if (mode == kCap) return launch<T, kCap>(a, mk, mv, ctas, s);
+    if (mode == kBias) return launch<T, kBias>(a, mk, mv, ctas, s);
+    return launch<T, kCap | kBias>(a, mk, mv, ctas, s);
+}
+
+}  // namespace
+
+cudaError_t launch_cached_tiles(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s)
+{
+    return a.p.a.format == GN_FORMAT_BF16 ? launch_mode<__nv_bfloat16>(a, mk, mv, ctas, s) : launch_mode<__half>(a, mk, mv, ctas, s);
+}
+
+}  // namespace cattn
+}  // namespace gn
