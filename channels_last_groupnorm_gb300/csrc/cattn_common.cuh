@@ -30,7 +30,6 @@ struct CattnArgs {
     int rows;                     // room for rows in a tile's piece
     int chunk;                    // keys that one load brings: they lie in one page
     int extra;                    // blocks that a tile's start and end count as
-    int stages;
     float *pieces;                // [CTAs][2][rows][2 + dim]: maxima, sums, outputs
 };
 
@@ -63,7 +62,7 @@ __device__ __forceinline__ int blocks_of(const CattnArgs &a, const Sequence &s, 
 __device__ __forceinline__ int first_sequence(const CattnArgs &a) { return a.p.c.cu ? -1 : 0; }
 __device__ __forceinline__ int sequence_count(const CattnArgs &a) { return a.p.c.sequences + (a.p.c.cu ? 2 : 0); }
 
-// (units of work: a tile's first `extra` are its start and end, the others its blocks)
+// (Units of work: a tile's first `extra` are its start and end, the others its blocks.)
 struct Walk {
     const CattnArgs &a;
     int64_t left, per_head;
@@ -78,6 +77,7 @@ struct Walk {
         s = cache::sequence_of(a.p.c, a.p.a.tokens, n);
         runs = (s.end - s.begin + a.tokens - 1) / a.tokens;
         per_head = 0;
+#pragma unroll 1
         for (int r = 0; r < runs; ++r) per_head += a.extra + blocks_of(a, s, r);
     }
     __device__ __forceinline__ int heads() const { return a.p.c.kv_heads * a.chunks; }
@@ -89,8 +89,9 @@ struct Walk {
         left = count;
         if (count <= 0) return;
         load(n);
-        head = static_cast<int>(offset / per_head);
-        offset -= head * per_head;
+#pragma unroll 1
+        for (head = 0; offset >= per_head; ++head) offset -= per_head;
+#pragma unroll 1
         for (run = 0; run < runs - 1; ++run) {
             const int b = a.extra + blocks_of(a, s, run);
             if (offset < b) break;
@@ -101,6 +102,7 @@ struct Walk {
     // the next tile of which the part has blocks
     __device__ __forceinline__ bool next(Segment &g)
     {
+#pragma unroll 1
         while (left > 0) {
             g.seq = seq;
             g.s = s;
@@ -119,6 +121,7 @@ struct Walk {
                     head = 0;
                     const int last = first_sequence(a) + sequence_count(a);
                     int n = seq + 1;
+#pragma unroll 1
                     for (load(n); runs == 0 && n + 1 < last; load(n)) ++n;
                     if (runs == 0) left = 0;
                 }
@@ -129,23 +132,34 @@ struct Walk {
     }
 };
 
-// This CTA's part of the work: `count` units that begin `offset` into sequence `seq`;
-// also its number among those with work (G of them), the first unit and how many
-// there are.  For the whole CTA (threads a multiple of 32, at most 1024).
+// This CTA's part of the work: `count` units from unit `first` of `all`.  Its first unit
+// (its last, if that is what was asked for) lies `offset` into sequence `seq`.
 struct Part {
     int64_t offset, count, first, all;
-    int seq, ctas;
+    int seq, ctas;                // the CTAs that have work
 };
 
-__device__ __forceinline__ int64_t part_begin(int64_t all, int ctas, int64_t n) { return all / ctas * n + all % ctas * n / ctas; }
+// Where part n of `all` units begins.  (By a fraction of 32 bits: it only has to grow with n
+// and be the same wherever it is asked for, and a division of 64 bits is a long stretch of
+// instructions.  The fraction is a little high, so that whole parts come out whole.)
+__device__ __forceinline__ int64_t part_begin(int64_t all, int ctas, int n)
+{
+    if (n >= ctas) return all;
+    const float share = static_cast<float>(n) * __frcp_rn(static_cast<float>(ctas));
+    const uint64_t fraction = static_cast<uint64_t>(share * 4294967296.0f) + (n > 0 ? 1024u : 0u);
+    return static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(all), fraction << 32));
+}
 
 // The part that holds a unit.
 __device__ __forceinline__ int part_of(int64_t all, int ctas, int64_t unit)
 {
-    int64_t n = unit * ctas / all;
-    while (n + 1 < ctas && part_begin(all, ctas, n + 1) <= unit) ++n;
+    int n = static_cast<int>(static_cast<float>(unit) / static_cast<float>(all) * static_cast<float>(ctas));
+    n = min(max(n, 0), ctas - 1);
+#pragma unroll 1
     while (n > 0 && part_begin(all, ctas, n) > unit) --n;
-    return static_cast<int>(n);
+#pragma unroll 1
+    while (n + 1 < ctas && part_begin(all, ctas, n + 1) <= unit) ++n;
+    return n;
 }
 
 struct DealRoom {
@@ -153,13 +167,15 @@ struct DealRoom {
     Part part;
 };
 
-__device__ __forceinline__ Part deal(const CattnArgs &a, DealRoom &room, int ctas)
+// For the whole CTA (whole warps).
+__device__ __forceinline__ Part deal(const CattnArgs &a, DealRoom &room, int ctas, bool want_last = false)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int count = sequence_count(a), each = (count + blockDim.x - 1) / blockDim.x;
     const int n0 = first_sequence(a) + threadIdx.x * each, n1 = min(n0 + each, first_sequence(a) + count);
     Walk w(a);
     int64_t own = 0;
+#pragma unroll 1
     for (int n = n0; n < n1; ++n) {
         w.load(n);
         own += w.units();
@@ -175,6 +191,7 @@ __device__ __forceinline__ Part deal(const CattnArgs &a, DealRoom &room, int cta
     __syncthreads();
     int64_t all = 0;
     before -= own;
+#pragma unroll 1
     for (int i = 0; i < warps; ++i) {
         if (i < warp) before += room.sums[i];
         all += room.sums[i];
@@ -182,17 +199,72 @@ __device__ __forceinline__ Part deal(const CattnArgs &a, DealRoom &room, int cta
     const int busy = static_cast<int>(all < ctas ? (all > 0 ? all : 1) : ctas);
     if (static_cast<int>(blockIdx.x) < busy && all > 0) {
         const int64_t u0 = part_begin(all, busy, blockIdx.x), u1 = part_begin(all, busy, blockIdx.x + 1);
-        if (u0 >= before && u0 < before + own) {
+        const int64_t at = want_last ? u1 - 1 : u0;
+        if (u0 < u1 && at >= before && at < before + own) {
             int n = n0;
-            for (w.load(n); before + w.units() <= u0 && n + 1 < n1; w.load(n)) {
+#pragma unroll 1
+            for (w.load(n); before + w.units() <= at && n + 1 < n1; w.load(n)) {
                 before += w.units();
                 ++n;
             }
-            room.part = {u0 - before, u1 - u0, u0, all, n, busy};
+            room.part = {at - before, u1 - u0, u0, all, n, busy};
         }
     }
     __syncthreads();
     return room.part;
+}
+
+// A CTA's segments, found by one thread and read by all roles, K at a time.  (Each role
+// walking by itself would be five copies of the walk, which pushed what the roles loop over
+// out of the instruction cache.)
+template <int K>
+struct WorkList {
+    Segment list[K];
+    int count, more;
+};
+
+// Every role of the CTA calls next() until it says no, whatever becomes of the others: the
+// list is refilled between two barriers of all threads.  fill(list) is the loader's.
+template <int K>
+struct Reader {
+    WorkList<K> &work;
+    int at = 0, count = 0, more = 1;
+
+    __device__ __forceinline__ explicit Reader(WorkList<K> &w) : work(w) {}
+
+    template <typename F>
+    __device__ __forceinline__ bool next(Segment &g, F &&fill)
+    {
+        if (at == count) {
+            if (!more) return false;
+            named_sync(0, blockDim.x);
+            fill(work);
+            named_sync(0, blockDim.x);
+            count = work.count;
+            more = work.more;
+            at = 0;
+            if (count == 0) return false;
+        }
+        g = work.list[at++];
+        return true;
+    }
+    __device__ __forceinline__ bool next(Segment &g)
+    {
+        return next(g, [](WorkList<K> &) {});
+    }
+};
+
+template <int K>
+__device__ __forceinline__ void fill_work(WorkList<K> &w, Walk &walk)
+{
+    if ((threadIdx.x & 31) == 0) {
+        int n = 0;
+#pragma unroll 1
+        while (n < K && walk.next(w.list[n])) ++n;
+        w.count = n;
+        w.more = n == K;
+    }
+    __syncwarp();
 }
 
 cudaError_t launch_join(const CattnArgs &a, int ctas, cudaStream_t s);

@@ -28,6 +28,7 @@ namespace cattn {
 namespace {
 
 constexpr int kThreads = 256;   // warps: 0 loads, 1 MMA, 2 the MMA's waits, 3 the next tile's rows, 4-7 softmax
+constexpr int kSegments = 32;  // that are found at a time
 constexpr int kScales = 4;      // blocks whose scales are in shared memory
 constexpr int kMaxStages = 6;
 // Weights: the row's largest at 2^6 when the maximum moves, which it does once a score
@@ -50,12 +51,12 @@ struct __align__(16) Row {
 };
 
 struct Layout {
-    uint32_t q, weights, operand, ring, rows, tops, scales, bars, words, deal, total;
+    uint32_t q, weights, operand, ring, rows, tops, scales, bars, words, deal, work, total;
 };
 
-__host__ __device__ inline Layout layout(int n, int parts, int stages)
+__host__ __device__ constexpr Layout layout(int n, int parts, int stages)
 {
-    Layout l;
+    Layout l = {};
     const uint32_t operand = static_cast<uint32_t>(parts) * static_cast<uint32_t>(n) * 128u;
     l.operand = operand;
     l.q = 0;                                                        // two of each: this tile's and the next one's,
@@ -67,8 +68,18 @@ __host__ __device__ inline Layout layout(int n, int parts, int stages)
     l.bars = l.scales + kScales * 16 * sizeof(float4);
     l.words = l.bars + 8 * kBars;                                   // tensor-memory slot, abort
     l.deal = l.words + 16;
-    l.total = l.deal + sizeof(DealRoom);
+    l.work = l.deal + sizeof(DealRoom);
+    l.total = l.work + sizeof(WorkList<kSegments>);
     return l;
+}
+
+// (two CTAs on an SM: 113 KB each)
+constexpr uint32_t kRoom = 113 * 1024;
+__host__ __device__ constexpr int stages_of(int n, int parts)
+{
+    int stages = kMaxStages;
+    while (layout(n, parts, stages).total > kRoom) --stages;
+    return stages;
 }
 
 __device__ __forceinline__ int ordered(float v)
@@ -116,14 +127,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     cached_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                       const __grid_constant__ CattnArgs args)
 {
-    constexpr int PARTS = IsBf16<T>::value ? 2 : 3;
+    constexpr int PARTS = IsBf16<T>::value ? 2 : 3, STAGES = stages_of(N, PARTS);
+    constexpr Layout lay = layout(N, PARTS, STAGES);
     extern __shared__ __align__(1024) uint8_t gbase[];
     const uint32_t base = smem_addr(gbase);
     const gn_cache &c = args.p.c;
     const gn_attn_cached_args &a = args.p.a;
-    const Layout lay = layout(N, PARTS, args.stages);
     const auto bar = [&](int i) { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
-    const auto stage = [&](int n) { return base + lay.ring + static_cast<uint32_t>(n % args.stages) * kTileBytes; };
+    const auto stage = [&](int n) { return base + lay.ring + static_cast<uint32_t>(n % STAGES) * kTileBytes; };
     volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(gbase + lay.words);
     volatile int *abort = reinterpret_cast<volatile int *>(words + 1);
     Row *all_rows = reinterpret_cast<Row *>(gbase + lay.rows);
@@ -154,8 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t tmem = words[0], t_s = tmem, t_o = tmem + 2 * N;
     const bool skip = *abort != 0;
 
-    Walk walk(args);
-    walk.start(part.seq, part.offset, skip ? 0 : part.count);
+    Reader<kSegments> work(*reinterpret_cast<WorkList<kSegments> *>(gbase + lay.work));
     Segment g;
     if (warp == 0) {
         // The pages, and each chunk's scales by the lane that brings it: a block's are
@@ -164,7 +174,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float by = (MODE & kCap) ? a.scale / a.cap : args.scale_log2;
         int n = 0, block = 0;         // tiles so far (keys and values by turns), blocks so far
         bool go = true;
-        while (go && walk.next(g)) {
+        Walk walk(args);
+        walk.start(part.seq, part.offset, skip ? 0 : part.count);
+        while (work.next(g, [&](WorkList<kSegments> &w) { fill_work(w, walk); })) {
+            if (!go) continue;
             const int keys = keys_of(args, g.s, g.run);
             int key = g.b0 * kTile + lane * args.chunk;
             bool mine = lane * args.chunk < kTile && key < keys;
@@ -181,8 +194,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 mine = lane * args.chunk < kTile && key < keys && b + 1 < g.b1;
                 if (mine) page = page_for(args, g.seq, key);
                 for (int e = 0; go && e < 2; ++e, ++n) {
-                    const int st = n % args.stages;
-                    if (n >= args.stages && !wait_warp(bar(kEmpty + st), (n / args.stages - 1) & 1, abort, args.limit)) {
+                    const int st = n % STAGES;
+                    if (n >= STAGES && !wait_warp(bar(kEmpty + st), (n / STAGES - 1) & 1, abort, args.limit)) {
                         go = false;
                         break;
                     }
@@ -195,14 +208,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
         // nothing is left in flight when the CTA goes on, whatever became of the others
-        for (int k = max(0, n - args.stages); k < n; ++k)
-            tc::drain(bar(kFull + k % args.stages), (k / args.stages) & 1, args.limit.timeout_ns);
+        for (int k = max(0, n - STAGES); k < n; ++k)
+            tc::drain(bar(kFull + k % STAGES), (k / STAGES) & 1, args.limit.timeout_ns);
         __syncwarp();
     } else if (warp == 1 || warp == 2) {
         const bool waits = warp == 2;
         const int steps = (c.dim + 31) / 32;
         const uint32_t is = instruction_e4m3(N, false), io = instruction_e4m3(PARTS * N, true);
-        const auto loaded = [&](int n) { wait_warp(bar(kFull + n % args.stages), (n / args.stages) & 1, abort, args.limit); };
+        const auto loaded = [&](int n) { wait_warp(bar(kFull + n % STAGES), (n / STAGES) & 1, abort, args.limit); };
         const auto scores = [&](int n, int q) {       // block n's with query buffer q, into buffer n & 1
             if (elect_one()) {
 #pragma unroll
@@ -217,10 +230,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             __syncwarp();
             commit(bar(kS + (n & 1)));
-            commit(bar(kEmpty + 2 * n % args.stages));
+            commit(bar(kEmpty + 2 * n % STAGES));
         };
         int n = 0, segment = 0;                       // blocks, tiles so far
-        for (; walk.next(g); ++segment) {
+        for (; work.next(g); ++segment) {
             if (waits) {
                 wait_warp(bar(kQ + (segment & 1)), (segment >> 1) & 1, abort, args.limit);
                 loaded(2 * n);
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         for (int k = 0; k < 4; ++k) umma_e4m3(t_o, dv + k * (4096u >> 4), dw + 2 * k, io, b > g.b0 || k > 0);
                     }
                     __syncwarp();
-                    commit(bar(kEmpty + (2 * n + 1) % args.stages));
+                    commit(bar(kEmpty + (2 * n + 1) % STAGES));
                     commit(bar(kO + (n & 1)));
                 }
             }
@@ -262,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else if (warp == 3) {
         // the rows of a tile while the one before it is worked on
-        for (int segment = 0; walk.next(g); ++segment) {
+        for (int segment = 0; work.next(g); ++segment) {
             const int buffer = segment & 1;
             Row *rows = all_rows + buffer * N;
             const int first_token = g.run * args.tokens, live = min(args.tokens, g.s.end - g.s.begin - first_token) * args.heads;
@@ -282,10 +295,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 rows[lane] = row;
             }
             __syncwarp();
-#pragma unroll 4
+            int h = g.first_head;
+            int64_t token = g.s.begin + first_token;
+#pragma unroll 2
             for (int q = 0; q < live; ++q) {
-                const int h = g.first_head + q % args.heads;
-                const int64_t token = g.s.begin + first_token + q / args.heads;
                 const bool there = h < args.p.group && 4 * lane < c.dim;
                 const float4 f = there ? load4<T>(a.q, token * a.q_token + (g.hk * args.p.group + h) * a.q_head, lane, c.dim)
                                        : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -305,6 +318,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int p = 0; p < PARTS; ++p)
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + p * N * 128u), "r"(w[p]) : "memory");
                 if (lane == 0) rows[q].factor = power_of_two(-shift);
+                if (++h == g.first_head + args.heads) {
+                    h = g.first_head;
+                    ++token;
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -318,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t piece = static_cast<uint32_t>(r >> 4);
         const int my_chunk = r / args.chunk;
         int n = 0;
-        for (int segment = 0; walk.next(g); ++segment) {
+        for (int segment = 0; work.next(g); ++segment) {
             Row *rows = all_rows + (segment & 1) * N;
             const int first_token = g.run * args.tokens, live = min(args.tokens, g.s.end - g.s.begin - first_token) * args.heads;
             const int keys = keys_of(args, g.s, g.run);
@@ -432,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (first + kTile > keys) {
                     // what lies behind the sequence has weight 0, but 0 x NaN is not 0
                     const int nv = 2 * n + 1;
-                    wait_warp(bar(kFull + nv % args.stages), (nv / args.stages) & 1, abort, args.limit);
+                    wait_warp(bar(kFull + nv % STAGES), (nv / STAGES) & 1, abort, args.limit);
                     if (j >= keys) zero_tile_row(stage(nv), r);
                 }
                 fence_proxy_async_smem();
@@ -514,16 +531,12 @@ template <typename T, int MODE, int N>
 cudaError_t launch(const CattnArgs &args, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s)
 {
     constexpr int PARTS = IsBf16<T>::value ? 2 : 3;
-    CattnArgs a = args;
-    // (two CTAs on an SM: 113 KB each)
-    a.stages = kMaxStages;
-    while (layout(N, PARTS, a.stages).total > 113 * 1024) --a.stages;
     static std::atomic<uint64_t> done{0}, wide{0};
     const Kernel kernel = cached_few_kernel<T, MODE, N>;
-    cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), 113 * 1024, done);
+    cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kRoom, done);
     if (e == cudaSuccess) e = allow_clusters(reinterpret_cast<const void *>(kernel), wide);
     if (e != cudaSuccess) return e;
-    return tc::launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), layout(N, PARTS, a.stages).total, s, mk, mv, a);
+    return tc::launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), layout(N, PARTS, stages_of(N, PARTS)).total, s, mk, mv, args);
 }
 
 template <typename T, int MODE>

@@ -9,8 +9,7 @@ namespace cattn {
 namespace {
 
 // Joins the pieces of the tiles that several CTAs shared.  Block (c, y) looks after the
-// tile in which the c-th part of the work begins, if part c - 1 holds the tile's first
-// unit, and there after some of its rows, a warp each: the pieces' maxima and sums on the lanes first,
+// tile that begins in the c-th part of the work and ends behind it, and there after some of its rows, a warp each: the pieces' maxima and sums on the lanes first,
 // then their outputs, four channels a lane, whose loads wait for nothing.
 constexpr int kJoinThreads = 256;
 
@@ -22,16 +21,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     const gn_cache &c = args.p.c;
     const gn_attn_cached_args &a = args.p.a;
-    const Part part = deal(args, room, gridDim.x);
+    const Part part = deal(args, room, gridDim.x, true);
     if (part.count == 0 || *reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) return;
-    // the tile in which this part begins, and its units [begin, end)
+    // the tile in which this part ends: of units from `begin` on, blocks from `blocks` on
     Walk walk(args);
-    walk.start(part.seq, part.offset, part.count);
-    const int64_t begin = part.first - walk.unit;
-    if (walk.unit == 0 || part_begin(part.all, part.ctas, static_cast<int64_t>(blockIdx.x) - 1) > begin) return;
+    walk.start(part.seq, part.offset, 1);
     const Sequence s = walk.s;
+    const int64_t begin = part.first + part.count - 1 - walk.unit, blocks = begin + args.extra;
+    const int64_t end = blocks + blocks_of(args, s, walk.run);
+    if (begin < part.first || end <= part.first + part.count) return;
     const int hk = walk.head / args.chunks, first_head = (walk.head - hk * args.chunks) * args.heads;
-    const int64_t blocks = begin + args.extra, end = blocks + blocks_of(args, s, walk.run);
     // the parts that have blocks of it: the first left its piece in slot 1, the others in slot 0
     const int from = part_of(part.all, part.ctas, blocks), pieces = part_of(part.all, part.ctas, end - 1) + 1 - from;
     if (pieces == 1) return;              // it wrote the outputs itself
@@ -55,7 +54,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
                 sum = fmaf(f, l, sum);
             }
             const int count = min(32, pieces - p0);
-#pragma unroll 8
+#pragma unroll 4
             for (int p = 0; p < count; ++p) {
                 const float g = __shfl_sync(0xffffffffu, f, p);
                 if (4 * lane < c.dim)
@@ -105,7 +104,7 @@ CattnArgs plan(const CachedAttn &p, bool *few)
     a.tokens = most / a.heads;
     if (!p.c.cu) a.tokens = static_cast<int>(std::min<int64_t>(a.tokens, each));
     a.rows = !*few ? kManyRows : a.tokens * a.heads <= 16 ? 16 : kFewRows;
-    a.extra = 3;
+    a.extra = *few ? 4 : 8;
     a.chunk = kTile;
     while (p.c.page_size % a.chunk) a.chunk /= 2;
     return a;

@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kThreads = 384;    // warps: 0 loads, 1 MMA, 2 the MMA's waits, 3 widens values, 4-7 and 8-11 the halves' softmax
 constexpr int kKeyStages = 3;    // at most
+constexpr int kSegments = 16;  // that are found at a time
 constexpr int kScales = 4;       // blocks whose scales are in shared memory
 constexpr float kLeastScale = 0x1p-100f;
 constexpr float kShift = 7.0f;   // fp16 weights, away from its subnormals (weight_shift of packed attention)
@@ -36,7 +37,7 @@ enum Bar { kQ = 0, kKFull = 2, kKEmpty = kKFull + kKeyStages, kVFull = kKEmpty +
            kDrain = kScale + kScales, kBars };
 
 struct Layout {
-    uint32_t q, keys, values, wide, scales, bars, words, deal, total;
+    uint32_t q, keys, values, wide, scales, bars, words, deal, work, total;
 };
 
 __host__ __device__ constexpr Layout layout(int parts)
@@ -50,7 +51,8 @@ __host__ __device__ constexpr Layout layout(int parts)
     l.bars = l.scales + kScales * 16 * sizeof(float4);
     l.words = l.bars + 8 * kBars;                                  // tensor-memory slot, abort
     l.deal = (l.words + 16 + 15) / 16 * 16;
-    l.total = l.deal + sizeof(DealRoom);
+    l.work = l.deal + sizeof(DealRoom);
+    l.total = l.work + sizeof(WorkList<kSegments>);
     return l;
 }
 
@@ -77,6 +79,47 @@ __device__ __forceinline__ void widen(uint32_t from, uint32_t to, int dim, int r
                    make_uint4(e4m3_half2(v.z), e4m3_half2(v.z >> 16), e4m3_half2(v.w), e4m3_half2(v.w >> 16)));
         }
     }
+}
+
+// A row's query (none: zeros) as row r of PARTS tiles; returns what its products are to be
+// multiplied by.
+template <typename T, int PARTS>
+__device__ __forceinline__ float split_query(const T *q, int dim, uint32_t tiles, int r)
+{
+    uint4 raw[16];
+    constexpr uint32_t kInf = IsBf16<T>::value ? 0x7f80u : 0x7c00u;
+    uint32_t most2 = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        raw[i] = q && 8 * i < dim ? __ldg(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0u, 0u, 0u, 0u);
+        most2 = __vmaxu2(most2, __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                                         __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu)));
+    }
+    const uint32_t top = max(most2 & 0xffffu, most2 >> 16);
+    // (infinities too: their products with keys of either sign are no numbers)
+    const bool number = top < kInf;
+    const int shift = number ? query_shift(Half2<T>::unpack(top).x) : 0;
+    const float up = number ? power_of_two(shift) : NAN;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w[8] = {raw[2 * i].x, raw[2 * i].y, raw[2 * i].z, raw[2 * i].w,
+                               raw[2 * i + 1].x, raw[2 * i + 1].y, raw[2 * i + 1].z, raw[2 * i + 1].w};
+        uint32_t bytes[PARTS][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 lo = Half2<T>::unpack(w[2 * e]), hi = Half2<T>::unpack(w[2 * e + 1]);
+            float x[4] = {lo.x * up, lo.y * up, hi.x * up, hi.y * up};
+            uint32_t b[PARTS];
+            split_e4m3<PARTS>(x, b);
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) bytes[p][e] = b[p];
+        }
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+            sts128(tiles + p * kTileBytes + r * 128u + ((i ^ (r & 7u)) << 4),
+                   make_uint4(bytes[p][0], bytes[p][1], bytes[p][2], bytes[p][3]));
+    }
+    return power_of_two(-shift);
 }
 
 template <typename T, int MODE>
@@ -118,8 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = words[0];
     const bool skip = *abort != 0;
 
-    Walk walk(args);
-    walk.start(part.seq, part.offset, skip ? 0 : part.count);
+    Reader<kSegments> work(*reinterpret_cast<WorkList<kSegments> *>(gbase + lay.work));
     Segment g;
     const auto rows_of = [&](const Segment &s) {
         return min(args.tokens, s.s.end - s.s.begin - s.run * args.tokens) * args.heads;
@@ -134,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bend.scale = a.scale;
         bend.cap = a.cap;
         int n = 0, block = 0, mine = 0;        // blocks of this half, of the CTA, tiles of this half
-        while (walk.next(g)) {
+        while (work.next(g)) {
             const int live = rows_of(g);
             if (half * kTile >= live) {        // (the whole half has no rows)
                 block += g.b1 - g.b0;
@@ -144,37 +186,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const auto place_of = [&](int i) { return g.s.first_place() + first_token + i / args.heads; };
             const auto end_of = [&](int place) { return a.causal ? min(max(place + 1, 0), g.s.length) : g.s.length; };
             const int place = place_of(min(row, live - 1)), end = end_of(place), all = end_of(place_of(half * kTile));
-            // the queries in parts
-            float factor = 0.f;
-#pragma unroll 4
-            for (int i = 0; i < 32; ++i) {
-                const int at = (warp & 3) * 32 + i, h = g.first_head + (half * kTile + at) % args.heads;
-                const int64_t token = g.s.begin + first_token + (half * kTile + at) / args.heads;
-                const bool there = half * kTile + at < live && h < args.p.group && 4 * lane < c.dim;
-                const float4 f = there ? load4<T>(a.q, token * a.q_token + (g.hk * args.p.group + h) * a.q_head, lane, c.dim)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-                float x[4] = {f.x, f.y, f.z, f.w}, most = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) most = max_nan(most, fabsf(x[e]));
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-                const int shift = most < INFINITY ? query_shift(most) : 0;
-                const float up = most < INFINITY ? power_of_two(shift) : NAN;
-                uint32_t w[PARTS];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] *= up;
-                split_e4m3<PARTS>(x, w);
-                const uint32_t dst = base + lay.q + half * PARTS * kTileBytes + at * 128u + (((lane >> 2) ^ (at & 7u)) << 4) + (lane & 3u) * 4u;
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p)
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + p * kTileBytes), "r"(w[p]) : "memory");
-                if (lane == i) factor = power_of_two(-shift);
-            }
+            const int head = g.hk * args.p.group + g.first_head + row % args.heads;
+            const bool there = row < live && g.first_head + row % args.heads < args.p.group;
+            const int64_t token = g.s.begin + first_token + row / args.heads;
+            // the row's query in parts, 16 channels at a time (all are asked for at once)
+            const float factor = split_query<T, PARTS>(there ? static_cast<const T *>(a.q) + token * a.q_token + head * a.q_head : nullptr,
+                                                       c.dim, base + lay.q + half * PARTS * kTileBytes, r);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kQ + half));
-            const int head = g.hk * args.p.group + g.first_head + row % args.heads;
-            const bool there = row < live && g.first_head + row % args.heads < args.p.group;
             const float slope2 = (MODE & kBias) && a.slopes && there ? __ldg(a.slopes + head) * kLog2e : 0.f;
             const float by = MODE ? factor : factor * args.scale_log2;
             float m = -INFINITY, l = 0.f;
@@ -203,14 +223,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bent = bend_scores<MODE>(s, bend, args.scale_log2, slope2, place - j0);
                 }
                 if (masked) mask_scores(s, 0, static_cast<unsigned>(max(0, end - j0)));
+                // What a group's scores are multiplied by and what is added: a group of which the row
+                // sees nothing has weights of 0, whatever its scale is (it may be no number).
+                const auto factors = [&](int q, float &f, float &add, float &inv) {
+                    const float4 kv = scale[q];
+                    const bool any = j0 + 8 * q < end;
+                    f = any && !MODE ? by * kv.x : bent;
+                    add = any ? kv.y : -INFINITY;
+                    inv = any ? kv.z : 0.f;
+                };
                 float mx = -INFINITY;
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
-                    const float2 kv = *reinterpret_cast<const float2 *>(scale + q);
-                    float top = fmaxf(s[8 * q], s[8 * q + 1]);
+                    float f, add, inv, top = fmaxf(s[8 * q], s[8 * q + 1]);
+                    factors(q, f, add, inv);
 #pragma unroll
                     for (int k = 2; k < 8; ++k) top = fmaxf(top, s[8 * q + k]);
-                    mx = fmaxf(mx, fmaf(top, MODE ? bent : by * kv.x, kv.y));
+                    mx = fmaxf(mx, fmaf(top, f, add));
                 }
                 const bool grew = mx > m + (kShift + kRescaleLog2) || (b == g.b0 && mx > m);
                 if (__any_sync(0xffffffffu, grew)) {
@@ -222,32 +251,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // the weights, 32 keys at a time; the first 64 are handed over early
                 const float m_use = m == -INFINITY ? 0.f : m;
-                uint64_t sum2[2] = {0, 0};
+                uint64_t sum2 = 0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float4 kv = scale[4 * q + e];
-                        const float f = MODE ? bent : by * kv.x, add = kv.y - m_use;
+                        float f, add, inv;
+                        factors(4 * q + e, f, add, inv);
+                        add -= m_use;
                         const uint64_t c2 = pack2(f, f), m2 = pack2(add, add);
                         uint64_t eight = 0;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int at = 32 * q + 8 * e + 2 * k;
                             const float2 x = unpack2(fma2(pack2(s[at], s[at + 1]), c2, m2));
-                            float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-                            if (masked) {
-                                // (an unseen key's scale may be no number)
-                                p0 = s[at] == -INFINITY ? 0.f : p0;
-                                p1 = s[at + 1] == -INFINITY ? 0.f : p1;
-                            }
-                            eight = add2(eight, pack2(p0, p1));
+                            const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+                            eight = k == 0 ? pack2(p0, p1) : add2(eight, pack2(p0, p1));
                             pk[4 * e + k] = Half2<__half>::pack(p0, p1);
                         }
-                        const float2 sum = unpack2(eight);
-                        const float got = sum.x + sum.y;
-                        if (!masked || got != 0.f) sum2[0] = fma2(eight, pack2(kv.z, kv.z), sum2[0]);
+                        sum2 = fma2(eight, pack2(inv, inv), sum2);
                     }
                     tmem_st16(ts + 16 * q, pk);
                     if (q == 1) {
@@ -257,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == 0) mbar_arrive(bar(kP + 2 * half));
                     }
                 }
-                const float2 sums = unpack2(add2(sum2[0], sum2[1]));
+                const float2 sums = unpack2(sum2);
                 l += sums.x + sums.y;
                 tmem_wait_st();
                 tc_fence_before_sync();
@@ -268,7 +291,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++mine;
             tc_fence_after_sync();
             const bool whole = g.b0 == 0 && g.b1 == g.total, good = *abort == 0;
-            const int64_t token = g.s.begin + first_token + row / args.heads;
             const float inv = l == 0.f ? 0.f : 1.0f / l;
             T *dst = static_cast<T *>(a.out) + (token * a.heads + head) * c.dim;
             float *piece = piece_of(args, blockIdx.x, g.b0 == 0 ? 1 : 0);
@@ -317,7 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int step = args.chunk / 8;
             int block = 0, key_tiles = 0, value_tiles = 0;
             bool go = true;
-            while (go && walk.next(g)) {
+            Walk walk(args);
+            walk.start(part.seq, part.offset, skip ? 0 : part.count);
+            while (work.next(g, [&](WorkList<kSegments> &w) { fill_work(w, walk); })) {
+                if (!go) continue;
                 const int keys = keys_of(args, g.s, g.run);
                 int key = g.b0 * kTile + lane * 8;
                 bool mine = lane < 16 && key < keys;
@@ -356,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 3) {
             // ---- values to fp16 ----
             int block = 0;
-            while (walk.next(g)) {
+            while (work.next(g)) {
                 const int keys = keys_of(args, g.s, g.run);
                 for (int b = g.b0; b < g.b1; ++b, ++block) {
                     wait_warp(bar(kVFull + block % 2), (block / 2) & 1, abort, args.limit);
@@ -377,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int steps = (c.dim + 31) / 32;
             const uint32_t is = instruction_e4m3(kTile, false), io = instruction<__half>((c.dim + 15) / 16 * 16, true);
             int block = 0, tiles = 0, n[2] = {0, 0}, q_full[2] = {0, 0};
-            for (; walk.next(g); ++tiles) {
+            for (; work.next(g); ++tiles) {
                 const int halves = rows_of(g) > kTile ? 2 : 1, blocks = g.b1 - g.b0;
                 for (int b = 0; b <= blocks; ++b) {
                     const int nv = block + b - 1, nk = block + b;
