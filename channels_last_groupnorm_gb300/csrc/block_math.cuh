@@ -59,6 +59,13 @@ __device__ __forceinline__ uint32_t e4m3_four(float a, float b, float c, float d
     return e4m3_pair(a, b) | e4m3_pair(c, d) << 16;
 }
 
+__device__ __forceinline__ uint32_t e4m3_pair_half(uint32_t half2)
+{
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(half2));
+    return r;
+}
+
 // The values of the two low bytes (exact).
 __device__ __forceinline__ uint32_t e4m3_half2(uint32_t pair)
 {

@@ -317,17 +317,20 @@ __device__ __forceinline__ void zero_tile_row(uint32_t tile, int r)
     for (int c = 0; c < 8; ++c) sts128(tile + static_cast<uint32_t>(r) * 128u + c * 16u, make_uint4(0u, 0u, 0u, 0u));
 }
 
-// Four channels of a query, scaled to 2^7 .. 2^8 for its largest, in PARTS e4m3 numbers
-// that add up to them.
+// Two channels of a query, scaled to 2^7 .. 2^8 for its largest, as PARTS pairs of e4m3
+// numbers that add up to them (by way of fp16, which holds either half format's bits).
 template <int PARTS>
-__device__ __forceinline__ void split_e4m3(float (&x)[4], uint32_t (&w)[PARTS])
+__device__ __forceinline__ void split_e4m3(float a, float b, uint32_t (&w)[PARTS])
 {
+    uint32_t h = Half2<__half>::pack(a, b);
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-        const uint32_t lo = e4m3_pair(x[0], x[1]), hi = e4m3_pair(x[2], x[3]);
-        w[p] = lo | hi << 16;
-        const float2 a = e4m3_values(lo), b = e4m3_values(hi);
-        x[0] -= a.x, x[1] -= a.y, x[2] -= b.x, x[3] -= b.y;
+        w[p] = e4m3_pair_half(h);
+        if (p + 1 < PARTS) {
+            const uint32_t near = e4m3_half2(w[p]);
+            const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&near));
+            h = *reinterpret_cast<const uint32_t *>(&d);
+        }
     }
 }
 

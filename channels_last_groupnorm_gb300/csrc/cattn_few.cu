@@ -94,14 +94,7 @@ __device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v)
     asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Two fp16 values as e4m3, and 16 times what that leaves of them (exact).
-__device__ __forceinline__ uint32_t e4m3_pair_half(uint32_t v)
-{
-    unsigned short r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
-    return r;
-}
-
+// 16 times what e4m3 leaves of two fp16 values (exact).
 __device__ __forceinline__ uint32_t sixteen_times_rest(uint32_t v, uint32_t near)
 {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&near));
@@ -309,14 +302,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
                 const int shift = most < INFINITY ? query_shift(most) : 0;
                 const float up = most < INFINITY ? power_of_two(shift) : NAN;
-                uint32_t w[PARTS];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] *= up;
-                split_e4m3<PARTS>(x, w);
+                uint32_t lo[PARTS], hi[PARTS];
+                split_e4m3<PARTS>(x[0] * up, x[1] * up, lo);
+                split_e4m3<PARTS>(x[2] * up, x[3] * up, hi);
                 const uint32_t at = base + lay.q + buffer * lay.operand + q * 128u + (((lane >> 2) ^ (q & 7u)) << 4) + (lane & 3u) * 4u;
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p)
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + p * N * 128u), "r"(w[p]) : "memory");
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + p * N * 128u), "r"(lo[p] | hi[p] << 16) : "memory");
                 if (lane == 0) rows[q].factor = power_of_two(-shift);
                 if (++h == g.first_head + args.heads) {
                     h = g.first_head;

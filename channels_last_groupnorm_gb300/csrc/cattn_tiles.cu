@@ -11,10 +11,13 @@
 //                      half-precision ones, so bf16 queries cost no more than before;
 //   P_t = 2^(S_t c + log2 v - m)   c the key's scale, v the value's, both one number for every 8
 //                      keys: v leaves the weights' sum again;
-//   O_t += P_t V       in fp16: a warp of its own widens the values, e4m3 is exact there.
+//   O_t += P_t V       in fp16: warps of their own widen the values, e4m3 is exact there.
 //                      (Splitting the weights would cost the softmax warps, which
 //                      bound this kernel, six operations more for every two.)
 // One CTA per SM, with an equal part of all blocks (cattn_common.cuh).
+// The softmax warps' instructions are what counts: pages of whole 32 tokens have a kernel of
+// their own with one pair of scales for 32 keys, and the widening is spread over the SM's
+// four schedulers (one warp for it all made the softmax warps beside it the last).
 #include <algorithm>
 
 #include "cattn_common.cuh"
@@ -23,13 +26,25 @@ namespace gn {
 namespace cattn {
 namespace {
 
-constexpr int kThreads = 384;    // warps: 0 loads, 1 MMA, 2 the MMA's waits, 3 widens values, 4-7 and 8-11 the halves' softmax
+constexpr int kThreads = 512;    // warps: 0 loads, 1 MMA, 2 the MMA's waits, 4-7 and 8-11 the halves' softmax, 12-15 widen values
 constexpr int kKeyStages = 3;    // at most
 constexpr int kSegments = 16;  // that are found at a time
 constexpr int kScales = 4;       // blocks whose scales are in shared memory
 constexpr float kLeastScale = 0x1p-100f;
 constexpr float kShift = 7.0f;   // fp16 weights, away from its subnormals (weight_shift of packed attention)
 constexpr uint32_t kWide = 2 * kHalfBytes;    // a tile of values in fp16
+
+// Registers: 512 threads are launched with 128 each; 256 x 192 + 256 x 64 is the same.
+__device__ __forceinline__ void softmax_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 192;"); }
+__device__ __forceinline__ void other_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+
+// The largest of three.
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 // kP: per half the weights of a block's first and last 64 keys; kWideFull: the values widened
 enum Bar { kQ = 0, kKFull = 2, kKEmpty = kKFull + kKeyStages, kVFull = kKEmpty + kKeyStages, kVEmpty = kVFull + 2,
@@ -62,57 +77,64 @@ __host__ __device__ constexpr Layout layout(int parts)
 // they are read and where they are written.
 __device__ __forceinline__ void widen(uint32_t from, uint32_t to, int dim, int rows)
 {
-    const int lane = threadIdx.x & 31, q0 = lane & 3, flip = lane & 4 ? 5 : 0, base = lane >> 3;
+    // (each warp 32 rows)
+    const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5 & 3) * 4, q0 = lane & 3, flip = lane & 4 ? 5 : 0, base = lane >> 3;
+    constexpr int kBatch = 4;       // loads that are under way together
     for (int part = 0; part * 64 < dim; ++part) {
         const int q = part * 4 + q0;
-#pragma unroll 4
-        for (int i = 0; i < kTile / 8; ++i) {
-            // rows 8 i + {0, 1, 2, 3} and, flipped, 8 i + {5, 4, 7, 6}
-            const int r = 8 * i + (base ^ flip);
-            const uint32_t key = r & 7u;
-            uint4 v = lds128(from + r * 128u + ((q ^ key) << 4));
-            if (r >= rows) v = make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t at = to + part * kHalfBytes + r * 128u;
+        uint4 v[kBatch];
+        // rows 8 i + {0, 1, 2, 3} and, flipped, 8 i + {5, 4, 7, 6}
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = 8 * (first + i) + (base ^ flip);
+            v[i] = lds128(from + r * 128u + ((q ^ (r & 7u)) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = 8 * (first + i) + (base ^ flip);
+            if (r >= rows) v[i] = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t key = r & 7u, at = to + part * kHalfBytes + r * 128u;
             sts128(at + (((2u * q0) ^ key) << 4),
-                   make_uint4(e4m3_half2(v.x), e4m3_half2(v.x >> 16), e4m3_half2(v.y), e4m3_half2(v.y >> 16)));
+                   make_uint4(e4m3_half2(v[i].x), e4m3_half2(v[i].x >> 16), e4m3_half2(v[i].y), e4m3_half2(v[i].y >> 16)));
             sts128(at + (((2u * q0 + 1u) ^ key) << 4),
-                   make_uint4(e4m3_half2(v.z), e4m3_half2(v.z >> 16), e4m3_half2(v.w), e4m3_half2(v.w >> 16)));
+                   make_uint4(e4m3_half2(v[i].z), e4m3_half2(v[i].z >> 16), e4m3_half2(v[i].w), e4m3_half2(v[i].w >> 16)));
         }
     }
 }
 
 // A row's query (none: zeros) as row r of PARTS tiles; returns what its products are to be
-// multiplied by.
+// multiplied by.  (Loops, with the query read twice: this runs once a tile, and as straight
+// code the fetching of its instructions took longer than a tile's first blocks.)
 template <typename T, int PARTS>
 __device__ __forceinline__ float split_query(const T *q, int dim, uint32_t tiles, int r)
 {
-    uint4 raw[16];
     constexpr uint32_t kInf = IsBf16<T>::value ? 0x7f80u : 0x7c00u;
-    uint32_t most2 = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        raw[i] = q && 8 * i < dim ? __ldg(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0u, 0u, 0u, 0u);
-        most2 = __vmaxu2(most2, __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
-                                         __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu)));
+    const uint4 *from = reinterpret_cast<const uint4 *>(q);
+    uint32_t most = 0;
+#pragma unroll 8
+    for (int i = 0; i < dim / 8; ++i) {
+        const uint4 v = q ? __ldg(from + i) : make_uint4(0u, 0u, 0u, 0u);
+        most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
     }
-    const uint32_t top = max(most2 & 0xffffu, most2 >> 16);
+    most = max(most & 0xffffu, most >> 16);
     // (infinities too: their products with keys of either sign are no numbers)
-    const bool number = top < kInf;
-    const int shift = number ? query_shift(Half2<T>::unpack(top).x) : 0;
+    const bool number = most < kInf;
+    const int shift = number ? query_shift(Half2<T>::unpack(most).x) : 0;
     const float up = number ? power_of_two(shift) : NAN;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) {
-        const uint32_t w[8] = {raw[2 * i].x, raw[2 * i].y, raw[2 * i].z, raw[2 * i].w,
-                               raw[2 * i + 1].x, raw[2 * i + 1].y, raw[2 * i + 1].z, raw[2 * i + 1].w};
-        uint32_t bytes[PARTS][4];
+        uint32_t bytes[PARTS][4] = {};
+        if (q && 16 * i < dim) {
+            const uint4 a = __ldg(from + 2 * i), b = __ldg(from + 2 * i + 1);
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 lo = Half2<T>::unpack(w[2 * e]), hi = Half2<T>::unpack(w[2 * e + 1]);
-            float x[4] = {lo.x * up, lo.y * up, hi.x * up, hi.y * up};
-            uint32_t b[PARTS];
-            split_e4m3<PARTS>(x, b);
+            for (int e = 0; e < 8; ++e) {
+                const float2 x = Half2<T>::unpack(w[e]);
+                uint32_t part[PARTS];
+                split_e4m3<PARTS>(x.x * up, x.y * up, part);
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p) bytes[p][e] = b[p];
+                for (int p = 0; p < PARTS; ++p) bytes[p][e / 2] |= part[p] << (e % 2 * 16);
+            }
         }
 #pragma unroll
         for (int p = 0; p < PARTS; ++p)
@@ -122,7 +144,7 @@ __device__ __forceinline__ float split_query(const T *q, int dim, uint32_t tiles
     return power_of_two(-shift);
 }
 
-template <typename T, int MODE>
+template <typename T, int MODE, int GROUP>
 __global__ void __launch_bounds__(kThreads, 1)
     cached_tiles_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                         const __grid_constant__ CattnArgs args)
@@ -140,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i < kQ + 2 || (i >= kP && i < kP + 4) ? 4 : 1);
+        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i < kQ + 2 || (i >= kP && i < kP + 4) || (i >= kWideFull && i < kWideFull + 2) || (i >= kVEmpty && i < kVEmpty + 2) ? 4 : 1);
         *abort = (*reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) ? 1 : 0;
         mbar_init_fence();
         prefetch_tensormap(&map_k);
@@ -166,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto rows_of = [&](const Segment &s) {
         return min(args.tokens, s.s.end - s.s.begin - s.run * args.tokens) * args.heads;
     };
-    if (warp >= 4) {
-        many_registers();
+    if (warp >= 4 && warp < 12) {
+        softmax_registers();
         // ---- softmax: one row per thread ----
         const int half = warp >= 8 ? 1 : 0, r = (warp & 3) * 32 + lane, row = half * kTile + r;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -210,11 +232,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float bent = 1.0f;
                 if (MODE) {
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const float f = by * scale[q].x;
+                    for (int q = 0; q < kTile / GROUP; ++q) {
+                        const float f = by * scale[q * (GROUP / 8)].x;
                         const uint64_t f2 = pack2(f, f);
 #pragma unroll
-                        for (int k = 8 * q; k < 8 * q + 8; k += 2) {
+                        for (int k = GROUP * q; k < GROUP * (q + 1); k += 2) {
                             const float2 v = unpack2(mul2(pack2(s[k], s[k + 1]), f2));
                             s[k] = v.x;
                             s[k + 1] = v.y;
@@ -226,20 +248,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // What a group's scores are multiplied by and what is added: a group of which the row
                 // sees nothing has weights of 0, whatever its scale is (it may be no number).
                 const auto factors = [&](int q, float &f, float &add, float &inv) {
-                    const float4 kv = scale[q];
-                    const bool any = j0 + 8 * q < end;
+                    const float4 kv = scale[q * (GROUP / 8)];
+                    const bool any = j0 + GROUP * q < end;
                     f = any && !MODE ? by * kv.x : bent;
                     add = any ? kv.y : -INFINITY;
                     inv = any ? kv.z : 0.f;
                 };
                 float mx = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    float f, add, inv, top = fmaxf(s[8 * q], s[8 * q + 1]);
+                for (int q = 0; q < kTile / GROUP; ++q) {
+                    float f, add, inv, top = s[GROUP * q], other = s[GROUP * q + 1];
                     factors(q, f, add, inv);
 #pragma unroll
-                    for (int k = 2; k < 8; ++k) top = fmaxf(top, s[8 * q + k]);
-                    mx = fmaxf(mx, fmaf(top, f, add));
+                    for (int k = 2; k < GROUP; k += 2) {
+                        if (k % 4) top = max3(top, s[GROUP * q + k], s[GROUP * q + k + 1]);
+                        else other = max3(other, s[GROUP * q + k], s[GROUP * q + k + 1]);
+                    }
+                    mx = fmaxf(mx, fmaf(fmaxf(top, other), f, add));
                 }
                 const bool grew = mx > m + (kShift + kRescaleLog2) || (b == g.b0 && mx > m);
                 if (__any_sync(0xffffffffu, grew)) {
@@ -256,21 +281,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int q = 0; q < 4; ++q) {
                     uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 32 / GROUP; ++e) {
                         float f, add, inv;
-                        factors(4 * q + e, f, add, inv);
+                        factors(q * (32 / GROUP) + e, f, add, inv);
                         add -= m_use;
                         const uint64_t c2 = pack2(f, f), m2 = pack2(add, add);
-                        uint64_t eight = 0;
+                        uint64_t some = 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int at = 32 * q + 8 * e + 2 * k;
+                        for (int k = 0; k < GROUP / 2; ++k) {
+                            const int at = 32 * q + GROUP * e + 2 * k;
                             const float2 x = unpack2(fma2(pack2(s[at], s[at + 1]), c2, m2));
                             const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-                            eight = k == 0 ? pack2(p0, p1) : add2(eight, pack2(p0, p1));
-                            pk[4 * e + k] = Half2<__half>::pack(p0, p1);
+                            some = k == 0 ? pack2(p0, p1) : add2(some, pack2(p0, p1));
+                            pk[GROUP / 2 * e + k] = Half2<__half>::pack(p0, p1);
                         }
-                        sum2 = fma2(eight, pack2(inv, inv), sum2);
+                        sum2 = fma2(some, pack2(inv, inv), sum2);
                     }
                     tmem_st16(ts + 16 * q, pk);
                     if (q == 1) {
@@ -331,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before_sync();
         }
     } else {
-        few_registers();
+        other_registers();
         if (warp == 0) {
             // ---- loads, and every 8 keys' scales by a lane of its own: asked for ahead of a
             // block's loads and stored behind them.  (Their slot was last read kScales blocks
@@ -378,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = max(0, value_tiles - 2); k < value_tiles; ++k)
                 tc::drain(bar(kVFull + k % 2), (k / 2) & 1, args.limit.timeout_ns);
             __syncwarp();
-        } else if (warp == 3) {
+        } else if (warp >= 12) {
             // ---- values to fp16 ----
             int block = 0;
             while (work.next(g)) {
@@ -395,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+        } else if (warp == 3) {
+            while (work.next(g)) {}
         } else {
             // ---- MMA: per block and half the weighted values of the block before, then
             // the scores of this one ----
@@ -475,15 +502,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <typename T, int MODE>
-cudaError_t launch(const CattnArgs &args, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s)
+template <typename T, int MODE, int GROUP>
+cudaError_t launch_group(const CattnArgs &args, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s)
 {
     constexpr uint32_t bytes = layout(IsBf16<T>::value ? 2 : 3).total;
     static_assert(bytes <= 227 * 1024, "a CTA's shared memory");
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(cached_tiles_kernel<T, MODE>), bytes, done);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(cached_tiles_kernel<T, MODE, GROUP>), bytes, done);
     if (e != cudaSuccess) return e;
-    return tc::launch_pdl(cached_tiles_kernel<T, MODE>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), bytes, s, mk, mv, args);
+    return tc::launch_pdl(cached_tiles_kernel<T, MODE, GROUP>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), bytes, s, mk, mv,
+                          args);
+}
+
+template <typename T, int MODE>
+cudaError_t launch(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s)
+{
+    return a.chunk >= 32 ? launch_group<T, MODE, 32>(a, mk, mv, ctas, s) : launch_group<T, MODE, 8>(a, mk, mv, ctas, s);
 }
 
 template <typename T>
