@@ -142,21 +142,42 @@ __device__ __forceinline__ Pieces pieces_of(int u, int pairs, bool halves)
     return {16 * u, 16 * u + 8};
 }
 
-template <typename T>
-__device__ __forceinline__ void turn_pieces(Eight<T> &x, Eight<T> &y, const float2 *angle, Pieces at, int pairs, bool halves)
-{
-    if (halves) {
-        if (at.a >= 2 * pairs || at.b != at.a + pairs) return;
+// A token's angles in shared memory: a lane takes eight pairs, two at a time, and lanes of
+// neighbouring eights lie side by side each time (pair by pair they would meet in the same banks,
+// 16 at once: 8555 tokens of 24 + 24 heads took 154 us instead of 84).
+struct Angles {
+    int eights;                   // of pairs, the last of which may be part empty
+    __host__ __device__ __forceinline__ explicit Angles(int pairs) : eights((pairs + 7) / 8) {}
+    __host__ __device__ __forceinline__ int row() const { return 8 * eights; }
+    __device__ __forceinline__ int at(int pair) const { return ((pair & 7) >> 1) * 2 * eights + (pair >> 3) * 2 + (pair & 1); }
+    // the eight pairs of lane unit u
+    __device__ __forceinline__ void get(const float2 *row, int u, float2 (&w)[8]) const
+    {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) turn_pair(x.f[e], y.f[e], angle[at.a + e]);
+        for (int j = 0; j < 4; ++j) {
+            const float4 v = *reinterpret_cast<const float4 *>(row + j * 2 * eights + 2 * u);
+            w[2 * j] = make_float2(v.x, v.y);
+            w[2 * j + 1] = make_float2(v.z, v.w);
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void turn_pieces(Eight<T> &x, Eight<T> &y, const float2 *row, int u, Pieces at, int pairs, bool halves)
+{
+    if (8 * u >= pairs) return;       // (with either pairing lane unit u has pairs 8 u .. 8 u + 7)
+    float2 w[8];
+    Angles(pairs).get(row, u, w);
+    if (halves) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) turn_pair(x.f[e], y.f[e], w[e]);
         return;
     }
-    if (at.a < 2 * pairs)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) turn_pair(x.f[2 * e], x.f[2 * e + 1], angle[at.a / 2 + e]);
+    for (int e = 0; e < 4; ++e) turn_pair(x.f[2 * e], x.f[2 * e + 1], w[e]);
     if (at.b < 2 * pairs)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) turn_pair(y.f[2 * e], y.f[2 * e + 1], angle[at.b / 2 + e]);
+        for (int e = 0; e < 4; ++e) turn_pair(y.f[2 * e], y.f[2 * e + 1], w[4 + e]);
 }
 
 __device__ __forceinline__ float warp_max(float v)
@@ -172,7 +193,7 @@ template <typename T, bool VEC>
 struct Head {
     const Append &p;
     const Unit &u;
-    const float2 *angle;          // [tokens][pairs]
+    const float2 *angle;          // [tokens][Angles::row()]
     int lane;
 
     // fn(token of the unit, where its two pieces are, the pieces turned) for each of the
@@ -192,7 +213,7 @@ struct Head {
                 Eight<T> x, y;
                 x.load(row + at.a);
                 y.load(row + at.b);
-                turn_pieces(x, y, angle + i * pairs, at, pairs, halves);
+                turn_pieces(x, y, angle + i * Angles(pairs).row(), w, at, pairs, halves);
                 fn(i, at, x, y);
             }
         } else {
@@ -204,7 +225,7 @@ struct Head {
                 Pieces at = {2 * k, 2 * k + 1};
                 if (halves && k < pairs) at = {k, pairs + k};
                 float x = to_float(row[at.a]), y = to_float(row[at.b]);
-                if (k < pairs) turn_pair(x, y, angle[i * pairs + k]);
+                if (k < pairs) turn_pair(x, y, angle[i * Angles(pairs).row() + Angles(pairs).at(k)]);
                 fn(i, at, x, y);
             }
         }
@@ -284,7 +305,7 @@ struct Head {
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Append p)
 {
-    extern __shared__ float2 angle[];
+    extern __shared__ __align__(16) float2 angle[];
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     const gn_cache &c = p.c;
@@ -312,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     u.page = cache::page_of(c, n, page0 + piece);
     for (int i = threadIdx.x; i < u.count * p.pairs; i += kThreads) {
         const int t = i / p.pairs, k = i - t * p.pairs;
-        angle[i] = angle_of(p, u.token + t, k);
+        angle[t * Angles(p.pairs).row() + Angles(p.pairs).at(k)] = angle_of(p, u.token + t, k);
     }
     __syncthreads();
     const Head<T, VEC> head = {p, u, angle, lane};
@@ -359,7 +380,7 @@ cudaError_t append(const Append &p, int sm_count, cudaStream_t s)
     const int heads = a.heads + 2 * c.kv_heads;
     const int64_t split = std::max<int64_t>(1, std::min<int64_t>((heads + kWarps - 1) / kWarps, 4 * sm_count / busy));
     const int most = static_cast<int>(std::min<int64_t>(c.page_size, c.cu ? a.tokens : each));
-    const size_t smem = sizeof(float2) * static_cast<size_t>(most) * static_cast<size_t>(p.pairs);
+    const size_t smem = sizeof(float2) * static_cast<size_t>(most) * static_cast<size_t>(Angles(p.pairs).row());
     const auto kernel = vec ? append_kernel<T, true> : append_kernel<T, false>;
     static std::atomic<uint64_t> done[2];
     // (pages of up to 256 tokens, 64 pairs: 128 KB)

@@ -15,7 +15,10 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
+#include <initializer_list>
+#include <utility>
 
 #include "block_internal.h"
 #include "block_math.cuh"
@@ -91,21 +94,29 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[EPV])
         *p = static_cast<uint8_t>(e4m3_pair(f[0], 0.f));
 }
 
-// The largest of a group's values (NaN if any is).
-__device__ __forceinline__ float row_max(float v, Group &gr)
+// A sum and a maximum (NaN if any value is) over a group, in one go.
+__device__ __forceinline__ void row_sum_max(float &sum, float &most, Group &gr)
 {
-    const int within = min(gr.tpr, 32) >> 1;
-    for (int o = within; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if (gr.tpr <= 32) return v;
+    for (int o = min(gr.tpr, 32) >> 1; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    if (gr.tpr <= 32) return;
     const int warp = gr.lane >> 5, lane = threadIdx.x & 31, warps = gr.tpr >> 5;
     float(*s)[2] = gr.scratch[gr.turn];
     gr.turn ^= 1;
-    if (lane == 0) s[warp][0] = v;
+    if (lane == 0) {
+        s[warp][0] = sum;
+        s[warp][1] = most;
+    }
     named_sync(1 + gr.g, gr.tpr);
-    v = lane < warps ? s[lane][0] : 0.f;
+    sum = lane < warps ? s[lane][0] : 0.f;
+    most = lane < warps ? s[lane][1] : 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+    for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
 }
 
 __device__ __forceinline__ Group group_of(int tpr, float (*scratch)[2][32][2])
@@ -121,47 +132,265 @@ __device__ __forceinline__ Group group_of(int tpr, float (*scratch)[2][32][2])
 
 constexpr int kMaxGroups = 8;      // of more than a warp in a CTA
 
-template <typename T, int EPV, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) rms_kernel(const __grid_constant__ RmsArgs a, int tpr)
+// The weight in fp32 in shared memory: as vectors whatever its format is, and no registers
+// held for it (two CTAs on an SM instead of one; 4608 x 6144 with residual, e4m3 out).
+__device__ __forceinline__ void stage_weight(float *to, const void *weight, int format, int cols)
+{
+    if (!weight) return;
+    const int bytes = format == GN_FORMAT_FP32 ? 4 : 2, wide = 16 / bytes;
+    if (cols % wide || reinterpret_cast<uintptr_t>(weight) % 16) {
+        for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+            float w[1];
+            load_params<1>(weight, format, c, w);
+            to[c] = w[0];
+        }
+        return;
+    }
+    for (int i = threadIdx.x; i < cols / wide; i += blockDim.x) {
+        const uint4 v = __ldg(static_cast<const uint4 *>(weight) + i);
+        if (format == GN_FORMAT_FP32) {
+            reinterpret_cast<uint4 *>(to)[i] = v;
+            continue;
+        }
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const float2 p = format == GN_FORMAT_BF16 ? Half2<__nv_bfloat16>::unpack(w[e]) : Half2<__half>::unpack(w[e]);
+            const float2 q = format == GN_FORMAT_BF16 ? Half2<__nv_bfloat16>::unpack(w[e + 1]) : Half2<__half>::unpack(w[e + 1]);
+            reinterpret_cast<float4 *>(to)[2 * i + e / 2] = make_float4(p.x, p.y, q.x, q.y);
+        }
+    }
+}
+
+// EPV of them, ones without a weight.
+template <int EPV>
+__device__ __forceinline__ void weight_at(const float *staged, bool there, int c, float (&w)[EPV])
+{
+    if (!there) {
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) w[e] = 1.0f;
+    } else if constexpr (EPV == 1) {
+        w[0] = staged[c];
+    } else {
+#pragma unroll
+        for (int e = 0; e < EPV; e += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(staged + c + e);
+            w[e] = v.x, w[e + 1] = v.y, w[e + 2] = v.z, w[e + 3] = v.w;
+        }
+    }
+}
+
+// A thread's slots of a row (zeros where there is none).
+template <typename T, int EPV, int NV>
+__device__ __forceinline__ void load_row(Slot<T, EPV> (&s)[NV], const void *p, const RowsAt &at, int64_t inner, int64_t rows,
+                                         int64_t n, const Group &gr, int cols)
+{
+    const T *row = p && n < rows ? static_cast<const T *>(p) + row_offset(at, inner, rows, n) : nullptr;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = (gr.lane + k * gr.tpr) * EPV;
+        if (row && c < cols)
+            s[k].load(row + c);
+        else
+            s[k].clear();
+    }
+}
+
+// Rows of up to 32 vectors (the heads of a projection): a group of lanes takes ROWS of them
+// at a time, so that enough is on its way (4608 x 24 rows of 128: 20 us with one, 12 with four).
+constexpr int kShortRows = 4;
+
+template <typename T, int EPV>
+__global__ void __launch_bounds__(256) rms_short_kernel(const __grid_constant__ RmsArgs a, int tpr)
+{
+    extern __shared__ __align__(16) float staged[];
+    tc::griddep_wait();
+    if (threadIdx.x == 0) tc::griddep_launch_dependents();
+    const int per = blockDim.x / tpr, group = threadIdx.x / tpr, lane = threadIdx.x - group * tpr, c = lane * EPV;
+    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    const bool in = c < a.cols;
+    stage_weight(staged, a.weight, a.weight_format, a.cols);
+    __syncthreads();
+    float w[EPV];
+    if (in) weight_at<EPV>(staged, a.weight != nullptr, c, w);
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * per * kShortRows; first < a.rows;
+         first += static_cast<int64_t>(gridDim.x) * per * kShortRows) {
+        Slot<T, EPV> t[kShortRows], r[kShortRows];
+        float sum[kShortRows], most[kShortRows];
+#pragma unroll
+        for (int q = 0; q < kShortRows; ++q) {
+            const int64_t n = first + group + q * per;
+            t[q].clear();
+            r[q].clear();
+            if (in && n < a.rows) {
+                t[q].load(static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, n) + c);
+                if (a.residual) r[q].load(static_cast<const T *>(a.residual) + row_offset(a.residual_at, a.inner, a.rows, n) + c);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kShortRows; ++q) {
+            const int64_t n = first + group + q * per;
+            float f[EPV], g[EPV];
+            t[q].get(f);
+            if (a.residual) {
+                r[q].get(g);
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) f[e] += g[e];
+                t[q].set(f);
+                if (in && n < a.rows) t[q].store(static_cast<T *>(a.total) + row_offset(a.total_at, a.inner, a.rows, n) + c);
+                t[q].get(f);
+            }
+            sum[q] = most[q] = 0.f;
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) sum[q] = fmaf(f[e], f[e], sum[q]);
+            if (a.scales && in)
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) most[q] = max_nan(most[q], fabsf(f[e] * w[e]));
+        }
+        for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int q = 0; q < kShortRows; ++q) {
+                sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], o);
+                if (a.scales) most[q] = max_nan(most[q], __shfl_xor_sync(0xffffffffu, most[q], o));
+            }
+#pragma unroll
+        for (int q = 0; q < kShortRows; ++q) {
+            const int64_t n = first + group + q * per;
+            if (!in || n >= a.rows) continue;
+            const float rstd = 1.0f / sqrtf(fmaf(sum[q], inv_cols, a.eps));
+            if (lane == 0 && a.rstd) a.rstd[n] = rstd;
+            float f[EPV];
+            t[q].get(f);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) f[e] = f[e] * rstd * w[e];
+            const int64_t at = row_offset(a.y_at, a.inner, a.rows, n) + c;
+            if (!a.scales) {
+                Slot<T, EPV> o;
+                o.set(f);
+                o.store(static_cast<T *>(a.y) + at);
+                continue;
+            }
+            const float top = most[q] * rstd;
+            const bool none = top < kLeastMagnitude;
+            const float by = none ? 0.f : 448.0f / top;
+            if (lane == 0) a.scales[n] = none ? 0.f : top / 448.0f;
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) f[e] *= by;
+            store_e4m3<EPV>(static_cast<uint8_t *>(a.y) + at, f);
+        }
+    }
+}
+
+template <typename T, int EPV>
+__global__ void __launch_bounds__(256) rms_short_grad_kernel(const __grid_constant__ RmsGradArgs a, int tpr)
+{
+    extern __shared__ __align__(16) float staged[];       // the weight, then [groups][cols] sums
+    tc::griddep_wait();
+    if (threadIdx.x == 0) tc::griddep_launch_dependents();
+    const int per = blockDim.x / tpr, group = threadIdx.x / tpr, lane = threadIdx.x - group * tpr, c = lane * EPV;
+    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    const bool in = c < a.cols;
+    stage_weight(staged, a.weight, a.weight_format, a.cols);
+    __syncthreads();
+    float w[EPV], dw[EPV] = {};
+    if (in) weight_at<EPV>(staged, a.weight != nullptr, c, w);
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * per * kShortRows; first < a.rows;
+         first += static_cast<int64_t>(gridDim.x) * per * kShortRows) {
+        Slot<T, EPV> t[kShortRows], dy[kShortRows], dt[kShortRows];
+        float sum[kShortRows], rstd[kShortRows];
+#pragma unroll
+        for (int q = 0; q < kShortRows; ++q) {
+            const int64_t n = first + group + q * per;
+            t[q].clear();
+            dy[q].clear();
+            dt[q].clear();
+            rstd[q] = 0.f;
+            if (in && n < a.rows) {
+                t[q].load(static_cast<const T *>(a.total) + row_offset(a.total_at, a.inner, a.rows, n) + c);
+                dy[q].load(static_cast<const T *>(a.dy) + row_offset(a.dy_at, a.inner, a.rows, n) + c);
+                if (a.dtotal) dt[q].load(static_cast<const T *>(a.dtotal) + row_offset(a.dtotal_at, a.inner, a.rows, n) + c);
+                rstd[q] = __ldg(a.rstd + n);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kShortRows; ++q) {
+            float f[EPV], g[EPV];
+            t[q].get(f);
+            dy[q].get(g);
+            sum[q] = 0.f;
+            if (in)
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) {
+                    dw[e] = fmaf(g[e], f[e] * rstd[q], dw[e]);
+                    sum[q] = fmaf(g[e] * w[e], f[e], sum[q]);
+                }
+        }
+        for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int q = 0; q < kShortRows; ++q) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], o);
+#pragma unroll
+        for (int q = 0; q < kShortRows; ++q) {
+            const int64_t n = first + group + q * per;
+            if (!in || n >= a.rows) continue;
+            const float along = sum[q] * inv_cols * rstd[q] * rstd[q];
+            float f[EPV], g[EPV], r[EPV];
+            t[q].get(f);
+            dy[q].get(g);
+            dt[q].get(r);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) f[e] = fmaf(rstd[q], fmaf(-f[e], along, g[e] * w[e]), r[e]);
+            Slot<T, EPV> o;
+            o.set(f);
+            o.store(static_cast<T *>(a.dx) + row_offset(a.dx_at, a.inner, a.rows, n) + c);
+        }
+    }
+    if (!a.weight) return;
+    float *columns = staged + (a.cols + 3) / 4 * 4;
+    if (in)
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) columns[group * a.cols + c + e] = dw[e];
+    __syncthreads();
+    float *out = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
+    for (int i = threadIdx.x; i < a.cols; i += blockDim.x) {
+        float v = 0.f;
+        for (int g = 0; g < per; ++g) v += columns[g * a.cols + i];
+        out[i] = v;
+    }
+}
+
+template <typename T, int EPV, int NV, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) rms_kernel(const __grid_constant__ RmsArgs a, int tpr)
 {
     __shared__ float scratch[kMaxGroups][2][32][2];
+    extern __shared__ __align__(16) float staged[];
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     Group gr = group_of(tpr, scratch);
     const int per = blockDim.x / tpr;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * per;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    const bool weighed = a.weight != nullptr;
+    int64_t first = static_cast<int64_t>(blockIdx.x) * per;
+    Slot<T, EPV> x[NV], r[NV];
+    load_row(x, a.x, a.x_at, a.inner, a.rows, first + gr.g, gr, a.cols);
+    if (a.residual) load_row(r, a.residual, a.residual_at, a.inner, a.rows, first + gr.g, gr, a.cols);
+    stage_weight(staged, a.weight, a.weight_format, a.cols);
+    __syncthreads();
     // (the rows of a CTA's groups end together: a warp's lanes shuffle as one)
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * per; first < a.rows; first += static_cast<int64_t>(gridDim.x) * per) {
+    for (; first < a.rows; first += step) {
         const int64_t n = first + gr.g;
         const bool live = n < a.rows;
         Slot<T, EPV> t[NV];
-        float sum[1] = {0.f};
-        const T *x = live ? static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, n) : nullptr;
+        float sum = 0.f, most = 0.f;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (gr.lane + k * tpr) * EPV;
-            if (live && c < a.cols)
-                t[k].load(x + c);
-            else
-                t[k].clear();
-        }
+        for (int k = 0; k < NV; ++k) t[k] = x[k];
         if (a.residual) {
-            Slot<T, EPV> r[NV];
-            const T *p = live ? static_cast<const T *>(a.residual) + row_offset(a.residual_at, a.inner, a.rows, n) : nullptr;
             T *to = live ? static_cast<T *>(a.total) + row_offset(a.total_at, a.inner, a.rows, n) : nullptr;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int c = (gr.lane + k * tpr) * EPV;
-                if (live && c < a.cols)
-                    r[k].load(p + c);
-                else
-                    r[k].clear();
-            }
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = (gr.lane + k * tpr) * EPV;
                 float f[EPV], g[EPV];
-                t[k].get(f);
+                x[k].get(f);
                 r[k].get(g);
 #pragma unroll
                 for (int e = 0; e < EPV; ++e) f[e] += g[e];
@@ -169,22 +398,32 @@ __global__ void __launch_bounds__(THREADS) rms_kernel(const __grid_constant__ Rm
                 if (live && c < a.cols) t[k].store(to + c);
             }
         }
+        // the next row is on its way while this one is worked on (in place, another
+        // row's elements are another's: nothing written here is read there)
+        load_row(x, a.x, a.x_at, a.inner, a.rows, n + step, gr, a.cols);
+        if (a.residual) load_row(r, a.residual, a.residual_at, a.inner, a.rows, n + step, gr, a.cols);
+        // the squares' sum, and the largest |t w| with it: |y| is that times rstd
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float f[EPV];
+            const int c = (gr.lane + k * tpr) * EPV;
+            float f[EPV], w[EPV];
             t[k].get(f);
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) sum[0] = fmaf(f[e], f[e], sum[0]);
+            for (int e = 0; e < EPV; ++e) sum = fmaf(f[e], f[e], sum);
+            if (!a.scales || c >= a.cols) continue;
+            weight_at<EPV>(staged, weighed, c, w);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) most = max_nan(most, fabsf(f[e] * w[e]));
         }
-        row_sum(sum, gr);
-        const float rstd = 1.0f / sqrtf(fmaf(sum[0], inv_cols, a.eps));
+        row_sum_max(sum, most, gr);
+        const float rstd = 1.0f / sqrtf(fmaf(sum, inv_cols, a.eps));
         if (live && gr.lane == 0 && a.rstd) a.rstd[n] = rstd;
         const auto value = [&](int k, int c, float (&f)[EPV]) {
-            t[k].get(f);
             float w[EPV];
-            if (a.weight) load_params<EPV>(a.weight, a.weight_format, c, w);
+            t[k].get(f);
+            weight_at<EPV>(staged, weighed, c, w);
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) f[e] = f[e] * rstd * (a.weight ? w[e] : 1.0f);
+            for (int e = 0; e < EPV; ++e) f[e] = f[e] * rstd * w[e];
         };
         if (!a.scales) {
             T *y = live ? static_cast<T *>(a.y) + row_offset(a.y_at, a.inner, a.rows, n) : nullptr;
@@ -200,17 +439,7 @@ __global__ void __launch_bounds__(THREADS) rms_kernel(const __grid_constant__ Rm
             }
             continue;
         }
-        float most = 0.f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (gr.lane + k * tpr) * EPV;
-            if (!live || c >= a.cols) continue;
-            float f[EPV];
-            value(k, c, f);
-#pragma unroll
-            for (int e = 0; e < EPV; ++e) most = max_nan(most, fabsf(f[e]));
-        }
-        most = row_max(most, gr);
+        most *= rstd;
         const bool none = most < kLeastMagnitude;
         const float by = none ? 0.f : 448.0f / most;
         if (live && gr.lane == 0) a.scales[n] = none ? 0.f : most / 448.0f;
@@ -228,77 +457,78 @@ __global__ void __launch_bounds__(THREADS) rms_kernel(const __grid_constant__ Rm
     }
 }
 
-template <typename T, int EPV, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) rms_grad_kernel(const __grid_constant__ RmsGradArgs a, int tpr)
+template <typename T, int EPV, int NV, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) rms_grad_kernel(const __grid_constant__ RmsGradArgs a, int tpr)
 {
     __shared__ float scratch[kMaxGroups][2][32][2];
-    extern __shared__ float columns[];       // [groups][cols] where a CTA has several
+    extern __shared__ __align__(16) float staged[];       // the weight, then [groups][cols] sums where a CTA has several
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     Group gr = group_of(tpr, scratch);
     const int per = blockDim.x / tpr;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * per;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    const bool weighed = a.weight != nullptr;
     float dw[NV][EPV] = {};
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * per; first < a.rows; first += static_cast<int64_t>(gridDim.x) * per) {
+    int64_t first = static_cast<int64_t>(blockIdx.x) * per;
+    Slot<T, EPV> t[NV], dy[NV], dt[NV];
+    const auto load = [&](int64_t n) {
+        load_row(t, a.total, a.total_at, a.inner, a.rows, n, gr, a.cols);
+        load_row(dy, a.dy, a.dy_at, a.inner, a.rows, n, gr, a.cols);
+        if (a.dtotal) load_row(dt, a.dtotal, a.dtotal_at, a.inner, a.rows, n, gr, a.cols);
+    };
+    load(first + gr.g);
+    float rstd_next = first + gr.g < a.rows ? __ldg(a.rstd + first + gr.g) : 0.f;
+    stage_weight(staged, a.weight, a.weight_format, a.cols);
+    __syncthreads();
+    for (; first < a.rows; first += step) {
         const int64_t n = first + gr.g;
         const bool live = n < a.rows;
-        Slot<T, EPV> t[NV], dy[NV], dt[NV];
-        const T *pt = live ? static_cast<const T *>(a.total) + row_offset(a.total_at, a.inner, a.rows, n) : nullptr;
-        const T *pd = live ? static_cast<const T *>(a.dy) + row_offset(a.dy_at, a.inner, a.rows, n) : nullptr;
-        const T *pr = live && a.dtotal ? static_cast<const T *>(a.dtotal) + row_offset(a.dtotal_at, a.inner, a.rows, n) : nullptr;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (gr.lane + k * tpr) * EPV;
-            t[k].clear();
-            dy[k].clear();
-            dt[k].clear();
-            if (live && c < a.cols) {
-                t[k].load(pt + c);
-                dy[k].load(pd + c);
-                if (pr) dt[k].load(pr + c);
-            }
-        }
-        const float rstd = live ? __ldg(a.rstd + n) : 0.f;
+        const float rstd = rstd_next;
         float sum[1] = {0.f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = (gr.lane + k * tpr) * EPV;
+            if (c >= a.cols) continue;
             float f[EPV], g[EPV], w[EPV];
             t[k].get(f);
             dy[k].get(g);
-            if (a.weight && c < a.cols) {
-                load_params<EPV>(a.weight, a.weight_format, c, w);
+            weight_at<EPV>(staged, weighed, c, w);
 #pragma unroll
-                for (int e = 0; e < EPV; ++e) {
-                    if (live) dw[k][e] = fmaf(g[e], f[e] * rstd, dw[k][e]);
-                    g[e] *= w[e];
-                }
+            for (int e = 0; e < EPV; ++e) {
+                if (weighed && live) dw[k][e] = fmaf(g[e], f[e] * rstd, dw[k][e]);
+                sum[0] = fmaf(g[e] * w[e], f[e], sum[0]);
             }
-#pragma unroll
-            for (int e = 0; e < EPV; ++e) sum[0] = fmaf(g[e], f[e], sum[0]);
         }
         row_sum(sum, gr);
-        // (the factors of t in this order: rstd^2 may leave fp32's range where the product does not)
         const float along = sum[0] * inv_cols * rstd * rstd;
+        Slot<T, EPV> o[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (gr.lane + k * tpr) * EPV;
+            if (c >= a.cols) continue;
+            float f[EPV], g[EPV], r[EPV], w[EPV];
+            t[k].get(f);
+            dy[k].get(g);
+            weight_at<EPV>(staged, weighed, c, w);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) r[e] = 0.f;
+            if (a.dtotal) dt[k].get(r);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) f[e] = fmaf(rstd, fmaf(-f[e], along, g[e] * w[e]), r[e]);
+            o[k].set(f);
+        }
+        // the next row is on its way while this one is written
+        load(n + step);
+        rstd_next = n + step < a.rows ? __ldg(a.rstd + n + step) : 0.f;
         T *dx = live ? static_cast<T *>(a.dx) + row_offset(a.dx_at, a.inner, a.rows, n) : nullptr;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = (gr.lane + k * tpr) * EPV;
-            if (!live || c >= a.cols) continue;
-            float f[EPV], g[EPV], r[EPV], w[EPV];
-            t[k].get(f);
-            dy[k].get(g);
-            dt[k].get(r);
-            if (a.weight) load_params<EPV>(a.weight, a.weight_format, c, w);
-#pragma unroll
-            for (int e = 0; e < EPV; ++e)
-                f[e] = fmaf(rstd, fmaf(-f[e], along, a.weight ? g[e] * w[e] : g[e]), r[e]);
-            Slot<T, EPV> o;
-            o.set(f);
-            o.store(dx + c);
+            if (live && c < a.cols) o[k].store(dx + c);
         }
     }
-    if (!a.weight) return;
+    if (!weighed) return;
     float *out = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
     if (per == 1) {
 #pragma unroll
@@ -310,6 +540,7 @@ __global__ void __launch_bounds__(THREADS) rms_grad_kernel(const __grid_constant
         }
         return;
     }
+    float *columns = staged + (a.cols + 3) / 4 * 4;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int c = (gr.lane + k * tpr) * EPV;
@@ -325,24 +556,24 @@ __global__ void __launch_bounds__(THREADS) rms_grad_kernel(const __grid_constant
     }
 }
 
-// dweight: the CTAs' rows of partial sums, 32 columns a CTA, 8 warps taking every
-// eighth row, and those eight sums in order.
-__global__ void __launch_bounds__(256) rms_columns_kernel(const __grid_constant__ RmsGradArgs a, int blocks)
+// dweight: the CTAs' rows of partial sums, 32 columns a CTA, 32 warps taking every 32nd
+// row, and those sums in order.  (8 warps took 10 us for 608 rows.)
+__global__ void __launch_bounds__(1024) rms_columns_kernel(const __grid_constant__ RmsGradArgs a, int blocks)
 {
-    __shared__ float part[8][33];
+    __shared__ float part[32][33];
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (c < a.cols)
-#pragma unroll 8
-        for (int b = warp; b < blocks; b += 8) v += a.partial[static_cast<int64_t>(b) * a.cols + c];
+#pragma unroll 10
+        for (int b = warp; b < blocks; b += 32) v += a.partial[static_cast<int64_t>(b) * a.cols + c];
     part[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && c < a.cols) {
         v = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) v += part[w][lane];
+        for (int w = 0; w < 32; ++w) v += part[w][lane];
         store_param(a.dweight, a.weight_format, c, v);
     }
 }
@@ -350,6 +581,7 @@ __global__ void __launch_bounds__(256) rms_columns_kernel(const __grid_constant_
 // Slots of a thread, threads of a row and of a CTA.
 struct Shape {
     int nv, tpr, threads;
+    int rows = 1;                 // of a group at a time
 };
 
 int row_threads(int slots, int nv)
@@ -363,14 +595,18 @@ int row_threads(int slots, int nv)
     return (need + 31) / 32 * 32;
 }
 
-Shape shape_of(int slots, bool vec)
+// (one slot a thread where the rows are few: 1 x 6144 11.4 us replayed, 15.5 with two;
+// where they are many two keep more rows on an SM: 4608 x 6144 58 us, 73 with one)
+Shape shape_of(int slots, bool vec, int64_t rows, int sm_count)
 {
     Shape s;
+    const int one = rows <= sm_count ? 1024 : 512;
     if (vec)
-        s.nv = slots <= 512 ? 1 : slots <= 1024 ? 2 : 4;
+        s.nv = slots <= one ? 1 : slots <= 1024 ? 2 : 4;
     else
         s.nv = slots <= 4096 ? 4 : 16;
     s.tpr = row_threads(slots, s.nv);
+    if (vec && s.tpr <= 32 && s.nv == 1 && rows > 256 / s.tpr * sm_count) s.rows = kShortRows;
     s.threads = s.tpr >= 256 ? s.tpr : s.tpr * std::max(1, 256 / s.tpr);
     return s;
 }
@@ -383,6 +619,22 @@ bool vectors(int cols, int epv, std::initializer_list<std::pair<const void *, co
     return true;
 }
 
+template <auto KERNEL, typename Args>
+cudaError_t run(const Args &a, const Shape &d, int64_t most, size_t smem, int sm_count, cudaStream_t s, int *blocks)
+{
+    // (weights of up to 16384 columns and the sums of a few groups: 64 KB and a few more)
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = smem > 40 * 1024 ? allow_shared(reinterpret_cast<const void *>(KERNEL), 96 * 1024, done) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    // as many CTAs as are on the SMs at once: each goes through several rows
+    const int64_t per = d.threads / d.tpr * d.rows, all = std::min((a.rows + per - 1) / per, most);
+    int fit = 1;
+    if (all > sm_count) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, KERNEL, d.threads, smem);
+    if (e != cudaSuccess) return e;
+    *blocks = static_cast<int>(std::min<int64_t>(all, static_cast<int64_t>(std::max(1, fit)) * sm_count));
+    return tc::launch_pdl(KERNEL, dim3(static_cast<unsigned>(*blocks)), dim3(d.threads), smem, s, a, d.tpr);
+}
+
 template <typename T>
 cudaError_t forward(const RmsArgs &a, int sm_count, cudaStream_t s)
 {
@@ -392,14 +644,16 @@ cudaError_t forward(const RmsArgs &a, int sm_count, cudaStream_t s)
     const bool vec = y_ok && vectors(a.cols, EPV, {{a.x, &a.x_at}, {a.residual, &a.residual_at}, {a.total, &a.total_at},
                                                    {a.scales ? nullptr : a.y, &a.y_at}}) &&
                      a.y_at.outer % EPV == 0 && a.y_at.stride % EPV == 0;
-    const Shape d = shape_of(vec ? a.cols / EPV : a.cols, vec);
-    const int64_t per = d.threads / d.tpr, fit = 2048 / d.threads;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((a.rows + per - 1) / per, fit * sm_count))), block(d.threads);
-    if (vec && d.nv == 1) return tc::launch_pdl(rms_kernel<T, EPV, 1, 512>, grid, block, 0, s, a, d.tpr);
-    if (vec && d.nv == 2) return tc::launch_pdl(rms_kernel<T, EPV, 2, 512>, grid, block, 0, s, a, d.tpr);
-    if (vec) return tc::launch_pdl(rms_kernel<T, EPV, 4, EPV == 8 ? 512 : 1024>, grid, block, 0, s, a, d.tpr);
-    if (d.nv == 4) return tc::launch_pdl(rms_kernel<T, 1, 4, 1024>, grid, block, 0, s, a, d.tpr);
-    return tc::launch_pdl(rms_kernel<T, 1, 16, 1024>, grid, block, 0, s, a, d.tpr);
+    const Shape d = shape_of(vec ? a.cols / EPV : a.cols, vec, a.rows, sm_count);
+    const size_t smem = a.weight ? 4u * static_cast<size_t>(a.cols) : 0;
+    int blocks;
+    if (d.rows > 1) return run<rms_short_kernel<T, EPV>>(a, d, INT32_MAX, smem, sm_count, s, &blocks);
+    if (vec && d.nv == 1) return run<rms_kernel<T, EPV, 1, 1024, 1>>(a, d, INT32_MAX, smem, sm_count, s, &blocks);
+    if (vec && d.nv == 2 && d.threads <= 384) return run<rms_kernel<T, EPV, 2, 384, 3>>(a, d, INT32_MAX, smem, sm_count, s, &blocks);
+    if (vec && d.nv == 2) return run<rms_kernel<T, EPV, 2, 512, 1>>(a, d, INT32_MAX, smem, sm_count, s, &blocks);
+    if (vec) return run<rms_kernel<T, EPV, 4, (EPV == 8 ? 512 : 1024), 1>>(a, d, INT32_MAX, smem, sm_count, s, &blocks);
+    if (d.nv == 4) return run<rms_kernel<T, 1, 4, 1024, 1>>(a, d, INT32_MAX, smem, sm_count, s, &blocks);
+    return run<rms_kernel<T, 1, 16, 1024, 1>>(a, d, INT32_MAX, smem, sm_count, s, &blocks);
 }
 
 template <typename T>
@@ -407,16 +661,17 @@ cudaError_t backward(const RmsGradArgs &a, int sm_count, cudaStream_t s, int *bl
 {
     constexpr int EPV = 16 / sizeof(T);
     const bool vec = vectors(a.cols, EPV, {{a.total, &a.total_at}, {a.dy, &a.dy_at}, {a.dtotal, &a.dtotal_at}, {a.dx, &a.dx_at}});
-    const Shape d = shape_of(vec ? a.cols / EPV : a.cols, vec);
-    const int64_t per = d.threads / d.tpr;
-    *blocks = static_cast<int>(std::min<int64_t>((a.rows + per - 1) / per, rms_norm_blocks(a.rows, sm_count)));
-    const dim3 grid(static_cast<unsigned>(*blocks)), block(d.threads);
-    const size_t smem = a.weight && per > 1 ? 4u * static_cast<size_t>(per) * static_cast<size_t>(a.cols) : 0;
-    if (vec && d.nv == 1) return tc::launch_pdl(rms_grad_kernel<T, EPV, 1, 512>, grid, block, smem, s, a, d.tpr);
-    if (vec && d.nv == 2) return tc::launch_pdl(rms_grad_kernel<T, EPV, 2, 512>, grid, block, smem, s, a, d.tpr);
-    if (vec) return tc::launch_pdl(rms_grad_kernel<T, EPV, 4, EPV == 8 ? 512 : 1024>, grid, block, smem, s, a, d.tpr);
-    if (d.nv == 4) return tc::launch_pdl(rms_grad_kernel<T, 1, 4, 1024>, grid, block, smem, s, a, d.tpr);
-    return tc::launch_pdl(rms_grad_kernel<T, 1, 16, 1024>, grid, block, smem, s, a, d.tpr);
+    const Shape d = shape_of(vec ? a.cols / EPV : a.cols, vec, a.rows, sm_count);
+    const size_t per = static_cast<size_t>(d.threads / d.tpr), cols = static_cast<size_t>(a.cols);
+    const size_t smem = a.weight ? 4u * ((cols + 3) / 4 * 4 + (per > 1 ? per * cols : 0)) : 0;
+    const int64_t most = rms_norm_blocks(a.rows, sm_count);
+    if (d.rows > 1) return run<rms_short_grad_kernel<T, EPV>>(a, d, most, smem, sm_count, s, blocks);
+    if (vec && d.nv == 1) return run<rms_grad_kernel<T, EPV, 1, 1024, 1>>(a, d, most, smem, sm_count, s, blocks);
+    if (vec && d.nv == 2 && d.threads <= 384) return run<rms_grad_kernel<T, EPV, 2, 384, 2>>(a, d, most, smem, sm_count, s, blocks);
+    if (vec && d.nv == 2) return run<rms_grad_kernel<T, EPV, 2, 512, 1>>(a, d, most, smem, sm_count, s, blocks);
+    if (vec) return run<rms_grad_kernel<T, EPV, 4, (EPV == 8 ? 512 : 1024), 1>>(a, d, most, smem, sm_count, s, blocks);
+    if (d.nv == 4) return run<rms_grad_kernel<T, 1, 4, 1024, 1>>(a, d, most, smem, sm_count, s, blocks);
+    return run<rms_grad_kernel<T, 1, 16, 1024, 1>>(a, d, most, smem, sm_count, s, blocks);
 }
 
 }  // namespace
@@ -443,7 +698,7 @@ cudaError_t launch_rms_norm_backward(const RmsGradArgs &a, int sm_count, cudaStr
     if (e != cudaSuccess) return e;
     *launches = 1;
     if (!a.weight) return e;
-    e = tc::launch_pdl(rms_columns_kernel, dim3((a.cols + 31) / 32), dim3(256), 0, s, a, blocks);
+    e = tc::launch_pdl(rms_columns_kernel, dim3((a.cols + 31) / 32), dim3(1024), 0, s, a, blocks);
     if (e == cudaSuccess) *launches = 2;
     return e;
 }
