@@ -8,10 +8,12 @@
 //   scale max(old, needed); where that is larger, what it holds is rounded again.
 //
 // A unit is what the call adds to one page: its tokens' angles are formed once, in
-// shared memory, for all heads, and each warp of the CTA (and of a few others where
-// there are few units) takes heads of q, k and v by turns.  A key or value head is
-// gone over twice, for the largest magnitude and for the bytes; the second time its
-// rows come from L1 or L2.
+// shared memory, for all heads, and teams of warps (of a few other CTAs too where there
+// are few units) take heads of q, k and v by turns.  A team is one warp for a few tokens,
+// up to the whole CTA for a large page: a head's tokens one after the other in one warp are a
+// chain of waits (8004 tokens in pages of 128: 66 us with single warps).  A key or value
+// head is gone over twice, for the largest magnitude and for the bytes; the second time
+// its rows come from L1 or L2.
 //
 // Bound by memory: q, k and v are read once, q and a byte per channel are written.
 // The angles are formed in turns with 64-bit whole numbers: position times the
@@ -27,6 +29,7 @@
 #include "block_internal.h"
 #include "block_math.cuh"
 #include "cache_common.cuh"
+#include "gn_ptx.cuh"
 #include "tc_common.cuh"
 
 namespace gn {
@@ -36,10 +39,9 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kLeastExponent = -100;
 
 // The turns of a pair at a position, in [-1/2, 1/2), in units of 2^-64.
-__device__ __forceinline__ bool turns_of(const Append &p, int64_t token, int pair, int64_t &turns)
+__device__ __forceinline__ bool turns_of(const Append &p, int64_t token, uint64_t unit, int axis, int64_t &turns)
 {
-    const int64_t at = token * p.a.axes + p.axis[pair];
-    const uint64_t unit = p.turns[pair];
+    const int64_t at = token * p.a.axes + axis;
     uint64_t whole;
     if (p.a.position_format == GN_POSITIONS_INT32) {
         whole = static_cast<uint64_t>(static_cast<int64_t>(static_cast<const int32_t *>(p.a.positions)[at])) * unit;
@@ -56,14 +58,14 @@ __device__ __forceinline__ bool turns_of(const Append &p, int64_t token, int pai
     return true;
 }
 
-// Cosine and sine: of the turns rounded to fp32, and to first order of what the
-// rounding left (which would cost as much precision as everything else together).
-__device__ __forceinline__ float2 angle_of(const Append &p, int64_t token, int pair)
+// Cosine and sine: of the turns' first 24 bits, which fp32 holds, and to first order of
+// the rest (which would cost as much precision as everything else together).
+__device__ __forceinline__ float2 angle_of(const Append &p, int64_t token, uint64_t unit, int axis)
 {
     int64_t turns;
-    if (!turns_of(p, token, pair, turns)) return make_float2(NAN, NAN);
-    const float near = static_cast<float>(turns >> 24) * 0x1p-40f;
-    const float left = static_cast<float>(turns - static_cast<int64_t>(near * 0x1p64f)) * (6.2831853f * 0x1p-64f);
+    if (!turns_of(p, token, unit, axis, turns)) return make_float2(NAN, NAN);
+    const float near = static_cast<float>(static_cast<int>(turns >> 40)) * 0x1p-24f;
+    const float left = static_cast<float>(static_cast<uint32_t>(turns >> 8)) * (6.2831853f * 0x1p-56f);
     float s, c;
     sincospif(2.0f * near, &s, &c);
     return make_float2(fmaf(-left, s, c), fmaf(left, c, s));
@@ -124,9 +126,8 @@ struct Eight {
 
 __device__ __forceinline__ void turn_pair(float &a, float &b, float2 w)
 {
-    // (no contraction: a key is the same whoever forms it)
-    const float x = __fsub_rn(__fmul_rn(a, w.x), __fmul_rn(b, w.y));
-    b = __fadd_rn(__fmul_rn(a, w.y), __fmul_rn(b, w.x));
+    const float x = fmaf(a, w.x, -(b * w.y));
+    b = fmaf(a, w.y, b * w.x);
     a = x;
 }
 
@@ -194,7 +195,9 @@ struct Head {
     const Append &p;
     const Unit &u;
     const float2 *angle;          // [tokens][Angles::row()]
-    int lane;
+    int lane, member, team;       // this warp among those that share the head
+    float (*tops)[kWarps];        // two rows of the CTA's, taken by turns
+    int turn = 0;
 
     // fn(token of the unit, where its two pieces are, the pieces turned) for each of the
     // head's rows from `in` on, lanes side by side
@@ -208,7 +211,7 @@ struct Head {
             const Pieces at = pieces_of(w, pairs, halves);
             if (n >= rows) return;
 #pragma unroll 4
-            for (int i = n; i < u.count; i += rows) {
+            for (int i = n + rows * member; i < u.count; i += rows * team) {
                 const T *row = in + (u.token + i) * stride;
                 Eight<T> x, y;
                 x.load(row + at.a);
@@ -219,7 +222,7 @@ struct Head {
         } else {
             // single channels: pairs first, then the rest two at a time
             const int half = dim / 2;
-            for (int n = lane; n < u.count * half; n += 32) {
+            for (int n = lane + 32 * member; n < u.count * half; n += 32 * team) {
                 const int i = n / half, k = n - i * half;
                 const T *row = in + (u.token + i) * stride;
                 Pieces at = {2 * k, 2 * k + 1};
@@ -245,27 +248,73 @@ struct Head {
         });
     }
 
+    // The largest magnitude of the head's rows as they are, from their bits: of numbers
+    // without a sign the larger has the larger bits, and NaN the largest.
+    __device__ __forceinline__ float largest(const T *in, int64_t stride) const
+    {
+        const int units = p.c.dim / 16, rows = 32 / units, n = lane / units, w = lane - n * units;
+        uint32_t most = 0;
+        if (n < rows)
+#pragma unroll 4
+            for (int i = n + rows * member; i < u.count; i += rows * team) {
+                const uint4 *at = reinterpret_cast<const uint4 *>(in + (u.token + i) * stride + 16 * w);
+#pragma unroll
+                for (int e = 0; e < static_cast<int>(sizeof(T)); ++e) {
+                    const uint4 v = __ldg(at + e);
+                    if (sizeof(T) == 2)
+                        most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+                    else
+                        most = max(most, max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu)));
+                }
+            }
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(most);
+        else
+            return Half2<T>::unpack(max(most & 0xffffu, most >> 16)).x;
+    }
+
+    // The largest of the team's values (NaN if any is); what the team has read before is read.
+    __device__ __forceinline__ float team_max(float v)
+    {
+        v = warp_max(v);
+        if (team == 1) {
+            __syncwarp();
+            return v;
+        }
+        const int first = (threadIdx.x >> 5) - member;
+        float *row = tops[turn];
+        turn ^= 1;
+        if (lane == 0) row[first + member] = v;
+        named_sync(1 + first, 32 * team);
+        v = row[first];
+        for (int i = 1; i < team; ++i) v = max_nan(v, row[first + i]);
+        return v;
+    }
+
     __device__ __forceinline__ void keep(const T *in, int64_t stride, bool turned, uint8_t *page, int64_t page_stride,
-                                         float *scale) const
+                                         float *scale)
     {
         if (u.page < 0) return;
         float most = 0.f;
-        each(in, stride, turned, [&](int, Pieces, const auto &x, const auto &y) {
+        if (VEC && !turned)
+            most = largest(in, stride);
+        else
+            each(in, stride, turned, [&](int, Pieces, const auto &x, const auto &y) {
             if constexpr (VEC) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) most = max_nan(most, max_nan(fabsf(x.f[e]), fabsf(y.f[e])));
+                for (int e = 0; e < 8; ++e) most = max_nan3(most, x.f[e], y.f[e]);
             } else {
-                most = max_nan(most, max_nan(fabsf(x), fabsf(y)));
+                most = max_nan3(most, x, y);
             }
         });
-        float now = scale_for(warp_max(most));
+        const float old = u.slot > 0 ? *scale : 0.f;
+        float now = scale_for(team_max(most));
         if (u.slot > 0) {
-            const float old = *scale;
             now = max_nan(old, now);
-            __syncwarp();                       // every lane has read the old scale
             if (now > old) {
                 const float by = old / now;
-                for (int n = lane; n < u.slot * (p.c.dim / 16); n += 32) {
+                for (int n = lane + 32 * member; n < u.slot * (p.c.dim / 16); n += 32 * team) {
                     const int i = n / (p.c.dim / 16), w = n - i * (p.c.dim / 16);
                     uint4 *at = reinterpret_cast<uint4 *>(page + i * page_stride + 16 * w);
                     const uint4 v = *at;
@@ -279,7 +328,7 @@ struct Head {
                 }
             }
         }
-        if (lane == 0) *scale = now;
+        if (lane == 0 && member == 0) *scale = now;
         const bool number = now == now;
         const float by = number ? 1.0f / now : 0.f;
         each(in, stride, turned, [&](int i, Pieces at, const auto &x, const auto &y) {
@@ -303,9 +352,12 @@ struct Head {
 };
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Append p)
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Append p, int team)
 {
     extern __shared__ __align__(16) float2 angle[];
+    __shared__ float tops[2][kWarps];
+    __shared__ uint64_t units[kRopeMaxPairs];
+    __shared__ unsigned char axes[kRopeMaxPairs];
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     const gn_cache &c = p.c;
@@ -331,15 +383,22 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     u.count = high - low;
     u.slot = low - (page0 + piece) * size;
     u.page = cache::page_of(c, n, page0 + piece);
-    for (int i = threadIdx.x; i < u.count * p.pairs; i += kThreads) {
-        const int t = i / p.pairs, k = i - t * p.pairs;
-        angle[t * Angles(p.pairs).row() + Angles(p.pairs).at(k)] = angle_of(p, u.token + t, k);
+    // (the pairs' turns by way of shared memory: parameters are read one address at a time)
+    for (int k = threadIdx.x; k < p.pairs; k += kThreads) {
+        units[k] = p.turns[k];
+        axes[k] = p.axis[k];
     }
     __syncthreads();
-    const Head<T, VEC> head = {p, u, angle, lane};
-    const int heads = a.heads + 2 * c.kv_heads;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < u.count * p.pairs; i += kThreads) {
+        const int t = i / p.pairs, k = i - t * p.pairs;
+        angle[t * Angles(p.pairs).row() + Angles(p.pairs).at(k)] = angle_of(p, u.token + t, units[k], axes[k]);
+    }
+    __syncthreads();
+    Head<T, VEC> head = {p, u, angle, lane, warp % team, team, tops};
+    const int heads = a.heads + 2 * c.kv_heads, teams = kWarps / team;
     // keys and values first: they take longer
-    for (int i = blockIdx.y * kWarps + warp; i < heads; i += gridDim.y * kWarps) {
+    for (int i = blockIdx.y * teams + warp / team; i < heads; i += gridDim.y * teams) {
         if (i < 2 * c.kv_heads) {
             const bool key = i < c.kv_heads;
             const int h = key ? i : i - c.kv_heads;
@@ -378,15 +437,22 @@ cudaError_t append(const Append &p, int sm_count, cudaStream_t s)
     // about the units that hold tokens; enough CTAs for every SM to have a few
     const int64_t busy = c.cu ? a.tokens / c.page_size + c.sequences : units;
     const int heads = a.heads + 2 * c.kv_heads;
-    const int64_t split = std::max<int64_t>(1, std::min<int64_t>((heads + kWarps - 1) / kWarps, 4 * sm_count / busy));
     const int most = static_cast<int>(std::min<int64_t>(c.page_size, c.cu ? a.tokens : each));
+    // Teams: until there are some 48 warps of work for an SM, with 8 tokens a warp at least
+    // (145 pages of 64 tokens, 72 heads: 83 us with single warps, 102 with four; 70 pages of 128
+    // tokens, 18 heads: 56 us with single warps, 36 with eight).
+    const int64_t tokens = std::min<int64_t>(most, a.tokens / c.sequences);
+    int team = 1;
+    while (team < kWarps && 16 * team <= tokens && busy * heads * team < 48 * sm_count) team *= 2;
+    const int teams = kWarps / team;
+    const int64_t split = std::max<int64_t>(1, std::min<int64_t>((heads + teams - 1) / teams, 3 * sm_count / busy));
     const size_t smem = sizeof(float2) * static_cast<size_t>(most) * static_cast<size_t>(Angles(p.pairs).row());
     const auto kernel = vec ? append_kernel<T, true> : append_kernel<T, false>;
     static std::atomic<uint64_t> done[2];
     // (pages of up to 256 tokens, 64 pairs: 128 KB)
-    cudaError_t e = smem > 48 * 1024 ? allow_shared(reinterpret_cast<const void *>(kernel), 128 * 1024, done[vec]) : cudaSuccess;
+    cudaError_t e = smem > 40 * 1024 ? allow_shared(reinterpret_cast<const void *>(kernel), 128 * 1024, done[vec]) : cudaSuccess;
     if (e != cudaSuccess) return e;
-    return tc::launch_pdl(kernel, dim3(static_cast<unsigned>(units), static_cast<unsigned>(split)), dim3(kThreads), smem, s, p);
+    return tc::launch_pdl(kernel, dim3(static_cast<unsigned>(units), static_cast<unsigned>(split)), dim3(kThreads), smem, s, p, team);
 }
 
 }  // namespace

@@ -84,6 +84,14 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+// The largest of three magnitudes, or NaN where any is.
+__device__ __forceinline__ float max_nan3(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return r;
+}
+
 // ---- two fp32 operations per instruction ------------------------------------------
 __device__ __forceinline__ uint64_t pack2(float a, float b)
 {
