@@ -30,7 +30,16 @@ struct CattnArgs {
     int rows;                     // room for rows in a tile's piece
     int chunk;                    // keys that one load brings: they lie in one page
     int extra;                    // blocks that a tile's start and end count as
+    struct Shared *shared;        // [CTAs]
     float *pieces;                // [CTAs][2][rows][2 + dim]: maxima, sums, outputs
+};
+
+// A tile that this CTA began and others go on with: how many pieces it is in (0: there is no
+// such tile; the first is this CTA's, the others those of the CTAs behind it) and where its
+// results go.
+struct __align__(32) Shared {
+    int pieces, token, rows, head, heads;     // rows with head < heads of the tile's are real
+    int pad[3];
 };
 
 // A CTA's piece: slot 0 of a tile that it did not begin, slot 1 of one that it did.
@@ -65,7 +74,7 @@ __device__ __forceinline__ int sequence_count(const CattnArgs &a) { return a.p.c
 // (Units of work: a tile's first `extra` are its start and end, the others its blocks.)
 struct Walk {
     const CattnArgs &a;
-    int64_t left, per_head;
+    int64_t left, per_head, at, tile_end;    // units to go; among all: the next one, and the current tile's end
     int seq, head, run, unit, runs;
     Sequence s;
 
@@ -84,9 +93,10 @@ struct Walk {
     __device__ __forceinline__ int64_t units() const { return per_head * heads(); }
 
     // begins `offset` units into sequence n
-    __device__ __forceinline__ void start(int n, int64_t offset, int64_t count)
+    __device__ __forceinline__ void start(int n, int64_t offset, int64_t count, int64_t first)
     {
         left = count;
+        at = first;
         if (count <= 0) return;
         load(n);
 #pragma unroll 1
@@ -113,6 +123,8 @@ struct Walk {
             const int all = a.extra + g.total, take = static_cast<int>(left < all - unit ? left : all - unit);
             g.b0 = max(unit - a.extra, 0);
             g.b1 = max(unit + take - a.extra, 0);
+            tile_end = at + all - unit;
+            at += take;
             left -= take;
             unit = 0;
             if (left > 0 && ++run == runs) {
@@ -132,8 +144,8 @@ struct Walk {
     }
 };
 
-// This CTA's part of the work: `count` units from unit `first` of `all`.  Its first unit
-// (its last, if that is what was asked for) lies `offset` into sequence `seq`.
+// This CTA's part of the work: `count` units from unit `first` of `all`, which lies
+// `offset` into sequence `seq`.
 struct Part {
     int64_t offset, count, first, all;
     int seq, ctas;                // the CTAs that have work
@@ -168,7 +180,7 @@ struct DealRoom {
 };
 
 // For the whole CTA (whole warps).
-__device__ __forceinline__ Part deal(const CattnArgs &a, DealRoom &room, int ctas, bool want_last = false)
+__device__ __forceinline__ Part deal(const CattnArgs &a, DealRoom &room, int ctas)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int count = sequence_count(a), each = (count + blockDim.x - 1) / blockDim.x;
@@ -199,15 +211,14 @@ __device__ __forceinline__ Part deal(const CattnArgs &a, DealRoom &room, int cta
     const int busy = static_cast<int>(all < ctas ? (all > 0 ? all : 1) : ctas);
     if (static_cast<int>(blockIdx.x) < busy && all > 0) {
         const int64_t u0 = part_begin(all, busy, blockIdx.x), u1 = part_begin(all, busy, blockIdx.x + 1);
-        const int64_t at = want_last ? u1 - 1 : u0;
-        if (u0 < u1 && at >= before && at < before + own) {
+        if (u0 < u1 && u0 >= before && u0 < before + own) {
             int n = n0;
 #pragma unroll 1
-            for (w.load(n); before + w.units() <= at && n + 1 < n1; w.load(n)) {
+            for (w.load(n); before + w.units() <= u0 && n + 1 < n1; w.load(n)) {
                 before += w.units();
                 ++n;
             }
-            room.part = {at - before, u1 - u0, u0, all, n, busy};
+            room.part = {u0 - before, u1 - u0, u0, all, n, busy};
         }
     }
     __syncthreads();
@@ -254,15 +265,29 @@ struct Reader {
     }
 };
 
+// (the loader's, which also says which tile of this CTA's is to be joined)
 template <int K>
-__device__ __forceinline__ void fill_work(WorkList<K> &w, Walk &walk)
+__device__ __forceinline__ void fill_work(WorkList<K> &w, Walk &walk, const Part &part)
 {
     if ((threadIdx.x & 31) == 0) {
+        const CattnArgs &a = walk.a;
         int n = 0;
+        Shared s = {};
 #pragma unroll 1
-        while (n < K && walk.next(w.list[n])) ++n;
+        for (; n < K && walk.next(w.list[n]); ++n) {
+            const Segment &g = w.list[n];
+            if (g.b0 != 0 || g.b1 == g.total) continue;
+            const int first_token = g.run * a.tokens;
+            s.pieces = part_of(part.all, part.ctas, walk.tile_end - 1) + 1 - static_cast<int>(blockIdx.x);
+            s.token = g.s.begin + first_token;
+            s.rows = min(a.tokens, g.s.end - g.s.begin - first_token) * a.heads;
+            s.head = g.hk * a.p.group + g.first_head;
+            s.heads = a.p.group - g.first_head;
+        }
         w.count = n;
         w.more = n == K;
+        // (such a tile is the last of all)
+        if (s.pieces || !w.more) a.shared[blockIdx.x] = s;
     }
     __syncwarp();
 }

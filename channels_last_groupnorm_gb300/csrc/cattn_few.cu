@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         int n = 0, block = 0;         // tiles so far (keys and values by turns), blocks so far
         bool go = true;
         Walk walk(args);
-        walk.start(part.seq, part.offset, skip ? 0 : part.count);
-        while (work.next(g, [&](WorkList<kSegments> &w) { fill_work(w, walk); })) {
+        walk.start(part.seq, part.offset, skip ? 0 : part.count, part.first);
+        while (work.next(g, [&](WorkList<kSegments> &w) { fill_work(w, walk, part); })) {
             if (!go) continue;
             const int keys = keys_of(args, g.s, g.run);
             int key = g.b0 * kTile + lane * args.chunk;

@@ -9,52 +9,42 @@ namespace cattn {
 namespace {
 
 // Joins the pieces of the tiles that several CTAs shared.  Block (c, y) looks after the
-// tile that begins in the c-th part of the work and ends behind it, and there after some of its rows, a warp each: the pieces' maxima and sums on the lanes first,
-// then their outputs, four channels a lane, whose loads wait for nothing.
+// tile that CTA c began, if others went on with it, and there after some of its rows, a
+// warp each: the pieces' maxima and sums on the lanes first, then their outputs, four
+// channels a lane, whose loads wait for nothing.
 constexpr int kJoinThreads = 256;
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ CattnArgs args)
 {
-    __shared__ DealRoom room;
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     const gn_cache &c = args.p.c;
     const gn_attn_cached_args &a = args.p.a;
-    const Part part = deal(args, room, gridDim.x, true);
-    if (part.count == 0 || *reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) return;
-    // the tile in which this part ends: of units from `begin` on, blocks from `blocks` on
-    Walk walk(args);
-    walk.start(part.seq, part.offset, 1);
-    const Sequence s = walk.s;
-    const int64_t begin = part.first + part.count - 1 - walk.unit, blocks = begin + args.extra;
-    const int64_t end = blocks + blocks_of(args, s, walk.run);
-    if (begin < part.first || end <= part.first + part.count) return;
-    const int hk = walk.head / args.chunks, first_head = (walk.head - hk * args.chunks) * args.heads;
-    // the parts that have blocks of it: the first left its piece in slot 1, the others in slot 0
-    const int from = part_of(part.all, part.ctas, blocks), pieces = part_of(part.all, part.ctas, end - 1) + 1 - from;
-    if (pieces == 1) return;              // it wrote the outputs itself
-    const int first_token = walk.run * args.tokens, live = min(args.tokens, s.end - s.begin - first_token) * args.heads;
+    const Shared s = args.shared[blockIdx.x];
+    if (s.pieces <= 1 || *reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) return;
     const int lane = threadIdx.x & 31;
-    const auto piece = [&](int p) { return piece_of(args, from + p, p == 0 ? 1 : 0); };
-    for (int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); row < live; row += gridDim.y * (kJoinThreads / 32)) {
-        const int h = first_head + row % args.heads;
-        if (h >= args.p.group) continue;
+    const float *first = piece_of(args, blockIdx.x, 1), *others = piece_of(args, blockIdx.x, 0);
+    const int64_t step = 2 * static_cast<int64_t>(args.rows) * (2 + c.dim);
+    const auto piece = [&](int p) { return p == 0 ? first : others + p * step; };
+    for (int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); row < s.rows; row += gridDim.y * (kJoinThreads / 32)) {
+        const int i = row / args.heads, h = row - i * args.heads;
+        if (h >= s.heads) continue;
         float top = -INFINITY, sum = 0.f;
-        for (int p = lane; p < pieces; p += 32) top = fmaxf(top, piece(p)[row]);
+        for (int p = lane; p < s.pieces; p += 32) top = fmaxf(top, piece(p)[row]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = 0; p0 < pieces; p0 += 32) {
+        for (int p0 = 0; p0 < s.pieces; p0 += 32) {
             float f = 0.f;
-            if (p0 + lane < pieces) {
+            if (p0 + lane < s.pieces) {
                 const float l = piece(p0 + lane)[args.rows + row];
                 // (a part that saw nothing has a sum of zero)
                 f = l == 0.f ? 0.f : ex2_approx(piece(p0 + lane)[row] - top);
                 sum = fmaf(f, l, sum);
             }
-            const int count = min(32, pieces - p0);
-#pragma unroll 4
+            const int count = min(32, s.pieces - p0);
+#pragma unroll 8
             for (int p = 0; p < count; ++p) {
                 const float g = __shfl_sync(0xffffffffu, f, p);
                 if (4 * lane < c.dim)
@@ -63,7 +53,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         }
         sum = warp_sum(sum);
         const float by = sum == 0.f ? 0.f : 1.0f / sum;
-        const int64_t token = s.begin + first_token + row / args.heads, head = hk * args.p.group + h;
+        const int64_t token = s.token + i, head = s.head + h;
         store4<T>(a.out, (token * a.heads + head) * c.dim, lane, c.dim, make_float4(out.x * by, out.y * by, out.z * by, out.w * by));
         if (lane == 0) a.lse[head * a.tokens + token] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
@@ -115,15 +105,22 @@ CattnArgs plan(const CachedAttn &p, bool *few)
 cudaError_t launch_join(const CattnArgs &a, int ctas, cudaStream_t s)
 {
     return tc::launch_pdl(a.p.a.format == GN_FORMAT_BF16 ? join_kernel<__nv_bfloat16> : join_kernel<__half>,
-                          dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(std::min(a.rows / 8, 8))), dim3(kJoinThreads), 0, s, a);
+                          dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(std::min(a.rows / 8, 16))), dim3(kJoinThreads), 0, s, a);
 }
 
 }  // namespace cattn
 
+namespace {
+
+// The CTAs' words about tiles that are to be joined, ahead of the pieces.
+size_t shared_bytes(int sm_count) { return (2u * static_cast<size_t>(sm_count) * sizeof(cattn::Shared) + 255) / 256 * 256; }
+
+}  // namespace
+
 // (the few rows of two CTAs an SM, or the many of one)
 size_t cached_attn_workspace_bytes(int64_t, int, int, int, int dim, int sm_count)
 {
-    return 4u * 2u * static_cast<size_t>(sm_count) * cattn::kManyRows * static_cast<size_t>(2 + dim);
+    return shared_bytes(sm_count) + 4u * 2u * static_cast<size_t>(sm_count) * cattn::kManyRows * static_cast<size_t>(2 + dim);
 }
 
 cudaError_t launch_cached_attn(const CachedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s, int *launches)
@@ -131,7 +128,8 @@ cudaError_t launch_cached_attn(const CachedAttn &p, int sm_count, const WaitLimi
     bool few;
     cattn::CattnArgs a = cattn::plan(p, &few);
     a.limit = limit;
-    a.pieces = static_cast<float *>(p.workspace);
+    a.shared = static_cast<cattn::Shared *>(p.workspace);
+    a.pieces = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + shared_bytes(sm_count));
     const gn_cache &c = p.c;
     CUtensorMap mk, mv;
     if (!cattn::encode_pool(&mk, c.k_pages, c, c.k_page, c.k_token, c.k_head, a.chunk) ||

@@ -365,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int block = 0, key_tiles = 0, value_tiles = 0;
             bool go = true;
             Walk walk(args);
-            walk.start(part.seq, part.offset, skip ? 0 : part.count);
-            while (work.next(g, [&](WorkList<kSegments> &w) { fill_work(w, walk); })) {
+            walk.start(part.seq, part.offset, skip ? 0 : part.count, part.first);
+            while (work.next(g, [&](WorkList<kSegments> &w) { fill_work(w, walk, part); })) {
                 if (!go) continue;
                 const int keys = keys_of(args, g.s, g.run);
                 int key = g.b0 * kTile + lane * 8;
