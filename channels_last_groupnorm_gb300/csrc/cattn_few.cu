@@ -51,8 +51,29 @@ struct __align__(16) Row {
 };
 
 struct Layout {
-    uint32_t q, weights, operand, ring, rows, tops, scales, bars, words, deal, work, total;
+    uint32_t q, operand, weights, weights_bytes, ring, rows, tops, scales, bars, words, deal, work, total;
 };
+
+// Weights lie as the threads have them, a key's next to each other ([128 keys][parts][n],
+// MN-major, swizzled over as many bytes as a row has): whole vectors are stored, where
+// [rows][keys] would take a byte at a time (96 of them a thread with 32 rows in three parts).
+__host__ __device__ constexpr uint32_t weight_row(int n, int parts)
+{
+    return n * parts <= 32 ? 32u : n * parts <= 64 ? 64u : 128u;
+}
+
+// Descriptor of the weights as the B operand: 8 keys after 8 keys (stride offset); the
+// swizzle mode is 2 for 128 bytes, 4 for 64, 6 for 32.
+template <uint32_t ROW>
+__device__ __forceinline__ uint64_t weights_desc(uint32_t smem)
+{
+    uint64_t d = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(1u) << 16;
+    d |= static_cast<uint64_t>((8u * ROW) >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(ROW == 128 ? 2u : ROW == 64 ? 4u : 6u) << 61;
+    return d;
+}
 
 __host__ __device__ constexpr Layout layout(int n, int parts, int stages)
 {
@@ -61,7 +82,8 @@ __host__ __device__ constexpr Layout layout(int n, int parts, int stages)
     l.operand = operand;
     l.q = 0;                                                        // two of each: this tile's and the next one's,
     l.weights = 2 * operand;                                        // this block's and the next one's
-    l.ring = 4 * operand;
+    l.weights_bytes = kTile * weight_row(n, parts);
+    l.ring = l.weights + 2 * l.weights_bytes;
     l.rows = l.ring + static_cast<uint32_t>(stages) * kTileBytes;   // 2 x n Row
     l.tops = l.rows + 2 * static_cast<uint32_t>(n) * sizeof(Row);   // 4 x n maxima or sums of a warp
     l.scales = l.tops + 16u * static_cast<uint32_t>(n);             // kScales x 16 chunks
@@ -88,11 +110,6 @@ __device__ __forceinline__ int ordered(float v)
     return i >= 0 ? i : i ^ 0x7fffffff;
 }
 __device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
-
-__device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v)
-{
-    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
 
 // 16 times what e4m3 leaves of two fp16 values (exact).
 __device__ __forceinline__ uint32_t sixteen_times_rest(uint32_t v, uint32_t near)
@@ -122,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 {
     constexpr int PARTS = IsBf16<T>::value ? 2 : 3, STAGES = stages_of(N, PARTS);
     constexpr Layout lay = layout(N, PARTS, STAGES);
+    constexpr uint32_t kRow = weight_row(N, PARTS);
     extern __shared__ __align__(1024) uint8_t gbase[];
     const uint32_t base = smem_addr(gbase);
     const gn_cache &c = args.p.c;
@@ -207,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else if (warp == 1 || warp == 2) {
         const bool waits = warp == 2;
         const int steps = (c.dim + 31) / 32;
-        const uint32_t is = instruction_e4m3(N, false), io = instruction_e4m3(PARTS * N, true);
+        const uint32_t is = instruction_e4m3(N, false), io = instruction_e4m3(PARTS * N, true) | 1u << 16;
         const auto loaded = [&](int n) { wait_warp(bar(kFull + n % STAGES), (n / STAGES) & 1, abort, args.limit); };
         const auto scores = [&](int n, int q) {       // block n's with query buffer q, into buffer n & 1
             if (elect_one()) {
@@ -251,10 +269,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (!waits) {
                     tc_fence_after_sync();
                     const uint64_t dv = sw128_mnmajor_desc(stage(2 * n + 1));
-                    const uint64_t dw = sw128_kmajor_desc(base + lay.weights + (n & 1) * lay.operand);
+                    const uint64_t dw = weights_desc<kRow>(base + lay.weights + (n & 1) * lay.weights_bytes);
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) umma_e4m3(t_o, dv + k * (4096u >> 4), dw + 2 * k, io, b > g.b0 || k > 0);
+                        for (int k = 0; k < 4; ++k) umma_e4m3(t_o, dv + k * (4096u >> 4), dw + k * (32u * kRow >> 4), io, b > g.b0 || k > 0);
                     }
                     __syncwarp();
                     commit(bar(kEmpty + (2 * n + 1) % STAGES));
@@ -288,31 +306,44 @@ __global__ void __launch_bounds__(kThreads, 2)
                 rows[lane] = row;
             }
             __syncwarp();
+            // (eight rows on their way together)
             int h = g.first_head;
             int64_t token = g.s.begin + first_token;
-#pragma unroll 2
-            for (int q = 0; q < live; ++q) {
-                const bool there = h < args.p.group && 4 * lane < c.dim;
-                const float4 f = there ? load4<T>(a.q, token * a.q_token + (g.hk * args.p.group + h) * a.q_head, lane, c.dim)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-                float x[4] = {f.x, f.y, f.z, f.w}, most = 0.f;
+#pragma unroll 1
+            for (int q0 = 0; q0 < live; q0 += 8) {
+                float4 f[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) most = max_nan(most, fabsf(x[e]));
+                for (int e = 0; e < 8; ++e) {
+                    const bool there = q0 + e < live && h < args.p.group && 4 * lane < c.dim;
+                    f[e] = there ? load4<T>(a.q, token * a.q_token + (g.hk * args.p.group + h) * a.q_head, lane, c.dim)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (++h == g.first_head + args.heads) {
+                        h = g.first_head;
+                        ++token;
+                    }
+                }
+                float most[8];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-                const int shift = most < INFINITY ? query_shift(most) : 0;
-                const float up = most < INFINITY ? power_of_two(shift) : NAN;
-                uint32_t lo[PARTS], hi[PARTS];
-                split_e4m3<PARTS>(x[0] * up, x[1] * up, lo);
-                split_e4m3<PARTS>(x[2] * up, x[3] * up, hi);
-                const uint32_t at = base + lay.q + buffer * lay.operand + q * 128u + (((lane >> 2) ^ (q & 7u)) << 4) + (lane & 3u) * 4u;
+                for (int e = 0; e < 8; ++e) most[e] = max_nan3(max_nan(fabsf(f[e].x), fabsf(f[e].y)), f[e].z, f[e].w);
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p)
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + p * N * 128u), "r"(lo[p] | hi[p] << 16) : "memory");
-                if (lane == 0) rows[q].factor = power_of_two(-shift);
-                if (++h == g.first_head + args.heads) {
-                    h = g.first_head;
-                    ++token;
+                for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) most[e] = max_nan(most[e], __shfl_xor_sync(0xffffffffu, most[e], o));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int q = q0 + e;
+                    if (q >= live) break;
+                    // (infinities too: their products with keys of either sign are no numbers)
+                    const int shift = most[e] < INFINITY ? query_shift(most[e]) : 0;
+                    const float up = most[e] < INFINITY ? power_of_two(shift) : NAN;
+                    uint32_t lo[PARTS], hi[PARTS];
+                    split_e4m3<PARTS>(f[e].x * up, f[e].y * up, lo);
+                    split_e4m3<PARTS>(f[e].z * up, f[e].w * up, hi);
+                    const uint32_t at = base + lay.q + buffer * lay.operand + q * 128u + (((lane >> 2) ^ (q & 7u)) << 4) + (lane & 3u) * 4u;
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + p * N * 128u), "r"(lo[p] | hi[p] << 16) : "memory");
+                    if (lane == 0) rows[q].factor = power_of_two(-shift);
                 }
             }
             fence_proxy_async_smem();
@@ -322,9 +353,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else if (warp >= 4) {
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int r = (warp & 3) * 32 + lane;
-        // this thread's key within the block: its place in the weights' rows
-        const uint32_t place = base + lay.weights + static_cast<uint32_t>(r & 15);
-        const uint32_t piece = static_cast<uint32_t>(r >> 4);
+        // this thread's key within the block: its row of weights, and what its 16-byte pieces'
+        // numbers are swizzled with
+        const uint32_t place = base + lay.weights + static_cast<uint32_t>(r) * kRow;
+        const uint32_t flip = kRow == 128 ? r & 7u : kRow == 64 ? r >> 1 & 3u : r >> 2 & 1u;
         const int my_chunk = r / args.chunk;
         int n = 0;
         for (int segment = 0; work.next(g); ++segment) {
@@ -412,7 +444,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 // the weights' buffer is free once the products of two blocks ago are done
                 if (n >= 2) wait_warp(bar(kO + (n & 1)), ((n - 2) >> 1) & 1, abort, args.limit);
-                const uint32_t to = place + (n & 1) * lay.operand;
+                const uint32_t to = place + (n & 1) * lay.weights_bytes;
+                uint32_t packed[PARTS][N / 4] = {};
 #pragma unroll
                 for (int i = 0; i < N; i += 4) {
                     if (i >= live) break;
@@ -429,15 +462,22 @@ __global__ void __launch_bounds__(kThreads, 2)
                     uint32_t h[2] = {Half2<__half>::pack(p[0], p[1]), Half2<__half>::pack(p[2], p[3])};
 #pragma unroll
                     for (int q = 0; q < PARTS; ++q) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t w = e4m3_pair_half(h[e]), row = q * N + i + 2 * e, bits = (i + 2 * e) & 7u;
-                            sts_u8(to + row * 128u + ((piece ^ bits) << 4), w);
-                            sts_u8(to + (row + 1) * 128u + ((piece ^ (bits + 1)) << 4), w >> 8);
-                            if (q + 1 < PARTS) h[e] = sixteen_times_rest(h[e], e4m3_half2(w));
+                        const uint32_t lo = e4m3_pair_half(h[0]), hi = e4m3_pair_half(h[1]);
+                        packed[q][i / 4] = lo | hi << 16;
+                        if (q + 1 < PARTS) {
+                            h[0] = sixteen_times_rest(h[0], e4m3_half2(lo));
+                            h[1] = sixteen_times_rest(h[1], e4m3_half2(hi));
                         }
                     }
                 }
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                    for (int i = 0; i < N; i += 16) {
+                        if (i >= live) break;
+                        sts128(to + ((static_cast<uint32_t>(q * N + i) / 16u ^ flip) << 4),
+                               make_uint4(packed[q][i / 4], packed[q][i / 4 + 1], packed[q][i / 4 + 2], packed[q][i / 4 + 3]));
+                    }
                 if (first + kTile > keys) {
                     // what lies behind the sequence has weight 0, but 0 x NaN is not 0
                     const int nv = 2 * n + 1;
