@@ -31,9 +31,11 @@ constexpr int kThreads = 256;   // warps: 0 loads, 1 MMA, 2 the MMA's waits, 3 t
 constexpr int kSegments = 32;  // that are found at a time
 constexpr int kScales = 4;      // blocks whose scales are in shared memory
 constexpr int kMaxStages = 6;
-// Weights: the row's largest at 2^6 when the maximum moves, which it does once a score
-// is 2^2 above it: below 448 = 2^8.8, and as far as can be from e4m3's smallest step.
-constexpr float kShift = 6.0f, kRescale = 2.0f;
+// Weights: the row's largest at 2^4 when the maximum moves, which it does once a score
+// is 2^4 above it: below 448 = 2^8.8, and weights of 2^-10 of the largest still have all
+// their bits.  (With 2^6 and 2^2 it moved more often: four tokens each over 7 caches, 32 rows,
+// 54 us replayed.)
+constexpr float kShift = 4.0f, kRescale = 4.0f;
 constexpr float kLeastScale = 0x1p-100f;
 
 enum Bar { kQ = 0, kQFree = 2, kFull = kQFree + 2, kEmpty = kFull + kMaxStages, kS = kEmpty + kMaxStages, kP = kS + 2, kO = kP + 2,
@@ -140,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int PARTS = IsBf16<T>::value ? 2 : 3, STAGES = stages_of(N, PARTS);
     constexpr Layout lay = layout(N, PARTS, STAGES);
     constexpr uint32_t kRow = weight_row(N, PARTS);
+    constexpr int SIDE = N == 32 ? 8 : 4;      // rows that are worked on side by side
     extern __shared__ __align__(1024) uint8_t gbase[];
     const uint32_t base = smem_addr(gbase);
     const gn_cache &c = args.p.c;
@@ -306,22 +309,29 @@ __global__ void __launch_bounds__(kThreads, 2)
                 rows[lane] = row;
             }
             __syncwarp();
-            // (eight rows on their way together)
+            // (eight rows on their way together, and the next eight while these are split)
             int h = g.first_head;
             int64_t token = g.s.begin + first_token;
-#pragma unroll 1
-            for (int q0 = 0; q0 < live; q0 += 8) {
-                float4 f[8];
+            float4 ahead[8];
+            const auto load_rows = [&](int q0) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const bool there = q0 + e < live && h < args.p.group && 4 * lane < c.dim;
-                    f[e] = there ? load4<T>(a.q, token * a.q_token + (g.hk * args.p.group + h) * a.q_head, lane, c.dim)
-                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                    ahead[e] = there ? load4<T>(a.q, token * a.q_token + (g.hk * args.p.group + h) * a.q_head, lane, c.dim)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
                     if (++h == g.first_head + args.heads) {
                         h = g.first_head;
                         ++token;
                     }
                 }
+            };
+            load_rows(0);
+#pragma unroll 1
+            for (int q0 = 0; q0 < live; q0 += 8) {
+                float4 f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = ahead[e];
+                if (q0 + 8 < live) load_rows(q0 + 8);
                 float most[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) most[e] = max_nan3(max_nan(fabsf(f[e].x), fabsf(f[e].y)), f[e].z, f[e].w);
@@ -379,20 +389,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                 float s[N];
                 tmem_ld_cols<N>(t_s + (n & 1) * N + lanes, s);
                 bool grew = b == g.b0;
-                // (four rows at a time: the tile may have fewer, what the others hold goes
-                // nowhere, and the four run side by side)
+                // (some rows at a time: the tile may have fewer, what the others hold goes
+                // nowhere, and they run side by side)
 #pragma unroll
-                for (int i = 0; i < N; i += 4) {
+                for (int i = 0; i < N; i += SIDE) {
                     if (i >= live) break;
-                    float4 row[4];
-                    int end[4];
+                    float4 row[SIDE];
+                    int end[SIDE];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < SIDE; ++e) {
                         row[e] = *reinterpret_cast<const float4 *>(&rows[i + e]);
                         if (masked) end[e] = rows[i + e].end;
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < SIDE; ++e) {
                         float t = s[i + e] * (ks * row[e].x);
                         if (MODE & kCap) t = tanh_fast(t) * (a.cap * kLog2e);
                         if (MODE & kBias) t = fmaf(-row[e].z, fabsf(row[e].w - static_cast<float>(j)), t);
@@ -447,11 +457,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint32_t to = place + (n & 1) * lay.weights_bytes;
                 uint32_t packed[PARTS][N / 4] = {};
 #pragma unroll
-                for (int i = 0; i < N; i += 4) {
+                for (int i = 0; i < N; i += SIDE) {
                     if (i >= live) break;
-                    float p[4];
+                    float p[SIDE];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < SIDE; ++e) {
                         const float top = rows[i + e].top;
                         // (0 x inv_vs would not be 0 if an unseen key's scale is no number)
                         const bool seen = s[i + e] != -INFINITY;
@@ -459,16 +469,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                         l[i + e] = seen ? fmaf(p[e], inv_vs, l[i + e]) : l[i + e];
                     }
                     // in fp16, whose 11 bits the parts hold
-                    uint32_t h[2] = {Half2<__half>::pack(p[0], p[1]), Half2<__half>::pack(p[2], p[3])};
+                    uint32_t h[SIDE / 2];
 #pragma unroll
-                    for (int q = 0; q < PARTS; ++q) {
-                        const uint32_t lo = e4m3_pair_half(h[0]), hi = e4m3_pair_half(h[1]);
-                        packed[q][i / 4] = lo | hi << 16;
-                        if (q + 1 < PARTS) {
-                            h[0] = sixteen_times_rest(h[0], e4m3_half2(lo));
-                            h[1] = sixteen_times_rest(h[1], e4m3_half2(hi));
+                    for (int e = 0; e < SIDE / 2; ++e) h[e] = Half2<__half>::pack(p[2 * e], p[2 * e + 1]);
+#pragma unroll
+                    for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                        for (int e = 0; e < SIDE / 2; e += 2) {
+                            const uint32_t lo = e4m3_pair_half(h[e]), hi = e4m3_pair_half(h[e + 1]);
+                            packed[q][(i + 2 * e) / 4] = lo | hi << 16;
+                            if (q + 1 < PARTS) {
+                                h[e] = sixteen_times_rest(h[e], e4m3_half2(lo));
+                                h[e + 1] = sixteen_times_rest(h[e + 1], e4m3_half2(hi));
+                            }
                         }
-                    }
                 }
 #pragma unroll
                 for (int q = 0; q < PARTS; ++q)

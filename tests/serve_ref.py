@@ -144,7 +144,7 @@ def attention(q, cache, cu, causal=True, slopes=None, cap=0.0, scale=None):
         ends.append(ends[-1] + n)
     r = br.attention(q, k, v, cu, ends, causal=causal, slopes=slopes, cap=cap, scale=scale)
     # The query's split drops less than 2^-17 of its largest channel from a channel;
-    # the weights' drops less than 2^-19 of the largest weight from a weight, and keeps
+    # the weights' drops at most 2^-18 of the largest weight from a weight, and keeps
     # 2^-9 of each (which the half format's step covers in bf16, and 2^-11 in fp16).
     heads, group = q.shape[1], q.shape[1] // k.shape[1]
     scale = q.shape[2] ** -0.5 if scale is None else scale
