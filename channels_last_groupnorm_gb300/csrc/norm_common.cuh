@@ -65,6 +65,20 @@ __device__ __forceinline__ int64_t row_offset(const RowsAt &at, int64_t inner, i
     return a * at.outer + (n - a * inner) * at.stride;
 }
 
+// The same in two steps, for several tensors of a row: the division is most of it.
+struct Place {
+    int64_t a, b;
+};
+
+__device__ __forceinline__ Place row_place(int64_t inner, int64_t rows, int64_t n)
+{
+    if (inner >= rows) return {0, n};
+    const uint32_t a = static_cast<uint32_t>(n) / static_cast<uint32_t>(inner);
+    return {a, static_cast<int64_t>(static_cast<uint32_t>(n) - a * static_cast<uint32_t>(inner))};
+}
+
+__device__ __forceinline__ int64_t offset_at(const RowsAt &at, const Place &p) { return p.a * at.outer + p.b * at.stride; }
+
 // The threads of one row: tpr of them (a power of two up to 32, or whole
 // warps), group g of the CTA's.
 struct Group {

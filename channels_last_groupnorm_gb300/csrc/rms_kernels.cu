@@ -196,9 +196,11 @@ __device__ __forceinline__ void load_row(Slot<T, EPV> (&s)[NV], const void *p, c
     }
 }
 
-// Rows of up to 32 vectors (the heads of a projection): a group of lanes takes ROWS of them
-// at a time, so that enough is on its way (4608 x 24 rows of 128: 20 us with one, 12 with four).
-constexpr int kShortRows = 4;
+// Rows of up to 32 vectors (the heads of a projection): a group of lanes takes some of them
+// at a time, so that enough is on its way, and looks up once where a row lies in all tensors
+// (4608 x 24 rows of 128, a training step replayed: 42 us with two rows, 49 with four, 58 with
+// eight, whose registers leave too few CTAs).
+constexpr int kShortRows = 2;
 
 template <typename T, int EPV>
 __global__ void __launch_bounds__(256) rms_short_kernel(const __grid_constant__ RmsArgs a, int tpr)
@@ -217,14 +219,16 @@ __global__ void __launch_bounds__(256) rms_short_kernel(const __grid_constant__ 
          first += static_cast<int64_t>(gridDim.x) * per * kShortRows) {
         Slot<T, EPV> t[kShortRows], r[kShortRows];
         float sum[kShortRows], most[kShortRows];
+        Place at[kShortRows];
 #pragma unroll
         for (int q = 0; q < kShortRows; ++q) {
             const int64_t n = first + group + q * per;
             t[q].clear();
             r[q].clear();
+            at[q] = row_place(a.inner, a.rows, n);
             if (in && n < a.rows) {
-                t[q].load(static_cast<const T *>(a.x) + row_offset(a.x_at, a.inner, a.rows, n) + c);
-                if (a.residual) r[q].load(static_cast<const T *>(a.residual) + row_offset(a.residual_at, a.inner, a.rows, n) + c);
+                t[q].load(static_cast<const T *>(a.x) + offset_at(a.x_at, at[q]) + c);
+                if (a.residual) r[q].load(static_cast<const T *>(a.residual) + offset_at(a.residual_at, at[q]) + c);
             }
         }
 #pragma unroll
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(256) rms_short_kernel(const __grid_constant__ 
 #pragma unroll
                 for (int e = 0; e < EPV; ++e) f[e] += g[e];
                 t[q].set(f);
-                if (in && n < a.rows) t[q].store(static_cast<T *>(a.total) + row_offset(a.total_at, a.inner, a.rows, n) + c);
+                if (in && n < a.rows) t[q].store(static_cast<T *>(a.total) + offset_at(a.total_at, at[q]) + c);
                 t[q].get(f);
             }
             sum[q] = most[q] = 0.f;
@@ -263,11 +267,11 @@ __global__ void __launch_bounds__(256) rms_short_kernel(const __grid_constant__ 
             t[q].get(f);
 #pragma unroll
             for (int e = 0; e < EPV; ++e) f[e] = f[e] * rstd * w[e];
-            const int64_t at = row_offset(a.y_at, a.inner, a.rows, n) + c;
+            const int64_t to = offset_at(a.y_at, at[q]) + c;
             if (!a.scales) {
                 Slot<T, EPV> o;
                 o.set(f);
-                o.store(static_cast<T *>(a.y) + at);
+                o.store(static_cast<T *>(a.y) + to);
                 continue;
             }
             const float top = most[q] * rstd;
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(256) rms_short_kernel(const __grid_constant__ 
             if (lane == 0) a.scales[n] = none ? 0.f : top / 448.0f;
 #pragma unroll
             for (int e = 0; e < EPV; ++e) f[e] *= by;
-            store_e4m3<EPV>(static_cast<uint8_t *>(a.y) + at, f);
+            store_e4m3<EPV>(static_cast<uint8_t *>(a.y) + to, f);
         }
     }
 }
@@ -298,6 +302,7 @@ __global__ void __launch_bounds__(256) rms_short_grad_kernel(const __grid_consta
          first += static_cast<int64_t>(gridDim.x) * per * kShortRows) {
         Slot<T, EPV> t[kShortRows], dy[kShortRows], dt[kShortRows];
         float sum[kShortRows], rstd[kShortRows];
+        Place at[kShortRows];
 #pragma unroll
         for (int q = 0; q < kShortRows; ++q) {
             const int64_t n = first + group + q * per;
@@ -305,10 +310,11 @@ __global__ void __launch_bounds__(256) rms_short_grad_kernel(const __grid_consta
             dy[q].clear();
             dt[q].clear();
             rstd[q] = 0.f;
+            at[q] = row_place(a.inner, a.rows, n);
             if (in && n < a.rows) {
-                t[q].load(static_cast<const T *>(a.total) + row_offset(a.total_at, a.inner, a.rows, n) + c);
-                dy[q].load(static_cast<const T *>(a.dy) + row_offset(a.dy_at, a.inner, a.rows, n) + c);
-                if (a.dtotal) dt[q].load(static_cast<const T *>(a.dtotal) + row_offset(a.dtotal_at, a.inner, a.rows, n) + c);
+                t[q].load(static_cast<const T *>(a.total) + offset_at(a.total_at, at[q]) + c);
+                dy[q].load(static_cast<const T *>(a.dy) + offset_at(a.dy_at, at[q]) + c);
+                if (a.dtotal) dt[q].load(static_cast<const T *>(a.dtotal) + offset_at(a.dtotal_at, at[q]) + c);
                 rstd[q] = __ldg(a.rstd + n);
             }
         }
@@ -341,7 +347,7 @@ __global__ void __launch_bounds__(256) rms_short_grad_kernel(const __grid_consta
             for (int e = 0; e < EPV; ++e) f[e] = fmaf(rstd[q], fmaf(-f[e], along, g[e] * w[e]), r[e]);
             Slot<T, EPV> o;
             o.set(f);
-            o.store(static_cast<T *>(a.dx) + row_offset(a.dx_at, a.inner, a.rows, n) + c);
+            o.store(static_cast<T *>(a.dx) + offset_at(a.dx_at, at[q]) + c);
         }
     }
     if (!a.weight) return;
