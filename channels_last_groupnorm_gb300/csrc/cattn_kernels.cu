@@ -9,52 +9,78 @@ namespace cattn {
 namespace {
 
 // Joins the pieces of the tiles that several CTAs shared.  Block (c, y) looks after the
-// tile that CTA c began, if others went on with it, and there after some of its rows, a
-// warp each: the pieces' maxima and sums on the lanes first, then their outputs, four
-// channels a lane, whose loads wait for nothing.
-constexpr int kJoinThreads = 256;
+// tile that CTA c began, if others went on with it, and there after some of its rows: a
+// warp each, or with many pieces all warps, each with some of the pieces (one token at 131072,
+// 38 pieces of a tile: 26 us with a warp for a row).  Four channels a lane; every load of a
+// row's outputs is on its way before the first is used.
+constexpr int kJoinWarps = 8, kJoinMany = 8;
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ CattnArgs args)
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ CattnArgs args)
 {
+    __shared__ float4 sums[kJoinWarps][32];
+    __shared__ float weights[kJoinWarps];
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     const gn_cache &c = args.p.c;
     const gn_attn_cached_args &a = args.p.a;
     const Shared s = args.shared[blockIdx.x];
     if (s.pieces <= 1 || *reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) return;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool many = s.pieces > kJoinMany;
     const float *first = piece_of(args, blockIdx.x, 1), *others = piece_of(args, blockIdx.x, 0);
     const int64_t step = 2 * static_cast<int64_t>(args.rows) * (2 + c.dim);
     const auto piece = [&](int p) { return p == 0 ? first : others + p * step; };
-    for (int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); row < s.rows; row += gridDim.y * (kJoinThreads / 32)) {
+    const int at = min(4 * lane, c.dim - 4);       // (lanes past the width read what another does)
+    const int row0 = many ? blockIdx.y : blockIdx.y * kJoinWarps + warp, rows = many ? gridDim.y : gridDim.y * kJoinWarps;
+    for (int row = row0; row < s.rows; row += rows) {
         const int i = row / args.heads, h = row - i * args.heads;
-        if (h >= s.heads) continue;
+        const bool there = h < s.heads;            // (the same for all who share the row)
         float top = -INFINITY, sum = 0.f;
         for (int p = lane; p < s.pieces; p += 32) top = fmaxf(top, piece(p)[row]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = 0; p0 < s.pieces; p0 += 32) {
-            float f = 0.f;
-            if (p0 + lane < s.pieces) {
-                const float l = piece(p0 + lane)[args.rows + row];
-                // (a part that saw nothing has a sum of zero)
-                f = l == 0.f ? 0.f : ex2_approx(piece(p0 + lane)[row] - top);
-                sum = fmaf(f, l, sum);
+        const int p0 = many ? warp : 0, by = many ? kJoinWarps : 1;
+        for (int q = p0; q < s.pieces; q += 8 * by) {
+            float4 v[8];
+            float f[8], l[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int p = min(q + e * by, s.pieces - 1);
+                f[e] = piece(p)[row];
+                l[e] = q + e * by < s.pieces ? piece(p)[args.rows + row] : 0.f;
+                v[e] = *reinterpret_cast<const float4 *>(piece(p) + 2 * args.rows + row * c.dim + at);
             }
-            const int count = min(32, s.pieces - p0);
-#pragma unroll 8
-            for (int p = 0; p < count; ++p) {
-                const float g = __shfl_sync(0xffffffffu, f, p);
-                if (4 * lane < c.dim)
-                    axpy4(out, g, *reinterpret_cast<const float4 *>(piece(p0 + p) + 2 * args.rows + row * c.dim + 4 * lane));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                // (a part that saw nothing has a sum of zero)
+                if (l[e] == 0.f) continue;
+                const float g = ex2_approx(f[e] - top);
+                sum = fmaf(g, l[e], sum);
+                axpy4(out, g, v[e]);
             }
         }
-        sum = warp_sum(sum);
-        const float by = sum == 0.f ? 0.f : 1.0f / sum;
+        if (many) {
+            sums[warp][lane] = out;
+            if (lane == 0) weights[warp] = sum;
+            __syncthreads();
+            if (warp == 0) {
+                sum = 0.f;
+                out = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kJoinWarps; ++w) {
+                    sum += weights[w];
+                    axpy4(out, 1.0f, sums[w][lane]);
+                }
+            }
+            __syncthreads();
+            if (warp != 0) continue;
+        }
+        if (!there) continue;
+        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
         const int64_t token = s.token + i, head = s.head + h;
-        store4<T>(a.out, (token * a.heads + head) * c.dim, lane, c.dim, make_float4(out.x * by, out.y * by, out.z * by, out.w * by));
+        store4<T>(a.out, (token * a.heads + head) * c.dim, lane, c.dim, make_float4(out.x * inv, out.y * inv, out.z * inv, out.w * inv));
         if (lane == 0) a.lse[head * a.tokens + token] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
 }
@@ -105,7 +131,7 @@ CattnArgs plan(const CachedAttn &p, bool *few)
 cudaError_t launch_join(const CattnArgs &a, int ctas, cudaStream_t s)
 {
     return tc::launch_pdl(a.p.a.format == GN_FORMAT_BF16 ? join_kernel<__nv_bfloat16> : join_kernel<__half>,
-                          dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(std::min(a.rows / 8, 16))), dim3(kJoinThreads), 0, s, a);
+                          dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(std::min(a.rows, 16))), dim3(32 * kJoinWarps), 0, s, a);
 }
 
 }  // namespace cattn
