@@ -9,11 +9,11 @@
 namespace gn {
 namespace cache {
 
-// Sequence n of the call: its packed tokens [begin, end) and the cache's tokens,
-// clamped.  With `cu`, n = -1 and n = sequences are the tokens ahead of the first
+// Sequence n of the call: its packed tokens [begin, end), its length, by which its tokens
+// have their places, and how much of it the table has room for.  With `cu`, n = -1 and n = sequences are the tokens ahead of the first
 // sequence and behind the last: they have no cache (length 0).
 struct Sequence {
-    int begin, end, length;
+    int begin, end, length, held;
     __device__ __forceinline__ int first_place() const { return length - (end - begin); }
 };
 
@@ -30,8 +30,8 @@ __device__ __forceinline__ Sequence sequence_of(const gn_cache &c, int64_t token
         s.begin = n * each;
         s.end = s.begin + each;
     }
-    const int most = static_cast<int>(c.table_width) * c.page_size;
-    s.length = real ? min(max(__ldg(c.lengths + n), 0), most) : 0;
+    s.length = real ? min(max(__ldg(c.lengths + n), 0), 1 << 30) : 0;
+    s.held = min(s.length, static_cast<int>(c.table_width) * c.page_size);
     return s;
 }
 

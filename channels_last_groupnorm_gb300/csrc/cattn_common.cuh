@@ -59,8 +59,8 @@ struct Segment {
 // rows that see nothing are written too).
 __device__ __forceinline__ int keys_of(const CattnArgs &a, const Sequence &s, int run)
 {
-    if (!a.p.a.causal) return s.length;
-    return min(max(s.first_place() + min(s.end - s.begin, (run + 1) * a.tokens), 0), s.length);
+    if (!a.p.a.causal) return s.held;
+    return min(max(s.first_place() + min(s.end - s.begin, (run + 1) * a.tokens), 0), s.held);
 }
 
 __device__ __forceinline__ int blocks_of(const CattnArgs &a, const Sequence &s, int run)

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 row.top = -INFINITY;
                 row.slope = (MODE & kBias) && a.slopes && there ? __ldg(a.slopes + head) * kLog2e : 0.f;
                 row.place = static_cast<float>(place);
-                row.end = a.causal ? min(max(place + 1, 0), g.s.length) : g.s.length;
+                row.end = a.causal ? min(max(place + 1, 0), g.s.held) : g.s.held;
                 row.out = there ? token * a.heads + head : -1;
                 row.lse = head * a.tokens + token;
                 rows[lane] = row;
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             Row *rows = all_rows + (segment & 1) * N;
             const int first_token = g.run * args.tokens, live = min(args.tokens, g.s.end - g.s.begin - first_token) * args.heads;
             const int keys = keys_of(args, g.s, g.run);
-            const int all = a.causal ? min(max(g.s.first_place() + first_token + 1, 0), g.s.length) : g.s.length;
+            const int all = a.causal ? min(max(g.s.first_place() + first_token + 1, 0), g.s.held) : g.s.held;
             wait_warp(bar(kQ + (segment & 1)), (segment >> 1) & 1, abort, args.limit);
             float l[N];
 #pragma unroll

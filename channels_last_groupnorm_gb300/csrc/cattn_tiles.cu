@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int first_token = g.run * args.tokens, keys = keys_of(args, g.s, g.run);
             const auto place_of = [&](int i) { return g.s.first_place() + first_token + i / args.heads; };
-            const auto end_of = [&](int place) { return a.causal ? min(max(place + 1, 0), g.s.length) : g.s.length; };
+            const auto end_of = [&](int place) { return a.causal ? min(max(place + 1, 0), g.s.held) : g.s.held; };
             const int place = place_of(min(row, live - 1)), end = end_of(place), all = end_of(place_of(half * kTile));
             const int head = g.hk * args.p.group + g.first_head + row % args.heads;
             const bool there = row < live && g.first_head + row % args.heads < args.p.group;

@@ -673,8 +673,8 @@ int gn_rms_norm_backward(const void *dy, const void *total, const void *weight, 
  *
  * Values of table, lengths and cu are clamped into range on the device: bad ones
  * give wrong results, never a wrong address.  A new token whose place is negative or
- * past the table, or whose page is not one of `pages`, is not stored; keys of such a
- * page read as zeros.
+ * past the table, or whose page is not one of `pages`, is not stored; keys past the
+ * table are not seen, and those of a page that there is not read as zeros.
  */
 typedef struct gn_cache {
     void *k_pages, *v_pages;          /* DEVICE e4m3 [pages][page_size][kv_heads][dim], 16-byte aligned, any order

@@ -152,6 +152,30 @@ def test_rms_norm_nothing_and_not_supported():
         assert gn.rms_norm(x[:2], out=x[1:3]) is None
 
 
+@pytest.mark.parametrize("rows,cols,dtype", [(600, 2048, BF), (9000, 64, FP), (300, 77, F32)])
+def test_rms_norm_outputs_in_bytes_that_lie_anywhere_and_captured(rows, cols, dtype):
+    x, w = rand((rows, cols), dtype, 1, 2.0), rand((cols,), dtype, 2) + 1.0
+    y, scales, _, rstd = gn.rms_norm(x, w, quantize=True)
+    buf = torch.full((rows, cols + 9), 0x11, dtype=torch.uint8, device="cuda")
+    into = buf[:, 3:3 + cols].view(sr.E4M3)
+    got = gn.rms_norm(x, w, quantize=True, out=into)
+    # (single bytes are another kernel's work, whose sums may be a rounding off)
+    want = sr.rms_norm(x, w, 1e-6)
+    assert got[0] is into
+    br.check(into.double() * got[1].double()[:, None], *want["y8"], "bytes")
+    br.check(got[1], *want["scales"], "scales")
+    assert (buf[:, :3] == 0x11).all() and (buf[:, 3 + cols:] == 0x11).all()
+    dy = rand((rows, cols), dtype, 3)
+    dx, dw = gn.rms_norm_backward(dy, x, rstd, w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a = gn.rms_norm(x, w, quantize=True)
+        b = gn.rms_norm_backward(dy, x, a[3], w)
+    x.neg_()
+    graph.replay()
+    assert same(a[1], scales) and same(a[3], rstd) and same(a[0].float(), -y.float()) and same(b[1], -dw)
+
+
 # ---------------------------------------------------------------------------
 # appending
 # ---------------------------------------------------------------------------
@@ -294,6 +318,32 @@ def test_append_bad_tables_lengths_and_ends():
                 br.check(got, value, bound, "q of every token, stored or not") if sorted(cu) == cu else None
                 for name in "kv":
                     assert torch.equal(cache.pages(name), before.pages(name)) and same(cache.scales(name), before.scales(name))
+
+
+@pytest.mark.parametrize("new", [1, 12, 90])
+def test_lengths_past_the_table(new):
+    """Tokens past the table are dropped, and nothing moves in their place: what is there
+    stays, and the queries see what the table holds."""
+    cache = sr.Cache([64, 40], 32, 2, 32, seed=1, width=2)
+    before = cache.copy()
+    k, v = rand((2 * new, 2, 32), BF, 1), rand((2 * new, 2, 32), BF, 2)
+    q = rand((2 * new, 4, 32), BF, 3)
+    lengths = i32([64 + new, 64 + new])                     # all new tokens of both lie behind the table
+    args = (*cache.args()[:5], lengths)
+    assert gn.cache_append(k, v, *args) is True
+    for name in "kv":
+        assert torch.equal(cache.pages(name), before.pages(name)) and same(cache.scales(name), before.scales(name))
+    out, lse = gn.attention_cached(q, *args)
+    want = sr.attention(q[:new].contiguous(), sr_first(cache), [0, new], causal=False)
+    br.check(out[:new], *want["out"], "out")
+    br.check(lse[:, :new], *want["lse"], "lse")
+
+
+def sr_first(cache):
+    """The cache with its first sequence alone."""
+    one = cache.copy()
+    one.lens, one.table_host = cache.lens[:1], cache.table_host[:1]
+    return one
 
 
 def test_append_layouts_of_one_buffer():
