@@ -6,7 +6,9 @@
 // a call, in the order of sequences, heads, runs and blocks, are dealt to the CTAs in
 // equal consecutive parts, whatever the sequences' lengths are (only the device
 // knows them); a tile counts as some blocks more than it has (`extra`), for its start
-// and end.  A CTA's part is a list of segments, one for each tile that it meets; a
+// and end, and one of no more blocks than that is not split: it belongs to the CTA whose part
+// holds its first unit (two prompts of 512 tokens, 32 heads on 8: 128 tiles of up to 4 blocks,
+// 38 us replayed with nearly every tile in pieces, 32 so).  A CTA's part is a list of segments, one for each tile that it meets; a
 // tile that several CTAs share leaves unnormalised pieces in the workspace, which
 // a second kernel joins in the order of the keys.
 #pragma once
@@ -108,6 +110,26 @@ struct Walk {
             offset -= b;
         }
         unit = static_cast<int>(offset);
+        const int total = blocks_of(a, s, run);
+        if (unit > 0 && total <= a.extra) spend(a.extra + total - unit);      // another CTA's
+    }
+    // `count` units are done with, which end the tile or the part
+    __device__ __forceinline__ void spend(int count)
+    {
+        at += count;
+        left -= count;
+        unit = 0;
+        if (left > 0 && ++run == runs) {
+            run = 0;
+            if (++head == heads()) {
+                head = 0;
+                const int last = first_sequence(a) + sequence_count(a);
+                int n = seq + 1;
+#pragma unroll 1
+                for (load(n); runs == 0 && n + 1 < last; load(n)) ++n;
+                if (runs == 0) left = 0;
+            }
+        }
     }
     // the next tile of which the part has blocks
     __device__ __forceinline__ bool next(Segment &g)
@@ -120,24 +142,12 @@ struct Walk {
             g.first_head = (head - g.hk * a.chunks) * a.heads;
             g.run = run;
             g.total = blocks_of(a, s, run);
-            const int all = a.extra + g.total, take = static_cast<int>(left < all - unit ? left : all - unit);
+            const int all = a.extra + g.total;
+            const int take = g.total <= a.extra || left > all - unit ? all - unit : static_cast<int>(left);
             g.b0 = max(unit - a.extra, 0);
             g.b1 = max(unit + take - a.extra, 0);
             tile_end = at + all - unit;
-            at += take;
-            left -= take;
-            unit = 0;
-            if (left > 0 && ++run == runs) {
-                run = 0;
-                if (++head == heads()) {
-                    head = 0;
-                    const int last = first_sequence(a) + sequence_count(a);
-                    int n = seq + 1;
-#pragma unroll 1
-                    for (load(n); runs == 0 && n + 1 < last; load(n)) ++n;
-                    if (runs == 0) left = 0;
-                }
-            }
+            spend(take);
             if (g.b0 < g.b1) return true;
         }
         return false;

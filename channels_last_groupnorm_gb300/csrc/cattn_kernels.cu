@@ -13,6 +13,7 @@ namespace {
 // warp each, or with many pieces all warps, each with some of the pieces (one token at 131072,
 // 38 pieces of a tile: 26 us with a warp for a row).  Four channels a lane; every load of a
 // row's outputs is on its way before the first is used.
+constexpr int kFewRows = 32, kManyRows = 2 * kTile;
 constexpr int kJoinWarps = 8, kJoinMany = 8;
 
 template <typename T>
@@ -27,7 +28,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     const Shared s = args.shared[blockIdx.x];
     if (s.pieces <= 1 || *reinterpret_cast<volatile unsigned int *>(args.limit.status) != 0u) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool many = s.pieces > kJoinMany;
+    const bool many = s.pieces > kJoinMany && args.rows <= kFewRows;      // (more rows keep the warps busy)
     const float *first = piece_of(args, blockIdx.x, 1), *others = piece_of(args, blockIdx.x, 0);
     const int64_t step = 2 * static_cast<int64_t>(args.rows) * (2 + c.dim);
     const auto piece = [&](int p) { return p == 0 ? first : others + p * step; };
@@ -102,8 +103,6 @@ bool encode_pool(CUtensorMap *map, const void *base, const gn_cache &c, int64_t 
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-constexpr int kFewRows = 32, kManyRows = 2 * kTile;
 
 // The tiles of a call and the kernel for them: up to 32 rows on the tensor core's narrow
 // side (16 where that is all there is), or 256 on its wide side.
