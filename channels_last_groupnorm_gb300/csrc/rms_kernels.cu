@@ -463,34 +463,86 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_kernel(const __grid_constan
     }
 }
 
-template <typename T, int EPV, int NV, int THREADS, int CTAS>
+// Rows on their way to a thread's own places in shared memory (whole vectors only):
+// nobody else reads them, so no barrier is needed, and no registers are held.
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// AHEAD rows of each thread's groups are on their way while one is worked on (vectors only;
+// 4608 x 6144 with dtotal, a step replayed: 104 us with the next row's loads behind this one's
+// stores, 98 with one row ahead, 99 with two).
+template <typename T, int EPV, int NV, int THREADS, int CTAS, int AHEAD>
 __global__ void __launch_bounds__(THREADS, CTAS) rms_grad_kernel(const __grid_constant__ RmsGradArgs a, int tpr)
 {
     __shared__ float scratch[kMaxGroups][2][32][2];
-    extern __shared__ __align__(16) float staged[];       // the weight, then [groups][cols] sums where a CTA has several
+    // the weight, [AHEAD][3][NV][threads] vectors, then [groups][cols] sums where a CTA has several
+    extern __shared__ __align__(16) float staged[];
     tc::griddep_wait();
     if (threadIdx.x == 0) tc::griddep_launch_dependents();
     Group gr = group_of(tpr, scratch);
-    const int per = blockDim.x / tpr;
+    const int per = blockDim.x / tpr, weight_floats = a.weight ? (a.cols + 3) / 4 * 4 : 0;
     const int64_t step = static_cast<int64_t>(gridDim.x) * per;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
     const bool weighed = a.weight != nullptr;
     float dw[NV][EPV] = {};
     int64_t first = static_cast<int64_t>(blockIdx.x) * per;
     Slot<T, EPV> t[NV], dy[NV], dt[NV];
-    const auto load = [&](int64_t n) {
-        load_row(t, a.total, a.total_at, a.inner, a.rows, n, gr, a.cols);
-        load_row(dy, a.dy, a.dy_at, a.inner, a.rows, n, gr, a.cols);
-        if (a.dtotal) load_row(dt, a.dtotal, a.dtotal_at, a.inner, a.rows, n, gr, a.cols);
+    const uint32_t room = smem_addr(staged + weight_floats) + 16u * threadIdx.x;
+    const auto place = [&](int stage, int which, int k) {
+        return room + 16u * blockDim.x * static_cast<uint32_t>((stage * 3 + which) * NV + k);
     };
-    load(first + gr.g);
-    float rstd_next = first + gr.g < a.rows ? __ldg(a.rstd + first + gr.g) : 0.f;
+    const auto load = [&](int64_t n, int stage) {
+        if constexpr (AHEAD == 0) {
+            load_row(t, a.total, a.total_at, a.inner, a.rows, n, gr, a.cols);
+            load_row(dy, a.dy, a.dy_at, a.inner, a.rows, n, gr, a.cols);
+            if (a.dtotal) load_row(dt, a.dtotal, a.dtotal_at, a.inner, a.rows, n, gr, a.cols);
+        } else {
+            if (n < a.rows) {
+                const Place at = row_place(a.inner, a.rows, n);
+                const T *rows[3] = {static_cast<const T *>(a.total) + offset_at(a.total_at, at),
+                                    static_cast<const T *>(a.dy) + offset_at(a.dy_at, at),
+                                    a.dtotal ? static_cast<const T *>(a.dtotal) + offset_at(a.dtotal_at, at) : nullptr};
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    const int c = (gr.lane + k * gr.tpr) * EPV;
+#pragma unroll
+                    for (int w = 0; w < 3; ++w)
+                        if (rows[w] && c < a.cols) copy_async(place(stage, w, k), rows[w] + c);
+                }
+            }
+            copy_commit();
+        }
+    };
+    const auto rstd_of = [&](int64_t n) { return n < a.rows ? __ldg(a.rstd + n) : 0.f; };
+    constexpr int kDeep = AHEAD ? AHEAD : 1;
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) load(first + gr.g + i * step, i);
+    float rstd_next = rstd_of(first + gr.g);
     stage_weight(staged, a.weight, a.weight_format, a.cols);
     __syncthreads();
+    int stage = 0;
     for (; first < a.rows; first += step) {
         const int64_t n = first + gr.g;
         const bool live = n < a.rows;
         const float rstd = rstd_next;
+        if constexpr (AHEAD > 0) {
+            copy_wait<kDeep - 1>();
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                t[k].raw = lds128(place(stage, 0, k));
+                dy[k].raw = lds128(place(stage, 1, k));
+                if (a.dtotal) dt[k].raw = lds128(place(stage, 2, k));
+            }
+        }
+        rstd_next = rstd_of(n + step);
         float sum[1] = {0.f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -505,6 +557,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_grad_kernel(const __grid_co
                 if (weighed && live) dw[k][e] = fmaf(g[e], f[e] * rstd, dw[k][e]);
                 sum[0] = fmaf(g[e] * w[e], f[e], sum[0]);
             }
+        }
+        if constexpr (AHEAD > 0) {
+            load(n + kDeep * step, stage);         // (what was in its place is in registers)
+            stage = stage + 1 == kDeep ? 0 : stage + 1;
         }
         row_sum(sum, gr);
         const float along = sum[0] * inv_cols * rstd * rstd;
@@ -524,9 +580,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_grad_kernel(const __grid_co
             for (int e = 0; e < EPV; ++e) f[e] = fmaf(rstd, fmaf(-f[e], along, g[e] * w[e]), r[e]);
             o[k].set(f);
         }
-        // the next row is on its way while this one is written
-        load(n + step);
-        rstd_next = n + step < a.rows ? __ldg(a.rstd + n + step) : 0.f;
+        if constexpr (AHEAD == 0) load(n + step, 0);
         T *dx = live ? static_cast<T *>(a.dx) + row_offset(a.dx_at, a.inner, a.rows, n) : nullptr;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -534,6 +588,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_grad_kernel(const __grid_co
             if (live && c < a.cols) o[k].store(dx + c);
         }
     }
+    if constexpr (AHEAD > 0) copy_wait<0>();
     if (!weighed) return;
     float *out = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
     if (per == 1) {
@@ -546,7 +601,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_grad_kernel(const __grid_co
         }
         return;
     }
-    float *columns = staged + (a.cols + 3) / 4 * 4;
+    float *columns = staged + weight_floats + AHEAD * 3 * NV * 4 * blockDim.x;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int c = (gr.lane + k * tpr) * EPV;
@@ -628,9 +683,9 @@ bool vectors(int cols, int epv, std::initializer_list<std::pair<const void *, co
 template <auto KERNEL, typename Args>
 cudaError_t run(const Args &a, const Shape &d, int64_t most, size_t smem, int sm_count, cudaStream_t s, int *blocks)
 {
-    // (weights of up to 16384 columns and the sums of a few groups: 64 KB and a few more)
+    // (weights of up to 16384 columns and the sums of a few groups, or two rows on their way)
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = smem > 40 * 1024 ? allow_shared(reinterpret_cast<const void *>(KERNEL), 96 * 1024, done) : cudaSuccess;
+    cudaError_t e = smem > 40 * 1024 ? allow_shared(reinterpret_cast<const void *>(KERNEL), 160 * 1024, done) : cudaSuccess;
     if (e != cudaSuccess) return e;
     // as many CTAs as are on the SMs at once: each goes through several rows
     const int64_t per = d.threads / d.tpr * d.rows, all = std::min((a.rows + per - 1) / per, most);
@@ -669,15 +724,19 @@ cudaError_t backward(const RmsGradArgs &a, int sm_count, cudaStream_t s, int *bl
     const bool vec = vectors(a.cols, EPV, {{a.total, &a.total_at}, {a.dy, &a.dy_at}, {a.dtotal, &a.dtotal_at}, {a.dx, &a.dx_at}});
     const Shape d = shape_of(vec ? a.cols / EPV : a.cols, vec, a.rows, sm_count);
     const size_t per = static_cast<size_t>(d.threads / d.tpr), cols = static_cast<size_t>(a.cols);
-    const size_t smem = a.weight ? 4u * ((cols + 3) / 4 * 4 + (per > 1 ? per * cols : 0)) : 0;
+    const auto smem = [&](int ahead) {
+        return (a.weight ? 4u * ((cols + 3) / 4 * 4 + (per > 1 ? per * cols : 0)) : 0) +
+               16u * static_cast<size_t>(3 * ahead * d.nv * d.threads);
+    };
     const int64_t most = rms_norm_blocks(a.rows, sm_count);
-    if (d.rows > 1) return run<rms_short_grad_kernel<T, EPV>>(a, d, most, smem, sm_count, s, blocks);
-    if (vec && d.nv == 1) return run<rms_grad_kernel<T, EPV, 1, 1024, 1>>(a, d, most, smem, sm_count, s, blocks);
-    if (vec && d.nv == 2 && d.threads <= 384) return run<rms_grad_kernel<T, EPV, 2, 384, 2>>(a, d, most, smem, sm_count, s, blocks);
-    if (vec && d.nv == 2) return run<rms_grad_kernel<T, EPV, 2, 512, 1>>(a, d, most, smem, sm_count, s, blocks);
-    if (vec) return run<rms_grad_kernel<T, EPV, 4, (EPV == 8 ? 512 : 1024), 1>>(a, d, most, smem, sm_count, s, blocks);
-    if (d.nv == 4) return run<rms_grad_kernel<T, 1, 4, 1024, 1>>(a, d, most, smem, sm_count, s, blocks);
-    return run<rms_grad_kernel<T, 1, 16, 1024, 1>>(a, d, most, smem, sm_count, s, blocks);
+    if (d.rows > 1) return run<rms_short_grad_kernel<T, EPV>>(a, d, most, smem(0), sm_count, s, blocks);
+    if (vec && d.nv == 1) return run<rms_grad_kernel<T, EPV, 1, 1024, 1, 1>>(a, d, most, smem(1), sm_count, s, blocks);
+    if (vec && d.nv == 2 && d.threads <= 384)
+        return run<rms_grad_kernel<T, EPV, 2, 384, 2, 1>>(a, d, most, smem(1), sm_count, s, blocks);
+    if (vec && d.nv == 2) return run<rms_grad_kernel<T, EPV, 2, 512, 1, 2>>(a, d, most, smem(2), sm_count, s, blocks);
+    if (vec) return run<rms_grad_kernel<T, EPV, 4, (EPV == 8 ? 512 : 1024), 1, 0>>(a, d, most, smem(0), sm_count, s, blocks);
+    if (d.nv == 4) return run<rms_grad_kernel<T, 1, 4, 1024, 1, 0>>(a, d, most, smem(0), sm_count, s, blocks);
+    return run<rms_grad_kernel<T, 1, 16, 1024, 1, 0>>(a, d, most, smem(0), sm_count, s, blocks);
 }
 
 }  // namespace
