@@ -145,7 +145,7 @@ __device__ __forceinline__ Pieces pieces_of(int u, int pairs, bool halves)
 
 // A token's angles in shared memory: a lane takes eight pairs, two at a time, and lanes of
 // neighbouring eights lie side by side each time (pair by pair they would meet in the same banks,
-// 16 at once: 8555 tokens of 24 + 24 heads took 154 us instead of 84).
+// 16 at once: 8555 tokens of 24 + 24 heads took 118 us instead of 84).
 struct Angles {
     int eights;                   // of pairs, the last of which may be part empty
     __host__ __device__ __forceinline__ explicit Angles(int pairs) : eights((pairs + 7) / 8) {}

@@ -617,6 +617,233 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_grad_kernel(const __grid_co
     }
 }
 
+// ---- half-type rows that begin at any element, alike in all tensors ------------------
+// (Odd widths of contiguous tensors.)  A row is peeled: up to 7 elements to the first 16-byte
+// boundary, whole vectors, up to 7 elements behind them; the first ones and the last ones are
+// single elements of the row's first lanes.  Which column a thread has changes from row to row,
+// so the weight and, backward, its gradient's sums are in shared memory, a place left free behind
+// every eight: eight neighbours a lane then lie in different banks.
+constexpr int kEdge = 14;
+
+__device__ __forceinline__ int padded(int c) { return c + (c >> 3); }
+
+struct Peel {
+    int head, vectors, edge;          // edge: this lane's single element, or -1
+    __device__ __forceinline__ Peel(uintptr_t row, int cols, int lane)
+    {
+        head = static_cast<int>((8 - (row >> 1 & 7)) & 7);
+        vectors = (cols - head) >> 3;
+        const int tail = head + 8 * vectors;
+        const int c = lane < head ? lane : tail + lane - head;
+        edge = lane < kEdge && c < cols ? c : -1;
+    }
+};
+
+__device__ __forceinline__ void stage_padded(float *to, const void *weight, int format, int cols)
+{
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+        float w[1] = {1.0f};
+        if (weight) load_params<1>(weight, format, c, w);
+        to[padded(c)] = w[0];
+    }
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(512, 2) rms_peeled_kernel(const __grid_constant__ RmsArgs a, int tpr)
+{
+    __shared__ float scratch[kMaxGroups][2][32][2];
+    extern __shared__ __align__(16) float staged[];
+    tc::griddep_wait();
+    if (threadIdx.x == 0) tc::griddep_launch_dependents();
+    Group gr = group_of(tpr, scratch);
+    const int per = blockDim.x / tpr;
+    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    stage_padded(staged, a.weight, a.weight_format, a.cols);
+    __syncthreads();
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * per; first < a.rows; first += static_cast<int64_t>(gridDim.x) * per) {
+        const int64_t n = first + gr.g;
+        const bool live = n < a.rows;
+        const Place at = row_place(a.inner, a.rows, live ? n : 0);
+        const T *x = static_cast<const T *>(a.x) + offset_at(a.x_at, at);
+        const T *r = a.residual ? static_cast<const T *>(a.residual) + offset_at(a.residual_at, at) : nullptr;
+        T *total = a.residual ? static_cast<T *>(a.total) + offset_at(a.total_at, at) : nullptr;
+        const Peel p(reinterpret_cast<uintptr_t>(x), a.cols, gr.lane);
+        const int edge = live ? p.edge : -1;
+        Slot<T, 8> t[NV], s[NV];
+        float one = 0.f, sum = 0.f, most = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = gr.lane + k * tpr;
+            t[k].clear();
+            s[k].clear();
+            if (live && j < p.vectors) {
+                t[k].load(x + p.head + 8 * j);
+                if (r) s[k].load(r + p.head + 8 * j);
+            }
+        }
+        if (edge >= 0) {
+            one = to_float(x[edge]);
+            if (r) {
+                const T v = from_float<T>(one + to_float(r[edge]));
+                total[edge] = v;
+                one = to_float(v);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = gr.lane + k * tpr, c = p.head + 8 * j;
+            float f[8], g[8];
+            t[k].get(f);
+            if (r) {
+                s[k].get(g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] += g[e];
+                t[k].set(f);
+                if (live && j < p.vectors) t[k].store(total + c);
+                t[k].get(f);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
+            if (a.scales && live && j < p.vectors)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) most = max_nan(most, fabsf(f[e] * staged[padded(c + e)]));
+        }
+        sum = fmaf(one, one, sum);
+        if (a.scales && edge >= 0) most = max_nan(most, fabsf(one * staged[padded(edge)]));
+        row_sum_max(sum, most, gr);
+        const float rstd = 1.0f / sqrtf(fmaf(sum, inv_cols, a.eps));
+        most *= rstd;
+        const bool none = most < kLeastMagnitude;
+        const float by = none ? 0.f : 448.0f / most;
+        if (live && gr.lane == 0) {
+            if (a.rstd) a.rstd[n] = rstd;
+            if (a.scales) a.scales[n] = none ? 0.f : most / 448.0f;
+        }
+        const int64_t to = offset_at(a.y_at, at);
+        const auto put = [&](int c, float v) {
+            v = v * rstd * staged[padded(c)];
+            if (a.scales)
+                static_cast<uint8_t *>(a.y)[to + c] = static_cast<uint8_t>(e4m3_pair(v * by, 0.f));
+            else
+                static_cast<T *>(a.y)[to + c] = from_float<T>(v);
+        };
+        if (edge >= 0) put(edge, one);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = gr.lane + k * tpr, c = p.head + 8 * j;
+            if (!live || j >= p.vectors) continue;
+            float f[8];
+            t[k].get(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * staged[padded(c + e)];
+            if (a.scales) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] *= by;
+                store_e4m3<8>(static_cast<uint8_t *>(a.y) + to + c, f);
+            } else {
+                Slot<T, 8> o;
+                o.set(f);
+                o.store(static_cast<T *>(a.y) + to + c);
+            }
+        }
+    }
+}
+
+// (NV = 4, 2300 rows of 12001: 111 us in the 64 registers that two CTAs leave, 94 with one)
+template <typename T, int NV>
+__global__ void __launch_bounds__(512, NV == 2 ? 2 : 1) rms_peeled_grad_kernel(const __grid_constant__ RmsGradArgs a, int tpr)
+{
+    __shared__ float scratch[kMaxGroups][2][32][2];
+    extern __shared__ __align__(16) float staged[];       // the weight, then [groups] sums of its gradient
+    tc::griddep_wait();
+    if (threadIdx.x == 0) tc::griddep_launch_dependents();
+    Group gr = group_of(tpr, scratch);
+    const int per = blockDim.x / tpr, width = padded(a.cols) + 1;
+    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    float *dw = staged + width * (1 + gr.g);
+    stage_padded(staged, a.weight, a.weight_format, a.cols);
+    if (a.weight)
+        for (int c = threadIdx.x; c < width * per; c += blockDim.x) staged[width + c] = 0.f;
+    __syncthreads();
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * per; first < a.rows; first += static_cast<int64_t>(gridDim.x) * per) {
+        const int64_t n = first + gr.g;
+        const bool live = n < a.rows;
+        const Place at = row_place(a.inner, a.rows, live ? n : 0);
+        const T *pt = static_cast<const T *>(a.total) + offset_at(a.total_at, at);
+        const T *pd = static_cast<const T *>(a.dy) + offset_at(a.dy_at, at);
+        const T *pr = a.dtotal ? static_cast<const T *>(a.dtotal) + offset_at(a.dtotal_at, at) : nullptr;
+        const Peel p(reinterpret_cast<uintptr_t>(pt), a.cols, gr.lane);
+        const int edge = live ? p.edge : -1;
+        const float rstd = live ? __ldg(a.rstd + n) : 0.f;
+        Slot<T, 8> t[NV], dy[NV], dt[NV];
+        float one = 0.f, grad = 0.f, back = 0.f, sum[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = gr.lane + k * tpr, c = p.head + 8 * j;
+            t[k].clear();
+            dy[k].clear();
+            dt[k].clear();
+            if (live && j < p.vectors) {
+                t[k].load(pt + c);
+                dy[k].load(pd + c);
+                if (pr) dt[k].load(pr + c);
+            }
+        }
+        if (edge >= 0) {
+            one = to_float(pt[edge]);
+            grad = to_float(pd[edge]);
+            if (pr) back = to_float(pr[edge]);
+        }
+        // (Sums of a column are added to by one thread a row; the row's threads meet in its
+        // reduction before the next row, whose columns are dealt out anew.)
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = gr.lane + k * tpr, c = p.head + 8 * j;
+            if (!live || j >= p.vectors) continue;
+            float f[8], g[8];
+            t[k].get(f);
+            dy[k].get(g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (a.weight) dw[padded(c + e)] += g[e] * (f[e] * rstd);
+                sum[0] = fmaf(g[e] * staged[padded(c + e)], f[e], sum[0]);
+            }
+        }
+        if (edge >= 0) {
+            if (a.weight) dw[padded(edge)] += grad * (one * rstd);
+            grad *= staged[padded(edge)];
+            sum[0] = fmaf(grad, one, sum[0]);
+        }
+        row_sum(sum, gr);
+        if (gr.tpr <= 32) __syncwarp();
+        const float along = sum[0] * inv_cols * rstd * rstd;
+        T *dx = static_cast<T *>(a.dx) + offset_at(a.dx_at, at);
+        if (edge >= 0) dx[edge] = from_float<T>(fmaf(rstd, fmaf(-one, along, grad), back));
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int j = gr.lane + k * tpr, c = p.head + 8 * j;
+            if (!live || j >= p.vectors) continue;
+            float f[8], g[8], r[8];
+            t[k].get(f);
+            dy[k].get(g);
+            dt[k].get(r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = fmaf(rstd, fmaf(-f[e], along, g[e] * staged[padded(c + e)]), r[e]);
+            Slot<T, 8> o;
+            o.set(f);
+            o.store(dx + c);
+        }
+    }
+    if (!a.weight) return;
+    __syncthreads();
+    float *out = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
+    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+        float v = 0.f;
+        for (int g = 0; g < per; ++g) v += staged[width * (1 + g) + padded(c)];
+        out[c] = v;
+    }
+}
+
 // dweight: the CTAs' rows of partial sums, 32 columns a CTA, 32 warps taking every 32nd
 // row, and those sums in order.  (8 warps took 10 us for 608 rows.)
 __global__ void __launch_bounds__(1024) rms_columns_kernel(const __grid_constant__ RmsGradArgs a, int blocks)
@@ -680,6 +907,39 @@ bool vectors(int cols, int epv, std::initializer_list<std::pair<const void *, co
     return true;
 }
 
+// Whether all tensors' rows lie alike to 16 bytes (`y`: a row of bytes, eight of which go
+// with 16 of the others').
+bool alike(std::initializer_list<std::pair<const void *, const RowsAt *>> rows, const void *y, const RowsAt *y_at)
+{
+    const void *first = nullptr;
+    const RowsAt *at = nullptr;
+    for (const auto &r : rows) {
+        if (!r.first) continue;
+        if (!first) first = r.first, at = r.second;
+        if ((reinterpret_cast<uintptr_t>(r.first) - reinterpret_cast<uintptr_t>(first)) % 16 ||
+            (r.second->outer - at->outer) % 8 || (r.second->stride - at->stride) % 8)
+            return false;
+    }
+    return !y || ((reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(first) / 2) % 8 == 0 &&
+                  (y_at->outer - at->outer) % 8 == 0 && (y_at->stride - at->stride) % 8 == 0);
+}
+
+// Peeled rows: two vectors a thread (4608 x 6143 backward 73 us, 100 with four), four where two
+// would take more than 512 threads a row.
+Shape peeled_shape(int cols)
+{
+    Shape s;
+    const int slots = cols / 8;
+    s.nv = slots <= 1024 ? 2 : 4;
+    s.tpr = std::max(16, row_threads(slots, s.nv));
+    s.threads = s.tpr >= 256 ? s.tpr : s.tpr * std::max(1, 256 / s.tpr);
+    return s;
+}
+
+// Fewer columns than this take single elements (forward, 300000 x 65: 88 us, 138 so;
+// 500000 x 33: 140 us peeled, 115 so).
+constexpr int kPeeledCols = 64;
+
 template <auto KERNEL, typename Args>
 cudaError_t run(const Args &a, const Shape &d, int64_t most, size_t smem, int sm_count, cudaStream_t s, int *blocks)
 {
@@ -705,6 +965,17 @@ cudaError_t forward(const RmsArgs &a, int sm_count, cudaStream_t s)
     const bool vec = y_ok && vectors(a.cols, EPV, {{a.x, &a.x_at}, {a.residual, &a.residual_at}, {a.total, &a.total_at},
                                                    {a.scales ? nullptr : a.y, &a.y_at}}) &&
                      a.y_at.outer % EPV == 0 && a.y_at.stride % EPV == 0;
+    if constexpr (sizeof(T) == 2) {
+        if (!vec && a.cols >= kPeeledCols &&
+            alike({{a.x, &a.x_at}, {a.residual, &a.residual_at}, {a.total, &a.total_at}, {a.scales ? nullptr : a.y, &a.y_at}},
+                  a.scales ? a.y : nullptr, &a.y_at)) {
+            const Shape d = peeled_shape(a.cols);
+            const size_t smem = 4u * (static_cast<size_t>(a.cols) + static_cast<size_t>(a.cols) / 8 + 1);
+            int blocks;
+            if (d.nv == 2) return run<rms_peeled_kernel<T, 2>>(a, d, INT32_MAX, smem, sm_count, s, &blocks);
+            return run<rms_peeled_kernel<T, 4>>(a, d, INT32_MAX, smem, sm_count, s, &blocks);
+        }
+    }
     const Shape d = shape_of(vec ? a.cols / EPV : a.cols, vec, a.rows, sm_count);
     const size_t smem = a.weight ? 4u * static_cast<size_t>(a.cols) : 0;
     int blocks;
@@ -722,6 +993,17 @@ cudaError_t backward(const RmsGradArgs &a, int sm_count, cudaStream_t s, int *bl
 {
     constexpr int EPV = 16 / sizeof(T);
     const bool vec = vectors(a.cols, EPV, {{a.total, &a.total_at}, {a.dy, &a.dy_at}, {a.dtotal, &a.dtotal_at}, {a.dx, &a.dx_at}});
+    if constexpr (sizeof(T) == 2) {
+        if (!vec && a.cols >= kPeeledCols &&
+            alike({{a.total, &a.total_at}, {a.dy, &a.dy_at}, {a.dtotal, &a.dtotal_at}, {a.dx, &a.dx_at}}, nullptr, nullptr)) {
+            const Shape d = peeled_shape(a.cols);
+            const size_t width = static_cast<size_t>(a.cols) + static_cast<size_t>(a.cols) / 8 + 1;
+            const size_t smem = 4u * width * (a.weight ? 1 + static_cast<size_t>(d.threads / d.tpr) : 1);
+            const int64_t most = rms_norm_blocks(a.rows, sm_count);
+            if (d.nv == 2) return run<rms_peeled_grad_kernel<T, 2>>(a, d, most, smem, sm_count, s, blocks);
+            return run<rms_peeled_grad_kernel<T, 4>>(a, d, most, smem, sm_count, s, blocks);
+        }
+    }
     const Shape d = shape_of(vec ? a.cols / EPV : a.cols, vec, a.rows, sm_count);
     const size_t per = static_cast<size_t>(d.threads / d.tpr), cols = static_cast<size_t>(a.cols);
     const auto smem = [&](int ahead) {

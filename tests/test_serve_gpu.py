@@ -83,6 +83,39 @@ def test_rms_norm_many_rows_out_of_wider_tensors(rows, cols, wide, start, dtype)
     assert all(same(got[n], again[n]) for n in got)
 
 
+@pytest.mark.parametrize("start", range(8))
+@pytest.mark.parametrize("rows,cols,dtype", [
+    (777, 64, BF), (2001, 65, FP), (1301, 131, BF), (401, 4101, BF), (333, 8191, FP), (211, 8198, BF), (5, 16384, FP), (1, 71, BF)])
+def test_rms_norm_rows_that_begin_at_any_element(rows, cols, dtype, start):
+    def shifted(seed):
+        wide = rand((rows * cols + start,), dtype, seed, 2.0)
+        return wide[start:].view(rows, cols)
+
+    x, r, dy, dt = (shifted(s) for s in (1, 2, 3, 4))
+    w = rand((cols,), dtype, 5, 0.3) + 1.0
+    want = sr.rms_norm(x, w, 1e-3, r, dy, dt)
+    got = {}
+    room = {n: torch.full((rows * cols + start + 9,), 7.0, dtype=dtype, device="cuda") for n in ("y", "total", "dx")}
+    into = {n: v[start:start + rows * cols].view(rows, cols) for n, v in room.items()}
+    bytes_ = torch.full((rows * cols + start + 9,), 99, dtype=torch.uint8, device="cuda")
+    y8 = bytes_[start:start + rows * cols].view(rows, cols).view(sr.E4M3)
+    for again in range(2):
+        _, _, _, rstd = gn.rms_norm(x, w, residual=r, eps=1e-3, out=into["y"], total_out=into["total"])
+        _, scales, _, rstd8 = gn.rms_norm(x, w, residual=r, eps=1e-3, out=y8, total_out=into["total"], quantize=True)
+        _, dw = gn.rms_norm_backward(dy, into["total"], rstd, w, dtotal=dt, out=into["dx"])
+        now = dict(y=into["y"], total=into["total"], rstd=rstd, dx=into["dx"], dw=dw, scales=scales,
+                   y8=y8.double() * scales.double()[:, None])
+        if again:
+            assert all(same(now[n], got[n]) for n in now)
+        got = {n: v.clone() for n, v in now.items()}
+    for name, value in got.items():
+        br.check(value, *want[name], f"{name} {rows}x{cols} from {start}")
+    assert same(rstd8, rstd)
+    for v in room.values():
+        assert (v[:start] == 7.0).all() and (v[start + rows * cols:] == 7.0).all()
+    assert (bytes_[:start] == 99).all() and (bytes_[start + rows * cols:] == 99).all()
+
+
 def test_rms_norm_heads_of_a_projection_and_broadcast_rows():
     qkv = rand((300, 7, 64), BF, 1, 2.0)
     w = rand((64,), BF, 2) + 1.0
