@@ -24,10 +24,14 @@ namespace cattn {
 using namespace pattn;
 using cache::Sequence;
 
+// Rows of a tile in the kernel for few of them and in the one for many.
+constexpr int kFewTile = 16, kManyRows = 2 * kTile;
+
 struct CattnArgs {
     CachedAttn p;
     WaitLimit limit;
     float scale_log2;
+    int least, most;              // tokens of the sequences that this kernel looks after
     int tokens, heads, chunks;    // of a tile: its tokens, its query heads; chunks of heads per key / value head
     int rows;                     // room for rows in a tile's piece
     int chunk;                    // keys that one load brings: they lie in one page
@@ -86,7 +90,8 @@ struct Walk {
     {
         seq = n;
         s = cache::sequence_of(a.p.c, a.p.a.tokens, n);
-        runs = (s.end - s.begin + a.tokens - 1) / a.tokens;
+        const int count = s.end - s.begin;
+        runs = count < a.least || count > a.most ? 0 : (count + a.tokens - 1) / a.tokens;
         per_head = 0;
 #pragma unroll 1
         for (int r = 0; r < runs; ++r) per_head += a.extra + blocks_of(a, s, r);
@@ -302,7 +307,6 @@ __device__ __forceinline__ void fill_work(WorkList<K> &w, Walk &walk, const Part
     __syncwarp();
 }
 
-cudaError_t launch_join(const CattnArgs &a, int ctas, cudaStream_t s);
 cudaError_t launch_cached_few(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s);
 cudaError_t launch_cached_tiles(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s);
 

@@ -58,14 +58,11 @@ struct Layout {
 
 // Weights lie as the threads have them, a key's next to each other ([128 keys][parts][n],
 // MN-major, swizzled over as many bytes as a row has): whole vectors are stored, where
-// [rows][keys] would take a byte at a time (96 of them a thread with 32 rows in three parts).
-__host__ __device__ constexpr uint32_t weight_row(int n, int parts)
-{
-    return n * parts <= 32 ? 32u : n * parts <= 64 ? 64u : 128u;
-}
+// [rows][keys] would take a byte at a time (48 of them a thread in three parts).
+__host__ __device__ constexpr uint32_t weight_row(int n, int parts) { return n * parts <= 32 ? 32u : 64u; }
 
 // Descriptor of the weights as the B operand: 8 keys after 8 keys (stride offset); the
-// swizzle mode is 2 for 128 bytes, 4 for 64, 6 for 32.
+// swizzle mode is 4 for 64 bytes, 6 for 32.
 template <uint32_t ROW>
 __device__ __forceinline__ uint64_t weights_desc(uint32_t smem)
 {
@@ -73,7 +70,7 @@ __device__ __forceinline__ uint64_t weights_desc(uint32_t smem)
     d |= static_cast<uint64_t>(1u) << 16;
     d |= static_cast<uint64_t>((8u * ROW) >> 4) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(ROW == 128 ? 2u : ROW == 64 ? 4u : 6u) << 61;
+    d |= static_cast<uint64_t>(ROW == 64 ? 4u : 6u) << 61;
     return d;
 }
 
@@ -134,15 +131,15 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[N])
     tmem_wait_ld();
 }
 
-template <typename T, int MODE, int N>
+template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 2)
     cached_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                       const __grid_constant__ CattnArgs args)
 {
-    constexpr int PARTS = IsBf16<T>::value ? 2 : 3, STAGES = stages_of(N, PARTS);
+    constexpr int N = kFewTile, PARTS = IsBf16<T>::value ? 2 : 3, STAGES = stages_of(N, PARTS);
     constexpr Layout lay = layout(N, PARTS, STAGES);
     constexpr uint32_t kRow = weight_row(N, PARTS);
-    constexpr int SIDE = N == 32 ? 8 : 4;      // rows that are worked on side by side
+    constexpr int SIDE = 4;      // rows that are worked on side by side
     extern __shared__ __align__(1024) uint8_t gbase[];
     const uint32_t base = smem_addr(gbase);
     const gn_cache &c = args.p.c;
@@ -163,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
     }
-    constexpr uint32_t kColumns = 2 * N + PARTS * N <= 128 ? 128 : 256;
+    constexpr uint32_t kColumns = 128;
+    static_assert(2 * N + PARTS * N <= kColumns, "a CTA's tensor memory");
     if (warp == 1) {
         tmem_alloc(base + lay.words, kColumns);
         tmem_relinquish();
@@ -573,32 +571,26 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CattnArgs);
 
-template <typename T, int MODE, int N>
+template <typename T, int MODE>
 cudaError_t launch(const CattnArgs &args, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s)
 {
     constexpr int PARTS = IsBf16<T>::value ? 2 : 3;
-    static std::atomic<uint64_t> done{0}, wide{0};
-    const Kernel kernel = cached_few_kernel<T, MODE, N>;
-    cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kRoom, done);
-    if (e == cudaSuccess) e = allow_clusters(reinterpret_cast<const void *>(kernel), wide);
+    static std::atomic<uint64_t> done{0};
+    const Kernel kernel = cached_few_kernel<T, MODE>;
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kRoom, done);
     if (e != cudaSuccess) return e;
-    return tc::launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), layout(N, PARTS, stages_of(N, PARTS)).total, s, mk, mv, args);
-}
-
-template <typename T, int MODE>
-cudaError_t launch_rows(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s)
-{
-    return a.rows == 16 ? launch<T, MODE, 16>(a, mk, mv, ctas, s) : launch<T, MODE, 32>(a, mk, mv, ctas, s);
+    return tc::launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads),
+                          layout(kFewTile, PARTS, stages_of(kFewTile, PARTS)).total, s, mk, mv, args);
 }
 
 template <typename T>
 cudaError_t launch_mode(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s)
 {
     const int mode = (a.p.a.cap > 0.f ? kCap : 0) | (a.p.a.slopes ? kBias : 0);
-    if (mode == 0) return launch_rows<T, 0>(a, mk, mv, ctas, s);
-    if (mode == kCap) return launch_rows<T, kCap>(a, mk, mv, ctas, s);
-    if (mode == kBias) return launch_rows<T, kBias>(a, mk, mv, ctas, s);
-    return launch_rows<T, kCap | kBias>(a, mk, mv, ctas, s);
+    if (mode == 0) return launch<T, 0>(a, mk, mv, ctas, s);
+    if (mode == kCap) return launch<T, kCap>(a, mk, mv, ctas, s);
+    if (mode == kBias) return launch<T, kBias>(a, mk, mv, ctas, s);
+    return launch<T, kCap | kBias>(a, mk, mv, ctas, s);
 }
 
 }  // namespace

@@ -465,6 +465,33 @@ def test_attention_many_sequences():
     attend_and_check(cache, [n % 3 for n in range(1500)], 2, 32)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("h,hk,dim,page,new,lens", [
+    (8, 2, 128, 64, [300, 1, 1, 8, 9, 0, 1], [300, 2000, 5, 8, 700, 40, 0]), (4, 4, 64, 16, [1, 32, 33, 1, 200], [900, 32, 3000, 1, 200]),
+    (16, 1, 96, 32, [2, 3, 1, 1, 40], [800, 900, 1, 130, 41]), (32, 1, 80, 24, [1, 2, 1, 7], [500, 600, 3, 7]),
+    (33, 1, 48, 8, [1, 2, 1], [100, 300, 0]), (64, 8, 128, 256, [4, 5, 1, 1, 70], [4, 3000, 1500, 257, 900]),
+    (16, 2, 112, 40, [0, 0, 500], [10, 0, 900]), (16, 2, 112, 40, [1] * 20 + [4], [100] * 21)])
+def test_attention_single_tokens_beside_long_runs(h, hk, dim, page, new, lens, dtype):
+    """Few tokens and many of them in one call, with tokens of no sequence around them."""
+    cache = sr.Cache(lens, page, hk, dim, seed=dim)
+    ahead, behind = 37, 5
+    begins = [0]
+    for n in new:
+        begins.append(begins[-1] + n)
+    q = rand((ahead + begins[-1] + behind, h, dim), dtype, 3, 1.5)
+    inside = slice(ahead, ahead + begins[-1])
+    cu = i32([ahead + n for n in begins])
+    for how in (dict(), dict(causal=False, cap=7.0), dict(slopes=torch.full((h,), 0.03, device="cuda"))):
+        out, lse = gn.attention_cached(q, *cache.args(), cu, **how)
+        again = gn.attention_cached(q, *cache.args(), cu, **how)
+        want = sr.attention(q[inside].contiguous(), cache, begins, **how)
+        br.check(out[inside], *want["out"], f"out {new} {how}")
+        br.check(lse[:, inside], *want["lse"], f"lse {new} {how}")
+        assert same(again[0], out) and same(again[1], lse)
+        for gone in (slice(0, ahead), slice(ahead + begins[-1], None)):
+            assert not out[gone].any() and (lse[:, gone] == -math.inf).all()
+
+
 def test_attention_padded_batch():
     """Tokens ahead of the first sequence and behind the last, sequences without tokens."""
     cache = sr.Cache([50, 60, 7, 0], 16, 2, 64, seed=1)
