@@ -83,6 +83,26 @@ def test_rms_norm_many_rows_out_of_wider_tensors(rows, cols, wide, start, dtype)
     assert all(same(got[n], again[n]) for n in got)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+@pytest.mark.parametrize("cols", [32, 128, 351, 352, 6144, 6143, 30])
+def test_rms_norm_halves_of_a_step_in_8_bits(cols, dtype):
+    """What lies halfway between two e4m3 numbers goes to the even one: t weight is exact here,
+    and so is which side of the middle 448 / max of it lies (all else is 2^-11 away from one)."""
+    most = torch.tensor([28, 56, 84, 112, 140, 168, 196, 224, 252], dtype=torch.float64)
+    gen = torch.Generator().manual_seed(cols)
+    x = torch.randint(-252, 253, (most.shape[0], cols), generator=gen).double().clamp(-most[:, None], most[:, None])
+    x[:, cols // 2] = most
+    q = x * 448 / most[:, None]
+    step = torch.exp2(torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6))) - 3)
+    want = torch.round(q / step) * step
+    w = torch.full((cols,), 0.75, device="cuda", dtype=dtype)
+    for weight in (None, w):
+        y, scales, _, rstd = gn.rms_norm(x.to(dtype).cuda(), weight, eps=1e-3, quantize=True)
+        assert torch.equal(y.double().cpu(), want)
+        by = rstd.double() * (1.0 if weight is None else 0.75) * most.cuda() / 448
+        assert ((scales.double() - by).abs() <= 2.0 ** -22 * by).all()
+
+
 @pytest.mark.parametrize("start", range(8))
 @pytest.mark.parametrize("rows,cols,dtype", [
     (777, 64, BF), (2001, 65, FP), (1301, 131, BF), (401, 4101, BF), (333, 8191, FP), (211, 8198, BF), (5, 16384, FP), (1, 71, BF)])
