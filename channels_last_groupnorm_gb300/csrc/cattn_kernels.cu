@@ -147,7 +147,7 @@ int join_blocks(const CattnArgs &a, int ctas, bool few)
     const int rows = static_cast<int>(std::min<int64_t>(a.p.a.tokens, a.tokens)) * a.heads;
     const int64_t tiles = std::max<int64_t>(a.p.c.sequences, a.p.a.tokens / a.tokens) * a.p.c.kv_heads * a.chunks;
     const bool many = tiles * kJoinMany < ctas;
-    if (few) return many ? rows : (rows + kJoinWarps - 1) / kJoinWarps;
+    if (few) return many ? rows : std::min(rows, 4);      // (a long sequence among many still has four)
     return many ? (rows + kJoinWarps - 1) / kJoinWarps : 16;
 }
 
@@ -185,7 +185,7 @@ size_t cached_attn_workspace_bytes(int64_t, int, int, int, int dim, int sm_count
 cudaError_t launch_cached_attn(const CachedAttn &p, int sm_count, const WaitLimit &limit, cudaStream_t s, int *launches)
 {
     const int most = cattn::few_tokens(p);
-    cattn::CattnArgs few = cattn::plan(p, true, 0, most), tiles = cattn::plan(p, false, most + 1, INT_MAX);
+    cattn::CattnArgs few = cattn::plan(p, true, 0, most), tiles = cattn::plan(p, false, most == INT_MAX ? 0 : most + 1, INT_MAX);
     few.limit = tiles.limit = limit;
     few.shared = static_cast<cattn::Shared *>(p.workspace);
     tiles.shared = few.shared + 2 * sm_count;

@@ -625,8 +625,9 @@ int gn_attn_packed_backward(const gn_attn_packed_args *args, const void *dout, i
  * the norm sends back).  In 8 bits a row is stored as e4m3 of y / scale with
  * scale = max |y| / 448, so that its largest magnitude becomes 448; a row whose
  * largest magnitude is below 1e-30 (or below 2^-110 as t weight) has scale 0 and bytes
- * 0.  y / scale is taken in fp32, as 448 t weight / max |t weight|, and rounded once.  Sums are fp32 and added up in a fixed order: the same inputs give
- * the same bits.
+ * 0.  y / scale is taken in fp32, as 448 t weight / max |t weight|, and rounded once.
+ * Sums are fp32 and added up in a fixed order: the same inputs, at the same alignment
+ * to 16 bytes, give the same bits.
  */
 
 /* RMS norm.

@@ -172,6 +172,25 @@ def test_rms_norm_in_place():
         assert got[0] is a[n] and same(got[0], dx) and same(got[1], dw)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols", [71, 1001, 9001])
+def test_rms_norm_in_place_in_odd_widths(cols, dtype):
+    x, r, dy, dt = (rand((777, cols), dtype, s) for s in (1, 2, 3, 4))
+    w = rand((cols,), F32, 5) + 1.0
+    want = gn.rms_norm(x, w, residual=r)
+    for onto in (r.clone(), x.clone()):
+        a, b = (x, onto) if same(onto, r) else (onto, r)
+        y, _, total, rstd = gn.rms_norm(a, w, residual=b, total_out=onto)
+        assert total is onto and same(y, want[0]) and same(onto, want[2]) and same(rstd, want[3])
+    own = x.clone()
+    assert same(gn.rms_norm(own, w, out=own)[0], gn.rms_norm(x, w)[0])
+    dx, dw = gn.rms_norm_backward(dy, total, rstd, w, dtotal=dt)
+    for n in range(3):
+        a = [dy.clone(), total.clone(), dt.clone()]
+        got = gn.rms_norm_backward(a[0], a[1], rstd, w, dtotal=a[2], out=a[n])
+        assert got[0] is a[n] and same(got[0], dx) and same(got[1], dw)
+
+
 def test_rms_norm_rows_of_zeros_nan_and_infinity():
     x = rand((6, 64), F32, 1)
     x[1] = 0.0
