@@ -531,6 +531,30 @@ def test_attention_single_tokens_beside_long_runs(h, hk, dim, page, new, lens, d
             assert not out[gone].any() and (lse[:, gone] == -math.inf).all()
 
 
+def test_attention_captured_once_for_any_counts():
+    """The counts of new tokens are the device's: a captured call follows them."""
+    cache = sr.Cache([300, 900, 40, 5], 32, 2, 64, seed=1)
+    q = rand((240, 8, 64), BF, 1, 1.5)
+    cu = i32([0, 60, 120, 160, 165])
+    gn.attention_cached(q, *cache.args(), cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = gn.attention_cached(q, *cache.args(), cu)
+    for begins in ([0, 1, 2, 3, 4], [0, 200, 201, 240, 240], [10, 18, 27, 27, 28], [0, 0, 0, 40, 45], [0, 60, 120, 160, 165]):
+        cu.copy_(i32(begins))
+        for again in range(2):
+            out.fill_(9.0)
+            lse.fill_(9.0)
+            graph.replay()
+        eager = gn.attention_cached(q, *cache.args(), i32(begins))
+        assert same(out, eager[0]) and same(lse, eager[1])
+        inside = slice(begins[0], begins[-1])
+        want = sr.attention(q[inside].contiguous(), cache, [b - begins[0] for b in begins])
+        br.check(out[inside], *want["out"], f"out {begins}")
+        br.check(lse[:, inside], *want["lse"], f"lse {begins}")
+
+
 def test_attention_padded_batch():
     """Tokens ahead of the first sequence and behind the last, sequences without tokens."""
     cache = sr.Cache([50, 60, 7, 0], 16, 2, 64, seed=1)
