@@ -9,28 +9,37 @@
 namespace gn {
 namespace cache {
 
+__host__ __device__ __forceinline__ int read(const int32_t *p)
+{
+#ifdef __CUDA_ARCH__
+    return __ldg(p);
+#else
+    return *p;
+#endif
+}
+
 // Sequence n of the call: its packed tokens [begin, end), its length, by which its tokens
 // have their places, and how much of it the table has room for.  With `cu`, n = -1 and n = sequences are the tokens ahead of the first
 // sequence and behind the last: they have no cache (length 0).
 struct Sequence {
     int begin, end, length, held;
-    __device__ __forceinline__ int first_place() const { return length - (end - begin); }
+    __host__ __device__ __forceinline__ int first_place() const { return length - (end - begin); }
 };
 
-__device__ __forceinline__ Sequence sequence_of(const gn_cache &c, int64_t tokens, int n)
+__host__ __device__ __forceinline__ Sequence sequence_of(const gn_cache &c, int64_t tokens, int n)
 {
     const int t = static_cast<int>(tokens);
     Sequence s;
     const bool real = n >= 0 && n < c.sequences;
     if (c.cu) {
-        s.begin = n < 0 ? 0 : min(max(__ldg(c.cu + min(n, c.sequences)), 0), t);
-        s.end = n >= c.sequences ? t : min(max(__ldg(c.cu + n + 1), s.begin), t);
+        s.begin = n < 0 ? 0 : min(max(read(c.cu + min(n, c.sequences)), 0), t);
+        s.end = n >= c.sequences ? t : min(max(read(c.cu + n + 1), s.begin), t);
     } else {
         const int each = t / c.sequences;
         s.begin = n * each;
         s.end = s.begin + each;
     }
-    s.length = real ? min(max(__ldg(c.lengths + n), 0), 1 << 30) : 0;
+    s.length = real ? min(max(read(c.lengths + n), 0), 1 << 30) : 0;
     s.held = min(s.length, static_cast<int>(c.table_width) * c.page_size);
     return s;
 }

@@ -63,19 +63,19 @@ struct Segment {
 
 // The keys that the last token of a run sees, and the run's blocks (one at least:
 // rows that see nothing are written too).
-__device__ __forceinline__ int keys_of(const CattnArgs &a, const Sequence &s, int run)
+__host__ __device__ __forceinline__ int keys_of(const CattnArgs &a, const Sequence &s, int run)
 {
     if (!a.p.a.causal) return s.held;
     return min(max(s.first_place() + min(s.end - s.begin, (run + 1) * a.tokens), 0), s.held);
 }
 
-__device__ __forceinline__ int blocks_of(const CattnArgs &a, const Sequence &s, int run)
+__host__ __device__ __forceinline__ int blocks_of(const CattnArgs &a, const Sequence &s, int run)
 {
     return max(1, (keys_of(a, s, run) + kTile - 1) / kTile);
 }
 
-__device__ __forceinline__ int first_sequence(const CattnArgs &a) { return a.p.c.cu ? -1 : 0; }
-__device__ __forceinline__ int sequence_count(const CattnArgs &a) { return a.p.c.sequences + (a.p.c.cu ? 2 : 0); }
+__host__ __device__ __forceinline__ int first_sequence(const CattnArgs &a) { return a.p.c.cu ? -1 : 0; }
+__host__ __device__ __forceinline__ int sequence_count(const CattnArgs &a) { return a.p.c.sequences + (a.p.c.cu ? 2 : 0); }
 
 // (Units of work: a tile's first `extra` are its start and end, the others its blocks.)
 struct Walk {
@@ -84,9 +84,9 @@ struct Walk {
     int seq, head, run, unit, runs;
     Sequence s;
 
-    __device__ __forceinline__ explicit Walk(const CattnArgs &args) : a(args) {}
+    __host__ __device__ __forceinline__ explicit Walk(const CattnArgs &args) : a(args) {}
 
-    __device__ __forceinline__ void load(int n)
+    __host__ __device__ __forceinline__ void load(int n)
     {
         seq = n;
         s = cache::sequence_of(a.p.c, a.p.a.tokens, n);
@@ -96,11 +96,11 @@ struct Walk {
 #pragma unroll 1
         for (int r = 0; r < runs; ++r) per_head += a.extra + blocks_of(a, s, r);
     }
-    __device__ __forceinline__ int heads() const { return a.p.c.kv_heads * a.chunks; }
-    __device__ __forceinline__ int64_t units() const { return per_head * heads(); }
+    __host__ __device__ __forceinline__ int heads() const { return a.p.c.kv_heads * a.chunks; }
+    __host__ __device__ __forceinline__ int64_t units() const { return per_head * heads(); }
 
     // begins `offset` units into sequence n
-    __device__ __forceinline__ void start(int n, int64_t offset, int64_t count, int64_t first)
+    __host__ __device__ __forceinline__ void start(int n, int64_t offset, int64_t count, int64_t first)
     {
         left = count;
         at = first;
@@ -119,7 +119,7 @@ struct Walk {
         if (unit > 0 && total <= a.extra) spend(a.extra + total - unit);      // another CTA's
     }
     // `count` units are done with, which end the tile or the part
-    __device__ __forceinline__ void spend(int count)
+    __host__ __device__ __forceinline__ void spend(int count)
     {
         at += count;
         left -= count;
@@ -137,7 +137,7 @@ struct Walk {
         }
     }
     // the next tile of which the part has blocks
-    __device__ __forceinline__ bool next(Segment &g)
+    __host__ __device__ __forceinline__ bool next(Segment &g)
     {
 #pragma unroll 1
         while (left > 0) {
@@ -169,16 +169,24 @@ struct Part {
 // Where part n of `all` units begins.  (By a fraction of 32 bits: it only has to grow with n
 // and be the same wherever it is asked for, and a division of 64 bits is a long stretch of
 // instructions.  The fraction is a little high, so that whole parts come out whole.)
-__device__ __forceinline__ int64_t part_begin(int64_t all, int ctas, int n)
+__host__ __device__ __forceinline__ int64_t part_begin(int64_t all, int ctas, int n)
 {
     if (n >= ctas) return all;
+#ifdef __CUDA_ARCH__
     const float share = static_cast<float>(n) * __frcp_rn(static_cast<float>(ctas));
+#else
+    const float share = static_cast<float>(n) * (1.0f / static_cast<float>(ctas));
+#endif
     const uint64_t fraction = static_cast<uint64_t>(share * 4294967296.0f) + (n > 0 ? 1024u : 0u);
+#ifdef __CUDA_ARCH__
     return static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(all), fraction << 32));
+#else
+    return static_cast<int64_t>(static_cast<unsigned __int128>(all) * fraction >> 32);
+#endif
 }
 
 // The part that holds a unit.
-__device__ __forceinline__ int part_of(int64_t all, int ctas, int64_t unit)
+__host__ __device__ __forceinline__ int part_of(int64_t all, int ctas, int64_t unit)
 {
     int n = static_cast<int>(static_cast<float>(unit) / static_cast<float>(all) * static_cast<float>(ctas));
     n = min(max(n, 0), ctas - 1);
@@ -280,30 +288,41 @@ struct Reader {
     }
 };
 
-// (the loader's, which also says which tile of this CTA's is to be joined)
+// Of CTA `cta`, which also says in `shared` which tile of its own is to be joined (one at the
+// most, its last; the list that it is in need not be the last one that is asked for, so
+// `shared` says none ahead of the first list, and is only written where there is one).
+template <int K>
+__host__ __device__ __forceinline__ void list_work(WorkList<K> &w, Walk &walk, const Part &part, int cta, Shared &shared)
+{
+    const CattnArgs &a = walk.a;
+    int n = 0;
+#pragma unroll 1
+    for (; n < K && walk.next(w.list[n]); ++n) {
+        const Segment &g = w.list[n];
+        if (g.b0 != 0 || g.b1 == g.total) continue;
+        const int first_token = g.run * a.tokens;
+        Shared s = {};
+        s.pieces = part_of(part.all, part.ctas, walk.tile_end - 1) + 1 - cta;
+        s.token = g.s.begin + first_token;
+        s.rows = min(a.tokens, g.s.end - g.s.begin - first_token) * a.heads;
+        s.head = g.hk * a.p.group + g.first_head;
+        s.heads = a.p.group - g.first_head;
+        shared = s;
+    }
+    w.count = n;
+    w.more = n == K && walk.left > 0;
+}
+
+// (the loader's)
+__device__ __forceinline__ void begin_work(const CattnArgs &a)
+{
+    if ((threadIdx.x & 31) == 0) a.shared[blockIdx.x] = {};
+}
+
 template <int K>
 __device__ __forceinline__ void fill_work(WorkList<K> &w, Walk &walk, const Part &part)
 {
-    if ((threadIdx.x & 31) == 0) {
-        const CattnArgs &a = walk.a;
-        int n = 0;
-        Shared s = {};
-#pragma unroll 1
-        for (; n < K && walk.next(w.list[n]); ++n) {
-            const Segment &g = w.list[n];
-            if (g.b0 != 0 || g.b1 == g.total) continue;
-            const int first_token = g.run * a.tokens;
-            s.pieces = part_of(part.all, part.ctas, walk.tile_end - 1) + 1 - static_cast<int>(blockIdx.x);
-            s.token = g.s.begin + first_token;
-            s.rows = min(a.tokens, g.s.end - g.s.begin - first_token) * a.heads;
-            s.head = g.hk * a.p.group + g.first_head;
-            s.heads = a.p.group - g.first_head;
-        }
-        w.count = n;
-        w.more = n == K;
-        // (such a tile is the last of all)
-        if (s.pieces || !w.more) a.shared[blockIdx.x] = s;
-    }
+    if ((threadIdx.x & 31) == 0) list_work(w, walk, part, static_cast<int>(blockIdx.x), walk.a.shared[blockIdx.x]);
     __syncwarp();
 }
 

@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float by = (MODE & kCap) ? a.scale / a.cap : args.scale_log2;
         int n = 0, block = 0;         // tiles so far (keys and values by turns), blocks so far
         bool go = true;
+        begin_work(args);
         Walk walk(args);
         walk.start(part.seq, part.offset, skip ? 0 : part.count, part.first);
         while (work.next(g, [&](WorkList<kSegments> &w) { fill_work(w, walk, part); })) {

@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int step = args.chunk / 8;
             int block = 0, key_tiles = 0, value_tiles = 0;
             bool go = true;
+            begin_work(args);
             Walk walk(args);
             walk.start(part.seq, part.offset, skip ? 0 : part.count, part.first);
             while (work.next(g, [&](WorkList<kSegments> &w) { fill_work(w, walk, part); })) {

@@ -1,0 +1,103 @@
+"""Attention over the paged cache at the sizes of long prompts and large batches, where every
+CTA has many tiles, against its definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import channels_last_groupnorm_gb300 as gn
+from channels_last_groupnorm_gb300 import build as gnbuild
+from tests import block_ref as br
+from tests import gpu_util as gu
+from tests import serve_ref as sr
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+U32 = br.U32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    gnbuild.build()
+    yield
+    gu.assert_clean_device()
+
+
+class Even:
+    """A cache of sequences of equally many tokens, made on the GPU."""
+
+    def __init__(self, count, length, hk, dim, page=64, seed=0):
+        gen = torch.Generator("cuda").manual_seed(seed)
+        width = (length + page - 1) // page
+        self.length, self.page = length, page
+        self.table = torch.randperm(count * width, generator=gen, device="cuda").to(torch.int32).view(count, width)
+        self.lengths = torch.full((count,), length, dtype=torch.int32, device="cuda")
+        for name in "kv":
+            x = torch.randn(count * width, hk, page, dim, generator=gen, device="cuda")
+            scale = torch.exp2(torch.randint(-9, -5, (count * width, hk), generator=gen, device="cuda").float())
+            setattr(self, name + "_pages", (x * 128.0).clamp(-448.0, 448.0).to(sr.E4M3).transpose(1, 2))
+            setattr(self, name + "_scales", scale)
+
+    def args(self):
+        return self.k_pages, self.v_pages, self.k_scales, self.v_scales, self.table, self.lengths
+
+    def values(self, name, head):
+        """[sequences, length, dim] in 64 bits."""
+        pages, scales = getattr(self, name + "_pages")[:, :, head], getattr(self, name + "_scales")[:, head]
+        x = pages.float().double() * scales.double()[:, None, None]
+        return x[self.table.long()].flatten(1, 2)[:, :self.length]
+
+
+def check(q, cache, got, floor, what, scale=None):
+    """Causal attention of equally many new tokens for each sequence.  The bound is that of
+    serve_ref.attention, but for the weights' floor: `floor` of the row's largest for each key."""
+    tokens, h, dim = q.shape
+    count, hk = cache.table.shape[0], cache.k_scales.shape[1]
+    new = tokens // count
+    scale = dim ** -0.5 if scale is None else scale
+    u, low = br.half_step(q.dtype), br.least(q.dtype)
+    j, place = torch.arange(cache.length, device="cuda"), torch.arange(cache.length - new, cache.length, device="cuda")
+    seen = j <= place[:, None]
+    for head in range(h):
+        k, v = (cache.values(n, head * hk // h) for n in "kv")
+        qh = q.view(count, new, h, dim)[:, :, head].double()
+        t = qh @ k.transpose(1, 2) * scale
+        size = qh.abs() @ k.abs().transpose(1, 2) * abs(scale)
+        worst = (U32 * ((dim + 4) * size + 4 * t.abs() + 4)).masked_fill_(~seen, 0.0).amax(2, keepdim=True)
+        del size
+        t.masked_fill_(~seen, -math.inf)
+        lse = torch.logsumexp(t, 2, keepdim=True)
+        top = t.amax(2, keepdim=True)
+        p = t.sub_(lse).exp_()
+        rel = 2 * worst + 2.0 ** -20 + cache.length * U32 / 64
+        drop = 2.0 ** -17 * qh.abs().amax(2, keepdim=True) * k.abs().sum(2).amax(1)[:, None, None] * abs(scale)
+        out, absout = p @ v, p @ v.abs()
+        del p
+        least = floor * torch.exp(top - lse)
+        off = low + u * out.abs() + (u + rel) * absout + (low + least) * v.abs().sum(1, keepdim=True) + 2 * drop * absout
+        br.check(got[0].view(count, new, h, dim)[:, :, head], out, off, f"out of head {head}, {what}")
+        br.check(got[1][head].view(count, new), lse[..., 0], (rel + 4 * U32 * lse.abs() + drop)[..., 0], f"lse of head {head}, {what}")
+
+
+@pytest.mark.parametrize("count,length,new,h,hk,dtype", [
+    (296, 700, 1, 32, 32, BF), (1180, 640, 1, 32, 8, BF), (1180, 1000, 1, 32, 8, FP),        # 32 tiles of single tokens a CTA
+    (1, 12288, 12288, 64, 2, BF), (1, 10000, 10000, 32, 8, FP), (290, 2000, 64, 32, 8, BF),  # 16 tiles of many tokens a CTA
+    (8, 2048, 2048, 32, 8, FP), (64, 3000, 1, 32, 32, BF), (400, 1500, 3, 16, 4, FP)])
+def test_every_row_of_large_calls_is_written(count, length, new, h, hk, dtype):
+    """Calls in which CTAs begin a tile that others go on with as the last of a full list."""
+    dim = 16
+    cache = Even(count, length, hk, dim, seed=count)
+    q = torch.randn(count * new, h, dim, generator=torch.Generator("cuda").manual_seed(1), device="cuda").to(dtype)
+    outs = []
+    for fill in (math.nan, 7.0):
+        out = torch.full_like(q, fill)
+        other = torch.full((h, count * new), fill, device="cuda")      # (where the next lse will probably lie)
+        del other
+        outs.append(gn.attention_cached(q, *cache.args(), out=out))
+    (a, a_lse), (b, b_lse) = outs
+    assert not a.isnan().any() and not a_lse.isnan().any()
+    assert torch.equal(a, b) and torch.equal(a_lse, b_lse)
+    check(q, cache, outs[0], 2.0 ** -18, f"{count} x {new} tokens")
