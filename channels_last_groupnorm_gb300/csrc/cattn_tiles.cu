@@ -30,7 +30,7 @@ constexpr int kThreads = 512;    // warps: 0 loads, 1 MMA, 2 the MMA's waits, 4-
 constexpr int kKeyStages = 3;    // at most
 constexpr int kSegments = 16;  // that are found at a time
 constexpr int kScales = 4;       // blocks whose scales are in shared memory
-constexpr float kLeastScale = 0x1p-100f;
+constexpr float kLeastScale = 0x1p-100f, kLeastFactor = 0x1p-126f;
 constexpr float kShift = 7.0f;   // fp16 weights, away from its subnormals (weight_shift of packed attention)
 constexpr uint32_t kWide = 2 * kHalfBytes;    // a tile of values in fp16
 
@@ -246,11 +246,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (masked) mask_scores(s, 0, static_cast<unsigned>(max(0, end - j0)));
                 // What a group's scores are multiplied by and what is added: a group of which the row
-                // sees nothing has weights of 0, whatever its scale is (it may be no number).
+                // sees nothing has weights of 0, whatever its scale is (it may be no number).  The factor
+                // is above 0, as masked scores are -inf by now: keys of scale 0 (a page that there is not)
+                // or a zero query's product with that of zero keys (2^-120 x 2^-100) would make them NaN.
                 const auto factors = [&](int q, float &f, float &add, float &inv) {
                     const float4 kv = scale[q * (GROUP / 8)];
                     const bool any = j0 + GROUP * q < end;
-                    f = any && !MODE ? by * kv.x : bent;
+                    f = any && !MODE ? max_nan(by * kv.x, kLeastFactor) : bent;
                     add = any ? kv.y : -INFINITY;
                     inv = any ? kv.z : 0.f;
                 };

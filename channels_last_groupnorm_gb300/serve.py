@@ -13,7 +13,7 @@ The cache belongs to the caller, as plain tensors:
   order of the first three axes in memory (a head's tokens of a page next to each
   other read fastest: ``torch.zeros(pages, Hk, page_size, D, ...).transpose(1, 2)``);
 * ``k_scales`` and ``v_scales``, fp32 [pages, Hk]: an element is its byte's value times
-  its page's and head's scale;
+  its page's and head's scale, which is not negative;
 * ``table``, int32 [sequences, width]: the pages of every sequence in order;
 * ``lengths``, int32 [sequences]: the tokens of every sequence, the new ones of the call
   among them.

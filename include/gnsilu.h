@@ -736,8 +736,8 @@ int gn_cache_append(const gn_cache *cache, const gn_append_args *args, void *str
  * lse = -inf.  What slots hold that a query does not see has no influence on it, with two
  * exceptions: a page has one scale, and a byte that is no number (0x7f, 0xff, which
  * gn_cache_append() never writes) among a sequence's values makes every query of its
- * new tokens NaN there.  v_scales are 0 or 2^-100 .. 2^100 in magnitude and not
- * negative.  Query head h reads key / value head h / (heads / kv_heads).
+ * new tokens NaN there.  Scales are not negative; v_scales are 0 or 2^-100 .. 2^100.
+ * Query head h reads key / value head h / (heads / kv_heads).
  *
  * Scores, softmax and sums are fp32.  For the tensor cores' products a query is split into
  * two (bf16) or three (fp16) e4m3 numbers that add up to it, less what lies under 2^-17 of its
