@@ -27,6 +27,10 @@ using cache::Sequence;
 // Rows of a tile in the kernel for few of them and in the one for many.
 constexpr int kFewTile = 16, kManyRows = 2 * kTile;
 
+// Sums of weights, which are taken without the values' scales, are in units of 2^20: 2^30 keys whose
+// values have the least scale (2^-100: zeros) add up to 2^(30 + 100) and more.
+constexpr float kSumDown = 0x1p-20f, kSumUnit = 20.0f;
+
 struct CattnArgs {
     CachedAttn p;
     WaitLimit limit;

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     load_pages(stage(n), e ? &map_v : &map_k, args, key_now, page_now, g.hk, bar(kFull + st), now);
                 }
                 vs = vs < kLeastScale ? kLeastScale : vs;
-                if (lane < 16) scales[(block % kScales) * 16 + lane] = make_float4(ks * by, log2f(vs), 1.0f / vs, 0.f);
+                if (lane < 16) scales[(block % kScales) * 16 + lane] = make_float4(ks * by, log2f(vs), kSumDown / vs, 0.f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kScale + block % kScales));
             }
@@ -540,12 +540,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const float sum = sum_of(i + e);
                         const int64_t at = rows[i + e].out;
                         if (at >= 0 && r < c.dim)
-                            static_cast<T *>(a.out)[at * c.dim + r] = from_float<T>(sum == 0.f ? 0.f : __fdividef(o[i + e], sum));
+                            static_cast<T *>(a.out)[at * c.dim + r] = from_float<T>(sum == 0.f ? 0.f : __fdividef(o[i + e] * kSumDown, sum));
                     }
                 }
                 if (r < N && rows[r].out >= 0) {
                     const float sum = sum_of(r);
-                    a.lse[rows[r].lse] = sum == 0.f ? -INFINITY : (rows[r].top + log2f(sum)) * kLn2;
+                    a.lse[rows[r].lse] = sum == 0.f ? -INFINITY : (rows[r].top + kSumUnit + log2f(sum)) * kLn2;
                 }
             } else if (good) {
 #pragma unroll

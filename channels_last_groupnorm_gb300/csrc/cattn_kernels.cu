@@ -104,10 +104,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
             if (warp != 0) continue;
         }
         if (!there) continue;
-        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+        const float inv = sum == 0.f ? 0.f : kSumDown / sum;
         const int64_t token = s.token + i, head = s.head + h;
         store4<T>(a.out, (token * a.heads + head) * c.dim, lane, c.dim, make_float4(out.x * inv, out.y * inv, out.z * inv, out.w * inv));
-        if (lane == 0) a.lse[head * a.tokens + token] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        if (lane == 0) a.lse[head * a.tokens + token] = sum == 0.f ? -INFINITY : (top + kSumUnit + log2f(sum)) * kLn2;
     }
 }
 

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++mine;
             tc_fence_after_sync();
             const bool whole = g.b0 == 0 && g.b1 == g.total, good = *abort == 0;
-            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            const float inv = l == 0.f ? 0.f : kSumDown / l;
             T *dst = static_cast<T *>(a.out) + (token * a.heads + head) * c.dim;
             float *piece = piece_of(args, blockIdx.x, g.b0 == 0 ? 1 : 0);
             float *dst_piece = piece + 2 * args.rows + static_cast<int64_t>(row) * c.dim;
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (there && good) {
                 if (whole) {
-                    a.lse[static_cast<int64_t>(head) * a.tokens + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                    a.lse[static_cast<int64_t>(head) * a.tokens + token] = l == 0.f ? -INFINITY : (m + kSumUnit + log2f(l)) * kLn2;
                 } else {
                     piece[row] = m;
                     piece[args.rows + row] = l;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     load_pages(base + lay.values + block % 2 * kTileBytes, &map_v, args, key_now, page_now, g.hk, bar(kVFull + block % 2), load);
                     ++value_tiles;
                     vs = vs < kLeastScale ? kLeastScale : vs;
-                    if (lane < 16) scales[(block % kScales) * 16 + lane] = make_float4(ks, log2f(vs), 1.0f / vs, 0.f);
+                    if (lane < 16) scales[(block % kScales) * 16 + lane] = make_float4(ks, log2f(vs), kSumDown / vs, 0.f);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kScale + block % kScales));
                 }

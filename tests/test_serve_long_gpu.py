@@ -101,3 +101,31 @@ def test_every_row_of_large_calls_is_written(count, length, new, h, hk, dtype):
     assert not a.isnan().any() and not a_lse.isnan().any()
     assert torch.equal(a, b) and torch.equal(a_lse, b_lse)
     check(q, cache, outs[0], 2.0 ** -18, f"{count} x {new} tokens")
+
+
+@pytest.mark.parametrize("new,keys,h", [(1, 2 ** 24, 1), (3, 2 ** 24, 2), (70, 2 ** 22, 1), (300, 2 ** 21, 4)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_zero_values_of_very_long_sequences(new, keys, h, dtype):
+    """Values of the least scale leave the sum of the weights as 2^100 of each.  A page is
+    all of the cache: every query sees it keys / 256 times over."""
+    gen = torch.Generator("cuda").manual_seed(new)
+    k_pages = torch.randn(1, 256, 1, 16, generator=gen, device="cuda").mul(64.0).to(sr.E4M3)
+    k_scales, v_scales = torch.full((1, 1), 2.0 ** -8, device="cuda"), torch.full((1, 1), 2.0 ** -100, device="cuda")
+    table = torch.zeros(1, keys // 256, dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([keys], dtype=torch.int32, device="cuda")
+    q = torch.randn(new, h, 16, generator=gen, device="cuda").to(dtype)
+    k = k_pages[0, :, 0].float().double() * 2.0 ** -8
+    t = torch.einsum("nhd,kd->hnk", q.double(), k) / 4
+    lse = torch.logsumexp(t, 2) + math.log(keys // 256)
+    # a score's error, and a thread's sum of one key of each of its CTA's blocks (under 2^10 of them)
+    size = torch.einsum("nhd,kd->hnk", q.double().abs(), k.abs()) / 4
+    drop = 2.0 ** -17 * q.double().abs().amax(2).T * k.abs().sum(1).amax() / 4
+    off = drop + U32 * (20 * size.amax(2) + 4 * t.abs().amax(2) + 4) + 2.0 ** -14 + 4 * U32 * lse.abs()
+    for values in (0.0, 3.0):
+        v_pages = torch.full((1, 256, 1, 16), values, device="cuda").to(sr.E4M3)
+        out, got = gn.attention_cached(q, k_pages, v_pages, k_scales, v_scales, table, lengths, causal=False)
+        br.check(got, lse, off, "lse")
+        want = torch.full(out.shape, values * 2.0 ** -100, dtype=torch.float64, device="cuda")
+        if dtype == FP:
+            want *= 0                                          # (under half of the least half number)
+        br.check(out, want, (br.half_step(dtype) + 2.0 ** -8) * want.abs(), "out")
