@@ -66,6 +66,14 @@ __device__ __forceinline__ uint32_t e4m3_pair_half(uint32_t half2)
     return r;
 }
 
+// (e5m2: past 57344 57344; NaN: 0x7f)
+__device__ __forceinline__ uint32_t e5m2_pair_half(uint32_t half2)
+{
+    unsigned short r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(half2));
+    return r;
+}
+
 // The values of the two low bytes (exact).
 __device__ __forceinline__ uint32_t e4m3_half2(uint32_t pair)
 {

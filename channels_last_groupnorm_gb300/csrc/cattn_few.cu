@@ -4,11 +4,15 @@
 // Such a call is bound by reading the cache once (2 bytes per token, head and
 // channel).  The pages go from memory to the tensor cores as they are: a block of 128
 // keys is the A operand of S^T = K Q^T (keys are the accumulator's lanes, rows its
-// columns) and, read MN-major, of O^T += V^T P^T.  What has more than 4 bits is on the
-// narrow side, and is split into e4m3 numbers that add up to it: a query (its largest
-// channel at 2^7) into 2 of bf16's 8 bits, 3 of fp16's 11, whose products go into the same
-// accumulator; the weights into 2 or 3, each next one times 2^4, with accumulators of
-// their own.  That costs the tensor core's time, of which there is plenty, and no pass
+// columns) and, read MN-major, of O^T += V^T P^T.  What has more bits is on the
+// narrow side, and is split into numbers of 8 bits that add up to it: a query (its largest
+// channel at 2^7) into 2 (bf16's 8 bits) or 3 (fp16's 11) of e4m3, whose products go into the same
+// accumulator; the weights, rounded to fp16, into 3 or 4 of e5m2, each next one times 2^3, with
+// accumulators of their own.  (e5m2 for its range: a long context's small weights, together
+// most of a sum, are held to as many bits as the large ones.  Two or three parts of e4m3, which
+// hold none under 2^-18 of the largest, took as long for single tokens -- 64 of 32 heads on 8 over
+// 3000 keys 79 us replayed either way -- and 158 or 167 us instead of 160 or 174 for 64 x 4
+// tokens of 64 heads.)  That costs the tensor core's time, of which there is plenty, and no pass
 // over the keys: converted to half precision they would cross shared memory three
 // times more, which it has no room for at this rate (141 of 128 bytes a cycle).
 //
@@ -31,11 +35,10 @@ constexpr int kThreads = 256;   // warps: 0 loads, 1 MMA, 2 the MMA's waits, 3 t
 constexpr int kSegments = 32;  // that are found at a time
 constexpr int kScales = 4;      // blocks whose scales are in shared memory
 constexpr int kMaxStages = 6;
-// Weights: the row's largest at 2^4 when the maximum moves, which it does once a score
-// is 2^4 above it: below 448 = 2^8.8, and weights of 2^-10 of the largest still have all
-// their bits.  (With 2^6 and 2^2 it moved more often: four tokens each over 7 caches, 32 rows,
-// 54 us replayed.)
-constexpr float kShift = 4.0f, kRescale = 4.0f;
+// Weights: the row's largest at 2^11 when the maximum moves, which it does once a score
+// is 2^4 above it: fp16's largest number is under 2^16, its least normal one 2^-14, so weights of
+// 2^-25 of the row's largest still have all their bits.
+constexpr float kShift = 11.0f, kRescale = 4.0f;
 constexpr float kLeastScale = 0x1p-100f;
 
 enum Bar { kQ = 0, kQFree = 2, kFull = kQFree + 2, kEmpty = kFull + kMaxStages, kS = kEmpty + kMaxStages, kP = kS + 2, kO = kP + 2,
@@ -53,24 +56,23 @@ struct __align__(16) Row {
 };
 
 struct Layout {
-    uint32_t q, operand, weights, weights_bytes, ring, rows, tops, scales, bars, words, deal, work, total;
+    uint32_t q, operand, weights, ring, rows, tops, scales, bars, words, deal, work, total;
 };
 
 // Weights lie as the threads have them, a key's next to each other ([128 keys][parts][n],
-// MN-major, swizzled over as many bytes as a row has): whole vectors are stored, where
+// MN-major, swizzled over rows of 64 bytes): whole vectors are stored, where
 // [rows][keys] would take a byte at a time (48 of them a thread in three parts).
-__host__ __device__ constexpr uint32_t weight_row(int n, int parts) { return n * parts <= 32 ? 32u : 64u; }
+constexpr uint32_t kWeightRow = 64, kWeightBytes = kTile * kWeightRow;
 
 // Descriptor of the weights as the B operand: 8 keys after 8 keys (stride offset); the
-// swizzle mode is 4 for 64 bytes, 6 for 32.
-template <uint32_t ROW>
+// swizzle mode is 4 for 64 bytes.
 __device__ __forceinline__ uint64_t weights_desc(uint32_t smem)
 {
     uint64_t d = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4);
     d |= static_cast<uint64_t>(1u) << 16;
-    d |= static_cast<uint64_t>((8u * ROW) >> 4) << 32;
+    d |= static_cast<uint64_t>((8u * kWeightRow) >> 4) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(ROW == 64 ? 4u : 6u) << 61;
+    d |= static_cast<uint64_t>(4u) << 61;
     return d;
 }
 
@@ -81,8 +83,7 @@ __host__ __device__ constexpr Layout layout(int n, int parts, int stages)
     l.operand = operand;
     l.q = 0;                                                        // two of each: this tile's and the next one's,
     l.weights = 2 * operand;                                        // this block's and the next one's
-    l.weights_bytes = kTile * weight_row(n, parts);
-    l.ring = l.weights + 2 * l.weights_bytes;
+    l.ring = l.weights + 2 * kWeightBytes;
     l.rows = l.ring + static_cast<uint32_t>(stages) * kTileBytes;   // 2 x n Row
     l.tops = l.rows + 2 * static_cast<uint32_t>(n) * sizeof(Row);   // 4 x n maxima or sums of a warp
     l.scales = l.tops + 16u * static_cast<uint32_t>(n);             // kScales x 16 chunks
@@ -110,12 +111,22 @@ __device__ __forceinline__ int ordered(float v)
 }
 __device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
 
-// 16 times what e4m3 leaves of two fp16 values (exact).
-__device__ __forceinline__ uint32_t sixteen_times_rest(uint32_t v, uint32_t near)
+// e5m2 is the upper half of fp16: four values' bytes, cut off there, ...
+__device__ __forceinline__ uint32_t e5m2_four(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x7531); }
+
+// ... 8 times what that leaves of two of them (exact: at most 8 bits, under a quarter of the value), ...
+__device__ __forceinline__ uint32_t eight_times_rest(uint32_t v)
 {
+    const uint32_t near = v & 0xff00ff00u;
     const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&near));
-    const __half2 r = __hmul2(d, __float2half2_rn(16.0f));
+    const __half2 r = __hmul2(d, __float2half2_rn(8.0f));
     return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// ... and for the last of the parts rounded to nearest.
+__device__ __forceinline__ uint32_t e5m2_four_rounded(uint32_t lo, uint32_t hi)
+{
+    return e5m2_pair_half(lo) | e5m2_pair_half(hi) << 16;
 }
 
 template <int N>
@@ -131,14 +142,16 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[N])
     tmem_wait_ld();
 }
 
+template <typename T>
+__host__ __device__ constexpr int query_parts() { return IsBf16<T>::value ? 2 : 3; }
+
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 2)
     cached_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                       const __grid_constant__ CattnArgs args)
 {
-    constexpr int N = kFewTile, PARTS = IsBf16<T>::value ? 2 : 3, STAGES = stages_of(N, PARTS);
+    constexpr int N = kFewTile, PARTS = query_parts<T>(), WEIGHTS = PARTS + 1, STAGES = stages_of(N, PARTS);
     constexpr Layout lay = layout(N, PARTS, STAGES);
-    constexpr uint32_t kRow = weight_row(N, PARTS);
     constexpr int SIDE = 4;      // rows that are worked on side by side
     extern __shared__ __align__(1024) uint8_t gbase[];
     const uint32_t base = smem_addr(gbase);
@@ -161,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         prefetch_tensormap(&map_v);
     }
     constexpr uint32_t kColumns = 128;
-    static_assert(2 * N + PARTS * N <= kColumns, "a CTA's tensor memory");
+    static_assert(2 * N + WEIGHTS * N <= kColumns, "a CTA's tensor memory");
     if (warp == 1) {
         tmem_alloc(base + lay.words, kColumns);
         tmem_relinquish();
@@ -227,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else if (warp == 1 || warp == 2) {
         const bool waits = warp == 2;
         const int steps = (c.dim + 31) / 32;
-        const uint32_t is = instruction_e4m3(N, false), io = instruction_e4m3(PARTS * N, true) | 1u << 16;
+        const uint32_t is = instruction_e4m3(N, false), io = instruction_e4m3(WEIGHTS * N, true) | 1u << 16 | 1u << 10;
         const auto loaded = [&](int n) { wait_warp(bar(kFull + n % STAGES), (n / STAGES) & 1, abort, args.limit); };
         const auto scores = [&](int n, int q) {       // block n's with query buffer q, into buffer n & 1
             if (elect_one()) {
@@ -271,10 +284,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (!waits) {
                     tc_fence_after_sync();
                     const uint64_t dv = sw128_mnmajor_desc(stage(2 * n + 1));
-                    const uint64_t dw = weights_desc<kRow>(base + lay.weights + (n & 1) * lay.weights_bytes);
+                    const uint64_t dw = weights_desc(base + lay.weights + (n & 1) * kWeightBytes);
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) umma_e4m3(t_o, dv + k * (4096u >> 4), dw + k * (32u * kRow >> 4), io, b > g.b0 || k > 0);
+                        for (int k = 0; k < 4; ++k) umma_e4m3(t_o, dv + k * (4096u >> 4), dw + k * (32u * kWeightRow >> 4), io, b > g.b0 || k > 0);
                     }
                     __syncwarp();
                     commit(bar(kEmpty + (2 * n + 1) % STAGES));
@@ -364,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int r = (warp & 3) * 32 + lane;
         // this thread's key within the block: its row of weights, and what its 16-byte pieces'
         // numbers are swizzled with
-        const uint32_t place = base + lay.weights + static_cast<uint32_t>(r) * kRow;
-        const uint32_t flip = kRow == 128 ? r & 7u : kRow == 64 ? r >> 1 & 3u : r >> 2 & 1u;
+        const uint32_t place = base + lay.weights + static_cast<uint32_t>(r) * kWeightRow;
+        const uint32_t flip = r >> 1 & 3u;
         const int my_chunk = r / args.chunk;
         int n = 0;
         for (int segment = 0; work.next(g); ++segment) {
@@ -440,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         wait_warp(bar(kO + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort, args.limit);
                         tc_fence_after_sync();
 #pragma unroll 1
-                        for (int q = 0; q < PARTS * N / 16; ++q) {
+                        for (int q = 0; q < WEIGHTS * N / 16; ++q) {
                             uint32_t u[16];
                             tmem_ld16(t_o + lanes + 16 * q, u);
                             tmem_wait_ld();
@@ -453,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 // the weights' buffer is free once the products of two blocks ago are done
                 if (n >= 2) wait_warp(bar(kO + (n & 1)), ((n - 2) >> 1) & 1, abort, args.limit);
-                const uint32_t to = place + (n & 1) * lay.weights_bytes;
-                uint32_t packed[PARTS][N / 4] = {};
+                const uint32_t to = place + (n & 1) * kWeightBytes;
+                uint32_t packed[WEIGHTS][N / 4] = {};
 #pragma unroll
                 for (int i = 0; i < N; i += SIDE) {
                     if (i >= live) break;
@@ -467,24 +480,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                         p[e] = seen ? ex2_approx(s[i + e] - (top == -INFINITY ? 0.f : top)) : 0.f;
                         l[i + e] = seen ? fmaf(p[e], inv_vs, l[i + e]) : l[i + e];
                     }
-                    // in fp16, whose 11 bits the parts hold
                     uint32_t h[SIDE / 2];
 #pragma unroll
                     for (int e = 0; e < SIDE / 2; ++e) h[e] = Half2<__half>::pack(p[2 * e], p[2 * e + 1]);
 #pragma unroll
-                    for (int q = 0; q < PARTS; ++q)
+                    for (int q = 0; q < WEIGHTS; ++q)
 #pragma unroll
                         for (int e = 0; e < SIDE / 2; e += 2) {
-                            const uint32_t lo = e4m3_pair_half(h[e]), hi = e4m3_pair_half(h[e + 1]);
-                            packed[q][(i + 2 * e) / 4] = lo | hi << 16;
-                            if (q + 1 < PARTS) {
-                                h[e] = sixteen_times_rest(h[e], e4m3_half2(lo));
-                                h[e + 1] = sixteen_times_rest(h[e + 1], e4m3_half2(hi));
-                            }
+                            packed[q][(i + 2 * e) / 4] = q + 1 < WEIGHTS ? e5m2_four(h[e], h[e + 1]) : e5m2_four_rounded(h[e], h[e + 1]);
+                            h[e] = eight_times_rest(h[e]);
+                            h[e + 1] = eight_times_rest(h[e + 1]);
                         }
                 }
 #pragma unroll
-                for (int q = 0; q < PARTS; ++q)
+                for (int q = 0; q < WEIGHTS; ++q)
 #pragma unroll
                     for (int i = 0; i < N; i += 16) {
                         if (i >= live) break;
@@ -520,9 +529,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             float *to = piece_of(args, blockIdx.x, g.b0 == 0 ? 1 : 0);
             float o[N];
             tmem_ld_cols<N>(t_o + lanes, o);
-            float step = 1.0f / 16.0f;
+            float step = 1.0f / 8.0f;
 #pragma unroll
-            for (int q = 1; q < PARTS; ++q, step *= 1.0f / 16.0f) {
+            for (int q = 1; q < WEIGHTS; ++q, step *= 1.0f / 8.0f) {
                 float more[N];
                 tmem_ld_cols<N>(t_o + q * N + lanes, more);
 #pragma unroll
@@ -575,7 +584,7 @@ using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CattnArgs);
 template <typename T, int MODE>
 cudaError_t launch(const CattnArgs &args, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s)
 {
-    constexpr int PARTS = IsBf16<T>::value ? 2 : 3;
+    constexpr int PARTS = query_parts<T>();
     static std::atomic<uint64_t> done{0};
     const Kernel kernel = cached_few_kernel<T, MODE>;
     const cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kRoom, done);

@@ -741,9 +741,8 @@ int gn_cache_append(const gn_cache *cache, const gn_append_args *args, void *str
  *
  * Scores, softmax and sums are fp32.  For the tensor cores' products a query is split into
  * two (bf16) or three (fp16) e4m3 numbers that add up to it, less what lies under 2^-17 of its
- * largest channel.  The weights are split likewise, to 2^-9 of each (bf16) or 2^-13 (fp16) and
- * 2^-18 of the row's largest; with many new tokens they are rounded to fp16.  The same inputs
- * give the same bits.
+ * largest channel.  The weights are rounded to 2^-11 of each and 2^-32 of the row's largest (in
+ * fp16), and for few new tokens of bf16 queries to 2^-9 of each.  The same inputs give the same bits.
  */
 typedef struct gn_attn_cached_args {
     const void *q;                /* DEVICE [tokens][heads][dim], 16-byte aligned */

@@ -129,3 +129,32 @@ def test_zero_values_of_very_long_sequences(new, keys, h, dtype):
         if dtype == FP:
             want *= 0                                          # (under half of the least half number)
         br.check(out, want, (br.half_step(dtype) + 2.0 ** -8) * want.abs(), "out")
+
+
+@pytest.mark.parametrize("count,length,new,h,hk", [(40, 32768, 1, 8, 8), (1, 131072, 3, 16, 8), (2, 32768, 70, 4, 2)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("above", [9, 12, 13, 14, 16])
+@pytest.mark.parametrize("even", [False, True])
+def test_one_key_far_above_a_long_context(count, length, new, h, hk, dtype, above, even):
+    """A key with most of the weight and hardly a value: what comes out is the sum of many
+    small weights, which may be off by a rounding of each, and no more.  (even: all alike)"""
+    dim = 64
+    cache = Even(count, length, hk, dim, seed=above)
+    k, v = (getattr(cache, n + "_pages").transpose(1, 2) for n in "kv")           # [pages, head, slot, channel]
+    for name, pages, scale in (("k", k, 2.0 ** -4), ("v", v, 2.0 ** -7)):
+        getattr(cache, name + "_scales").fill_(scale)
+    if even:
+        k.view(torch.uint8).zero_()
+    else:
+        k.copy_((k.float() / 8).to(sr.E4M3))                                        # deviation 1
+    # channel 0 is the far key's own; one of it in every sequence
+    k.view(torch.uint8)[..., 0] = 0
+    at = cache.table[:, cache.table.shape[1] // 2].long()
+    far = torch.zeros(dim, device="cuda")
+    far[0] = above * 16.0
+    k.view(torch.uint8)[at, :, 5] = far.to(sr.E4M3).view(torch.uint8)
+    v.view(torch.uint8)[at, :, 5] = 1                                               # 2^-9 of a unit of 2^-7
+    q = torch.randn(count * new, h, dim, generator=torch.Generator("cuda").manual_seed(1), device="cuda").to(dtype)
+    q[..., 0] = 8.0
+    got = gn.attention_cached(q, *cache.args())
+    check(q, cache, got, 2.0 ** -32, f"{above} above")
