@@ -44,15 +44,17 @@ constexpr float kLeastScale = 0x1p-100f;
 enum Bar { kQ = 0, kQFree = 2, kFull = kQFree + 2, kEmpty = kFull + kMaxStages, kS = kEmpty + kMaxStages, kP = kS + 2, kO = kP + 2,
            kScale = kO + 2, kDrain = kScale + kScales, kBars };
 
-// One row of a tile: its scores' factor, its running maximum, the bias and the query's
-// place; what the maximum's last move makes of sums, and the keys that it sees; where its
-// results go (-1: it has none).
+// One row of a tile: its scores' factor, its running maximum, the bias and the first place of
+// the block of 128 that the query stands in; what the maximum's last move makes of sums, and the
+// keys that it sees; where its results go (-1: it has none); the query's place in its block.
+// (Apart, since fp32 holds no odd place past 2^24: what blocks are away and what places within
+// one are is exact.)
 struct __align__(16) Row {
-    float factor, top, slope, place;
+    float factor, top, slope, block;
     float grow;
     int end;
     int64_t out, lse;
-    int64_t pad;
+    float within, pad;
 };
 
 struct Layout {
@@ -314,7 +316,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 row.factor = row.grow = 1.0f;
                 row.top = -INFINITY;
                 row.slope = (MODE & kBias) && a.slopes && there ? __ldg(a.slopes + head) * kLog2e : 0.f;
-                row.place = static_cast<float>(place);
+                row.block = static_cast<float>(place & ~(kTile - 1));
+                row.within = static_cast<float>(place & (kTile - 1));
                 row.end = a.causal ? min(max(place + 1, 0), g.s.held) : g.s.held;
                 row.out = there ? token * a.heads + head : -1;
                 row.lse = head * a.tokens + token;
@@ -417,7 +420,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     for (int e = 0; e < SIDE; ++e) {
                         float t = s[i + e] * (ks * row[e].x);
                         if (MODE & kCap) t = tanh_fast(t) * (a.cap * kLog2e);
-                        if (MODE & kBias) t = fmaf(-row[e].z, fabsf(row[e].w - static_cast<float>(j)), t);
+                        if (MODE & kBias) {
+                            const float away = (row[e].w - static_cast<float>(first)) + (rows[i + e].within - static_cast<float>(r));
+                            t = fmaf(-row[e].z, fabsf(away), t);
+                        }
                         t += log_vs;
                         if (masked) t = j < end[e] ? t : -INFINITY;
                         s[i + e] = t;

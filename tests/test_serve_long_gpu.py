@@ -158,3 +158,43 @@ def test_one_key_far_above_a_long_context(count, length, new, h, hk, dtype, abov
     q[..., 0] = 8.0
     got = gn.attention_cached(q, *cache.args())
     check(q, cache, got, 2.0 ** -32, f"{above} above")
+
+
+@pytest.mark.parametrize("keys", [2 ** 24 + 1001, 2 ** 25 + 130])
+@pytest.mark.parametrize("new", [1, 3, 70])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_distances_in_very_long_sequences(new, keys, dtype):
+    """Where fp32 no longer holds every place, neighbouring keys still are one apart."""
+    gen = torch.Generator("cuda").manual_seed(new)
+    h, dim, page, near = 4, 16, 256, 2048
+    own = near // page + 1                                     # the last pages are their own, all others one
+    pools = [torch.randn(own + 1, 1, page, dim, generator=gen, device="cuda").mul(64.0).clamp(-448, 448).to(sr.E4M3).transpose(1, 2)
+             for _ in "kv"]
+    scales = [torch.full((own + 1, 1), 2.0 ** -6, device="cuda") for _ in "kv"]
+    width = (keys + page - 1) // page
+    table = torch.zeros(1, width, dtype=torch.int32, device="cuda")
+    table[0, -own:] = torch.arange(1, own + 1, device="cuda")
+    lengths = torch.tensor([keys], dtype=torch.int32, device="cuda")
+    slopes = torch.tensor([0.5, 0.25, 1.0, 2.0], device="cuda")
+    q = torch.randn(new, h, dim, generator=gen, device="cuda").to(dtype)
+    out, got = gn.attention_cached(q, *pools, *scales, table, lengths, slopes=slopes)
+    # what lies further back than 2000 keys has less than e^(-0.25 x 1900) of the weight
+    place = torch.arange(keys - near, keys, device="cuda")
+    k, v = (p[table[0, place // page].long()][torch.arange(near), place % page, 0].float().double() * 2.0 ** -6
+            for p in pools)
+    at = torch.arange(keys - new, keys, device="cuda")
+    gap = (at[:, None] - place).double()
+    t = torch.einsum("nhd,kd->hnk", q.double(), k) / 4 - slopes.double()[:, None, None] * gap.abs()
+    size = torch.einsum("nhd,kd->hnk", q.double().abs(), k.abs()) / 4
+    t.masked_fill_(gap < 0, -math.inf)
+    lse = torch.logsumexp(t, 2)
+    p = torch.exp(t - lse[..., None])
+    # scores of the keys that matter: those with more than 2^-40 of the weight
+    worst = (U32 * (20 * size + 4 * t.abs() + 4)).masked_fill(p < 2.0 ** -40, 0.0).amax(2)
+    drop = 2.0 ** -17 * q.double().abs().amax(2).T * k.abs().sum(1).amax() / 4
+    rel = 2 * worst + 2.0 ** -14
+    br.check(got, lse, rel + drop + 4 * U32 * lse.abs(), "lse")
+    want, absout = (torch.einsum("hnk,kd->nhd", p, x) for x in (v, v.abs()))
+    u, low = br.half_step(dtype), br.least(dtype)
+    off = low + u * want.abs() + (u + rel + 2 * drop).T[..., None] * absout + 2.0 ** -32 * near * v.abs().amax()
+    br.check(out, want, off, "out")
