@@ -333,6 +333,16 @@ __device__ __forceinline__ void fill_work(WorkList<K> &w, Walk &walk, const Part
 cudaError_t launch_cached_few(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s);
 cudaError_t launch_cached_tiles(const CattnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int ctas, cudaStream_t s);
 
+// Two weights in fp16, past 65504 as that (NaN: NaN).  A weight is bounded by how far its score may
+// be above the row's maximum, but scores of 2^26 and more (a bias far from its query) have steps of
+// 8 and more: infinities there, times values of either sign and times 0 in the join, would be NaN.
+__device__ __forceinline__ uint32_t weight_pair(float a, float b)
+{
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
 // ---- operands in 8 bits ------------------------------------------------------------
 // Instruction descriptor: fp32 accumulator, M = 128, e4m3 operands, both K-major but
 // for a_mn: the A operand is MN-major.

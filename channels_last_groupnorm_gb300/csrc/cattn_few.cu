@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     uint32_t h[SIDE / 2];
 #pragma unroll
-                    for (int e = 0; e < SIDE / 2; ++e) h[e] = Half2<__half>::pack(p[2 * e], p[2 * e + 1]);
+                    for (int e = 0; e < SIDE / 2; ++e) h[e] = weight_pair(p[2 * e], p[2 * e + 1]);
 #pragma unroll
                     for (int q = 0; q < WEIGHTS; ++q)
 #pragma unroll

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float2 x = unpack2(fma2(pack2(s[at], s[at + 1]), c2, m2));
                             const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
                             some = k == 0 ? pack2(p0, p1) : add2(some, pack2(p0, p1));
-                            pk[GROUP / 2 * e + k] = Half2<__half>::pack(p0, p1);
+                            pk[GROUP / 2 * e + k] = weight_pair(p0, p1);
                         }
                         sum2 = fma2(some, pack2(inv, inv), sum2);
                     }

@@ -160,7 +160,7 @@ def test_one_key_far_above_a_long_context(count, length, new, h, hk, dtype, abov
     check(q, cache, got, 2.0 ** -32, f"{above} above")
 
 
-@pytest.mark.parametrize("keys", [2 ** 24 + 1001, 2 ** 25 + 130])
+@pytest.mark.parametrize("keys", [2 ** 24 + 1001, 2 ** 25 + 130, 2 ** 27 + 777, 2 ** 30 - 300])
 @pytest.mark.parametrize("new", [1, 3, 70])
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_distances_in_very_long_sequences(new, keys, dtype):
