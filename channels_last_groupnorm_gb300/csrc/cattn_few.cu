@@ -314,7 +314,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const bool there = lane < live && h < args.p.group;
                 Row row;
                 row.factor = row.grow = 1.0f;
-                row.top = -INFINITY;
+                // (the last four rows that are worked on together may be past the tile's: no score is above
+                // their maximum, and nothing is made of their weights)
+                row.top = lane < live ? -INFINITY : INFINITY;
                 row.slope = (MODE & kBias) && a.slopes && there ? __ldg(a.slopes + head) * kLog2e : 0.f;
                 row.block = static_cast<float>(place & ~(kTile - 1));
                 row.within = static_cast<float>(place & (kTile - 1));
