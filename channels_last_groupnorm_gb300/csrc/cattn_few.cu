@@ -418,10 +418,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                         row[e] = *reinterpret_cast<const float4 *>(&rows[i + e]);
                         if (masked) end[e] = rows[i + e].end;
                     }
+                    float x[SIDE];
+#pragma unroll
+                    for (int e = 0; e < SIDE; ++e) x[e] = s[i + e] * (ks * row[e].x);
+                    if (MODE & kCap) tanh_all(x, 1.0f);
 #pragma unroll
                     for (int e = 0; e < SIDE; ++e) {
-                        float t = s[i + e] * (ks * row[e].x);
-                        if (MODE & kCap) t = tanh_fast(t) * (a.cap * kLog2e);
+                        float t = x[e];
+                        if (MODE & kCap) t *= a.cap * kLog2e;
                         if (MODE & kBias) {
                             const float away = (row[e].w - static_cast<float>(first)) + (rows[i + e].within - static_cast<float>(r));
                             t = fmaf(-row[e].z, fabsf(away), t);

@@ -135,6 +135,9 @@ CattnArgs plan(const CachedAttn &p, bool few, int least, int most)
 {
     CattnArgs a = {};
     a.p = p;
+    // (a cap above every score there can be does nothing, one under fp32's step makes scores equal:
+    // within these bounds its quotients and products are ordinary numbers)
+    if (a.p.a.cap > 0.f) a.p.a.cap = std::min(std::max(a.p.a.cap, 0x1p-60f), 0x1p60f);
     a.scale_log2 = p.a.scale * kLog2e;
     a.least = least;
     a.most = most;

@@ -92,3 +92,22 @@ def test_scales_far_apart_in_one_call():
         q = rand((new, 4, 64), BF, 4)
         q *= torch.exp2(-(4.0 * torch.arange(new, device="cuda") % 128))[:, None, None].to(BF)
         attend(q, cache, [0, new], f"{new} queries of all sizes")
+
+
+@pytest.mark.parametrize("cap", [1e-38, 1e-9, 0.01, 0.7, 3.0, 50.0, 1e3, 1e5, 1e9, 1e20, 9e37])
+@pytest.mark.parametrize("new", [1, 5, 70])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_caps_of_any_size(new, dtype, cap):
+    """A capped score is as exact as an uncapped one, however far it is from its cap."""
+    cache = sr.Cache([new + 300, new], 32, 2, 64, seed=5)
+    begins = [0, new, 2 * new]
+    q = rand((2 * new, 8, 64), dtype, 6)
+    cu = torch.tensor(begins, dtype=torch.int32, device="cuda")
+    out, lse = gn.attention_cached(q, *cache.args(), cu, cap=cap)
+    want, plain = sr.attention(q, cache, begins, cap=cap), sr.attention(q, cache, begins)
+    # the bounds of uncapped scores, and of the capped ones' tanh 16 roundings of the score
+    size = max(float((cache.values("k", s).norm(dim=2).amax() * q.double().norm(dim=2).amax() / 8)) for s in range(2))
+    more = 16 * br.U32 * min(size, cap)
+    v = max(float(cache.values("v", s).abs().amax()) for s in range(2))
+    br.check(out, want["out"][0], plain["out"][1] + 2 * (more + br.half_step(dtype)) * v, "out")
+    br.check(lse, want["lse"][0], plain["lse"][1] + more + 4 * br.U32 * want["lse"][0].abs(), "lse")
