@@ -567,7 +567,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 if (n >= rows) break;             // (the same for all: rows that are not there cost nothing)
-                if (MODE & kCap) s[n] = tanh_fast(s[n] * inv_cap);
+                if ((MODE & kCap) && n % 4 == 0) {
+                    float x[4] = {s[n], s[n + 1], s[n + 2], s[n + 3]};
+                    tanh_all(x, inv_cap);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n + e] = x[e];
+                }
                 s[n] *= by;
                 if ((MODE & kBias) || masked) {
                     const int4 w = info[n];
