@@ -11,8 +11,8 @@
 // accumulators of their own.  (e5m2 for its range: a long context's small weights, together
 // most of a sum, are held to as many bits as the large ones.  Two or three parts of e4m3, which
 // hold none under 2^-18 of the largest, took as long for single tokens -- 64 of 32 heads on 8 over
-// 3000 keys 79 us replayed either way -- and 158 or 167 us instead of 160 or 174 for 64 x 4
-// tokens of 64 heads.)  That costs the tensor core's time, of which there is plenty, and no pass
+// 3000 keys 85 us replayed either way -- and 176 us instead of 182 for 64 x 4 tokens of 64
+// heads.)  That costs the tensor core's time, of which there is plenty, and no pass
 // over the keys: converted to half precision they would cross shared memory three
 // times more, which it has no room for at this rate (141 of 128 bytes a cycle).
 //
