@@ -7,6 +7,9 @@ The conventions are those of ``block``: every step runs in the library's kernels
 unsupported input gives ``None``, a CUDA or kernel failure raises ``GnError``, and
 ``stream`` is a ``torch.cuda.Stream`` to run on instead of the current one.
 
+Calls can be captured into CUDA graphs.  The first call of a process on a device sets the
+library up there (a status word in mapped memory) and has to come ahead of a capture.
+
 The cache belongs to the caller, as plain tensors:
 
 * ``k_pages`` and ``v_pages``, ``torch.float8_e4m3fn`` [pages, page_size, Hk, D], any

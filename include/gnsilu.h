@@ -676,6 +676,9 @@ int gn_rms_norm_backward(const void *dy, const void *total, const void *weight, 
  * give wrong results, never a wrong address.  A new token whose place is negative or
  * past the table, or whose page is not one of `pages`, is not stored; keys past the
  * table are not seen, and those of a page that there is not read as zeros.
+ *
+ * These calls, and those of RMS norm, can be captured into CUDA graphs, but for the first
+ * call of the library on a device, which sets it up there.
  */
 typedef struct gn_cache {
     void *k_pages, *v_pages;          /* DEVICE e4m3 [pages][page_size][kv_heads][dim], 16-byte aligned, any order
